@@ -25,6 +25,8 @@ KIND = {"ffn": 0, "attn": 1, "layer": 2}
 DTYPE = {"f32": 0, "bf16": 1, "mxfp8": 2}
 RECOMPUTE = {"none": 0, "full": 1, "fine": 2, "selective": 3}
 REDUCE = {"fused": 0, "separate": 1}
+ACT = {"silu": 0, "gelu": 1}
+KEEP = {"none": 0, "pre": 1, "mxfp8": 2}
 EVENTS = ["F", "R", "B", "C(F)", "C(R)", "C(B)", "Sync"]
 OPS = ["ln", "f", "col", "row", "g", "attn"]
 PARAM_NAMES = ("ln1_g", "ln1_b", "wqkv", "bqkv", "wo", "bo",
@@ -49,6 +51,30 @@ class Weights(ctypes.Structure):
 
 class Grads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in PARAM_NAMES]
+
+
+class GluDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("dtype", "rows", "hidden", "ffn", "act", "keep", "dx_dtype", "grad_dtype",
+                 "accumulate")]
+
+
+class GluWeights(ctypes.Structure):
+    """Gated feed-forward weights (w1, b1, w2, b2); the biases may be None."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "b1", "w2", "b2")]
+
+    @classmethod
+    def of(cls, params: Dict):
+        return cls(*[_ptr(params.get(n)) for n in ("w1", "b1", "w2", "b2")])
+
+
+class GluGrads(GluWeights):
+    """Their gradients; None leaves one out."""
+
+
+class CeDesc(ctypes.Structure):
+    _fields_ = [("ignore_index", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in
+                ("dtype", "rows", "hidden", "vocab", "dloss_per_row", "grad_dtype", "accumulate")]
 
 
 def lib():
@@ -80,6 +106,21 @@ def lib():
         L.oases_check_device.restype = i32
         L.oases_shutdown.argtypes = []
         L.oases_shutdown.restype = i32
+        gd, gw, cd = ctypes.POINTER(GluDesc), ctypes.POINTER(GluWeights), ctypes.POINTER(CeDesc)
+        L.oases_glu_saved_bytes.argtypes = [gd]
+        L.oases_glu_saved_bytes.restype = sz
+        L.oases_glu_workspace_bytes.argtypes = [gd, i32]
+        L.oases_glu_workspace_bytes.restype = sz
+        L.oases_glu_fwd.argtypes = [gd, gw, vp, vp, vp, vp, vp, sz, vp]
+        L.oases_glu_fwd.restype = i32
+        L.oases_glu_bwd.argtypes = [gd, gw, vp, vp, vp, vp, ctypes.POINTER(GluGrads), vp, sz, vp]
+        L.oases_glu_bwd.restype = i32
+        L.oases_ce_workspace_bytes.argtypes = [cd, i32]
+        L.oases_ce_workspace_bytes.restype = sz
+        L.oases_ce_fwd.argtypes = [cd, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.oases_ce_fwd.restype = i32
+        L.oases_ce_bwd.argtypes = [cd, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.oases_ce_bwd.restype = i32
         _lib = L
     return _lib
 
@@ -168,6 +209,48 @@ def oases_stack_step(desc, per_layer: Sequence, x, g, y, dx, per_layer_grads: Se
                                   G, _ptr(workspace), nb, _stream(s0), _stream(s1)))
 
 
+def oases_glu_saved_bytes(desc: GluDesc) -> int:
+    return int(lib().oases_glu_saved_bytes(ctypes.byref(desc)))
+
+
+def oases_glu_workspace_bytes(desc: GluDesc, backward: bool) -> int:
+    return int(lib().oases_glu_workspace_bytes(ctypes.byref(desc), int(backward)))
+
+
+def oases_glu_fwd(desc, weights, x, resid, y, saved, workspace, ws_bytes=None, stream=None) -> None:
+    w = weights if isinstance(weights, GluWeights) else GluWeights.of(weights)
+    nb = ws_bytes if ws_bytes is not None else _nbytes(workspace)
+    _check(lib().oases_glu_fwd(ctypes.byref(desc), ctypes.byref(w), _ptr(x), _ptr(resid), _ptr(y),
+                               _ptr(saved), _ptr(workspace), nb, _stream(stream)))
+
+
+def oases_glu_bwd(desc, weights, x, dy, saved, dx, grads, workspace, ws_bytes=None,
+                  stream=None) -> None:
+    w = weights if isinstance(weights, GluWeights) else GluWeights.of(weights)
+    g = grads if isinstance(grads, GluGrads) else GluGrads.of(grads)
+    nb = ws_bytes if ws_bytes is not None else _nbytes(workspace)
+    _check(lib().oases_glu_bwd(ctypes.byref(desc), ctypes.byref(w), _ptr(x), _ptr(dy), _ptr(saved),
+                               _ptr(dx), ctypes.byref(g), _ptr(workspace), nb, _stream(stream)))
+
+
+def oases_ce_workspace_bytes(desc: CeDesc, backward: bool) -> int:
+    return int(lib().oases_ce_workspace_bytes(ctypes.byref(desc), int(backward)))
+
+
+def oases_ce_fwd(desc, x, w, target, loss, lse, workspace, ws_bytes=None, stream=None) -> None:
+    nb = ws_bytes if ws_bytes is not None else _nbytes(workspace)
+    _check(lib().oases_ce_fwd(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(target), _ptr(loss),
+                              _ptr(lse), _ptr(workspace), nb, _stream(stream)))
+
+
+def oases_ce_bwd(desc, x, w, target, lse, dloss, dx, dw, workspace, ws_bytes=None,
+                 stream=None) -> None:
+    nb = ws_bytes if ws_bytes is not None else _nbytes(workspace)
+    _check(lib().oases_ce_bwd(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(target), _ptr(lse),
+                              _ptr(dloss), _ptr(dx), _ptr(dw), _ptr(workspace), nb,
+                              _stream(stream)))
+
+
 def oases_schedule_trace(desc, n_layers: int, phase: int) -> List[tuple]:
     L = lib()
     n = L.oases_schedule_trace(ctypes.byref(desc), n_layers, phase, None, 0)
@@ -214,4 +297,7 @@ __all__ = ["BlockDesc", "Weights", "Grads", "OasesError", "build_library", "lib"
            "desc_from_shape", "weights_struct", "grads_struct", "oases_workspace_bytes",
            "oases_block_fwd", "oases_block_recompute_bwd", "oases_stack_step",
            "oases_schedule_trace", "oases_last_launch_count", "oases_check_device", "oases_shutdown",
-           "oases_status_str", "oases_version", "PARAM_NAMES"]
+           "oases_status_str", "oases_version", "PARAM_NAMES",
+           "ACT", "KEEP", "GluDesc", "GluWeights", "GluGrads", "CeDesc",
+           "oases_glu_saved_bytes", "oases_glu_workspace_bytes", "oases_glu_fwd", "oases_glu_bwd",
+           "oases_ce_workspace_bytes", "oases_ce_fwd", "oases_ce_bwd"]
