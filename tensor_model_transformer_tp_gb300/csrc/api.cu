@@ -37,6 +37,8 @@
 #include "oases.h"
 
 namespace oases {
+int ce_read_and_clear_error();    // ce_tc.cu: likewise of the cross-entropy kernels
+int glu_read_and_clear_error();   // glu_tc.cu: a wait of the gated feed-forward kernels gave up
 int norm_read_and_clear_error();  // norm.cu: a LayerNorm kernel's wait gave up
 cudaError_t layer_norm_bwd_dx_colsum(const float* du, const void* x, const float* mean,
                                      const float* rstd, const void* gamma, const void* dres, void* dx,
@@ -1375,9 +1377,10 @@ oases_status oases_check_device(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   const int v = gemm_read_and_clear_error(), w = attention_read_and_clear_error(),
-            u = norm_read_and_clear_error();
-  if (v < 0 || w < 0 || u < 0) return cuda_fail(cudaGetLastError());
-  return (v || w || u) ? OASES_ERR_TIMEOUT : OASES_OK;
+            u = norm_read_and_clear_error(), g = glu_read_and_clear_error(),
+            c = ce_read_and_clear_error();
+  if (v < 0 || w < 0 || u < 0 || g < 0 || c < 0) return cuda_fail(cudaGetLastError());
+  return (v || w || u || g || c) ? OASES_ERR_TIMEOUT : OASES_OK;
 }
 
 }  // extern "C"

@@ -1,13 +1,13 @@
-// Softmax cross entropy of a linear head (oases_ce.h), in pieces of the
-// vocabulary: logits of a piece l = x W_piece^T, reduced to a running maximum
-// and sum of every row, and, in the backward, turned into g of the piece, from
-// which dx += g W_piece and dW_piece = g^T x.
+// Softmax cross entropy of a linear head (oases_ce.h).  bf16 runs on the
+// tensor-core kernels of ce_tc.cu.  fp32, on the CUDA-core GEMM, goes through
+// the vocabulary in pieces: logits of a piece l = x W_piece^T, reduced to a
+// running maximum and sum of every row, and, in the backward, turned into g of
+// the piece, from which dx += g W_piece and dW_piece = g^T x.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
-#include "common.cuh"
-#include "oases_ce.h"
+#include "ce.cuh"
 
 namespace oases {
 void api_begin();
@@ -19,15 +19,6 @@ namespace {
 constexpr int64_t PIECE_BYTES = 256ll << 20;  // logits of one piece in the workspace
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
-struct CeShape {
-  int M, H, V;
-  DType t, grad_t;
-  bool per_row, accumulate;
-  int64_t ignore;
-  int piece;     // columns of the vocabulary per piece
-  int64_t ld;    // leading dimension of the piece buffers
-};
 
 oases_status ce_shape(const oases_ce_desc* d, CeShape* s) {
   if (!d) return OASES_ERR_INVALID_ARG;
@@ -53,7 +44,7 @@ oases_status ce_shape(const oases_ce_desc* d, CeShape* s) {
 }
 
 struct Layout {
-  size_t logits = 0, g = 0, run = 0, dx = 0, dw = 0, scale = 0, total = 0;
+  size_t logits = 0, run = 0, scale = 0, total = 0;
 };
 Layout layout(const CeShape& s, bool backward) {
   Layout l;
@@ -62,15 +53,14 @@ Layout layout(const CeShape& s, bool backward) {
     l.total += align256(bytes);
   };
   if (s.M == 0) return l;
-  take(&l.logits, (size_t)s.M * s.ld * 4);
-  if (!backward) {
-    take(&l.run, (size_t)s.M * 12);
-  } else {
-    take(&l.g, (size_t)s.M * s.ld * dtype_size(s.t));
-    take(&l.dx, (size_t)s.M * s.H * 4);
-    take(&l.dw, (size_t)s.piece * s.H * 4);
-    take(&l.scale, 256);
+  if (backward && s.per_row) take(&l.scale, 256);
+  if (s.t == DType::BF16) {
+    l.logits = l.total;  // the tensor-core path's own region
+    l.total += backward ? ce_tc_bwd_bytes(s) : ce_tc_fwd_bytes(s);
+    return l;
   }
+  take(&l.logits, (size_t)s.M * s.ld * 4);
+  take(&l.run, backward ? (size_t)s.piece * s.H * 4 : (size_t)s.M * 12);
   return l;
 }
 
@@ -125,7 +115,7 @@ ce_stat_kernel(const float* logits, int64_t ld, int n, int v0, bool first, bool 
       if (last) {
         const float l = ref + logf(s);
         lse[m] = l;
-        loss[m] = t == ignore ? 0.f : t < 0 || t >= V ? NAN : l - at;
+        loss[m] = row_loss(t, ignore, V, l, at);
       } else {
         run[m] = top;
         run[M + m] = s;
@@ -135,64 +125,45 @@ ce_stat_kernel(const float* logits, int64_t ld, int n, int v0, bool first, bool 
   }
 }
 
-// The largest |dloss| of the rows that have a loss, as the common factor s of
-// g: g / s has entries up to 1 in magnitude, and with one dloss for every row
-// the entry of the target, about -1, does not depend on what dloss rounds to.
+// The largest |dloss| of the rows that have a loss (CeRows::scale).
 __global__ void __launch_bounds__(1024)
-ce_scale_kernel(const float* dloss, int per_row, const int64_t* target, int64_t ignore, int M,
-                float* scale) {
+ce_scale_kernel(const float* dloss, const int64_t* target, int64_t ignore, int M, float* scale) {
   __shared__ float red[32];
   pdl_wait();
   pdl_trigger();
   float mx = 0.f;
   for (int m = threadIdx.x; m < M; m += blockDim.x)
-    if (target[m] != ignore) mx = fmaxf(mx, fabsf(dloss[per_row ? m : 0]));
+    if (target[m] != ignore) mx = fmaxf(mx, fabsf(dloss[m]));
   mx = block_max(mx, red);
   if (threadIdx.x == 0) scale[0] = mx;
 }
 
-__device__ __forceinline__ float row_factor(const float* dloss, int per_row, const float* scale,
-                                            int64_t t, int64_t ignore, int V, int m) {
-  if (t == ignore) return 0.f;
-  if (t < 0 || t >= V) return NAN;
-  const float d = dloss[per_row ? m : 0], s = scale[0];
-  return s == 0.f ? d : d / s;  // s == 0: d is 0 or NaN
-}
-
-// g / s of a piece: (exp(l - lse) - [v == target]) dloss / s; rows without a
-// loss are 0 whatever their logits are.
-template <typename T>
+// g / s of a piece over its logits: (exp(l - lse) - [v == target]) r; rows
+// without a loss are 0 whatever their logits are.
 __global__ void __launch_bounds__(256)
-ce_grad_kernel(const float* logits, int64_t ld, int n, int v0, const float* lse,
-               const int64_t* target, int64_t ignore, int V, const float* dloss, int per_row,
-               const float* scale, T* g, int M) {
+ce_grad_kernel(float* logits, int64_t ld, int n, int v0, const float* lse, const CeRows rows, int M) {
   pdl_wait();
   pdl_trigger();
   for (int m = blockIdx.x; m < M; m += gridDim.x) {
-    const int64_t t = target[m];
-    const float r = row_factor(dloss, per_row, scale, t, ignore, V, m), l = lse[m];
-    const float* row = logits + (int64_t)m * ld;
-    T* out = g + (int64_t)m * ld;
+    const int64_t t = rows.target[m];
+    const float r = row_factor(rows, t, m), l = lse[m];
+    float* row = logits + (int64_t)m * ld;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
       const float p = expf(row[i] - l) - (t == v0 + i ? 1.f : 0.f);
-      st_elem(out, i, t == ignore ? 0.f : p * r);
+      row[i] = t == rows.ignore ? 0.f : p * r;
     }
   }
 }
 
 // out (+)= s in
-template <typename T>
 __global__ void __launch_bounds__(256)
-ce_finish_kernel(const float* in, const float* scale, T* out, int64_t n, int accumulate) {
+ce_finish_kernel(const float* in, const float* scale, float* out, int64_t n, int accumulate) {
   pdl_wait();
   pdl_trigger();
   const float s = scale[0];
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    float v = s * in[i];
-    if (accumulate) v += ld_elem(out, i);
-    st_elem(out, i, v);
-  }
+       i += (int64_t)gridDim.x * blockDim.x)
+    out[i] = accumulate ? out[i] + s * in[i] : s * in[i];
 }
 
 int grid_for(int64_t n) { return (int)std::min<int64_t>((n + 255) / 256, 152 * 16); }
@@ -228,6 +199,7 @@ cudaError_t piece_logits(const CeShape& s, const void* x, const void* w, int v0,
 cudaError_t fwd(const CeShape& s, const void* x, const void* w, const int64_t* target, float* loss,
                 float* lse, char* ws, cudaStream_t st) {
   const Layout l = layout(s, false);
+  if (s.t == DType::BF16) return ce_tc_fwd(s, x, w, target, loss, lse, ws + l.logits, st);
   float* logits = reinterpret_cast<float*>(ws + l.logits);
   for (int v0 = 0; v0 < s.V; v0 += s.piece) {
     const int n = std::min(s.piece, s.V - v0);
@@ -240,72 +212,69 @@ cudaError_t fwd(const CeShape& s, const void* x, const void* w, const int64_t* t
   return cudaSuccess;
 }
 
-template <typename T>
 cudaError_t finish(const float* in, const float* scale, void* out, int64_t n, bool accumulate,
                    cudaStream_t st) {
-  return launch_pdl(ce_finish_kernel<T>, dim3(grid_for(n)), dim3(256), 0, st, in, scale,
-                    static_cast<T*>(out), n, accumulate ? 1 : 0);
+  return launch_pdl(ce_finish_kernel, dim3(grid_for(n)), dim3(256), 0, st, in, scale,
+                    static_cast<float*>(out), n, accumulate ? 1 : 0);
 }
 
-template <typename T>
 cudaError_t bwd(const CeShape& s, const void* x, const void* w, const int64_t* target,
                 const float* lse, const float* dloss, void* dx, void* dw, char* ws,
                 cudaStream_t st) {
   const Layout l = layout(s, true);
-  float* logits = reinterpret_cast<float*>(ws + l.logits);
-  T* gp = reinterpret_cast<T*>(ws + l.g);
-  float* dx32 = reinterpret_cast<float*>(ws + l.dx);
-  float* dw32 = reinterpret_cast<float*>(ws + l.dw);
-  float* scale = reinterpret_cast<float*>(ws + l.scale);
-  OASES_TRY(launch_pdl(ce_scale_kernel, dim3(1), dim3(1024), 0, st, dloss, (int)s.per_row, target,
-                       s.ignore, s.M, scale));
+  CeRows rows{target, dloss, dloss, s.per_row ? 1 : 0, s.V, s.ignore};
+  if (s.per_row) {
+    float* scale = reinterpret_cast<float*>(ws + l.scale);
+    OASES_TRY(launch_pdl(ce_scale_kernel, dim3(1), dim3(1024), 0, st, dloss, target, s.ignore, s.M,
+                         scale));
+    rows.scale = scale;
+  }
+  if (s.t == DType::BF16) return ce_tc_bwd(s, x, w, rows, lse, dx, dw, ws + l.logits, st);
+  float* g = reinterpret_cast<float*>(ws + l.logits);
+  float* tmp = reinterpret_cast<float*>(ws + l.run);
   for (int v0 = 0; v0 < s.V; v0 += s.piece) {
     const int n = std::min(s.piece, s.V - v0);
-    OASES_TRY(piece_logits(s, x, w, v0, n, logits, st));
-    OASES_TRY(launch_pdl(ce_grad_kernel<T>, dim3(std::min(s.M, 152 * 8)), dim3(256), 0, st,
-                         (const float*)logits, s.ld, n, v0, lse, target, s.ignore, s.V, dloss,
-                         (int)s.per_row, (const float*)scale, gp, s.M));
-    if (dx) {
-      GemmArgs g;
-      g.M = s.M;
-      g.N = s.H;
-      g.K = n;
-      g.in_t = s.t;
-      g.A = gp;
-      g.lda = s.ld;
-      g.B = row_of(w, v0, s.H, s.t);
-      g.ldb = s.H;
-      g.b_kmajor = false;
-      g.epi = v0 == 0 ? Epi::Store : Epi::Accum;
-      g.C = dx32;
-      g.ldc = s.H;
-      g.c_t = DType::F32;
-      OASES_TRY(gemm(g, st));
-    }
+    OASES_TRY(piece_logits(s, x, w, v0, n, g, st));
+    OASES_TRY(launch_pdl(ce_grad_kernel, dim3(std::min(s.M, 152 * 8)), dim3(256), 0, st, g, s.ld, n,
+                         v0, lse, rows, s.M));
     if (dw) {
-      GemmArgs g;
-      g.M = n;
-      g.N = s.H;
-      g.K = s.M;
-      g.in_t = s.t;
-      g.A = gp;
-      g.lda = s.ld;
-      g.a_kmajor = false;
-      g.B = x;
-      g.ldb = s.H;
-      g.b_kmajor = false;
-      g.C = dw32;
-      g.ldc = s.H;
-      g.c_t = DType::F32;
-      OASES_TRY(gemm(g, st));
-      const int64_t n_out = (int64_t)n * s.H;
-      char* out = static_cast<char*>(dw) + (size_t)v0 * s.H * dtype_size(s.grad_t);
-      OASES_TRY(s.grad_t == DType::F32
-                    ? finish<float>(dw32, scale, out, n_out, s.accumulate, st)
-                    : finish<__nv_bfloat16>(dw32, scale, out, n_out, false, st));
+      GemmArgs q;
+      q.M = n;
+      q.N = s.H;
+      q.K = s.M;
+      q.in_t = s.t;
+      q.A = g;
+      q.lda = s.ld;
+      q.a_kmajor = false;
+      q.B = x;
+      q.ldb = s.H;
+      q.b_kmajor = false;
+      q.C = tmp;
+      q.ldc = s.H;
+      q.c_t = DType::F32;
+      OASES_TRY(gemm(q, st));
+      OASES_TRY(finish(tmp, rows.scale, static_cast<float*>(dw) + (size_t)v0 * s.H, (int64_t)n * s.H,
+                       s.accumulate, st));
+    }
+    if (dx) {
+      GemmArgs q;
+      q.M = s.M;
+      q.N = s.H;
+      q.K = n;
+      q.in_t = s.t;
+      q.A = g;
+      q.lda = s.ld;
+      q.B = row_of(w, v0, s.H, s.t);
+      q.ldb = s.H;
+      q.b_kmajor = false;
+      q.epi = v0 == 0 ? Epi::Store : Epi::Accum;
+      q.C = dx;
+      q.ldc = s.H;
+      q.c_t = DType::F32;
+      OASES_TRY(gemm(q, st));
     }
   }
-  if (dx) OASES_TRY(finish<T>(dx32, scale, dx, (int64_t)s.M * s.H, false, st));
+  if (dx) OASES_TRY(finish((const float*)dx, rows.scale, dx, (int64_t)s.M * s.H, false, st));
   return cudaSuccess;
 }
 
@@ -360,6 +329,5 @@ extern "C" oases_status oases_ce_bwd(const oases_ce_desc* desc, const void* x, c
   const size_t need = layout(s, true).total;
   if (need > 0 && (!workspace || ws_bytes < need)) return OASES_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  return api_end(s.t == DType::F32 ? bwd<float>(s, x, w, target, lse, dloss, dx, dw, ws, st)
-                                   : bwd<__nv_bfloat16>(s, x, w, target, lse, dloss, dx, dw, ws, st));
+  return api_end(bwd(s, x, w, target, lse, dloss, dx, dw, ws, st));
 }

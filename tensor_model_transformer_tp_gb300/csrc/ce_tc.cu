@@ -1,0 +1,347 @@
+// Tensor-core kernels of the linear head's cross entropy (bf16): the main loop
+// of gemm_core.cuh over tiles of rows x vocabulary, with the softmax in its
+// epilogues, so that no logit leaves the chip.
+#include "ce.cuh"
+#include "epi_out.cuh"
+
+namespace oases {
+namespace {
+
+using core::Problem;
+using core::WarpBase;
+using core::pack2;
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
+constexpr int64_t PART_BYTES = 256ll << 20;   // partial maxima and sums of the forward
+constexpr int64_t PIECE_BYTES = 256ll << 20;  // g of one piece of the backward
+constexpr int MIN_PIECE = 4096;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- forward -------------------------------------------------------------------
+// Each warp reduces its half of a tile's columns of its 32 rows, one row per
+// lane, to (r, s): r the maximum of the logits in base-2 units (l log2 e), s
+// the sum of 2^(l log2 e - r); -inf and 0 where every logit is -inf.  The
+// target's logit goes out as it is met.
+struct EpiStat {
+  static constexpr bool DUAL = false, PAD_ROWS = false;
+  static constexpr int STG = 1024;  // unused
+  struct Params {
+    float2* part;  // [slots][M]
+    float* at;     // [M]
+    const int64_t* target;
+  };
+  struct Warp : WarpBase {
+    int64_t t;
+    __device__ __forceinline__ void before(const Params& e, const Problem& p, int mw, int, int) {
+      const int m = mw + lane;
+      t = m < p.M ? e.target[m] : -1;
+    }
+    template <int BN>
+    __device__ __forceinline__ void tile(const Params& e, const Problem& p, int mw, int n0, int half,
+                                         int, uint32_t trow) {
+      const int m = mw + lane, nh = n0 + half * (BN / 2);
+      if (nh >= p.N) return;
+      float r = -INFINITY, s = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < BN / 2; c += 64) {
+        const int n = nh + c;
+        if (n >= p.N) break;
+        float v[64];
+        ptx::tmem_ld32x2(trow + half * (BN / 2) + c, trow + half * (BN / 2) + c + 32,
+                         *reinterpret_cast<float(*)[32]>(v), *reinterpret_cast<float(*)[32]>(v + 32));
+        const int left = p.N - n;
+        if (left < 64) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i >= left) v[i] = -INFINITY;
+        }
+        const int64_t d = t - n;
+        const bool here = d >= 0 && d < min(64, left);
+        if (__any_sync(0xffffffffu, here)) {
+          float a = 0.f;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) a = d == i ? v[i] : a;
+          if (here && m < p.M) e.at[m] = a;
+        }
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = v[k];
+#pragma unroll
+        for (int i = 4; i < 64; ++i) mx[i % 4] = fmaxf(mx[i % 4], v[i]);
+        const float top = fmaxf(r, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * LOG2E);
+        const float ref = top == -INFINITY ? 0.f : top;
+        s *= ex2(r - ref);
+        r = top;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t l2 = f2_splat(LOG2E), nr = f2_splat(-ref);
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          const uint64_t q = f2_fma(f2_pack(v[i], v[i + 1]), l2, nr);
+          sum[i % 4] += ex2(f2_lo(q));
+          sum[i % 4 + 1] += ex2(f2_hi(q));
+        }
+        s += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
+      if (m < p.M) e.part[(int64_t)(nh / (BN / 2)) * p.M + m] = make_float2(r, s);
+    }
+  };
+};
+
+// Joins the (r, s) of a row's slots in a fixed order: 32 rows per block, 16
+// threads per row over the slots.
+__global__ void __launch_bounds__(512)
+ce_join_kernel(const float2* part, int slots, const float* at, const int64_t* target, int64_t ignore,
+               int V, int M, float* loss, float* lse) {
+  __shared__ float2 red[16][33];
+  pdl_wait();
+  pdl_trigger();
+  const int x = threadIdx.x, y = threadIdx.y, m = blockIdx.x * 32 + x;
+  float r = -INFINITY, s = 0.f;
+  auto join = [&](float2 q) {
+    const float top = fmaxf(r, q.x), ref = top == -INFINITY ? 0.f : top;
+    s = s * exp2f(r - ref) + q.y * exp2f(q.x - ref);
+    r = top;
+  };
+  if (m < M) {
+#pragma unroll 4
+    for (int i = y; i < slots; i += 16) join(part[(int64_t)i * M + m]);
+  }
+  red[y][x] = make_float2(r, s);
+  __syncthreads();
+  if (y == 0 && m < M) {
+    for (int i = 1; i < 16; ++i) join(red[i][x]);
+    const float l = ((r == -INFINITY ? 0.f : r) + log2f(s)) * LN2;
+    lse[m] = l;
+    const int64_t t = target[m];
+    loss[m] = row_loss(t, ignore, V, l, t >= 0 && t < V ? at[m] : 0.f);
+  }
+}
+
+// ---- backward ------------------------------------------------------------------
+// g / s of a piece, rounded to bf16: r (2^(l log2 e - lse log2 e) - [v == target]);
+// rows without a loss are 0 whatever their logits are.
+struct EpiG {
+  static constexpr bool DUAL = false, PAD_ROWS = false;
+  static constexpr int STG = 4096;
+  struct Params {
+    CUtensorMap g;  // boxes of 32 rows x 64 columns of the piece
+    CeRows rows;
+    const float* lse;
+    int v0;  // first column of the piece
+  };
+  struct Warp : WarpBase {
+    int64_t t;
+    float r, l2;
+    bool dead;
+    __device__ __forceinline__ void before(const Params& e, const Problem& p, int mw, int, int) {
+      const int m = mw + lane;
+      t = -1;
+      r = l2 = 0.f;
+      dead = true;
+      if (m < p.M) {
+        t = e.rows.target[m];
+        dead = t == e.rows.ignore;
+        r = row_factor(e.rows, t, m);
+        l2 = e.lse[m] * LOG2E;
+        t -= e.v0;
+      }
+    }
+    template <int BN>
+    __device__ __forceinline__ void tile(const Params& e, const Problem& p, int mw, int n0, int half,
+                                         int, uint32_t trow) {
+#pragma unroll 1
+      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 64) {
+        const int n = n0 + c;
+        if (n >= p.N) break;
+        float v[64];
+        ptx::tmem_ld32x2(trow + c, trow + c + 32, *reinterpret_cast<float(*)[32]>(v),
+                         *reinterpret_cast<float(*)[32]>(v + 32));
+        const uint64_t le = f2_splat(LOG2E), nl = f2_splat(-l2);
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          const uint64_t q = f2_fma(f2_pack(v[i], v[i + 1]), le, nl);
+          v[i] = ex2(f2_lo(q));
+          v[i + 1] = ex2(f2_hi(q));
+        }
+        const int64_t d = t - n;
+        if (__any_sync(0xffffffffu, d >= 0 && d < 64)) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] -= d == i ? 1.f : 0.f;
+        }
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = dead ? 0u : pack2(v[2 * i] * r, v[2 * i + 1] * r);
+        wait_free();
+        stage_row(w);
+        store_box(&e.g, n, mw);
+      }
+    }
+  };
+};
+
+// dx = s * sum of the splits' partial products, in their order.
+__global__ void __launch_bounds__(256)
+ce_slabs_kernel(const float* slabs, int splits, int64_t slab, const float* scale, __nv_bfloat16* dx,
+                int64_t n) {
+  pdl_wait();
+  pdl_trigger();
+  const float s = *scale;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n / 4;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int z = 0; z < splits; ++z) {
+      const float4 q = *reinterpret_cast<const float4*>(slabs + z * slab + 4 * i);
+      a.x += q.x;
+      a.y += q.y;
+      a.z += q.z;
+      a.w += q.w;
+    }
+    reinterpret_cast<uint2*>(dx)[i] = make_uint2(pack2(s * a.x, s * a.y), pack2(s * a.z, s * a.w));
+  }
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Tiles of the logits: 128 columns while one row block holds every row (the
+// product is bound by reading w, and 128-column tiles spread it over more SMs),
+// else 256-column CTA-pair tiles.
+int stat_slots(const CeShape& s) { return (s.V + (s.M <= 128 ? 63 : 127)) / (s.M <= 128 ? 64 : 128); }
+// Rows per pass of the forward: the partial results of a pass fit PART_BYTES.
+int fwd_rows(const CeShape& s) {
+  const int64_t fit = PART_BYTES / (8ll * stat_slots(s)) / 256 * 256;
+  return (int)std::min<int64_t>(s.M, std::max<int64_t>(fit, 256));
+}
+
+struct BwdPlan {
+  int piece, splits;
+  int64_t ld, slab;  // slab: floats between the partial dx of two splits
+  size_t g, dx, total;
+};
+BwdPlan bwd_plan(const CeShape& s) {
+  BwdPlan b;
+  const int64_t fit = PIECE_BYTES / (2ll * s.M) / 256 * 256;
+  const int pieces = (int)((s.V + std::max<int64_t>(fit, MIN_PIECE) - 1) / std::max<int64_t>(fit, MIN_PIECE));
+  b.piece = pieces == 1 ? s.V : ((s.V + pieces - 1) / pieces + 255) / 256 * 256;
+  b.ld = (b.piece + 7) / 8 * 8;
+  // dx of few rows has few tiles, each a contraction over the whole vocabulary:
+  // split it over the SMs
+  const int tiles = s.M <= 128 ? (s.H + 127) / 128 : (s.M + 255) / 256 * ((s.H + 255) / 256);
+  const int slots = s.M <= 128 ? core::sm_count() : core::sm_count() / 2;
+  b.splits = pieces == 1 ? std::max(1, std::min(slots / tiles, s.V / 512)) : 1;
+  core::slices_per_split(s.V, &b.splits);
+  const int64_t rows = (s.M + 255) / 256 * 256;
+  b.slab = rows * s.H;
+  b.g = 0;
+  b.dx = align256((size_t)s.M * b.ld * 2);
+  b.total = b.dx;
+  if (b.splits > 1)
+    b.total += align256((size_t)b.slab * 4 * b.splits);
+  else if (pieces > 1)
+    b.total += align256((size_t)s.M * s.H * 4);
+  return b;
+}
+
+#define OASES_TRY(expr)                       \
+  do {                                        \
+    const cudaError_t e_ = (expr);            \
+    if (e_ != cudaSuccess) return e_;         \
+  } while (0)
+
+}  // namespace
+
+size_t ce_tc_fwd_bytes(const CeShape& s) {
+  const size_t rows = fwd_rows(s);
+  return align256(rows * stat_slots(s) * 8) + align256(rows * 4);
+}
+
+cudaError_t ce_tc_fwd(const CeShape& s, const void* x, const void* w, const int64_t* target,
+                      float* loss, float* lse, char* ws, cudaStream_t st) {
+  const int step = fwd_rows(s), slots = stat_slots(s);
+  EpiStat::Params e;
+  e.part = reinterpret_cast<float2*>(ws);
+  e.at = reinterpret_cast<float*>(ws + align256((size_t)step * slots * 8));
+  for (int m0 = 0; m0 < s.M; m0 += step) {
+    const int M = std::min(step, s.M - m0);
+    e.target = target + m0;
+    core::Operands o{M, s.V, s.H, static_cast<const __nv_bfloat16*>(x) + (int64_t)m0 * s.H, s.H, w, s.H};
+    OASES_TRY(s.M <= 128 ? (core::launch<EpiStat, 128, true, true, 1>(o, e, st))
+                         : (core::launch<EpiStat, 256, true, true, 2>(o, e, st)));
+    OASES_TRY(launch_pdl(ce_join_kernel, dim3((M + 31) / 32), dim3(32, 16), 0, st,
+                         (const float2*)e.part, slots, (const float*)e.at, e.target, s.ignore, s.V,
+                         M, loss + m0, lse + m0));
+  }
+  return cudaSuccess;
+}
+
+size_t ce_tc_bwd_bytes(const CeShape& s) { return bwd_plan(s).total; }
+
+cudaError_t ce_tc_bwd(const CeShape& s, const void* x, const void* w, const CeRows& rows,
+                      const float* lse, void* dx, void* dw, char* ws, cudaStream_t st) {
+  using core::EpiOut;
+  const BwdPlan b = bwd_plan(s);
+  void* g = ws + b.g;
+  float* dx32 = reinterpret_cast<float*>(ws + b.dx);
+  const bool few = s.M <= 128;
+  for (int v0 = 0; v0 < s.V; v0 += b.piece) {
+    const int n = std::min(b.piece, s.V - v0);
+    const bool first = v0 == 0, last = v0 + n == s.V;
+    const __nv_bfloat16* wp = static_cast<const __nv_bfloat16*>(w) + (int64_t)v0 * s.H;
+    {
+      EpiG::Params e;
+      if (!core::tensor_map(&e.g, g, false, n, s.M, b.ld, 64, 32)) return cudaErrorInvalidValue;
+      e.rows = rows;
+      e.lse = lse;
+      e.v0 = v0;
+      core::Operands o{s.M, n, s.H, x, s.H, wp, s.H};
+      OASES_TRY(few ? (core::launch<EpiG, 128, true, true, 1>(o, e, st))
+                    : (core::launch<EpiG, 256, true, true, 2>(o, e, st)));
+    }
+    if (dx) {
+      EpiOut::Params e = {};
+      bool ok = true;
+      if (b.splits > 1) {
+        e.slab_rows = (int)(b.slab / s.H);
+        ok = core::out_map(&e, dx32, DType::F32, e.slab_rows * b.splits, s.H, s.H);
+      } else if (last) {
+        ok = core::out_map(&e, dx, DType::BF16, s.M, s.H, s.H);
+        e.scale = rows.scale;
+        e.prior = first ? nullptr : dx32;
+      } else {
+        ok = core::out_map(&e, dx32, DType::F32, s.M, s.H, s.H);
+        e.accumulate = !first;
+      }
+      if (!ok) return cudaErrorInvalidValue;
+      core::Operands o{s.M, s.H, n, g, b.ld, wp, s.H};
+      o.splits = b.splits;
+      OASES_TRY(few ? (core::launch<EpiOut, 128, true, false, 1>(o, e, st))
+                    : (core::launch<EpiOut, 256, true, false, 2>(o, e, st)));
+      if (b.splits > 1) {
+        const int64_t count = (int64_t)s.M * s.H;
+        OASES_TRY(launch_pdl(ce_slabs_kernel,
+                             dim3((unsigned)std::min<int64_t>((count / 4 + 255) / 256, 152 * 8)),
+                             dim3(256), 0, st, (const float*)dx32, b.splits, b.slab, rows.scale,
+                             static_cast<__nv_bfloat16*>(dx), count));
+      }
+    }
+    if (dw) {
+      EpiOut::Params e = {};
+      char* out = static_cast<char*>(dw) + (size_t)v0 * s.H * dtype_size(s.grad_t);
+      if (!core::out_map(&e, out, s.grad_t, n, s.H, s.H)) return cudaErrorInvalidValue;
+      e.scale = rows.scale;
+      e.accumulate = s.accumulate;
+      core::Operands o{n, s.H, s.M, g, b.ld, x, s.H};
+      OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o, e, st)));
+    }
+  }
+  return cudaSuccess;
+}
+
+int ce_read_and_clear_error() { return core::read_and_clear_error(); }
+
+}  // namespace oases

@@ -1,13 +1,13 @@
 // Gated feed-forward block (oases_glu.h):
 //   a = x Wg^T + bg, b = x Wu^T + bu, h = act(a) b, y = h W2^T + b2 (+ resid)
-// and its backward.  The products are GEMMs; what lies between them is
-// element-wise over [rows, ffn].
+// and its backward.  bf16 runs on the fused tensor-core kernels of glu_tc.cu;
+// fp32 on the CUDA-core GEMM with the element-wise parts as kernels here.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
-#include "common.cuh"
-#include "oases_glu.h"
+#include "glu.cuh"
+#include "mx_block.cuh"
 #include "oases_mx.h"
 
 namespace oases {
@@ -16,18 +16,6 @@ void api_set_error(const char* what);
 oases_status api_end(cudaError_t e);
 
 namespace {
-
-constexpr int MXB = 32;  // elements per scale of the 8-bit form
-
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
-struct GluShape {
-  int M, H, F;
-  DType t, dx_t, grad_t;
-  int act, keep;
-  bool accumulate;
-  int64_t ldq;  // leading dimension of the 8-bit codes
-};
 
 oases_status glu_shape(const oases_glu_desc* d, GluShape* s) {
   if (!d) return OASES_ERR_INVALID_ARG;
@@ -54,8 +42,6 @@ oases_status glu_shape(const oases_glu_desc* d, GluShape* s) {
   return OASES_OK;
 }
 
-// Kept activations (oases_glu_keep): where the scales of the 8-bit form start.
-size_t saved_scale_offset(const GluShape& s) { return align256(2 * (size_t)s.M * s.ldq); }
 size_t saved_bytes(const GluShape& s) {
   if (s.keep == OASES_GLU_KEEP_PRE) return 2 * (size_t)s.M * s.F * dtype_size(s.t);
   if (s.keep == OASES_GLU_KEEP_MXFP8)
@@ -76,10 +62,11 @@ Layout layout(const GluShape& s, bool backward) {
   };
   if (s.M == 0) return l;
   const int wide = std::max(2 * s.F, s.H);
-  if (!backward || s.keep == OASES_GLU_KEEP_NONE) take(&l.pre, 2 * MF * 4);
+  const bool f32 = s.t == DType::F32;
+  if (backward ? s.keep == OASES_GLU_KEEP_NONE : f32) take(&l.pre, 2 * MF * e);
   take(&l.h, MF * e);
   if (backward) {
-    take(&l.dh, MF * 4);
+    if (f32) take(&l.dh, MF * 4);
     take(&l.dpre, 2 * MF * e);
     take(&l.part, (size_t)colsum_blocks(s.M) * wide * 4);
   }
@@ -103,12 +90,10 @@ __device__ __forceinline__ void act_both(int act, float a, float& f, float& df) 
   }
 }
 
-// h = act(a + bg) (b + bu) from the fp32 projections p [M, 2F]; keeps [a | b]
-// with the biases in `kept` if given, and leaves them in p (what the 8-bit
-// form is quantised from).
-template <typename T>
+// h = act(a + bg) (b + bu) from the projections p [M, 2F]; leaves them with
+// their biases in p, or in `kept` if given.
 __global__ void __launch_bounds__(256)
-glu_act_kernel(float* p, const T* bias, T* h, T* kept, int64_t MF, int F, int act) {
+glu_act_kernel(float* p, const float* bias, float* h, float* kept, int64_t MF, int F, int act) {
   pdl_wait();
   pdl_trigger();
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < MF;
@@ -118,42 +103,23 @@ glu_act_kernel(float* p, const T* bias, T* h, T* kept, int64_t MF, int F, int ac
     const int64_t ia = m * 2 * F + f, ib = ia + F;
     float a = p[ia], b = p[ib];
     if (bias) {
-      a += ld_elem(bias, f);
-      b += ld_elem(bias, F + f);
-      p[ia] = a;
-      p[ib] = b;
+      a += bias[f];
+      b += bias[F + f];
     }
-    if (kept) {
-      st_elem(kept, ia, a);
-      st_elem(kept, ib, b);
+    if (bias || kept) {
+      (kept ? kept : p)[ia] = a;
+      (kept ? kept : p)[ib] = b;
     }
     float g, dg;
     act_both(act, a, g, dg);
-    if (h) st_elem(h, i, g * b);
+    if (h) h[i] = g * b;
   }
 }
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  // sign, 4 exponent bits (bias 7), 3 mantissa bits
-  const int e = (c >> 3) & 15, m = c & 7;
-  const float v = e ? ldexpf((float)(8 + m), e - 10) : ldexpf((float)m, -9);
-  return c & 0x80 ? -v : v;
-}
-
-// Where the backward takes a and b from.
-struct KeptIn {
-  const void* pre;        // [M, 2F] in the storage type
-  const float* pre32;     // [M, 2F] fp32 (recomputed)
-  const uint8_t* codes;   // MX operands, gate then up
-  const uint8_t* scales;
-  int64_t code_stride, scale_stride, ldq;
-  int kgroups;
-};
-
-// dh fp32 [M, F] -> dpre = [da | db] [M, 2F] and h [M, F].
-template <typename T>
+// dpre = [da | db] [M, 2F] and h [M, F] from dh [M, F] at pre = [a | b].
 __global__ void __launch_bounds__(256)
-glu_grad_kernel(const KeptIn k, const float* dh, T* dpre, T* h, int64_t MF, int F, int act) {
+glu_grad_kernel(const float* pre, const float* dh, float* dpre, float* h, int64_t MF, int F,
+                int act) {
   pdl_wait();
   pdl_trigger();
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < MF;
@@ -161,27 +127,12 @@ glu_grad_kernel(const KeptIn k, const float* dh, T* dpre, T* h, int64_t MF, int 
     const int64_t m = i / F;
     const int f = (int)(i - m * F);
     const int64_t ia = m * 2 * F + f, ib = ia + F;
-    float a, b;
-    if (k.codes) {
-      const int64_t at = ((m / 128) * k.kgroups + f / 128) * 512 + (m % 32) * 16 + ((m % 128) / 32) * 4 +
-                         (f / MXB) % 4;
-      const int64_t c = m * k.ldq + f;
-      a = e4m3_value(k.codes[c]) * ldexpf(1.0f, (int)k.scales[at] - 127);
-      b = e4m3_value(k.codes[k.code_stride + c]) *
-          ldexpf(1.0f, (int)k.scales[k.scale_stride + at] - 127);
-    } else if (k.pre32) {
-      a = k.pre32[ia];
-      b = k.pre32[ib];
-    } else {
-      a = ld_elem(static_cast<const T*>(k.pre), ia);
-      b = ld_elem(static_cast<const T*>(k.pre), ib);
-    }
+    const float a = pre[ia], b = pre[ib], d = dh[i];
     float g, dg;
     act_both(act, a, g, dg);
-    const float d = dh[i];
-    st_elem(dpre, ia, d * b * dg);
-    st_elem(dpre, ib, d * g);
-    st_elem(h, i, g * b);
+    dpre[ia] = d * b * dg;
+    dpre[ib] = d * g;
+    h[i] = g * b;
   }
 }
 
@@ -224,39 +175,32 @@ cudaError_t bias_grad(const void* in, int M, int N, DType t, void* out, DType ou
     if (e_ != cudaSuccess) return e_;         \
   } while (0)
 
-// [a | b] without biases, fp32, and what follows from it.
-template <typename T>
-cudaError_t project(const GluShape& s, const oases_glu_weights& w, const void* x, float* pre, T* h,
-                    void* saved, cudaStream_t st) {
-  const int64_t MF = (int64_t)s.M * s.F;
+// [a | b] and h = act(a) b; h, pre and kept8 are each left out when null.
+cudaError_t project(const GluShape& s, const oases_glu_weights& w, const void* x, void* h, void* pre,
+                    void* kept8, float* scratch, cudaStream_t st) {
+  if (s.t == DType::BF16) return glu_project_tc(s, x, w.w1, w.b1, h, pre, kept8, st);
   Gemm g(s.M, 2 * s.F, s.H, s.t);
   g.A = x;
   g.lda = s.H;
   g.B = w.w1;
   g.ldb = s.H;
-  g.C = pre;
+  g.C = scratch;
   g.ldc = 2 * s.F;
   g.c_t = DType::F32;
   OASES_TRY(gemm(g, st));
-  OASES_TRY(launch_pdl(glu_act_kernel<T>, dim3(grid_for(MF)), dim3(256), 0, st, pre, (const T*)w.b1,
-                       h, s.keep == OASES_GLU_KEEP_PRE ? (T*)saved : (T*)nullptr, MF, s.F, s.act));
-  if (s.keep == OASES_GLU_KEEP_MXFP8 && saved) {
-    uint8_t* q = static_cast<uint8_t*>(saved);
-    uint8_t* sf = q + saved_scale_offset(s);
-    for (int half = 0; half < 2; ++half)
-      OASES_TRY(mx_quantize_rows(pre + half * s.F, 2 * s.F, s.M, s.F, DType::F32,
-                                 q + (size_t)half * s.M * s.ldq, s.ldq,
-                                 sf + (size_t)half * mx_sf_bytes(s.M, s.F), st));
-  }
-  return cudaSuccess;
+  const int64_t MF = (int64_t)s.M * s.F;
+  return launch_pdl(glu_act_kernel, dim3(grid_for(MF)), dim3(256), 0, st, scratch,
+                    (const float*)w.b1, (float*)h, (float*)pre, MF, s.F, s.act);
 }
 
-template <typename T>
 cudaError_t fwd(const GluShape& s, const oases_glu_weights& w, const void* x, const void* resid,
                 void* y, void* saved, char* ws, cudaStream_t st) {
   const Layout l = layout(s, false);
-  T* h = reinterpret_cast<T*>(ws + l.h);
-  OASES_TRY(project<T>(s, w, x, reinterpret_cast<float*>(ws + l.pre), h, saved, st));
+  void* h = ws + l.h;
+  OASES_TRY(project(s, w, x, h, s.keep == OASES_GLU_KEEP_PRE ? saved : nullptr,
+                    s.keep == OASES_GLU_KEEP_MXFP8 ? saved : nullptr,
+                    reinterpret_cast<float*>(ws + l.pre), st));
+  if (s.t == DType::BF16) return glu_down_tc(s, h, w.w2, w.b2, resid, y, st);
   Gemm g(s.M, s.H, s.F, s.t);
   g.A = h;
   g.lda = s.F;
@@ -297,43 +241,39 @@ cudaError_t weight_grad(const GluShape& s, const void* A, int N, const void* B, 
   return gemm(g, st);
 }
 
-template <typename T>
 cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, const void* dy,
                 const void* saved, void* dx, const oases_glu_grads& gr, char* ws, cudaStream_t st) {
   const Layout l = layout(s, true);
-  const int64_t MF = (int64_t)s.M * s.F;
-  T* h = reinterpret_cast<T*>(ws + l.h);
-  T* dpre = reinterpret_cast<T*>(ws + l.dpre);
-  float* dh = reinterpret_cast<float*>(ws + l.dh);
+  void *h = ws + l.h, *dpre = ws + l.dpre;
   float* part = reinterpret_cast<float*>(ws + l.part);
   float* tmp = reinterpret_cast<float*>(ws + l.bias);
-  KeptIn k = {};
+  const void *pre = saved, *kept8 = nullptr;
   if (s.keep == OASES_GLU_KEEP_NONE) {
-    float* pre = reinterpret_cast<float*>(ws + l.pre);
-    OASES_TRY(project<T>(s, w, x, pre, (T*)nullptr, nullptr, st));
-    k.pre32 = pre;
-  } else if (s.keep == OASES_GLU_KEEP_PRE) {
-    k.pre = saved;
-  } else {
-    k.codes = static_cast<const uint8_t*>(saved);
-    k.scales = k.codes + saved_scale_offset(s);
-    k.code_stride = (int64_t)s.M * s.ldq;
-    k.scale_stride = mx_sf_bytes(s.M, s.F);
-    k.ldq = s.ldq;
-    k.kgroups = (s.F + 127) / 128;
+    float* p = reinterpret_cast<float*>(ws + l.pre);
+    OASES_TRY(project(s, w, x, nullptr, p, nullptr, p, st));
+    pre = p;
+  } else if (s.keep == OASES_GLU_KEEP_MXFP8) {
+    pre = nullptr;
+    kept8 = saved;
   }
-  Gemm g(s.M, s.F, s.H, s.t);
-  g.A = dy;
-  g.lda = s.H;
-  g.B = w.w2;
-  g.ldb = s.F;
-  g.b_kmajor = false;
-  g.C = dh;
-  g.ldc = s.F;
-  g.c_t = DType::F32;
-  OASES_TRY(gemm(g, st));
-  OASES_TRY(launch_pdl(glu_grad_kernel<T>, dim3(grid_for(MF)), dim3(256), 0, st, k, (const float*)dh,
-                       dpre, h, MF, s.F, s.act));
+  if (s.t == DType::BF16) {
+    OASES_TRY(glu_grad_tc(s, dy, w.w2, pre, kept8, dpre, h, st));
+  } else {
+    float* dh = reinterpret_cast<float*>(ws + l.dh);
+    Gemm g(s.M, s.F, s.H, s.t);
+    g.A = dy;
+    g.lda = s.H;
+    g.B = w.w2;
+    g.ldb = s.F;
+    g.b_kmajor = false;
+    g.C = dh;
+    g.ldc = s.F;
+    g.c_t = DType::F32;
+    OASES_TRY(gemm(g, st));
+    const int64_t MF = (int64_t)s.M * s.F;
+    OASES_TRY(launch_pdl(glu_grad_kernel, dim3(grid_for(MF)), dim3(256), 0, st, (const float*)pre,
+                         (const float*)dh, (float*)dpre, (float*)h, MF, s.F, s.act));
+  }
   if (gr.w2) OASES_TRY(weight_grad(s, dy, s.H, h, s.F, gr.w2, st));
   if (gr.w1) OASES_TRY(weight_grad(s, dpre, 2 * s.F, x, s.H, gr.w1, st));
   if (gr.b2) OASES_TRY(bias_grad(dy, s.M, s.H, s.t, gr.b2, s.grad_t, s.accumulate, part, tmp, st));
@@ -392,8 +332,7 @@ extern "C" oases_status oases_glu_fwd(const oases_glu_desc* desc, const oases_gl
   if (need > 0 && (!workspace || ws_bytes < need)) return OASES_ERR_WORKSPACE;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  return api_end(s.t == DType::F32 ? fwd<float>(s, *wts, x, resid, y, saved, ws, st)
-                                   : fwd<__nv_bfloat16>(s, *wts, x, resid, y, saved, ws, st));
+  return api_end(fwd(s, *wts, x, resid, y, saved, ws, st));
 }
 
 extern "C" oases_status oases_glu_bwd(const oases_glu_desc* desc, const oases_glu_weights* wts,
@@ -429,7 +368,5 @@ extern "C" oases_status oases_glu_bwd(const oases_glu_desc* desc, const oases_gl
   const size_t need = layout(s, true).total;
   if (need > 0 && (!workspace || ws_bytes < need)) return OASES_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  return api_end(s.t == DType::F32
-                     ? bwd<float>(s, *wts, x, dy, saved, dx, *grads, ws, st)
-                     : bwd<__nv_bfloat16>(s, *wts, x, dy, saved, dx, *grads, ws, st));
+  return api_end(bwd(s, *wts, x, dy, saved, dx, *grads, ws, st));
 }

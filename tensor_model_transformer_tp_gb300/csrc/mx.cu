@@ -23,42 +23,13 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "mx_block.cuh"
 
 namespace oases {
 namespace {
 
-constexpr int MXB = 32;  // elements per scale block
-
 __device__ __forceinline__ float load_f(const float* p) { return *p; }
 __device__ __forceinline__ float load_f(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
-// floor(log2(m)) of a finite m > 0, subnormals included.
-__device__ __forceinline__ int floor_log2(float m) {
-  const uint32_t b = __float_as_uint(m);
-  const int ex = (int)(b >> 23);
-  if (ex > 0) return ex - 127;
-  return (31 - __clz((int)(b & 0x7FFFFFu))) - 149;
-}
-
-// Scale exponent of a block with maximum magnitude amax (0 for amax = 0).
-__device__ __forceinline__ int block_exponent(float amax) {
-  if (!(amax > 0.f)) return 0;
-  return max(-127, min(127, floor_log2(amax) - 8));
-}
-
-// 2^-xe as an fp32 (xe in [-127, 126]: always a normal number).
-__device__ __forceinline__ float pow2_neg(int xe) { return __int_as_float((127 - xe) << 23); }
-
-// Two E4M3 codes, a at the lower address.
-__device__ __forceinline__ uint16_t e4m3x2(float a, float b) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
-  return d;
-}
-
-__device__ __forceinline__ int64_t sf_offset(int r, int j, int kgroups) {
-  return ((int64_t)(r / 128) * kgroups + j / 4) * 512 + (r % 32) * 16 + ((r % 128) / 32) * 4 + (j % 4);
-}
 
 // Quantises 32 values (n of them real, the rest 0) into codes + scale byte.
 __device__ __forceinline__ uint8_t quantize_block(const float (&v)[MXB], int n, uint8_t (&code)[MXB]) {
