@@ -1,13 +1,12 @@
 // Softmax cross entropy of a linear head (oases_ce.h).  bf16 runs on the
-// tensor-core kernels of ce_tc.cu.  fp32, on the CUDA-core GEMM, goes through
-// the vocabulary in pieces: logits of a piece l = x W_piece^T, reduced to a
-// running maximum and sum of every row, and, in the backward, turned into g of
-// the piece, from which dx += g W_piece and dW_piece = g^T x.
+// tensor-core kernels of ce_tc.cu, fp32 on the CUDA-core GEMM with the same
+// epilogues.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
 #include "ce.cuh"
+#include "gemm_f32.cuh"
 
 namespace oases {
 void api_begin();
@@ -16,7 +15,8 @@ oases_status api_end(cudaError_t e);
 
 namespace {
 
-constexpr int64_t PIECE_BYTES = 256ll << 20;  // logits of one piece in the workspace
+constexpr int64_t PART_BYTES = 256ll << 20;   // fp32: partial maxima and sums of the forward
+constexpr int64_t PIECE_BYTES = 256ll << 20;  // fp32: g of one piece of the backward
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -43,8 +43,15 @@ oases_status ce_shape(const oases_ce_desc* d, CeShape* s) {
   return OASES_OK;
 }
 
+// fp32: one partial result per row and 64 columns; rows per pass of the forward.
+int f32_slots(const CeShape& s) { return (s.V + f32::BN - 1) / f32::BN; }
+int fwd_rows(const CeShape& s) {
+  const int64_t fit = PART_BYTES / (8ll * f32_slots(s)) / 64 * 64;
+  return (int)std::min<int64_t>(s.M, std::max<int64_t>(fit, 64));
+}
+
 struct Layout {
-  size_t logits = 0, run = 0, scale = 0, total = 0;
+  size_t tc = 0, part = 0, at = 0, g = 0, scale = 0, total = 0;
 };
 Layout layout(const CeShape& s, bool backward) {
   Layout l;
@@ -55,12 +62,16 @@ Layout layout(const CeShape& s, bool backward) {
   if (s.M == 0) return l;
   if (backward && s.per_row) take(&l.scale, 256);
   if (s.t == DType::BF16) {
-    l.logits = l.total;  // the tensor-core path's own region
+    l.tc = l.total;  // the tensor-core path's own region
     l.total += backward ? ce_tc_bwd_bytes(s) : ce_tc_fwd_bytes(s);
     return l;
   }
-  take(&l.logits, (size_t)s.M * s.ld * 4);
-  take(&l.run, backward ? (size_t)s.piece * s.H * 4 : (size_t)s.M * 12);
+  if (backward) {
+    take(&l.g, (size_t)s.M * s.ld * 4);
+  } else {
+    take(&l.part, (size_t)fwd_rows(s) * f32_slots(s) * 8);
+    take(&l.at, (size_t)fwd_rows(s) * 4);
+  }
   return l;
 }
 
@@ -74,56 +85,57 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   __syncthreads();
   return v;
 }
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  v = lane < (int)blockDim.x / 32 ? red[lane] : 0.f;
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  __syncthreads();
-  return v;
-}
+constexpr float LOG2E = 1.4426950408889634f;
 
-// The reference point of exponentials of values with maximum m: m, or 0 where
-// every value is -inf (exp(-inf - 0) = 0).
-__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
+// fp32 forward: a row's 64 columns, four per thread of sixteen, to (r, s) as in
+// ce_tc.cu: the maximum in base-2 units and the sum of 2^(l log2 e - r).
+struct StatF32 {
+  static constexpr bool DUAL = false;
+  float2* part;
+  float* at;
+  const int64_t* target;
+  __device__ __forceinline__ void tile(int m, int n0, const float (&v)[4], int col, int M, int N) const {
+    float r = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n0 + col + i < N) r = fmaxf(r, v[i] * LOG2E);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+    const float ref = r == -INFINITY ? 0.f : r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n0 + col + i < N) s += exp2f(fmaf(v[i], LOG2E, -ref));
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (m >= M) return;
+    if (col == 0) part[(int64_t)(n0 / f32::BN) * M + m] = make_float2(r, s);
+    const int64_t d = target[m] - n0 - col;
+    if (d >= 0 && d < 4 && target[m] < N) at[m] = d == 0 ? v[0] : d == 1 ? v[1] : d == 2 ? v[2] : v[3];
+  }
+};
 
-// One row of a piece [v0, v0 + n): joins its maximum and sum with the row's
-// running ones (run[0], run[1] of [3][M]) and notes the target's logit
-// (run[2]); the last piece writes lse and loss.
-__global__ void __launch_bounds__(256)
-ce_stat_kernel(const float* logits, int64_t ld, int n, int v0, bool first, bool last, float* run,
-               const int64_t* target, int64_t ignore, int V, float* loss, float* lse, int M) {
-  __shared__ float red[8];
-  pdl_wait();
-  pdl_trigger();
-  for (int m = blockIdx.x; m < M; m += gridDim.x) {
-    const float* row = logits + (int64_t)m * ld;
-    float mx = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) mx = fmaxf(mx, row[i]);
-    mx = block_max(mx, red);
-    const float old = first ? -INFINITY : run[m], top = fmaxf(old, mx), ref = ref_of(top);
-    float s = 0.f;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) s += expf(row[i] - ref);
-    s = block_sum(s, red);
-    if (threadIdx.x == 0) {
-      if (!first) s += run[M + m] * expf(old - ref);
-      const int64_t t = target[m];
-      float at = first ? 0.f : run[2 * M + m];
-      if (t >= v0 && t < v0 + n) at = row[t - v0];
-      if (last) {
-        const float l = ref + logf(s);
-        lse[m] = l;
-        loss[m] = row_loss(t, ignore, V, l, at);
-      } else {
-        run[m] = top;
-        run[M + m] = s;
-        run[2 * M + m] = at;
-      }
+// fp32 backward: g / s of a piece, (exp(l - lse) - [v == target]) r; rows
+// without a loss are 0 whatever their logits are.
+struct GradF32 {
+  static constexpr bool DUAL = false;
+  float* g;
+  int64_t ld;
+  CeRows rows;
+  const float* lse;
+  int v0;
+  __device__ __forceinline__ void tile(int m, int n0, const float (&v)[4], int col, int M, int N) const {
+    if (m >= M) return;
+    const int64_t t = rows.target[m];
+    const float r = row_factor(rows, t, m), l = lse[m];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = n0 + col + i;
+      if (n >= N) break;
+      const float p = expf(v[i] - l) - (t == v0 + n ? 1.f : 0.f);
+      g[(int64_t)m * ld + n] = t == rows.ignore ? 0.f : p * r;
     }
   }
-}
+};
 
 // The largest |dloss| of the rows that have a loss (CeRows::scale).
 __global__ void __launch_bounds__(1024)
@@ -138,84 +150,27 @@ ce_scale_kernel(const float* dloss, const int64_t* target, int64_t ignore, int M
   if (threadIdx.x == 0) scale[0] = mx;
 }
 
-// g / s of a piece over its logits: (exp(l - lse) - [v == target]) r; rows
-// without a loss are 0 whatever their logits are.
-__global__ void __launch_bounds__(256)
-ce_grad_kernel(float* logits, int64_t ld, int n, int v0, const float* lse, const CeRows rows, int M) {
-  pdl_wait();
-  pdl_trigger();
-  for (int m = blockIdx.x; m < M; m += gridDim.x) {
-    const int64_t t = rows.target[m];
-    const float r = row_factor(rows, t, m), l = lse[m];
-    float* row = logits + (int64_t)m * ld;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const float p = expf(row[i] - l) - (t == v0 + i ? 1.f : 0.f);
-      row[i] = t == rows.ignore ? 0.f : p * r;
-    }
-  }
-}
-
-// out (+)= s in
-__global__ void __launch_bounds__(256)
-ce_finish_kernel(const float* in, const float* scale, float* out, int64_t n, int accumulate) {
-  pdl_wait();
-  pdl_trigger();
-  const float s = scale[0];
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x)
-    out[i] = accumulate ? out[i] + s * in[i] : s * in[i];
-}
-
-int grid_for(int64_t n) { return (int)std::min<int64_t>((n + 255) / 256, 152 * 16); }
-
 #define OASES_TRY(expr)                       \
   do {                                        \
     const cudaError_t e_ = (expr);            \
     if (e_ != cudaSuccess) return e_;         \
   } while (0)
 
-const char* row_of(const void* p, int64_t row, int H, DType t) {
-  return static_cast<const char*>(p) + (size_t)row * H * dtype_size(t);
-}
-
-// Logits of the piece [v0, v0 + n), fp32.
-cudaError_t piece_logits(const CeShape& s, const void* x, const void* w, int v0, int n, float* out,
-                         cudaStream_t st) {
-  GemmArgs g;
-  g.M = s.M;
-  g.N = n;
-  g.K = s.H;
-  g.in_t = s.t;
-  g.A = x;
-  g.lda = s.H;
-  g.B = row_of(w, v0, s.H, s.t);
-  g.ldb = s.H;
-  g.C = out;
-  g.ldc = s.ld;
-  g.c_t = DType::F32;
-  return gemm(g, st);
-}
-
 cudaError_t fwd(const CeShape& s, const void* x, const void* w, const int64_t* target, float* loss,
                 float* lse, char* ws, cudaStream_t st) {
   const Layout l = layout(s, false);
-  if (s.t == DType::BF16) return ce_tc_fwd(s, x, w, target, loss, lse, ws + l.logits, st);
-  float* logits = reinterpret_cast<float*>(ws + l.logits);
-  for (int v0 = 0; v0 < s.V; v0 += s.piece) {
-    const int n = std::min(s.piece, s.V - v0);
-    OASES_TRY(piece_logits(s, x, w, v0, n, logits, st));
-    OASES_TRY(launch_pdl(ce_stat_kernel, dim3(std::min(s.M, 152 * 8)), dim3(256), 0, st,
-                         (const float*)logits, s.ld, n, v0, v0 == 0, v0 + n == s.V,
-                         reinterpret_cast<float*>(ws + l.run), target, s.ignore, s.V, loss, lse,
-                         s.M));
+  if (s.t == DType::BF16) return ce_tc_fwd(s, x, w, target, loss, lse, ws + l.tc, st);
+  const int step = fwd_rows(s);
+  for (int m0 = 0; m0 < s.M; m0 += step) {
+    const int M = std::min(step, s.M - m0);
+    const StatF32 e{reinterpret_cast<float2*>(ws + l.part), reinterpret_cast<float*>(ws + l.at),
+                    target + m0};
+    const f32::Args g{M, s.V, s.H, static_cast<const float*>(x) + (int64_t)m0 * s.H, s.H,
+                      static_cast<const float*>(w), s.H, 0, 0};
+    OASES_TRY((f32::launch<StatF32, true, true>(g, e, st)));
+    OASES_TRY(ce_join(e.part, f32_slots(s), e.at, e.target, s, M, loss + m0, lse + m0, st));
   }
   return cudaSuccess;
-}
-
-cudaError_t finish(const float* in, const float* scale, void* out, int64_t n, bool accumulate,
-                   cudaStream_t st) {
-  return launch_pdl(ce_finish_kernel, dim3(grid_for(n)), dim3(256), 0, st, in, scale,
-                    static_cast<float*>(out), n, accumulate ? 1 : 0);
 }
 
 cudaError_t bwd(const CeShape& s, const void* x, const void* w, const int64_t* target,
@@ -229,52 +184,25 @@ cudaError_t bwd(const CeShape& s, const void* x, const void* w, const int64_t* t
                          scale));
     rows.scale = scale;
   }
-  if (s.t == DType::BF16) return ce_tc_bwd(s, x, w, rows, lse, dx, dw, ws + l.logits, st);
-  float* g = reinterpret_cast<float*>(ws + l.logits);
-  float* tmp = reinterpret_cast<float*>(ws + l.run);
+  if (s.t == DType::BF16) return ce_tc_bwd(s, x, w, rows, lse, dx, dw, ws + l.tc, st);
+  float* g = reinterpret_cast<float*>(ws + l.g);
   for (int v0 = 0; v0 < s.V; v0 += s.piece) {
     const int n = std::min(s.piece, s.V - v0);
-    OASES_TRY(piece_logits(s, x, w, v0, n, g, st));
-    OASES_TRY(launch_pdl(ce_grad_kernel, dim3(std::min(s.M, 152 * 8)), dim3(256), 0, st, g, s.ld, n,
-                         v0, lse, rows, s.M));
-    if (dw) {
-      GemmArgs q;
-      q.M = n;
-      q.N = s.H;
-      q.K = s.M;
-      q.in_t = s.t;
-      q.A = g;
-      q.lda = s.ld;
-      q.a_kmajor = false;
-      q.B = x;
-      q.ldb = s.H;
-      q.b_kmajor = false;
-      q.C = tmp;
-      q.ldc = s.H;
-      q.c_t = DType::F32;
-      OASES_TRY(gemm(q, st));
-      OASES_TRY(finish(tmp, rows.scale, static_cast<float*>(dw) + (size_t)v0 * s.H, (int64_t)n * s.H,
-                       s.accumulate, st));
-    }
-    if (dx) {
-      GemmArgs q;
-      q.M = s.M;
-      q.N = s.H;
-      q.K = n;
-      q.in_t = s.t;
-      q.A = g;
-      q.lda = s.ld;
-      q.B = row_of(w, v0, s.H, s.t);
-      q.ldb = s.H;
-      q.b_kmajor = false;
-      q.epi = v0 == 0 ? Epi::Store : Epi::Accum;
-      q.C = dx;
-      q.ldc = s.H;
-      q.c_t = DType::F32;
-      OASES_TRY(gemm(q, st));
-    }
+    const float* wp = static_cast<const float*>(w) + (int64_t)v0 * s.H;
+    OASES_TRY((f32::launch<GradF32, true, true>(
+        f32::Args{s.M, n, s.H, (const float*)x, s.H, wp, s.H, 0, 0},
+        GradF32{g, s.ld, rows, lse, v0}, st)));
+    if (dw)
+      OASES_TRY((f32::launch<f32::Out, false, false>(
+          f32::Args{n, s.H, s.M, g, s.ld, (const float*)x, s.H, 0, 0},
+          f32::Out{static_cast<float*>(dw) + (int64_t)v0 * s.H, s.H, rows.scale, nullptr, nullptr,
+                   s.accumulate},
+          st)));
+    if (dx)
+      OASES_TRY((f32::launch<f32::Out, true, false>(
+          f32::Args{s.M, s.H, n, g, s.ld, wp, s.H, 0, 0},
+          f32::Out{(float*)dx, s.H, rows.scale, nullptr, nullptr, v0 > 0}, st)));
   }
-  if (dx) OASES_TRY(finish((const float*)dx, rows.scale, dx, (int64_t)s.M * s.H, false, st));
   return cudaSuccess;
 }
 

@@ -49,6 +49,9 @@ cudaError_t ce_tc_fwd(const CeShape& s, const void* x, const void* w, const int6
 size_t ce_tc_bwd_bytes(const CeShape& s);
 cudaError_t ce_tc_bwd(const CeShape& s, const void* x, const void* w, const CeRows& rows,
                       const float* lse, void* dx, void* dw, char* ws, cudaStream_t st);
+// Joins `slots` partial results (r, s) per row, part [slots][M], to lse and loss.
+cudaError_t ce_join(const float2* part, int slots, const float* at, const int64_t* target,
+                    const CeShape& s, int M, float* loss, float* lse, cudaStream_t st);
 int ce_read_and_clear_error();
 
 }  // namespace oases

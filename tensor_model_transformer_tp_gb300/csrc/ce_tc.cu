@@ -272,11 +272,15 @@ cudaError_t ce_tc_fwd(const CeShape& s, const void* x, const void* w, const int6
     core::Operands o{M, s.V, s.H, static_cast<const __nv_bfloat16*>(x) + (int64_t)m0 * s.H, s.H, w, s.H};
     OASES_TRY(s.M <= 128 ? (core::launch<EpiStat, 128, true, true, 1>(o, e, st))
                          : (core::launch<EpiStat, 256, true, true, 2>(o, e, st)));
-    OASES_TRY(launch_pdl(ce_join_kernel, dim3((M + 31) / 32), dim3(32, 16), 0, st,
-                         (const float2*)e.part, slots, (const float*)e.at, e.target, s.ignore, s.V,
-                         M, loss + m0, lse + m0));
+    OASES_TRY(ce_join(e.part, slots, e.at, e.target, s, M, loss + m0, lse + m0, st));
   }
   return cudaSuccess;
+}
+
+cudaError_t ce_join(const float2* part, int slots, const float* at, const int64_t* target,
+                    const CeShape& s, int M, float* loss, float* lse, cudaStream_t st) {
+  return launch_pdl(ce_join_kernel, dim3((M + 31) / 32), dim3(32, 16), 0, st, part, slots, at, target,
+                    s.ignore, s.V, M, loss, lse);
 }
 
 size_t ce_tc_bwd_bytes(const CeShape& s) { return bwd_plan(s).total; }

@@ -1,11 +1,12 @@
 // Gated feed-forward block (oases_glu.h):
 //   a = x Wg^T + bg, b = x Wu^T + bu, h = act(a) b, y = h W2^T + b2 (+ resid)
-// and its backward.  bf16 runs on the fused tensor-core kernels of glu_tc.cu;
-// fp32 on the CUDA-core GEMM with the element-wise parts as kernels here.
+// and its backward.  bf16 runs on the fused tensor-core kernels of glu_tc.cu and
+// glu_few.cu, fp32 on the CUDA-core GEMM with the same epilogues.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
+#include "gemm_f32.cuh"
 #include "glu.cuh"
 #include "mx_block.cuh"
 #include "oases_mx.h"
@@ -16,6 +17,10 @@ void api_set_error(const char* what);
 oases_status api_end(cudaError_t e);
 
 namespace {
+
+// Bias gradients of up to this many rows are summed by one launch, a column per
+// thread and 16 row groups; more rows go through partial rows.
+constexpr int DIRECT_SUM_ROWS = 2048;
 
 oases_status glu_shape(const oases_glu_desc* d, GluShape* s) {
   if (!d) return OASES_ERR_INVALID_ARG;
@@ -51,7 +56,7 @@ size_t saved_bytes(const GluShape& s) {
 
 // Workspace regions, each a multiple of 256 bytes.
 struct Layout {
-  size_t pre = 0, h = 0, dh = 0, dpre = 0, bias = 0, part = 0, total = 0;
+  size_t pre = 0, h = 0, dpre = 0, bias = 0, part = 0, total = 0;
 };
 Layout layout(const GluShape& s, bool backward) {
   Layout l;
@@ -62,20 +67,20 @@ Layout layout(const GluShape& s, bool backward) {
   };
   if (s.M == 0) return l;
   const int wide = std::max(2 * s.F, s.H);
-  const bool f32 = s.t == DType::F32;
-  if (backward ? s.keep == OASES_GLU_KEEP_NONE : f32) take(&l.pre, 2 * MF * e);
   take(&l.h, MF * e);
   if (backward) {
-    if (f32) take(&l.dh, MF * 4);
+    if (s.keep == OASES_GLU_KEEP_NONE) take(&l.pre, 2 * MF * e);
     take(&l.dpre, 2 * MF * e);
-    take(&l.part, (size_t)colsum_blocks(s.M) * wide * 4);
+    if (s.M > DIRECT_SUM_ROWS) {
+      take(&l.part, (size_t)colsum_blocks(s.M) * wide * 4);
+      take(&l.bias, (size_t)wide * 4);
+    }
   }
-  take(&l.bias, (size_t)wide * 4);
   return l;
 }
 
-// ---- element-wise kernels ----------------------------------------------------
-// act(a) and its derivative in fp32.  SiLU: s = 1 / (1 + e^-a), act = a s,
+// ---- fp32 epilogues ------------------------------------------------------------
+// act(a) and its derivative.  SiLU: s = 1 / (1 + e^-a), act = a s,
 // act' = s (1 + a (1 - s)).
 __device__ __forceinline__ void act_both(int act, float a, float& f, float& df) {
   if (act == OASES_ACT_SILU) {
@@ -90,49 +95,85 @@ __device__ __forceinline__ void act_both(int act, float a, float& f, float& df) 
   }
 }
 
-// h = act(a + bg) (b + bu) from the projections p [M, 2F]; leaves them with
-// their biases in p, or in `kept` if given.
-__global__ void __launch_bounds__(256)
-glu_act_kernel(float* p, const float* bias, float* h, float* kept, int64_t MF, int F, int act) {
-  pdl_wait();
-  pdl_trigger();
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < MF;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t m = i / F;
-    const int f = (int)(i - m * F);
-    const int64_t ia = m * 2 * F + f, ib = ia + F;
-    float a = p[ia], b = p[ib];
-    if (bias) {
-      a += bias[f];
-      b += bias[F + f];
+// Both projections of an output: h = act(a + bg) (b + bu), and [a | b] to `pre`.
+struct UpF32 {
+  static constexpr bool DUAL = true;
+  const float* bias;
+  float *h, *pre;
+  int act;
+  __device__ __forceinline__ void tile(int m, int n0, const float (&va)[4], const float (&vb)[4],
+                                       int col, int M, int N) const {
+    if (m >= M) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = n0 + col + i;
+      if (n >= N) break;
+      float a = va[i], b = vb[i], f, df;
+      if (bias) {
+        a += bias[n];
+        b += bias[N + n];
+      }
+      if (pre) {
+        pre[(int64_t)m * 2 * N + n] = a;
+        pre[(int64_t)m * 2 * N + N + n] = b;
+      }
+      if (h) {
+        act_both(act, a, f, df);
+        h[(int64_t)m * N + n] = f * b;
+      }
     }
-    if (bias || kept) {
-      (kept ? kept : p)[ia] = a;
-      (kept ? kept : p)[ib] = b;
-    }
-    float g, dg;
-    act_both(act, a, g, dg);
-    if (h) h[i] = g * b;
   }
-}
+};
 
-// dpre = [da | db] [M, 2F] and h [M, F] from dh [M, F] at pre = [a | b].
-__global__ void __launch_bounds__(256)
-glu_grad_kernel(const float* pre, const float* dh, float* dpre, float* h, int64_t MF, int F,
-                int act) {
+// dh of an output: [da | db] to `dpre` and h, at pre = [a | b].
+struct GradF32 {
+  static constexpr bool DUAL = false;
+  const float* pre;
+  float *dpre, *h;
+  int act;
+  __device__ __forceinline__ void tile(int m, int n0, const float (&d)[4], int col, int M, int N) const {
+    if (m >= M) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = n0 + col + i;
+      if (n >= N) break;
+      const int64_t ia = (int64_t)m * 2 * N + n, ib = ia + N;
+      const float a = pre[ia], b = pre[ib];
+      float f, df;
+      act_both(act, a, f, df);
+      dpre[ia] = d[i] * b * df;
+      dpre[ib] = d[i] * f;
+      h[(int64_t)m * N + n] = f * b;
+    }
+  }
+};
+
+// Column sums of in[0] [M, N0] and in[1] [M, N1] in one launch, out (+)= sums.
+struct Sums {
+  const void* in[2];
+  void* out[2];
+  int N[2];
+};
+template <typename T, typename O>
+__global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, int accumulate) {
+  __shared__ float red[16][33];
   pdl_wait();
   pdl_trigger();
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < MF;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t m = i / F;
-    const int f = (int)(i - m * F);
-    const int64_t ia = m * 2 * F + f, ib = ia + F;
-    const float a = pre[ia], b = pre[ib], d = dh[i];
-    float g, dg;
-    act_both(act, a, g, dg);
-    dpre[ia] = d * b * dg;
-    dpre[ib] = d * g;
-    h[i] = g * b;
+  const int x = threadIdx.x, y = threadIdx.y, first = (s.N[0] + 31) / 32;
+  const int which = (int)blockIdx.x < first ? 0 : 1;
+  const int n = ((int)blockIdx.x - (which ? first : 0)) * 32 + x, N = s.N[which];
+  const T* in = static_cast<const T*>(s.in[which]);
+  float v = 0.f;
+  if (n < N) {
+#pragma unroll 8
+    for (int m = y; m < M; m += 16) v += ld_elem(in, (int64_t)m * N + n);
+  }
+  red[y][x] = v;
+  __syncthreads();
+  if (y == 0 && n < N) {
+    for (int i = 1; i < 16; ++i) v += red[i][x];
+    O* out = static_cast<O*>(s.out[which]);
+    st_elem(out, n, accumulate ? ld_elem(out, n) + v : v);
   }
 }
 
@@ -145,8 +186,6 @@ __global__ void __launch_bounds__(256) cast_kernel(const float* in, T* out, int 
   if (i < n) st_elem(out, i, in[i]);
 }
 
-int grid_for(int64_t n) { return (int)std::min<int64_t>((n + 255) / 256, 152 * 16); }
-
 struct Gemm : GemmArgs {
   Gemm(int m, int n, int k, DType t) {
     M = m;
@@ -155,6 +194,12 @@ struct Gemm : GemmArgs {
     in_t = aux_t = t;
   }
 };
+
+#define OASES_TRY(expr)                       \
+  do {                                        \
+    const cudaError_t e_ = (expr);            \
+    if (e_ != cudaSuccess) return e_;         \
+  } while (0)
 
 // Column sums of in [M, N] (type t) to a bias gradient.
 cudaError_t bias_grad(const void* in, int M, int N, DType t, void* out, DType out_t, bool accumulate,
@@ -169,64 +214,55 @@ cudaError_t bias_grad(const void* in, int M, int N, DType t, void* out, DType ou
   return e;
 }
 
-#define OASES_TRY(expr)                       \
-  do {                                        \
-    const cudaError_t e_ = (expr);            \
-    if (e_ != cudaSuccess) return e_;         \
-  } while (0)
+// db1 = colsum(dpre), db2 = colsum(dy), each where it is wanted.
+cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, const oases_glu_grads& gr,
+                       float* part, float* tmp, cudaStream_t st) {
+  if (!gr.b1 && !gr.b2) return cudaSuccess;
+  if (s.M > DIRECT_SUM_ROWS) {
+    if (gr.b1)
+      OASES_TRY(bias_grad(dpre, s.M, 2 * s.F, s.t, gr.b1, s.grad_t, s.accumulate, part, tmp, st));
+    if (gr.b2)
+      OASES_TRY(bias_grad(dy, s.M, s.H, s.t, gr.b2, s.grad_t, s.accumulate, part, tmp, st));
+    return cudaSuccess;
+  }
+  const Sums q{{dpre, dy}, {gr.b1, gr.b2}, {gr.b1 ? 2 * s.F : 0, gr.b2 ? s.H : 0}};
+  const dim3 grid((unsigned)((q.N[0] + 31) / 32 + (q.N[1] + 31) / 32)), block(32, 16);
+  const int acc = s.accumulate ? 1 : 0;
+  if (s.t == DType::F32)
+    return launch_pdl(column_sums_kernel<float, float>, grid, block, 0, st, q, s.M, acc);
+  if (s.grad_t == DType::F32)
+    return launch_pdl(column_sums_kernel<__nv_bfloat16, float>, grid, block, 0, st, q, s.M, acc);
+  return launch_pdl(column_sums_kernel<__nv_bfloat16, __nv_bfloat16>, grid, block, 0, st, q, s.M, acc);
+}
 
 // [a | b] and h = act(a) b; h, pre and kept8 are each left out when null.
 cudaError_t project(const GluShape& s, const oases_glu_weights& w, const void* x, void* h, void* pre,
-                    void* kept8, float* scratch, cudaStream_t st) {
+                    void* kept8, cudaStream_t st) {
   if (s.t == DType::BF16) return glu_project_tc(s, x, w.w1, w.b1, h, pre, kept8, st);
-  Gemm g(s.M, 2 * s.F, s.H, s.t);
-  g.A = x;
-  g.lda = s.H;
-  g.B = w.w1;
-  g.ldb = s.H;
-  g.C = scratch;
-  g.ldc = 2 * s.F;
-  g.c_t = DType::F32;
-  OASES_TRY(gemm(g, st));
-  const int64_t MF = (int64_t)s.M * s.F;
-  return launch_pdl(glu_act_kernel, dim3(grid_for(MF)), dim3(256), 0, st, scratch,
-                    (const float*)w.b1, (float*)h, (float*)pre, MF, s.F, s.act);
+  const f32::Args g{s.M, s.F, s.H, (const float*)x, s.H, (const float*)w.w1, s.H, s.F, 0};
+  return f32::launch<UpF32, true, true>(
+      g, UpF32{(const float*)w.b1, (float*)h, (float*)pre, s.act}, st);
 }
 
 cudaError_t fwd(const GluShape& s, const oases_glu_weights& w, const void* x, const void* resid,
                 void* y, void* saved, char* ws, cudaStream_t st) {
-  const Layout l = layout(s, false);
-  void* h = ws + l.h;
+  void* h = ws + layout(s, false).h;
   OASES_TRY(project(s, w, x, h, s.keep == OASES_GLU_KEEP_PRE ? saved : nullptr,
-                    s.keep == OASES_GLU_KEEP_MXFP8 ? saved : nullptr,
-                    reinterpret_cast<float*>(ws + l.pre), st));
+                    s.keep == OASES_GLU_KEEP_MXFP8 ? saved : nullptr, st));
   if (s.t == DType::BF16) return glu_down_tc(s, h, w.w2, w.b2, resid, y, st);
-  Gemm g(s.M, s.H, s.F, s.t);
-  g.A = h;
-  g.lda = s.F;
-  g.B = w.w2;
-  g.ldb = s.F;
-  g.C = y;
-  g.ldc = s.H;
-  g.c_t = s.t;
-  g.bias = w.b2;
-  if (resid) {
-    if (!w.b2) {  // BiasResid with a zero bias
-      OASES_TRY(cudaMemsetAsync(ws + l.bias, 0, (size_t)s.H * 4, st));
-      g.bias = ws + l.bias;
-    }
-    g.epi = Epi::BiasResid;
-    g.aux = resid;
-    g.ld_aux = s.H;
-  } else {
-    g.epi = w.b2 ? Epi::Bias : Epi::Store;
-  }
-  return gemm(g, st);
+  const f32::Args g{s.M, s.H, s.F, (const float*)h, s.F, (const float*)w.w2, s.F, 0, 0};
+  return f32::launch<f32::Out, true, true>(
+      g, f32::Out{(float*)y, s.H, nullptr, (const float*)w.b2, (const float*)resid, 0}, st);
 }
 
 // dW [N, K] (+)= A^T B over the rows, A [M, N], B [M, K].
 cudaError_t weight_grad(const GluShape& s, const void* A, int N, const void* B, int K, void* out,
                         cudaStream_t st) {
+  if (s.t == DType::F32) {
+    const f32::Args g{N, K, s.M, (const float*)A, N, (const float*)B, K, 0, 0};
+    return f32::launch<f32::Out, false, false>(
+        g, f32::Out{(float*)out, K, nullptr, nullptr, nullptr, s.accumulate}, st);
+  }
   Gemm g(N, K, s.M, s.t);
   g.A = A;
   g.lda = N;
@@ -245,12 +281,10 @@ cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
                 const void* saved, void* dx, const oases_glu_grads& gr, char* ws, cudaStream_t st) {
   const Layout l = layout(s, true);
   void *h = ws + l.h, *dpre = ws + l.dpre;
-  float* part = reinterpret_cast<float*>(ws + l.part);
-  float* tmp = reinterpret_cast<float*>(ws + l.bias);
   const void *pre = saved, *kept8 = nullptr;
   if (s.keep == OASES_GLU_KEEP_NONE) {
-    float* p = reinterpret_cast<float*>(ws + l.pre);
-    OASES_TRY(project(s, w, x, nullptr, p, nullptr, p, st));
+    void* p = ws + l.pre;
+    OASES_TRY(project(s, w, x, nullptr, p, nullptr, st));
     pre = p;
   } else if (s.keep == OASES_GLU_KEEP_MXFP8) {
     pre = nullptr;
@@ -259,39 +293,32 @@ cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
   if (s.t == DType::BF16) {
     OASES_TRY(glu_grad_tc(s, dy, w.w2, pre, kept8, dpre, h, st));
   } else {
-    float* dh = reinterpret_cast<float*>(ws + l.dh);
-    Gemm g(s.M, s.F, s.H, s.t);
-    g.A = dy;
-    g.lda = s.H;
-    g.B = w.w2;
-    g.ldb = s.F;
-    g.b_kmajor = false;
-    g.C = dh;
-    g.ldc = s.F;
-    g.c_t = DType::F32;
-    OASES_TRY(gemm(g, st));
-    const int64_t MF = (int64_t)s.M * s.F;
-    OASES_TRY(launch_pdl(glu_grad_kernel, dim3(grid_for(MF)), dim3(256), 0, st, (const float*)pre,
-                         (const float*)dh, (float*)dpre, (float*)h, MF, s.F, s.act));
+    const f32::Args g{s.M, s.F, s.H, (const float*)dy, s.H, (const float*)w.w2, s.F, 0, 0};
+    OASES_TRY((f32::launch<GradF32, true, false>(
+        g, GradF32{(const float*)pre, (float*)dpre, (float*)h, s.act}, st)));
   }
   if (gr.w2) OASES_TRY(weight_grad(s, dy, s.H, h, s.F, gr.w2, st));
   if (gr.w1) OASES_TRY(weight_grad(s, dpre, 2 * s.F, x, s.H, gr.w1, st));
-  if (gr.b2) OASES_TRY(bias_grad(dy, s.M, s.H, s.t, gr.b2, s.grad_t, s.accumulate, part, tmp, st));
-  if (gr.b1)
-    OASES_TRY(bias_grad(dpre, s.M, 2 * s.F, s.t, gr.b1, s.grad_t, s.accumulate, part, tmp, st));
   if (dx) {
-    Gemm q(s.M, s.H, 2 * s.F, s.t);
-    q.A = dpre;
-    q.lda = 2 * s.F;
-    q.B = w.w1;
-    q.ldb = s.H;
-    q.b_kmajor = false;
-    q.C = dx;
-    q.ldc = s.H;
-    q.c_t = s.dx_t;
-    OASES_TRY(gemm(q, st));
+    if (s.t == DType::F32) {
+      const f32::Args g{s.M, s.H, 2 * s.F, (const float*)dpre, 2 * s.F, (const float*)w.w1, s.H, 0, 0};
+      OASES_TRY((f32::launch<f32::Out, true, false>(
+          g, f32::Out{(float*)dx, s.H, nullptr, nullptr, nullptr, 0}, st)));
+    } else {
+      Gemm q(s.M, s.H, 2 * s.F, s.t);
+      q.A = dpre;
+      q.lda = 2 * s.F;
+      q.B = w.w1;
+      q.ldb = s.H;
+      q.b_kmajor = false;
+      q.C = dx;
+      q.ldc = s.H;
+      q.c_t = s.dx_t;
+      OASES_TRY(gemm(q, st));
+    }
   }
-  return cudaSuccess;
+  return bias_grads(s, dpre, dy, gr, reinterpret_cast<float*>(ws + l.part),
+                    reinterpret_cast<float*>(ws + l.bias), st);
 }
 
 bool misaligned(std::initializer_list<const void*> ps) {

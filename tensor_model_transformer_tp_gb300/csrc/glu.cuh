@@ -19,6 +19,35 @@ struct GluShape {
 // Kept activations (oases_glu_keep): where the scales of the 8-bit form start.
 inline size_t saved_scale_offset(const GluShape& s) { return align256(2 * (size_t)s.M * s.ldq); }
 
+// SiLU and its derivative: s = 1 / (1 + e^-a), act = a s,
+// act' = s (1 + a (1 - s)) = s + act (1 - s).  Hardware base-2 exponential and
+// reciprocal (relative error ~2^-22); an exponential that overflows gives
+// s = 0, one that underflows s = 1.
+__device__ __forceinline__ void silu(float a, float& f, float& s) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * a));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+  f = a * s;
+}
+__device__ __forceinline__ void act_both_fast(int act, float a, float& f, float& df) {
+  if (act == OASES_ACT_SILU) {
+    float s;
+    silu(a, f, s);
+    df = fmaf(f, 1.0f - s, s);
+  } else {
+    float cdf, pdf;
+    gelu_cdf_pdf(a, cdf, pdf);
+    f = a * cdf;
+    df = fmaf(a, pdf, cdf);
+  }
+}
+__device__ __forceinline__ float act_fast(int act, float a) {
+  if (act != OASES_ACT_SILU) return gelu_f(a);
+  float f, s;
+  silu(a, f, s);
+  return f;
+}
+
 // bf16, tensor cores.
 // [a | b] = x w1^T + b1 of every row, and from the fp32 accumulators
 //   h = act(a) b      (h given)
@@ -34,5 +63,12 @@ cudaError_t glu_grad_tc(const GluShape& s, const void* dy, const void* w2, const
 cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const void* b2,
                         const void* resid, void* y, cudaStream_t st);
 int glu_read_and_clear_error();
+// The forward's two products for at most GLU_FEW_ROWS rows (glu_few.cu).
+constexpr int GLU_FEW_ROWS = 128;
+cudaError_t glu_project_few(const GluShape& s, const void* x, const void* w1, const void* b1,
+                            void* h, void* pre, void* kept8, cudaStream_t st);
+cudaError_t glu_down_few(const GluShape& s, const void* h, const void* w2, const void* b2,
+                         const void* resid, void* y, cudaStream_t st);
+int glu_few_read_and_clear_error();
 
 }  // namespace oases

@@ -12,29 +12,6 @@ using core::WarpBase;
 using core::pack2;
 using core::unpack2;
 
-// SiLU of a pair and its derivative: s = 1 / (1 + e^-a), act = a s,
-// act' = s (1 + a (1 - s)) = s + act (1 - s).  Hardware base-2 exponential and
-// reciprocal (relative error ~2^-22); an exponential that overflows gives
-// s = 0, one that underflows s = 1.
-__device__ __forceinline__ void silu(float a, float& f, float& s) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * a));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-  f = a * s;
-}
-__device__ __forceinline__ void act_both(int act, float a, float& f, float& df) {
-  if (act == OASES_ACT_SILU) {
-    float s;
-    silu(a, f, s);
-    df = fmaf(f, 1.0f - s, s);
-  } else {
-    float cdf, pdf;
-    gelu_cdf_pdf(a, cdf, pdf);
-    f = a * cdf;
-    df = fmaf(a, pdf, cdf);
-  }
-}
-
 // ---- projections, activation and product -------------------------------------
 // Tiles of 256 rows x 128 columns of a and the same of b (DUAL): every
 // accumulator pair (a, b) of an output is in one thread, so h, and what is kept
@@ -246,8 +223,8 @@ struct EpiGrad {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float f0, f1, g0, g1;
-            act_both(e.act, a[2 * i], f0, g0);
-            act_both(e.act, a[2 * i + 1], f1, g1);
+            act_both_fast(e.act, a[2 * i], f0, g0);
+            act_both_fast(e.act, a[2 * i + 1], f1, g1);
             const float d0 = d[2 * i], d1 = d[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
             wa[16 * hh + i] = pack2(d0 * b0 * g0, d1 * b1 * g1);
             wb[16 * hh + i] = pack2(d0 * f0, d1 * f1);
@@ -324,6 +301,7 @@ cudaError_t grad(const GluShape& s, const void* dy, const void* w2, const void* 
 
 cudaError_t glu_project_tc(const GluShape& s, const void* x, const void* w1, const void* b1,
                            void* h, void* pre, void* kept8, cudaStream_t st) {
+  if (s.M <= GLU_FEW_ROWS && h) return glu_project_few(s, x, w1, b1, h, pre, kept8, st);
   if (kept8) return project<OASES_GLU_KEEP_MXFP8>(s, x, w1, b1, h, nullptr, kept8, st);
   if (pre) return project<OASES_GLU_KEEP_PRE>(s, x, w1, b1, h, pre, nullptr, st);
   return project<OASES_GLU_KEEP_NONE>(s, x, w1, b1, h, nullptr, nullptr, st);
@@ -337,6 +315,7 @@ cudaError_t glu_grad_tc(const GluShape& s, const void* dy, const void* w2, const
 
 cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const void* b2,
                         const void* resid, void* y, cudaStream_t st) {
+  if (s.M <= GLU_FEW_ROWS) return glu_down_few(s, h, w2, b2, resid, y, st);
   using E = core::EpiOut;
   E::Params e = {};
   if (!core::out_map(&e, y, DType::BF16, s.M, s.H, s.H)) return cudaErrorInvalidValue;
@@ -344,12 +323,14 @@ cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const 
   e.resid = static_cast<const __nv_bfloat16*>(resid);
   core::Operands o{s.M, s.H, s.F, h, s.F, w2, s.F};
   const int tiles256 = (s.M + 127) / 128 * ((s.H + 255) / 256);
-  if (s.M <= 128) return core::launch<E, 128, true, true, 1>(o, e, st);
   if (2 * tiles256 < core::sm_count() || s.H <= 128)
     return core::launch<E, 128, true, true, 2>(o, e, st);
   return core::launch<E, 256, true, true, 2>(o, e, st);
 }
 
-int glu_read_and_clear_error() { return core::read_and_clear_error(); }
+int glu_read_and_clear_error() {
+  const int v = core::read_and_clear_error(), w = glu_few_read_and_clear_error();
+  return v ? v : w;
+}
 
 }  // namespace oases

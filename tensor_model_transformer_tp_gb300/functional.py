@@ -13,16 +13,17 @@ backward functions are called with what the forward returned.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 from typing import Dict, Optional, Tuple
 
 import torch
 
-from . import (ACT, KEEP, CeDesc, GluDesc, GluGrads, GluWeights, oases_ce_bwd, oases_ce_fwd,
-               oases_ce_workspace_bytes, oases_glu_bwd, oases_glu_fwd, oases_glu_saved_bytes,
-               oases_glu_workspace_bytes)
+from . import (ACT, KEEP, CeDesc, GluDesc, GluGrads, GluWeights, _check as _check_status, lib,
+               oases_ce_workspace_bytes, oases_glu_saved_bytes, oases_glu_workspace_bytes)
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
+_NAMES = ("w1", "b1", "w2", "b2")
 
 
 def _need(ok: bool, what: str) -> None:
@@ -30,40 +31,47 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _check(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, device) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape:
+def _sig(t: Optional[torch.Tensor]):
+    """What a plan is checked against: shape, type and CUDA device (-1 for the
+    CPU); None where there is no tensor."""
+    if t is None:
+        return None
+    try:
+        if t.is_contiguous():
+            return t.shape, t.dtype, t.get_device()
+    except AttributeError:
+        raise ValueError("expected a tensor or None, got %s" % type(t)) from None
+    raise ValueError("a tensor of shape %s is not contiguous" % (tuple(t.shape),))
+
+
+def _match(name: str, sig, shape: tuple, dtype: torch.dtype, device) -> None:
+    if sig is None or tuple(sig[0]) != shape or sig[1] != dtype:
         raise ValueError("%s must be a %s tensor of shape %s, got %s" % (
-            name, dtype, shape, (t.dtype, tuple(t.shape)) if isinstance(t, torch.Tensor) else type(t)))
-    if t.device != device:
-        raise ValueError("%s is on %s, x on %s" % (name, t.device, device))
-    if not t.is_contiguous():
-        raise ValueError("%s is not contiguous" % name)
+            name, dtype, shape, None if sig is None else (sig[1], tuple(sig[0]))))
+    if sig[2] != device:
+        raise ValueError("%s is on device %d, x on %d" % (name, sig[2], device))
 
 
-def _rows(x: torch.Tensor) -> Tuple[int, int]:
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a [rows, hidden] tensor")
-    _need(x.dtype in _CODE, "x must be float32 or bfloat16, got %s" % x.dtype)
-    _need(x.is_cuda, "x must be on a CUDA device, got %s" % x.device)
-    _need(x.is_contiguous(), "x is not contiguous")
-    return x.shape[0], x.shape[1]
+def _rows(x) -> Tuple[int, int]:
+    _need(x is not None and len(x[0]) == 2, "x must be a [rows, hidden] tensor")
+    _need(x[1] in _CODE, "x must be float32 or bfloat16, got %s" % (x[1],))
+    _need(x[2] >= 0, "x must be on a CUDA device")
+    return x[0][0], x[0][1]
 
 
-class _on:
-    """The tensors' device, current for the call."""
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, device):
-        self.device = device
 
-    def __enter__(self):
-        self.guard = None
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(fn, index: int, *args) -> None:
+    """One library call on torch's current stream of device ``index``, made current."""
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _check_status(st)
 
 
 def _bytes(n: int, device) -> Optional[torch.Tensor]:
@@ -71,26 +79,66 @@ def _bytes(n: int, device) -> Optional[torch.Tensor]:
 
 
 # ---- gated feed-forward block ---------------------------------------------------
-@functools.lru_cache(maxsize=256)
-def _glu_desc(dtype, rows, hidden, ffn, act, keep, dx_dtype, grad_dtype, accumulate):
-    d = GluDesc(dtype, rows, hidden, ffn, act, keep, dx_dtype, grad_dtype, accumulate)
-    return (d, oases_glu_saved_bytes(d), oases_glu_workspace_bytes(d, False),
-            oases_glu_workspace_bytes(d, True))
-
-
-def _glu_weights(x, weights: Dict[str, torch.Tensor], hidden: int):
-    unknown = set(weights) - {"w1", "b1", "w2", "b2"}
-    _need(not unknown, "unknown weights %s" % sorted(unknown))
-    _need("w1" in weights and "w2" in weights, "weights needs w1 and w2")
-    w2 = weights["w2"]
-    _need(isinstance(w2, torch.Tensor) and w2.dim() == 2, "w2 must be [hidden, ffn]")
-    ffn = w2.shape[1]
+# Plans are checked once per combination of shapes, types and options.
+def _glu_shapes(x, w):
+    rows, hidden = _rows(x)
+    _need(w[0] is not None and w[2] is not None, "weights needs w1 and w2")
+    _need(len(w[2][0]) == 2, "w2 must be [hidden, ffn]")
+    ffn = w[2][0][1]
     shapes = {"w1": (2 * ffn, hidden), "b1": (2 * ffn,), "w2": (hidden, ffn), "b2": (hidden,)}
-    for k, v in weights.items():
-        if v is not None:
-            _check(k, v, shapes[k], x.dtype, x.device)
-    _need(weights["w1"] is not None, "weights needs w1 and w2")
-    return ffn, shapes
+    for name, sig in zip(_NAMES, w):
+        if sig is not None:
+            _match(name, sig, shapes[name], x[1], x[2])
+    return rows, hidden, ffn, shapes
+
+
+def _glu_options(act, save):
+    _need(act in ACT, "act must be one of %s" % sorted(ACT))
+    _need(save in KEEP, "save must be one of %s" % sorted(KEEP))
+
+
+@functools.lru_cache(maxsize=512)
+def _glu_fwd_plan(x, w, resid, y, act, save):
+    rows, hidden, ffn, _ = _glu_shapes(x, w)
+    _glu_options(act, save)
+    for name, sig in (("resid", resid), ("y", y)):
+        if sig is not None:
+            _match(name, sig, (rows, hidden), x[1], x[2])
+    t = _CODE[x[1]]
+    d = GluDesc(t, rows, hidden, ffn, ACT[act], KEEP[save], t, t, 0)
+    return (ctypes.byref(d), oases_glu_saved_bytes(d), oases_glu_workspace_bytes(d, False),
+            (rows, 2 * ffn))
+
+
+@functools.lru_cache(maxsize=512)
+def _glu_bwd_plan(x, w, dy, saved, grads, act, save, dx_dtype):
+    rows, hidden, ffn, shapes = _glu_shapes(x, w)
+    _glu_options(act, save)
+    _match("dy", dy, (rows, hidden), x[1], x[2])
+    accumulate = grads is not None
+    if accumulate:
+        for name, sig, weight in zip(_NAMES, grads, w):
+            if sig is not None:
+                _need(weight is not None, "grads[%r] has no weight" % name)
+                _match("grads[%r]" % name, sig, shapes[name], torch.float32, x[2])
+    _need(dx_dtype in (None, x[1], torch.float32), "dx_dtype must be x's type or float32")
+    t = _CODE[x[1]]
+    d = GluDesc(t, rows, hidden, ffn, ACT[act], KEEP[save], t if dx_dtype is None else
+                _CODE[dx_dtype], 0 if accumulate else t, int(accumulate))
+    if save == "none":
+        _need(saved is None, "saved is given, but save is \"none\"")
+    elif save == "pre":
+        _match("saved", saved, (rows, 2 * ffn), x[1], x[2])
+    else:
+        _match("saved", saved, (oases_glu_saved_bytes(d),), torch.uint8, x[2])
+    return ctypes.byref(d), oases_glu_workspace_bytes(d, True)
+
+
+def _named(tensors: Dict[str, torch.Tensor], what: str):
+    if not tensors.keys() <= set(_NAMES):
+        raise ValueError("unknown %s %s" % (what, sorted(set(tensors) - set(_NAMES))))
+    get = tensors.get
+    return get("w1"), get("b1"), get("w2"), get("b2")
 
 
 def glu_fwd(x: torch.Tensor, weights: Dict[str, torch.Tensor], act: str = "silu",
@@ -106,26 +154,21 @@ def glu_fwd(x: torch.Tensor, weights: Dict[str, torch.Tensor], act: str = "silu"
     Returns (y, kept activations or None).  y may be given (resid itself, for
     an in-place residual).
     """
-    rows, hidden = _rows(x)
-    ffn, _ = _glu_weights(x, weights, hidden)
-    _need(act in ACT, "act must be one of %s" % sorted(ACT))
-    _need(save in KEEP, "save must be one of %s" % sorted(KEEP))
-    if resid is not None:
-        _check("resid", resid, (rows, hidden), x.dtype, x.device)
+    w1, b1, w2, b2 = _named(weights, "weights")
+    desc, n_saved, n_ws, kept = _glu_fwd_plan(
+        _sig(x), (_sig(w1), _sig(b1), _sig(w2), _sig(b2)), _sig(resid), _sig(y), act, save)
+    device = x.device
     if y is None:
         y = torch.empty_like(x)
-    else:
-        _check("y", y, (rows, hidden), x.dtype, x.device)
-    t = _CODE[x.dtype]
-    desc, n_saved, n_ws, _ = _glu_desc(t, rows, hidden, ffn, ACT[act], KEEP[save], t, t, 0)
     saved = None
     if save == "pre":
-        saved = torch.empty((rows, 2 * ffn), dtype=x.dtype, device=x.device)
+        saved = torch.empty(kept, dtype=x.dtype, device=device)
     elif save == "mxfp8":
-        saved = torch.empty(n_saved, dtype=torch.uint8, device=x.device)
-    with _on(x.device) as stream:
-        oases_glu_fwd(desc, GluWeights.of(weights), x, resid, y, saved, _bytes(n_ws, x.device),
-                      n_ws, stream)
+        saved = torch.empty(n_saved, dtype=torch.uint8, device=device)
+    ws = _bytes(n_ws, device)
+    w = GluWeights(_ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2))
+    _call(lib().oases_glu_fwd, x.get_device(), desc, ctypes.byref(w), _ptr(x), _ptr(resid), _ptr(y),
+          _ptr(saved), _ptr(ws), n_ws)
     return y, saved
 
 
@@ -142,50 +185,43 @@ def glu_bwd(x: torch.Tensor, dy: torch.Tensor, weights: Dict[str, torch.Tensor],
     added to (+=), the convention of the block; the rest are left out.
     dx_dtype: x's type (default) or float32.  Returns (dx or None, grads).
     """
-    rows, hidden = _rows(x)
-    ffn, shapes = _glu_weights(x, weights, hidden)
-    _need(act in ACT, "act must be one of %s" % sorted(ACT))
-    _need(save in KEEP, "save must be one of %s" % sorted(KEEP))
-    _check("dy", dy, (rows, hidden), x.dtype, x.device)
-    accumulate = grads is not None
-    if accumulate:
-        for k, v in grads.items():
-            _need(weights.get(k) is not None, "grads[%r] has no weight" % k)
-            _check("grads[%r]" % k, v, shapes[k], torch.float32, x.device)
-    else:
+    w1, b1, w2, b2 = _named(weights, "weights")
+    given = None if grads is None else _named(grads, "grads")
+    desc, n_ws = _glu_bwd_plan(
+        _sig(x), (_sig(w1), _sig(b1), _sig(w2), _sig(b2)), _sig(dy), _sig(saved),
+        None if given is None else tuple(_sig(g) for g in given), act, save, dx_dtype)
+    device = x.device
+    if grads is None:
         grads = {k: torch.empty_like(v) for k, v in weights.items() if v is not None}
-    dx_dtype = x.dtype if dx_dtype is None else dx_dtype
-    _need(dx_dtype in (x.dtype, torch.float32), "dx_dtype must be x's type or float32")
-    t = _CODE[x.dtype]
-    desc, n_saved, _, n_ws = _glu_desc(t, rows, hidden, ffn, ACT[act], KEEP[save], _CODE[dx_dtype],
-                                       0 if accumulate else t, int(accumulate))
-    if save == "none":
-        _need(saved is None, "saved is given, but save is \"none\"")
-    elif save == "pre":
-        _check("saved", saved, (rows, 2 * ffn), x.dtype, x.device)
-    else:
-        _check("saved", saved, (n_saved,), torch.uint8, x.device)
-    dx = torch.empty((rows, hidden), dtype=dx_dtype, device=x.device) if need_dx else None
-    with _on(x.device) as stream:
-        oases_glu_bwd(desc, GluWeights.of(weights), x, dy, saved, dx, GluGrads.of(grads),
-                      _bytes(n_ws, x.device), n_ws, stream)
+        given = _named(grads, "grads")
+    dx = torch.empty_like(x, dtype=dx_dtype) if need_dx else None
+    ws = _bytes(n_ws, device)
+    w = GluWeights(_ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2))
+    g = GluGrads(*[_ptr(v) for v in given])
+    _call(lib().oases_glu_bwd, x.get_device(), desc, ctypes.byref(w), _ptr(x), _ptr(dy), _ptr(saved),
+          _ptr(dx), ctypes.byref(g), _ptr(ws), n_ws)
     return dx, grads
 
 
 # ---- cross entropy of the linear head -----------------------------------------------
-@functools.lru_cache(maxsize=256)
-def _ce_desc(ignore_index, dtype, rows, hidden, vocab, per_row, grad_dtype, accumulate):
-    d = CeDesc(ignore_index, dtype, rows, hidden, vocab, per_row, grad_dtype, accumulate)
-    return d, oases_ce_workspace_bytes(d, False), oases_ce_workspace_bytes(d, True)
-
-
-def _ce_check(x, w, targets):
+@functools.lru_cache(maxsize=512)
+def _ce_plan(x, w, targets, lse, dloss, dw, backward, ignore_index):
     rows, hidden = _rows(x)
-    _need(isinstance(w, torch.Tensor) and w.dim() == 2 and w.shape[0] > 0,
-          "w must be a [vocab, hidden] tensor")
-    _check("w", w, (w.shape[0], hidden), x.dtype, x.device)
-    _check("targets", targets, (rows,), torch.int64, x.device)
-    return rows, hidden, w.shape[0]
+    _need(w is not None and len(w[0]) == 2 and w[0][0] > 0, "w must be a [vocab, hidden] tensor")
+    vocab = w[0][0]
+    _match("w", w, (vocab, hidden), x[1], x[2])
+    _match("targets", targets, (rows,), torch.int64, x[2])
+    t, per_row, accumulate = _CODE[x[1]], False, dw is not None
+    if backward:
+        _match("lse", lse, (rows,), torch.float32, x[2])
+        _need(dloss is not None, "dloss must be a tensor")
+        per_row = tuple(dloss[0]) not in ((), (1,))
+        _match("dloss", dloss, (rows,) if per_row else tuple(dloss[0]), torch.float32, x[2])
+    if accumulate:
+        _match("dw", dw, (vocab, hidden), torch.float32, x[2])
+    d = CeDesc(ignore_index, t, rows, hidden, vocab, int(per_row), 0 if accumulate else t,
+               int(accumulate))
+    return ctypes.byref(d), oases_ce_workspace_bytes(d, backward), rows
 
 
 def ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
@@ -196,13 +232,14 @@ def ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     target is ignore_index have loss 0; another target outside [0, vocab)
     gives NaN.  The logits are not kept.
     """
-    rows, hidden, vocab = _ce_check(x, w, targets)
-    t = _CODE[x.dtype]
-    desc, n_ws, _ = _ce_desc(ignore_index, t, rows, hidden, vocab, 0, t, 0)
-    loss = torch.empty(rows, dtype=torch.float32, device=x.device)
-    lse = torch.empty(rows, dtype=torch.float32, device=x.device)
-    with _on(x.device) as stream:
-        oases_ce_fwd(desc, x, w, targets, loss, lse, _bytes(n_ws, x.device), n_ws, stream)
+    desc, n_ws, rows = _ce_plan(_sig(x), _sig(w), _sig(targets), None, None, None, False,
+                                ignore_index)
+    device = x.device
+    loss = torch.empty(rows, dtype=torch.float32, device=device)
+    lse = torch.empty(rows, dtype=torch.float32, device=device)
+    ws = _bytes(n_ws, device)
+    _call(lib().oases_ce_fwd, x.get_device(), desc, _ptr(x), _ptr(w), _ptr(targets), _ptr(loss), _ptr(lse),
+          _ptr(ws), n_ws)
     return loss, lse
 
 
@@ -217,23 +254,16 @@ def ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.T
     dw None: returned in x's type.  dw a float32 [vocab, hidden] tensor: it is
     added to (+=) and returned.
     """
-    rows, hidden, vocab = _ce_check(x, w, targets)
-    _check("lse", lse, (rows,), torch.float32, x.device)
-    _need(isinstance(dloss, torch.Tensor), "dloss must be a tensor")
-    per_row = tuple(dloss.shape) not in ((), (1,))
-    _check("dloss", dloss, (rows,) if per_row else tuple(dloss.shape), torch.float32, x.device)
-    accumulate = dw is not None
-    _need(need_dw or not accumulate, "dw is given, but need_dw is false")
-    if accumulate:
-        _check("dw", dw, (vocab, hidden), torch.float32, x.device)
-    elif need_dw:
+    desc, n_ws, _ = _ce_plan(_sig(x), _sig(w), _sig(targets), _sig(lse), _sig(dloss), _sig(dw),
+                             True, ignore_index)
+    _need(need_dw or dw is None, "dw is given, but need_dw is false")
+    device = x.device
+    if dw is None and need_dw:
         dw = torch.empty_like(w)
-    t = _CODE[x.dtype]
-    desc, _, n_ws = _ce_desc(ignore_index, t, rows, hidden, vocab, int(per_row),
-                             0 if accumulate else t, int(accumulate))
     dx = torch.empty_like(x) if need_dx else None
-    with _on(x.device) as stream:
-        oases_ce_bwd(desc, x, w, targets, lse, dloss, dx, dw, _bytes(n_ws, x.device), n_ws, stream)
+    ws = _bytes(n_ws, device)
+    _call(lib().oases_ce_bwd, x.get_device(), desc, _ptr(x), _ptr(w), _ptr(targets), _ptr(lse), _ptr(dloss),
+          _ptr(dx), _ptr(dw), _ptr(ws), n_ws)
     return dx, dw
 
 
