@@ -29,7 +29,7 @@ __device__ __forceinline__ float ex2(float x) {
 // target's logit goes out as it is met.
 struct EpiStat {
   static constexpr bool DUAL = false, PAD_ROWS = false;
-  static constexpr int STG = 1024;  // unused
+  static constexpr int STG = 1024, WBARS = 0;  // unused
   struct Params {
     float2* part;  // [slots][M]
     float* at;     // [M]
@@ -37,6 +37,7 @@ struct EpiStat {
   };
   struct Warp : WarpBase {
     int64_t t;
+    template <int BN>
     __device__ __forceinline__ void before(const Params& e, const Problem& p, int mw, int, int) {
       const int m = mw + lane;
       t = m < p.M ? e.target[m] : -1;
@@ -92,15 +93,17 @@ struct EpiStat {
   };
 };
 
-// Joins the (r, s) of a row's slots in a fixed order: 32 rows per block, 16
-// threads per row over the slots.
+// Joins the (r, s) of a row's slots in a fixed order: RB rows per block (whole
+// sectors of `part` per slot), 512 / RB threads per row over the slots.
+template <int RB>
 __global__ void __launch_bounds__(512)
 ce_join_kernel(const float2* part, int slots, const float* at, const int64_t* target, int64_t ignore,
                int V, int M, float* loss, float* lse) {
-  __shared__ float2 red[16][33];
+  constexpr int Y = 512 / RB;
+  __shared__ float2 red[Y][RB + 1];
   pdl_wait();
   pdl_trigger();
-  const int x = threadIdx.x, y = threadIdx.y, m = blockIdx.x * 32 + x;
+  const int x = threadIdx.x % RB, y = threadIdx.x / RB, m = blockIdx.x * RB + x;
   float r = -INFINITY, s = 0.f;
   auto join = [&](float2 q) {
     const float top = fmaxf(r, q.x), ref = top == -INFINITY ? 0.f : top;
@@ -109,12 +112,18 @@ ce_join_kernel(const float2* part, int slots, const float* at, const int64_t* ta
   };
   if (m < M) {
 #pragma unroll 4
-    for (int i = y; i < slots; i += 16) join(part[(int64_t)i * M + m]);
+    for (int i = y; i < slots; i += Y) join(part[(int64_t)i * M + m]);
   }
   red[y][x] = make_float2(r, s);
-  __syncthreads();
+#pragma unroll
+  for (int o = Y / 2; o; o >>= 1) {
+    __syncthreads();
+    if (y < o) {
+      join(red[y + o][x]);
+      red[y][x] = make_float2(r, s);
+    }
+  }
   if (y == 0 && m < M) {
-    for (int i = 1; i < 16; ++i) join(red[i][x]);
     const float l = ((r == -INFINITY ? 0.f : r) + log2f(s)) * LN2;
     lse[m] = l;
     const int64_t t = target[m];
@@ -127,7 +136,7 @@ ce_join_kernel(const float2* part, int slots, const float* at, const int64_t* ta
 // rows without a loss are 0 whatever their logits are.
 struct EpiG {
   static constexpr bool DUAL = false, PAD_ROWS = false;
-  static constexpr int STG = 4096;
+  static constexpr int STG = 4096, WBARS = 0;
   struct Params {
     CUtensorMap g;  // boxes of 32 rows x 64 columns of the piece
     CeRows rows;
@@ -138,6 +147,7 @@ struct EpiG {
     int64_t t;
     float r, l2;
     bool dead;
+    template <int BN>
     __device__ __forceinline__ void before(const Params& e, const Problem& p, int mw, int, int) {
       const int m = mw + lane;
       t = -1;
@@ -279,7 +289,11 @@ cudaError_t ce_tc_fwd(const CeShape& s, const void* x, const void* w, const int6
 
 cudaError_t ce_join(const float2* part, int slots, const float* at, const int64_t* target,
                     const CeShape& s, int M, float* loss, float* lse, cudaStream_t st) {
-  return launch_pdl(ce_join_kernel, dim3((M + 31) / 32), dim3(32, 16), 0, st, part, slots, at, target,
+  // few rows: more threads per row, for the latency of the chain of joins
+  if (M <= 512)
+    return launch_pdl(ce_join_kernel<4>, dim3((M + 3) / 4), dim3(512), 0, st, part, slots, at, target,
+                      s.ignore, s.V, M, loss, lse);
+  return launch_pdl(ce_join_kernel<16>, dim3((M + 15) / 16), dim3(512), 0, st, part, slots, at, target,
                     s.ignore, s.V, M, loss, lse);
 }
 

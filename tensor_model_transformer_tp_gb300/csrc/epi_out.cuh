@@ -9,7 +9,7 @@ namespace core {
 
 struct EpiOut {
   static constexpr bool DUAL = false, PAD_ROWS = false;
-  static constexpr int STG = 4096;  // 32 rows x 128 bytes
+  static constexpr int STG = 4096, WBARS = 0;  // 32 rows x 128 bytes
   struct Params {
     CUtensorMap c;             // boxes of 32 rows x 128 bytes of C
     int f32;                   // C's type: fp32, else bf16
@@ -22,6 +22,7 @@ struct EpiOut {
   };
   struct Warp : WarpBase {
     float alpha;
+    template <int BN>
     __device__ __forceinline__ void before(const Params& e, const Problem&, int, int, int) {
       alpha = e.scale ? *e.scale : 1.f;
     }

@@ -38,7 +38,7 @@ constexpr int NTHREADS = 320;              // 2 control warps + 8 epilogue warps
 constexpr int64_t A_L2_BYTES = 48ll << 20;  // A up to this size stays in L2 across tile rounds
 constexpr int GROUP_M = 8;                 // row blocks per group of the tile order beyond it
 
-template <int BN, int CL, int STG>  // STG: staging bytes per epilogue warp
+template <int BN, int CL, int STG, int WBARS>  // STG, WBARS: staging bytes and barriers per epilogue warp
 struct Cfg {
   static constexpr int A_BYTES = BM * 128;
   static constexpr int B_BYTES = BN / CL * 128;
@@ -46,7 +46,7 @@ struct Cfg {
   static constexpr int EPI_BYTES = 8 * STG;
   static constexpr int STAGES = (226 * 1024 - EPI_BYTES - 1536) / STAGE;
   static constexpr int EPI_OFF = STAGES * STAGE;
-  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5) + 8;
+  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8 * WBARS) + 8;
   static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + BAR_BYTES + 1024;
   static constexpr int TMEM_COLS = 2 * BN;
   static_assert(STAGE % 1024 == 0 && STG % 1024 == 0, "swizzled tiles keep 1024-byte alignment");
@@ -66,7 +66,7 @@ template <class Epi, int BN, bool A_K, bool B_K, int CL>
 __global__ void __launch_bounds__(NTHREADS, 1)
 gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ typename Epi::Params ep, const Problem p) {
-  using C = Cfg<BN, CL, Epi::STG>;
+  using C = Cfg<BN, CL, Epi::STG, Epi::WBARS>;
   constexpr int BNH = BN / CL;                    // B rows held by this CTA
   constexpr int TN = Epi::DUAL ? BN / 2 : BN;     // output columns per tile
   constexpr uint32_t IDESC = ptx::idesc_bf16_f32(BM * CL, BN, !A_K, !B_K);
@@ -81,7 +81,7 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   auto tfull = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };
   auto tempty = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 + b); };
   const uint32_t drain = bars + 8u * (2 * C::STAGES + 4);
-  const uint32_t tslot = bars + 8u * (2 * C::STAGES + 5);
+  const uint32_t wbars = drain + 8, tslot = wbars + 8u * (8 * Epi::WBARS);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = CL > 1 ? (int)ptx::cluster_rank() : 0;
@@ -116,6 +116,7 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       ptx::mbar_init(tempty(b), 8 * CL);  // one arrival per epilogue warp of the pair
     }
     ptx::mbar_init(drain, 1);
+    for (int i = 0; i < 8 * Epi::WBARS; ++i) ptx::mbar_init(wbars + 8u * i, 1);
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -239,12 +240,14 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     w.stg = gbase + C::EPI_OFF + (warp - 2) * Epi::STG;
     w.stg_s = base + C::EPI_OFF + (warp - 2) * Epi::STG;
     w.lane = lane;
+    w.bars = wbars + 8u * (warp - 2) * Epi::WBARS;
+    w.init();
     int n = 0;
     for (int t = first; t < tiles; t += stride, ++n) {
       const int buf = n & 1;
       const Tile tl = tile_of(t);
       const int mw = tl.m0 + q * 32;
-      w.before(ep, p, mw, tl.n0, half);  // loads that do not wait for the accumulator
+      w.template before<BN>(ep, p, mw, tl.n0, half);  // loads that do not wait for the accumulator
       // the decision is warp-uniform: tcgen05.ld is warp-collective
       if (!__all_sync(0xffffffffu, ptx::mbar_wait(tfull(buf), ((uint32_t)n >> 1) & 1u))) {
         if (lane == 0) atomicExch(&g_core_error, 3);
@@ -263,6 +266,7 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           ptx::mbar_arrive(tempty(buf));
       }
     }
+    w.finish();
     if (lane == 0) ptx::bulk_wait0();  // stores performed before the CTA retires
   }
   ptx::tc_fence_before();
@@ -292,8 +296,14 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
 // Common state of an epilogue warp: its staging buffer and the store through it.
 struct WarpBase {
   uint8_t* stg;
-  uint32_t stg_s;
+  uint32_t stg_s, bars;
   int lane;
+  // hooks of an epilogue: set up; what a tile can do before its accumulator is
+  // there; whatever it has in flight is waited for before the CTA leaves
+  __device__ __forceinline__ void init() {}
+  template <int BN, class Params>
+  __device__ __forceinline__ void before(const Params&, const Problem&, int, int, int) {}
+  __device__ __forceinline__ void finish() {}
   // One row of 128 bytes per lane (32 words w) goes to the swizzled staging
   // buffer at stg + off, then lane 0 stores the box at (x, y); the TMA unit
   // clips rows and columns beyond the matrix.
@@ -328,7 +338,8 @@ struct WarpBase {
 
 // ---- host side ---------------------------------------------------------------
 // 2-D tensor map over a row-major [outer, inner] matrix with leading dimension
-// ld (elements), 128-byte swizzle, zero fill; false if it cannot be encoded.
+// ld (elements), box rows of 128 bytes with 128-byte swizzle or of 64 bytes with
+// 64-byte swizzle, zero fill; false if it cannot be encoded.
 inline bool tensor_map(CUtensorMap* out, const void* ptr, bool f32, uint64_t inner, uint64_t outer,
                        uint64_t ld, uint32_t box_inner, uint32_t box_outer) {
   typedef CUresult (*Fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -350,8 +361,8 @@ inline bool tensor_map(CUtensorMap* out, const void* ptr, bool f32, uint64_t inn
   const cuuint32_t box[2] = {box_inner, box_outer}, estr[2] = {1, 1};
   return fn(out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            box_inner * (f32 ? 4 : 2) == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline int sm_count() {
@@ -386,7 +397,7 @@ inline int slices_per_split(int K, int* splits) {
 
 template <class Epi, int BN, bool A_K, bool B_K, int CL>
 cudaError_t launch(const Operands& o, const typename Epi::Params& ep, cudaStream_t st) {
-  using C = Cfg<BN, CL, Epi::STG>;
+  using C = Cfg<BN, CL, Epi::STG, Epi::WBARS>;
   constexpr int TN = Epi::DUAL ? BN / 2 : BN;
   Problem p;
   p.M = o.M;

@@ -154,26 +154,47 @@ struct Sums {
   void* out[2];
   int N[2];
 };
+// Two neighbouring columns per thread (one 4- or 8-byte load per row; an odd N
+// goes a column at a time), 16 warps over the rows.
+template <typename T>
+__device__ __forceinline__ float2 ld_pair(const T* p, bool pair, bool second) {
+  if (pair) {
+    if constexpr (sizeof(T) == 4)
+      return *reinterpret_cast<const float2*>(p);
+    else
+      return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+  }
+  return make_float2(ld_elem(p, 0), second ? ld_elem(p, 1) : 0.f);
+}
 template <typename T, typename O>
 __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, int accumulate) {
-  __shared__ float red[16][33];
+  __shared__ float2 red[16][33];
   pdl_wait();
   pdl_trigger();
-  const int x = threadIdx.x, y = threadIdx.y, first = (s.N[0] + 31) / 32;
+  const int x = threadIdx.x, y = threadIdx.y, first = (s.N[0] + 63) / 64;
   const int which = (int)blockIdx.x < first ? 0 : 1;
-  const int n = ((int)blockIdx.x - (which ? first : 0)) * 32 + x, N = s.N[which];
-  const T* in = static_cast<const T*>(s.in[which]);
-  float v = 0.f;
+  const int n = ((int)blockIdx.x - (which ? first : 0)) * 64 + 2 * x, N = s.N[which];
+  const T* in = static_cast<const T*>(s.in[which]) + n;
+  const bool pair = N % 2 == 0, second = n + 1 < N;
+  float2 v = make_float2(0.f, 0.f);
   if (n < N) {
 #pragma unroll 8
-    for (int m = y; m < M; m += 16) v += ld_elem(in, (int64_t)m * N + n);
+    for (int m = y; m < M; m += 16) {
+      const float2 q = ld_pair(in + (int64_t)m * N, pair, second);
+      v.x += q.x;
+      v.y += q.y;
+    }
   }
   red[y][x] = v;
   __syncthreads();
   if (y == 0 && n < N) {
-    for (int i = 1; i < 16; ++i) v += red[i][x];
+    for (int i = 1; i < 16; ++i) {
+      v.x += red[i][x].x;
+      v.y += red[i][x].y;
+    }
     O* out = static_cast<O*>(s.out[which]);
-    st_elem(out, n, accumulate ? ld_elem(out, n) + v : v);
+    st_elem(out, n, accumulate ? ld_elem(out, n) + v.x : v.x);
+    if (second) st_elem(out, n + 1, accumulate ? ld_elem(out, n + 1) + v.y : v.y);
   }
 }
 
@@ -226,7 +247,7 @@ cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, cons
     return cudaSuccess;
   }
   const Sums q{{dpre, dy}, {gr.b1, gr.b2}, {gr.b1 ? 2 * s.F : 0, gr.b2 ? s.H : 0}};
-  const dim3 grid((unsigned)((q.N[0] + 31) / 32 + (q.N[1] + 31) / 32)), block(32, 16);
+  const dim3 grid((unsigned)((q.N[0] + 63) / 64 + (q.N[1] + 63) / 64)), block(32, 16);
   const int acc = s.accumulate ? 1 : 0;
   if (s.t == DType::F32)
     return launch_pdl(column_sums_kernel<float, float>, grid, block, 0, st, q, s.M, acc);

@@ -20,7 +20,9 @@ template <int KEEP>
 struct EpiDual {
   static constexpr bool DUAL = true;
   static constexpr bool PAD_ROWS = KEEP == OASES_GLU_KEEP_MXFP8;  // scales of the rows past M
-  static constexpr int STG = 4096;
+  // a buffer each for h and for what is kept of a and b: a tile's stores drain
+  // while the next tile is computed
+  static constexpr int STG = KEEP == OASES_GLU_KEEP_PRE ? 3 * 4096 : 4096, WBARS = 0;
   struct Params {
     CUtensorMap h, a, b;  // boxes of 32 rows x 64 columns of h, pre's halves
     const __nv_bfloat16* bias;
@@ -30,7 +32,6 @@ struct EpiDual {
     int kgroups;
   };
   struct Warp : WarpBase {
-    __device__ __forceinline__ void before(const Params&, const Problem&, int, int, int) {}
     __device__ __forceinline__ void add_bias(const __nv_bfloat16* src, int left, float (&v)[32]) {
 #pragma unroll
       for (int i = 0; i < 32; i += 8)
@@ -126,18 +127,16 @@ struct EpiDual {
         *reinterpret_cast<uint16_t*>(s + e.scale_stride) = (uint16_t)sb;
       }
       if (n >= p.N || mw >= p.M) return;
+      wait_free();
       if (e.want_h) {
-        wait_free();
         stage_row(wh);
         store_box(&e.h, n, mw);
       }
       if constexpr (KEEP == OASES_GLU_KEEP_PRE) {
-        wait_free();
-        stage_row(wa);
-        store_box(&e.a, n, mw);
-        wait_free();
-        stage_row(wb);
-        store_box(&e.b, n, mw);
+        stage_row(wa, 4096);
+        store_box(&e.a, n, mw, 4096);
+        stage_row(wb, 8192);
+        store_box(&e.b, n, mw, 8192);
       }
     }
   };
@@ -145,111 +144,171 @@ struct EpiDual {
 
 // ---- gradients of the projections --------------------------------------------
 // dh = dy W2 stays in the accumulator; the epilogue reads a and b of its
-// elements and writes da = dh b act'(a), db = dh act(a) and h = act(a) b.
+// elements and writes da = dh b act'(a), db = dh act(a) and h = act(a) b, 32
+// columns of a warp's 32 rows at a time.  Two staging sets of three 2 KB
+// buffers (64-byte rows, 64-byte swizzle) alternate: TMA brings a and b of the
+// next 32 columns into one while the other's are turned, in place, into da and
+// db, with h beside them, and stored.  (One row per lane straight from global
+// memory costs a cache-line lookup per lane and load: the kernel took 73 us
+// instead of 41 at 4096 x 1024 x 4096.)
+// EIGHT: a and b come from the 8-bit form, 32 bytes of a row per lane (whole
+// sectors), loaded one step ahead.
 template <bool EIGHT>
 struct EpiGrad {
   static constexpr bool DUAL = false, PAD_ROWS = false;
-  static constexpr int STG = 4096;
+  static constexpr int STG = 2 * 6144, WBARS = EIGHT ? 0 : 2;
   struct Params {
-    CUtensorMap da, db, h;  // boxes of 32 rows x 64 columns
-    const __nv_bfloat16* pre;  // [M, 2F]
+    CUtensorMap a, b;       // boxes of 32 rows x 32 columns of pre's halves
+    CUtensorMap da, db, h;  // of dpre's halves and of h
     const uint8_t *codes, *scales;
     int64_t ldq, code_stride, scale_stride;
     int kgroups, act;
   };
   struct Warp : WarpBase {
-    __device__ __forceinline__ void before(const Params&, const Problem&, int, int, int) {}
-    // 32 columns of one row; zeros past `left` columns (a multiple of 8)
-    __device__ __forceinline__ void load_pre(const __nv_bfloat16* src, int left, bool row, float (&v)[32]) {
+    uint32_t count, asked;  // 32-column steps taken by this warp, and requested
+    uint4 ca[2], cb[2];  // EIGHT: codes of the next step
+    uint32_t sa, sb;     // and their scale bytes
+    __device__ __forceinline__ void init() { count = asked = 0; }
+    // Request a and b of columns n .. n+31 for the step `step`.
+    __device__ __forceinline__ void request(const Params& e, const Problem& p, int mw, int n, uint32_t step) {
+      if constexpr (EIGHT) {
+        const int m = mw + lane, left = p.N - n;
+        sa = sb = 127;
+        ca[0] = ca[1] = cb[0] = cb[1] = make_uint4(0, 0, 0, 0);
+        if (m < p.M && left > 0) {
+          // codes rows are padded to 16 bytes, so a 16-byte load is whole
+          const uint8_t* q = e.codes + (int64_t)m * e.ldq + n;
+          const uint8_t* s = e.scales + sf_offset(m, n / MXB, e.kgroups);
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (row && i < left) u = __ldg(reinterpret_cast<const uint4*>(src + i));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = unpack2(w[k]);
-          v[i + 2 * k] = f.x;
-          v[i + 2 * k + 1] = f.y;
+          for (int i = 0; i < 2; ++i)
+            if (16 * i < left) {
+              ca[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
+              cb[i] = __ldg(reinterpret_cast<const uint4*>(q + e.code_stride) + i);
+            }
+          sa = __ldg(s);
+          sb = __ldg(s + e.scale_stride);
         }
+      } else if (lane == 0) {
+        ptx::bulk_wait_read0();  // the set's last stores have read it
+        const uint32_t set = step & 1u, at = stg_s + set * 6144;
+        ptx::mbar_arrive_expect_tx(bars + 8 * set, 4096);
+        ptx::tma_load_2d(at, &e.a, bars + 8 * set, n, mw);
+        ptx::tma_load_2d(at + 2048, &e.b, bars + 8 * set, n, mw);
+      }
+      asked = step + 1;
+    }
+    __device__ __forceinline__ void finish() {  // a request that no step took
+      if (!EIGHT && asked > count) ptx::mbar_wait(bars + 8 * (count & 1u), (count >> 1) & 1u);
+    }
+    template <int BN>
+    __device__ __forceinline__ void before(const Params& e, const Problem& p, int mw, int n0, int half) {
+      const int n = n0 + half * (BN / 2);
+      if (mw < p.M && n < p.N) request(e, p, mw, n, count);
+    }
+    __device__ __forceinline__ void codes_to(const uint4& c, float x, float* v) {
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 f = e4m3x2_values((uint16_t)(w[k / 2] >> (16 * (k % 2))));
+        v[2 * k] = f.x * x;
+        v[2 * k + 1] = f.y * x;
       }
     }
-    __device__ __forceinline__ void load8(const uint8_t* q, uint32_t s, int left, bool row, float (&v)[32]) {
-      const float x = scale_value(s);
+    template <int ACT>
+    __device__ __forceinline__ void gradients(const float (&a)[32], const float (&b)[32],
+                                              const float (&d)[32], uint32_t (&wa)[16],
+                                              uint32_t (&wb)[16], uint32_t (&wh)[16]) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        uint2 u = make_uint2(0, 0);
-        if (row && i < left) u = __ldg(reinterpret_cast<const uint2*>(q + i));
-        const uint32_t w[2] = {u.x, u.y};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = e4m3x2_values((uint16_t)(w[k / 2] >> (16 * (k % 2))));
-          v[i + 2 * k] = f.x * x;
-          v[i + 2 * k + 1] = f.y * x;
-        }
+      for (int i = 0; i < 16; ++i) {
+        float f0, f1, g0, g1;
+        act_both_fast(ACT, a[2 * i], f0, g0);
+        act_both_fast(ACT, a[2 * i + 1], f1, g1);
+        const float d0 = d[2 * i], d1 = d[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+        wa[i] = pack2(d0 * b0 * g0, d1 * b1 * g1);
+        wb[i] = pack2(d0 * f0, d1 * f1);
+        wh[i] = pack2(f0 * b0, f1 * b1);
       }
+    }
+    // one of the four 16-byte units of this lane's 64-byte row
+    __device__ __forceinline__ uint4* unit(uint32_t set, int buf, int u) {
+      return reinterpret_cast<uint4*>(stg + set * 6144 + buf * 2048 + lane * 64 +
+                                      ((u ^ ((lane >> 1) & 3)) << 4));
     }
     template <int BN>
     __device__ __forceinline__ void tile(const Params& e, const Problem& p, int mw, int n0, int half,
                                          int, uint32_t trow) {
-      const int m = mw + lane;
-      const bool row = m < p.M;
 #pragma unroll 1
-      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 64) {
+      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
         const int n = n0 + c;
         if (n >= p.N) break;
-        uint32_t wa[32], wb[32], wh[32];
+        const bool more = c + 32 < (half + 1) * (BN / 2) && n + 32 < p.N;
+        const uint32_t set = count & 1u;
+        float a[32], b[32], d[32];
+        if constexpr (EIGHT) {
+          const float xa = scale_value(sa), xb = scale_value(sb);
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int nn = n + 32 * hh, left = p.N - nn;
-          float a[32], b[32], d[32];
-          if (EIGHT) {
-            const uint8_t* q = e.codes + (int64_t)m * e.ldq + nn;
-            uint32_t sa = 127, sb = 127;
-            if (row && left > 0) {
-              const uint8_t* s = e.scales + ((int64_t)(m / 128) * e.kgroups + nn / 128) * 512 +
-                                 (m % 32) * 16 + ((m % 128) / 32) * 4 + (nn / 32) % 4;
-              sa = __ldg(s);
-              sb = __ldg(s + e.scale_stride);
-            }
-            load8(q, sa, left, row, a);
-            load8(q + e.code_stride, sb, left, row, b);
-          } else {
-            const __nv_bfloat16* q = e.pre + (int64_t)m * 2 * p.N + nn;
-            load_pre(q, left, row, a);
-            load_pre(q + p.N, left, row, b);
+          for (int i = 0; i < 2; ++i) {
+            codes_to(ca[i], xa, a + 16 * i);
+            codes_to(cb[i], xb, b + 16 * i);
           }
-          ptx::tmem_ld32(trow + c + 32 * hh, d);
+          if (more) request(e, p, mw, n + 32, count + 1);
+          wait_free_but_one();
+        } else {
+          if (more) request(e, p, mw, n + 32, count + 1);
+          if (!__all_sync(0xffffffffu, ptx::mbar_wait(bars + 8 * set, (count >> 1) & 1u))) {
+            if (lane == 0) atomicExch(&core::g_core_error, 4);
+          }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float f0, f1, g0, g1;
-            act_both_fast(e.act, a[2 * i], f0, g0);
-            act_both_fast(e.act, a[2 * i + 1], f1, g1);
-            const float d0 = d[2 * i], d1 = d[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-            wa[16 * hh + i] = pack2(d0 * b0 * g0, d1 * b1 * g1);
-            wb[16 * hh + i] = pack2(d0 * f0, d1 * f1);
-            wh[16 * hh + i] = pack2(f0 * b0, f1 * b1);
+          for (int u = 0; u < 4; ++u) {
+            unpack8(*unit(set, 0, u), a + 8 * u);
+            unpack8(*unit(set, 1, u), b + 8 * u);
           }
         }
-        wait_free();
-        stage_row(wa);
-        store_box(&e.da, n, mw);
-        wait_free();
-        stage_row(wb);
-        store_box(&e.db, n, mw);
-        wait_free();
-        stage_row(wh);
-        store_box(&e.h, n, mw);
+        ptx::tmem_ld32(trow + c, d);
+        uint32_t wa[16], wb[16], wh[16];
+        if (e.act == OASES_ACT_SILU)
+          gradients<OASES_ACT_SILU>(a, b, d, wa, wb, wh);
+        else
+          gradients<OASES_ACT_GELU>(a, b, d, wa, wb, wh);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          *unit(set, 0, u) = make_uint4(wa[4 * u], wa[4 * u + 1], wa[4 * u + 2], wa[4 * u + 3]);
+          *unit(set, 1, u) = make_uint4(wb[4 * u], wb[4 * u + 1], wb[4 * u + 2], wb[4 * u + 3]);
+          *unit(set, 2, u) = make_uint4(wh[4 * u], wh[4 * u + 1], wh[4 * u + 2], wh[4 * u + 3]);
+        }
+        ptx::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_2d(&e.da, stg_s + set * 6144, n, mw);
+          ptx::tma_store_2d(&e.db, stg_s + set * 6144 + 2048, n, mw);
+          ptx::tma_store_2d(&e.h, stg_s + set * 6144 + 4096, n, mw);
+          ptx::bulk_commit();
+        }
+        ++count;
+      }
+    }
+    // EIGHT: at most the last step's stores still read shared memory
+    __device__ __forceinline__ void wait_free_but_one() {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+    }
+    __device__ __forceinline__ void unpack8(uint4 q, float* v) {
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2(w[k]);
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
       }
     }
   };
 };
 
-// Maps of the 32 x 64 boxes of pre's (or dpre's) two halves and of h.
-bool halves(CUtensorMap* a, CUtensorMap* b, void* pre, const GluShape& s) {
-  __nv_bfloat16* q = static_cast<__nv_bfloat16*>(pre);
-  return core::tensor_map(a, q, false, s.F, s.M, 2 * (int64_t)s.F, 64, 32) &&
-         core::tensor_map(b, q + s.F, false, s.F, s.M, 2 * (int64_t)s.F, 64, 32);
+// Maps of pre's (or dpre's) two halves, boxes of 32 rows x `box` columns.
+bool halves(CUtensorMap* a, CUtensorMap* b, const void* pre, const GluShape& s, int box) {
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(pre);
+  return core::tensor_map(a, q, false, s.F, s.M, 2 * (int64_t)s.F, box, 32) &&
+         core::tensor_map(b, q + s.F, false, s.F, s.M, 2 * (int64_t)s.F, box, 32);
 }
 
 template <int KEEP>
@@ -261,7 +320,7 @@ cudaError_t project(const GluShape& s, const void* x, const void* w1, const void
   e.act = s.act;
   e.want_h = h != nullptr;
   if (h && !core::tensor_map(&e.h, h, false, s.F, s.M, s.F, 64, 32)) return cudaErrorInvalidValue;
-  if (pre && !halves(&e.a, &e.b, pre, s)) return cudaErrorInvalidValue;
+  if (pre && !halves(&e.a, &e.b, pre, s, 64)) return cudaErrorInvalidValue;
   if (kept8) {
     e.codes = static_cast<uint8_t*>(kept8);
     e.scales = e.codes + saved_scale_offset(s);
@@ -281,10 +340,11 @@ cudaError_t grad(const GluShape& s, const void* dy, const void* w2, const void* 
   using E = EpiGrad<EIGHT>;
   typename E::Params e = {};
   e.act = s.act;
-  if (!halves(&e.da, &e.db, dpre, s) || !core::tensor_map(&e.h, h, false, s.F, s.M, s.F, 64, 32))
+  if (!halves(&e.da, &e.db, dpre, s, 32) || !core::tensor_map(&e.h, h, false, s.F, s.M, s.F, 32, 32))
     return cudaErrorInvalidValue;
-  e.pre = static_cast<const __nv_bfloat16*>(pre);
-  if (EIGHT) {
+  if (!EIGHT) {
+    if (!halves(&e.a, &e.b, pre, s, 32)) return cudaErrorInvalidValue;
+  } else {
     e.codes = static_cast<const uint8_t*>(kept8);
     e.scales = e.codes + saved_scale_offset(s);
     e.ldq = s.ldq;
