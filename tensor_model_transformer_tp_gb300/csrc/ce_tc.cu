@@ -320,41 +320,49 @@ cudaError_t ce_tc_bwd(const CeShape& s, const void* x, const void* w, const CeRo
       OASES_TRY(few ? (core::launch<EpiG, 128, true, true, 1>(o, e, st))
                     : (core::launch<EpiG, 256, true, true, 2>(o, e, st)));
     }
+    EpiOut::Params e_dx = {}, e_dw = {};
+    bool ok = true;
     if (dx) {
-      EpiOut::Params e = {};
-      bool ok = true;
       if (b.splits > 1) {
-        e.slab_rows = (int)(b.slab / s.H);
-        ok = core::out_map(&e, dx32, DType::F32, e.slab_rows * b.splits, s.H, s.H);
+        e_dx.slab_rows = (int)(b.slab / s.H);
+        ok = core::out_map(&e_dx, dx32, DType::F32, e_dx.slab_rows * b.splits, s.H, s.H);
       } else if (last) {
-        ok = core::out_map(&e, dx, DType::BF16, s.M, s.H, s.H);
-        e.scale = rows.scale;
-        e.prior = first ? nullptr : dx32;
+        ok = core::out_map(&e_dx, dx, DType::BF16, s.M, s.H, s.H);
+        e_dx.scale = rows.scale;
+        e_dx.prior = first ? nullptr : dx32;
       } else {
-        ok = core::out_map(&e, dx32, DType::F32, s.M, s.H, s.H);
-        e.accumulate = !first;
-      }
-      if (!ok) return cudaErrorInvalidValue;
-      core::Operands o{s.M, s.H, n, g, b.ld, wp, s.H};
-      o.splits = b.splits;
-      OASES_TRY(few ? (core::launch<EpiOut, 128, true, false, 1>(o, e, st))
-                    : (core::launch<EpiOut, 256, true, false, 2>(o, e, st)));
-      if (b.splits > 1) {
-        const int64_t count = (int64_t)s.M * s.H;
-        OASES_TRY(launch_pdl(ce_slabs_kernel,
-                             dim3((unsigned)std::min<int64_t>((count / 4 + 255) / 256, 152 * 8)),
-                             dim3(256), 0, st, (const float*)dx32, b.splits, b.slab, rows.scale,
-                             static_cast<__nv_bfloat16*>(dx), count));
+        ok = core::out_map(&e_dx, dx32, DType::F32, s.M, s.H, s.H);
+        e_dx.accumulate = !first;
       }
     }
     if (dw) {
-      EpiOut::Params e = {};
       char* out = static_cast<char*>(dw) + (size_t)v0 * s.H * dtype_size(s.grad_t);
-      if (!core::out_map(&e, out, s.grad_t, n, s.H, s.H)) return cudaErrorInvalidValue;
-      e.scale = rows.scale;
-      e.accumulate = s.accumulate;
-      core::Operands o{n, s.H, s.M, g, b.ld, x, s.H};
-      OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o, e, st)));
+      ok = ok && core::out_map(&e_dw, out, s.grad_t, n, s.H, s.H);
+      e_dw.scale = rows.scale;
+      e_dw.accumulate = s.accumulate;
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    core::Operands o_dx{s.M, s.H, n, g, b.ld, wp, s.H};
+    o_dx.splits = b.splits;
+    const core::Operands o_dw{n, s.H, s.M, g, b.ld, x, s.H};
+    bool taken = false;
+    if (dx && dw && !few) {
+      const core::Product prod[2] = {{o_dx, true}, {o_dw, false}};
+      const EpiOut::Params ep[2] = {e_dx, e_dw};
+      OASES_TRY((core::launch_group<EpiOut, 2>(prod, ep, &taken, st)));
+    }
+    if (!taken) {
+      if (dx)
+        OASES_TRY(few ? (core::launch<EpiOut, 128, true, false, 1>(o_dx, e_dx, st))
+                      : (core::launch<EpiOut, 256, true, false, 2>(o_dx, e_dx, st)));
+      if (dw) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_dw, e_dw, st)));
+    }
+    if (dx && b.splits > 1) {
+      const int64_t count = (int64_t)s.M * s.H;
+      OASES_TRY(launch_pdl(ce_slabs_kernel,
+                           dim3((unsigned)std::min<int64_t>((count / 4 + 255) / 256, 152 * 8)),
+                           dim3(256), 0, st, (const float*)dx32, b.splits, b.slab, rows.scale,
+                           static_cast<__nv_bfloat16*>(dx), count));
     }
   }
   return cudaSuccess;

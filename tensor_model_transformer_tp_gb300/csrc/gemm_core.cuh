@@ -15,6 +15,11 @@
 // A contraction that leaves SMs idle is split: split z of `splits` takes
 // K-slices [z kbs, (z + 1) kbs) and its epilogue sees z.
 //
+// Several products can share a launch (a backward's dx and weight gradients):
+// their tiles, of different lengths, are dealt to the CTAs longest first so that
+// the CTAs finish together, instead of every product leaving its last round of
+// tiles partly idle.
+//
 // Every mbarrier wait is bounded (2 s); on expiry the thread records an error,
 // drains what it has in flight and leaves, so the kernel always terminates.
 #pragma once
@@ -62,14 +67,70 @@ struct Problem {
   int splits, kbs;     // splits of the contraction, K-slices per split
 };
 
-template <class Epi, int BN, bool A_K, bool B_K, int CL>
+constexpr int MAX_SLOTS = 160;  // CTAs or CTA pairs of a launch of several products
+
+template <class Epi>
+struct Item {
+  CUtensorMap a, b;
+  typename Epi::Params ep;
+  Problem p;
+  int a_k;  // A is K-major
+};
+// The products of a launch.  One: its tiles go round the CTAs.  Several: slot s
+// (CTA or pair) takes tiles [first[i][s], first[i][s + 1]) of product i, in turn.
+template <class Epi, int ITEMS>
+struct Work {
+  Item<Epi> item[ITEMS];
+  uint16_t first[ITEMS][MAX_SLOTS + 1];
+};
+template <class Epi>
+struct Work<Epi, 1> {
+  Item<Epi> item[1];
+};
+
+// Walks the tiles of a slot.
+template <class Epi, int ITEMS>
+struct Walk {
+  const Work<Epi, ITEMS>& w;
+  const int slot, slots;
+  int i, t, end;
+  __device__ __forceinline__ Walk(const Work<Epi, ITEMS>& w_, int slot_, int slots_)
+      : w(w_), slot(slot_), slots(slots_), i(0) {
+    if constexpr (ITEMS == 1) {
+      t = slot;
+      end = w.item[0].p.num_mp * w.item[0].p.num_n * w.item[0].p.splits;
+    } else {
+      t = w.first[0][slot];
+      end = w.first[0][slot + 1];
+      skip();
+    }
+  }
+  __device__ __forceinline__ void skip() {
+    if constexpr (ITEMS > 1)
+      while (t >= end && ++i < ITEMS) {
+        t = w.first[i][slot];
+        end = w.first[i][slot + 1];
+      }
+  }
+  __device__ __forceinline__ bool more() const { return ITEMS == 1 ? t < end : i < ITEMS; }
+  __device__ __forceinline__ void next() {
+    if constexpr (ITEMS == 1) {
+      t += slots;
+    } else {
+      ++t;
+      skip();
+    }
+  }
+  __device__ __forceinline__ const Item<Epi>& item() const { return w.item[ITEMS == 1 ? 0 : i]; }
+};
+
+// A_MODE: 1 A is K-major, 0 it is not, 2 as each item says.
+template <class Epi, int BN, int A_MODE, bool B_K, int CL, int ITEMS>
 __global__ void __launch_bounds__(NTHREADS, 1)
-gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ typename Epi::Params ep, const Problem p) {
+gemm_core_kernel(const __grid_constant__ Work<Epi, ITEMS> work) {
   using C = Cfg<BN, CL, Epi::STG, Epi::WBARS>;
   constexpr int BNH = BN / CL;                    // B rows held by this CTA
   constexpr int TN = Epi::DUAL ? BN / 2 : BN;     // output columns per tile
-  constexpr uint32_t IDESC = ptx::idesc_bf16_f32(BM * CL, BN, !A_K, !B_K);
   static_assert(!Epi::DUAL || (CL == 2 && B_K), "DUAL tiles are CTA pairs over K-major weights");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -85,16 +146,15 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = CL > 1 ? (int)ptx::cluster_rank() : 0;
-  const int tiles1 = p.num_mp * p.num_n, tiles = tiles1 * p.splits;
-  const int nkb = (p.K + BKE - 1) / BKE;
-  const int first = blockIdx.x / CL, stride = gridDim.x / CL;
+  const int slot = blockIdx.x / CL, slots = gridDim.x / CL;
   // Tile order within a split: groups of `group` row blocks, the row block
   // fastest inside a group (the operands of the tiles in flight stay in L2).
   struct Tile {
     int m0, n0, z, kb0, kb1;
   };
-  auto tile_of = [&](int t) {
+  auto tile_of = [&](const Problem& p, int t) {
     Tile q;
+    const int tiles1 = p.num_mp * p.num_n, nkb = (p.K + BKE - 1) / BKE;
     q.z = t / tiles1;
     const int r = t - q.z * tiles1, g = r / (p.group * p.num_n);
     const int gm = min(p.group, p.num_mp - g * p.group), i = r - g * p.group * p.num_n;
@@ -104,6 +164,7 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     q.kb1 = min(nkb, q.kb0 + p.kbs);
     return q;
   };
+  auto a_kmajor = [&](const Item<Epi>& it) { return A_MODE == 2 ? it.a_k != 0 : A_MODE == 1; };
   constexpr uint16_t MASK = (1u << CL) - 1u;
 
   if (threadIdx.x == 0) {
@@ -128,9 +189,9 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       ptx::tmem_relinquish();
     }
   }
-  if (warp == 0 && lane == 0) {
-    ptx::prefetch_tmap(&tmA);
-    ptx::prefetch_tmap(&tmB);
+  if (warp == 0 && lane < ITEMS) {
+    ptx::prefetch_tmap(&work.item[lane].a);
+    ptx::prefetch_tmap(&work.item[lane].b);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -146,9 +207,12 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       int stage = 0;
       uint32_t phase = 0, issued = 0, iphase = 0;  // bit s: stage s loaded, parity of its last load
       bool ok = true;
-      const uint32_t bytes = (uint32_t)(CL * (p.a_rows * 128 + C::B_BYTES));
-      for (int t = first; t < tiles && ok; t += stride) {
-        const Tile q = tile_of(t);
+      for (Walk<Epi, ITEMS> k(work, slot, slots); k.more() && ok; k.next()) {
+        const Item<Epi>& it = k.item();
+        const Problem& p = it.p;
+        const bool ak = a_kmajor(it);
+        const uint32_t bytes = (uint32_t)(CL * (p.a_rows * 128 + C::B_BYTES));
+        const Tile q = tile_of(p, k.t);
         for (int kb = q.kb0; kb < q.kb1; ++kb) {
           if (!ptx::mbar_wait(empty(stage), phase ^ 1u)) { ok = false; break; }
           // a pair's loads complete on the even CTA's barrier, which expects both
@@ -162,18 +226,18 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           };
           const uint32_t sa = base + stage * C::STAGE, sb = sa + C::A_BYTES;
           const int k0 = kb * BKE;
-          if (A_K) {
-            load(sa, &tmA, k0, q.m0);
+          if (ak) {
+            load(sa, &it.a, k0, q.m0);
           } else {
-            load(sa, &tmA, q.m0, k0);
-            load(sa + 8192, &tmA, q.m0 + 64, k0);
+            load(sa, &it.a, q.m0, k0);
+            load(sa + 8192, &it.a, q.m0 + 64, k0);
           }
           const int nb = Epi::DUAL ? q.n0 + rank * p.b_off : q.n0 + rank * BNH;
           if (B_K) {
-            load(sb, &tmB, k0, nb);
+            load(sb, &it.b, k0, nb);
           } else {
 #pragma unroll
-            for (int c = 0; c < BNH / 64; ++c) load(sb + c * 8192, &tmB, nb + 64 * c, k0);
+            for (int c = 0; c < BNH / 64; ++c) load(sb + c * 8192, &it.b, nb + 64 * c, k0);
           }
           issued |= 1u << stage;
           iphase = (iphase & ~(1u << stage)) | (phase << stage);
@@ -192,27 +256,30 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       int stage = 0, n = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += stride, ++n) {
-        const int buf = n & 1, z = t / tiles1;
-        const int kb0 = z * p.kbs, kb1 = min(nkb, kb0 + p.kbs);
+      for (Walk<Epi, ITEMS> k(work, slot, slots); k.more() && ok; k.next(), ++n) {
+        const int buf = n & 1;
+        const bool ak = a_kmajor(k.item());
+        const uint32_t idesc = ak ? ptx::idesc_bf16_f32(BM * CL, BN, false, !B_K)
+                                  : ptx::idesc_bf16_f32(BM * CL, BN, true, !B_K);
+        const Tile q = tile_of(k.item().p, k.t);
         if (!ptx::mbar_wait(tempty(buf), (((uint32_t)n >> 1) & 1u) ^ 1u)) { ok = false; break; }
         ptx::tc_fence_after();
         const uint32_t dt = tmem + (uint32_t)(buf * BN);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = q.kb0; kb < q.kb1; ++kb) {
           if (!ptx::mbar_wait(full(stage), phase)) { ok = false; break; }
           ptx::tc_fence_after();
           const uint32_t sa = base + stage * C::STAGE, sb = sa + C::A_BYTES;
-          const uint64_t ad0 = A_K ? ptx::smem_desc_sw128(sa, 16, 1024) : ptx::smem_desc_sw128(sa, 8192, 1024);
+          const uint64_t ad0 = ak ? ptx::smem_desc_sw128(sa, 16, 1024) : ptx::smem_desc_sw128(sa, 8192, 1024);
           const uint64_t bd0 = B_K ? ptx::smem_desc_sw128(sb, 16, 1024) : ptx::smem_desc_sw128(sb, 8192, 1024);
 #pragma unroll
           for (int kk = 0; kk < BKE / 16; ++kk) {
-            const uint64_t ad = ad0 + (uint64_t)(A_K ? 2 * kk : 128 * kk);
+            const uint64_t ad = ad0 + (uint64_t)(ak ? 2 * kk : 128 * kk);
             const uint64_t bd = bd0 + (uint64_t)(B_K ? 2 * kk : 128 * kk);
-            const uint32_t acc = (kb > kb0 || kk != 0) ? 1u : 0u;
+            const uint32_t acc = (kb > q.kb0 || kk != 0) ? 1u : 0u;
             if (CL > 1)
-              ptx::mma_bf16_pair(dt, ad, bd, IDESC, acc);
+              ptx::mma_bf16_pair(dt, ad, bd, idesc, acc);
             else
-              ptx::mma_bf16(dt, ad, bd, IDESC, acc);
+              ptx::mma_bf16(dt, ad, bd, idesc, acc);
           }
           if (CL > 1)
             ptx::mma_commit_pair_mc(empty(stage), MASK);
@@ -235,7 +302,7 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       if (!ok) atomicExch(&g_core_error, 2);
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;  // lane quarter, half of the columns
+    const int quarter = warp & 3, half = (warp - 2) >> 2;  // of the lanes, of the columns
     typename Epi::Warp w;
     w.stg = gbase + C::EPI_OFF + (warp - 2) * Epi::STG;
     w.stg_s = base + C::EPI_OFF + (warp - 2) * Epi::STG;
@@ -243,10 +310,12 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     w.bars = wbars + 8u * (warp - 2) * Epi::WBARS;
     w.init();
     int n = 0;
-    for (int t = first; t < tiles; t += stride, ++n) {
+    for (Walk<Epi, ITEMS> k(work, slot, slots); k.more(); k.next(), ++n) {
       const int buf = n & 1;
-      const Tile tl = tile_of(t);
-      const int mw = tl.m0 + q * 32;
+      const Problem& p = k.item().p;
+      const typename Epi::Params& ep = k.item().ep;
+      const Tile tl = tile_of(p, k.t);
+      const int mw = tl.m0 + quarter * 32;
       w.template before<BN>(ep, p, mw, tl.n0, half);  // loads that do not wait for the accumulator
       // the decision is warp-uniform: tcgen05.ld is warp-collective
       if (!__all_sync(0xffffffffu, ptx::mbar_wait(tfull(buf), ((uint32_t)n >> 1) & 1u))) {
@@ -254,7 +323,7 @@ gemm_core_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         break;
       }
       ptx::tc_fence_after();
-      const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
+      const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN);
       if (mw < (Epi::PAD_ROWS ? (p.M + BM - 1) / BM * BM : p.M))
         w.template tile<BN>(ep, p, mw, tl.n0, half, tl.z, trow);
       ptx::tc_fence_before();
@@ -395,72 +464,189 @@ inline int slices_per_split(int K, int* splits) {
   return kbs;
 }
 
-template <class Epi, int BN, bool A_K, bool B_K, int CL>
-cudaError_t launch(const Operands& o, const typename Epi::Params& ep, cudaStream_t st) {
-  using C = Cfg<BN, CL, Epi::STG, Epi::WBARS>;
+// One product of a launch with BN-column tiles of CL CTAs.
+template <class Epi, int BN, bool B_K, int CL>
+bool make_item(Item<Epi>* it, const Operands& o, bool a_k, const typename Epi::Params& ep) {
   constexpr int TN = Epi::DUAL ? BN / 2 : BN;
-  Problem p;
+  Problem& p = it->p;
   p.M = o.M;
   p.N = o.N;
   p.K = o.K;
   p.b_off = o.b_off;
-  p.a_rows = A_K ? std::min(BM, (o.M + 7) / 8 * 8) : BM;
-  if (CL > 1) p.a_rows = BM;
+  p.a_rows = a_k && CL == 1 ? std::min(BM, (o.M + 7) / 8 * 8) : BM;
   p.num_mp = ((o.M + BM - 1) / BM + CL - 1) / CL;
   p.num_n = (o.N + TN - 1) / TN;
   p.group = (int64_t)o.M * o.K * 2 > A_L2_BYTES ? std::min(GROUP_M, p.num_mp) : p.num_mp;
   p.splits = o.splits;
   p.kbs = slices_per_split(o.K, &p.splits);
-  CUtensorMap ma, mb;
+  it->ep = ep;
+  it->a_k = a_k;
   const uint64_t rows_b = (uint64_t)o.N + o.b_off;
-  const bool ok = (A_K ? tensor_map(&ma, o.a, false, o.K, o.M, o.lda, BKE, p.a_rows)
-                       : tensor_map(&ma, o.a, false, o.M, o.K, o.lda, 64, BKE)) &&
-                  (B_K ? tensor_map(&mb, o.b, false, o.K, rows_b, o.ldb, BKE, BN / CL)
-                       : tensor_map(&mb, o.b, false, rows_b, o.K, o.ldb, 64, BKE));
-  if (!ok) return cudaErrorInvalidValue;
-  auto kern = gemm_core_kernel<Epi, BN, A_K, B_K, CL>;
+  return (a_k ? tensor_map(&it->a, o.a, false, o.K, o.M, o.lda, BKE, p.a_rows)
+              : tensor_map(&it->a, o.a, false, o.M, o.K, o.lda, 64, BKE)) &&
+         (B_K ? tensor_map(&it->b, o.b, false, o.K, rows_b, o.ldb, BKE, BN / CL)
+              : tensor_map(&it->b, o.b, false, rows_b, o.K, o.ldb, 64, BKE));
+}
+
+// A kernel's launch configuration and the CTAs (CL = 1) or CTA pairs of it that
+// can be resident at once on the current device (per kernel: the statics belong to this one).
+template <int BN, int CL, class Epi, auto kern>
+cudaError_t prepare(cudaStream_t st, cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attrs,
+                    int* slots) {
+  using C = Cfg<BN, CL, Epi::STG, Epi::WBARS>;
   static DeviceOnce attr;
   const cudaError_t ea = attr.run([&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (ea != cudaSuccess) return ea;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(NTHREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attrs[2];
+  *cfg = {};
+  cfg->blockDim = dim3(NTHREADS);
+  cfg->dynamicSmemBytes = C::SMEM;
+  cfg->stream = st;
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
   attrs[1].id = cudaLaunchAttributeClusterDimension;
   attrs[1].val.clusterDim.x = CL;
   attrs[1].val.clusterDim.y = 1;
   attrs[1].val.clusterDim.z = 1;
-  // persistent grid: as many clusters as can be resident at once (per device),
-  // and no more than finish in the same number of tile rounds
-  static std::atomic<int> slots_by_dev[64];
+  cfg->attrs = attrs;
+  cfg->numAttrs = CL > 1 ? 2 : 1;
+  static std::atomic<int> by_dev[64];
   const int dev = current_device();
-  int slots = dev < 64 ? slots_by_dev[dev].load(std::memory_order_relaxed) : 0;
-  if (slots == 0) {
-    slots = std::max(1, sm_count() / CL);
+  int n = dev < 64 ? by_dev[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    n = std::max(1, sm_count() / CL);
     if (CL > 1) {
-      cudaLaunchConfig_t q = cfg;
-      q.gridDim = dim3(slots * CL);
+      cudaLaunchConfig_t q = *cfg;
+      q.gridDim = dim3(n * CL);
       q.attrs = attrs + 1;
       q.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &q) == cudaSuccess && n > 0 && n < slots) slots = n;
+      int c = 0;
+      if (cudaOccupancyMaxActiveClusters(&c, kern, &q) == cudaSuccess && c > 0 && c < n) n = c;
       cudaGetLastError();
     }
-    if (dev < 64) slots_by_dev[dev].store(slots, std::memory_order_relaxed);
+    if (dev < 64) by_dev[dev].store(n, std::memory_order_relaxed);
   }
+  *slots = n;
+  return cudaSuccess;
+}
+
+template <class Epi, int BN, bool A_K, bool B_K, int CL>
+cudaError_t launch(const Operands& o, const typename Epi::Params& ep, cudaStream_t st) {
+  Work<Epi, 1> w;
+  if (!make_item<Epi, BN, B_K, CL>(&w.item[0], o, A_K, ep)) return cudaErrorInvalidValue;
+  constexpr auto kern = gemm_core_kernel<Epi, BN, A_K ? 1 : 0, B_K, CL, 1>;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attrs[2];
+  int slots;
+  const cudaError_t e = prepare<BN, CL, Epi, kern>(st, &cfg, attrs, &slots);
+  if (e != cudaSuccess) return e;
+  const Problem& p = w.item[0].p;
   const int64_t tiles = (int64_t)p.num_mp * p.num_n * p.splits;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  // no more CTAs than finish in the same number of tile rounds
   const int rounds = (int)((tiles + slots - 1) / slots);
   cfg.gridDim = dim3((unsigned)((tiles + rounds - 1) / rounds) * CL);
-  cfg.attrs = attrs;
-  cfg.numAttrs = CL > 1 ? 2 : 1;
   ++g_launch_count;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, ep, p);
+  return cudaLaunchKernelEx(&cfg, kern, w);
+}
+
+// Several products with N-major B (BN = 256 CTA-pair tiles) in one launch.
+struct Product {
+  Operands o;
+  bool a_k;
+};
+constexpr int64_t GROUP_BYTES = 256ll << 20;  // operands of the products, counted for each
+constexpr int TILE_COST = 4;  // a tile's fixed cost in K-slices (fill, hand-over)
+
+// Deals `tiles` tiles of length `len` to the slots, least loaded first, and adds
+// them to `load`; first[s] .. first[s + 1] are slot s's tiles.
+inline void deal(int tiles, int len, int slots, int* load, uint16_t* first) {
+  // the highest level (in K-slices) to which the slots can be filled
+  int lo = *std::min_element(load, load + slots);
+  int hi = *std::max_element(load, load + slots) + (tiles / slots + 1) * len;
+  auto fits = [&](int level) {
+    int n = 0;
+    for (int s = 0; s < slots; ++s) n += std::max(0, level - load[s]) / len;
+    return n;
+  };
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (fits(mid) <= tiles)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  int count[MAX_SLOTS], left = tiles - fits(lo);
+  for (int s = 0; s < slots; ++s) {
+    count[s] = std::max(0, lo - load[s]) / len;
+    load[s] += count[s] * len;
+  }
+  while (left-- > 0) {
+    int best = 0;
+    for (int s = 1; s < slots; ++s)
+      if (load[s] < load[best]) best = s;
+    ++count[best];
+    load[best] += len;
+  }
+  int at = 0;
+  for (int s = 0; s < slots; ++s) {
+    first[s] = (uint16_t)at;
+    at += count[s];
+  }
+  first[slots] = (uint16_t)at;
+}
+
+// Whether `n` products are better dealt out in one launch than launched one
+// after the other, by the K-slices on the longest path.
+inline int64_t rounds_cost(int64_t tiles, int len, int slots) {
+  return (tiles + slots - 1) / slots * len;
+}
+
+template <class Epi, int N>
+cudaError_t launch_group(const Product* prod, const typename Epi::Params* ep, bool* taken,
+                         cudaStream_t st) {
+  constexpr auto kern = gemm_core_kernel<Epi, 256, 2, false, 2, N>;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attrs[2];
+  int slots;
+  *taken = false;
+  const cudaError_t e = prepare<256, 2, Epi, kern>(st, &cfg, attrs, &slots);
+  if (e != cudaSuccess) return e;
+  if (slots > MAX_SLOTS) return cudaSuccess;
+  // A slot's tiles of a product are neighbours, so the tiles in flight are spread
+  // over the whole product: right while the operands stay in L2, else each is
+  // streamed more than once (operands of 132 MB: 126 to 100 us together; of 290
+  // MB: 245 us apart, 249 together; of 1 GB: 4% slower together).
+  int64_t bytes = 0;
+  for (int i = 0; i < N; ++i)
+    bytes += 2ll * prod[i].o.K * ((int64_t)prod[i].o.M + prod[i].o.N);
+  if (bytes > GROUP_BYTES) return cudaSuccess;
+  // longest tiles first
+  int order[N], len[N];
+  int64_t tiles[N], apart = 0;
+  for (int i = 0; i < N; ++i) {
+    const Operands& o = prod[i].o;
+    int splits = o.splits;
+    len[i] = slices_per_split(o.K, &splits) + TILE_COST;
+    tiles[i] = (int64_t)((o.M + 2 * BM - 1) / (2 * BM)) * ((o.N + 255) / 256) * splits;
+    if (tiles[i] > UINT16_MAX || tiles[i] * len[i] > INT32_MAX / 8) return cudaSuccess;
+    apart += rounds_cost(tiles[i], len[i], slots) + 2 * TILE_COST;  // a launch more
+    order[i] = i;
+  }
+  std::sort(order, order + N, [&](int a, int b) { return len[a] > len[b]; });
+  Work<Epi, N> w;
+  int load[MAX_SLOTS] = {};
+  for (int k = 0; k < N; ++k) deal((int)tiles[order[k]], len[order[k]], slots, load, w.first[k]);
+  const int together = *std::max_element(load, load + slots);
+  if (together * 100ll > apart * 97ll) return cudaSuccess;
+  for (int k = 0; k < N; ++k)
+    if (!make_item<Epi, 256, false, 2>(&w.item[k], prod[order[k]].o, prod[order[k]].a_k, ep[order[k]]))
+      return cudaErrorInvalidValue;
+  cfg.gridDim = dim3((unsigned)slots * 2);
+  ++g_launch_count;
+  *taken = true;
+  return cudaLaunchKernelEx(&cfg, kern, w);
 }
 
 // Reads and clears this translation unit's error word (-1: unreadable).

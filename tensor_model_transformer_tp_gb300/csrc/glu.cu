@@ -56,7 +56,7 @@ size_t saved_bytes(const GluShape& s) {
 
 // Workspace regions, each a multiple of 256 bytes.
 struct Layout {
-  size_t pre = 0, h = 0, dpre = 0, bias = 0, part = 0, total = 0;
+  size_t pre = 0, h = 0, dpre = 0, dx = 0, bias = 0, part = 0, total = 0;
 };
 Layout layout(const GluShape& s, bool backward) {
   Layout l;
@@ -71,6 +71,7 @@ Layout layout(const GluShape& s, bool backward) {
   if (backward) {
     if (s.keep == OASES_GLU_KEEP_NONE) take(&l.pre, 2 * MF * e);
     take(&l.dpre, 2 * MF * e);
+    if (s.t == DType::BF16) take(&l.dx, glu_grads_tc_bytes(s));
     if (s.M > DIRECT_SUM_ROWS) {
       take(&l.part, (size_t)colsum_blocks(s.M) * wide * 4);
       take(&l.bias, (size_t)wide * 4);
@@ -154,17 +155,10 @@ struct Sums {
   void* out[2];
   int N[2];
 };
-// Two neighbouring columns per thread (one 4- or 8-byte load per row; an odd N
-// goes a column at a time), 16 warps over the rows.
-template <typename T>
-__device__ __forceinline__ float2 ld_pair(const T* p, bool pair, bool second) {
-  if (pair) {
-    if constexpr (sizeof(T) == 4)
-      return *reinterpret_cast<const float2*>(p);
-    else
-      return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
-  }
-  return make_float2(ld_elem(p, 0), second ? ld_elem(p, 1) : 0.f);
+// Two neighbouring columns per thread, 16 warps over the rows.
+__device__ __forceinline__ float2 ld_pair(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 ld_pair(const __nv_bfloat16* p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
 }
 template <typename T, typename O>
 __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, int accumulate) {
@@ -175,14 +169,19 @@ __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, i
   const int which = (int)blockIdx.x < first ? 0 : 1;
   const int n = ((int)blockIdx.x - (which ? first : 0)) * 64 + 2 * x, N = s.N[which];
   const T* in = static_cast<const T*>(s.in[which]) + n;
-  const bool pair = N % 2 == 0, second = n + 1 < N;
+  const bool second = n + 1 < N;
   float2 v = make_float2(0.f, 0.f);
-  if (n < N) {
+  if (N % 2 == 0 && n < N) {  // one 4- or 8-byte load per row
 #pragma unroll 8
     for (int m = y; m < M; m += 16) {
-      const float2 q = ld_pair(in + (int64_t)m * N, pair, second);
+      const float2 q = ld_pair(in + (int64_t)m * N);
       v.x += q.x;
       v.y += q.y;
+    }
+  } else if (n < N) {
+    for (int m = y; m < M; m += 16) {
+      v.x += ld_elem(in, (int64_t)m * N);
+      if (second) v.y += ld_elem(in, (int64_t)m * N + 1);
     }
   }
   red[y][x] = v;
@@ -206,15 +205,6 @@ __global__ void __launch_bounds__(256) cast_kernel(const float* in, T* out, int 
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i < n) st_elem(out, i, in[i]);
 }
-
-struct Gemm : GemmArgs {
-  Gemm(int m, int n, int k, DType t) {
-    M = m;
-    N = n;
-    K = k;
-    in_t = aux_t = t;
-  }
-};
 
 #define OASES_TRY(expr)                       \
   do {                                        \
@@ -276,26 +266,12 @@ cudaError_t fwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
       g, f32::Out{(float*)y, s.H, nullptr, (const float*)w.b2, (const float*)resid, 0}, st);
 }
 
-// dW [N, K] (+)= A^T B over the rows, A [M, N], B [M, K].
+// fp32: dW [N, K] (+)= A^T B over the rows, A [M, N], B [M, K].
 cudaError_t weight_grad(const GluShape& s, const void* A, int N, const void* B, int K, void* out,
                         cudaStream_t st) {
-  if (s.t == DType::F32) {
-    const f32::Args g{N, K, s.M, (const float*)A, N, (const float*)B, K, 0, 0};
-    return f32::launch<f32::Out, false, false>(
-        g, f32::Out{(float*)out, K, nullptr, nullptr, nullptr, s.accumulate}, st);
-  }
-  Gemm g(N, K, s.M, s.t);
-  g.A = A;
-  g.lda = N;
-  g.a_kmajor = false;
-  g.B = B;
-  g.ldb = K;
-  g.b_kmajor = false;
-  g.epi = s.accumulate ? Epi::Accum : Epi::Store;
-  g.C = out;
-  g.ldc = K;
-  g.c_t = s.grad_t;
-  return gemm(g, st);
+  const f32::Args g{N, K, s.M, (const float*)A, N, (const float*)B, K, 0, 0};
+  return f32::launch<f32::Out, false, false>(
+      g, f32::Out{(float*)out, K, nullptr, nullptr, nullptr, s.accumulate}, st);
 }
 
 cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, const void* dy,
@@ -313,29 +289,17 @@ cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
   }
   if (s.t == DType::BF16) {
     OASES_TRY(glu_grad_tc(s, dy, w.w2, pre, kept8, dpre, h, st));
+    OASES_TRY(glu_grads_tc(s, x, dy, w.w1, dpre, h, dx, gr.w1, gr.w2, ws + l.dx, st));
   } else {
     const f32::Args g{s.M, s.F, s.H, (const float*)dy, s.H, (const float*)w.w2, s.F, 0, 0};
     OASES_TRY((f32::launch<GradF32, true, false>(
         g, GradF32{(const float*)pre, (float*)dpre, (float*)h, s.act}, st)));
-  }
-  if (gr.w2) OASES_TRY(weight_grad(s, dy, s.H, h, s.F, gr.w2, st));
-  if (gr.w1) OASES_TRY(weight_grad(s, dpre, 2 * s.F, x, s.H, gr.w1, st));
-  if (dx) {
-    if (s.t == DType::F32) {
-      const f32::Args g{s.M, s.H, 2 * s.F, (const float*)dpre, 2 * s.F, (const float*)w.w1, s.H, 0, 0};
+    if (gr.w2) OASES_TRY(weight_grad(s, dy, s.H, h, s.F, gr.w2, st));
+    if (gr.w1) OASES_TRY(weight_grad(s, dpre, 2 * s.F, x, s.H, gr.w1, st));
+    if (dx) {
+      const f32::Args q{s.M, s.H, 2 * s.F, (const float*)dpre, 2 * s.F, (const float*)w.w1, s.H, 0, 0};
       OASES_TRY((f32::launch<f32::Out, true, false>(
-          g, f32::Out{(float*)dx, s.H, nullptr, nullptr, nullptr, 0}, st)));
-    } else {
-      Gemm q(s.M, s.H, 2 * s.F, s.t);
-      q.A = dpre;
-      q.lda = 2 * s.F;
-      q.B = w.w1;
-      q.ldb = s.H;
-      q.b_kmajor = false;
-      q.C = dx;
-      q.ldc = s.H;
-      q.c_t = s.dx_t;
-      OASES_TRY(gemm(q, st));
+          q, f32::Out{(float*)dx, s.H, nullptr, nullptr, nullptr, 0}, st)));
     }
   }
   return bias_grads(s, dpre, dy, gr, reinterpret_cast<float*>(ws + l.part),

@@ -59,6 +59,12 @@ cudaError_t glu_project_tc(const GluShape& s, const void* x, const void* w1, con
 // pre (bf16 [M, 2F]) or kept8.
 cudaError_t glu_grad_tc(const GluShape& s, const void* dy, const void* w2, const void* pre,
                         const void* kept8, void* dpre, void* h, cudaStream_t st);
+// dw2 (+)= dy^T h, dw1 (+)= dpre^T x, dx = dpre w1, each where it is given; ws
+// as glu_grads_tc_bytes.
+size_t glu_grads_tc_bytes(const GluShape& s);
+cudaError_t glu_grads_tc(const GluShape& s, const void* x, const void* dy, const void* w1,
+                         const void* dpre, const void* h, void* dx, void* dw1, void* dw2, char* ws,
+                         cudaStream_t st);
 // y = h w2^T + b2 (+ resid)
 cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const void* b2,
                         const void* resid, void* y, cudaStream_t st);

@@ -432,6 +432,60 @@ def test_ce_minus_infinity_logits():
     assert (lse - lse0).abs().max() <= 2.0 ** -18 and (loss - loss0).abs().max() <= 2.0 ** -18
 
 
+def _rms_close(got, want, rel, what):
+    """Relative 2-norm, for sizes whose element-wise bounds would take minutes."""
+    r = float((got.double() - want).norm() / want.norm())
+    assert r <= rel, (what, r)
+
+
+@pytest.mark.parametrize("M,H,Fn,save", [(4096, 1024, 6000, "mxfp8"), (3000, 2048, 5464, "pre"),
+                                         (8200, 512, 1032, "none")])
+def test_glu_larger_sizes(M, H, Fn, save):
+    """Products that take several launches or share one, on float64 products of
+    the same roundings' size: kept and intermediate values carry up to three bf16
+    roundings of 2^-9 rms each and the output one more, 2 * 2^-9 in all."""
+    x, w, r, dy = glu_case("bf16", M, H, Fn, True, True)
+    y, saved = F.glu_fwd(x, w, resid=r, save=save)
+    dx, grads = F.glu_bwd(x, dy, w, save=save, saved=saved)
+    oz.oases_check_device(torch.cuda.current_stream())
+    W = {k: v.double() for k, v in w.items()}
+    p = x.double() @ W["w1"].t() + W["b1"]
+    a, b = p[:, :Fn], p[:, Fn:]
+    _rms_close(y, (a * torch.sigmoid(a) * b) @ W["w2"].t() + W["b2"] + r.double(), 2.0 ** -8, "y")
+    if save != "none":
+        a, b = (torch.from_numpy(v).cuda() for v in kept_values(saved, save, M, Fn))
+    s = torch.sigmoid(a)
+    dh = dy.double() @ W["w2"]
+    dp = torch.cat([dh * b * s * (1 + a * (1 - s)), dh * a * s], dim=1)
+    _rms_close(dx, dp @ W["w1"], 2.0 ** -8, "dx")
+    _rms_close(grads["w1"], dp.t() @ x.double(), 2.0 ** -8, "dw1")
+    _rms_close(grads["w2"], dy.double().t() @ (a * s * b), 2.0 ** -8, "dw2")
+    _rms_close(grads["b1"], dp.sum(0), 2.0 ** -8, "db1")
+    _rms_close(grads["b2"], dy.double().sum(0), 2.0 ** -8, "db2")
+
+
+@pytest.mark.parametrize("M,H,V", [(8000, 256, 20001), (300, 512, 60000), (4096, 1024, 33000),
+                                   (2000, 128, 100)])
+def test_ce_larger_sizes(M, H, V):
+    """Several pieces of the vocabulary (8000 x 20001 logits), split contractions
+    and products that share a launch or do not."""
+    x, w, t, d = ce_case("bf16", M, H, V, True, std=2.0)
+    loss, lse = F.ce_fwd(x, w, t)
+    dx, dw = F.ce_bwd(x, w, t, lse, d)
+    oz.oases_check_device(torch.cuda.current_stream())
+    l = x.double() @ w.double().t()
+    ref = torch.logsumexp(l, dim=1)
+    used = t != -100
+    at = torch.where(used, t, 0)[:, None]
+    want = torch.where(used, ref - l.gather(1, at)[:, 0], torch.zeros_like(ref))
+    assert (lse.double() - ref).abs().max() <= 1e-5 * ref.abs().max()
+    assert (loss.double() - want).abs().max() <= 1e-5 * want.abs().max()
+    g = torch.exp(l - ref[:, None]).scatter_add_(1, at, -torch.ones_like(ref)[:, None])
+    g = g * torch.where(used, d.double(), torch.zeros_like(ref))[:, None]
+    _rms_close(dx, g @ w.double(), 2.0 ** -8, "dx")
+    _rms_close(dw, g.t() @ x.double(), 2.0 ** -8, "dw")
+
+
 def test_empty_batches():
     for dtype in ("bf16", "f32"):
         x, w, _, dy = glu_case(dtype, 0, 64, 104, True, False)
