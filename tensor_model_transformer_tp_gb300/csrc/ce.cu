@@ -192,16 +192,14 @@ cudaError_t bwd(const CeShape& s, const void* x, const void* w, const int64_t* t
     OASES_TRY((f32::launch<GradF32, true, true>(
         f32::Args{s.M, n, s.H, (const float*)x, s.H, wp, s.H, 0, 0},
         GradF32{g, s.ld, rows, lse, v0}, st)));
-    if (dw)
-      OASES_TRY((f32::launch<f32::Out, false, false>(
-          f32::Args{n, s.H, s.M, g, s.ld, (const float*)x, s.H, 0, 0},
-          f32::Out{static_cast<float*>(dw) + (int64_t)v0 * s.H, s.H, rows.scale, nullptr, nullptr,
-                   s.accumulate},
-          st)));
-    if (dx)
-      OASES_TRY((f32::launch<f32::Out, true, false>(
-          f32::Args{s.M, s.H, n, g, s.ld, wp, s.H, 0, 0},
-          f32::Out{(float*)dx, s.H, rows.scale, nullptr, nullptr, v0 > 0}, st)));
+    const f32::Args args[3] = {{s.M, s.H, n, g, s.ld, wp, s.H, 0, 0},
+                               {n, s.H, s.M, g, s.ld, (const float*)x, s.H, 0, 0},
+                               {}};
+    float* out_w = dw ? static_cast<float*>(dw) + (int64_t)v0 * s.H : nullptr;
+    const f32::Out out[3] = {{(float*)dx, s.H, rows.scale, nullptr, nullptr, v0 > 0},
+                             {out_w, s.H, rows.scale, nullptr, nullptr, s.accumulate},
+                             {}};
+    OASES_TRY(f32::launch_group(args, out, {true, false, false}, st));
   }
   return cudaSuccess;
 }

@@ -2,22 +2,25 @@
 // operators' fp32 form (TF32 tensor cores would round the operands to 11 bits):
 //   D[m, n] = sum_k A(m, k) B(n, k).
 //
-// 64 x 64 output tiles, 64 threads of 8 x 8 outputs each, kept as pairs along
-// m for the packed fp32x2 FMA; K goes 16 at a time through two shared-memory
+// 64 x 64 output tiles, 128 threads of 8 x 4 outputs each, kept as pairs along
+// m for the packed fp32x2 FMA; K goes 32 at a time through two shared-memory
 // buffers, the next step's elements in registers meanwhile.  The models in fp32
 // are small, so a product has few tiles: a cluster of S CTAs splits K, and the
 // partial tiles meet through distributed shared memory, each CTA summing (in
 // the order of the splits) and finishing 64 / S rows.  In a DUAL tile, B rows
 // 0..31 come from n0 and 32..63 from b_off further down (gate and up), and the
-// epilogue sees both products of an output.
+// epilogue sees both products of an output.  Several products (a backward's dx
+// and weight gradients) share a launch: alone, none of them fills the SMs.
 #pragma once
+#include <algorithm>
+
 #include "common.cuh"
 #include "sm100_ptx.cuh"
 
 namespace oases {
 namespace f32 {
 
-constexpr int BM = 64, BN = 64, BK = 16, NT = 64, LDS = 68;  // LDS: row pitch in shared memory
+constexpr int BM = 64, BN = 64, BK = 32, NT = 128, LDS = 68;  // LDS: row pitch in shared memory
 
 struct Args {
   int M, N, K;  // N: outputs per row (of each product, DUAL)
@@ -38,7 +41,7 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   return v;
 }
 
-// One step's 64 x 16 elements of an operand, four per thread and register
+// One step's 64 x 32 elements of an operand, four per thread and register
 // group: K-major rows are read 4 along k, MN-major ones 4 along the row index.
 template <bool KM, bool VEC>
 struct Loader {
@@ -51,7 +54,7 @@ struct Loader {
       const int idx = threadIdx.x + NT * i;
       float v[4] = {0.f, 0.f, 0.f, 0.f};
       if (KM) {
-        const int row = row_of(idx / 4), k = k0 + idx % 4 * 4;
+        const int row = row_of(idx / 8), k = k0 + idx % 8 * 4;
         if (row >= 0) {
           const float* q = p + (int64_t)row * ld + k;
           if (VEC) {
@@ -86,7 +89,7 @@ struct Loader {
     for (int i = 0; i < 4; ++i) {
       const int idx = threadIdx.x + NT * i;
       if (KM) {
-        const int row = idx / 4, k = idx % 4 * 4;
+        const int row = idx / 8, k = idx % 8 * 4;
         s[k * LDS + row] = r[i].x;
         s[(k + 1) * LDS + row] = r[i].y;
         s[(k + 2) * LDS + row] = r[i].z;
@@ -103,17 +106,13 @@ struct Loader {
 //   of row m (v[i] for columns inside the matrix only), or, DUAL,
 //   device void tile(m, n0, const float (&a)[4], const float (&b)[4], col, M, N).
 // Sixteen consecutive threads (8, DUAL) hold one row of a tile, in order.
+// One tile, m0 .. and n0 .., by the cluster's S CTAs.
 template <class Epi, bool A_K, bool B_K, bool VEC>
-__global__ void __launch_bounds__(NT) gemm_f32_kernel(const Args g, const Epi e) {
-  __shared__ __align__(16) float smem[2 * 2 * BK * LDS];
-  static_assert(2 * 2 * BK * LDS >= BM * BN, "the partial tile takes the buffers' place");
+__device__ __forceinline__ void tile_body(const Args& g, const Epi& e, int m0, int n0, float* smem) {
   constexpr int TN = Epi::DUAL ? BN / 2 : BN;
   const int S = gridDim.x, rank = blockIdx.x;
-  const int m0 = blockIdx.z * BM, n0 = blockIdx.y * TN;
-  const int tid = threadIdx.x, tx = tid % 8, ty = tid / 8;
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
   const int k0 = min(g.K, rank * g.kspan), kend = min(g.K, k0 + g.kspan);
-  pdl_wait();
-  pdl_trigger();
   auto row_a = [&](int i) { return m0 + i < g.M ? m0 + i : -1; };
   auto row_b = [&](int i) {
     if (Epi::DUAL) {
@@ -125,11 +124,11 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(const Args g, const Epi e)
   float *As = smem, *Bs = smem + 2 * BK * LDS;
   Loader<A_K, VEC> la;
   Loader<B_K, VEC> lb;
-  uint64_t acc[4][8];  // pairs of rows (8 ty + 2 i, + 1), columns 8 tx + j
+  uint64_t acc[4][4];  // pairs of rows (8 ty + 2 i, + 1), columns 4 tx + j
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0ull;
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
   if (k0 < kend) {
     la.load(g.a, g.lda, k0, kend, row_a);
     lb.load(g.b, g.ldb, k0, kend, row_b);
@@ -144,17 +143,16 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(const Args g, const Epi e)
       la.load(g.a, g.lda, k + BK, kend, row_a);
       lb.load(g.b, g.ldb, k + BK, kend, row_b);
     }
-    const float *pa = As + buf * BK * LDS + 8 * ty, *pb = Bs + buf * BK * LDS + 8 * tx;
-#pragma unroll
+    const float *pa = As + buf * BK * LDS + 8 * ty, *pb = Bs + buf * BK * LDS + 4 * tx;
+#pragma unroll 16
     for (int kk = 0; kk < BK; ++kk) {
       const ulonglong2 a0 = *reinterpret_cast<const ulonglong2*>(pa + kk * LDS);
       const ulonglong2 a1 = *reinterpret_cast<const ulonglong2*>(pa + kk * LDS + 4);
       const float4 b0 = *reinterpret_cast<const float4*>(pb + kk * LDS);
-      const float4 b1 = *reinterpret_cast<const float4*>(pb + kk * LDS + 4);
       const uint64_t a[4] = {a0.x, a0.y, a1.x, a1.y};
-      const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+      const float b[4] = {b0.x, b0.y, b0.z, b0.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const uint64_t bb = f2_splat(b[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i][j] = f2_fma(a[i], bb, acc[i][j]);
@@ -171,12 +169,11 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(const Args g, const Epi e)
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float* q = smem + (8 * ty + 2 * i + h) * BN + 8 * tx;
-      float v[8];
+      float v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = h ? f2_hi(acc[i][j]) : f2_lo(acc[i][j]);
-      *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      for (int j = 0; j < 4; ++j) v[j] = h ? f2_hi(acc[i][j]) : f2_lo(acc[i][j]);
+      *reinterpret_cast<float4*>(smem + (8 * ty + 2 * i + h) * BN + 4 * tx) =
+          make_float4(v[0], v[1], v[2], v[3]);
     }
   if (S > 1)
     ptx::cluster_sync();
@@ -219,6 +216,17 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(const Args g, const Epi e)
   }
 }
 
+constexpr int SMEM_FLOATS = 2 * 2 * BK * LDS;
+static_assert(SMEM_FLOATS >= BM * BN, "the partial tile takes the buffers' place");
+
+template <class Epi, bool A_K, bool B_K, bool VEC>
+__global__ void __launch_bounds__(NT) gemm_f32_kernel(const Args g, const Epi e) {
+  __shared__ __align__(16) float smem[SMEM_FLOATS];
+  pdl_wait();
+  pdl_trigger();
+  tile_body<Epi, A_K, B_K, VEC>(g, e, blockIdx.z * BM, blockIdx.y * (Epi::DUAL ? BN / 2 : BN), smem);
+}
+
 // C (+)= scale * D + bias + resid, each optional; resid may be C.
 struct Out {
   static constexpr bool DUAL = false;
@@ -243,36 +251,114 @@ struct Out {
   }
 };
 
+// Products with MN-major B in one launch, tiles in order; A is K-major where a_k.
+struct Group {
+  Args g[3];
+  Out e[3];
+  int a_k[3], vec[3], tn[3];
+  int end[3];  // tiles of products 0 .. i
+};
+static __global__ void __launch_bounds__(NT) gemm_f32_group_kernel(const Group q) {
+  __shared__ __align__(16) float smem[SMEM_FLOATS];
+  pdl_wait();
+  pdl_trigger();
+  const int t = blockIdx.y, i = t < q.end[0] ? 0 : t < q.end[1] ? 1 : 2;
+  const int r = t - (i ? q.end[i - 1] : 0), m0 = r / q.tn[i] * BM, n0 = r % q.tn[i] * BN;
+  if (q.a_k[i]) {
+    if (q.vec[i])
+      tile_body<Out, true, false, true>(q.g[i], q.e[i], m0, n0, smem);
+    else
+      tile_body<Out, true, false, false>(q.g[i], q.e[i], m0, n0, smem);
+  } else {
+    if (q.vec[i])
+      tile_body<Out, false, false, true>(q.g[i], q.e[i], m0, n0, smem);
+    else
+      tile_body<Out, false, false, false>(q.g[i], q.e[i], m0, n0, smem);
+  }
+}
+
+// CTAs of the cluster that splits a contraction over K: while the launch has
+// fewer than four CTAs per SM and a CTA keeps two steps of K.
+inline int split_of(int64_t tiles, int K) {
+  int S = 1;
+  while (S < 8 && tiles * S * 2 <= 152 * 4 && K >= S * 2 * 2 * BK) S *= 2;
+  return S;
+}
+inline int span_of(int K, int S) { return ((K + S - 1) / S + BK - 1) / BK * BK; }
+// 16-byte loads: every row starts on one and the extents read are whole ones.
+inline bool vector_loads(const Args& g, bool a_k, bool b_k) {
+  auto ok4 = [](const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 4 == 0; };
+  return ok4(g.a, g.lda) && ok4(g.b, g.ldb) && (!(a_k || b_k) || g.K % 4 == 0) &&
+         (a_k || g.M % 4 == 0) && (b_k || g.N % 4 == 0);
+}
+inline void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attrs, dim3 grid, cudaStream_t st) {
+  *cfg = {};
+  cfg->gridDim = grid;
+  cfg->blockDim = dim3(NT);
+  cfg->stream = st;
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = grid.x;
+  attrs[1].val.clusterDim.y = 1;
+  attrs[1].val.clusterDim.z = 1;
+  cfg->attrs = attrs;
+  cfg->numAttrs = 2;
+  ++g_launch_count;
+}
+
 template <class Epi, bool A_K, bool B_K>
 cudaError_t launch(Args g, const Epi& e, cudaStream_t st) {
   constexpr int TN = Epi::DUAL ? BN / 2 : BN;
   if (g.M == 0 || g.N == 0) return cudaSuccess;
   const int64_t tm = (g.M + BM - 1) / BM, tn = (g.N + TN - 1) / TN;
   if (tm > 65535 || tn > 65535) return cudaErrorInvalidConfiguration;
-  // split K while the SMs hold fewer than four CTAs each and a CTA keeps two steps
-  int S = 1;
-  while (S < 8 && tm * tn * S * 2 <= 152 * 6 && g.K >= S * 2 * 2 * BK) S *= 2;
-  g.kspan = ((g.K + S - 1) / S + BK - 1) / BK * BK;
-  auto ok4 = [](const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 4 == 0; };
-  // 16-byte loads: every row starts on one and the extents read are whole ones
-  const bool vec = ok4(g.a, g.lda) && ok4(g.b, g.ldb) && (A_K || B_K ? g.K % 4 == 0 : true) &&
-                   (A_K || g.M % 4 == 0) && (B_K || g.N % 4 == 0);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)S, (unsigned)tn, (unsigned)tm);
-  cfg.blockDim = dim3(NT);
-  cfg.stream = st;
+  const int S = split_of(tm * tn, g.K);
+  g.kspan = span_of(g.K, S);
+  cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attrs[2];
-  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attrs[0].val.programmaticStreamSerializationAllowed = 1;
-  attrs[1].id = cudaLaunchAttributeClusterDimension;
-  attrs[1].val.clusterDim.x = S;
-  attrs[1].val.clusterDim.y = 1;
-  attrs[1].val.clusterDim.z = 1;
-  cfg.attrs = attrs;
-  cfg.numAttrs = 2;
-  ++g_launch_count;
-  return vec ? cudaLaunchKernelEx(&cfg, gemm_f32_kernel<Epi, A_K, B_K, true>, g, e)
+  configure(&cfg, attrs, dim3((unsigned)S, (unsigned)tn, (unsigned)tm), st);
+  return vector_loads(g, A_K, B_K)
+             ? cudaLaunchKernelEx(&cfg, gemm_f32_kernel<Epi, A_K, B_K, true>, g, e)
              : cudaLaunchKernelEx(&cfg, gemm_f32_kernel<Epi, A_K, B_K, false>, g, e);
+}
+
+// Up to three products with MN-major B; those with no output (e.c null) are left out.
+static inline cudaError_t launch_group(const Args (&g)[3], const Out (&e)[3], const bool (&a_k)[3],
+                                cudaStream_t st) {
+  Group q = {};
+  int n = 0, K = INT32_MAX;
+  int64_t tiles = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!e[i].c || g[i].M == 0 || g[i].N == 0) continue;
+    const int64_t tm = (g[i].M + BM - 1) / BM, tn = (g[i].N + BN - 1) / BN;
+    tiles += tm * tn;
+    if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+    q.g[n] = g[i];
+    q.e[n] = e[i];
+    q.a_k[n] = a_k[i];
+    q.vec[n] = vector_loads(g[i], a_k[i], false);
+    q.tn[n] = (int)tn;
+    q.end[n] = (int)tiles;
+    K = std::min(K, g[i].K);
+    ++n;
+  }
+  if (n == 0) return cudaSuccess;
+  for (int i = n; i < 3; ++i) q.end[i] = (int)tiles;
+  if (tiles > 65535) {  // more tiles than a grid dimension holds
+    for (int i = 0; i < n; ++i) {
+      const cudaError_t err = q.a_k[i] ? launch<Out, true, false>(q.g[i], q.e[i], st)
+                                       : launch<Out, false, false>(q.g[i], q.e[i], st);
+      if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+  }
+  const int S = split_of(tiles, K);
+  for (int i = 0; i < n; ++i) q.g[i].kspan = span_of(q.g[i].K, S);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attrs[2];
+  configure(&cfg, attrs, dim3((unsigned)S, (unsigned)tiles), st);
+  return cudaLaunchKernelEx(&cfg, gemm_f32_group_kernel, q);
 }
 
 }  // namespace f32

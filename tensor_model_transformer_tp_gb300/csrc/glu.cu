@@ -266,14 +266,6 @@ cudaError_t fwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
       g, f32::Out{(float*)y, s.H, nullptr, (const float*)w.b2, (const float*)resid, 0}, st);
 }
 
-// fp32: dW [N, K] (+)= A^T B over the rows, A [M, N], B [M, K].
-cudaError_t weight_grad(const GluShape& s, const void* A, int N, const void* B, int K, void* out,
-                        cudaStream_t st) {
-  const f32::Args g{N, K, s.M, (const float*)A, N, (const float*)B, K, 0, 0};
-  return f32::launch<f32::Out, false, false>(
-      g, f32::Out{(float*)out, K, nullptr, nullptr, nullptr, s.accumulate}, st);
-}
-
 cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, const void* dy,
                 const void* saved, void* dx, const oases_glu_grads& gr, char* ws, cudaStream_t st) {
   const Layout l = layout(s, true);
@@ -294,13 +286,17 @@ cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
     const f32::Args g{s.M, s.F, s.H, (const float*)dy, s.H, (const float*)w.w2, s.F, 0, 0};
     OASES_TRY((f32::launch<GradF32, true, false>(
         g, GradF32{(const float*)pre, (float*)dpre, (float*)h, s.act}, st)));
-    if (gr.w2) OASES_TRY(weight_grad(s, dy, s.H, h, s.F, gr.w2, st));
-    if (gr.w1) OASES_TRY(weight_grad(s, dpre, 2 * s.F, x, s.H, gr.w1, st));
-    if (dx) {
-      const f32::Args q{s.M, s.H, 2 * s.F, (const float*)dpre, 2 * s.F, (const float*)w.w1, s.H, 0, 0};
-      OASES_TRY((f32::launch<f32::Out, true, false>(
-          q, f32::Out{(float*)dx, s.H, nullptr, nullptr, nullptr, 0}, st)));
-    }
+    // dx, dw1 = dpre^T x, dw2 = dy^T h
+    const float *px = (const float*)x, *pdy = (const float*)dy, *pw1 = (const float*)w.w1;
+    const float *pd = (const float*)dpre, *ph = (const float*)h;
+    const f32::Args args[3] = {{s.M, s.H, 2 * s.F, pd, 2 * s.F, pw1, s.H, 0, 0},
+                               {2 * s.F, s.H, s.M, pd, 2 * s.F, px, s.H, 0, 0},
+                               {s.H, s.F, s.M, pdy, s.H, ph, s.F, 0, 0}};
+    const int acc = s.accumulate;
+    const f32::Out out[3] = {{(float*)dx, s.H, nullptr, nullptr, nullptr, 0},
+                             {(float*)gr.w1, s.H, nullptr, nullptr, nullptr, acc},
+                             {(float*)gr.w2, s.F, nullptr, nullptr, nullptr, acc}};
+    OASES_TRY(f32::launch_group(args, out, {true, false, false}, st));
   }
   return bias_grads(s, dpre, dy, gr, reinterpret_cast<float*>(ws + l.part),
                     reinterpret_cast<float*>(ws + l.bias), st);
