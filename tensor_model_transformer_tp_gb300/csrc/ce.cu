@@ -130,7 +130,10 @@ struct GradF32 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = n0 + col + i;
-      if (n >= N) break;
+      if (n >= N) {  // the row's padding
+        if (n < ld) g[(int64_t)m * ld + n] = 0.f;
+        continue;
+      }
       const float p = expf(v[i] - l) - (t == v0 + n ? 1.f : 0.f);
       g[(int64_t)m * ld + n] = t == rows.ignore ? 0.f : p * r;
     }
@@ -166,7 +169,7 @@ cudaError_t fwd(const CeShape& s, const void* x, const void* w, const int64_t* t
     const StatF32 e{reinterpret_cast<float2*>(ws + l.part), reinterpret_cast<float*>(ws + l.at),
                     target + m0};
     const f32::Args g{M, s.V, s.H, static_cast<const float*>(x) + (int64_t)m0 * s.H, s.H,
-                      static_cast<const float*>(w), s.H, 0, 0};
+                      static_cast<const float*>(w), s.H};
     OASES_TRY((f32::launch<StatF32, true, true>(g, e, st)));
     OASES_TRY(ce_join(e.part, f32_slots(s), e.at, e.target, s, M, loss + m0, lse + m0, st));
   }
@@ -190,10 +193,10 @@ cudaError_t bwd(const CeShape& s, const void* x, const void* w, const int64_t* t
     const int n = std::min(s.piece, s.V - v0);
     const float* wp = static_cast<const float*>(w) + (int64_t)v0 * s.H;
     OASES_TRY((f32::launch<GradF32, true, true>(
-        f32::Args{s.M, n, s.H, (const float*)x, s.H, wp, s.H, 0, 0},
+        f32::Args{s.M, n, s.H, (const float*)x, s.H, wp, s.H},
         GradF32{g, s.ld, rows, lse, v0}, st)));
-    const f32::Args args[3] = {{s.M, s.H, n, g, s.ld, wp, s.H, 0, 0},
-                               {n, s.H, s.M, g, s.ld, (const float*)x, s.H, 0, 0},
+    const f32::Args args[3] = {{s.M, s.H, n, g, s.ld, wp, s.H, 0, 1},
+                               {n, s.H, s.M, g, s.ld, (const float*)x, s.H, 0, 1},
                                {}};
     float* out_w = dw ? static_cast<float*>(dw) + (int64_t)v0 * s.H : nullptr;
     const f32::Out out[3] = {{(float*)dx, s.H, rows.scale, nullptr, nullptr, v0 > 0},

@@ -20,7 +20,13 @@
 namespace oases {
 namespace f32 {
 
-constexpr int BM = 64, BN = 64, BK = 32, NT = 128, LDS = 68;  // LDS: row pitch in shared memory
+constexpr int BM = 64, BN = 64, BK = 32, NT = 128;
+constexpr int CLUSTER = 8;  // largest split of a contraction
+
+// Operand tiles in shared memory are [BK][64] with each k's sixteen groups of
+// four rows permuted by k / 4, so that the transposing stores of a K-major
+// operand (eight k / 4 by four rows per warp) meet no bank twice.
+__device__ __forceinline__ int at_of(int k, int row) { return k * 64 + (((row >> 2) ^ ((k >> 2) & 7)) << 2) + (row & 3); }
 
 struct Args {
   int M, N, K;  // N: outputs per row (of each product, DUAL)
@@ -28,8 +34,9 @@ struct Args {
   int64_t lda;
   const float* b;
   int64_t ldb;
-  int b_off;  // DUAL: row offset of the second product's B
-  int kspan;  // K per CTA of the cluster, a multiple of BK
+  int b_off = 0;   // DUAL: row offset of the second product's B
+  int padded = 0;  // a's rows go on with finite values up to a multiple of four elements
+  int kspan = 0;   // K per CTA of the cluster, a multiple of BK
 };
 
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
@@ -90,12 +97,13 @@ struct Loader {
       const int idx = threadIdx.x + NT * i;
       if (KM) {
         const int row = idx / 8, k = idx % 8 * 4;
-        s[k * LDS + row] = r[i].x;
-        s[(k + 1) * LDS + row] = r[i].y;
-        s[(k + 2) * LDS + row] = r[i].z;
-        s[(k + 3) * LDS + row] = r[i].w;
+        float* q = s + at_of(k, row);  // k .. k+3 share the permutation
+        q[0] = r[i].x;
+        q[64] = r[i].y;
+        q[128] = r[i].z;
+        q[192] = r[i].w;
       } else {
-        *reinterpret_cast<float4*>(s + idx / 16 * LDS + idx % 16 * 4) = r[i];
+        *reinterpret_cast<float4*>(s + at_of(idx / 16, idx % 16 * 4)) = r[i];
       }
     }
   }
@@ -106,13 +114,15 @@ struct Loader {
 //   of row m (v[i] for columns inside the matrix only), or, DUAL,
 //   device void tile(m, n0, const float (&a)[4], const float (&b)[4], col, M, N).
 // Sixteen consecutive threads (8, DUAL) hold one row of a tile, in order.
-// One tile, m0 .. and n0 .., by the cluster's S CTAs.
+// One tile, m0 .. and n0 .., by S CTAs of the cluster, rank0 .. rank0 + S - 1.
+// (m0 past the matrix: a CTA of the cluster with no tile.)
 template <class Epi, bool A_K, bool B_K, bool VEC>
-__device__ __forceinline__ void tile_body(const Args& g, const Epi& e, int m0, int n0, float* smem) {
+__device__ __forceinline__ void tile_body(const Args& g, const Epi& e, int m0, int n0, int S, int rank0,
+                                          float* smem) {
   constexpr int TN = Epi::DUAL ? BN / 2 : BN;
-  const int S = gridDim.x, rank = blockIdx.x;
+  const int rank = (int)blockIdx.x - rank0;
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  const int k0 = min(g.K, rank * g.kspan), kend = min(g.K, k0 + g.kspan);
+  const int k0 = min(m0 < g.M ? g.K : 0, rank * g.kspan), kend = min(m0 < g.M ? g.K : 0, k0 + g.kspan);
   auto row_a = [&](int i) { return m0 + i < g.M ? m0 + i : -1; };
   auto row_b = [&](int i) {
     if (Epi::DUAL) {
@@ -121,7 +131,7 @@ __device__ __forceinline__ void tile_body(const Args& g, const Epi& e, int m0, i
     }
     return n0 + i < g.N ? n0 + i : -1;
   };
-  float *As = smem, *Bs = smem + 2 * BK * LDS;
+  float *As = smem, *Bs = smem + 2 * BK * 64;
   Loader<A_K, VEC> la;
   Loader<B_K, VEC> lb;
   uint64_t acc[4][4];  // pairs of rows (8 ty + 2 i, + 1), columns 4 tx + j
@@ -143,12 +153,12 @@ __device__ __forceinline__ void tile_body(const Args& g, const Epi& e, int m0, i
       la.load(g.a, g.lda, k + BK, kend, row_a);
       lb.load(g.b, g.ldb, k + BK, kend, row_b);
     }
-    const float *pa = As + buf * BK * LDS + 8 * ty, *pb = Bs + buf * BK * LDS + 4 * tx;
-#pragma unroll 16
+    const float *pa = As + buf * BK * 64, *pb = Bs + buf * BK * 64;
+#pragma unroll
     for (int kk = 0; kk < BK; ++kk) {
-      const ulonglong2 a0 = *reinterpret_cast<const ulonglong2*>(pa + kk * LDS);
-      const ulonglong2 a1 = *reinterpret_cast<const ulonglong2*>(pa + kk * LDS + 4);
-      const float4 b0 = *reinterpret_cast<const float4*>(pb + kk * LDS);
+      const ulonglong2 a0 = *reinterpret_cast<const ulonglong2*>(pa + at_of(kk, 8 * ty));
+      const ulonglong2 a1 = *reinterpret_cast<const ulonglong2*>(pa + at_of(kk, 8 * ty + 4));
+      const float4 b0 = *reinterpret_cast<const float4*>(pb + at_of(kk, 4 * tx));
       const uint64_t a[4] = {a0.x, a0.y, a1.x, a1.y};
       const float b[4] = {b0.x, b0.y, b0.z, b0.w};
 #pragma unroll
@@ -159,8 +169,8 @@ __device__ __forceinline__ void tile_body(const Args& g, const Epi& e, int m0, i
       }
     }
     if (more) {
-      la.store(As + (buf ^ 1) * BK * LDS);
-      lb.store(Bs + (buf ^ 1) * BK * LDS);
+      la.store(As + (buf ^ 1) * BK * 64);
+      lb.store(Bs + (buf ^ 1) * BK * 64);
     }
     __syncthreads();
   }
@@ -175,18 +185,18 @@ __device__ __forceinline__ void tile_body(const Args& g, const Epi& e, int m0, i
       *reinterpret_cast<float4*>(smem + (8 * ty + 2 * i + h) * BN + 4 * tx) =
           make_float4(v[0], v[1], v[2], v[3]);
     }
-  if (S > 1)
+  if (gridDim.x > 1)
     ptx::cluster_sync();
   else
     __syncthreads();
   const uint32_t base = ptx::smem_u32(smem);
-  uint32_t from[8];
+  uint32_t from[CLUSTER];
 #pragma unroll
-  for (int s = 0; s < 8; ++s) from[s] = s < S ? ptx::mapa(base, (uint32_t)s) : 0u;
+  for (int s = 0; s < CLUSTER; ++s) from[s] = s < S ? ptx::mapa(base, (uint32_t)(rank0 + s)) : 0u;
   auto total = [&](int at, float (&v)[4]) {
     v[0] = v[1] = v[2] = v[3] = 0.f;
 #pragma unroll
-    for (int s = 0; s < 8; ++s)
+    for (int s = 0; s < CLUSTER; ++s)
       if (s < S) {
         const float4 q = ld_cluster4(from[s] + 4u * at);
         v[0] += q.x;
@@ -210,21 +220,22 @@ __device__ __forceinline__ void tile_body(const Args& g, const Epi& e, int m0, i
       e.tile(m, n0, v, col, g.M, g.N);
     }
   }
-  if (S > 1) {
+  if (gridDim.x > 1) {
     __syncwarp();
     ptx::cluster_sync();  // no CTA leaves while another reads its partial tile
   }
 }
 
-constexpr int SMEM_FLOATS = 2 * 2 * BK * LDS;
+constexpr int SMEM_FLOATS = 2 * 2 * BK * 64;
 static_assert(SMEM_FLOATS >= BM * BN, "the partial tile takes the buffers' place");
 
 template <class Epi, bool A_K, bool B_K, bool VEC>
-__global__ void __launch_bounds__(NT) gemm_f32_kernel(const Args g, const Epi e) {
+__global__ void __launch_bounds__(NT, 4) gemm_f32_kernel(const Args g, const Epi e) {
   __shared__ __align__(16) float smem[SMEM_FLOATS];
   pdl_wait();
   pdl_trigger();
-  tile_body<Epi, A_K, B_K, VEC>(g, e, blockIdx.z * BM, blockIdx.y * (Epi::DUAL ? BN / 2 : BN), smem);
+  tile_body<Epi, A_K, B_K, VEC>(g, e, blockIdx.z * BM, blockIdx.y * (Epi::DUAL ? BN / 2 : BN),
+                                gridDim.x, 0, smem);
 }
 
 // C (+)= scale * D + bias + resid, each optional; resid may be C.
@@ -251,45 +262,50 @@ struct Out {
   }
 };
 
-// Products with MN-major B in one launch, tiles in order; A is K-major where a_k.
+// Products with MN-major B in one launch; A is K-major where a_k.  Product i
+// splits its contraction over split[i] CTAs, so a cluster takes CLUSTER /
+// split[i] of its tiles; its clusters are end[i - 1] .. end[i] - 1.
 struct Group {
   Args g[3];
   Out e[3];
-  int a_k[3], vec[3], tn[3];
-  int end[3];  // tiles of products 0 .. i
+  int a_k[3], vec[3], tn[3], split[3], end[3];
 };
-static __global__ void __launch_bounds__(NT) gemm_f32_group_kernel(const Group q) {
+static __global__ void __launch_bounds__(NT, 4) gemm_f32_group_kernel(const Group q) {
   __shared__ __align__(16) float smem[SMEM_FLOATS];
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.y, i = t < q.end[0] ? 0 : t < q.end[1] ? 1 : 2;
-  const int r = t - (i ? q.end[i - 1] : 0), m0 = r / q.tn[i] * BM, n0 = r % q.tn[i] * BN;
+  const int c = blockIdx.y, i = c < q.end[0] ? 0 : c < q.end[1] ? 1 : 2;
+  const int S = q.split[i], rank0 = (int)blockIdx.x / S * S;
+  const int r = (c - (i ? q.end[i - 1] : 0)) * ((int)gridDim.x / S) + (int)blockIdx.x / S;
+  const int m0 = r / q.tn[i] * BM, n0 = r % q.tn[i] * BN;
   if (q.a_k[i]) {
     if (q.vec[i])
-      tile_body<Out, true, false, true>(q.g[i], q.e[i], m0, n0, smem);
+      tile_body<Out, true, false, true>(q.g[i], q.e[i], m0, n0, S, rank0, smem);
     else
-      tile_body<Out, true, false, false>(q.g[i], q.e[i], m0, n0, smem);
+      tile_body<Out, true, false, false>(q.g[i], q.e[i], m0, n0, S, rank0, smem);
   } else {
     if (q.vec[i])
-      tile_body<Out, false, false, true>(q.g[i], q.e[i], m0, n0, smem);
+      tile_body<Out, false, false, true>(q.g[i], q.e[i], m0, n0, S, rank0, smem);
     else
-      tile_body<Out, false, false, false>(q.g[i], q.e[i], m0, n0, smem);
+      tile_body<Out, false, false, false>(q.g[i], q.e[i], m0, n0, S, rank0, smem);
   }
 }
 
-// CTAs of the cluster that splits a contraction over K: while the launch has
-// fewer than four CTAs per SM and a CTA keeps two steps of K.
-inline int split_of(int64_t tiles, int K) {
+// CTAs that split a contraction over K: a CTA is left the K-steps that an even
+// share of the launch's would give it with four CTAs per SM, two at least.
+inline int split_of(int64_t launch_steps, int K) {
+  const int64_t share = std::max<int64_t>(2, launch_steps / (4 * 152)), steps = (K + BK - 1) / BK;
   int S = 1;
-  while (S < 8 && tiles * S * 2 <= 152 * 4 && K >= S * 2 * 2 * BK) S *= 2;
+  while (S < CLUSTER && steps > S * share) S *= 2;
   return S;
 }
 inline int span_of(int K, int S) { return ((K + S - 1) / S + BK - 1) / BK * BK; }
 // 16-byte loads: every row starts on one and the extents read are whole ones.
+// What a padded row of A has past K meets zeros of B, past M no output.
 inline bool vector_loads(const Args& g, bool a_k, bool b_k) {
   auto ok4 = [](const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 4 == 0; };
-  return ok4(g.a, g.lda) && ok4(g.b, g.ldb) && (!(a_k || b_k) || g.K % 4 == 0) &&
-         (a_k || g.M % 4 == 0) && (b_k || g.N % 4 == 0);
+  return ok4(g.a, g.lda) && ok4(g.b, g.ldb) && (g.padded || (a_k ? g.K : g.M) % 4 == 0) &&
+         (b_k ? g.K : g.N) % 4 == 0;
 }
 inline void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attrs, dim3 grid, cudaStream_t st) {
   *cfg = {};
@@ -313,7 +329,7 @@ cudaError_t launch(Args g, const Epi& e, cudaStream_t st) {
   if (g.M == 0 || g.N == 0) return cudaSuccess;
   const int64_t tm = (g.M + BM - 1) / BM, tn = (g.N + TN - 1) / TN;
   if (tm > 65535 || tn > 65535) return cudaErrorInvalidConfiguration;
-  const int S = split_of(tm * tn, g.K);
+  const int S = split_of(tm * tn * ((g.K + BK - 1) / BK), g.K);
   g.kspan = span_of(g.K, S);
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attrs[2];
@@ -327,25 +343,34 @@ cudaError_t launch(Args g, const Epi& e, cudaStream_t st) {
 static inline cudaError_t launch_group(const Args (&g)[3], const Out (&e)[3], const bool (&a_k)[3],
                                 cudaStream_t st) {
   Group q = {};
-  int n = 0, K = INT32_MAX;
-  int64_t tiles = 0;
+  int n = 0;
+  int64_t tiles[3], steps = 0;
   for (int i = 0; i < 3; ++i) {
     if (!e[i].c || g[i].M == 0 || g[i].N == 0) continue;
     const int64_t tm = (g[i].M + BM - 1) / BM, tn = (g[i].N + BN - 1) / BN;
-    tiles += tm * tn;
-    if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+    tiles[n] = tm * tn;
+    steps += tiles[n] * ((g[i].K + BK - 1) / BK);
     q.g[n] = g[i];
     q.e[n] = e[i];
     q.a_k[n] = a_k[i];
     q.vec[n] = vector_loads(g[i], a_k[i], false);
     q.tn[n] = (int)tn;
-    q.end[n] = (int)tiles;
-    K = std::min(K, g[i].K);
     ++n;
   }
   if (n == 0) return cudaSuccess;
-  for (int i = n; i < 3; ++i) q.end[i] = (int)tiles;
-  if (tiles > 65535) {  // more tiles than a grid dimension holds
+  int64_t clusters = 0;
+  for (int i = 0; i < n; ++i) {
+    q.split[i] = split_of(steps, q.g[i].K);
+    q.g[i].kspan = span_of(q.g[i].K, q.split[i]);
+    const int per = CLUSTER / q.split[i];
+    clusters += (tiles[i] + per - 1) / per;
+    q.end[i] = (int)std::min<int64_t>(clusters, INT32_MAX);
+  }
+  for (int i = n; i < 3; ++i) {
+    q.split[i] = 1;
+    q.end[i] = q.end[n - 1];
+  }
+  if (clusters > 65535) {  // more than a grid dimension holds
     for (int i = 0; i < n; ++i) {
       const cudaError_t err = q.a_k[i] ? launch<Out, true, false>(q.g[i], q.e[i], st)
                                        : launch<Out, false, false>(q.g[i], q.e[i], st);
@@ -353,11 +378,9 @@ static inline cudaError_t launch_group(const Args (&g)[3], const Out (&e)[3], co
     }
     return cudaSuccess;
   }
-  const int S = split_of(tiles, K);
-  for (int i = 0; i < n; ++i) q.g[i].kspan = span_of(q.g[i].K, S);
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attrs[2];
-  configure(&cfg, attrs, dim3((unsigned)S, (unsigned)tiles), st);
+  configure(&cfg, attrs, dim3(CLUSTER, (unsigned)clusters), st);
   return cudaLaunchKernelEx(&cfg, gemm_f32_group_kernel, q);
 }
 

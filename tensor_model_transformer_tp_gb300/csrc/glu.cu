@@ -250,7 +250,7 @@ cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, cons
 cudaError_t project(const GluShape& s, const oases_glu_weights& w, const void* x, void* h, void* pre,
                     void* kept8, cudaStream_t st) {
   if (s.t == DType::BF16) return glu_project_tc(s, x, w.w1, w.b1, h, pre, kept8, st);
-  const f32::Args g{s.M, s.F, s.H, (const float*)x, s.H, (const float*)w.w1, s.H, s.F, 0};
+  const f32::Args g{s.M, s.F, s.H, (const float*)x, s.H, (const float*)w.w1, s.H, s.F};
   return f32::launch<UpF32, true, true>(
       g, UpF32{(const float*)w.b1, (float*)h, (float*)pre, s.act}, st);
 }
@@ -261,7 +261,7 @@ cudaError_t fwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
   OASES_TRY(project(s, w, x, h, s.keep == OASES_GLU_KEEP_PRE ? saved : nullptr,
                     s.keep == OASES_GLU_KEEP_MXFP8 ? saved : nullptr, st));
   if (s.t == DType::BF16) return glu_down_tc(s, h, w.w2, w.b2, resid, y, st);
-  const f32::Args g{s.M, s.H, s.F, (const float*)h, s.F, (const float*)w.w2, s.F, 0, 0};
+  const f32::Args g{s.M, s.H, s.F, (const float*)h, s.F, (const float*)w.w2, s.F};
   return f32::launch<f32::Out, true, true>(
       g, f32::Out{(float*)y, s.H, nullptr, (const float*)w.b2, (const float*)resid, 0}, st);
 }
@@ -283,15 +283,15 @@ cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
     OASES_TRY(glu_grad_tc(s, dy, w.w2, pre, kept8, dpre, h, st));
     OASES_TRY(glu_grads_tc(s, x, dy, w.w1, dpre, h, dx, gr.w1, gr.w2, ws + l.dx, st));
   } else {
-    const f32::Args g{s.M, s.F, s.H, (const float*)dy, s.H, (const float*)w.w2, s.F, 0, 0};
+    const f32::Args g{s.M, s.F, s.H, (const float*)dy, s.H, (const float*)w.w2, s.F};
     OASES_TRY((f32::launch<GradF32, true, false>(
         g, GradF32{(const float*)pre, (float*)dpre, (float*)h, s.act}, st)));
     // dx, dw1 = dpre^T x, dw2 = dy^T h
     const float *px = (const float*)x, *pdy = (const float*)dy, *pw1 = (const float*)w.w1;
     const float *pd = (const float*)dpre, *ph = (const float*)h;
-    const f32::Args args[3] = {{s.M, s.H, 2 * s.F, pd, 2 * s.F, pw1, s.H, 0, 0},
-                               {2 * s.F, s.H, s.M, pd, 2 * s.F, px, s.H, 0, 0},
-                               {s.H, s.F, s.M, pdy, s.H, ph, s.F, 0, 0}};
+    const f32::Args args[3] = {{s.M, s.H, 2 * s.F, pd, 2 * s.F, pw1, s.H},
+                               {2 * s.F, s.H, s.M, pd, 2 * s.F, px, s.H},
+                               {s.H, s.F, s.M, pdy, s.H, ph, s.F}};
     const int acc = s.accumulate;
     const f32::Out out[3] = {{(float*)dx, s.H, nullptr, nullptr, nullptr, 0},
                              {(float*)gr.w1, s.H, nullptr, nullptr, nullptr, acc},
