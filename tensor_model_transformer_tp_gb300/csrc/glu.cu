@@ -18,8 +18,8 @@ oases_status api_end(cudaError_t e);
 
 namespace {
 
-// Bias gradients of up to this many rows are summed by one launch, a column per
-// thread and 16 row groups; more rows go through partial rows.
+// Bias gradients of up to this many rows are summed by one launch, two columns per
+// thread and 32 row groups; more rows go through partial rows.
 constexpr int DIRECT_SUM_ROWS = 2048;
 
 oases_status glu_shape(const oases_glu_desc* d, GluShape* s) {
@@ -155,31 +155,31 @@ struct Sums {
   void* out[2];
   int N[2];
 };
-// Two neighbouring columns per thread, 16 warps over the rows.
+// Two neighbouring columns per thread; 32 columns and 32 row groups per block.
 __device__ __forceinline__ float2 ld_pair(const float* p) { return *reinterpret_cast<const float2*>(p); }
 __device__ __forceinline__ float2 ld_pair(const __nv_bfloat16* p) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
 }
 template <typename T, typename O>
 __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, int accumulate) {
-  __shared__ float2 red[16][33];
+  __shared__ float2 red[32][17];
   pdl_wait();
   pdl_trigger();
-  const int x = threadIdx.x, y = threadIdx.y, first = (s.N[0] + 63) / 64;
+  const int x = threadIdx.x % 16, y = threadIdx.x / 16, first = (s.N[0] + 31) / 32;
   const int which = (int)blockIdx.x < first ? 0 : 1;
-  const int n = ((int)blockIdx.x - (which ? first : 0)) * 64 + 2 * x, N = s.N[which];
+  const int n = ((int)blockIdx.x - (which ? first : 0)) * 32 + 2 * x, N = s.N[which];
   const T* in = static_cast<const T*>(s.in[which]) + n;
   const bool second = n + 1 < N;
   float2 v = make_float2(0.f, 0.f);
   if (N % 2 == 0 && n < N) {  // one 4- or 8-byte load per row
-#pragma unroll 8
-    for (int m = y; m < M; m += 16) {
+#pragma unroll 16
+    for (int m = y; m < M; m += 32) {
       const float2 q = ld_pair(in + (int64_t)m * N);
       v.x += q.x;
       v.y += q.y;
     }
   } else if (n < N) {
-    for (int m = y; m < M; m += 16) {
+    for (int m = y; m < M; m += 32) {
       v.x += ld_elem(in, (int64_t)m * N);
       if (second) v.y += ld_elem(in, (int64_t)m * N + 1);
     }
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, i
   red[y][x] = v;
   __syncthreads();
   if (y == 0 && n < N) {
-    for (int i = 1; i < 16; ++i) {
+    for (int i = 1; i < 32; ++i) {
       v.x += red[i][x].x;
       v.y += red[i][x].y;
     }
@@ -237,7 +237,7 @@ cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, cons
     return cudaSuccess;
   }
   const Sums q{{dpre, dy}, {gr.b1, gr.b2}, {gr.b1 ? 2 * s.F : 0, gr.b2 ? s.H : 0}};
-  const dim3 grid((unsigned)((q.N[0] + 63) / 64 + (q.N[1] + 63) / 64)), block(32, 16);
+  const dim3 grid((unsigned)((q.N[0] + 31) / 32 + (q.N[1] + 31) / 32)), block(512);
   const int acc = s.accumulate ? 1 : 0;
   if (s.t == DType::F32)
     return launch_pdl(column_sums_kernel<float, float>, grid, block, 0, st, q, s.M, acc);
