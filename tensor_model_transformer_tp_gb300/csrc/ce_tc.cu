@@ -194,28 +194,6 @@ struct EpiG {
   };
 };
 
-// dx = s * sum of the splits' partial products, in their order.
-__global__ void __launch_bounds__(256)
-ce_slabs_kernel(const float* slabs, int splits, int64_t slab, const float* scale, __nv_bfloat16* dx,
-                int64_t n) {
-  pdl_wait();
-  pdl_trigger();
-  const float s = *scale;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n / 4;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int z = 0; z < splits; ++z) {
-      const float4 q = *reinterpret_cast<const float4*>(slabs + z * slab + 4 * i);
-      a.x += q.x;
-      a.y += q.y;
-      a.z += q.z;
-      a.w += q.w;
-    }
-    reinterpret_cast<uint2*>(dx)[i] = make_uint2(pack2(s * a.x, s * a.y), pack2(s * a.z, s * a.w));
-  }
-}
-
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Tiles of the logits: 128 columns while one row block holds every row (the
@@ -245,8 +223,7 @@ BwdPlan bwd_plan(const CeShape& s) {
   const int slots = s.M <= 128 ? core::sm_count() : core::sm_count() / 2;
   b.splits = pieces == 1 ? std::max(1, std::min(slots / tiles, s.V / 512)) : 1;
   core::slices_per_split(s.V, &b.splits);
-  const int64_t rows = (s.M + 255) / 256 * 256;
-  b.slab = rows * s.H;
+  b.slab = (int64_t)core::slab_rows(s.M) * s.H;
   b.g = 0;
   b.dx = align256((size_t)s.M * b.ld * 2);
   b.total = b.dx;
@@ -358,11 +335,8 @@ cudaError_t ce_tc_bwd(const CeShape& s, const void* x, const void* w, const CeRo
       if (dw) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_dw, e_dw, st)));
     }
     if (dx && b.splits > 1) {
-      const int64_t count = (int64_t)s.M * s.H;
-      OASES_TRY(launch_pdl(ce_slabs_kernel,
-                           dim3((unsigned)std::min<int64_t>((count / 4 + 255) / 256, 152 * 8)),
-                           dim3(256), 0, st, (const float*)dx32, b.splits, b.slab, rows.scale,
-                           static_cast<__nv_bfloat16*>(dx), count));
+      OASES_TRY(core::slab_sum(dx32, b.splits, b.slab, rows.scale, nullptr, nullptr, dx, DType::BF16, s.M,
+                               s.H, st));
     }
   }
   return cudaSuccess;

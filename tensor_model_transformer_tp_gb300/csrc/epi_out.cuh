@@ -69,9 +69,12 @@ struct EpiOut {
     __device__ __forceinline__ void tile(const Params& e, const Problem& p, int mw, int n0, int half,
                                          int z, uint32_t trow) {
       const int m = mw + lane;
+      // the warps' halves of the columns are whole 64-column boxes
+      constexpr int MID = (BN / 2 + 63) / 64 * 64;
+      const int c0 = half ? MID : 0, c1 = half ? BN : MID;
       if (!e.f32) {
 #pragma unroll 1
-        for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 64) {
+        for (int c = c0; c < c1; c += 64) {
           const int n = n0 + c;
           if (n >= p.N) break;
           float v[64];
@@ -87,7 +90,7 @@ struct EpiOut {
         }
       } else {
 #pragma unroll 1
-        for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+        for (int c = c0; c < c1; c += 32) {
           const int n = n0 + c;
           if (n >= p.N) break;
           float v[32];
@@ -112,6 +115,86 @@ struct EpiOut {
 inline bool out_map(EpiOut::Params* e, void* c, DType t, int rows, int N, int64_t ld) {
   e->f32 = t == DType::F32;
   return tensor_map(&e->c, c, e->f32 != 0, N, rows, ld, e->f32 ? 32 : 64, 32);
+}
+
+// out = scale * (sum of the splits' partial products, in their order) + bias +
+// resid, each optional; [rows, N] from slabs of [slab / N, N] fp32.
+template <typename T>
+__global__ void __launch_bounds__(256)
+slab_sum_kernel(const float* slabs, int splits, int64_t slab, const float* scale,
+                const __nv_bfloat16* bias, const __nv_bfloat16* resid, T* out, int64_t n, int N) {
+  pdl_wait();
+  pdl_trigger();
+  const float s = scale ? *scale : 1.f;
+  for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * 4; i < n;
+       i += (int64_t)gridDim.x * blockDim.x * 4) {
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int z = 0; z < splits; ++z) {
+      const float4 q = *reinterpret_cast<const float4*>(slabs + z * slab + i);
+      a[0] += q.x;
+      a[1] += q.y;
+      a[2] += q.z;
+      a[3] += q.w;
+    }
+    const int c = (int)(i % N);  // N is a multiple of 8
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] *= s;
+      if (bias) a[k] += __bfloat162float(bias[c + k]);
+      if (resid) a[k] += __bfloat162float(resid[i + k]);
+    }
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(out + i) = make_uint2(pack2(a[0], a[1]), pack2(a[2], a[3]));
+    else
+      *reinterpret_cast<float4*>(out + i) = make_float4(a[0], a[1], a[2], a[3]);
+  }
+}
+inline cudaError_t slab_sum(const float* slabs, int splits, int64_t slab, const float* scale,
+                            const void* bias, const void* resid, void* out, DType t, int rows, int N,
+                            cudaStream_t st) {
+  const int64_t n = (int64_t)rows * N;
+  const dim3 grid((unsigned)std::min<int64_t>((n / 4 + 255) / 256, 152 * 8));
+  const __nv_bfloat16 *b = static_cast<const __nv_bfloat16*>(bias),
+                      *r = static_cast<const __nv_bfloat16*>(resid);
+  if (t == DType::F32)
+    return launch_pdl(slab_sum_kernel<float>, grid, dim3(256), 0, st, slabs, splits, slab, scale, b, r,
+                      static_cast<float*>(out), n, N);
+  return launch_pdl(slab_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, slabs, splits, slab, scale,
+                    b, r, static_cast<__nv_bfloat16*>(out), n, N);
+}
+// Rows of a slab: whole tiles, so that the rows of one never reach the next.
+inline int slab_rows(int rows) { return (rows + 255) / 256 * 256; }
+
+// How a product [M, N] over K with few tiles is cut: columns per tile and splits
+// of the contraction, by the clocks of the longest path: a K-slice takes about
+// 512 of a CTA pair for 256 columns, 400 for 192 and 300 for 128 (operand bytes
+// bound the narrow tiles), a tile 3000 more, and a split's partial products are
+// written and read back at about 1600 bytes per clock, with a launch of 6000.
+struct Cut {
+  int bn, splits;
+};
+inline Cut cut_of(int M, int N, int K, int slots) {
+  const int nkb = (K + BKE - 1) / BKE, mp = (M + 2 * BM - 1) / (2 * BM);
+  const int bn[3] = {256, 192, 128}, clk[3] = {512, 400, 300};
+  Cut best{256, 1};
+  double least = 1e30;
+  for (int splits = 1; splits <= 8; ++splits) {
+    const int kbs = (nkb + splits - 1) / splits;
+    if (splits > 1 && kbs < 8) break;
+    for (int i = 0; i < 3; ++i) {
+      if (splits > 1 && i > 0) continue;  // a split has tiles enough
+      const int64_t tiles = (int64_t)mp * ((N + bn[i] - 1) / bn[i]) * splits;
+      double c = (double)((tiles + slots - 1) / slots) * ((double)kbs * clk[i] + 3000);
+      if (splits > 1) c += 6000 + splits * (double)M * N * 8 / 1600;
+      if (c < least * 0.97) {
+        least = c;
+        best = {bn[i], splits};
+      }
+    }
+  }
+  slices_per_split(K, &best.splits);
+  return best;
 }
 
 }  // namespace core

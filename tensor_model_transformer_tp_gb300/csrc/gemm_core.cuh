@@ -53,7 +53,7 @@ struct Cfg {
   static constexpr int EPI_OFF = STAGES * STAGE;
   static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8 * WBARS) + 8;
   static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + BAR_BYTES + 1024;
-  static constexpr int TMEM_COLS = 2 * BN;
+  static constexpr int TMEM_COLS = 2 * BN > 256 ? 512 : 2 * BN;  // a power of two
   static_assert(STAGE % 1024 == 0 && STG % 1024 == 0, "swizzled tiles keep 1024-byte alignment");
   static_assert(SMEM <= 227 * 1024 && STAGES >= 3 && STAGES <= 31, "shared memory");
 };

@@ -56,7 +56,7 @@ size_t saved_bytes(const GluShape& s) {
 
 // Workspace regions, each a multiple of 256 bytes.
 struct Layout {
-  size_t pre = 0, h = 0, dpre = 0, dx = 0, bias = 0, part = 0, total = 0;
+  size_t pre = 0, h = 0, dpre = 0, dx = 0 /* partial sums of dx, or of y */, bias = 0, part = 0, total = 0;
 };
 Layout layout(const GluShape& s, bool backward) {
   Layout l;
@@ -68,6 +68,7 @@ Layout layout(const GluShape& s, bool backward) {
   if (s.M == 0) return l;
   const int wide = std::max(2 * s.F, s.H);
   take(&l.h, MF * e);
+  if (!backward && s.t == DType::BF16) take(&l.dx, glu_down_tc_bytes(s));
   if (backward) {
     if (s.keep == OASES_GLU_KEEP_NONE) take(&l.pre, 2 * MF * e);
     take(&l.dpre, 2 * MF * e);
@@ -260,7 +261,8 @@ cudaError_t fwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
   void* h = ws + layout(s, false).h;
   OASES_TRY(project(s, w, x, h, s.keep == OASES_GLU_KEEP_PRE ? saved : nullptr,
                     s.keep == OASES_GLU_KEEP_MXFP8 ? saved : nullptr, st));
-  if (s.t == DType::BF16) return glu_down_tc(s, h, w.w2, w.b2, resid, y, st);
+  if (s.t == DType::BF16)
+    return glu_down_tc(s, h, w.w2, w.b2, resid, y, ws + layout(s, false).dx, st);
   const f32::Args g{s.M, s.H, s.F, (const float*)h, s.F, (const float*)w.w2, s.F};
   return f32::launch<f32::Out, true, true>(
       g, f32::Out{(float*)y, s.H, nullptr, (const float*)w.b2, (const float*)resid, 0}, st);

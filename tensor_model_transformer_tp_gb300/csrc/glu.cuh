@@ -65,9 +65,10 @@ size_t glu_grads_tc_bytes(const GluShape& s);
 cudaError_t glu_grads_tc(const GluShape& s, const void* x, const void* dy, const void* w1,
                          const void* dpre, const void* h, void* dx, void* dw1, void* dw2, char* ws,
                          cudaStream_t st);
-// y = h w2^T + b2 (+ resid)
+// y = h w2^T + b2 (+ resid); ws as glu_down_tc_bytes
+size_t glu_down_tc_bytes(const GluShape& s);
 cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const void* b2,
-                        const void* resid, void* y, cudaStream_t st);
+                        const void* resid, void* y, char* ws, cudaStream_t st);
 int glu_read_and_clear_error();
 // The forward's two products for at most GLU_FEW_ROWS rows (glu_few.cu).
 constexpr int GLU_FEW_ROWS = 128;

@@ -377,35 +377,24 @@ namespace {
 
 using core::EpiOut;
 
-// dx of few rows is a contraction over 2 ffn with few tiles: split over the SMs.
+// dx is a contraction over 2 ffn with few tiles when rows are few: split it over
+// the SMs (up to 128 rows: a launch of its own), or so that none of its tiles is
+// longer than the CTAs' even share of the three gradients' work.
 int dx_splits(const GluShape& s) {
+  const int64_t slices = (2 * (int64_t)s.F + core::BKE - 1) / core::BKE;
   int splits = 1;
-  if (s.M <= 128)
+  if (s.M <= 128) {
     splits = std::max(1, std::min(core::sm_count() / ((s.H + 127) / 128), 2 * s.F / 512));
+  } else {
+    auto tiles = [](int64_t m, int64_t n) { return (m + 255) / 256 * ((n + 255) / 256); };
+    const int64_t k = (s.M + core::BKE - 1) / core::BKE + core::TILE_COST;
+    const int64_t work = tiles(s.M, s.H) * slices + (tiles(s.H, s.F) + tiles(2 * (int64_t)s.F, s.H)) * k;
+    const int64_t share = std::max<int64_t>(8, work / std::max(1, core::sm_count() / 2));
+    // (a quarter longer than the share is cheaper than the partial sums)
+    if (slices * 4 > share * 5) splits = (int)std::min<int64_t>(16, (slices + share - 1) / share);
+  }
   core::slices_per_split(2 * s.F, &splits);
   return splits;
-}
-
-// out = the sum of the splits' partial products, in their order.
-template <typename T>
-__global__ void __launch_bounds__(256)
-glu_slabs_kernel(const float* slabs, int splits, int64_t slab, T* out, int64_t n) {
-  pdl_wait();
-  pdl_trigger();
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n / 4;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int z = 0; z < splits; ++z) {
-      const float4 q = *reinterpret_cast<const float4*>(slabs + z * slab + 4 * i);
-      a[0] += q.x;
-      a[1] += q.y;
-      a[2] += q.z;
-      a[3] += q.w;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) st_elem(out, 4 * i + k, a[k]);
-  }
 }
 
 #define OASES_TRY(expr)                       \
@@ -418,64 +407,77 @@ glu_slabs_kernel(const float* slabs, int splits, int64_t slab, T* out, int64_t n
 
 size_t glu_grads_tc_bytes(const GluShape& s) {
   const int splits = dx_splits(s);
-  return splits > 1 ? align256((size_t)128 * s.H * 4 * splits) : 0;
+  return splits > 1 ? align256((size_t)core::slab_rows(s.M) * s.H * 4 * splits) : 0;
 }
 
 cudaError_t glu_grads_tc(const GluShape& s, const void* x, const void* dy, const void* w1,
                          const void* dpre, const void* h, void* dx, void* dw1, void* dw2, char* ws,
                          cudaStream_t st) {
   const int64_t F2 = 2 * (int64_t)s.F;
-  const core::Operands o_dx{s.M, s.H, 2 * s.F, dpre, F2, w1, s.H};
+  core::Operands o_dx{s.M, s.H, 2 * s.F, dpre, F2, w1, s.H};
   const core::Operands o_w2{s.H, s.F, s.M, dy, s.H, h, s.F};
   const core::Operands o_w1{2 * s.F, s.H, s.M, dpre, F2, x, s.H};
   EpiOut::Params e_dx = {}, e_w1 = {}, e_w2 = {};
   e_w1.accumulate = e_w2.accumulate = s.accumulate;
-  if ((dw1 && !core::out_map(&e_w1, dw1, s.grad_t, 2 * s.F, s.H, s.H)) ||
-      (dw2 && !core::out_map(&e_w2, dw2, s.grad_t, s.H, s.F, s.F)) ||
-      (dx && !core::out_map(&e_dx, dx, s.dx_t, s.M, s.H, s.H)))
-    return cudaErrorInvalidValue;
+  const int splits = dx ? dx_splits(s) : 1;
+  const int64_t slab = (int64_t)core::slab_rows(s.M) * s.H;
+  bool ok = true;
+  if (dw1) ok = core::out_map(&e_w1, dw1, s.grad_t, 2 * s.F, s.H, s.H);
+  if (dw2) ok = ok && core::out_map(&e_w2, dw2, s.grad_t, s.H, s.F, s.F);
+  if (dx && splits > 1) {
+    o_dx.splits = splits;
+    e_dx.slab_rows = core::slab_rows(s.M);
+    ok = ok && core::out_map(&e_dx, ws, DType::F32, e_dx.slab_rows * splits, s.H, s.H);
+  } else if (dx) {
+    ok = ok && core::out_map(&e_dx, dx, s.dx_t, s.M, s.H, s.H);
+  }
+  if (!ok) return cudaErrorInvalidValue;
   const bool few = s.M <= 128;
+  bool taken = false;
   if (dw1 && dw2 && dx && !few) {
     const core::Product prod[3] = {{o_dx, true}, {o_w2, false}, {o_w1, false}};
     const EpiOut::Params ep[3] = {e_dx, e_w2, e_w1};
-    bool taken;
     OASES_TRY((core::launch_group<EpiOut, 3>(prod, ep, &taken, st)));
-    if (taken) return cudaSuccess;
   }
-  if (dw2) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_w2, e_w2, st)));
-  if (dw1) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_w1, e_w1, st)));
-  if (!dx) return cudaSuccess;
-  if (!few) return core::launch<EpiOut, 256, true, false, 2>(o_dx, e_dx, st);
-  const int splits = dx_splits(s);
-  if (splits == 1) return core::launch<EpiOut, 128, true, false, 1>(o_dx, e_dx, st);
-  core::Operands o = o_dx;
-  o.splits = splits;
-  EpiOut::Params e = {};
-  e.slab_rows = 128;
-  if (!core::out_map(&e, ws, DType::F32, 128 * splits, s.H, s.H)) return cudaErrorInvalidValue;
-  OASES_TRY((core::launch<EpiOut, 128, true, false, 1>(o, e, st)));
-  const int64_t n = (int64_t)s.M * s.H, slab = (int64_t)128 * s.H;
-  const dim3 grid((unsigned)std::min<int64_t>((n / 4 + 255) / 256, 152 * 8));
-  const float* slabs = reinterpret_cast<const float*>(ws);
-  if (s.dx_t == DType::F32)
-    return launch_pdl(glu_slabs_kernel<float>, grid, dim3(256), 0, st, slabs, splits, slab, (float*)dx, n);
-  return launch_pdl(glu_slabs_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, slabs, splits, slab,
-                    (__nv_bfloat16*)dx, n);
+  if (!taken) {
+    if (dw2) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_w2, e_w2, st)));
+    if (dw1) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_w1, e_w1, st)));
+    if (dx)
+      OASES_TRY(few ? (core::launch<EpiOut, 128, true, false, 1>(o_dx, e_dx, st))
+                    : (core::launch<EpiOut, 256, true, false, 2>(o_dx, e_dx, st)));
+  }
+  if (dx && splits > 1)
+    OASES_TRY(core::slab_sum(reinterpret_cast<const float*>(ws), splits, slab, nullptr, nullptr, nullptr,
+                             dx, s.dx_t, s.M, s.H, st));
+  return cudaSuccess;
+}
+
+size_t glu_down_tc_bytes(const GluShape& s) {
+  if (s.M <= GLU_FEW_ROWS) return 0;
+  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::sm_count() / 2);
+  return c.splits > 1 ? align256((size_t)core::slab_rows(s.M) * s.H * 4 * c.splits) : 0;
 }
 
 cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const void* b2,
-                        const void* resid, void* y, cudaStream_t st) {
+                        const void* resid, void* y, char* ws, cudaStream_t st) {
   if (s.M <= GLU_FEW_ROWS) return glu_down_few(s, h, w2, b2, resid, y, st);
-  using E = core::EpiOut;
-  E::Params e = {};
+  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::sm_count() / 2);
+  EpiOut::Params e = {};
+  core::Operands o{s.M, s.H, s.F, h, s.F, w2, s.F};
+  if (c.splits > 1) {
+    o.splits = c.splits;
+    e.slab_rows = core::slab_rows(s.M);
+    if (!core::out_map(&e, ws, DType::F32, e.slab_rows * c.splits, s.H, s.H)) return cudaErrorInvalidValue;
+    OASES_TRY((core::launch<EpiOut, 256, true, true, 2>(o, e, st)));
+    return core::slab_sum(reinterpret_cast<const float*>(ws), c.splits, (int64_t)e.slab_rows * s.H,
+                          nullptr, b2, resid, y, DType::BF16, s.M, s.H, st);
+  }
   if (!core::out_map(&e, y, DType::BF16, s.M, s.H, s.H)) return cudaErrorInvalidValue;
   e.bias = static_cast<const __nv_bfloat16*>(b2);
   e.resid = static_cast<const __nv_bfloat16*>(resid);
-  core::Operands o{s.M, s.H, s.F, h, s.F, w2, s.F};
-  const int tiles256 = (s.M + 127) / 128 * ((s.H + 255) / 256);
-  if (2 * tiles256 < core::sm_count() || s.H <= 128)
-    return core::launch<E, 128, true, true, 2>(o, e, st);
-  return core::launch<E, 256, true, true, 2>(o, e, st);
+  if (c.bn == 128) return core::launch<EpiOut, 128, true, true, 2>(o, e, st);
+  if (c.bn == 192) return core::launch<EpiOut, 192, true, true, 2>(o, e, st);
+  return core::launch<EpiOut, 256, true, true, 2>(o, e, st);
 }
 
 int glu_read_and_clear_error() {
