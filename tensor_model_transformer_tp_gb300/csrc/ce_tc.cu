@@ -216,7 +216,7 @@ BwdPlan bwd_plan(const CeShape& s) {
   const int64_t fit = PIECE_BYTES / (2ll * s.M) / 256 * 256;
   const int pieces = (int)((s.V + std::max<int64_t>(fit, MIN_PIECE) - 1) / std::max<int64_t>(fit, MIN_PIECE));
   b.piece = pieces == 1 ? s.V : ((s.V + pieces - 1) / pieces + 255) / 256 * 256;
-  b.ld = (b.piece + 7) / 8 * 8;
+  b.ld = ((int64_t)b.piece + 63) / 64 * 64;  // rows on 128-byte lines
   // dx of few rows has few tiles, each a contraction over the whole vocabulary:
   // split it over the SMs
   const int tiles = s.M <= 128 ? (s.H + 127) / 128 : (s.M + 255) / 256 * ((s.H + 255) / 256);

@@ -168,7 +168,7 @@ inline int slab_rows(int rows) { return (rows + 255) / 256 * 256; }
 
 // How a product [M, N] over K with few tiles is cut: columns per tile and splits
 // of the contraction, by the clocks of the longest path: a K-slice takes about
-// 512 of a CTA pair for 256 columns, 400 for 192 and 300 for 128 (operand bytes
+// 512 of a CTA pair for 256 columns, 430 for 192 and 480 for 128 (operand bytes
 // bound the narrow tiles), a tile 3000 more, and a split's partial products are
 // written and read back at about 1600 bytes per clock, with a launch of 6000.
 struct Cut {
@@ -176,7 +176,7 @@ struct Cut {
 };
 inline Cut cut_of(int M, int N, int K, int slots) {
   const int nkb = (K + BKE - 1) / BKE, mp = (M + 2 * BM - 1) / (2 * BM);
-  const int bn[3] = {256, 192, 128}, clk[3] = {512, 400, 300};
+  const int bn[3] = {256, 192, 128}, clk[3] = {512, 430, 480};
   Cut best{256, 1};
   double least = 1e30;
   for (int splits = 1; splits <= 8; ++splits) {

@@ -44,6 +44,9 @@ oases_status glu_shape(const oases_glu_desc* d, GluShape* s) {
   s->keep = d->keep;
   s->accumulate = d->accumulate != 0;
   s->ldq = (s->F + 15) / 16 * 16;
+  const bool bf = s->t == DType::BF16;
+  s->ldh = bf ? ((int64_t)s->F + 63) / 64 * 64 : s->F;
+  s->ldp = bf ? (2 * (int64_t)s->F + 63) / 64 * 64 : 2 * (int64_t)s->F;
   return OASES_OK;
 }
 
@@ -60,18 +63,18 @@ struct Layout {
 };
 Layout layout(const GluShape& s, bool backward) {
   Layout l;
-  const size_t MF = (size_t)s.M * s.F, e = dtype_size(s.t);
+  const size_t e = dtype_size(s.t), h = (size_t)s.M * s.ldh * e, pre = (size_t)s.M * s.ldp * e;
   auto take = [&](size_t* at, size_t bytes) {
     *at = l.total;
     l.total += align256(bytes);
   };
   if (s.M == 0) return l;
   const int wide = std::max(2 * s.F, s.H);
-  take(&l.h, MF * e);
+  take(&l.h, h);
   if (!backward && s.t == DType::BF16) take(&l.dx, glu_down_tc_bytes(s));
   if (backward) {
-    if (s.keep == OASES_GLU_KEEP_NONE) take(&l.pre, 2 * MF * e);
-    take(&l.dpre, 2 * MF * e);
+    if (s.keep == OASES_GLU_KEEP_NONE) take(&l.pre, pre);
+    take(&l.dpre, pre);
     if (s.t == DType::BF16) take(&l.dx, glu_grads_tc_bytes(s));
     if (s.M > DIRECT_SUM_ROWS) {
       take(&l.part, (size_t)colsum_blocks(s.M) * wide * 4);
@@ -150,11 +153,13 @@ struct GradF32 {
   }
 };
 
-// Column sums of in[0] [M, N0] and in[1] [M, N1] in one launch, out (+)= sums.
+// Column sums of in[0] [M, N0] and in[1] [M, N1] (leading dimensions ld) in one
+// launch, out (+)= sums.
 struct Sums {
   const void* in[2];
   void* out[2];
   int N[2];
+  int64_t ld[2];
 };
 // Two neighbouring columns per thread; 32 columns and 32 row groups per block.
 __device__ __forceinline__ float2 ld_pair(const float* p) { return *reinterpret_cast<const float2*>(p); }
@@ -171,18 +176,19 @@ __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, i
   const int n = ((int)blockIdx.x - (which ? first : 0)) * 32 + 2 * x, N = s.N[which];
   const T* in = static_cast<const T*>(s.in[which]) + n;
   const bool second = n + 1 < N;
+  const int64_t ld = s.ld[which];
   float2 v = make_float2(0.f, 0.f);
-  if (N % 2 == 0 && n < N) {  // one 4- or 8-byte load per row
+  if (ld % 2 == 0 && second) {  // one 4- or 8-byte load per row
 #pragma unroll 16
     for (int m = y; m < M; m += 32) {
-      const float2 q = ld_pair(in + (int64_t)m * N);
+      const float2 q = ld_pair(in + m * ld);
       v.x += q.x;
       v.y += q.y;
     }
   } else if (n < N) {
     for (int m = y; m < M; m += 32) {
-      v.x += ld_elem(in, (int64_t)m * N);
-      if (second) v.y += ld_elem(in, (int64_t)m * N + 1);
+      v.x += ld_elem(in, m * ld);
+      if (second) v.y += ld_elem(in, m * ld + 1);
     }
   }
   red[y][x] = v;
@@ -213,13 +219,13 @@ __global__ void __launch_bounds__(256) cast_kernel(const float* in, T* out, int 
     if (e_ != cudaSuccess) return e_;         \
   } while (0)
 
-// Column sums of in [M, N] (type t) to a bias gradient.
-cudaError_t bias_grad(const void* in, int M, int N, DType t, void* out, DType out_t, bool accumulate,
-                      float* part, float* tmp, cudaStream_t st) {
-  if (accumulate) return colsum_accum(in, N, M, N, t, part, static_cast<float*>(out), st);
+// Column sums of in [M, N] (type t, leading dimension ld) to a bias gradient.
+cudaError_t bias_grad(const void* in, int64_t ld, int M, int N, DType t, void* out, DType out_t,
+                      bool accumulate, float* part, float* tmp, cudaStream_t st) {
+  if (accumulate) return colsum_accum(in, ld, M, N, t, part, static_cast<float*>(out), st);
   float* sum = out_t == DType::F32 ? static_cast<float*>(out) : tmp;
   cudaError_t e = cudaMemsetAsync(sum, 0, (size_t)N * 4, st);
-  if (e == cudaSuccess) e = colsum_accum(in, N, M, N, t, part, sum, st);
+  if (e == cudaSuccess) e = colsum_accum(in, ld, M, N, t, part, sum, st);
   if (e == cudaSuccess && out_t == DType::BF16)
     e = launch_pdl(cast_kernel<__nv_bfloat16>, dim3((N + 255) / 256), dim3(256), 0, st,
                    (const float*)tmp, (__nv_bfloat16*)out, N);
@@ -232,12 +238,13 @@ cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, cons
   if (!gr.b1 && !gr.b2) return cudaSuccess;
   if (s.M > DIRECT_SUM_ROWS) {
     if (gr.b1)
-      OASES_TRY(bias_grad(dpre, s.M, 2 * s.F, s.t, gr.b1, s.grad_t, s.accumulate, part, tmp, st));
+      OASES_TRY(bias_grad(dpre, s.ldp, s.M, 2 * s.F, s.t, gr.b1, s.grad_t, s.accumulate, part, tmp, st));
     if (gr.b2)
-      OASES_TRY(bias_grad(dy, s.M, s.H, s.t, gr.b2, s.grad_t, s.accumulate, part, tmp, st));
+      OASES_TRY(bias_grad(dy, s.H, s.M, s.H, s.t, gr.b2, s.grad_t, s.accumulate, part, tmp, st));
     return cudaSuccess;
   }
-  const Sums q{{dpre, dy}, {gr.b1, gr.b2}, {gr.b1 ? 2 * s.F : 0, gr.b2 ? s.H : 0}};
+  const Sums q{{dpre, dy}, {gr.b1, gr.b2}, {gr.b1 ? 2 * s.F : 0, gr.b2 ? s.H : 0},
+               {s.ldp, s.H}};
   const dim3 grid((unsigned)((q.N[0] + 31) / 32 + (q.N[1] + 31) / 32)), block(512);
   const int acc = s.accumulate ? 1 : 0;
   if (s.t == DType::F32)
@@ -249,8 +256,8 @@ cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, cons
 
 // [a | b] and h = act(a) b; h, pre and kept8 are each left out when null.
 cudaError_t project(const GluShape& s, const oases_glu_weights& w, const void* x, void* h, void* pre,
-                    void* kept8, cudaStream_t st) {
-  if (s.t == DType::BF16) return glu_project_tc(s, x, w.w1, w.b1, h, pre, kept8, st);
+                    int64_t ld_pre, void* kept8, cudaStream_t st) {
+  if (s.t == DType::BF16) return glu_project_tc(s, x, w.w1, w.b1, h, pre, ld_pre, kept8, st);
   const f32::Args g{s.M, s.F, s.H, (const float*)x, s.H, (const float*)w.w1, s.H, s.F};
   return f32::launch<UpF32, true, true>(
       g, UpF32{(const float*)w.b1, (float*)h, (float*)pre, s.act}, st);
@@ -259,7 +266,7 @@ cudaError_t project(const GluShape& s, const oases_glu_weights& w, const void* x
 cudaError_t fwd(const GluShape& s, const oases_glu_weights& w, const void* x, const void* resid,
                 void* y, void* saved, char* ws, cudaStream_t st) {
   void* h = ws + layout(s, false).h;
-  OASES_TRY(project(s, w, x, h, s.keep == OASES_GLU_KEEP_PRE ? saved : nullptr,
+  OASES_TRY(project(s, w, x, h, s.keep == OASES_GLU_KEEP_PRE ? saved : nullptr, 2 * (int64_t)s.F,
                     s.keep == OASES_GLU_KEEP_MXFP8 ? saved : nullptr, st));
   if (s.t == DType::BF16)
     return glu_down_tc(s, h, w.w2, w.b2, resid, y, ws + layout(s, false).dx, st);
@@ -273,16 +280,18 @@ cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
   const Layout l = layout(s, true);
   void *h = ws + l.h, *dpre = ws + l.dpre;
   const void *pre = saved, *kept8 = nullptr;
+  int64_t ld_pre = 2 * (int64_t)s.F;
   if (s.keep == OASES_GLU_KEEP_NONE) {
     void* p = ws + l.pre;
-    OASES_TRY(project(s, w, x, nullptr, p, nullptr, st));
+    ld_pre = s.ldp;
+    OASES_TRY(project(s, w, x, nullptr, p, ld_pre, nullptr, st));
     pre = p;
   } else if (s.keep == OASES_GLU_KEEP_MXFP8) {
     pre = nullptr;
     kept8 = saved;
   }
   if (s.t == DType::BF16) {
-    OASES_TRY(glu_grad_tc(s, dy, w.w2, pre, kept8, dpre, h, st));
+    OASES_TRY(glu_grad_tc(s, dy, w.w2, pre, ld_pre, kept8, dpre, h, st));
     OASES_TRY(glu_grads_tc(s, x, dy, w.w1, dpre, h, dx, gr.w1, gr.w2, ws + l.dx, st));
   } else {
     const f32::Args g{s.M, s.F, s.H, (const float*)dy, s.H, (const float*)w.w2, s.F};

@@ -14,6 +14,11 @@ struct GluShape {
   int act, keep;
   bool accumulate;
   int64_t ldq;  // leading dimension of the 8-bit codes
+  // Leading dimensions in the workspace of h, and of [a | b] and [da | db]: bf16
+  // rows start on 128-byte lines.  (A row that does not makes every 128-byte
+  // operand row of a TMA box two lines: 1531 x 2048 x 5464 took 37 us against 29
+  // with the rows of both operands on lines.)
+  int64_t ldh, ldp;
 };
 
 // Kept activations (oases_glu_keep): where the scales of the 8-bit form start.
@@ -51,14 +56,14 @@ __device__ __forceinline__ float act_fast(int act, float a) {
 // bf16, tensor cores.
 // [a | b] = x w1^T + b1 of every row, and from the fp32 accumulators
 //   h = act(a) b      (h given)
-//   pre = [a | b]     (pre given), bf16 [M, 2F]
+//   pre = [a | b]     (pre given), bf16 [M, 2F], leading dimension ld_pre
 //   the 8-bit form    (kept8 given, laid out as oases_glu_keep MXFP8)
 cudaError_t glu_project_tc(const GluShape& s, const void* x, const void* w1, const void* b1,
-                           void* h, void* pre, void* kept8, cudaStream_t st);
+                           void* h, void* pre, int64_t ld_pre, void* kept8, cudaStream_t st);
 // dh = dy w2, and from it dpre = [da | db] [M, 2F] and h [M, F] at the a, b of
-// pre (bf16 [M, 2F]) or kept8.
+// pre (bf16 [M, 2F], leading dimension ld_pre) or kept8.
 cudaError_t glu_grad_tc(const GluShape& s, const void* dy, const void* w2, const void* pre,
-                        const void* kept8, void* dpre, void* h, cudaStream_t st);
+                        int64_t ld_pre, const void* kept8, void* dpre, void* h, cudaStream_t st);
 // dw2 (+)= dy^T h, dw1 (+)= dpre^T x, dx = dpre w1, each where it is given; ws
 // as glu_grads_tc_bytes.
 size_t glu_grads_tc_bytes(const GluShape& s);
@@ -73,7 +78,7 @@ int glu_read_and_clear_error();
 // The forward's two products for at most GLU_FEW_ROWS rows (glu_few.cu).
 constexpr int GLU_FEW_ROWS = 128;
 cudaError_t glu_project_few(const GluShape& s, const void* x, const void* w1, const void* b1,
-                            void* h, void* pre, void* kept8, cudaStream_t st);
+                            void* h, void* pre, int64_t ld_pre, void* kept8, cudaStream_t st);
 cudaError_t glu_down_few(const GluShape& s, const void* h, const void* w2, const void* b2,
                          const void* resid, void* y, cudaStream_t st);
 int glu_few_read_and_clear_error();

@@ -37,6 +37,7 @@ struct FewArgs {
   const __nv_bfloat16 *bias, *resid;
   __nv_bfloat16 *out;   // h [M, N] or y [M, N]
   __nv_bfloat16 *pre;   // [M, 2N]
+  int64_t ldx, ldo, ldp;  // leading dimensions of x, out and pre
   uint8_t *codes, *scales;
   int64_t ldq, code_stride, scale_stride;
   int kgroups;
@@ -190,8 +191,8 @@ glu_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         b += __bfloat162float(g.bias[g.N + c]);
       }
       if (g.keep == OASES_GLU_KEEP_PRE && in) {
-        g.pre[(int64_t)m * 2 * g.N + c] = __float2bfloat16_rn(a);
-        g.pre[(int64_t)m * 2 * g.N + g.N + c] = __float2bfloat16_rn(b);
+        g.pre[m * g.ldp + c] = __float2bfloat16_rn(a);
+        g.pre[m * g.ldp + g.N + c] = __float2bfloat16_rn(b);
       } else if (g.keep == OASES_GLU_KEEP_MXFP8) {
         // a warp holds 32 consecutive columns of a row: one scale block of each
         float ta = in ? fabsf(a) : 0.f, tb = in ? fabsf(b) : 0.f;
@@ -212,11 +213,11 @@ glu_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           s[g.scale_stride] = (uint8_t)(xb + 127);
         }
       }
-      if (in) g.out[(int64_t)m * g.N + c] = __float2bfloat16_rn(act_fast(g.act, a) * b);
+      if (in) g.out[m * g.ldo + c] = __float2bfloat16_rn(act_fast(g.act, a) * b);
     } else if (in) {
       float v = total(m * 128 + r);
       if (g.bias) v += __bfloat162float(g.bias[c]);
-      const int64_t at = (int64_t)m * g.N + c;
+      const int64_t at = m * g.ldo + c;  // resid's too
       if (g.resid) v += __bfloat162float(g.resid[at]);
       g.out[at] = __float2bfloat16_rn(v);
     }
@@ -249,7 +250,7 @@ cudaError_t launch_few(FewArgs g, const void* w, const void* x, int tiles, cudaS
   using C = Few<NT>;
   CUtensorMap mw, mx;
   if (!core::tensor_map(&mw, w, false, g.K, UP ? 2 * (int64_t)g.N : g.N, g.K, BKE, UP ? 64 : 128) ||
-      !core::tensor_map(&mx, x, false, g.K, g.M, g.K, BKE, NT))
+      !core::tensor_map(&mx, x, false, g.K, g.M, g.ldx, BKE, NT))
     return cudaErrorInvalidValue;
   const int nkb = (g.K + BKE - 1) / BKE, S = few_split(tiles, nkb);
   g.kbs = (nkb + S - 1) / S;
@@ -288,7 +289,7 @@ cudaError_t dispatch(const FewArgs& g, const void* w, const void* x, int tiles, 
 }  // namespace
 
 cudaError_t glu_project_few(const GluShape& s, const void* x, const void* w1, const void* b1,
-                            void* h, void* pre, void* kept8, cudaStream_t st) {
+                            void* h, void* pre, int64_t ld_pre, void* kept8, cudaStream_t st) {
   FewArgs g = {};
   g.M = s.M;
   g.N = s.F;
@@ -296,6 +297,9 @@ cudaError_t glu_project_few(const GluShape& s, const void* x, const void* w1, co
   g.act = s.act;
   g.bias = static_cast<const __nv_bfloat16*>(b1);
   g.out = static_cast<__nv_bfloat16*>(h);
+  g.ldx = s.H;
+  g.ldo = s.ldh;
+  g.ldp = ld_pre;
   int tiles = (s.F + 63) / 64;
   if (kept8) {
     g.keep = OASES_GLU_KEEP_MXFP8;
@@ -322,6 +326,8 @@ cudaError_t glu_down_few(const GluShape& s, const void* h, const void* w2, const
   g.bias = static_cast<const __nv_bfloat16*>(b2);
   g.resid = static_cast<const __nv_bfloat16*>(resid);
   g.out = static_cast<__nv_bfloat16*>(y);
+  g.ldx = s.ldh;
+  g.ldo = s.H;
   return dispatch<false>(g, w2, h, (s.H + 127) / 128, st);
 }
 

@@ -305,22 +305,22 @@ struct EpiGrad {
 };
 
 // Maps of pre's (or dpre's) two halves, boxes of 32 rows x `box` columns.
-bool halves(CUtensorMap* a, CUtensorMap* b, const void* pre, const GluShape& s, int box) {
+bool halves(CUtensorMap* a, CUtensorMap* b, const void* pre, int64_t ld, const GluShape& s, int box) {
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(pre);
-  return core::tensor_map(a, q, false, s.F, s.M, 2 * (int64_t)s.F, box, 32) &&
-         core::tensor_map(b, q + s.F, false, s.F, s.M, 2 * (int64_t)s.F, box, 32);
+  return core::tensor_map(a, q, false, s.F, s.M, ld, box, 32) &&
+         core::tensor_map(b, q + s.F, false, s.F, s.M, ld, box, 32);
 }
 
 template <int KEEP>
 cudaError_t project(const GluShape& s, const void* x, const void* w1, const void* b1, void* h,
-                    void* pre, void* kept8, cudaStream_t st) {
+                    void* pre, int64_t ld_pre, void* kept8, cudaStream_t st) {
   using E = EpiDual<KEEP>;
   typename E::Params e = {};
   e.bias = static_cast<const __nv_bfloat16*>(b1);
   e.act = s.act;
   e.want_h = h != nullptr;
-  if (h && !core::tensor_map(&e.h, h, false, s.F, s.M, s.F, 64, 32)) return cudaErrorInvalidValue;
-  if (pre && !halves(&e.a, &e.b, pre, s, 64)) return cudaErrorInvalidValue;
+  if (h && !core::tensor_map(&e.h, h, false, s.F, s.M, s.ldh, 64, 32)) return cudaErrorInvalidValue;
+  if (pre && !halves(&e.a, &e.b, pre, ld_pre, s, 64)) return cudaErrorInvalidValue;
   if (kept8) {
     e.codes = static_cast<uint8_t*>(kept8);
     e.scales = e.codes + saved_scale_offset(s);
@@ -335,15 +335,16 @@ cudaError_t project(const GluShape& s, const void* x, const void* w1, const void
 }
 
 template <bool EIGHT>
-cudaError_t grad(const GluShape& s, const void* dy, const void* w2, const void* pre,
+cudaError_t grad(const GluShape& s, const void* dy, const void* w2, const void* pre, int64_t ld_pre,
                  const void* kept8, void* dpre, void* h, cudaStream_t st) {
   using E = EpiGrad<EIGHT>;
   typename E::Params e = {};
   e.act = s.act;
-  if (!halves(&e.da, &e.db, dpre, s, 32) || !core::tensor_map(&e.h, h, false, s.F, s.M, s.F, 32, 32))
+  if (!halves(&e.da, &e.db, dpre, s.ldp, s, 32) ||
+      !core::tensor_map(&e.h, h, false, s.F, s.M, s.ldh, 32, 32))
     return cudaErrorInvalidValue;
   if (!EIGHT) {
-    if (!halves(&e.a, &e.b, pre, s, 32)) return cudaErrorInvalidValue;
+    if (!halves(&e.a, &e.b, pre, ld_pre, s, 32)) return cudaErrorInvalidValue;
   } else {
     e.codes = static_cast<const uint8_t*>(kept8);
     e.scales = e.codes + saved_scale_offset(s);
@@ -360,17 +361,17 @@ cudaError_t grad(const GluShape& s, const void* dy, const void* w2, const void* 
 }  // namespace
 
 cudaError_t glu_project_tc(const GluShape& s, const void* x, const void* w1, const void* b1,
-                           void* h, void* pre, void* kept8, cudaStream_t st) {
-  if (s.M <= GLU_FEW_ROWS && h) return glu_project_few(s, x, w1, b1, h, pre, kept8, st);
-  if (kept8) return project<OASES_GLU_KEEP_MXFP8>(s, x, w1, b1, h, nullptr, kept8, st);
-  if (pre) return project<OASES_GLU_KEEP_PRE>(s, x, w1, b1, h, pre, nullptr, st);
-  return project<OASES_GLU_KEEP_NONE>(s, x, w1, b1, h, nullptr, nullptr, st);
+                           void* h, void* pre, int64_t ld_pre, void* kept8, cudaStream_t st) {
+  if (s.M <= GLU_FEW_ROWS && h) return glu_project_few(s, x, w1, b1, h, pre, ld_pre, kept8, st);
+  if (kept8) return project<OASES_GLU_KEEP_MXFP8>(s, x, w1, b1, h, nullptr, 0, kept8, st);
+  if (pre) return project<OASES_GLU_KEEP_PRE>(s, x, w1, b1, h, pre, ld_pre, nullptr, st);
+  return project<OASES_GLU_KEEP_NONE>(s, x, w1, b1, h, nullptr, 0, nullptr, st);
 }
 
 cudaError_t glu_grad_tc(const GluShape& s, const void* dy, const void* w2, const void* pre,
-                        const void* kept8, void* dpre, void* h, cudaStream_t st) {
-  return kept8 ? grad<true>(s, dy, w2, nullptr, kept8, dpre, h, st)
-               : grad<false>(s, dy, w2, pre, nullptr, dpre, h, st);
+                        int64_t ld_pre, const void* kept8, void* dpre, void* h, cudaStream_t st) {
+  return kept8 ? grad<true>(s, dy, w2, nullptr, 0, kept8, dpre, h, st)
+               : grad<false>(s, dy, w2, pre, ld_pre, nullptr, dpre, h, st);
 }
 
 namespace {
@@ -413,10 +414,9 @@ size_t glu_grads_tc_bytes(const GluShape& s) {
 cudaError_t glu_grads_tc(const GluShape& s, const void* x, const void* dy, const void* w1,
                          const void* dpre, const void* h, void* dx, void* dw1, void* dw2, char* ws,
                          cudaStream_t st) {
-  const int64_t F2 = 2 * (int64_t)s.F;
-  core::Operands o_dx{s.M, s.H, 2 * s.F, dpre, F2, w1, s.H};
-  const core::Operands o_w2{s.H, s.F, s.M, dy, s.H, h, s.F};
-  const core::Operands o_w1{2 * s.F, s.H, s.M, dpre, F2, x, s.H};
+  core::Operands o_dx{s.M, s.H, 2 * s.F, dpre, s.ldp, w1, s.H};
+  const core::Operands o_w2{s.H, s.F, s.M, dy, s.H, h, s.ldh};
+  const core::Operands o_w1{2 * s.F, s.H, s.M, dpre, s.ldp, x, s.H};
   EpiOut::Params e_dx = {}, e_w1 = {}, e_w2 = {};
   e_w1.accumulate = e_w2.accumulate = s.accumulate;
   const int splits = dx ? dx_splits(s) : 1;
@@ -463,7 +463,7 @@ cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const 
   if (s.M <= GLU_FEW_ROWS) return glu_down_few(s, h, w2, b2, resid, y, st);
   const core::Cut c = core::cut_of(s.M, s.H, s.F, core::sm_count() / 2);
   EpiOut::Params e = {};
-  core::Operands o{s.M, s.H, s.F, h, s.F, w2, s.F};
+  core::Operands o{s.M, s.H, s.F, h, s.ldh, w2, s.F};
   if (c.splits > 1) {
     o.splits = c.splits;
     e.slab_rows = core::slab_rows(s.M);
