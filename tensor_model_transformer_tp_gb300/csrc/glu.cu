@@ -18,8 +18,8 @@ oases_status api_end(cudaError_t e);
 
 namespace {
 
-// Bias gradients of up to this many rows are summed by one launch, two columns per
-// thread and 32 row groups; more rows go through partial rows.
+// Bias gradients of up to this many rows are summed by one launch with 64 row
+// groups per column; more rows go through partial rows.
 constexpr int DIRECT_SUM_ROWS = 2048;
 
 oases_status glu_shape(const oases_glu_desc* d, GluShape* s) {
@@ -161,46 +161,70 @@ struct Sums {
   int N[2];
   int64_t ld[2];
 };
-// Two neighbouring columns per thread; 32 columns and 32 row groups per block.
-__device__ __forceinline__ float2 ld_pair(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ float2 ld_pair(const __nv_bfloat16* p) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
-}
-template <typename T, typename O>
-__global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, int accumulate) {
-  __shared__ float2 red[32][17];
-  pdl_wait();
-  pdl_trigger();
-  const int x = threadIdx.x % 16, y = threadIdx.x / 16, first = (s.N[0] + 31) / 32;
-  const int which = (int)blockIdx.x < first ? 0 : 1;
-  const int n = ((int)blockIdx.x - (which ? first : 0)) * 32 + 2 * x, N = s.N[which];
-  const T* in = static_cast<const T*>(s.in[which]) + n;
-  const bool second = n + 1 < N;
-  const int64_t ld = s.ld[which];
-  float2 v = make_float2(0.f, 0.f);
-  if (ld % 2 == 0 && second) {  // one 4- or 8-byte load per row
-#pragma unroll 16
-    for (int m = y; m < M; m += 32) {
-      const float2 q = ld_pair(in + m * ld);
-      v.x += q.x;
-      v.y += q.y;
-    }
-  } else if (n < N) {
-    for (int m = y; m < M; m += 32) {
-      v.x += ld_elem(in, m * ld);
-      if (second) v.y += ld_elem(in, m * ld + 1);
+// V neighbouring columns per thread (16 bytes of bf16 rows, which start on such;
+// one column of fp32 rows), 8 V columns and 64 row groups per block.
+template <typename T, int V>
+struct RowLoad;
+template <>
+struct RowLoad<__nv_bfloat16, 8> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void add(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
+      v[2 * k] += f.x;
+      v[2 * k + 1] += f.y;
     }
   }
-  red[y][x] = v;
-  __syncthreads();
-  if (y == 0 && n < N) {
-    for (int i = 1; i < 32; ++i) {
-      v.x += red[i][x].x;
-      v.y += red[i][x].y;
+};
+template <>
+struct RowLoad<float, 1> {
+  float u;
+  __device__ __forceinline__ void load(const float* p) { u = __ldg(p); }
+  __device__ __forceinline__ void add(float (&v)[1]) const { v[0] += u; }
+};
+template <typename T, typename O, int V>
+__global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, int accumulate) {
+  __shared__ float red[16][8 * V + 1];
+  pdl_wait();
+  pdl_trigger();
+  const int x = threadIdx.x % 8, y = threadIdx.x / 8, first = (s.N[0] + 8 * V - 1) / (8 * V);
+  const int which = (int)blockIdx.x < first ? 0 : 1;
+  const int n0 = ((int)blockIdx.x - (which ? first : 0)) * 8 * V, n = n0 + V * x, N = s.N[which];
+  const int64_t ld = s.ld[which];
+  const T* in = static_cast<const T*>(s.in[which]) + n;
+  float v[V] = {};
+  if (n < N) {  // bf16: N is a multiple of V
+    RowLoad<T, V> r[8];
+    int m = y;
+    for (; m + 7 * 64 < M; m += 8 * 64) {  // eight rows in flight
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i].load(in + (m + 64 * i) * ld);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i].add(v);
     }
-    O* out = static_cast<O*>(s.out[which]);
-    st_elem(out, n, accumulate ? ld_elem(out, n) + v.x : v.x);
-    if (second) st_elem(out, n + 1, accumulate ? ld_elem(out, n + 1) + v.y : v.y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (m + 64 * i < M) r[i].load(in + (m + 64 * i) * ld);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (m + 64 * i < M) r[i].add(v);
+  }
+  // the four row groups of a warp, then the sixteen warps, in a fixed order
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    v[k] += __shfl_down_sync(0xffffffffu, v[k], 16);
+    v[k] += __shfl_down_sync(0xffffffffu, v[k], 8);
+    if (threadIdx.x % 32 < 8) red[threadIdx.x / 32][V * x + k] = v[k];
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < 8 * V && n0 + (int)threadIdx.x < N) {
+    float t = 0.f;
+    for (int i = 0; i < 16; ++i) t += red[i][threadIdx.x];
+    O* out = static_cast<O*>(s.out[which]) + n0 + threadIdx.x;
+    st_elem(out, 0, accumulate ? ld_elem(out, 0) + t : t);
   }
 }
 
@@ -245,13 +269,13 @@ cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, cons
   }
   const Sums q{{dpre, dy}, {gr.b1, gr.b2}, {gr.b1 ? 2 * s.F : 0, gr.b2 ? s.H : 0},
                {s.ldp, s.H}};
-  const dim3 grid((unsigned)((q.N[0] + 31) / 32 + (q.N[1] + 31) / 32)), block(512);
-  const int acc = s.accumulate ? 1 : 0;
+  const int per = s.t == DType::F32 ? 8 : 64, acc = s.accumulate ? 1 : 0;
+  const dim3 grid((unsigned)((q.N[0] + per - 1) / per + (q.N[1] + per - 1) / per)), block(512);
   if (s.t == DType::F32)
-    return launch_pdl(column_sums_kernel<float, float>, grid, block, 0, st, q, s.M, acc);
+    return launch_pdl(column_sums_kernel<float, float, 1>, grid, block, 0, st, q, s.M, acc);
   if (s.grad_t == DType::F32)
-    return launch_pdl(column_sums_kernel<__nv_bfloat16, float>, grid, block, 0, st, q, s.M, acc);
-  return launch_pdl(column_sums_kernel<__nv_bfloat16, __nv_bfloat16>, grid, block, 0, st, q, s.M, acc);
+    return launch_pdl(column_sums_kernel<__nv_bfloat16, float, 8>, grid, block, 0, st, q, s.M, acc);
+  return launch_pdl(column_sums_kernel<__nv_bfloat16, __nv_bfloat16, 8>, grid, block, 0, st, q, s.M, acc);
 }
 
 // [a | b] and h = act(a) b; h, pre and kept8 are each left out when null.
