@@ -18,8 +18,10 @@
  *
  * Layout: row-major, contiguous: x, dx [rows, hidden]; w, dw [vocab, hidden];
  * target int64 [rows]; loss, lse, dloss fp32.  Conventions of memory, threads,
- * errors and determinism as in oases.h: the caller owns every buffer, device
- * pointers are 16-byte aligned, argument errors are returned before anything
+ * errors and determinism as in oases.h: the caller owns every buffer, the
+ * device pointers of x, w, dx, dw and the workspace are 16-byte aligned (those
+ * of target and of loss, lse, dloss need only their elements' alignment, so
+ * shifted targets can be a slice), argument errors are returned before anything
  * is enqueued, calls are asynchronous on `stream` (one stream), identical
  * inputs give identical bits.
  *
@@ -58,7 +60,8 @@ size_t oases_ce_workspace_bytes(const oases_ce_desc *desc, int backward);
 
 /* loss, lse: fp32 [rows], written.
  * Errors: INVALID_ARG for a bad descriptor, a NULL or misaligned pointer;
- * UNSUPPORTED for a bf16 hidden that is no multiple of 8; WORKSPACE for a
+ * UNSUPPORTED for a bf16 hidden that is no multiple of 8 and for rows, hidden or
+ * vocab beyond 2^29 (fp32: 2097120); WORKSPACE for a
  * workspace that is NULL or too small. */
 oases_status oases_ce_fwd(const oases_ce_desc *desc, const void *x, const void *w,
                           const int64_t *target, float *loss, float *lse, void *workspace,

@@ -90,8 +90,8 @@ size_t oases_glu_workspace_bytes(const oases_glu_desc *desc, int backward);
  * bytes, written (NULL for KEEP_NONE).
  * Errors: INVALID_ARG for a bad descriptor, a NULL or misaligned pointer;
  * UNSUPPORTED for a bf16 hidden or ffn that is no multiple of 8 and for
- * KEEP_MXFP8 with dtype F32; WORKSPACE for a workspace that is NULL or too
- * small. */
+ * KEEP_MXFP8 with dtype F32, and for rows, hidden or ffn beyond 2^29 (fp32:
+ * 2097120); WORKSPACE for a workspace that is NULL or too small. */
 oases_status oases_glu_fwd(const oases_glu_desc *desc, const oases_glu_weights *wts, const void *x,
                            const void *resid, void *y, void *saved, void *workspace,
                            size_t ws_bytes, void *stream);

@@ -29,6 +29,8 @@ oases_status ce_shape(const oases_ce_desc* d, CeShape* s) {
   if (d->accumulate != 0 && d->accumulate != 1) return OASES_ERR_INVALID_ARG;
   if (d->accumulate && d->grad_dtype != OASES_F32) return OASES_ERR_INVALID_ARG;
   if (d->dtype == OASES_BF16 && d->hidden % 8 != 0) return OASES_ERR_UNSUPPORTED;
+  if (std::max({d->rows, d->hidden, d->vocab}) > (d->dtype == OASES_F32 ? f32::MAX_DIM : 1 << 29))
+    return OASES_ERR_UNSUPPORTED;  // 32-bit tile and TMA coordinates
   s->M = d->rows;
   s->H = d->hidden;
   s->V = d->vocab;
@@ -140,7 +142,7 @@ struct GradF32 {
   }
 };
 
-// The largest |dloss| of the rows that have a loss (CeRows::scale).
+// The largest finite |dloss| of the rows that have a loss (CeRows::scale).
 __global__ void __launch_bounds__(1024)
 ce_scale_kernel(const float* dloss, const int64_t* target, int64_t ignore, int M, float* scale) {
   __shared__ float red[32];
@@ -148,7 +150,7 @@ ce_scale_kernel(const float* dloss, const int64_t* target, int64_t ignore, int M
   pdl_trigger();
   float mx = 0.f;
   for (int m = threadIdx.x; m < M; m += blockDim.x)
-    if (target[m] != ignore) mx = fmaxf(mx, fabsf(dloss[m]));
+    if (const float a = fabsf(dloss[m]); target[m] != ignore && a < INFINITY) mx = fmaxf(mx, a);
   mx = block_max(mx, red);
   if (threadIdx.x == 0) scale[0] = mx;
 }
@@ -207,9 +209,9 @@ cudaError_t bwd(const CeShape& s, const void* x, const void* w, const int64_t* t
   return cudaSuccess;
 }
 
-bool misaligned(std::initializer_list<const void*> ps) {
+bool misaligned(std::initializer_list<const void*> ps, uintptr_t bytes) {
   for (const void* p : ps)
-    if ((uintptr_t)p & 15) return true;
+    if ((uintptr_t)p & (bytes - 1)) return true;
   return false;
 }
 
@@ -232,7 +234,8 @@ extern "C" oases_status oases_ce_fwd(const oases_ce_desc* desc, const void* x, c
   if (v != OASES_OK) return v;
   if (s.M == 0) return OASES_OK;
   if (!x || !w || !target || !loss || !lse) return OASES_ERR_INVALID_ARG;
-  if (misaligned({x, w, target, loss, lse, workspace})) return OASES_ERR_INVALID_ARG;
+  if (misaligned({x, w, workspace}, 16) || misaligned({target}, 8) || misaligned({loss, lse}, 4))
+    return OASES_ERR_INVALID_ARG;
   const size_t need = layout(s, false).total;
   if (need > 0 && (!workspace || ws_bytes < need)) return OASES_ERR_WORKSPACE;
   return api_end(fwd(s, x, w, target, loss, lse, static_cast<char*>(workspace),
@@ -248,7 +251,9 @@ extern "C" oases_status oases_ce_bwd(const oases_ce_desc* desc, const void* x, c
   CeShape s;
   const oases_status v = ce_shape(desc, &s);
   if (v != OASES_OK) return v;
-  if (misaligned({x, w, target, lse, dloss, dx, dw, workspace})) return OASES_ERR_INVALID_ARG;
+  if (misaligned({x, w, dx, dw, workspace}, 16) || misaligned({target}, 8) ||
+      misaligned({lse, dloss}, 4))
+    return OASES_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s.M == 0) {  // sums over no rows
     if (!dw || s.accumulate) return OASES_OK;

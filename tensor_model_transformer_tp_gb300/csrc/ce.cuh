@@ -18,8 +18,8 @@ struct CeShape {
 };
 
 // g = s r (softmax - onehot): s one factor for all rows, r one per row.  s is
-// the dloss given for all rows, or the largest |dloss| of the rows that have a
-// loss, so r is at most 1 in magnitude, and exactly 1 where the rows share one
+// the dloss given for all rows, or the largest finite |dloss| of the rows that
+// have a loss, so r is at most 1 in magnitude, and exactly 1 where the rows share one
 // dloss: the products then see entries of g / s such as the target's, close to
 // -1, that do not depend on how dloss itself rounds to the storage type.
 struct CeRows {

@@ -220,7 +220,7 @@ BwdPlan bwd_plan(const CeShape& s) {
   // dx of few rows has few tiles, each a contraction over the whole vocabulary:
   // split it over the SMs
   const int tiles = s.M <= 128 ? (s.H + 127) / 128 : (s.M + 255) / 256 * ((s.H + 255) / 256);
-  const int slots = s.M <= 128 ? core::sm_count() : core::sm_count() / 2;
+  const int slots = s.M <= 128 ? core::sm_count() : core::pair_count();
   b.splits = pieces == 1 ? std::max(1, std::min(slots / tiles, s.V / 512)) : 1;
   core::slices_per_split(s.V, &b.splits);
   b.slab = (int64_t)core::slab_rows(s.M) * s.H;

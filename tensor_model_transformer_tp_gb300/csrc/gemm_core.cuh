@@ -439,11 +439,13 @@ inline int sm_count() {
   const int dev = current_device();
   int n = dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
   if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 1;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      return 2;  // no device: sizes can still be asked for
     if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
   }
   return n;
 }
+inline int pair_count() { return std::max(1, sm_count() / 2); }
 
 // Operands of one product.  A(m, k): A_K ? a[m * lda + k] : a[k * lda + m]; B
 // likewise over N (DUAL: over b_off + N rows).

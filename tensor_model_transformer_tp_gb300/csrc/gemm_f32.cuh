@@ -21,6 +21,7 @@ namespace oases {
 namespace f32 {
 
 constexpr int BM = 64, BN = 64, BK = 32, NT = 128;
+constexpr int MAX_DIM = 32 * 65535;  // rows and columns: tiles of 32 and 64 fit a grid dimension
 constexpr int CLUSTER = 8;  // largest split of a contraction
 
 // Operand tiles in shared memory are [BK][64] with each k's sixteen groups of

@@ -18,6 +18,8 @@ oases_status api_end(cudaError_t e);
 
 namespace {
 
+constexpr int MAX_DIM = 1 << 29;  // rows, hidden, ffn: 32-bit tile and TMA coordinates
+
 // Bias gradients of up to this many rows are summed by one launch with 64 row
 // groups per column; more rows go through partial rows.
 constexpr int DIRECT_SUM_ROWS = 2048;
@@ -25,7 +27,7 @@ constexpr int DIRECT_SUM_ROWS = 2048;
 oases_status glu_shape(const oases_glu_desc* d, GluShape* s) {
   if (!d) return OASES_ERR_INVALID_ARG;
   if (d->dtype != OASES_F32 && d->dtype != OASES_BF16) return OASES_ERR_INVALID_ARG;
-  if (d->rows < 0 || d->hidden <= 0 || d->ffn <= 0 || d->ffn > (1 << 29)) return OASES_ERR_INVALID_ARG;
+  if (d->rows < 0 || d->hidden <= 0 || d->ffn <= 0) return OASES_ERR_INVALID_ARG;
   if (d->act != OASES_ACT_SILU && d->act != OASES_ACT_GELU) return OASES_ERR_INVALID_ARG;
   if (d->keep < OASES_GLU_KEEP_NONE || d->keep > OASES_GLU_KEEP_MXFP8) return OASES_ERR_INVALID_ARG;
   if (d->dx_dtype != OASES_F32 && d->dx_dtype != d->dtype) return OASES_ERR_INVALID_ARG;
@@ -33,6 +35,8 @@ oases_status glu_shape(const oases_glu_desc* d, GluShape* s) {
   if (d->accumulate != 0 && d->accumulate != 1) return OASES_ERR_INVALID_ARG;
   if (d->accumulate && d->grad_dtype != OASES_F32) return OASES_ERR_INVALID_ARG;
   if (d->dtype == OASES_BF16 && (d->hidden % 8 != 0 || d->ffn % 8 != 0)) return OASES_ERR_UNSUPPORTED;
+  if (std::max({d->rows, d->hidden, d->ffn}) > (d->dtype == OASES_F32 ? f32::MAX_DIM : MAX_DIM))
+    return OASES_ERR_UNSUPPORTED;
   if (d->dtype == OASES_F32 && d->keep == OASES_GLU_KEEP_MXFP8) return OASES_ERR_UNSUPPORTED;
   s->M = d->rows;
   s->H = d->hidden;

@@ -390,7 +390,7 @@ int dx_splits(const GluShape& s) {
     auto tiles = [](int64_t m, int64_t n) { return (m + 255) / 256 * ((n + 255) / 256); };
     const int64_t k = (s.M + core::BKE - 1) / core::BKE + core::TILE_COST;
     const int64_t work = tiles(s.M, s.H) * slices + (tiles(s.H, s.F) + tiles(2 * (int64_t)s.F, s.H)) * k;
-    const int64_t share = std::max<int64_t>(8, work / std::max(1, core::sm_count() / 2));
+    const int64_t share = std::max<int64_t>(8, work / core::pair_count());
     // (a quarter longer than the share is cheaper than the partial sums)
     if (slices * 4 > share * 5) splits = (int)std::min<int64_t>(16, (slices + share - 1) / share);
   }
@@ -454,14 +454,14 @@ cudaError_t glu_grads_tc(const GluShape& s, const void* x, const void* dy, const
 
 size_t glu_down_tc_bytes(const GluShape& s) {
   if (s.M <= GLU_FEW_ROWS) return 0;
-  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::sm_count() / 2);
+  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::pair_count());
   return c.splits > 1 ? align256((size_t)core::slab_rows(s.M) * s.H * 4 * c.splits) : 0;
 }
 
 cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const void* b2,
                         const void* resid, void* y, char* ws, cudaStream_t st) {
   if (s.M <= GLU_FEW_ROWS) return glu_down_few(s, h, w2, b2, resid, y, st);
-  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::sm_count() / 2);
+  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::pair_count());
   EpiOut::Params e = {};
   core::Operands o{s.M, s.H, s.F, h, s.ldh, w2, s.F};
   if (c.splits > 1) {

@@ -78,6 +78,12 @@ def _bytes(n: int, device) -> Optional[torch.Tensor]:
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
+def _sized(index: int, *asked):
+    """The library's answers about sizes, for the device (its number of SMs)."""
+    with torch.cuda.device(index):
+        return tuple(f(*a) for f, *a in asked)
+
+
 # ---- gated feed-forward block ---------------------------------------------------
 # Plans are checked once per combination of shapes, types and options.
 def _glu_shapes(x, w):
@@ -106,8 +112,8 @@ def _glu_fwd_plan(x, w, resid, y, act, save):
             _match(name, sig, (rows, hidden), x[1], x[2])
     t = _CODE[x[1]]
     d = GluDesc(t, rows, hidden, ffn, ACT[act], KEEP[save], t, t, 0)
-    return (ctypes.byref(d), oases_glu_saved_bytes(d), oases_glu_workspace_bytes(d, False),
-            (rows, 2 * ffn))
+    return (ctypes.byref(d), oases_glu_saved_bytes(d),
+            *_sized(x[2], (oases_glu_workspace_bytes, d, False)), (rows, 2 * ffn))
 
 
 @functools.lru_cache(maxsize=512)
@@ -131,7 +137,7 @@ def _glu_bwd_plan(x, w, dy, saved, grads, act, save, dx_dtype):
         _match("saved", saved, (rows, 2 * ffn), x[1], x[2])
     else:
         _match("saved", saved, (oases_glu_saved_bytes(d),), torch.uint8, x[2])
-    return ctypes.byref(d), oases_glu_workspace_bytes(d, True)
+    return (ctypes.byref(d), *_sized(x[2], (oases_glu_workspace_bytes, d, True)))
 
 
 def _named(tensors: Dict[str, torch.Tensor], what: str):
@@ -221,7 +227,7 @@ def _ce_plan(x, w, targets, lse, dloss, dw, backward, ignore_index):
         _match("dw", dw, (vocab, hidden), torch.float32, x[2])
     d = CeDesc(ignore_index, t, rows, hidden, vocab, int(per_row), 0 if accumulate else t,
                int(accumulate))
-    return ctypes.byref(d), oases_ce_workspace_bytes(d, backward), rows
+    return (ctypes.byref(d), *_sized(x[2], (oases_ce_workspace_bytes, d, backward)), rows)
 
 
 def ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,

@@ -119,6 +119,7 @@ GLU_SHAPES = [
     ("bf16", 1, 64, 104), ("bf16", 2, 2560, 512), ("bf16", 7, 72, 136), ("bf16", 33, 520, 264),
     ("bf16", 128, 256, 512), ("bf16", 129, 264, 520), ("bf16", 300, 512, 1000),
     ("bf16", 257, 128, 2048), ("bf16", 640, 1032, 776), ("bf16", 1, 8, 8),
+    ("bf16", 17, 1096, 72), ("bf16", 65, 264, 1160), ("bf16", 180, 200, 3000),
     ("f32", 1, 33, 17), ("f32", 5, 64, 100), ("f32", 130, 97, 250), ("f32", 200, 256, 520),
     ("f32", 1, 1, 1),
 ]
@@ -416,6 +417,26 @@ def test_ce_ignored_rows_count_for_nothing_whatever_they_hold():
     loss, lse = F.ce_fwd(x, w, t, ignore_index=7)
     dx, dw = F.ce_bwd(x, w, t, lse, d, ignore_index=7)
     assert not loss.any() and not dx.any() and not dw.any()
+
+
+def test_ce_targets_may_be_a_slice_and_dloss_infinite():
+    """Shifted targets start 8 bytes into their buffer; an infinite dloss of one
+    row stays in that row's dx."""
+    x, w, t, d = ce_case("bf16", 12, 64, 300, True)
+    tokens = torch.cat([t[:1], t])
+    loss0, lse0 = F.ce_fwd(x, w, t)
+    loss, lse = F.ce_fwd(x, w, tokens[1:])
+    assert torch.equal(loss, loss0) and torch.equal(lse, lse0)
+    dx0, _ = F.ce_bwd(x, w, t, lse0, d)
+    d2 = d.clone()
+    d2[3] = float("inf")
+    d2[1] = float("nan")        # an ignored row
+    dx, _ = F.ce_bwd(x, w, tokens[1:], lse0, d2)
+    rest = [m for m in range(12) if m != 3]
+    assert not torch.isfinite(dx[3]).any()
+    # the common factor is another one without row 3: one bf16 step at most
+    assert ((dx[rest].double() - dx0[rest].double()).abs()
+            <= 2.0 ** -6 * dx0[rest].double().abs().amax(dim=1, keepdim=True)).all()
 
 
 def test_ce_minus_infinity_logits():

@@ -60,7 +60,8 @@ def ce_status(desc, bwd=False, ws=FAKE, nb=1 << 40, **ptr):
     (dict(ffn=0), 1), (dict(act=2), 1), (dict(keep=3), 1), (dict(keep=-1), 1),
     (dict(dx_dtype=2), 1), (dict(grad_dtype=2), 1), (dict(accumulate=2), 1),
     (dict(grad_dtype=1, accumulate=1), 1), (dict(dtype=0, dx_dtype=1), 1),
-    (dict(hidden=60), 2), (dict(ffn=100), 2), (dict(dtype=0, dx_dtype=0, keep=2), 2),
+    (dict(hidden=60), 2), (dict(ffn=100), 2), (dict(rows=(1 << 29) + 1), 2),
+    (dict(ffn=(1 << 29) + 8), 2), (dict(dtype=0, dx_dtype=0, rows=1 << 22), 2), (dict(dtype=0, dx_dtype=0, keep=2), 2),
 ])
 def test_glu_descriptors(bad, status):
     d = glu_desc(**bad)
@@ -72,7 +73,8 @@ def test_glu_descriptors(bad, status):
 @pytest.mark.parametrize("bad,status", [
     (dict(dtype=2), 1), (dict(rows=-1), 1), (dict(hidden=0), 1), (dict(vocab=0), 1),
     (dict(dloss_per_row=2), 1), (dict(grad_dtype=2), 1), (dict(accumulate=-1), 1),
-    (dict(grad_dtype=1, accumulate=1), 1), (dict(hidden=36), 2),
+    (dict(grad_dtype=1, accumulate=1), 1), (dict(hidden=36), 2), (dict(vocab=(1 << 29) + 1), 2),
+    (dict(dtype=0, vocab=1 << 22), 2),
 ])
 def test_ce_descriptors(bad, status):
     d = ce_desc(**bad)
@@ -94,17 +96,33 @@ def test_pointers_and_workspaces():
     c = ce_desc()
     for name in ("x", "w", "target", "loss", "lse"):
         assert ce_status(c, **{name: None}) == 1
-        assert ce_status(c, **{name: FAKE + 8}) == 1
+    for name, off in (("x", 8), ("w", 8), ("target", 4), ("loss", 2), ("lse", 2)):
+        assert ce_status(c, **{name: FAKE + off}) == 1
     for name in ("x", "w", "target", "lse", "dloss"):
         assert ce_status(c, bwd=True, **{name: None}) == 1
-    for name in ("dx", "dw", "dloss"):
-        assert ce_status(c, bwd=True, **{name: FAKE + 2}) == 1
+    for name, off in (("dx", 8), ("dw", 8), ("target", 4), ("lse", 2), ("dloss", 2)):
+        assert ce_status(c, bwd=True, **{name: FAKE + off}) == 1
     for bwd in (False, True):
         for need, status, desc in ((oz.oases_glu_workspace_bytes(d, bwd), glu_status, d),
                                    (oz.oases_ce_workspace_bytes(c, bwd), ce_status, c)):
             if need:
                 assert status(desc, bwd, ws=None) == 3
                 assert status(desc, bwd, nb=need - 1) == 3
+
+
+def test_workspaces_of_every_size_can_be_asked_for():
+    """From one row to millions, without a device: positive, and no smaller for
+    more rows than what the rows' own intermediate results need."""
+    for rows in (1, 127, 128, 129, 256, 1000, 8192, 100000, 1 << 22):
+        for keep in (0, 1, 2):
+            d = glu_desc(rows=rows, hidden=2560, ffn=10240, keep=keep)
+            assert oz.oases_glu_workspace_bytes(d, False) >= rows * 10240 * 2
+            assert oz.oases_glu_workspace_bytes(d, True) >= rows * 3 * 10240 * 2
+        c = ce_desc(rows=rows, hidden=2560, vocab=50257)
+        assert oz.oases_ce_workspace_bytes(c, False) > 0
+        # g of one piece, not of the whole vocabulary
+        n = oz.oases_ce_workspace_bytes(c, True)
+        assert 0 < n <= (600 << 20) + rows * (4096 + 256) * 2 + rows * 2560 * 4
 
 
 def test_no_rows_need_nothing():
