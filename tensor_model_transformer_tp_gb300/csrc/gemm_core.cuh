@@ -561,6 +561,22 @@ struct Product {
 constexpr int64_t GROUP_BYTES = 256ll << 20;  // operands of the products, counted for each
 constexpr int TILE_COST = 4;  // a tile's fixed cost in K-slices (fill, hand-over)
 
+inline int64_t tiles256(int64_t M, int64_t N) {
+  return (M + 2 * BM - 1) / (2 * BM) * ((N + 255) / 256);
+}
+inline int64_t operand_bytes(int64_t M, int64_t N, int64_t K) { return 2 * K * (M + N); }
+
+// Splits of a long contraction of `tiles` tiles that shares a launch with other
+// work (K-slices of tiles), so that none of its tiles is longer than the slots'
+// even share.  (A quarter longer is cheaper than the partial sums.)
+inline int even_splits(int64_t tiles, int K, int64_t other, int slots) {
+  const int64_t slices = (K + BKE - 1) / BKE;
+  const int64_t share = std::max<int64_t>(8, (tiles * slices + other) / slots);
+  int splits = slices * 4 > share * 5 ? (int)std::min<int64_t>(16, (slices + share - 1) / share) : 1;
+  slices_per_split(K, &splits);
+  return splits;
+}
+
 // Deals `tiles` tiles of length `len` to the slots, least loaded first, and adds
 // them to `load`; first[s] .. first[s + 1] are slot s's tiles.
 inline void deal(int tiles, int len, int slots, int* load, uint16_t* first) {
@@ -622,7 +638,7 @@ cudaError_t launch_group(const Product* prod, const typename Epi::Params* ep, bo
   // MB: 245 us apart, 249 together; of 1 GB: 4% slower together).
   int64_t bytes = 0;
   for (int i = 0; i < N; ++i)
-    bytes += 2ll * prod[i].o.K * ((int64_t)prod[i].o.M + prod[i].o.N);
+    bytes += operand_bytes(prod[i].o.M, prod[i].o.N, prod[i].o.K);
   if (bytes > GROUP_BYTES) return cudaSuccess;
   // longest tiles first
   int order[N], len[N];
@@ -631,7 +647,7 @@ cudaError_t launch_group(const Product* prod, const typename Epi::Params* ep, bo
     const Operands& o = prod[i].o;
     int splits = o.splits;
     len[i] = slices_per_split(o.K, &splits) + TILE_COST;
-    tiles[i] = (int64_t)((o.M + 2 * BM - 1) / (2 * BM)) * ((o.N + 255) / 256) * splits;
+    tiles[i] = tiles256(o.M, o.N) * splits;
     if (tiles[i] > UINT16_MAX || tiles[i] * len[i] > INT32_MAX / 8) return cudaSuccess;
     apart += rounds_cost(tiles[i], len[i], slots) + 2 * TILE_COST;  // a launch more
     order[i] = i;

@@ -378,24 +378,11 @@ namespace {
 
 using core::EpiOut;
 
-// dx is a contraction over 2 ffn with few tiles when rows are few: split it over
-// the SMs (up to 128 rows: a launch of its own), or so that none of its tiles is
-// longer than the CTAs' even share of the three gradients' work.
+// dx is a contraction over 2 ffn with few tiles when rows are few.
 int dx_splits(const GluShape& s) {
-  const int64_t slices = (2 * (int64_t)s.F + core::BKE - 1) / core::BKE;
-  int splits = 1;
-  if (s.M <= 128) {
-    splits = std::max(1, std::min(core::sm_count() / ((s.H + 127) / 128), 2 * s.F / 512));
-  } else {
-    auto tiles = [](int64_t m, int64_t n) { return (m + 255) / 256 * ((n + 255) / 256); };
-    const int64_t k = (s.M + core::BKE - 1) / core::BKE + core::TILE_COST;
-    const int64_t work = tiles(s.M, s.H) * slices + (tiles(s.H, s.F) + tiles(2 * (int64_t)s.F, s.H)) * k;
-    const int64_t share = std::max<int64_t>(8, work / core::pair_count());
-    // (a quarter longer than the share is cheaper than the partial sums)
-    if (slices * 4 > share * 5) splits = (int)std::min<int64_t>(16, (slices + share - 1) / share);
-  }
-  core::slices_per_split(2 * s.F, &splits);
-  return splits;
+  const int64_t k = (s.M + core::BKE - 1) / core::BKE + core::TILE_COST, F2 = 2 * (int64_t)s.F;
+  return core::even_splits(core::tiles256(s.M, s.H), 2 * s.F,
+                           (core::tiles256(s.H, s.F) + core::tiles256(F2, s.H)) * k, core::pair_count());
 }
 
 #define OASES_TRY(expr)                       \
@@ -432,9 +419,8 @@ cudaError_t glu_grads_tc(const GluShape& s, const void* x, const void* dy, const
     ok = ok && core::out_map(&e_dx, dx, s.dx_t, s.M, s.H, s.H);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const bool few = s.M <= 128;
   bool taken = false;
-  if (dw1 && dw2 && dx && !few) {
+  if (dw1 && dw2 && dx) {
     const core::Product prod[3] = {{o_dx, true}, {o_w2, false}, {o_w1, false}};
     const EpiOut::Params ep[3] = {e_dx, e_w2, e_w1};
     OASES_TRY((core::launch_group<EpiOut, 3>(prod, ep, &taken, st)));
@@ -442,9 +428,7 @@ cudaError_t glu_grads_tc(const GluShape& s, const void* x, const void* dy, const
   if (!taken) {
     if (dw2) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_w2, e_w2, st)));
     if (dw1) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_w1, e_w1, st)));
-    if (dx)
-      OASES_TRY(few ? (core::launch<EpiOut, 128, true, false, 1>(o_dx, e_dx, st))
-                    : (core::launch<EpiOut, 256, true, false, 2>(o_dx, e_dx, st)));
+    if (dx) OASES_TRY((core::launch<EpiOut, 256, true, false, 2>(o_dx, e_dx, st)));
   }
   if (dx && splits > 1)
     OASES_TRY(core::slab_sum(reinterpret_cast<const float*>(ws), splits, slab, nullptr, nullptr, nullptr,
