@@ -13,7 +13,11 @@ using core::pack2;
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
 constexpr int64_t PART_BYTES = 256ll << 20;   // partial maxima and sums of the forward
-constexpr int64_t PIECE_BYTES = 256ll << 20;  // g of one piece of the backward
+// g of one piece of the backward.  A piece's dx is added to the others' in fp32,
+// so pieces are long; 8192 x 50304 x 2560 takes 3.60 ms with 64 MB, 3.50 with 128,
+// 3.42 with 256, 3.36 with 512, 3.30 with 1024; 2041 x 50257 x 1024 the same from
+// 128 on.
+constexpr int64_t PIECE_BYTES = 256ll << 20;
 constexpr int MIN_PIECE = 4096;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -23,6 +27,10 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ---- forward -------------------------------------------------------------------
+// Bound by the product: 4096 x 32000 x 4096 runs at 1.8 PFLOP/s, 2041 x 50257 x
+// 1024 in 105 us (the exponentials, 2048 clocks of a 256-column tile's 8192 at
+// hidden 1024, hide behind the next tile's main loop); few rows by reading w:
+// 37 x 50257 x 1024 in 19 us, 5.5 TB/s with the join.
 // Each warp reduces its half of a tile's columns of its 32 rows, one row per
 // lane, to (r, s): r the maximum of the logits in base-2 units (l log2 e), s
 // the sum of 2^(l log2 e - r); -inf and 0 where every logit is -inf.  The

@@ -634,8 +634,9 @@ cudaError_t launch_group(const Product* prod, const typename Epi::Params* ep, bo
   if (slots > MAX_SLOTS) return cudaSuccess;
   // A slot's tiles of a product are neighbours, so the tiles in flight are spread
   // over the whole product: right while the operands stay in L2, else each is
-  // streamed more than once (operands of 132 MB: 126 to 100 us together; of 290
-  // MB: 245 us apart, 249 together; of 1 GB: 4% slower together).
+  // streamed more than once.  Measured apart and together, operands counted for
+  // each product: 192 MB 126 and 98 us, 134 MB 142 and 98, 493 MB 245 and 249,
+  // 980 MB 4% slower together.
   int64_t bytes = 0;
   for (int i = 0; i < N; ++i)
     bytes += operand_bytes(prod[i].o.M, prod[i].o.N, prod[i].o.K);

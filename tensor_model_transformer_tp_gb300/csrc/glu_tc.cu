@@ -16,6 +16,11 @@ using core::unpack2;
 // Tiles of 256 rows x 128 columns of a and the same of b (DUAL): every
 // accumulator pair (a, b) of an output is in one thread, so h, and what is kept
 // of a and b, leave from registers and the projections never go to memory.
+// Bound by the product (4096 x 4096 x 11008 runs at 1.7 PFLOP/s with the second
+// product, the rate the power limit sustains) where hidden is large, and by the
+// writes of what is kept where it is small: at 4096 x 1024 x 4096 it takes 40 us
+// keeping nothing and 57 keeping 67 MB of a and b, the same through plain stores
+// as through TMA.
 template <int KEEP>
 struct EpiDual {
   static constexpr bool DUAL = true;
@@ -148,11 +153,15 @@ struct EpiDual {
 // columns of a warp's 32 rows at a time.  Two staging sets of three 2 KB
 // buffers (64-byte rows, 64-byte swizzle) alternate: TMA brings a and b of the
 // next 32 columns into one while the other's are turned, in place, into da and
-// db, with h beside them, and stored.  (One row per lane straight from global
-// memory costs a cache-line lookup per lane and load: the kernel took 73 us
-// instead of 41 at 4096 x 1024 x 4096.)
+// db, with h beside them, and stored.  (With one row per lane loaded straight
+// from global memory, a cache-line lookup per lane, and the activation chosen
+// per element, the kernel took 73 us at 4096 x 1024 x 4096; staged 61, with the
+// choice outside the loops 48.)
 // EIGHT: a and b come from the 8-bit form, 32 bytes of a row per lane (whole
 // sectors), loaded one step ahead.
+// What bounds it: the product takes 24 us there, the 100 MB it writes 25 at the
+// 4 TB/s that fills reach, and the two add up; without its loads it takes 39,
+// without loads and stores 24, without the arithmetic between them 45.
 template <bool EIGHT>
 struct EpiGrad {
   static constexpr bool DUAL = false, PAD_ROWS = false;
