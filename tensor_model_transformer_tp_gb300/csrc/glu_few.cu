@@ -7,10 +7,13 @@
 // the partial D of the cluster meet through distributed shared memory, where
 // each CTA sums, in the order of the splits, and finishes its share of the
 // outputs.  Two CTAs per SM keep 190 KB of weight tiles in flight per SM.
-// One row at 2560 x 6912 (106 MB of weights) takes 20 us for both products, 5.3
-// TB/s; 16 rows at 4096 x 11008 (271 MB) 50 us, 5.4 TB/s; 61 rows at 1024 x 2736
-// (17 MB) 13 us, two kernels' fixed costs.  On the 256-row tiles of gemm_core.cuh
-// the three took 53, 83 and 22 us, and 128 rows at 2560 x 6912 48 against 40.
+// With the weights in memory, one row at 2560 x 6912 (106 MB) takes 22.5 us for
+// both products, 4.7 TB/s; 16 rows at 4096 x 11008 (271 MB) 48.5, 5.6 TB/s; 61
+// rows at 1024 x 2736 (17 MB) 13.8, two kernels' fixed costs.  One CTA per SM of
+// twelve stages took 24.1, 59.8 and 15.2, four of three 23.8, 51.0 and 15.6, and
+// asking for the second product's weights to be brought into L2 as the first's
+// CTAs end 24.7, 53.5 and 13.9.  On the 256-row tiles of gemm_core.cuh the three
+// took 53, 83 and 22, and 128 rows at 2560 x 6912 48 against 40.
 //
 // The second product's weight tiles are requested before the first kernel has
 // finished: they depend on nothing that it writes, and every earlier kernel of

@@ -1,10 +1,11 @@
 """The gated feed-forward block and the linear head's cross entropy on torch tensors.
 
-Each function checks its tensors, allocates outputs and workspace with torch's
-allocator and makes one call of liboases.so on torch's current stream of the
-tensors' device; nothing is computed here and nothing is kept between calls.
-Because the allocations follow torch's stream rules, the calls can be made on
-any stream, from several threads, and inside CUDA graph capture.
+Each function checks its tensors (once per combination of shapes, types and
+options), allocates outputs and workspace with torch's caching allocator and makes
+one call of liboases.so on torch's current stream of the tensors' device; nothing
+is computed here and no data is kept between calls.  Because the allocations
+follow torch's stream rules, the calls can be made on any stream, from several
+threads, and inside CUDA graph capture.
 
 Tensors are contiguous, on one CUDA device, ``float32`` or ``bfloat16`` as
 ``x`` is; anything else raises ``ValueError`` before a call is made.  Errors of
@@ -24,6 +25,9 @@ from . import (ACT, KEEP, CeDesc, GluDesc, GluGrads, GluWeights, _check as _chec
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
 _NAMES = ("w1", "b1", "w2", "b2")
+_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_raw_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
+_raw_delete = torch._C._cuda_cudaCachingAllocator_raw_delete
 
 
 def _need(ok: bool, what: str) -> None:
@@ -63,19 +67,24 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _call(fn, index: int, *args) -> None:
-    """One library call on torch's current stream of device ``index``, made current."""
-    if torch._C._cuda_getDevice() == index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
+def _call(fn, index: int, n_ws: int, *args) -> None:
+    """One library call on torch's current stream of device ``index``, made
+    current, with n_ws bytes of workspace from torch's caching allocator (raw, as
+    torch.cuda.caching_allocator_alloc gives it: a third of a tensor's cost)."""
+    if _get_device() != index:
         with torch.cuda.device(index):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            return _call(fn, index, n_ws, *args)
+    stream = _raw_stream(index)
+    if n_ws:
+        ws = _raw_alloc(n_ws, stream)
+        try:
+            st = fn(*args, ws, n_ws, stream)
+        finally:
+            _raw_delete(ws)
+    else:
+        st = fn(*args, None, 0, stream)
     if st:
         _check_status(st)
-
-
-def _bytes(n: int, device) -> Optional[torch.Tensor]:
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
 def _sized(index: int, *asked):
@@ -163,18 +172,16 @@ def glu_fwd(x: torch.Tensor, weights: Dict[str, torch.Tensor], act: str = "silu"
     w1, b1, w2, b2 = _named(weights, "weights")
     desc, n_saved, n_ws, kept = _glu_fwd_plan(
         _sig(x), (_sig(w1), _sig(b1), _sig(w2), _sig(b2)), _sig(resid), _sig(y), act, save)
-    device = x.device
     if y is None:
         y = torch.empty_like(x)
     saved = None
     if save == "pre":
-        saved = torch.empty(kept, dtype=x.dtype, device=device)
+        saved = torch.empty(kept, dtype=x.dtype, device=x.device)
     elif save == "mxfp8":
-        saved = torch.empty(n_saved, dtype=torch.uint8, device=device)
-    ws = _bytes(n_ws, device)
+        saved = torch.empty(n_saved, dtype=torch.uint8, device=x.device)
     w = GluWeights(_ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2))
-    _call(lib().oases_glu_fwd, x.get_device(), desc, ctypes.byref(w), _ptr(x), _ptr(resid), _ptr(y),
-          _ptr(saved), _ptr(ws), n_ws)
+    _call(lib().oases_glu_fwd, x.get_device(), n_ws, desc, ctypes.byref(w), _ptr(x), _ptr(resid),
+          _ptr(y), _ptr(saved))
     return y, saved
 
 
@@ -196,16 +203,14 @@ def glu_bwd(x: torch.Tensor, dy: torch.Tensor, weights: Dict[str, torch.Tensor],
     desc, n_ws = _glu_bwd_plan(
         _sig(x), (_sig(w1), _sig(b1), _sig(w2), _sig(b2)), _sig(dy), _sig(saved),
         None if given is None else tuple(_sig(g) for g in given), act, save, dx_dtype)
-    device = x.device
     if grads is None:
         grads = {k: torch.empty_like(v) for k, v in weights.items() if v is not None}
         given = _named(grads, "grads")
     dx = torch.empty_like(x, dtype=dx_dtype) if need_dx else None
-    ws = _bytes(n_ws, device)
     w = GluWeights(_ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2))
     g = GluGrads(*[_ptr(v) for v in given])
-    _call(lib().oases_glu_bwd, x.get_device(), desc, ctypes.byref(w), _ptr(x), _ptr(dy), _ptr(saved),
-          _ptr(dx), ctypes.byref(g), _ptr(ws), n_ws)
+    _call(lib().oases_glu_bwd, x.get_device(), n_ws, desc, ctypes.byref(w), _ptr(x), _ptr(dy),
+          _ptr(saved), _ptr(dx), ctypes.byref(g))
     return dx, grads
 
 
@@ -240,12 +245,10 @@ def ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     """
     desc, n_ws, rows = _ce_plan(_sig(x), _sig(w), _sig(targets), None, None, None, False,
                                 ignore_index)
-    device = x.device
-    loss = torch.empty(rows, dtype=torch.float32, device=device)
-    lse = torch.empty(rows, dtype=torch.float32, device=device)
-    ws = _bytes(n_ws, device)
-    _call(lib().oases_ce_fwd, x.get_device(), desc, _ptr(x), _ptr(w), _ptr(targets), _ptr(loss), _ptr(lse),
-          _ptr(ws), n_ws)
+    loss = torch.empty(rows, dtype=torch.float32, device=x.device)
+    lse = torch.empty_like(loss)
+    _call(lib().oases_ce_fwd, x.get_device(), n_ws, desc, _ptr(x), _ptr(w), _ptr(targets), _ptr(loss),
+          _ptr(lse))
     return loss, lse
 
 
@@ -263,13 +266,11 @@ def ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.T
     desc, n_ws, _ = _ce_plan(_sig(x), _sig(w), _sig(targets), _sig(lse), _sig(dloss), _sig(dw),
                              True, ignore_index)
     _need(need_dw or dw is None, "dw is given, but need_dw is false")
-    device = x.device
     if dw is None and need_dw:
         dw = torch.empty_like(w)
     dx = torch.empty_like(x) if need_dx else None
-    ws = _bytes(n_ws, device)
-    _call(lib().oases_ce_bwd, x.get_device(), desc, _ptr(x), _ptr(w), _ptr(targets), _ptr(lse), _ptr(dloss),
-          _ptr(dx), _ptr(dw), _ptr(ws), n_ws)
+    _call(lib().oases_ce_bwd, x.get_device(), n_ws, desc, _ptr(x), _ptr(w), _ptr(targets), _ptr(lse),
+          _ptr(dloss), _ptr(dx), _ptr(dw))
     return dx, dw
 
 
