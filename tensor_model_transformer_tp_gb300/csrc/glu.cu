@@ -77,7 +77,7 @@ Layout layout(const GluShape& s, bool backward) {
   take(&l.h, h);
   if (!backward && s.t == DType::BF16) take(&l.dx, glu_down_tc_bytes(s));
   if (backward) {
-    if (s.keep == OASES_GLU_KEEP_NONE) take(&l.pre, pre);
+    if (s.keep == OASES_GLU_KEEP_NONE && s.t == DType::F32) take(&l.pre, pre);
     take(&l.dpre, pre);
     if (s.t == DType::BF16) take(&l.dx, glu_grads_tc_bytes(s));
     if (s.M > DIRECT_SUM_ROWS) {
@@ -282,10 +282,10 @@ cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, cons
   return launch_pdl(column_sums_kernel<__nv_bfloat16, __nv_bfloat16, 8>, grid, block, 0, st, q, s.M, acc);
 }
 
-// [a | b] and h = act(a) b; h, pre and kept8 are each left out when null.
+// [a | b] and h = act(a) b; pre and kept8 (and, fp32, h) are left out when null.
 cudaError_t project(const GluShape& s, const oases_glu_weights& w, const void* x, void* h, void* pre,
-                    int64_t ld_pre, void* kept8, cudaStream_t st) {
-  if (s.t == DType::BF16) return glu_project_tc(s, x, w.w1, w.b1, h, pre, ld_pre, kept8, st);
+                    void* kept8, cudaStream_t st) {
+  if (s.t == DType::BF16) return glu_project_tc(s, x, w.w1, w.b1, h, pre, kept8, st);
   const f32::Args g{s.M, s.F, s.H, (const float*)x, s.H, (const float*)w.w1, s.H, s.F};
   return f32::launch<UpF32, true, true>(
       g, UpF32{(const float*)w.b1, (float*)h, (float*)pre, s.act}, st);
@@ -294,7 +294,7 @@ cudaError_t project(const GluShape& s, const oases_glu_weights& w, const void* x
 cudaError_t fwd(const GluShape& s, const oases_glu_weights& w, const void* x, const void* resid,
                 void* y, void* saved, char* ws, cudaStream_t st) {
   void* h = ws + layout(s, false).h;
-  OASES_TRY(project(s, w, x, h, s.keep == OASES_GLU_KEEP_PRE ? saved : nullptr, 2 * (int64_t)s.F,
+  OASES_TRY(project(s, w, x, h, s.keep == OASES_GLU_KEEP_PRE ? saved : nullptr,
                     s.keep == OASES_GLU_KEEP_MXFP8 ? saved : nullptr, st));
   if (s.t == DType::BF16)
     return glu_down_tc(s, h, w.w2, w.b2, resid, y, ws + layout(s, false).dx, st);
@@ -307,21 +307,20 @@ cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
                 const void* saved, void* dx, const oases_glu_grads& gr, char* ws, cudaStream_t st) {
   const Layout l = layout(s, true);
   void *h = ws + l.h, *dpre = ws + l.dpre;
-  const void *pre = saved, *kept8 = nullptr;
-  int64_t ld_pre = 2 * (int64_t)s.F;
-  if (s.keep == OASES_GLU_KEEP_NONE) {
-    void* p = ws + l.pre;
-    ld_pre = s.ldp;
-    OASES_TRY(project(s, w, x, nullptr, p, ld_pre, nullptr, st));
-    pre = p;
-  } else if (s.keep == OASES_GLU_KEEP_MXFP8) {
-    pre = nullptr;
-    kept8 = saved;
-  }
   if (s.t == DType::BF16) {
-    OASES_TRY(glu_grad_tc(s, dy, w.w2, pre, ld_pre, kept8, dpre, h, st));
+    if (s.keep == OASES_GLU_KEEP_NONE)
+      OASES_TRY(glu_grad_again_tc(s, x, dy, w.w1, w.b1, w.w2, dpre, h, st));
+    else if (s.keep == OASES_GLU_KEEP_PRE)
+      OASES_TRY(glu_grad_tc(s, dy, w.w2, saved, nullptr, dpre, h, st));
+    else
+      OASES_TRY(glu_grad_tc(s, dy, w.w2, nullptr, saved, dpre, h, st));
     OASES_TRY(glu_grads_tc(s, x, dy, w.w1, dpre, h, dx, gr.w1, gr.w2, ws + l.dx, st));
   } else {
+    const void* pre = saved;
+    if (s.keep == OASES_GLU_KEEP_NONE) {
+      OASES_TRY(project(s, w, x, nullptr, ws + l.pre, nullptr, st));
+      pre = ws + l.pre;
+    }
     const f32::Args g{s.M, s.F, s.H, (const float*)dy, s.H, (const float*)w.w2, s.F};
     OASES_TRY((f32::launch<GradF32, true, false>(
         g, GradF32{(const float*)pre, (float*)dpre, (float*)h, s.act}, st)));

@@ -44,7 +44,7 @@ struct FewArgs {
   const __nv_bfloat16 *bias, *resid;
   __nv_bfloat16 *out;   // h [M, N] or y [M, N]
   __nv_bfloat16 *pre;   // [M, 2N]
-  int64_t ldx, ldo, ldp;  // leading dimensions of x, out and pre
+  int64_t ldx, ldo;     // leading dimensions of x and out
   uint8_t *codes, *scales;
   int64_t ldq, code_stride, scale_stride;
   int kgroups;
@@ -198,8 +198,8 @@ glu_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         b += __bfloat162float(g.bias[g.N + c]);
       }
       if (g.keep == OASES_GLU_KEEP_PRE && in) {
-        g.pre[m * g.ldp + c] = __float2bfloat16_rn(a);
-        g.pre[m * g.ldp + g.N + c] = __float2bfloat16_rn(b);
+        g.pre[(int64_t)m * 2 * g.N + c] = __float2bfloat16_rn(a);
+        g.pre[(int64_t)m * 2 * g.N + g.N + c] = __float2bfloat16_rn(b);
       } else if (g.keep == OASES_GLU_KEEP_MXFP8) {
         // a warp holds 32 consecutive columns of a row: one scale block of each
         float ta = in ? fabsf(a) : 0.f, tb = in ? fabsf(b) : 0.f;
@@ -296,7 +296,7 @@ cudaError_t dispatch(const FewArgs& g, const void* w, const void* x, int tiles, 
 }  // namespace
 
 cudaError_t glu_project_few(const GluShape& s, const void* x, const void* w1, const void* b1,
-                            void* h, void* pre, int64_t ld_pre, void* kept8, cudaStream_t st) {
+                            void* h, void* pre, void* kept8, cudaStream_t st) {
   FewArgs g = {};
   g.M = s.M;
   g.N = s.F;
@@ -306,7 +306,6 @@ cudaError_t glu_project_few(const GluShape& s, const void* x, const void* w1, co
   g.out = static_cast<__nv_bfloat16*>(h);
   g.ldx = s.H;
   g.ldo = s.ldh;
-  g.ldp = ld_pre;
   int tiles = (s.F + 63) / 64;
   if (kept8) {
     g.keep = OASES_GLU_KEEP_MXFP8;

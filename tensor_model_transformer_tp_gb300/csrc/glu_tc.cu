@@ -31,25 +31,12 @@ struct EpiDual {
   struct Params {
     CUtensorMap h, a, b;  // boxes of 32 rows x 64 columns of h, pre's halves
     const __nv_bfloat16* bias;
-    int act, want_h;
+    int act;
     uint8_t *codes, *scales;
     int64_t ldq, code_stride, scale_stride;
     int kgroups;
   };
   struct Warp : WarpBase {
-    __device__ __forceinline__ void add_bias(const __nv_bfloat16* src, int left, float (&v)[32]) {
-#pragma unroll
-      for (int i = 0; i < 32; i += 8)
-        if (i < left) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + i));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = unpack2(w[k]);
-            add2_inplace(v[i + 2 * k], v[i + 2 * k + 1], f.x, f.y);
-          }
-        }
-    }
     // 32 columns of one row to E4M3 codes at q; returns the scale byte.
     // Columns at and past `left` (a multiple of 8) are not part of the matrix.
     __device__ __forceinline__ uint32_t keep8(const float (&v)[32], int left, bool row, uint8_t* q) {
@@ -133,10 +120,8 @@ struct EpiDual {
       }
       if (n >= p.N || mw >= p.M) return;
       wait_free();
-      if (e.want_h) {
-        stage_row(wh);
-        store_box(&e.h, n, mw);
-      }
+      stage_row(wh);
+      store_box(&e.h, n, mw);
       if constexpr (KEEP == OASES_GLU_KEEP_PRE) {
         stage_row(wa, 4096);
         store_box(&e.a, n, mw, 4096);
@@ -223,26 +208,6 @@ struct EpiGrad {
         v[2 * k + 1] = f.y * x;
       }
     }
-    template <int ACT>
-    __device__ __forceinline__ void gradients(const float (&a)[32], const float (&b)[32],
-                                              const float (&d)[32], uint32_t (&wa)[16],
-                                              uint32_t (&wb)[16], uint32_t (&wh)[16]) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float f0, f1, g0, g1;
-        act_both_fast(ACT, a[2 * i], f0, g0);
-        act_both_fast(ACT, a[2 * i + 1], f1, g1);
-        const float d0 = d[2 * i], d1 = d[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-        wa[i] = pack2(d0 * b0 * g0, d1 * b1 * g1);
-        wb[i] = pack2(d0 * f0, d1 * f1);
-        wh[i] = pack2(f0 * b0, f1 * b1);
-      }
-    }
-    // one of the four 16-byte units of this lane's 64-byte row
-    __device__ __forceinline__ uint4* unit(uint32_t set, int buf, int u) {
-      return reinterpret_cast<uint4*>(stg + set * 6144 + buf * 2048 + lane * 64 +
-                                      ((u ^ ((lane >> 1) & 3)) << 4));
-    }
     template <int BN>
     __device__ __forceinline__ void tile(const Params& e, const Problem& p, int mw, int n0, int half,
                                          int, uint32_t trow) {
@@ -269,8 +234,8 @@ struct EpiGrad {
           }
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            unpack8(*unit(set, 0, u), a + 8 * u);
-            unpack8(*unit(set, 1, u), b + 8 * u);
+            unpack8(*row_unit(stg + set * 6144, lane, u), a + 8 * u);
+            unpack8(*row_unit(stg + set * 6144 + 2048, lane, u), b + 8 * u);
           }
         }
         ptx::tmem_ld32(trow + c, d);
@@ -279,12 +244,9 @@ struct EpiGrad {
           gradients<OASES_ACT_SILU>(a, b, d, wa, wb, wh);
         else
           gradients<OASES_ACT_GELU>(a, b, d, wa, wb, wh);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          *unit(set, 0, u) = make_uint4(wa[4 * u], wa[4 * u + 1], wa[4 * u + 2], wa[4 * u + 3]);
-          *unit(set, 1, u) = make_uint4(wb[4 * u], wb[4 * u + 1], wb[4 * u + 2], wb[4 * u + 3]);
-          *unit(set, 2, u) = make_uint4(wh[4 * u], wh[4 * u + 1], wh[4 * u + 2], wh[4 * u + 3]);
-        }
+        put_row(stg + set * 6144, lane, wa);
+        put_row(stg + set * 6144 + 2048, lane, wb);
+        put_row(stg + set * 6144 + 4096, lane, wh);
         ptx::fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -313,23 +275,15 @@ struct EpiGrad {
   };
 };
 
-// Maps of pre's (or dpre's) two halves, boxes of 32 rows x `box` columns.
-bool halves(CUtensorMap* a, CUtensorMap* b, const void* pre, int64_t ld, const GluShape& s, int box) {
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(pre);
-  return core::tensor_map(a, q, false, s.F, s.M, ld, box, 32) &&
-         core::tensor_map(b, q + s.F, false, s.F, s.M, ld, box, 32);
-}
-
 template <int KEEP>
 cudaError_t project(const GluShape& s, const void* x, const void* w1, const void* b1, void* h,
-                    void* pre, int64_t ld_pre, void* kept8, cudaStream_t st) {
+                    void* pre, void* kept8, cudaStream_t st) {
   using E = EpiDual<KEEP>;
   typename E::Params e = {};
   e.bias = static_cast<const __nv_bfloat16*>(b1);
   e.act = s.act;
-  e.want_h = h != nullptr;
-  if (h && !core::tensor_map(&e.h, h, false, s.F, s.M, s.ldh, 64, 32)) return cudaErrorInvalidValue;
-  if (pre && !halves(&e.a, &e.b, pre, ld_pre, s, 64)) return cudaErrorInvalidValue;
+  if (!core::tensor_map(&e.h, h, false, s.F, s.M, s.ldh, 64, 32)) return cudaErrorInvalidValue;
+  if (pre && !halves(&e.a, &e.b, pre, 2 * (int64_t)s.F, s, 64)) return cudaErrorInvalidValue;
   if (kept8) {
     e.codes = static_cast<uint8_t*>(kept8);
     e.scales = e.codes + saved_scale_offset(s);
@@ -344,7 +298,7 @@ cudaError_t project(const GluShape& s, const void* x, const void* w1, const void
 }
 
 template <bool EIGHT>
-cudaError_t grad(const GluShape& s, const void* dy, const void* w2, const void* pre, int64_t ld_pre,
+cudaError_t grad(const GluShape& s, const void* dy, const void* w2, const void* pre,
                  const void* kept8, void* dpre, void* h, cudaStream_t st) {
   using E = EpiGrad<EIGHT>;
   typename E::Params e = {};
@@ -353,7 +307,7 @@ cudaError_t grad(const GluShape& s, const void* dy, const void* w2, const void* 
       !core::tensor_map(&e.h, h, false, s.F, s.M, s.ldh, 32, 32))
     return cudaErrorInvalidValue;
   if (!EIGHT) {
-    if (!halves(&e.a, &e.b, pre, ld_pre, s, 32)) return cudaErrorInvalidValue;
+    if (!halves(&e.a, &e.b, pre, 2 * (int64_t)s.F, s, 32)) return cudaErrorInvalidValue;
   } else {
     e.codes = static_cast<const uint8_t*>(kept8);
     e.scales = e.codes + saved_scale_offset(s);
@@ -370,17 +324,17 @@ cudaError_t grad(const GluShape& s, const void* dy, const void* w2, const void* 
 }  // namespace
 
 cudaError_t glu_project_tc(const GluShape& s, const void* x, const void* w1, const void* b1,
-                           void* h, void* pre, int64_t ld_pre, void* kept8, cudaStream_t st) {
-  if (s.M <= GLU_FEW_ROWS && h) return glu_project_few(s, x, w1, b1, h, pre, ld_pre, kept8, st);
-  if (kept8) return project<OASES_GLU_KEEP_MXFP8>(s, x, w1, b1, h, nullptr, 0, kept8, st);
-  if (pre) return project<OASES_GLU_KEEP_PRE>(s, x, w1, b1, h, pre, ld_pre, nullptr, st);
-  return project<OASES_GLU_KEEP_NONE>(s, x, w1, b1, h, nullptr, 0, nullptr, st);
+                           void* h, void* pre, void* kept8, cudaStream_t st) {
+  if (s.M <= GLU_FEW_ROWS) return glu_project_few(s, x, w1, b1, h, pre, kept8, st);
+  if (kept8) return project<OASES_GLU_KEEP_MXFP8>(s, x, w1, b1, h, nullptr, kept8, st);
+  if (pre) return project<OASES_GLU_KEEP_PRE>(s, x, w1, b1, h, pre, nullptr, st);
+  return project<OASES_GLU_KEEP_NONE>(s, x, w1, b1, h, nullptr, nullptr, st);
 }
 
 cudaError_t glu_grad_tc(const GluShape& s, const void* dy, const void* w2, const void* pre,
-                        int64_t ld_pre, const void* kept8, void* dpre, void* h, cudaStream_t st) {
-  return kept8 ? grad<true>(s, dy, w2, nullptr, 0, kept8, dpre, h, st)
-               : grad<false>(s, dy, w2, pre, ld_pre, nullptr, dpre, h, st);
+                        const void* kept8, void* dpre, void* h, cudaStream_t st) {
+  return kept8 ? grad<true>(s, dy, w2, nullptr, kept8, dpre, h, st)
+               : grad<false>(s, dy, w2, pre, nullptr, dpre, h, st);
 }
 
 namespace {
@@ -474,8 +428,9 @@ cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const 
 }
 
 int glu_read_and_clear_error() {
-  const int v = core::read_and_clear_error(), w = glu_few_read_and_clear_error();
-  return v ? v : w;
+  const int v = core::read_and_clear_error(), w = glu_few_read_and_clear_error(),
+            u = glu_again_read_and_clear_error();
+  return v ? v : w ? w : u;
 }
 
 }  // namespace oases
