@@ -100,8 +100,9 @@ oases_status oases_glu_fwd(const oases_glu_desc *desc, const oases_glu_weights *
  *   da = dh b act'(a), db = dh act(a), dx = da Wg + db Wu,
  *   dw1 = [da | db]^T x, db1 = colsum [da | db], dw2 = dy^T h, db2 = colsum dy.
  * (resid's gradient is dy.)  x and saved as given to and written by the
- * forward.  da, db and h are rounded to the storage type between the products,
- * which accumulate in fp32.  dx may be NULL (left out); it overlaps no input.
+ * forward; a and b are the kept values, or with KEEP_NONE fp32 sums formed again.
+ * da, db and h are rounded to the storage type between the products, which
+ * accumulate in fp32.  dx may be NULL (left out); it overlaps no input.
  * Errors as oases_glu_fwd, and INVALID_ARG for grads->b1 / b2 set where the
  * bias is NULL. */
 oases_status oases_glu_bwd(const oases_glu_desc *desc, const oases_glu_weights *wts, const void *x,
