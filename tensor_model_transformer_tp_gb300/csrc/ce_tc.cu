@@ -228,17 +228,15 @@ BwdPlan bwd_plan(const CeShape& s) {
   // dx of few rows has few tiles, each a contraction over the whole vocabulary:
   // split over the SMs, up to 128 rows in a launch of its own (it reads w at
   // 5.5 TB/s; with dw's tiles, which only write, 49 x 2024 x 40704 took 95 us
-  // against 30 + 61 apart); more rows to its even share of the launch it has
-  // with dw where launch_group takes the two
+  // against 30 + 61 apart)
   b.splits = 1;
   if (pieces == 1 && s.M <= 128) {
     b.splits = std::max(1, std::min(core::sm_count() / ((s.H + 127) / 128), s.V / 512));
     core::slices_per_split(s.V, &b.splits);
   } else if (pieces == 1) {
-    const int k = (s.M + core::BKE - 1) / core::BKE + core::TILE_COST;
-    const bool apart = core::operand_bytes(s.M, s.H, s.V) + core::operand_bytes(s.V, s.H, s.M) > core::GROUP_BYTES;
-    b.splits = core::even_splits(core::tiles256(s.M, s.H), s.V,
-                                 apart ? 0 : core::tiles256(s.V, s.H) * k, core::pair_count());
+    const int64_t k = (s.M + core::BKE - 1) / core::BKE + core::TILE_COST;
+    b.splits = core::dx_splits_of(s.M, s.H, s.V, core::tiles256(s.V, s.H) * k,
+                                  core::operand_bytes(s.M, s.H, s.V) + core::operand_bytes(s.V, s.H, s.M));
   }
   b.slab = (int64_t)core::slab_rows(s.M) * s.H;
   b.g = 0;

@@ -174,7 +174,8 @@ inline int slab_rows(int rows) { return (rows + 255) / 256 * 256; }
 struct Cut {
   int bn, splits;
 };
-inline Cut cut_of(int M, int N, int K, int slots) {
+// narrow: tiles of fewer than 256 columns are possible.
+inline Cut cut_of(int M, int N, int K, int slots, bool narrow) {
   const int nkb = (K + BKE - 1) / BKE, mp = (M + 2 * BM - 1) / (2 * BM);
   const int bn[3] = {256, 192, 128}, clk[3] = {512, 430, 480};
   Cut best{256, 1};
@@ -183,7 +184,7 @@ inline Cut cut_of(int M, int N, int K, int slots) {
     const int kbs = (nkb + splits - 1) / splits;
     if (splits > 1 && kbs < 8) break;
     for (int i = 0; i < 3; ++i) {
-      if (splits > 1 && i > 0) continue;  // a split has tiles enough
+      if (i > 0 && (splits > 1 || !narrow)) continue;  // a split has tiles enough
       const int64_t tiles = (int64_t)mp * ((N + bn[i] - 1) / bn[i]) * splits;
       double c = (double)((tiles + slots - 1) / slots) * ((double)kbs * clk[i] + 3000);
       if (splits > 1) c += 6000 + splits * (double)M * N * 8 / 1600;
@@ -195,6 +196,13 @@ inline Cut cut_of(int M, int N, int K, int slots) {
   }
   slices_per_split(K, &best.splits);
   return best;
+}
+
+// Splits of dx [M, N] over K beside weight gradients of `other` K-slices of tiles;
+// bytes: the operands of all of them, as launch_group counts them.
+inline int dx_splits_of(int M, int N, int K, int64_t other, int64_t bytes) {
+  if (bytes > GROUP_BYTES) return cut_of(M, N, K, pair_count(), false).splits;
+  return even_splits(tiles256(M, N), K, other, pair_count());
 }
 
 }  // namespace core

@@ -341,11 +341,11 @@ namespace {
 
 using core::EpiOut;
 
-// dx is a contraction over 2 ffn with few tiles when rows are few.
 int dx_splits(const GluShape& s) {
   const int64_t k = (s.M + core::BKE - 1) / core::BKE + core::TILE_COST, F2 = 2 * (int64_t)s.F;
-  return core::even_splits(core::tiles256(s.M, s.H), 2 * s.F,
-                           (core::tiles256(s.H, s.F) + core::tiles256(F2, s.H)) * k, core::pair_count());
+  return core::dx_splits_of(s.M, s.H, 2 * s.F, (core::tiles256(s.H, s.F) + core::tiles256(F2, s.H)) * k,
+                            core::operand_bytes(s.M, s.H, F2) + core::operand_bytes(s.H, s.F, s.M) +
+                                core::operand_bytes(F2, s.H, s.M));
 }
 
 #define OASES_TRY(expr)                       \
@@ -401,14 +401,14 @@ cudaError_t glu_grads_tc(const GluShape& s, const void* x, const void* dy, const
 
 size_t glu_down_tc_bytes(const GluShape& s) {
   if (s.M <= GLU_FEW_ROWS) return 0;
-  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::pair_count());
+  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::pair_count(), true);
   return c.splits > 1 ? align256((size_t)core::slab_rows(s.M) * s.H * 4 * c.splits) : 0;
 }
 
 cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const void* b2,
                         const void* resid, void* y, char* ws, cudaStream_t st) {
   if (s.M <= GLU_FEW_ROWS) return glu_down_few(s, h, w2, b2, resid, y, st);
-  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::pair_count());
+  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::pair_count(), true);
   EpiOut::Params e = {};
   core::Operands o{s.M, s.H, s.F, h, s.ldh, w2, s.F};
   if (c.splits > 1) {
