@@ -20,10 +20,6 @@ namespace {
 
 constexpr int MAX_DIM = 1 << 29;  // rows, hidden, ffn: 32-bit tile and TMA coordinates
 
-// Bias gradients of up to this many rows are summed by one launch with 64 row
-// groups per column; more rows go through partial rows.
-constexpr int DIRECT_SUM_ROWS = 2048;
-
 oases_status glu_shape(const oases_glu_desc* d, GluShape* s) {
   if (!d) return OASES_ERR_INVALID_ARG;
   if (d->dtype != OASES_F32 && d->dtype != OASES_BF16) return OASES_ERR_INVALID_ARG;
@@ -63,7 +59,7 @@ size_t saved_bytes(const GluShape& s) {
 
 // Workspace regions, each a multiple of 256 bytes.
 struct Layout {
-  size_t pre = 0, h = 0, dpre = 0, dx = 0 /* partial sums of dx, or of y */, bias = 0, part = 0, total = 0;
+  size_t pre = 0, h = 0, dpre = 0, dx = 0 /* partial sums of dx, or of y */, total = 0;
 };
 Layout layout(const GluShape& s, bool backward) {
   Layout l;
@@ -73,17 +69,12 @@ Layout layout(const GluShape& s, bool backward) {
     l.total += align256(bytes);
   };
   if (s.M == 0) return l;
-  const int wide = std::max(2 * s.F, s.H);
   take(&l.h, h);
   if (!backward && s.t == DType::BF16) take(&l.dx, glu_down_tc_bytes(s));
   if (backward) {
     if (s.keep == OASES_GLU_KEEP_NONE && s.t == DType::F32) take(&l.pre, pre);
     take(&l.dpre, pre);
     if (s.t == DType::BF16) take(&l.dx, glu_grads_tc_bytes(s));
-    if (s.M > DIRECT_SUM_ROWS) {
-      take(&l.part, (size_t)colsum_blocks(s.M) * wide * 4);
-      take(&l.bias, (size_t)wide * 4);
-    }
   }
   return l;
 }
@@ -158,7 +149,8 @@ struct GradF32 {
 };
 
 // Column sums of in[0] [M, N0] and in[1] [M, N1] (leading dimensions ld) in one
-// launch, out (+)= sums.
+// launch, out (+)= sums.  (At 8192 rows and ffn 4096, 10 us less than blocks of
+// rows summed to partial rows and those in a second launch.)
 struct Sums {
   const void* in[2];
   void* out[2];
@@ -232,45 +224,16 @@ __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int M, i
   }
 }
 
-// out (type T) = in (fp32)
-template <typename T>
-__global__ void __launch_bounds__(256) cast_kernel(const float* in, T* out, int n) {
-  pdl_wait();
-  pdl_trigger();
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < n) st_elem(out, i, in[i]);
-}
-
 #define OASES_TRY(expr)                       \
   do {                                        \
     const cudaError_t e_ = (expr);            \
     if (e_ != cudaSuccess) return e_;         \
   } while (0)
 
-// Column sums of in [M, N] (type t, leading dimension ld) to a bias gradient.
-cudaError_t bias_grad(const void* in, int64_t ld, int M, int N, DType t, void* out, DType out_t,
-                      bool accumulate, float* part, float* tmp, cudaStream_t st) {
-  if (accumulate) return colsum_accum(in, ld, M, N, t, part, static_cast<float*>(out), st);
-  float* sum = out_t == DType::F32 ? static_cast<float*>(out) : tmp;
-  cudaError_t e = cudaMemsetAsync(sum, 0, (size_t)N * 4, st);
-  if (e == cudaSuccess) e = colsum_accum(in, ld, M, N, t, part, sum, st);
-  if (e == cudaSuccess && out_t == DType::BF16)
-    e = launch_pdl(cast_kernel<__nv_bfloat16>, dim3((N + 255) / 256), dim3(256), 0, st,
-                   (const float*)tmp, (__nv_bfloat16*)out, N);
-  return e;
-}
-
 // db1 = colsum(dpre), db2 = colsum(dy), each where it is wanted.
 cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, const oases_glu_grads& gr,
-                       float* part, float* tmp, cudaStream_t st) {
+                       cudaStream_t st) {
   if (!gr.b1 && !gr.b2) return cudaSuccess;
-  if (s.M > DIRECT_SUM_ROWS) {
-    if (gr.b1)
-      OASES_TRY(bias_grad(dpre, s.ldp, s.M, 2 * s.F, s.t, gr.b1, s.grad_t, s.accumulate, part, tmp, st));
-    if (gr.b2)
-      OASES_TRY(bias_grad(dy, s.H, s.M, s.H, s.t, gr.b2, s.grad_t, s.accumulate, part, tmp, st));
-    return cudaSuccess;
-  }
   const Sums q{{dpre, dy}, {gr.b1, gr.b2}, {gr.b1 ? 2 * s.F : 0, gr.b2 ? s.H : 0},
                {s.ldp, s.H}};
   const int per = s.t == DType::F32 ? 8 : 64, acc = s.accumulate ? 1 : 0;
@@ -336,8 +299,7 @@ cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
                              {(float*)gr.w2, s.F, nullptr, nullptr, nullptr, acc}};
     OASES_TRY(f32::launch_group(args, out, {true, false, false}, st));
   }
-  return bias_grads(s, dpre, dy, gr, reinterpret_cast<float*>(ws + l.part),
-                    reinterpret_cast<float*>(ws + l.bias), st);
+  return bias_grads(s, dpre, dy, gr, st);
 }
 
 bool misaligned(std::initializer_list<const void*> ps) {
