@@ -87,6 +87,7 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   __syncthreads();
   return v;
 }
+
 constexpr float LOG2E = 1.4426950408889634f;
 
 // fp32 forward: a row's 64 columns, four per thread of sixteen, to (r, s) as in

@@ -1,15 +1,13 @@
 // Gated feed-forward block (oases_glu.h):
 //   a = x Wg^T + bg, b = x Wu^T + bu, h = act(a) b, y = h W2^T + b2 (+ resid)
-// and its backward.  bf16 runs on the fused tensor-core kernels of glu_tc.cu and
-// glu_few.cu, fp32 on the CUDA-core GEMM with the same epilogues.
+// and its backward.  bf16 runs on the fused tensor-core kernels of glu_tc.cu,
+// glu_few.cu and glu_again.cu, fp32 on the CUDA-core GEMM with the same epilogues.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
 #include "gemm_f32.cuh"
 #include "glu.cuh"
-#include "mx_block.cuh"
-#include "oases_mx.h"
 
 namespace oases {
 void api_begin();

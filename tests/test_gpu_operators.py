@@ -568,6 +568,33 @@ def test_repeated_calls_other_streams_and_captured_graphs_give_the_same_bits(M):
     oz.oases_check_device(torch.cuda.current_stream())
 
 
+def test_two_host_threads_on_their_own_streams():
+    import threading
+
+    jobs = []
+    for M in (5, 300):
+        x, w, _, _ = glu_case("bf16", M, 256, 512, True, False)
+        _, head, t, d = ce_case("bf16", M, 256, 1500, True)
+        jobs.append((x, w, head, t, d, [v.clone() for v in _chain(x, w, head, t, d)]))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(x, w, head, t, d, want):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = _chain(x, w, head, t, d)
+            torch.cuda.current_stream().synchronize()
+        wrong.extend(i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
+    oz.oases_check_device(None)
+
+
 def test_refusals_of_torch_arguments():
     x, w, r, dy = glu_case("bf16", 4, 64, 128, True, True)
     head, t = torch.randn(30, 64).bfloat16().cuda(), torch.zeros(4, dtype=torch.int64).cuda()
