@@ -26,8 +26,9 @@
  * inputs give identical bits.
  *
  * Targets.  A row whose target is ignore_index has loss 0 and no gradient (its
- * lse is written all the same).  A target outside [0, vocab) that is not
- * ignore_index is an error that only the device can see: that row's loss is
+ * lse is written all the same); its x counts in dw times 0, so an infinite or
+ * NaN one makes dw NaN, as in any product.  A target outside [0, vocab) that is
+ * not ignore_index is an error that only the device can see: that row's loss is
  * NaN, and so are its row of dx and all of dw.
  */
 #ifndef OASES_CE_H

@@ -261,7 +261,8 @@ def ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.T
     (1 / n for the mean over n rows with a loss).
 
     dw None: returned in x's type.  dw a float32 [vocab, hidden] tensor: it is
-    added to (+=) and returned.
+    added to (+=) and returned.  Ignored rows of x count in dw times 0: they must
+    be finite.
     """
     desc, n_ws, _ = _ce_plan(_sig(x), _sig(w), _sig(targets), _sig(lse), _sig(dloss), _sig(dw),
                              True, ignore_index)

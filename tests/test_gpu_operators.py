@@ -507,6 +507,36 @@ def test_ce_larger_sizes(M, H, V):
     _rms_close(dw, g.t() @ x.double(), 2.0 ** -8, "dw")
 
 
+@pytest.mark.parametrize("dtype,M,H,Fn", [("bf16", 1023, 8, 16), ("bf16", 1024, 16, 8), ("bf16", 2049, 72, 136),
+                                          ("bf16", 9001, 8, 64), ("f32", 1030, 3, 5), ("f32", 4097, 9, 40),
+                                          ("f32", 9001, 2, 2)])
+def test_glu_bias_gradients_of_many_rows_are_exact(dtype, M, H, Fn):
+    """Sums of small whole numbers, exact in any order: one row of w2 is not 0, so
+    |dh| <= 1, and a = 32, where the exact GeLU is a and its derivative 1, so
+    da = dh b and db = 32 dh."""
+    gen = torch.Generator().manual_seed(M + H)
+
+    def whole(lo, hi, *shape):
+        return torch.randint(lo, hi + 1, shape, generator=gen).to(T[dtype]).cuda()
+
+    x, dy = whole(-1, 1, M, H), whole(-1, 1, M, H)
+    w2 = torch.zeros(H, Fn, dtype=T[dtype], device="cuda")
+    w2[H - 1] = whole(-1, 1, Fn)
+    w = {"w1": whole(-1, 1, 2 * Fn, H), "w2": w2, "b1": whole(0, 0, 2 * Fn), "b2": whole(0, 0, H)}
+    b = whole(-3, 3, M, Fn)
+    saved = torch.cat([torch.full_like(b, 32.0), b], dim=1)
+    dh = dy[:, H - 1:].double() * w2[H - 1].double()
+    db1 = torch.cat([dh * b.double(), 32 * dh], dim=1).sum(0)
+    db2 = dy.double().sum(0)
+    prior = {k: whole(-5, 5, *w[k].shape).float() for k in ("b1", "b2")}
+    grads = {k: v.clone() for k, v in prior.items()}
+    F.glu_bwd(x, dy, w, act="gelu", save="pre", saved=saved, grads=grads, need_dx=False)
+    assert torch.equal(grads["b1"].double(), prior["b1"].double() + db1)
+    assert torch.equal(grads["b2"].double(), prior["b2"].double() + db2)
+    _, grads = F.glu_bwd(x, dy, w, act="gelu", save="pre", saved=saved)
+    assert torch.equal(grads["b1"], db1.to(T[dtype])) and torch.equal(grads["b2"], db2.to(T[dtype]))
+
+
 def test_empty_batches():
     for dtype in ("bf16", "f32"):
         x, w, _, dy = glu_case(dtype, 0, 64, 104, True, False)
