@@ -215,37 +215,36 @@ int fwd_rows(const CeShape& s) {
 }
 
 struct BwdPlan {
-  int piece, splits;
-  int64_t ld, slab;  // slab: floats between the partial dx of two splits
+  int piece, splits, dw_splits;  // columns of a piece, splits of dx and of dw
+  bool together;                 // dx and dw of a piece may share a launch
+  int64_t ld;
   size_t g, dx, total;
 };
-BwdPlan bwd_plan(const CeShape& s) {
+BwdPlan bwd_plan(const CeShape& s) {  // the same whichever gradients are wanted
   BwdPlan b;
   const int64_t fit = PIECE_BYTES / (2ll * s.M) / 256 * 256;
   const int pieces = (int)((s.V + std::max<int64_t>(fit, MIN_PIECE) - 1) / std::max<int64_t>(fit, MIN_PIECE));
   b.piece = pieces == 1 ? s.V : ((s.V + pieces - 1) / pieces + 255) / 256 * 256;
   b.ld = ((int64_t)b.piece + 63) / 64 * 64;  // rows on 128-byte lines
+  const int sizes[2][3] = {{s.M, s.H, b.piece}, {b.piece, s.H, s.M}};
+  int splits[2];
   // dx of few rows has few tiles, each a contraction over the whole vocabulary:
   // split over the SMs, up to 128 rows in a launch of its own (it reads w at
   // 5.5 TB/s; with dw's tiles, which only write, 49 x 2024 x 40704 took 95 us
   // against 30 + 61 apart)
-  b.splits = 1;
+  b.together = s.M > 128 && core::split_together(sizes);
+  core::splits_of(sizes, b.together, splits);
+  b.splits = pieces > 1 ? 1 : splits[0];  // a piece's dx is added to the others'
+  b.dw_splits = splits[1];
   if (pieces == 1 && s.M <= 128) {
     b.splits = std::max(1, std::min(core::sm_count() / ((s.H + 127) / 128), s.V / 512));
     core::slices_per_split(s.V, &b.splits);
-  } else if (pieces == 1) {
-    const int64_t k = (s.M + core::BKE - 1) / core::BKE + core::TILE_COST;
-    b.splits = core::dx_splits_of(s.M, s.H, s.V, core::tiles256(s.V, s.H) * k,
-                                  core::operand_bytes(s.M, s.H, s.V) + core::operand_bytes(s.V, s.H, s.M));
   }
-  b.slab = (int64_t)core::slab_rows(s.M) * s.H;
   b.g = 0;
   b.dx = align256((size_t)s.M * b.ld * 2);
   b.total = b.dx;
-  if (b.splits > 1)
-    b.total += align256((size_t)b.slab * 4 * b.splits);
-  else if (pieces > 1)
-    b.total += align256((size_t)s.M * s.H * 4);
+  if (pieces > 1) b.total += align256((size_t)s.M * s.H * 4);
+  b.total += core::slab_bytes(s.M, s.H, b.splits) + core::slab_bytes(b.piece, s.H, b.dw_splits);
   return b;
 }
 
@@ -312,47 +311,35 @@ cudaError_t ce_tc_bwd(const CeShape& s, const void* x, const void* w, const CeRo
       OASES_TRY(few ? (core::launch<EpiG, 128, true, true, 1>(o, e, st))
                     : (core::launch<EpiG, 256, true, true, 2>(o, e, st)));
     }
-    EpiOut::Params e_dx = {}, e_dw = {};
-    bool ok = true;
+    core::Product prod[2] = {{{s.M, s.H, n, g, b.ld, wp, s.H}, true},
+                             {{n, s.H, s.M, g, b.ld, x, s.H}, false}};
+    EpiOut::Params ep[2] = {};
+    core::Slabs slabs(dx32 + (b.piece < s.V ? align256((size_t)s.M * s.H * 4) / 4 : 0));
     if (dx) {
-      if (b.splits > 1) {
-        e_dx.slab_rows = (int)(b.slab / s.H);
-        ok = core::out_map(&e_dx, dx32, DType::F32, e_dx.slab_rows * b.splits, s.H, s.H);
-      } else if (last) {
-        ok = core::out_map(&e_dx, dx, DType::BF16, s.M, s.H, s.H);
-        e_dx.scale = rows.scale;
-        e_dx.prior = first ? nullptr : dx32;
+      if (last) {
+        ep[0].scale = rows.scale;
+        ep[0].prior = first ? nullptr : dx32;
       } else {
-        ok = core::out_map(&e_dx, dx32, DType::F32, s.M, s.H, s.H);
-        e_dx.accumulate = !first;
+        ep[0].accumulate = !first;
       }
+      if (!slabs.output(&prod[0].o, b.splits, &ep[0], last ? dx : dx32, last ? DType::BF16 : DType::F32))
+        return cudaErrorInvalidValue;
     }
     if (dw) {
       char* out = static_cast<char*>(dw) + (size_t)v0 * s.H * dtype_size(s.grad_t);
-      ok = ok && core::out_map(&e_dw, out, s.grad_t, n, s.H, s.H);
-      e_dw.scale = rows.scale;
-      e_dw.accumulate = s.accumulate;
+      ep[1].scale = rows.scale;
+      ep[1].accumulate = s.accumulate;
+      if (!slabs.output(&prod[1].o, b.dw_splits, &ep[1], out, s.grad_t)) return cudaErrorInvalidValue;
     }
-    if (!ok) return cudaErrorInvalidValue;
-    core::Operands o_dx{s.M, s.H, n, g, b.ld, wp, s.H};
-    o_dx.splits = b.splits;
-    const core::Operands o_dw{n, s.H, s.M, g, b.ld, x, s.H};
     bool taken = false;
-    if (dx && dw && !few) {
-      const core::Product prod[2] = {{o_dx, true}, {o_dw, false}};
-      const EpiOut::Params ep[2] = {e_dx, e_dw};
-      OASES_TRY((core::launch_group<EpiOut, 2>(prod, ep, &taken, st)));
-    }
+    if (b.together && dx && dw) OASES_TRY((core::launch_group<EpiOut, 2>(prod, ep, &taken, st)));
     if (!taken) {
       if (dx)
-        OASES_TRY(few ? (core::launch<EpiOut, 128, true, false, 1>(o_dx, e_dx, st))
-                      : (core::launch<EpiOut, 256, true, false, 2>(o_dx, e_dx, st)));
-      if (dw) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_dw, e_dw, st)));
+        OASES_TRY(few ? (core::launch<EpiOut, 128, true, false, 1>(prod[0].o, ep[0], st))
+                      : (core::launch<EpiOut, 256, true, false, 2>(prod[0].o, ep[0], st)));
+      if (dw) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(prod[1].o, ep[1], st)));
     }
-    if (dx && b.splits > 1) {
-      OASES_TRY(core::slab_sum(dx32, b.splits, b.slab, rows.scale, nullptr, nullptr, dx, DType::BF16, s.M,
-                               s.H, st));
-    }
+    OASES_TRY(slabs.sum(st));
   }
   return cudaSuccess;
 }

@@ -117,54 +117,96 @@ inline bool out_map(EpiOut::Params* e, void* c, DType t, int rows, int N, int64_
   return tensor_map(&e->c, c, e->f32 != 0, N, rows, ld, e->f32 ? 32 : 64, 32);
 }
 
-// out = scale * (sum of the splits' partial products, in their order) + bias +
-// resid, each optional; [rows, N] from slabs of [slab / N, N] fp32.
-template <typename T>
-__global__ void __launch_bounds__(256)
-slab_sum_kernel(const float* slabs, int splits, int64_t slab, const float* scale,
-                const __nv_bfloat16* bias, const __nv_bfloat16* resid, T* out, int64_t n, int N) {
+// The outputs of products whose contractions were split, in one launch (block row y
+// takes out y):  out (+)= scale * (sum of the splits' partial products, in their
+// order) + bias + resid, each optional; [rows, N] from slabs of [slab / N, N] fp32.
+struct SlabSum {
+  const float* slabs;
+  int splits;
+  int64_t slab;
+  const float* scale;
+  const __nv_bfloat16 *bias, *resid;
+  void* out;
+  int f32, accumulate;  // out's type: fp32, else bf16; += (fp32)
+  int64_t n;
+  int N;
+};
+struct SlabSums {
+  SlabSum q[3];
+};
+static __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSums all) {
   pdl_wait();
   pdl_trigger();
-  const float s = scale ? *scale : 1.f;
-  for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * 4; i < n;
+  const SlabSum q = all.q[blockIdx.y];
+  const float s = q.scale ? *q.scale : 1.f;
+  for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * 4; i < q.n;
        i += (int64_t)gridDim.x * blockDim.x * 4) {
     float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int z = 0; z < splits; ++z) {
-      const float4 q = *reinterpret_cast<const float4*>(slabs + z * slab + i);
-      a[0] += q.x;
-      a[1] += q.y;
-      a[2] += q.z;
-      a[3] += q.w;
+    for (int z = 0; z < q.splits; ++z) {
+      const float4 t = *reinterpret_cast<const float4*>(q.slabs + z * q.slab + i);
+      a[0] += t.x;
+      a[1] += t.y;
+      a[2] += t.z;
+      a[3] += t.w;
     }
-    const int c = (int)(i % N);  // N is a multiple of 8
+    const int c = (int)(i % q.N);  // N is a multiple of 8
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       a[k] *= s;
-      if (bias) a[k] += __bfloat162float(bias[c + k]);
-      if (resid) a[k] += __bfloat162float(resid[i + k]);
+      if (q.bias) a[k] += __bfloat162float(q.bias[c + k]);
+      if (q.resid) a[k] += __bfloat162float(q.resid[i + k]);
     }
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<uint2*>(out + i) = make_uint2(pack2(a[0], a[1]), pack2(a[2], a[3]));
-    else
-      *reinterpret_cast<float4*>(out + i) = make_float4(a[0], a[1], a[2], a[3]);
+    if (!q.f32) {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(q.out) + i) =
+          make_uint2(pack2(a[0], a[1]), pack2(a[2], a[3]));
+    } else {
+      float4* out = reinterpret_cast<float4*>(static_cast<float*>(q.out) + i);
+      if (q.accumulate) {
+        const float4 t = *out;
+        a[0] += t.x;
+        a[1] += t.y;
+        a[2] += t.z;
+        a[3] += t.w;
+      }
+      *out = make_float4(a[0], a[1], a[2], a[3]);
+    }
   }
 }
-inline cudaError_t slab_sum(const float* slabs, int splits, int64_t slab, const float* scale,
-                            const void* bias, const void* resid, void* out, DType t, int rows, int N,
-                            cudaStream_t st) {
-  const int64_t n = (int64_t)rows * N;
-  const dim3 grid((unsigned)std::min<int64_t>((n / 4 + 255) / 256, 152 * 8));
-  const __nv_bfloat16 *b = static_cast<const __nv_bfloat16*>(bias),
-                      *r = static_cast<const __nv_bfloat16*>(resid);
-  if (t == DType::F32)
-    return launch_pdl(slab_sum_kernel<float>, grid, dim3(256), 0, st, slabs, splits, slab, scale, b, r,
-                      static_cast<float*>(out), n, N);
-  return launch_pdl(slab_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, slabs, splits, slab, scale,
-                    b, r, static_cast<__nv_bfloat16*>(out), n, N);
-}
+
 // Rows of a slab: whole tiles, so that the rows of one never reach the next.
 inline int slab_rows(int rows) { return (rows + 255) / 256 * 256; }
+inline size_t slab_bytes(int rows, int N, int splits) {  // a multiple of 256: N of 8
+  return splits > 1 ? (size_t)slab_rows(rows) * N * 4 * splits : 0;
+}
+
+// The split products of an operator, summed by one launch at its end.
+struct Slabs {
+  SlabSums all = {};
+  int count = 0;
+  char* ws;  // slab_bytes() for each, in turn
+  explicit Slabs(void* p) : ws(static_cast<char*>(p)) {}
+  // Output [M, N] of o, contiguous, in o.splits parts or at once; the optional terms
+  // and `accumulate` are in e, and go to the sum where there are parts.
+  bool output(Operands* o, int splits, EpiOut::Params* e, void* out, DType t) {
+    o->splits = splits;
+    if (splits == 1) return out_map(e, out, t, o->M, o->N, o->N);
+    SlabSum& q = all.q[count++];
+    q = {reinterpret_cast<float*>(ws), splits, (int64_t)slab_rows(o->M) * o->N, e->scale, e->bias,
+         e->resid, out, t == DType::F32, e->accumulate, (int64_t)o->M * o->N, o->N};
+    ws += slab_bytes(o->M, o->N, splits);
+    *e = {};
+    e->slab_rows = slab_rows(o->M);
+    return out_map(e, const_cast<float*>(q.slabs), DType::F32, e->slab_rows * splits, o->N, o->N);
+  }
+  cudaError_t sum(cudaStream_t st) {
+    if (count == 0) return cudaSuccess;
+    int64_t n = 0;
+    for (int i = 0; i < count; ++i) n = std::max(n, all.q[i].n);
+    const dim3 grid((unsigned)std::min<int64_t>((n / 4 + 255) / 256, 152 * 8), (unsigned)count);
+    return launch_pdl(slab_sum_kernel, grid, dim3(256), 0, st, all);
+  }
+};
 
 // How a product [M, N] over K with few tiles is cut: columns per tile and splits
 // of the contraction, by the clocks of the longest path: a K-slice takes about
@@ -198,11 +240,31 @@ inline Cut cut_of(int M, int N, int K, int slots, bool narrow) {
   return best;
 }
 
-// Splits of dx [M, N] over K beside weight gradients of `other` K-slices of tiles;
-// bytes: the operands of all of them, as launch_group counts them.
-inline int dx_splits_of(int M, int N, int K, int64_t other, int64_t bytes) {
-  if (bytes > GROUP_BYTES) return cut_of(M, N, K, pair_count(), false).splits;
-  return even_splits(tiles256(M, N), K, other, pair_count());
+// Splits of the contractions of N products that belong together: sizes[i] = {M, N, K}.
+// In one launch where launch_group would take them (the operands stay in L2), no tile
+// longer than an even share; else each as it is best alone.  The weight gradients of
+// many rows and small weights are split too: 65536 x 512 x 1024 (dx, dw1, dw2) 625 ->
+// 230 us, 8000 x 256 x 512 the backward 50 -> 30, the head's at 65536 x 256 x 8000
+// 1176 -> 815.
+template <int N>
+bool split_together(const int (&sizes)[N][3]) {
+  int64_t bytes = 0;
+  for (const auto& q : sizes) bytes += operand_bytes(q[0], q[1], q[2]);
+  return bytes <= GROUP_BYTES;
+}
+template <int N>
+void splits_of(const int (&sizes)[N][3], bool together, int (&splits)[N]) {
+  int64_t slices[N], all = 0;
+  for (int i = 0; i < N; ++i) {
+    const int* q = sizes[i];
+    slices[i] = tiles256(q[0], q[1]) * ((q[2] + BKE - 1) / BKE + TILE_COST);
+    all += slices[i];
+  }
+  for (int i = 0; i < N; ++i) {
+    const int* q = sizes[i];
+    splits[i] = together ? even_splits(tiles256(q[0], q[1]), q[2], all - slices[i], pair_count())
+                         : cut_of(q[0], q[1], q[2], pair_count(), false).splits;
+  }
 }
 
 }  // namespace core

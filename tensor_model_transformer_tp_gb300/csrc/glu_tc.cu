@@ -341,12 +341,22 @@ namespace {
 
 using core::EpiOut;
 
-int dx_splits(const GluShape& s) {
-  const int64_t k = (s.M + core::BKE - 1) / core::BKE + core::TILE_COST, F2 = 2 * (int64_t)s.F;
-  return core::dx_splits_of(s.M, s.H, 2 * s.F, (core::tiles256(s.H, s.F) + core::tiles256(F2, s.H)) * k,
-                            core::operand_bytes(s.M, s.H, F2) + core::operand_bytes(s.H, s.F, s.M) +
-                                core::operand_bytes(F2, s.H, s.M));
-}
+// dx, dw2 and dw1 and the splits of their contractions, the same ones whichever of
+// them are wanted: a gradient does not depend on what else is asked for.
+struct GradSplits {
+  int sizes[3][3], splits[3];
+  bool together;
+  explicit GradSplits(const GluShape& s)
+      : sizes{{s.M, s.H, 2 * s.F}, {s.H, s.F, s.M}, {2 * s.F, s.H, s.M}} {
+    together = core::split_together(sizes);
+    core::splits_of(sizes, together, splits);
+  }
+  size_t bytes() const {
+    size_t n = 0;
+    for (int i = 0; i < 3; ++i) n += core::slab_bytes(sizes[i][0], sizes[i][1], splits[i]);
+    return n;
+  }
+};
 
 #define OASES_TRY(expr)                       \
   do {                                        \
@@ -356,75 +366,53 @@ int dx_splits(const GluShape& s) {
 
 }  // namespace
 
-size_t glu_grads_tc_bytes(const GluShape& s) {
-  const int splits = dx_splits(s);
-  return splits > 1 ? align256((size_t)core::slab_rows(s.M) * s.H * 4 * splits) : 0;
-}
+size_t glu_grads_tc_bytes(const GluShape& s) { return GradSplits(s).bytes(); }
 
 cudaError_t glu_grads_tc(const GluShape& s, const void* x, const void* dy, const void* w1,
                          const void* dpre, const void* h, void* dx, void* dw1, void* dw2, char* ws,
                          cudaStream_t st) {
-  core::Operands o_dx{s.M, s.H, 2 * s.F, dpre, s.ldp, w1, s.H};
-  const core::Operands o_w2{s.H, s.F, s.M, dy, s.H, h, s.ldh};
-  const core::Operands o_w1{2 * s.F, s.H, s.M, dpre, s.ldp, x, s.H};
-  EpiOut::Params e_dx = {}, e_w1 = {}, e_w2 = {};
-  e_w1.accumulate = e_w2.accumulate = s.accumulate;
-  const int splits = dx ? dx_splits(s) : 1;
-  const int64_t slab = (int64_t)core::slab_rows(s.M) * s.H;
-  bool ok = true;
-  if (dw1) ok = core::out_map(&e_w1, dw1, s.grad_t, 2 * s.F, s.H, s.H);
-  if (dw2) ok = ok && core::out_map(&e_w2, dw2, s.grad_t, s.H, s.F, s.F);
-  if (dx && splits > 1) {
-    o_dx.splits = splits;
-    e_dx.slab_rows = core::slab_rows(s.M);
-    ok = ok && core::out_map(&e_dx, ws, DType::F32, e_dx.slab_rows * splits, s.H, s.H);
-  } else if (dx) {
-    ok = ok && core::out_map(&e_dx, dx, s.dx_t, s.M, s.H, s.H);
+  core::Product prod[3] = {{{s.M, s.H, 2 * s.F, dpre, s.ldp, w1, s.H}, true},
+                           {{s.H, s.F, s.M, dy, s.H, h, s.ldh}, false},
+                           {{2 * s.F, s.H, s.M, dpre, s.ldp, x, s.H}, false}};
+  EpiOut::Params ep[3] = {};
+  void* const out[3] = {dx, dw2, dw1};
+  const GradSplits g(s);
+  core::Slabs slabs(ws);
+  for (int i = 0; i < 3; ++i) {
+    ep[i].accumulate = i > 0 && s.accumulate;
+    if (out[i] && !slabs.output(&prod[i].o, g.splits[i], &ep[i], out[i], i > 0 ? s.grad_t : s.dx_t))
+      return cudaErrorInvalidValue;
   }
-  if (!ok) return cudaErrorInvalidValue;
   bool taken = false;
-  if (dw1 && dw2 && dx) {
-    const core::Product prod[3] = {{o_dx, true}, {o_w2, false}, {o_w1, false}};
-    const EpiOut::Params ep[3] = {e_dx, e_w2, e_w1};
+  if (g.together && dx && dw1 && dw2)
     OASES_TRY((core::launch_group<EpiOut, 3>(prod, ep, &taken, st)));
-  }
   if (!taken) {
-    if (dw2) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_w2, e_w2, st)));
-    if (dw1) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(o_w1, e_w1, st)));
-    if (dx) OASES_TRY((core::launch<EpiOut, 256, true, false, 2>(o_dx, e_dx, st)));
+    if (dw2) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(prod[1].o, ep[1], st)));
+    if (dw1) OASES_TRY((core::launch<EpiOut, 256, false, false, 2>(prod[2].o, ep[2], st)));
+    if (dx) OASES_TRY((core::launch<EpiOut, 256, true, false, 2>(prod[0].o, ep[0], st)));
   }
-  if (dx && splits > 1)
-    OASES_TRY(core::slab_sum(reinterpret_cast<const float*>(ws), splits, slab, nullptr, nullptr, nullptr,
-                             dx, s.dx_t, s.M, s.H, st));
-  return cudaSuccess;
+  return slabs.sum(st);
 }
 
 size_t glu_down_tc_bytes(const GluShape& s) {
   if (s.M <= GLU_FEW_ROWS) return 0;
-  const core::Cut c = core::cut_of(s.M, s.H, s.F, core::pair_count(), true);
-  return c.splits > 1 ? align256((size_t)core::slab_rows(s.M) * s.H * 4 * c.splits) : 0;
+  return core::slab_bytes(s.M, s.H, core::cut_of(s.M, s.H, s.F, core::pair_count(), true).splits);
 }
 
 cudaError_t glu_down_tc(const GluShape& s, const void* h, const void* w2, const void* b2,
                         const void* resid, void* y, char* ws, cudaStream_t st) {
   if (s.M <= GLU_FEW_ROWS) return glu_down_few(s, h, w2, b2, resid, y, st);
   const core::Cut c = core::cut_of(s.M, s.H, s.F, core::pair_count(), true);
-  EpiOut::Params e = {};
   core::Operands o{s.M, s.H, s.F, h, s.ldh, w2, s.F};
-  if (c.splits > 1) {
-    o.splits = c.splits;
-    e.slab_rows = core::slab_rows(s.M);
-    if (!core::out_map(&e, ws, DType::F32, e.slab_rows * c.splits, s.H, s.H)) return cudaErrorInvalidValue;
-    OASES_TRY((core::launch<EpiOut, 256, true, true, 2>(o, e, st)));
-    return core::slab_sum(reinterpret_cast<const float*>(ws), c.splits, (int64_t)e.slab_rows * s.H,
-                          nullptr, b2, resid, y, DType::BF16, s.M, s.H, st);
-  }
-  if (!core::out_map(&e, y, DType::BF16, s.M, s.H, s.H)) return cudaErrorInvalidValue;
+  EpiOut::Params e = {};
   e.bias = static_cast<const __nv_bfloat16*>(b2);
   e.resid = static_cast<const __nv_bfloat16*>(resid);
+  core::Slabs slabs(ws);
+  if (!slabs.output(&o, c.splits, &e, y, DType::BF16)) return cudaErrorInvalidValue;
   if (c.bn == 128) return core::launch<EpiOut, 128, true, true, 2>(o, e, st);
   if (c.bn == 192) return core::launch<EpiOut, 192, true, true, 2>(o, e, st);
-  return core::launch<EpiOut, 256, true, true, 2>(o, e, st);
+  OASES_TRY((core::launch<EpiOut, 256, true, true, 2>(o, e, st)));
+  return slabs.sum(st);
 }
 
 int glu_read_and_clear_error() {

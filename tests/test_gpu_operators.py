@@ -181,7 +181,7 @@ def test_glu_forward_and_backward(dtype, M, H, Fn, act, save, bias, resid):
 
 
 @pytest.mark.parametrize("dtype,M,H,Fn", [("bf16", 140, 136, 264), ("f32", 9, 40, 50),
-                                          ("bf16", 3, 512, 256)])
+                                          ("bf16", 3, 512, 256), ("bf16", 5003, 72, 136)])
 def test_glu_accumulated_fp32_gradients(dtype, M, H, Fn):
     """grads given: fp32, added to, the same sums as written gradients; a subset
     leaves the others out; dx as fp32."""
@@ -335,7 +335,8 @@ def test_ce_forward_and_backward(dtype, M, H, V, per_row):
         assert loss[1] == 0 and not dx[1].any()
 
 
-@pytest.mark.parametrize("dtype,M,H,V", [("bf16", 70, 136, 900), ("f32", 11, 30, 100)])
+@pytest.mark.parametrize("dtype,M,H,V", [("bf16", 70, 136, 900), ("f32", 11, 30, 100),
+                                         ("bf16", 5003, 72, 300)])
 def test_ce_accumulated_fp32_gradient(dtype, M, H, V):
     x, w, t, d = ce_case(dtype, M, H, V, True)
     _, lse = F.ce_fwd(x, w, t)
@@ -460,7 +461,8 @@ def _rms_close(got, want, rel, what):
 
 
 @pytest.mark.parametrize("M,H,Fn,save", [(4096, 1024, 6000, "mxfp8"), (3000, 2048, 5464, "pre"),
-                                         (8200, 512, 1032, "none")])
+                                         (8200, 512, 1032, "none"), (40000, 264, 520, "pre"),
+                                         (12001, 256, 136, "mxfp8")])
 def test_glu_larger_sizes(M, H, Fn, save):
     """Products that take several launches or share one, on float64 products of
     the same roundings' size: kept and intermediate values carry up to three bf16
@@ -486,7 +488,7 @@ def test_glu_larger_sizes(M, H, Fn, save):
 
 
 @pytest.mark.parametrize("M,H,V", [(8000, 256, 20001), (300, 512, 60000), (4096, 1024, 33000),
-                                   (2000, 128, 100)])
+                                   (2000, 128, 100), (30001, 264, 1000), (40000, 72, 9000)])
 def test_ce_larger_sizes(M, H, V):
     """Several pieces of the vocabulary (8000 x 20001 logits), split contractions
     and products that share a launch or do not."""
