@@ -25,8 +25,9 @@
  * is enqueued, calls are asynchronous on `stream` (one stream), identical
  * inputs give identical bits.
  *
- * Targets.  A row whose target is ignore_index has loss 0 and no gradient (its
- * lse is written all the same); its x counts in dw times 0, so an infinite or
+ * Targets.  A row whose target is ignore_index has loss 0 and no gradient, also
+ * where a dloss given for every row is infinite or NaN (its lse is written all
+ * the same); its x counts in dw times 0, so an infinite or
  * NaN one makes dw NaN, as in any product.  A target outside [0, vocab) that is
  * not ignore_index is an error that only the device can see: that row's loss is
  * NaN, and so are its row of dx and all of dw.

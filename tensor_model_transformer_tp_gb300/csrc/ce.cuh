@@ -21,7 +21,10 @@ struct CeShape {
 // the dloss given for all rows, or the largest finite |dloss| of the rows that
 // have a loss, so r is at most 1 in magnitude, and exactly 1 where the rows share one
 // dloss: the products then see entries of g / s such as the target's, close to
-// -1, that do not depend on how dloss itself rounds to the storage type.
+// -1, that do not depend on how dloss itself rounds to the storage type.  A dloss
+// given for all rows that is infinite or NaN (the mean over no rows: 1 / 0) is r of
+// the rows with a loss instead, and s counts as 1 (product_factor): rows without a
+// loss keep their 0.
 struct CeRows {
   const int64_t* target;
   const float* dloss;
@@ -32,9 +35,12 @@ struct CeRows {
 __device__ __forceinline__ float row_factor(const CeRows& c, int64_t t, int m) {
   if (t == c.ignore) return 0.f;
   if (t < 0 || t >= c.V) return CUDART_NAN_F;
-  if (!c.per_row) return 1.f;
+  if (!c.per_row) {
+    const float d = *c.dloss;
+    return fabsf(d) < INFINITY ? 1.f : d;
+  }
   const float d = c.dloss[m], s = *c.scale;
-  return s == 0.f ? d : d / s;  // s == 0: d is 0 or NaN
+  return s == 0.f ? d : d / s;  // s == 0: d is 0, infinite or NaN
 }
 __device__ __forceinline__ float row_loss(int64_t t, int64_t ignore, int V, float lse, float at) {
   return t == ignore ? 0.f : t < 0 || t >= V ? CUDART_NAN_F : lse - at;

@@ -99,6 +99,14 @@ __device__ __forceinline__ void store_any(void* p, DType t, int64_t i, float v) 
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
+// The factor that an epilogue applies to a product: *s, 1 where there is none.  One
+// that is not finite is left to the product's operand, where it meets only the rows
+// it belongs to: 0 times it would be NaN in the others.
+__device__ __forceinline__ float product_factor(const float* s) {
+  const float v = s ? *s : 1.f;
+  return fabsf(v) < INFINITY ? v : 1.f;
+}
+
 // GeLU in its exact form a * Phi(a), Phi the standard normal CDF, and its
 // derivative Phi(a) + a * phi(a), phi the standard normal density.
 //

@@ -14,7 +14,7 @@ struct EpiOut {
     CUtensorMap c;             // boxes of 32 rows x 128 bytes of C
     int f32;                   // C's type: fp32, else bf16
     int accumulate;            // C (fp32) += by TMA reduction
-    const float* scale;        // one device value, or null (1)
+    const float* scale;        // one device value (product_factor), or null
     const float* prior;        // fp32 [M, N], leading dimension N
     const __nv_bfloat16* bias;  // [N]
     const __nv_bfloat16* resid;  // [M, N]
@@ -24,7 +24,7 @@ struct EpiOut {
     float alpha;
     template <int BN>
     __device__ __forceinline__ void before(const Params& e, const Problem&, int, int, int) {
-      alpha = e.scale ? *e.scale : 1.f;
+      alpha = product_factor(e.scale);
     }
     // CW accumulator columns from n, this lane's row m
     template <int CW>
@@ -138,7 +138,7 @@ static __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSums all
   pdl_wait();
   pdl_trigger();
   const SlabSum q = all.q[blockIdx.y];
-  const float s = q.scale ? *q.scale : 1.f;
+  const float s = product_factor(q.scale);
   for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * 4; i < q.n;
        i += (int64_t)gridDim.x * blockDim.x * 4) {
     float a[4] = {0.f, 0.f, 0.f, 0.f};

@@ -248,7 +248,7 @@ struct Out {
   int accumulate;
   __device__ __forceinline__ void tile(int m, int n0, const float (&v)[4], int col, int M, int N) const {
     if (m >= M) return;
-    const float s = scale ? *scale : 1.f;
+    const float s = product_factor(scale);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = n0 + col + i;
