@@ -56,10 +56,17 @@ def _match(name: str, sig, shape: tuple, dtype: torch.dtype, device) -> None:
         raise ValueError("%s is on device %d, x on %d" % (name, sig[2], device))
 
 
+def _fits(**sizes: int) -> None:
+    """The descriptors hold 32-bit sizes, which ctypes would cut off in silence."""
+    for name, n in sizes.items():
+        _need(n < 1 << 31, "%s is %d, beyond 2^31 - 1" % (name, n))
+
+
 def _rows(x) -> Tuple[int, int]:
     _need(x is not None and len(x[0]) == 2, "x must be a [rows, hidden] tensor")
     _need(x[1] in _CODE, "x must be float32 or bfloat16, got %s" % (x[1],))
     _need(x[2] >= 0, "x must be on a CUDA device")
+    _fits(rows=x[0][0], hidden=x[0][1])
     return x[0][0], x[0][1]
 
 
@@ -100,6 +107,7 @@ def _glu_shapes(x, w):
     _need(w[0] is not None and w[2] is not None, "weights needs w1 and w2")
     _need(len(w[2][0]) == 2, "w2 must be [hidden, ffn]")
     ffn = w[2][0][1]
+    _fits(ffn=ffn)
     shapes = {"w1": (2 * ffn, hidden), "b1": (2 * ffn,), "w2": (hidden, ffn), "b2": (hidden,)}
     for name, sig in zip(_NAMES, w):
         if sig is not None:
@@ -220,6 +228,8 @@ def _ce_plan(x, w, targets, lse, dloss, dw, backward, ignore_index):
     rows, hidden = _rows(x)
     _need(w is not None and len(w[0]) == 2 and w[0][0] > 0, "w must be a [vocab, hidden] tensor")
     vocab = w[0][0]
+    _fits(vocab=vocab)
+    _need(-1 << 63 <= ignore_index < 1 << 63, "ignore_index must be a 64-bit integer")
     _match("w", w, (vocab, hidden), x[1], x[2])
     _match("targets", targets, (rows,), torch.int64, x[2])
     t, per_row, accumulate = _CODE[x[1]], False, dw is not None
