@@ -40,6 +40,7 @@ struct Few {
 struct FewArgs {
   int M, N, K;        // rows, outputs per row (ffn or hidden), contraction
   int kbs;            // K-slices per CTA of the cluster
+  int split;          // CTAs of a cluster; the clusters follow one another in gridDim.x
   int act, keep;
   const __nv_bfloat16 *bias, *resid;
   __nv_bfloat16 *out;   // h [M, N] or y [M, N]
@@ -70,8 +71,8 @@ glu_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
   auto empty = [&](int s) { return bars + 8u * (C::STAGES + s); };
   const uint32_t done = bars + 8u * (2 * C::STAGES), tslot = done + 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int S = gridDim.x, rank = blockIdx.x;  // the cluster spans gridDim.x
-  const int n0 = blockIdx.y * (UP ? 64 : 128);
+  const int S = g.split, rank = (int)blockIdx.x % S;
+  const int n0 = (int)blockIdx.x / S * (UP ? 64 : 128);
   const int nkb = (g.K + BKE - 1) / BKE;
   const int kb0 = min(nkb, rank * g.kbs), n = min(nkb, kb0 + g.kbs) - kb0;
 
@@ -261,6 +262,7 @@ cudaError_t launch_few(FewArgs g, const void* w, const void* x, int tiles, cudaS
     return cudaErrorInvalidValue;
   const int nkb = (g.K + BKE - 1) / BKE, S = few_split(tiles, nkb);
   g.kbs = (nkb + S - 1) / S;
+  g.split = S;
   auto kern = glu_few_kernel<NT, UP>;
   static DeviceOnce attr;
   const cudaError_t ea = attr.run([&] {
@@ -268,7 +270,7 @@ cudaError_t launch_few(FewArgs g, const void* w, const void* x, int tiles, cudaS
   });
   if (ea != cudaSuccess) return ea;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(S, tiles);
+  cfg.gridDim = dim3((unsigned)S * tiles);  // x: wide weights have more than 65535 tiles
   cfg.blockDim = dim3(NTHREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;

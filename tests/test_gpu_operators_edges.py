@@ -53,3 +53,44 @@ def test_ce_non_finite_dloss_of_all_rows_stays_in_the_rows_with_a_loss(dtype, M,
     assert not dx.any() and not dw.any()
     dx, _ = F.ce_bwd(x, w, none, lse, d, dw=acc)
     assert not dx.any() and torch.equal(acc, start)
+
+
+# ---- few rows and more weight rows than a grid's second dimension has tiles ------
+def block_64(x, w, dy):
+    """(y, dx, dw1, dw2) of the block (SiLU, no biases) in float64."""
+    x, w1, w2, dy = x.double(), w["w1"].double(), w["w2"].double(), dy.double()
+    Fn = w2.shape[1]
+    p = x @ w1.t()
+    a, b = p[:, :Fn], p[:, Fn:]
+    s = torch.sigmoid(a)
+    h, dh = a * s * b, dy @ w2
+    dp = torch.cat([dh * b * s * (1 + a * (1 - s)), dh * a * s], dim=1)
+    return h @ w2.t(), dp @ w1, dp.t() @ x, dy.t() @ h
+
+
+@pytest.mark.parametrize("save", ["none", "pre", "mxfp8"])
+@pytest.mark.parametrize("H,Fn", [(8, 65536 * 64 - 56), (65535 * 128 + 8, 8)])
+def test_glu_few_rows_of_very_wide_weights(H, Fn, save):
+    """65536 tiles of 64 columns of ffn, and 65536 of 128 of hidden; as with 129
+    rows, to two bf16 roundings (h, and y itself) of 2^-9 rms each.  The gradients
+    rest on a, b and dh, sums over hidden in one chain of hidden / 16 matrix
+    instructions: each drops what is below the accumulator's last bit, up to 2^-23 of
+    a partial sum, and the partial sums of independent terms are in the mean square
+    no larger than the whole one.  So the three factors are off by hidden / 16 2^-23
+    each at most (1/16 at hidden 8388488, nothing at hidden 8)."""
+    gen = torch.Generator(device="cuda").manual_seed(H)
+
+    def rnd(*shape, std=1.0):
+        return (torch.randn(*shape, generator=gen, device="cuda") * std).bfloat16()
+
+    x, dy = rnd(2, H), rnd(2, H)
+    w = {"w1": rnd(2 * Fn, H, std=H ** -0.5), "w2": rnd(H, Fn, std=Fn ** -0.5)}
+    y, saved = F.glu_fwd(x, w, save=save)
+    oz.oases_check_device(torch.cuda.current_stream())
+    want, wdx, wdw1, wdw2 = block_64(x, w, dy)
+    assert float((y.double() - want).norm() / want.norm()) <= 2.0 ** -8
+    if save != "none":
+        return      # the kept values and the backward pass at them: the same kernels at any size
+    dx, grads = F.glu_bwd(x, dy, w, save=save, saved=saved)
+    for got, ref in ((dx, wdx), (grads["w1"], wdw1), (grads["w2"], wdw2)):
+        assert float((got.double() - ref).norm() / ref.norm()) <= 2.0 ** -8 + 3 * H / 16 * 2.0 ** -23
