@@ -324,13 +324,14 @@ inline void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attrs, dim3 
   ++g_launch_count;
 }
 
+// split: CTAs per contraction, 0: as is best for a launch of its own.
 template <class Epi, bool A_K, bool B_K>
-cudaError_t launch(Args g, const Epi& e, cudaStream_t st) {
+cudaError_t launch(Args g, const Epi& e, cudaStream_t st, int split = 0) {
   constexpr int TN = Epi::DUAL ? BN / 2 : BN;
   if (g.M == 0 || g.N == 0) return cudaSuccess;
   const int64_t tm = (g.M + BM - 1) / BM, tn = (g.N + TN - 1) / TN;
   if (tm > 65535 || tn > 65535) return cudaErrorInvalidConfiguration;
-  const int S = split_of(tm * tn * ((g.K + BK - 1) / BK), g.K);
+  const int S = split ? split : split_of(tm * tn * ((g.K + BK - 1) / BK), g.K);
   g.kspan = span_of(g.K, S);
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attrs[2];
@@ -341,16 +342,19 @@ cudaError_t launch(Args g, const Epi& e, cudaStream_t st) {
 }
 
 // Up to three products with MN-major B; those with no output (e.c null) are left out.
+// The contractions are split as if none were: a product's bits do not depend on
+// which others are wanted.
 static inline cudaError_t launch_group(const Args (&g)[3], const Out (&e)[3], const bool (&a_k)[3],
                                 cudaStream_t st) {
   Group q = {};
   int n = 0;
   int64_t tiles[3], steps = 0;
   for (int i = 0; i < 3; ++i) {
-    if (!e[i].c || g[i].M == 0 || g[i].N == 0) continue;
+    if (g[i].M == 0 || g[i].N == 0) continue;
     const int64_t tm = (g[i].M + BM - 1) / BM, tn = (g[i].N + BN - 1) / BN;
+    steps += tm * tn * ((g[i].K + BK - 1) / BK);
+    if (!e[i].c) continue;
     tiles[n] = tm * tn;
-    steps += tiles[n] * ((g[i].K + BK - 1) / BK);
     q.g[n] = g[i];
     q.e[n] = e[i];
     q.a_k[n] = a_k[i];
@@ -373,8 +377,8 @@ static inline cudaError_t launch_group(const Args (&g)[3], const Out (&e)[3], co
   }
   if (clusters > 65535) {  // more than a grid dimension holds
     for (int i = 0; i < n; ++i) {
-      const cudaError_t err = q.a_k[i] ? launch<Out, true, false>(q.g[i], q.e[i], st)
-                                       : launch<Out, false, false>(q.g[i], q.e[i], st);
+      const cudaError_t err = q.a_k[i] ? launch<Out, true, false>(q.g[i], q.e[i], st, q.split[i])
+                                       : launch<Out, false, false>(q.g[i], q.e[i], st, q.split[i]);
       if (err != cudaSuccess) return err;
     }
     return cudaSuccess;

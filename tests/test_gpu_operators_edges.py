@@ -94,3 +94,45 @@ def test_glu_few_rows_of_very_wide_weights(H, Fn, save):
     dx, grads = F.glu_bwd(x, dy, w, save=save, saved=saved)
     for got, ref in ((dx, wdx), (grads["w1"], wdw1), (grads["w2"], wdw2)):
         assert float((got.double() - ref).norm() / ref.norm()) <= 2.0 ** -8 + 3 * H / 16 * 2.0 ** -23
+
+
+# ---- a gradient does not depend on which others are wanted ------------------------
+@pytest.mark.parametrize("dtype,M,H,Fn", [("f32", 256, 256, 1024), ("f32", 100, 520, 2048),
+                                          ("f32", 2000, 64, 96), ("bf16", 256, 256, 1024),
+                                          ("bf16", 3000, 136, 264)])
+def test_glu_gradients_are_the_same_bits_whichever_are_wanted(dtype, M, H, Fn):
+    gen = torch.Generator().manual_seed(M + H)
+
+    def rnd(*shape, std=1.0):
+        return (torch.randn(*shape, generator=gen) * std).to(T[dtype]).cuda()
+
+    x, dy = rnd(M, H), rnd(M, H)
+    w = {"w1": rnd(2 * Fn, H, std=H ** -0.5), "w2": rnd(H, Fn, std=Fn ** -0.5), "b1": rnd(2 * Fn),
+         "b2": rnd(H)}
+    _, saved = F.glu_fwd(x, w, save="pre")
+
+    def run(names, need_dx):
+        grads = {k: torch.zeros_like(w[k], dtype=torch.float32) for k in names}
+        dx, _ = F.glu_bwd(x, dy, w, save="pre", saved=saved, grads=grads, need_dx=need_dx)
+        return dx, grads
+
+    dx0, all_ = run(sorted(w), True)
+    for n in range(len(w) + 1):
+        for names in itertools.combinations(sorted(w), n):
+            for need_dx in (False, True):
+                dx, grads = run(names, need_dx)
+                assert dx is None or torch.equal(dx, dx0), (names, need_dx)
+                for k in names:
+                    assert torch.equal(grads[k], all_[k]), (k, names, need_dx)
+
+
+@pytest.mark.parametrize("dtype,M,H,V", [("f32", 250, 256, 1003), ("f32", 512, 512, 3000),
+                                         ("f32", 60, 1024, 5000), ("bf16", 250, 256, 1003),
+                                         ("bf16", 2500, 72, 3000)])
+def test_ce_gradients_are_the_same_bits_whichever_are_wanted(dtype, M, H, V):
+    x, w, t = ce_tensors(dtype, M, H, V)
+    d = torch.full((1,), 1.0 / M, device="cuda")
+    _, lse = F.ce_fwd(x, w, t)
+    dx0, dw0 = F.ce_bwd(x, w, t, lse, d)
+    assert torch.equal(F.ce_bwd(x, w, t, lse, d, need_dw=False)[0], dx0)
+    assert torch.equal(F.ce_bwd(x, w, t, lse, d, need_dx=False)[1], dw0)
