@@ -88,10 +88,8 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return v;
 }
 
-constexpr float LOG2E = 1.4426950408889634f;
-
 // fp32 forward: a row's 64 columns, four per thread of sixteen, to (r, s) as in
-// ce_tc.cu: the maximum in base-2 units and the sum of 2^(l log2 e - r).
+// ce_tc.cu: the maximum and the sum of e^(l - r).
 struct StatF32 {
   static constexpr bool DUAL = false;
   float2* part;
@@ -101,13 +99,13 @@ struct StatF32 {
     float r = -INFINITY, s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n0 + col + i < N) r = fmaxf(r, v[i] * LOG2E);
+      if (n0 + col + i < N) r = fmaxf(r, v[i]);
 #pragma unroll
     for (int o = 8; o; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
     const float ref = r == -INFINITY ? 0.f : r;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n0 + col + i < N) s += exp2f(fmaf(v[i], LOG2E, -ref));
+      if (n0 + col + i < N) s += expf(v[i] - ref);
 #pragma unroll
     for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (m >= M) return;

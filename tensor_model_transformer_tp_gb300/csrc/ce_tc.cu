@@ -11,7 +11,7 @@ using core::Problem;
 using core::WarpBase;
 using core::pack2;
 
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
+constexpr float LOG2E = 1.4426950408889634f;
 constexpr int64_t PART_BYTES = 256ll << 20;   // partial maxima and sums of the forward
 // g of one piece of the backward.  A piece's dx is added to the others' in fp32,
 // so pieces are long; 8192 x 50304 x 2560 takes 3.60 ms with 64 MB, 3.50 with 128,
@@ -32,9 +32,11 @@ __device__ __forceinline__ float ex2(float x) {
 // hidden 1024, hide behind the next tile's main loop); few rows by reading w:
 // 37 x 50257 x 1024 in 19 us, 5.5 TB/s with the join.
 // Each warp reduces its half of a tile's columns of its 32 rows, one row per
-// lane, to (r, s): r the maximum of the logits in base-2 units (l log2 e), s
-// the sum of 2^(l log2 e - r); -inf and 0 where every logit is -inf.  The
-// target's logit goes out as it is met.
+// lane, to (r, s): r the maximum of the logits, s the sum of e^(l - r) as
+// 2^((l - r) log2 e); -inf and 0 where every logit is -inf.  The target's logit
+// goes out as it is met.  The maximum is a logit as it is, not one rounded to
+// base-2 units, and its own term is 1: so s >= 1, lse = r + log s is no less than
+// any logit, and the loss of a row whose target has all the weight is 0.
 struct EpiStat {
   static constexpr bool DUAL = false, PAD_ROWS = false;
   static constexpr int STG = 1024, WBARS = 0;  // unused
@@ -82,15 +84,15 @@ struct EpiStat {
         for (int k = 0; k < 4; ++k) mx[k] = v[k];
 #pragma unroll
         for (int i = 4; i < 64; ++i) mx[i % 4] = fmaxf(mx[i % 4], v[i]);
-        const float top = fmaxf(r, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * LOG2E);
+        const float top = fmaxf(r, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         const float ref = top == -INFINITY ? 0.f : top;
-        s *= ex2(r - ref);
+        s *= ex2((r - ref) * LOG2E);
         r = top;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         const uint64_t l2 = f2_splat(LOG2E), nr = f2_splat(-ref);
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {
-          const uint64_t q = f2_fma(f2_pack(v[i], v[i + 1]), l2, nr);
+          const uint64_t q = f2_mul(f2_add(f2_pack(v[i], v[i + 1]), nr), l2);
           sum[i % 4] += ex2(f2_lo(q));
           sum[i % 4 + 1] += ex2(f2_hi(q));
         }
@@ -115,7 +117,7 @@ ce_join_kernel(const float2* part, int slots, const float* at, const int64_t* ta
   float r = -INFINITY, s = 0.f;
   auto join = [&](float2 q) {
     const float top = fmaxf(r, q.x), ref = top == -INFINITY ? 0.f : top;
-    s = s * exp2f(r - ref) + q.y * exp2f(q.x - ref);
+    s = s * exp2f((r - ref) * LOG2E) + q.y * exp2f((q.x - ref) * LOG2E);
     r = top;
   };
   if (m < M) {
@@ -132,7 +134,7 @@ ce_join_kernel(const float2* part, int slots, const float* at, const int64_t* ta
     }
   }
   if (y == 0 && m < M) {
-    const float l = ((r == -INFINITY ? 0.f : r) + log2f(s)) * LN2;
+    const float l = (r == -INFINITY ? 0.f : r) + logf(s);
     lse[m] = l;
     const int64_t t = target[m];
     loss[m] = row_loss(t, ignore, V, l, t >= 0 && t < V ? at[m] : 0.f);

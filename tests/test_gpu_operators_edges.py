@@ -136,3 +136,51 @@ def test_ce_gradients_are_the_same_bits_whichever_are_wanted(dtype, M, H, V):
     dx0, dw0 = F.ce_bwd(x, w, t, lse, d)
     assert torch.equal(F.ce_bwd(x, w, t, lse, d, need_dw=False)[0], dx0)
     assert torch.equal(F.ce_bwd(x, w, t, lse, d, need_dx=False)[1], dw0)
+
+
+# ---- rows whose probability is all at one column ----------------------------------
+CE_ONE = [("bf16", 5, 64), ("bf16", 300, 72), ("f32", 5, 33), ("f32", 130, 64)]
+
+
+@pytest.mark.parametrize("dtype,M,H", CE_ONE)
+def test_ce_vocabulary_of_one(dtype, M, H):
+    """The softmax of one logit is 1: no loss, and lse is the logit (sums of
+    products of whole numbers, exact in fp32)."""
+    gen = torch.Generator().manual_seed(M)
+    x = torch.randint(-3, 4, (M, H), generator=gen).to(T[dtype]).cuda()
+    w = torch.randint(-60, 61, (1, H), generator=gen).to(T[dtype]).cuda()
+    t = torch.zeros(M, dtype=torch.int64, device="cuda")
+    loss, lse = F.ce_fwd(x, w, t)
+    assert not loss.any()
+    assert torch.equal(lse.double(), (x.double() @ w.double().t())[:, 0])
+
+
+@pytest.mark.parametrize("V", [2, 300, 1009])
+@pytest.mark.parametrize("dtype,M,H", CE_ONE)
+def test_ce_one_logit_far_above_the_others(dtype, M, H, V):
+    """Logits are whole numbers below 2^24; the target's is above the others by
+    1000 and more, so the others' share is below e^-1000."""
+    gen = torch.Generator().manual_seed(M + V)
+    x = torch.randint(1, 4, (M, H), generator=gen).to(T[dtype]).cuda()
+    w = torch.randint(-1, 2, (V, H), generator=gen)
+    hot = V // 2
+    w[hot] = torch.randint(50, 121, (H,), generator=gen)
+    w = w.to(T[dtype]).cuda()
+    t = torch.full((M,), hot, dtype=torch.int64, device="cuda")
+    loss, lse = F.ce_fwd(x, w, t)
+    l = x.double() @ w.double().t()
+    assert float((l[:, hot:hot + 1] - l[:, [v for v in range(V) if v != hot]]).min()) > 1000
+    assert not loss.any() and torch.equal(lse.double(), l[:, hot])
+
+
+@pytest.mark.parametrize("dtype,M,H", CE_ONE)
+def test_ce_loss_is_never_negative(dtype, M, H):
+    """Large logits, the target's among the largest: lse is no less than any of them."""
+    gen = torch.Generator().manual_seed(H)
+    x = (torch.randn(M, H, generator=gen) * 100).to(T[dtype]).cuda()
+    w = torch.randn(517, H, generator=gen).to(T[dtype]).cuda()
+    t = (x.float() @ w.float().t()).argmax(dim=1)
+    loss, lse = F.ce_fwd(x, w, t)
+    assert (loss >= 0).all()
+    # loss and lse are fp32 sums of the same logits: lse = logit + loss
+    assert torch.isfinite(lse).all()
