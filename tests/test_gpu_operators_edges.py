@@ -184,3 +184,19 @@ def test_ce_loss_is_never_negative(dtype, M, H):
     assert (loss >= 0).all()
     # loss and lse are fp32 sums of the same logits: lse = logit + loss
     assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("V", [1, 2, 300, 1009])
+@pytest.mark.parametrize("dtype,M,H", CE_ONE)
+def test_ce_no_gradient_where_the_probability_is_one(dtype, M, H, V):
+    """As above; the softmax is exactly the target's indicator, so g is 0."""
+    gen = torch.Generator().manual_seed(M + V)
+    x = torch.randint(1, 4, (M, H), generator=gen).to(T[dtype]).cuda()
+    w = torch.randint(-1, 2, (V, H), generator=gen)
+    w[V // 2] = torch.randint(50, 121, (H,), generator=gen)
+    w = w.to(T[dtype]).cuda()
+    t = torch.full((M,), V // 2, dtype=torch.int64, device="cuda")
+    lse = (x.double() @ w.double().t())[:, V // 2].float()
+    for d in (torch.ones(1, device="cuda"), torch.rand(M, generator=gen).cuda()):
+        dx, dw = F.ce_bwd(x, w, t, lse, d)
+        assert not dx.any() and not dw.any()
