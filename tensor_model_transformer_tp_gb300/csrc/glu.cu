@@ -78,18 +78,19 @@ Layout layout(const GluShape& s, bool backward) {
 }
 
 // ---- fp32 epilogues ------------------------------------------------------------
-// act(a) and its derivative.  SiLU: s = 1 / (1 + e^-a), act = a s,
-// act' = s (1 + a (1 - s)).
+// act(a) and its derivative, to fp32's own accuracy: SiLU with s = 1 / (1 + e^-a),
+// act = a s, act' = s (1 + a (1 - s)); GeLU a Phi(a), Phi(a) + a phi(a).  (The
+// rational form of Phi that serves bf16 is off by up to 7.5e-8, which at a = -5 is a
+// quarter of Phi; it saves 8 of 530 us in a forward of 4096 x 512 x 2048.)
 __device__ __forceinline__ void act_both(int act, float a, float& f, float& df) {
   if (act == OASES_ACT_SILU) {
     const float s = 1.0f / (1.0f + expf(-a));
     f = a * s;
     df = s * fmaf(a, 1.0f - s, 1.0f);
   } else {
-    float cdf, pdf;
-    gelu_cdf_pdf(a, cdf, pdf);
+    const float cdf = normcdff(a);
     f = a * cdf;
-    df = fmaf(a, pdf, cdf);
+    df = fmaf(a, 0.39894228040143268f * expf(-0.5f * a * a), cdf);
   }
 }
 

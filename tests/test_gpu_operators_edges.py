@@ -200,3 +200,28 @@ def test_ce_no_gradient_where_the_probability_is_one(dtype, M, H, V):
     for d in (torch.ones(1, device="cuda"), torch.rand(M, generator=gen).cuda()):
         dx, dw = F.ce_bwd(x, w, t, lse, d)
         assert not dx.any() and not dw.any()
+
+
+# ---- fp32 GeLU ---------------------------------------------------------------------
+def test_glu_fp32_gelu_keeps_its_relative_accuracy_in_the_tail():
+    """Wg = I, Wu = 0, bu = 1, W2 = I: y = gelu(x) and dx = dy gelu'(x), one fp32
+    value each.  With z = a / sqrt(2): the complementary error function is good to 4
+    ulp, z to 1.25 2^-24 relative, which counts 2 z^2 + 1 <= 26 times for |a| <= 5; the
+    exponential to 2 ulp, a^2 / 2 <= 12.5 to 2^-24 relative; a handful of products:
+    32 2^-23 covers each of Phi and phi."""
+    n = 512
+    a = torch.linspace(-5, 5, n).cuda().repeat(3, 1).contiguous()
+    a[1:] += torch.tensor([[0.003], [0.007]], device="cuda")
+    eye = torch.eye(n, device="cuda")
+    w = {"w1": torch.cat([eye, torch.zeros_like(eye)]),
+         "b1": torch.cat([torch.zeros(n), torch.ones(n)]).cuda(), "w2": eye}
+    dy = torch.full_like(a, 1.0)
+    A = a.double()
+    cdf = 0.5 * torch.special.erfc(-A * 0.5 ** 0.5)
+    pdf = torch.exp(-0.5 * A * A) * (2 * np.pi) ** -0.5
+    for save in ("pre", "none"):
+        y, saved = F.glu_fwd(a, w, act="gelu", save=save)
+        dx, _ = F.glu_bwd(a, dy, w, act="gelu", save=save, saved=saved)
+        assert ((y.double() - A * cdf).abs() <= 32 * 2.0 ** -23 * (A * cdf).abs()).all()
+        assert ((dx.double() - (cdf + A * pdf)).abs()
+                <= 32 * 2.0 ** -23 * (cdf + (A * pdf).abs())).all()
