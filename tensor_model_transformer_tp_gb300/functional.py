@@ -10,12 +10,14 @@ threads, and inside CUDA graph capture.
 Tensors are contiguous, on one CUDA device, ``float32`` or ``bfloat16`` as
 ``x`` is; anything else raises ``ValueError`` before a call is made.  Errors of
 the library raise ``OasesError``.  There is no autograd integration: the
-backward functions are called with what the forward returned.
+backward functions are called with what the forward returned.  (A forward function
+given a tensor that requires a gradient, in grad mode, warns of it once.)
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import warnings
 from typing import Dict, Optional, Tuple
 
 import torch
@@ -28,6 +30,22 @@ _NAMES = ("w1", "b1", "w2", "b2")
 _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 _raw_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
 _raw_delete = torch._C._cuda_cudaCachingAllocator_raw_delete
+
+
+_told = set()
+
+
+def _no_graph(name: str, *tensors: Optional[torch.Tensor]) -> None:
+    """Warn, once a function, where autograd would have followed the call."""
+    if name in _told or not torch.is_grad_enabled():
+        return
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            _told.add(name)
+            warnings.warn("%s builds no autograd graph: call the backward function for the "
+                          "gradients, or wrap both in a torch.autograd.Function" % name,
+                          stacklevel=3)
+            return
 
 
 def _need(ok: bool, what: str) -> None:
@@ -178,8 +196,9 @@ def glu_fwd(x: torch.Tensor, weights: Dict[str, torch.Tensor], act: str = "silu"
     an in-place residual).
     """
     w1, b1, w2, b2 = _named(weights, "weights")
-    desc, n_saved, n_ws, kept = _glu_fwd_plan(
-        _sig(x), (_sig(w1), _sig(b1), _sig(w2), _sig(b2)), _sig(resid), _sig(y), act, save)
+    sigs = _sig(x), (_sig(w1), _sig(b1), _sig(w2), _sig(b2)), _sig(resid), _sig(y)
+    _no_graph("glu_fwd", x, w1, b1, w2, b2, resid)
+    desc, n_saved, n_ws, kept = _glu_fwd_plan(*sigs, act, save)
     if y is None:
         y = torch.empty_like(x)
     saved = None
@@ -253,8 +272,9 @@ def ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     target is ignore_index have loss 0; another target outside [0, vocab)
     gives NaN.  The logits are not kept.
     """
-    desc, n_ws, rows = _ce_plan(_sig(x), _sig(w), _sig(targets), None, None, None, False,
-                                ignore_index)
+    sigs = _sig(x), _sig(w), _sig(targets)
+    _no_graph("ce_fwd", x, w)
+    desc, n_ws, rows = _ce_plan(*sigs, None, None, None, False, ignore_index)
     loss = torch.empty(rows, dtype=torch.float32, device=x.device)
     lse = torch.empty_like(loss)
     _call(lib().oases_ce_fwd, x.get_device(), n_ws, desc, _ptr(x), _ptr(w), _ptr(targets), _ptr(loss),

@@ -1,6 +1,8 @@
 """Arguments of the functions on torch tensors that no library call could carry,
 refused without a GPU: shapes are given as the signatures the plans are checked
 against (shape, type, CUDA device)."""
+import warnings
+
 import pytest
 import torch
 
@@ -52,3 +54,38 @@ def test_ce_ignore_index_beyond_64_bits(index):
     x, w, t = sig(4, 64), sig(100, 64), sig(4, dtype=torch.int64)
     with pytest.raises(ValueError, match="ignore_index"):
         F._ce_plan(x, w, t, None, None, None, False, index)
+
+
+# ---- tensors that autograd follows ---------------------------------------------------
+def test_a_forward_that_autograd_cannot_follow_says_so(monkeypatch, recwarn):
+    """The forward functions build no graph; with a tensor that requires a gradient, in
+    grad mode, they warn, once each."""
+    x = torch.zeros(2, 8, requires_grad=True)
+    w = {"w1": torch.zeros(16, 8), "w2": torch.zeros(8, 8)}
+    p = {k: v.clone().requires_grad_() for k, v in w.items()}
+    head, t = torch.zeros(5, 8), torch.zeros(2, dtype=torch.int64)
+    calls = {"glu_fwd": [lambda: F.glu_fwd(x, w), lambda: F.glu_fwd(x.detach(), p),
+                         lambda: F.glu_fwd(x.detach(), w, resid=x)],
+             "ce_fwd": [lambda: F.ce_fwd(x, head, t),
+                        lambda: F.ce_fwd(x.detach(), head.clone().requires_grad_(), t)]}
+    plain = [lambda: F.glu_fwd(x.detach(), w), lambda: F.ce_fwd(x.detach(), head, t)]
+
+    def refused():      # what follows the warning without a GPU
+        return pytest.raises(ValueError, match="CUDA device")
+
+    for name, some in calls.items():
+        for call in some:
+            warnings.simplefilter("always")
+            monkeypatch.setattr(F, "_told", set())
+            with torch.no_grad(), refused():
+                call()
+            assert not recwarn.list
+            for _ in range(2):
+                with refused():
+                    call()
+            assert len(recwarn.list) == 1
+            assert "%s builds no autograd graph" % name in str(recwarn.pop().message)
+    for call in plain:
+        with refused():
+            call()
+    assert not recwarn.list
