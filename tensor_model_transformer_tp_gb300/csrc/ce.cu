@@ -10,15 +10,12 @@
 
 namespace oases {
 void api_begin();
-void api_set_error(const char* what);
 oases_status api_end(cudaError_t e);
 
 namespace {
 
 constexpr int64_t PART_BYTES = 256ll << 20;   // fp32: partial maxima and sums of the forward
 constexpr int64_t PIECE_BYTES = 256ll << 20;  // fp32: g of one piece of the backward
-
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 oases_status ce_shape(const oases_ce_desc* d, CeShape* s) {
   if (!d) return OASES_ERR_INVALID_ARG;
@@ -154,12 +151,6 @@ ce_scale_kernel(const float* dloss, const int64_t* target, int64_t ignore, int M
   if (threadIdx.x == 0) scale[0] = mx;
 }
 
-#define OASES_TRY(expr)                       \
-  do {                                        \
-    const cudaError_t e_ = (expr);            \
-    if (e_ != cudaSuccess) return e_;         \
-  } while (0)
-
 cudaError_t fwd(const CeShape& s, const void* x, const void* w, const int64_t* target, float* loss,
                 float* lse, char* ws, cudaStream_t st) {
   const Layout l = layout(s, false);
@@ -206,12 +197,6 @@ cudaError_t bwd(const CeShape& s, const void* x, const void* w, const int64_t* t
     OASES_TRY(f32::launch_group(args, out, {true, false, false}, st));
   }
   return cudaSuccess;
-}
-
-bool misaligned(std::initializer_list<const void*> ps, uintptr_t bytes) {
-  for (const void* p : ps)
-    if ((uintptr_t)p & (bytes - 1)) return true;
-  return false;
 }
 
 }  // namespace

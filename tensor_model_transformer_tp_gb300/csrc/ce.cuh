@@ -13,7 +13,7 @@ struct CeShape {
   DType t, grad_t;
   bool per_row, accumulate;
   int64_t ignore;
-  int piece;   // columns of the vocabulary per piece of the backward (fp32: and of the forward)
+  int piece;   // fp32: columns of the vocabulary per piece of the backward
   int64_t ld;  // leading dimension of a piece's buffer
 };
 

@@ -7,9 +7,23 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <utility>
 
 namespace oases {
+
+// ---- host: helpers of the entry points ------------------------------------
+#define OASES_TRY(expr)                       \
+  do {                                        \
+    const cudaError_t e_ = (expr);            \
+    if (e_ != cudaSuccess) return e_;         \
+  } while (0)
+inline size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+inline bool misaligned(std::initializer_list<const void*> ps, uintptr_t bytes) {
+  for (const void* p : ps)
+    if ((uintptr_t)p & (bytes - 1)) return true;
+  return false;
+}
 
 // ---- host: per-device state for a process that drives several GPUs -------
 inline int current_device() {

@@ -615,12 +615,14 @@ inline void deal(int tiles, int len, int slots, int* load, uint16_t* first) {
   first[slots] = (uint16_t)at;
 }
 
-// Whether `n` products are better dealt out in one launch than launched one
-// after the other, by the K-slices on the longest path.
+// K-slices on the longest path of a product launched alone.
 inline int64_t rounds_cost(int64_t tiles, int len, int slots) {
   return (tiles + slots - 1) / slots * len;
 }
 
+// One launch of the N products, their tiles dealt out, where that is better than one
+// launch after the other by the K-slices on the longest path (*taken, else nothing is
+// launched).
 template <class Epi, int N>
 cudaError_t launch_group(const Product* prod, const typename Epi::Params* ep, bool* taken,
                          cudaStream_t st) {

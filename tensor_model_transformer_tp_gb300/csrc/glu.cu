@@ -11,7 +11,6 @@
 
 namespace oases {
 void api_begin();
-void api_set_error(const char* what);
 oases_status api_end(cudaError_t e);
 
 namespace {
@@ -182,11 +181,6 @@ struct RowLoad<float, 1> {
   __device__ __forceinline__ void load(const float* p) { u = __ldg(p); }
   __device__ __forceinline__ void add(float (&v)[1]) const { v[0] += u; }
 };
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
 template <typename T, typename O, int V>
 __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int rows, int split, int accumulate) {
   __shared__ float red[16][8 * V + 1];
@@ -233,7 +227,7 @@ __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int rows
   if (split > 1) {
     ptx::cluster_sync();
     if (rank == 0 && (int)threadIdx.x < 8 * V)
-      for (int i = 1; i < split; ++i) t += ld_cluster(ptx::mapa(ptx::smem_u32(&part[threadIdx.x]), i));
+      for (int i = 1; i < split; ++i) t += ptx::ld_cluster(ptx::mapa(ptx::smem_u32(&part[threadIdx.x]), i));
     ptx::cluster_sync();  // the others' shared memory is there while it is read
   }
   if (rank == 0 && (int)threadIdx.x < 8 * V && n0 + (int)threadIdx.x < N) {
@@ -241,12 +235,6 @@ __global__ void __launch_bounds__(512) column_sums_kernel(const Sums s, int rows
     st_elem(out, 0, accumulate ? ld_elem(out, 0) + t : t);
   }
 }
-
-#define OASES_TRY(expr)                       \
-  do {                                        \
-    const cudaError_t e_ = (expr);            \
-    if (e_ != cudaSuccess) return e_;         \
-  } while (0)
 
 // The rows are split, 512 at least to a CTA, where the blocks of columns leave SMs
 // idle: 16384 rows of 1536 x 2 + 1024 columns 58 -> 35 us, 65536 of 64 x 2 + 64 in
@@ -333,12 +321,6 @@ cudaError_t bwd(const GluShape& s, const oases_glu_weights& w, const void* x, co
   return bias_grads(s, dpre, dy, gr, st);
 }
 
-bool misaligned(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if ((uintptr_t)p & 15) return true;
-  return false;
-}
-
 }  // namespace
 }  // namespace oases
 
@@ -365,7 +347,7 @@ extern "C" oases_status oases_glu_fwd(const oases_glu_desc* desc, const oases_gl
   if (s.M == 0) return OASES_OK;
   if (!wts || !wts->w1 || !wts->w2 || !x || !y) return OASES_ERR_INVALID_ARG;
   if (s.keep != OASES_GLU_KEEP_NONE && !saved) return OASES_ERR_INVALID_ARG;
-  if (misaligned({wts->w1, wts->b1, wts->w2, wts->b2, x, resid, y, saved, workspace}))
+  if (misaligned({wts->w1, wts->b1, wts->w2, wts->b2, x, resid, y, saved, workspace}, 16))
     return OASES_ERR_INVALID_ARG;
   const size_t need = layout(s, false).total;
   if (need > 0 && (!workspace || ws_bytes < need)) return OASES_ERR_WORKSPACE;
@@ -386,7 +368,7 @@ extern "C" oases_status oases_glu_bwd(const oases_glu_desc* desc, const oases_gl
   if (!wts || !grads) return OASES_ERR_INVALID_ARG;
   if ((grads->b1 && !wts->b1) || (grads->b2 && !wts->b2)) return OASES_ERR_INVALID_ARG;
   if (misaligned({wts->w1, wts->b1, wts->w2, wts->b2, x, dy, saved, dx, grads->w1, grads->b1,
-                  grads->w2, grads->b2, workspace}))
+                  grads->w2, grads->b2, workspace}, 16))
     return OASES_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s.M == 0) {  // sums over no rows

@@ -6,8 +6,6 @@
 
 namespace oases {
 
-inline size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
 struct GluShape {
   int M, H, F;
   DType t, dx_t, grad_t;

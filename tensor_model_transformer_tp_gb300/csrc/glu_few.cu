@@ -51,12 +51,6 @@ struct FewArgs {
   int kgroups;
 };
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 template <int NT, bool UP>
 __global__ void __launch_bounds__(NTHREADS)
 glu_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -185,7 +179,7 @@ glu_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     float v = 0.f;
 #pragma unroll
     for (int s = 0; s < 8; ++s)
-      if (s < S) v += ld_cluster(from[s] + 4u * at);
+      if (s < S) v += ptx::ld_cluster(from[s] + 4u * at);
     return v;
   };
   constexpr int W = UP ? 64 : 128;  // outputs of a row in this cluster

@@ -358,12 +358,6 @@ struct GradSplits {
   }
 };
 
-#define OASES_TRY(expr)                       \
-  do {                                        \
-    const cudaError_t e_ = (expr);            \
-    if (e_ != cudaSuccess) return e_;         \
-  } while (0)
-
 }  // namespace
 
 size_t glu_grads_tc_bytes(const GluShape& s) { return GradSplits(s).bytes(); }
