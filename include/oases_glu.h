@@ -38,7 +38,10 @@ typedef enum { OASES_ACT_SILU = 0, OASES_ACT_GELU = 1 } oases_act;
 /* What the forward keeps for the backward, beside x.
  * NONE:  nothing; the backward computes a and b again (the recomputation of
  *        Oases §IV, Fig. 4d: the column-parallel part only, never y).
- * PRE:   [a | b] in the storage type: [rows, 2 ffn], contiguous.
+ * PRE:   [a | b] in the storage type: [rows, 2 ffn], contiguous.  In bf16 the
+ *        backward is then at other a and b than the forward's h was: dx, dw1 and dw2
+ *        are 0.0035 of their size off, where NONE gives 0.0024 and the outputs' own
+ *        rounding 0.0017.
  * MXFP8: a and b in 8 bits, half the bytes of PRE in bf16 (plus 1/32): two MX
  *        operands (oases_mx.h: E4M3 codes, one UE8M0 scale per 32 consecutive
  *        columns), gate first:
@@ -102,7 +105,7 @@ oases_status oases_glu_fwd(const oases_glu_desc *desc, const oases_glu_weights *
  * (resid's gradient is dy.)  x and saved as given to and written by the
  * forward; a and b are the kept values, or with KEEP_NONE fp32 sums formed again.
  * da, db and h are rounded to the storage type between the products, which
- * accumulate in fp32.  dx may be NULL (left out); it overlaps no input.
+ * accumulate in fp32; db1 sums the rounded da and db.  dx may be NULL (left out); it overlaps no input.
  * Errors as oases_glu_fwd, and INVALID_ARG for grads->b1 / b2 set where the
  * bias is NULL. */
 oases_status oases_glu_bwd(const oases_glu_desc *desc, const oases_glu_weights *wts, const void *x,

@@ -252,7 +252,10 @@ cudaError_t launch_sums(const Sums& q, int M, int accumulate, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, column_sums_kernel<T, O, V>, q, M, split, accumulate);
 }
 
-// db1 = colsum(dpre), db2 = colsum(dy), each where it is wanted.
+// db1 = colsum(dpre), db2 = colsum(dy), each where it is wanted.  dpre holds da and db
+// as they are rounded for dw1 and dx: the rounding errors of M rows mostly cancel in
+// the fp32 sum (2^-9 / sqrt(M) of its terms' size), and the epilogues that form da and
+// db need no second set of column sums.
 cudaError_t bias_grads(const GluShape& s, const void* dpre, const void* dy, const oases_glu_grads& gr,
                        cudaStream_t st) {
   if (!gr.b1 && !gr.b2) return cudaSuccess;

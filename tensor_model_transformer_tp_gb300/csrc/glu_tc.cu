@@ -145,8 +145,12 @@ struct EpiDual {
 // EIGHT: a and b come from the 8-bit form, 32 bytes of a row per lane (whole
 // sectors), loaded one step ahead.
 // What bounds it: the product takes 24 us there, the 100 MB it writes 25 at the
-// 4 TB/s that fills reach, and the two add up; without its loads it takes 39,
-// without loads and stores 24, without the arithmetic between them 45.
+// 4 TB/s that fills reach, and it takes their sum; without its loads it takes 39,
+// without loads and stores 24, without the arithmetic between them 45.  That is
+// latency: the issue slots are 70% idle and DRAM at a third of its rate, because a, b
+// and da, db share a staging set, and a request for the next a and b waits until every
+// earlier store has read shared memory.  A warp's loads, arithmetic and stores so run
+// one after the other.
 template <bool EIGHT>
 struct EpiGrad {
   static constexpr bool DUAL = false, PAD_ROWS = false;
