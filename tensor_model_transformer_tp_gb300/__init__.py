@@ -77,6 +77,27 @@ class CeDesc(ctypes.Structure):
                 ("dtype", "rows", "hidden", "vocab", "dloss_per_row", "grad_dtype", "accumulate")]
 
 
+class Strides(ctypes.Structure):
+    """Elements between neighbouring sequences, tokens and heads."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "token", "head")]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("dtype", "batch", "q_len", "k_len", "heads", "kv_heads", "head_dim", "causal",
+                 "q_start", "buckets", "max_distance", "bidirectional", "grad_dtype",
+                 "accumulate")] + [("scale", ctypes.c_float)] + \
+        [(n, Strides) for n in ("q", "k", "v", "o", "d_o", "dq", "dk", "dv")]
+
+
+class QknormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("dtype", "batch", "seq", "heads", "kv_heads", "head_dim", "rot", "interleaved",
+                 "positions_len", "positions_shared", "grad_dtype", "accumulate")] + \
+        [("eps", ctypes.c_float)] + \
+        [(n, Strides) for n in ("q", "k", "q_out", "k_out", "dq", "dk")]
+
+
 def lib():
     """The loaded shared library; raises if it has not been built."""
     global _lib
@@ -121,6 +142,19 @@ def lib():
         L.oases_ce_fwd.restype = i32
         L.oases_ce_bwd.argtypes = [cd, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.oases_ce_bwd.restype = i32
+        ad, qd = ctypes.POINTER(AttnDesc), ctypes.POINTER(QknormDesc)
+        L.oases_attn_workspace_bytes.argtypes = [ad, i32]
+        L.oases_attn_workspace_bytes.restype = sz
+        L.oases_attn_fwd.argtypes = [ad] + [vp] * 9 + [sz, vp]
+        L.oases_attn_fwd.restype = i32
+        L.oases_attn_bwd.argtypes = [ad] + [vp] * 14 + [sz, vp]
+        L.oases_attn_bwd.restype = i32
+        L.oases_qknorm_workspace_bytes.argtypes = [qd]
+        L.oases_qknorm_workspace_bytes.restype = sz
+        L.oases_qknorm_fwd.argtypes = [qd] + [vp] * 10
+        L.oases_qknorm_fwd.restype = i32
+        L.oases_qknorm_bwd.argtypes = [qd] + [vp] * 14 + [sz, vp]
+        L.oases_qknorm_bwd.restype = i32
         _lib = L
     return _lib
 
@@ -251,6 +285,47 @@ def oases_ce_bwd(desc, x, w, target, lse, dloss, dx, dw, workspace, ws_bytes=Non
                               _stream(stream)))
 
 
+def oases_attn_workspace_bytes(desc: AttnDesc, backward: bool) -> int:
+    return int(lib().oases_attn_workspace_bytes(ctypes.byref(desc), int(backward)))
+
+
+def oases_attn_fwd(desc, q, k, v, kv_lens, q_start, bias, o, lse, workspace, ws_bytes=None,
+                   stream=None) -> None:
+    nb = ws_bytes if ws_bytes is not None else _nbytes(workspace)
+    _check(lib().oases_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens),
+                                _ptr(q_start), _ptr(bias), _ptr(o), _ptr(lse), _ptr(workspace), nb,
+                                _stream(stream)))
+
+
+def oases_attn_bwd(desc, q, k, v, kv_lens, q_start, bias, o, lse, d_o, dq, dk, dv, dbias, workspace,
+                   ws_bytes=None, stream=None) -> None:
+    nb = ws_bytes if ws_bytes is not None else _nbytes(workspace)
+    _check(lib().oases_attn_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens),
+                                _ptr(q_start), _ptr(bias), _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq),
+                                _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(workspace), nb,
+                                _stream(stream)))
+
+
+def oases_qknorm_workspace_bytes(desc: QknormDesc) -> int:
+    return int(lib().oases_qknorm_workspace_bytes(ctypes.byref(desc)))
+
+
+def oases_qknorm_fwd(desc, q, k, cos, sin, positions, q_weight, k_weight, q_out, k_out,
+                     stream=None) -> None:
+    _check(lib().oases_qknorm_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(cos), _ptr(sin),
+                                  _ptr(positions), _ptr(q_weight), _ptr(k_weight), _ptr(q_out),
+                                  _ptr(k_out), _stream(stream)))
+
+
+def oases_qknorm_bwd(desc, q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight, dq, dk,
+                     dq_weight, dk_weight, workspace, ws_bytes=None, stream=None) -> None:
+    nb = ws_bytes if ws_bytes is not None else _nbytes(workspace)
+    _check(lib().oases_qknorm_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out),
+                                  _ptr(cos), _ptr(sin), _ptr(positions), _ptr(q_weight),
+                                  _ptr(k_weight), _ptr(dq), _ptr(dk), _ptr(dq_weight),
+                                  _ptr(dk_weight), _ptr(workspace), nb, _stream(stream)))
+
+
 def oases_schedule_trace(desc, n_layers: int, phase: int) -> List[tuple]:
     L = lib()
     n = L.oases_schedule_trace(ctypes.byref(desc), n_layers, phase, None, 0)
@@ -300,4 +375,7 @@ __all__ = ["BlockDesc", "Weights", "Grads", "OasesError", "build_library", "lib"
            "oases_status_str", "oases_version", "PARAM_NAMES",
            "ACT", "KEEP", "GluDesc", "GluWeights", "GluGrads", "CeDesc",
            "oases_glu_saved_bytes", "oases_glu_workspace_bytes", "oases_glu_fwd", "oases_glu_bwd",
-           "oases_ce_workspace_bytes", "oases_ce_fwd", "oases_ce_bwd"]
+           "oases_ce_workspace_bytes", "oases_ce_fwd", "oases_ce_bwd",
+           "Strides", "AttnDesc", "QknormDesc", "oases_attn_workspace_bytes", "oases_attn_fwd",
+           "oases_attn_bwd", "oases_qknorm_workspace_bytes", "oases_qknorm_fwd",
+           "oases_qknorm_bwd"]

@@ -1,0 +1,370 @@
+// Attention over keys of another length with a relative position bias
+// (oases_attn.h): entry points, workspace, the bias by distance and its gradient.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "xattn.cuh"
+
+namespace oases {
+void api_begin();
+oases_status api_end(cudaError_t e);
+
+namespace {
+using namespace xattn;
+
+// ---- buckets --------------------------------------------------------------------
+// Whole numbers of any length, little end first: enough for powers of a distance.
+struct Big {
+  std::vector<uint32_t> d{1};
+  void times(uint32_t m) {
+    uint64_t c = 0;
+    for (auto& x : d) {
+      c += (uint64_t)x * m;
+      x = (uint32_t)c;
+      c >>= 32;
+    }
+    if (c) d.push_back((uint32_t)c);
+  }
+  static Big product(uint32_t a, int na, uint32_t b, int nb) {  // a^na b^nb
+    Big r;
+    for (int i = 0; i < na; ++i) r.times(a);
+    for (int i = 0; i < nb; ++i) r.times(b);
+    return r;
+  }
+  bool operator<(const Big& o) const {
+    if (d.size() != o.d.size()) return d.size() < o.d.size();
+    for (size_t i = d.size(); i-- > 0;)
+      if (d[i] != o.d[i]) return d[i] < o.d[i];
+    return false;
+  }
+};
+
+// Of one sign's N buckets, the smallest distance of each but the first.
+struct Borders {
+  int n;  // N - 1
+  int at[MAX_BUCKETS];
+};
+Borders borders(int N, int max_distance) {
+  Borders r;
+  const int E = N / 2, L = N - E;
+  r.n = N - 1;
+  for (int t = 1; t <= E && t < N; ++t) r.at[t - 1] = t;
+  // bucket E + u begins at the smallest a with (a / E)^L >= (max_distance / E)^u,
+  // that is a^L >= E^(L - u) max_distance^u; a floating-point guess, put right
+  for (int u = 1; u < L; ++u) {
+    const Big want = Big::product((uint32_t)E, L - u, (uint32_t)max_distance, u);
+    auto reaches = [&](int a) { return !(Big::product((uint32_t)a, L, 1, 0) < want); };
+    int a = std::max(1, (int)lround(E * pow((double)max_distance / E, (double)u / L)));
+    while (a > 1 && reaches(a - 1)) --a;
+    while (!reaches(a)) ++a;
+    r.at[E + u - 1] = a;
+  }
+  return r;
+}
+
+struct Shape {
+  Args a = {};
+  bool grad_f32 = false, accumulate = false;
+  bool bidirectional = false;
+  int per_sign = 0, R = 0;  // buckets of one sign; the distance from which the bucket stays
+  Borders border = {};
+};
+
+bool strides_ok(const oases_strides& s, int64_t esize, int batch, int tokens, int heads, Strides* out) {
+  const int64_t v[3] = {s.batch, s.token, s.head};
+  const int n[3] = {batch, tokens, heads};
+  const bool empty = batch == 0 || tokens == 0 || heads == 0;
+  int64_t w[3];
+  for (int i = 0; i < 3; ++i) {
+    // not read: any that the tensor maps accept
+    w[i] = n[i] > 1 && !empty ? v[i] : 16;
+    if (w[i] <= 0 || w[i] > (1ll << 36) || w[i] * esize % 16 != 0) return false;
+  }
+  *out = {w[0], w[1], w[2]};
+  return true;
+}
+
+oases_status shape(const oases_attn_desc* d, bool backward, Shape* s) {
+  if (!d) return OASES_ERR_INVALID_ARG;
+  if (d->dtype != OASES_F32 && d->dtype != OASES_BF16) return OASES_ERR_INVALID_ARG;
+  if (d->batch < 0 || d->q_len < 0 || d->k_len < 0 || d->heads <= 0 || d->kv_heads <= 0 ||
+      d->heads % d->kv_heads != 0 || d->head_dim <= 0 || d->q_start < 0)
+    return OASES_ERR_INVALID_ARG;
+  if (((d->causal | d->accumulate) & ~1) || !(d->scale > 0.f) || !(d->scale < INFINITY))
+    return OASES_ERR_INVALID_ARG;
+  if (d->grad_dtype != OASES_F32 && d->grad_dtype != d->dtype) return OASES_ERR_INVALID_ARG;
+  if (d->accumulate && d->grad_dtype != OASES_F32) return OASES_ERR_INVALID_ARG;
+  int N = 0;
+  if (d->buckets != 0) {
+    if (d->bidirectional & ~1) return OASES_ERR_INVALID_ARG;
+    N = d->bidirectional ? d->buckets / 2 : d->buckets;
+    if (N < 2 || (d->bidirectional && d->buckets % 2) || d->max_distance <= N / 2)
+      return OASES_ERR_INVALID_ARG;
+    if (d->buckets > MAX_BUCKETS || d->max_distance > 65536) return OASES_ERR_UNSUPPORTED;
+  }
+  if (d->head_dim % 8 != 0 || d->head_dim > 128) return OASES_ERR_UNSUPPORTED;
+  constexpr int MOST = 1 << 24;
+  if (std::max({d->q_len, d->k_len, d->q_start, d->heads}) > MOST || (int64_t)d->batch * d->heads > MOST)
+    return OASES_ERR_UNSUPPORTED;
+  Args& a = s->a;
+  a.t = static_cast<DType>(d->dtype);
+  const int64_t e = (int64_t)dtype_size(a.t);
+  const int B = d->batch, Sq = d->q_len, Sk = d->k_len, H = d->heads, G = d->kv_heads;
+  if (!strides_ok(d->q, e, B, Sq, H, &a.sq) || !strides_ok(d->k, e, B, Sk, G, &a.sk) ||
+      !strides_ok(d->v, e, B, Sk, G, &a.sv) || !strides_ok(d->o, e, B, Sq, H, &a.so))
+    return OASES_ERR_INVALID_ARG;
+  if (backward && (!strides_ok(d->d_o, e, B, Sq, H, &a.sdo) || !strides_ok(d->dq, e, B, Sq, H, &a.sdq) ||
+                   !strides_ok(d->dk, e, B, Sk, G, &a.sdk) || !strides_ok(d->dv, e, B, Sk, G, &a.sdv)))
+    return OASES_ERR_INVALID_ARG;
+  a.B = B, a.Sq = Sq, a.Sk = Sk, a.H = H, a.G = G, a.share = H / G, a.D = d->head_dim;
+  a.causal = d->causal;
+  a.q_start0 = d->q_start;
+  a.scale = d->scale;
+  a.splits = 1;
+  s->grad_f32 = d->grad_dtype == OASES_F32;
+  s->accumulate = d->accumulate != 0;
+  if (N) {
+    s->bidirectional = d->bidirectional != 0;
+    s->per_sign = N;
+    s->border = borders(N, d->max_distance);
+    s->R = s->border.at[N - 2];
+    a.bias.buckets = d->buckets;
+    a.bias.R = s->R;
+    a.bias.pitch = (2 * (s->R + BIAS_PAD) + 1 + 3) / 4 * 4;
+    a.bias.left = N - 1;
+    a.bias.right = s->bidirectional ? d->buckets - 1 : 0;
+  }
+  return OASES_OK;
+}
+
+// ---- the bias by distance ---------------------------------------------------------
+// value[h][n + R + PAD] = factor * table[bucket(n)][h], and the run of distances of
+// each bucket.  A finite value stays finite behind the factor.
+template <typename T>
+__global__ void __launch_bounds__(256)
+xattn_bias_kernel(const T* table, float* value, int2* range, const __grid_constant__ Borders border,
+                  int heads, int pitch, int R, int buckets, int bidirectional, float factor) {
+  pdl_wait();
+  pdl_trigger();
+  const int N = border.n + 1;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < buckets) {
+    constexpr int FAR = 1 << 30;
+    const int u = threadIdx.x % N;
+    const int first = u == 0 ? 0 : border.at[u - 1], last = u + 1 < N ? border.at[u] - 1 : FAR;
+    int2 r;
+    if (bidirectional && threadIdx.x >= N)
+      r = make_int2(max(first, 1), last);
+    else
+      r = make_int2(-last, !bidirectional && u == 0 ? FAR : -first);
+    range[threadIdx.x] = r;
+  }
+  const int h = blockIdx.y, i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= pitch) return;
+  const int n = i - (R + BIAS_PAD);
+  const int x = bidirectional ? abs(n) : max(-n, 0);
+  int lo = 0, hi = border.n;  // the number of borders at or below x
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (border.at[mid] <= x) lo = mid + 1;
+    else hi = mid;
+  }
+  const int bucket = lo + (bidirectional && n > 0 ? N : 0);
+  const float v = ld_elem(table, (int64_t)bucket * heads + h);
+  float w = v * factor;
+  if (fabsf(v) < INFINITY) w = fminf(fmaxf(w, -3.402823466e38f), 3.402823466e38f);
+  value[(int64_t)h * pitch + i] = w;
+}
+
+// dbias[u][h] = the sum of the head's `rows` partial rows, in a fixed order.
+__global__ void __launch_bounds__(1024)
+xattn_bias_grad_kernel(const float* part, int64_t rows, int heads, int buckets, void* out, DType t,
+                       int accumulate) {
+  __shared__ float red[1024];
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.x;
+  const int lanes = 1024 / buckets;  // rows at a time
+  const int u = threadIdx.x % buckets, r0 = threadIdx.x / buckets;
+  float v = 0.f;
+  if (r0 < lanes)
+    for (int64_t r = r0; r < rows; r += lanes) v += part[(h * rows + r) * buckets + u];
+  red[threadIdx.x] = v;
+  __syncthreads();
+  if (r0 != 0) return;
+  v = 0.f;
+  for (int r = 0; r < lanes; ++r) v += red[r * buckets + u];
+  const int64_t at = (int64_t)u * heads + h;
+  if (accumulate) v += static_cast<const float*>(out)[at];
+  store_any(out, t, at, v);
+}
+
+// ---- workspace ---------------------------------------------------------------------
+struct Layout {
+  size_t value = 0, range = 0, delta = 0, part = 0, total = 0;
+  int64_t rows = 0;  // partial rows of the bias gradient, for each head
+};
+Layout layout(const Shape& s, bool backward) {
+  Layout l;
+  auto take = [&](size_t* at, size_t bytes) {
+    *at = l.total;
+    l.total += align256(bytes);
+  };
+  const Args& a = s.a;
+  if (a.B == 0 || a.Sq == 0 || a.Sk == 0) return l;
+  if (a.bias.buckets) {
+    take(&l.value, (size_t)a.H * a.bias.pitch * 4);
+    take(&l.range, (size_t)a.bias.buckets * 8);
+  }
+  if (backward) {
+    take(&l.delta, (size_t)a.B * a.H * a.Sq * 4);
+    if (a.bias.buckets) {
+      l.rows = (int64_t)a.B * ((a.Sq + 63) / 64);
+      take(&l.part, (size_t)l.rows * a.H * a.bias.buckets * 4);
+    }
+  }
+  return l;
+}
+
+cudaError_t bias_tables(const Shape& s, const void* table, char* ws, const Layout& l, Bias* out,
+                        cudaStream_t st) {
+  const Bias& b = s.a.bias;
+  *out = b;
+  float* value = reinterpret_cast<float*>(ws + l.value);
+  int2* range = reinterpret_cast<int2*>(ws + l.range);
+  out->value = value;
+  out->range = range;
+  const dim3 grid((b.pitch + 255) / 256, s.a.H);
+  if (s.a.t == DType::F32)
+    return launch_pdl(xattn_bias_kernel<float>, grid, dim3(256), 0, st, (const float*)table, value, range,
+                      s.border, s.a.H, b.pitch, s.R, b.buckets, (int)s.bidirectional, 1.f);
+  return launch_pdl(xattn_bias_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
+                    (const __nv_bfloat16*)table, value, range, s.border, s.a.H, b.pitch, s.R,
+                    b.buckets, (int)s.bidirectional, 1.f);
+}
+
+// lse = -infinity of every query, where there are no keys at all
+__global__ void xattn_fill_kernel(float* p, int64_t n, float v) {
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+    p[i] = v;
+}
+
+// A [tokens, heads, D] tensor of every sequence set to 0, 16 bytes at a time.
+__global__ void xattn_zero_kernel(char* p, Strides s, int esize, int tokens, int heads, int chunks, int64_t n) {
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    int64_t r = i;
+    const int64_t c = r % chunks;
+    r /= chunks;
+    const int64_t h = r % heads;
+    r /= heads;
+    const int64_t t = r % tokens, b = r / tokens;
+    *reinterpret_cast<uint4*>(p + (b * s.b + t * s.s + h * s.h) * esize + c * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+cudaError_t zero(void* p, const Strides& s, const Args& a, int tokens, int heads, cudaStream_t st) {
+  const int e = (int)dtype_size(a.t), chunks = a.D * e / 16;
+  const int64_t n = (int64_t)a.B * tokens * heads * chunks;
+  if (n == 0) return cudaSuccess;
+  return launch_pdl(xattn_zero_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)), dim3(256), 0, st,
+                    static_cast<char*>(p), s, e, tokens, heads, chunks, n);
+}
+
+cudaError_t forward(Shape& s, const void* bias, char* ws, cudaStream_t st) {
+  Args& a = s.a;
+  if (a.Sk == 0) {
+    const int64_t n = (int64_t)a.B * a.H * a.Sq;
+    OASES_TRY(zero(a.o, a.so, a, a.Sq, a.H, st));
+    return launch_pdl(xattn_fill_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)), dim3(256), 0, st,
+                      a.lse, n, -INFINITY);
+  }
+  const Layout l = layout(s, false);
+  if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, st));
+  return xattn_fwd_f32(a, st);
+}
+
+cudaError_t backward(Shape& s, const void* bias, void* dbias, char* ws, cudaStream_t st) {
+  Args& a = s.a;
+  const DType gt = s.grad_f32 ? DType::F32 : a.t;
+  if (a.B == 0 || a.Sq == 0 || a.Sk == 0) {  // sums over nothing
+    OASES_TRY(zero(a.dq, a.sdq, a, a.Sq, a.H, st));
+    OASES_TRY(zero(a.dk, a.sdk, a, a.Sk, a.G, st));
+    OASES_TRY(zero(a.dv, a.sdv, a, a.Sk, a.G, st));
+    if (!dbias || s.accumulate) return cudaSuccess;
+    return cudaMemsetAsync(dbias, 0, (size_t)a.bias.buckets * a.H * dtype_size(gt), st);
+  }
+  const Layout l = layout(s, true);
+  if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, st));
+  a.delta = reinterpret_cast<float*>(ws + l.delta);
+  a.bias_part = dbias ? reinterpret_cast<float*>(ws + l.part) : nullptr;
+  OASES_TRY(xattn_bwd_f32(a, st));
+  if (!dbias) return cudaSuccess;
+  return launch_pdl(xattn_bias_grad_kernel, dim3(a.H), dim3(1024), 0, st, (const float*)a.bias_part,
+                    l.rows, a.H, a.bias.buckets, dbias, gt, (int)s.accumulate);
+}
+
+}  // namespace
+}  // namespace oases
+
+extern "C" size_t oases_attn_workspace_bytes(const oases_attn_desc* desc, int backward) {
+  oases::Shape s;
+  if (oases::shape(desc, backward != 0, &s) != OASES_OK) return 0;
+  return oases::layout(s, backward != 0).total;
+}
+
+extern "C" oases_status oases_attn_fwd(const oases_attn_desc* desc, const void* q, const void* k,
+                                       const void* v, const int32_t* kv_lens,
+                                       const int32_t* q_start, const void* bias, void* o,
+                                       float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  using namespace oases;
+  api_begin();
+  Shape s;
+  const oases_status c = shape(desc, false, &s);
+  if (c != OASES_OK) return c;
+  if (misaligned({q, k, v, o, workspace}, 16) || misaligned({lse, kv_lens, q_start}, 4) ||
+      misaligned({bias}, dtype_size(s.a.t)))
+    return OASES_ERR_INVALID_ARG;
+  if (s.a.B == 0 || s.a.Sq == 0) return OASES_OK;
+  if (!q || !o || !lse || (s.a.Sk && (!k || !v)) || (s.a.bias.buckets && !bias) ||
+      (!s.a.bias.buckets && bias))
+    return OASES_ERR_INVALID_ARG;
+  const size_t need = layout(s, false).total;
+  if (need > 0 && (!workspace || ws_bytes < need)) return OASES_ERR_WORKSPACE;
+  s.a.q = q, s.a.k = k, s.a.v = v, s.a.o = o, s.a.lse = lse;
+  s.a.kv_lens = kv_lens, s.a.q_start = q_start;
+  return api_end(forward(s, bias, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" oases_status oases_attn_bwd(const oases_attn_desc* desc, const void* q, const void* k,
+                                       const void* v, const int32_t* kv_lens,
+                                       const int32_t* q_start, const void* bias, const void* o,
+                                       const float* lse, const void* d_o, void* dq, void* dk,
+                                       void* dv, void* dbias, void* workspace, size_t ws_bytes,
+                                       void* stream) {
+  using namespace oases;
+  api_begin();
+  Shape s;
+  const oases_status c = shape(desc, true, &s);
+  if (c != OASES_OK) return c;
+  const size_t ge = s.grad_f32 ? 4 : dtype_size(s.a.t);
+  if (misaligned({q, k, v, o, d_o, dq, dk, dv, workspace}, 16) ||
+      misaligned({lse, kv_lens, q_start}, 4) || misaligned({bias}, dtype_size(s.a.t)) ||
+      misaligned({dbias}, ge))
+    return OASES_ERR_INVALID_ARG;
+  const bool rows = s.a.B > 0 && s.a.Sq > 0, keys = s.a.B > 0 && s.a.Sk > 0;
+  if ((rows && (!q || !o || !lse || !d_o || !dq)) || (keys && (!k || !v || !dk || !dv)))
+    return OASES_ERR_INVALID_ARG;
+  if (rows && keys && !bias != !s.a.bias.buckets) return OASES_ERR_INVALID_ARG;
+  if (dbias && !s.a.bias.buckets) return OASES_ERR_INVALID_ARG;
+  const size_t need = layout(s, true).total;
+  if (need > 0 && (!workspace || ws_bytes < need)) return OASES_ERR_WORKSPACE;
+  s.a.q = q, s.a.k = k, s.a.v = v, s.a.o = const_cast<void*>(o), s.a.lse = const_cast<float*>(lse);
+  s.a.kv_lens = kv_lens, s.a.q_start = q_start;
+  s.a.d_o = d_o, s.a.dq = dq, s.a.dk = dk, s.a.dv = dv;
+  return api_end(backward(s, bias, dbias, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)));
+}

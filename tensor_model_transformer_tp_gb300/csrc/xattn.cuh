@@ -1,0 +1,71 @@
+// Attention over keys of another length with a relative position bias
+// (oases_attn.h): what its kernels share.
+#pragma once
+
+#include "common.cuh"
+#include "oases_attn.h"
+
+namespace oases {
+namespace xattn {
+
+struct Strides {
+  int64_t b, s, h;  // elements between sequences, tokens, heads
+};
+
+constexpr int MAX_BUCKETS = 128;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
+
+// The bias by distance, written to the workspace by bias_tables(): for every head the
+// values at n = -(R + PAD) .. R + PAD, where R is the distance from which the bucket no
+// longer changes; the PAD places beyond repeat the ends, so that a tile that holds some
+// |n| < R reads every one of its distances without clamping.
+constexpr int BIAS_PAD = 320;
+struct Bias {
+  const float* value = nullptr;  // [heads][pitch], in units of log2(e) for the tensor-core kernels
+  const int2* range = nullptr;   // [buckets]: the distances n of each bucket (first, last)
+  int pitch = 0, R = 0, buckets = 0;
+  int left = 0, right = 0;       // buckets of n <= -R and of n >= R
+  __device__ __forceinline__ const float* at(int h, int n) const {  // |n| <= R + PAD
+    return value + (int64_t)h * pitch + (R + BIAS_PAD) + n;
+  }
+  __device__ __forceinline__ float clamped(int h, int n) const { return *at(h, max(-R, min(R, n))); }
+};
+
+struct Args {
+  const void *q, *k, *v;
+  Strides sq, sk, sv, so, sdo, sdq, sdk, sdv;
+  void* o;           // forward: output; backward: the forward's
+  float* lse;        // [batch][heads][q_len]
+  const void* d_o;
+  void *dq, *dk, *dv;
+  float* delta;      // [batch][heads][q_len], workspace
+  const int *kv_lens, *q_start;
+  int q_start0;
+  int B, Sq, Sk, H, G, share, D, causal;
+  DType t;
+  float scale;
+  Bias bias;
+  float* bias_part;  // partial gradients of the bias, null: not wanted
+  int splits;        // forward: shares of the keys, joined by join_splits()
+  float* part_o;     // [splits][batch][q_len][heads][D], normalised
+  float* part_lse;   // [splits][batch][heads][q_len]
+
+  // visible keys before causality, and the first query's position, of sequence b
+  __device__ __forceinline__ int len(int b) const {
+    return kv_lens ? max(0, min(Sk, kv_lens[b])) : Sk;
+  }
+  __device__ __forceinline__ int start(int b) const {
+    return q_start ? max(-(1 << 28), min(1 << 28, q_start[b])) : q_start0;
+  }
+  __device__ __forceinline__ int64_t stat(int b, int h, int i) const {
+    return ((int64_t)b * H + h) * Sq + i;
+  }
+};
+
+}  // namespace xattn
+
+// fp32 (CUDA cores)
+cudaError_t xattn_fwd_f32(const xattn::Args& a, cudaStream_t st);
+cudaError_t xattn_bwd_f32(const xattn::Args& a, cudaStream_t st);
+
+}  // namespace oases
