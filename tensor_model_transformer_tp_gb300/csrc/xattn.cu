@@ -201,9 +201,57 @@ xattn_bias_grad_kernel(const float* part, int64_t rows, int heads, int buckets, 
   store_any(out, t, at, v);
 }
 
+// ---- shares of the keys ---------------------------------------------------------------
+// Where the forward has fewer items than the GPU has places for them, the keys are
+// shared out, `least` blocks to a share at least.
+int shares(int64_t items, int places, int blocks, int least) {
+  if (items >= places || blocks < 2 * least) return 1;
+  return (int)std::min<int64_t>(places / items, blocks / least);
+}
+
+// o = sum 2^.. of the shares' o, lse of all: a warp per query and head.
+template <typename T>
+__global__ void __launch_bounds__(256)
+xattn_join_kernel(const __grid_constant__ Args a, int64_t rows) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;  // (batch, query, head)
+  if (r >= rows) return;
+  const int lane = threadIdx.x % 32, h = (int)(r % a.H);
+  const int64_t bq = r / a.H, b = bq / a.Sq;
+  const int qi = (int)(bq - b * a.Sq);
+  const int64_t at = a.stat((int)b, h, qi), step = (int64_t)a.B * a.H * a.Sq;
+  float top = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * step + at]);
+  float sum = 0.f, v[4] = {};
+  for (int s = 0; s < a.splits; ++s) {
+    const float l = a.part_lse[s * step + at];
+    if (l == -INFINITY) continue;  // a share without keys
+    const float w = expf(l - top);
+    sum += w;
+    if (4 * lane < a.D) {
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + (s * rows + r) * a.D + 4 * lane);
+      v[0] = fmaf(w, x.x, v[0]), v[1] = fmaf(w, x.y, v[1]), v[2] = fmaf(w, x.z, v[2]), v[3] = fmaf(w, x.w, v[3]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* o = static_cast<T*>(a.o) + b * a.so.b + qi * a.so.s + h * a.so.h;
+  if (4 * lane < a.D)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) st_elem(o, 4 * lane + c, v[c] * inv);
+  if (lane == 0) a.lse[at] = top + logf(sum);
+}
+cudaError_t join_splits(const Args& a, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.B * a.Sq * a.H;
+  const dim3 grid((unsigned)((rows + 7) / 8));
+  return a.t == DType::F32 ? launch_pdl(xattn_join_kernel<float>, grid, dim3(256), 0, st, a, rows)
+                           : launch_pdl(xattn_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, a, rows);
+}
+
 // ---- workspace ---------------------------------------------------------------------
 struct Layout {
-  size_t value = 0, range = 0, delta = 0, part = 0, total = 0;
+  size_t value = 0, range = 0, delta = 0, part = 0, part_o = 0, part_lse = 0, total = 0;
+  int splits = 1;
   int64_t rows = 0;  // partial rows of the bias gradient, for each head
 };
 Layout layout(const Shape& s, bool backward) {
@@ -218,7 +266,17 @@ Layout layout(const Shape& s, bool backward) {
     take(&l.value, (size_t)a.H * a.bias.pitch * 4);
     take(&l.range, (size_t)a.bias.buckets * 8);
   }
-  if (backward) {
+  if (!backward) {
+    const int sms = sm_count();
+    if (a.t == DType::BF16)
+      l.splits = shares((int64_t)a.B * a.H * ((a.Sq + 255) / 256), sms, (a.Sk + 127) / 128, 4);
+    else
+      l.splits = shares((int64_t)a.B * a.H * ((a.Sq + 63) / 64), 2 * sms, (a.Sk + 63) / 64, 4);
+    if (l.splits > 1) {
+      take(&l.part_o, (size_t)l.splits * a.B * a.Sq * a.H * a.D * 4);
+      take(&l.part_lse, (size_t)l.splits * a.B * a.Sq * a.H * 4);
+    }
+  } else {
     take(&l.delta, (size_t)a.B * a.H * a.Sq * 4);
     if (a.bias.buckets) {
       l.rows = (int64_t)a.B * ((a.Sq + 63) / 64);
@@ -229,7 +287,7 @@ Layout layout(const Shape& s, bool backward) {
 }
 
 cudaError_t bias_tables(const Shape& s, const void* table, char* ws, const Layout& l, Bias* out,
-                        cudaStream_t st) {
+                        float factor, cudaStream_t st) {
   const Bias& b = s.a.bias;
   *out = b;
   float* value = reinterpret_cast<float*>(ws + l.value);
@@ -242,7 +300,7 @@ cudaError_t bias_tables(const Shape& s, const void* table, char* ws, const Layou
                       s.border, s.a.H, b.pitch, s.R, b.buckets, (int)s.bidirectional, 1.f);
   return launch_pdl(xattn_bias_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
                     (const __nv_bfloat16*)table, value, range, s.border, s.a.H, b.pitch, s.R,
-                    b.buckets, (int)s.bidirectional, 1.f);
+                    b.buckets, (int)s.bidirectional, factor);
 }
 
 // lse = -infinity of every query, where there are no keys at all
@@ -284,8 +342,12 @@ cudaError_t forward(Shape& s, const void* bias, char* ws, cudaStream_t st) {
                       a.lse, n, -INFINITY);
   }
   const Layout l = layout(s, false);
-  if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, st));
-  return xattn_fwd_f32(a, st);
+  if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, a.t == DType::BF16 ? LOG2E : 1.f, st));
+  a.splits = l.splits;
+  a.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  a.part_lse = reinterpret_cast<float*>(ws + l.part_lse);
+  OASES_TRY(a.t == DType::BF16 ? xattn_fwd_tc(a, st) : xattn_fwd_f32(a, st));
+  return a.splits > 1 ? join_splits(a, st) : cudaSuccess;
 }
 
 cudaError_t backward(Shape& s, const void* bias, void* dbias, char* ws, cudaStream_t st) {
@@ -299,7 +361,7 @@ cudaError_t backward(Shape& s, const void* bias, void* dbias, char* ws, cudaStre
     return cudaMemsetAsync(dbias, 0, (size_t)a.bias.buckets * a.H * dtype_size(gt), st);
   }
   const Layout l = layout(s, true);
-  if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, st));
+  if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, 1.f, st));
   a.delta = reinterpret_cast<float*>(ws + l.delta);
   a.bias_part = dbias ? reinterpret_cast<float*>(ws + l.part) : nullptr;
   OASES_TRY(xattn_bwd_f32(a, st));

@@ -62,8 +62,18 @@ struct Args {
   }
 };
 
+// SMs of the current device (152 where there is none to ask).
+inline int sm_count() {
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, current_device()) != cudaSuccess) n = 0;
+  return n > 0 ? n : 152;
+}
+
 }  // namespace xattn
 
+// bf16, tensor cores
+cudaError_t xattn_fwd_tc(const xattn::Args& a, cudaStream_t st);
+int xattn_fwd_read_and_clear_error();
 // fp32 (CUDA cores)
 cudaError_t xattn_fwd_f32(const xattn::Args& a, cudaStream_t st);
 cudaError_t xattn_bwd_f32(const xattn::Args& a, cudaStream_t st);
