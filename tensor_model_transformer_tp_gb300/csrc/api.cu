@@ -39,7 +39,8 @@
 namespace oases {
 int ce_read_and_clear_error();    // ce_tc.cu: likewise of the cross-entropy kernels
 int glu_read_and_clear_error();   // glu_tc.cu: a wait of the gated feed-forward kernels gave up
-int xattn_fwd_read_and_clear_error();  // xattn_fwd.cu: likewise, attention over other keys
+int xattn_fwd_read_and_clear_error();  // xattn_fwd.cu, xattn_bwd.cu: likewise, attention over
+int xattn_bwd_read_and_clear_error();  // keys of another length
 int norm_read_and_clear_error();  // norm.cu: a LayerNorm kernel's wait gave up
 cudaError_t layer_norm_bwd_dx_colsum(const float* du, const void* x, const float* mean,
                                      const float* rstd, const void* gamma, const void* dres, void* dx,
@@ -1379,9 +1380,11 @@ oases_status oases_check_device(void* stream) {
   if (e != cudaSuccess) return cuda_fail(e);
   const int v = gemm_read_and_clear_error(), w = attention_read_and_clear_error(),
             u = norm_read_and_clear_error(), g = glu_read_and_clear_error(),
-            c = ce_read_and_clear_error(), x = xattn_fwd_read_and_clear_error();
-  if (v < 0 || w < 0 || u < 0 || g < 0 || c < 0 || x < 0) return cuda_fail(cudaGetLastError());
-  return (v || w || u || g || c || x) ? OASES_ERR_TIMEOUT : OASES_OK;
+            c = ce_read_and_clear_error(), x = xattn_fwd_read_and_clear_error(),
+            y = xattn_bwd_read_and_clear_error();
+  if (v < 0 || w < 0 || u < 0 || g < 0 || c < 0 || x < 0 || y < 0)
+    return cuda_fail(cudaGetLastError());
+  return (v || w || u || g || c || x || y) ? OASES_ERR_TIMEOUT : OASES_OK;
 }
 
 }  // extern "C"

@@ -279,7 +279,7 @@ Layout layout(const Shape& s, bool backward) {
   } else {
     take(&l.delta, (size_t)a.B * a.H * a.Sq * 4);
     if (a.bias.buckets) {
-      l.rows = (int64_t)a.B * ((a.Sq + 63) / 64);
+      l.rows = (int64_t)a.B * (a.t == DType::BF16 ? (a.Sq + 127) / 128 * 16 : (a.Sq + 63) / 64);
       take(&l.part, (size_t)l.rows * a.H * a.bias.buckets * 4);
     }
   }
@@ -361,10 +361,10 @@ cudaError_t backward(Shape& s, const void* bias, void* dbias, char* ws, cudaStre
     return cudaMemsetAsync(dbias, 0, (size_t)a.bias.buckets * a.H * dtype_size(gt), st);
   }
   const Layout l = layout(s, true);
-  if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, 1.f, st));
+  if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, a.t == DType::BF16 ? LOG2E : 1.f, st));
   a.delta = reinterpret_cast<float*>(ws + l.delta);
   a.bias_part = dbias ? reinterpret_cast<float*>(ws + l.part) : nullptr;
-  OASES_TRY(xattn_bwd_f32(a, st));
+  OASES_TRY(a.t == DType::BF16 ? xattn_bwd_tc(a, st) : xattn_bwd_f32(a, st));
   if (!dbias) return cudaSuccess;
   return launch_pdl(xattn_bias_grad_kernel, dim3(a.H), dim3(1024), 0, st, (const float*)a.bias_part,
                     l.rows, a.H, a.bias.buckets, dbias, gt, (int)s.accumulate);

@@ -73,7 +73,7 @@ inline int sm_count() {
 
 // bf16, tensor cores
 cudaError_t xattn_fwd_tc(const xattn::Args& a, cudaStream_t st);
-int xattn_fwd_read_and_clear_error();
+cudaError_t xattn_bwd_tc(const xattn::Args& a, cudaStream_t st);
 // fp32 (CUDA cores)
 cudaError_t xattn_fwd_f32(const xattn::Args& a, cudaStream_t st);
 cudaError_t xattn_bwd_f32(const xattn::Args& a, cudaStream_t st);

@@ -434,6 +434,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 *reinterpret_cast<uint4*>(vr + c * BOX + 16 * x) = make_uint4(0, 0, 0, 0);
           }
           ptx::fence_async_smem();
+          __syncwarp();
         }
         ptx::tmem_wait_st();
         l += rs;

@@ -23,25 +23,15 @@ template <int DP>
 constexpr int pitch() { return DP + 4; }
 
 // rows [r0, r0 + 64) of a head into dst, zero from row `rows` and column D on
-template <typename T, int DP>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t stride, int r0, int rows, int D) {
-  constexpr int C = DP / 8;
+template <int DP>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t stride, int r0, int rows, int D) {
+  constexpr int C = DP / 4;
+#pragma unroll 4
   for (int i = threadIdx.x; i < TQ * C; i += NT) {
-    const int r = i / C, c = i % C * 8;
-    float f[8] = {};
-    if (r0 + r < rows && c < D) {
-      const T* p = src + (int64_t)(r0 + r) * stride + c;
-      if (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = ld_elem(p, e);
-      }
-    }
-    float4* d = reinterpret_cast<float4*>(dst + r * pitch<DP>() + c);
-    d[0] = make_float4(f[0], f[1], f[2], f[3]);
-    d[1] = make_float4(f[4], f[5], f[6], f[7]);
+    const int r = i / C, c = i % C * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < rows && c < D) v = *reinterpret_cast<const float4*>(src + (int64_t)(r0 + r) * stride + c);
+    *reinterpret_cast<float4*>(dst + r * pitch<DP>() + c) = v;
   }
 }
 
@@ -113,23 +103,23 @@ __device__ __forceinline__ float row_sum(float v) {
   for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-template <typename T, int DP>
-__device__ __forceinline__ void store_rows(T* out, int64_t stride, int r0, int rows, int D,
+template <int DP>
+__device__ __forceinline__ void store_rows(float* out, int64_t stride, int r0, int rows, int D,
                                            const float (&acc)[4][DP / 16], const float (&f)[4]) {
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + 4 * ty + i;
     if (r >= rows) continue;
-    T* p = out + (int64_t)r * stride;
+    float* p = out + (int64_t)r * stride;
 #pragma unroll
     for (int n = 0; n < DP / 16; ++n)
-      if (const int c = out_col<DP>(tx, n); c < D) st_elem(p, c, acc[i][n] * f[i]);
+      if (const int c = out_col<DP>(tx, n); c < D) p[c] = acc[i][n] * f[i];
   }
 }
 
 // One CTA: 64 queries of one (sequence, head) and one share of its keys.
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(NT)
 xattn_fwd_simt_kernel(const __grid_constant__ Args a, int tiles) {
   extern __shared__ float4 smem_f4[];
@@ -150,16 +140,16 @@ xattn_fwd_simt_kernel(const __grid_constant__ Args a, int tiles) {
   const int last = min(q0 + TQ, a.Sq) - 1;
   const int seen = a.causal ? min(len, max(0, p0 + last + 1)) : len;
   const int blocks = (seen + TQ - 1) / TQ, per = (blocks + a.splits - 1) / a.splits;
-  const T* k = static_cast<const T*>(a.k) + b * a.sk.b + g * a.sk.h;
-  const T* v = static_cast<const T*>(a.v) + b * a.sv.b + g * a.sv.h;
-  load_tile<T, DP>(Qs, static_cast<const T*>(a.q) + b * a.sq.b + h * a.sq.h, a.sq.s, q0, a.Sq, a.D);
+  const float* k = static_cast<const float*>(a.k) + b * a.sk.b + g * a.sk.h;
+  const float* v = static_cast<const float*>(a.v) + b * a.sv.b + g * a.sv.h;
+  load_tile<DP>(Qs, static_cast<const float*>(a.q) + b * a.sq.b + h * a.sq.h, a.sq.s, q0, a.Sq, a.D);
   float acc[4][DP / 16] = {}, m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
   for (int j = sp * per; j < min(blocks, (sp + 1) * per); ++j) {
     __syncthreads();
-    load_tile<T, DP>(Ks, k, a.sk.s, j * TQ, len, a.D);
-    load_tile<T, DP>(Vs, v, a.sv.s, j * TQ, len, a.D);
+    load_tile<DP>(Ks, k, a.sk.s, j * TQ, len, a.D);
+    load_tile<DP>(Vs, v, a.sv.s, j * TQ, len, a.D);
     __syncthreads();
     float s[4][4];
     rows_product<DP>(s, Qs, Ks);
@@ -204,10 +194,10 @@ xattn_fwd_simt_kernel(const __grid_constant__ Args a, int tiles) {
           m[i] + logf(l[i]);
   }
   if (a.splits > 1)
-    store_rows<float, DP>(a.part_o + (((int64_t)sp * a.B + b) * a.Sq * a.H + h) * a.D, (int64_t)a.H * a.D, q0, a.Sq,
+    store_rows<DP>(a.part_o + (((int64_t)sp * a.B + b) * a.Sq * a.H + h) * a.D, (int64_t)a.H * a.D, q0, a.Sq,
                           a.D, acc, inv);
   else
-    store_rows<T, DP>(static_cast<T*>(a.o) + b * a.so.b + h * a.so.h, a.so.s, q0, a.Sq, a.D, acc, inv);
+    store_rows<DP>(static_cast<float*>(a.o) + b * a.so.b + h * a.so.h, a.so.s, q0, a.Sq, a.D, acc, inv);
 }
 
 // Rows' weights and score gradients from s and dP of a tile (both overwritten):
@@ -220,7 +210,7 @@ __device__ __forceinline__ void weight_and_grad(float& s, float& dp, bool visibl
 }
 
 // dq (and delta, and the bias gradient's partial sums): one CTA per 64 queries.
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(NT)
 xattn_dq_simt_kernel(const __grid_constant__ Args a, int tiles) {
   extern __shared__ float4 smem_f4[];
@@ -240,13 +230,13 @@ xattn_dq_simt_kernel(const __grid_constant__ Args a, int tiles) {
   const int q0 = tile * TQ, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int last = min(q0 + TQ, a.Sq) - 1;
   const int seen = a.causal ? min(len, max(0, p0 + last + 1)) : len;
-  const T* k = static_cast<const T*>(a.k) + b * a.sk.b + g * a.sk.h;
-  const T* v = static_cast<const T*>(a.v) + b * a.sv.b + g * a.sv.h;
-  const T* o = static_cast<const T*>(a.o) + b * a.so.b + h * a.so.h;
-  const T* d_o = static_cast<const T*>(a.d_o) + b * a.sdo.b + h * a.sdo.h;
-  load_tile<T, DP>(Qs, static_cast<const T*>(a.q) + b * a.sq.b + h * a.sq.h, a.sq.s, q0, a.Sq, a.D);
-  load_tile<T, DP>(Os, d_o, a.sdo.s, q0, a.Sq, a.D);
-  load_tile<T, DP>(Ks, o, a.so.s, q0, a.Sq, a.D);
+  const float* k = static_cast<const float*>(a.k) + b * a.sk.b + g * a.sk.h;
+  const float* v = static_cast<const float*>(a.v) + b * a.sv.b + g * a.sv.h;
+  const float* o = static_cast<const float*>(a.o) + b * a.so.b + h * a.so.h;
+  const float* d_o = static_cast<const float*>(a.d_o) + b * a.sdo.b + h * a.sdo.h;
+  load_tile<DP>(Qs, static_cast<const float*>(a.q) + b * a.sq.b + h * a.sq.h, a.sq.s, q0, a.Sq, a.D);
+  load_tile<DP>(Os, d_o, a.sdo.s, q0, a.Sq, a.D);
+  load_tile<DP>(Ks, o, a.so.s, q0, a.Sq, a.D);
   __syncthreads();
   {  // delta, four threads a row
     const int r = threadIdx.x / 4;
@@ -266,8 +256,8 @@ xattn_dq_simt_kernel(const __grid_constant__ Args a, int tiles) {
   float db = 0.f;  // thread t < buckets: the bias gradient's bucket t
   for (int j = 0; j * TQ < seen; ++j) {
     __syncthreads();
-    load_tile<T, DP>(Ks, k, a.sk.s, j * TQ, len, a.D);
-    load_tile<T, DP>(Vs, v, a.sv.s, j * TQ, len, a.D);
+    load_tile<DP>(Ks, k, a.sk.s, j * TQ, len, a.D);
+    load_tile<DP>(Vs, v, a.sv.s, j * TQ, len, a.D);
     __syncthreads();
     float s[4][4], dp[4][4];
     rows_product<DP>(s, Qs, Ks);
@@ -307,13 +297,13 @@ xattn_dq_simt_kernel(const __grid_constant__ Args a, int tiles) {
     add_product<DP>(acc, Ds, Ks);
   }
   const float f[4] = {a.scale, a.scale, a.scale, a.scale};
-  store_rows<T, DP>(static_cast<T*>(a.dq) + b * a.sdq.b + h * a.sdq.h, a.sdq.s, q0, a.Sq, a.D, acc, f);
+  store_rows<DP>(static_cast<float*>(a.dq) + b * a.sdq.b + h * a.sdq.h, a.sdq.s, q0, a.Sq, a.D, acc, f);
   if (a.bias_part != nullptr && threadIdx.x < a.bias.buckets)
     a.bias_part[(((int64_t)h * a.B + b) * tiles + tile) * a.bias.buckets + threadIdx.x] = db;
 }
 
 // dk and dv: one CTA per 64 keys of one (sequence, key head), over its query heads.
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(NT)
 xattn_dkv_simt_kernel(const __grid_constant__ Args a, int tiles) {
   extern __shared__ float4 smem_f4[];
@@ -332,20 +322,20 @@ xattn_dkv_simt_kernel(const __grid_constant__ Args a, int tiles) {
   const int g = (int)(u % a.G), b = (int)(u / a.G);
   const int len = a.len(b), p0 = a.start(b);
   const int k0 = tile * TQ, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  load_tile<T, DP>(Ks, static_cast<const T*>(a.k) + b * a.sk.b + g * a.sk.h, a.sk.s, k0, len, a.D);
-  load_tile<T, DP>(Vs, static_cast<const T*>(a.v) + b * a.sv.b + g * a.sv.h, a.sv.s, k0, len, a.D);
+  load_tile<DP>(Ks, static_cast<const float*>(a.k) + b * a.sk.b + g * a.sk.h, a.sk.s, k0, len, a.D);
+  load_tile<DP>(Vs, static_cast<const float*>(a.v) + b * a.sv.b + g * a.sv.h, a.sv.s, k0, len, a.D);
   float dk[4][DP / 16] = {}, dv[4][DP / 16] = {};
   // queries before the first that sees key k0 give nothing
   const int i0 = a.causal ? max(0, k0 - p0) / TQ : 0;
   const int end = k0 < len ? a.Sq : 0;
   for (int hh = 0; hh < a.share; ++hh) {
     const int h = g * a.share + hh;
-    const T* q = static_cast<const T*>(a.q) + b * a.sq.b + h * a.sq.h;
-    const T* d_o = static_cast<const T*>(a.d_o) + b * a.sdo.b + h * a.sdo.h;
+    const float* q = static_cast<const float*>(a.q) + b * a.sq.b + h * a.sq.h;
+    const float* d_o = static_cast<const float*>(a.d_o) + b * a.sdo.b + h * a.sdo.h;
     for (int i = i0; i * TQ < end; ++i) {
       __syncthreads();
-      load_tile<T, DP>(Qs, q, a.sq.s, i * TQ, a.Sq, a.D);
-      load_tile<T, DP>(Os, d_o, a.sdo.s, i * TQ, a.Sq, a.D);
+      load_tile<DP>(Qs, q, a.sq.s, i * TQ, a.Sq, a.D);
+      load_tile<DP>(Os, d_o, a.sdo.s, i * TQ, a.Sq, a.D);
       if (threadIdx.x < TQ) {
         const int qi = i * TQ + threadIdx.x;
         const float l = qi < a.Sq ? a.lse[a.stat(b, h, qi)] : INFINITY;
@@ -384,8 +374,8 @@ xattn_dkv_simt_kernel(const __grid_constant__ Args a, int tiles) {
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) dk[r][n] = dv[r][n] = 0.f;
   }
-  store_rows<T, DP>(static_cast<T*>(a.dk) + b * a.sdk.b + g * a.sdk.h, a.sdk.s, k0, a.Sk, a.D, dk, fk);
-  store_rows<T, DP>(static_cast<T*>(a.dv) + b * a.sdv.b + g * a.sdv.h, a.sdv.s, k0, a.Sk, a.D, dv, fv);
+  store_rows<DP>(static_cast<float*>(a.dk) + b * a.sdk.b + g * a.sdk.h, a.sdk.s, k0, a.Sk, a.D, dk, fk);
+  store_rows<DP>(static_cast<float*>(a.dv) + b * a.sdv.b + g * a.sdv.h, a.sdv.s, k0, a.Sk, a.D, dv, fv);
 }
 
 template <int DP>
@@ -393,41 +383,40 @@ constexpr int smem(int tiles, int square) {
   return (tiles * TQ * pitch<DP>() + square * TQ * PITCH_P) * 4;
 }
 
-template <typename T, int DP>
+template <int DP>
 cudaError_t fwd(const Args& a, cudaStream_t st) {
   const int tiles = (a.Sq + TQ - 1) / TQ;
   const int64_t n = (int64_t)a.B * a.H * tiles * a.splits;
   if (n > INT32_MAX) return cudaErrorInvalidConfiguration;
   static DeviceOnce attr;
   OASES_TRY(attr.run([] {
-    return cudaFuncSetAttribute(xattn_fwd_simt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem<DP>(3, 1));
+    return cudaFuncSetAttribute(xattn_fwd_simt_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem<DP>(3, 1));
   }));
-  return launch_pdl(xattn_fwd_simt_kernel<T, DP>, dim3((unsigned)n), dim3(NT), smem<DP>(3, 1), st, a, tiles);
+  return launch_pdl(xattn_fwd_simt_kernel<DP>, dim3((unsigned)n), dim3(NT), smem<DP>(3, 1), st, a, tiles);
 }
-template <typename T, int DP>
+template <int DP>
 cudaError_t bwd(const Args& a, cudaStream_t st) {
   const int qt = (a.Sq + TQ - 1) / TQ, kt = (a.Sk + TQ - 1) / TQ;
   const int64_t nq = (int64_t)a.B * a.H * qt, nk = (int64_t)a.B * a.G * kt;
   if (nq > INT32_MAX || nk > INT32_MAX) return cudaErrorInvalidConfiguration;
   static DeviceOnce attr;
   OASES_TRY(attr.run([] {
-    cudaError_t e = cudaFuncSetAttribute(xattn_dq_simt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem<DP>(4, 1));
+    cudaError_t e = cudaFuncSetAttribute(xattn_dq_simt_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem<DP>(4, 1));
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(xattn_dkv_simt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem<DP>(4, 2));
+    return cudaFuncSetAttribute(xattn_dkv_simt_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem<DP>(4, 2));
   }));
-  OASES_TRY(launch_pdl(xattn_dq_simt_kernel<T, DP>, dim3((unsigned)nq), dim3(NT), smem<DP>(4, 1), st, a, qt));
+  OASES_TRY(launch_pdl(xattn_dq_simt_kernel<DP>, dim3((unsigned)nq), dim3(NT), smem<DP>(4, 1), st, a, qt));
   if (nk == 0) return cudaSuccess;
-  return launch_pdl(xattn_dkv_simt_kernel<T, DP>, dim3((unsigned)nk), dim3(NT), smem<DP>(4, 2), st, a, kt);
+  return launch_pdl(xattn_dkv_simt_kernel<DP>, dim3((unsigned)nk), dim3(NT), smem<DP>(4, 2), st, a, kt);
 }
 
 }  // namespace
 
-#define OASES_DIM(f, T) (a.D <= 32 ? f<T, 32>(a, st) : a.D <= 64 ? f<T, 64>(a, st) : f<T, 128>(a, st))
 cudaError_t xattn_fwd_f32(const Args& a, cudaStream_t st) {
-  return a.t == DType::F32 ? OASES_DIM(fwd, float) : OASES_DIM(fwd, __nv_bfloat16);
+  return a.D <= 32 ? fwd<32>(a, st) : a.D <= 64 ? fwd<64>(a, st) : fwd<128>(a, st);
 }
 cudaError_t xattn_bwd_f32(const Args& a, cudaStream_t st) {
-  return a.t == DType::F32 ? OASES_DIM(bwd, float) : OASES_DIM(bwd, __nv_bfloat16);
+  return a.D <= 32 ? bwd<32>(a, st) : a.D <= 64 ? bwd<64>(a, st) : bwd<128>(a, st);
 }
 
 }  // namespace oases
