@@ -268,7 +268,9 @@ Layout layout(const Shape& s, bool backward) {
   }
   if (!backward) {
     const int sms = sm_count();
-    if (a.t == DType::BF16)
+    if (xattn_few_takes(a))
+      l.splits = xattn_few_splits(a);
+    else if (a.t == DType::BF16)
       l.splits = shares((int64_t)a.B * a.H * ((a.Sq + 255) / 256), sms, (a.Sk + 127) / 128, 4);
     else
       l.splits = shares((int64_t)a.B * a.H * ((a.Sq + 63) / 64), 2 * sms, (a.Sk + 63) / 64, 4);
@@ -279,7 +281,7 @@ Layout layout(const Shape& s, bool backward) {
   } else {
     take(&l.delta, (size_t)a.B * a.H * a.Sq * 4);
     if (a.bias.buckets) {
-      l.rows = (int64_t)a.B * (a.t == DType::BF16 ? (a.Sq + 127) / 128 * 16 : (a.Sq + 63) / 64);
+      l.rows = (int64_t)a.B * (a.t == DType::BF16 ? (a.Sk + 127) / 128 * 16 : (a.Sq + 63) / 64);
       take(&l.part, (size_t)l.rows * a.H * a.bias.buckets * 4);
     }
   }
@@ -297,7 +299,7 @@ cudaError_t bias_tables(const Shape& s, const void* table, char* ws, const Layou
   const dim3 grid((b.pitch + 255) / 256, s.a.H);
   if (s.a.t == DType::F32)
     return launch_pdl(xattn_bias_kernel<float>, grid, dim3(256), 0, st, (const float*)table, value, range,
-                      s.border, s.a.H, b.pitch, s.R, b.buckets, (int)s.bidirectional, 1.f);
+                      s.border, s.a.H, b.pitch, s.R, b.buckets, (int)s.bidirectional, factor);
   return launch_pdl(xattn_bias_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
                     (const __nv_bfloat16*)table, value, range, s.border, s.a.H, b.pitch, s.R,
                     b.buckets, (int)s.bidirectional, factor);
@@ -342,11 +344,13 @@ cudaError_t forward(Shape& s, const void* bias, char* ws, cudaStream_t st) {
                       a.lse, n, -INFINITY);
   }
   const Layout l = layout(s, false);
-  if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, a.t == DType::BF16 ? LOG2E : 1.f, st));
+  const bool few = xattn_few_takes(a);
+  if (a.bias.buckets)
+    OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, few || a.t == DType::BF16 ? LOG2E : 1.f, st));
   a.splits = l.splits;
   a.part_o = reinterpret_cast<float*>(ws + l.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + l.part_lse);
-  OASES_TRY(a.t == DType::BF16 ? xattn_fwd_tc(a, st) : xattn_fwd_f32(a, st));
+  OASES_TRY(few ? xattn_few(a, st) : a.t == DType::BF16 ? xattn_fwd_tc(a, st) : xattn_fwd_f32(a, st));
   return a.splits > 1 ? join_splits(a, st) : cudaSuccess;
 }
 

@@ -71,6 +71,10 @@ inline int sm_count() {
 
 }  // namespace xattn
 
+// forward of a few rows a key head, any type
+bool xattn_few_takes(const xattn::Args& a);
+int xattn_few_splits(const xattn::Args& a);
+cudaError_t xattn_few(const xattn::Args& a, cudaStream_t st);
 // bf16, tensor cores
 cudaError_t xattn_fwd_tc(const xattn::Args& a, cudaStream_t st);
 cudaError_t xattn_bwd_tc(const xattn::Args& a, cudaStream_t st);

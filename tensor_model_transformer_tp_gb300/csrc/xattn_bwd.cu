@@ -13,9 +13,9 @@
 // ready) and 16 element-wise warps, four per TMEM lane quarter.  P and dS are rounded
 // to bf16, the operand type; the bias's gradient sums dS before that.
 //
-// The bias's gradient.  A warp's 32 x 32 scores that lie R or more from the diagonal on
-// one side belong to one bucket: every thread adds its own.  Nearer ones are summed
-// along their 63 diagonals, by passing a running sum from lane to lane as the column
+// The bias's gradient (dkv kernel).  A warp's 32 x 16 scores that lie R or more from the
+// diagonal on one side belong to one bucket: every thread adds its own.  Nearer ones are
+// summed along their 47 diagonals, by passing a running sum from lane to lane as the column
 // advances (lane r adds element (r, c) at step c, so a sum that moves one lane a step
 // stays on its diagonal), and the sums of each bucket's run of diagonals are added to
 // the warp's own buckets in shared memory: a fixed order throughout.
@@ -35,7 +35,6 @@ using namespace xattn;
 constexpr uint64_t WAIT = 1ull << 29;  // cycles before a wait gives up (~0.25 s)
 constexpr int NT = 608, ACC_WARP = 18, EW = 16;
 constexpr int BOX64 = 64 * 64 * 2;  // one TMA box of 64 rows
-constexpr int PB = 128 * 64 * 2;    // 128 rows x 64 bf16
 constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t IDESC_N64 = ptx::idesc_bf16_f32(128, 64, false, false);
 
@@ -92,15 +91,12 @@ xattn_delta_kernel(const __grid_constant__ Args a, int64_t rows) {
 // dQ MMAs.  TMEM: S 0..127, dP 128..255, dQ 256.., dS (packed bf16) 384..447.  S and dP
 // have one buffer each: the element-wise warps load their columns and release both at
 // once, so the next block's are formed while they work.
-template <int DP, bool BIAS>
+template <int DP>
 struct DqSmem {
   static constexpr int TILE = tile_bytes<DP>();
-  // the bias's buckets take the place of the third K stage of DP = 128
-  static constexpr int KST = DP == 64 ? 4 : BIAS ? 2 : 3, VST = DP == 64 ? 4 : 2;
+  static constexpr int KST = DP == 64 ? 4 : 3, VST = DP == 64 ? 4 : 2;
   static constexpr int Q = 0, DO = TILE, K = 2 * TILE, V = K + KST * TILE;
-  static constexpr int BUCKET = V + VST * TILE;                              // [16][MAX_BUCKETS] fp32
-  static constexpr int DIAG = BUCKET + (BIAS ? EW * MAX_BUCKETS * 4 : 0);    // [16][64] fp32
-  static constexpr int BAR = DIAG + (BIAS ? EW * 64 * 4 : 0);
+  static constexpr int BAR = V + VST * TILE;
   static constexpr int NBAR = 8 + 2 * KST + 2 * VST;
   static constexpr int BYTES = BAR + 8 * NBAR + 16 + 1024;
   static_assert(BYTES <= 232448, "more than 227 KB of shared memory");
@@ -131,7 +127,7 @@ __global__ void __launch_bounds__(NT, 1)
 xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                 const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                 const __grid_constant__ Plan p) {
-  using L = DqSmem<DP, BIAS>;
+  using L = DqSmem<DP>;
   constexpr int TILE = L::TILE, KST = L::KST, VST = L::VST;
   constexpr uint32_t IDESC_DQ = ptx::idesc_bf16_f32(128, DP, false, true);
   extern __shared__ uint8_t smem_raw[];
@@ -309,12 +305,6 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     const int qq = warp & 3, sub = (warp - 2) >> 2;  // lane quarter; columns 32 sub .. + 31
     const int row = qq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(qq * 32) << 16;
-    float* bucket = reinterpret_cast<float*>(gbase + L::BUCKET) + (warp - 2) * MAX_BUCKETS;
-    float* diag = reinterpret_cast<float*>(gbase + L::DIAG) + (warp - 2) * 64;
-    const bool grad = BIAS && a.bias_part != nullptr;
-    if (grad)
-      for (int u = lane; u < a.bias.buckets; u += 32) bucket[u] = 0.f;
-    __syncwarp();
     uint32_t g = 0, nf = 0;
     // this row's LSE (base 2) and delta of an item, read one item ahead
     auto stats = [&](int i, float& lse2, float& dlt) {
@@ -339,7 +329,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
       const float lse2 = lse2_next, dlt = dlt_next;
       stats(persistent_item(k + 1, cta, G), lse2_next, dlt_next);
       const int w0 = it.p0 + qq * 32;  // position of the warp's first query
-      float left = 0.f, right = 0.f, far_left = 0.f, far_right = 0.f;
+      float left = 0.f, right = 0.f;
       if (BIAS) {
         left = *a.bias.at(it.h, -a.bias.R);
         right = *a.bias.at(it.h, a.bias.R);
@@ -373,36 +363,24 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         uint32_t pk[16];  // dS as packed bf16 pairs (keys 2i, 2i+1 of these 32)
         if (full) {
           const uint64_t sc = f2_splat(mul), sh = f2_splat(shift), nd = f2_splat(-dlt);
-          uint64_t sum = 0ull;
 #pragma unroll
           for (int i2 = 0; i2 < 16; ++i2) {
             const uint64_t x = f2_fma(f2_pack(v[2 * i2], v[2 * i2 + 1]), sc, sh);
             const uint64_t pr = f2_pack(fast_exp2(f2_lo(x)), fast_exp2(f2_hi(x)));
             const uint64_t ds = f2_mul(pr, f2_add(f2_pack(w[2 * i2], w[2 * i2 + 1]), nd));
             pk[i2] = pack2(f2_lo(ds), f2_hi(ds));
-            if (BIAS) {
-              sum = f2_add(sum, ds);
-              v[2 * i2] = f2_lo(ds);
-              v[2 * i2 + 1] = f2_hi(ds);
-            }
           }
-          if (on_left) far_left += f2_lo(sum) + f2_hi(sum);
-          if (on_right) far_right += f2_lo(sum) + f2_hi(sum);
         } else {
           // keys kb + c with c >= nvis are past the diagonal or the sequence's keys (all
           // of them for a row past the queries)
           const int nvis = valid_q ? (a.causal ? min(w0 + lane + 1, it.len) : it.len) - kb : 0;
-          float sum = 0.f;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const float e = fast_exp2(fmaf(v[c], mul, shift));
             v[c] = c < nvis ? e * (w[c] - dlt) : 0.f;
-            if (BIAS) sum += v[c];
           }
 #pragma unroll
           for (int i2 = 0; i2 < 16; ++i2) pk[i2] = pack2(v[2 * i2], v[2 * i2 + 1]);
-          if (on_left) far_left += sum;
-          if (on_right) far_right += sum;
         }
         // the dS columns are free once the previous block's dQ MMAs are done
         if (g >= 1 && !warp_wait(ds_empty, (g - 1) & 1)) {
@@ -431,47 +409,8 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ds_full);
-        if (grad && near) {
-          // diagonal of element (r, c): c - r + 31
-          float run = 0.f;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            run = __shfl_up_sync(0xffffffffu, run, 1);
-            run = (lane == 0 ? 0.f : run) + v[c];
-            if (lane == 31) diag[c] = run;
-          }
-          if (lane < 31) diag[62 - lane] = run;
-          __syncwarp();
-          const int n0 = kb - w0 - 31;  // the distance of diagonal 0
-          for (int u = lane; u < a.bias.buckets; u += 32) {
-            const int2 r = a.bias.range[u];
-            float s = 0.f;
-            for (int x = max(0, r.x - n0); x <= min(62, r.y - n0); ++x) s += diag[x];
-            bucket[u] += s;
-          }
-          __syncwarp();
-        }
       }
       if (!ok) break;
-      if (grad) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          far_left += __shfl_xor_sync(~0u, far_left, o);
-          far_right += __shfl_xor_sync(~0u, far_right, o);
-        }
-        if (lane == 0) {
-          bucket[a.bias.left] += far_left;
-          bucket[a.bias.right] += far_right;
-        }
-        __syncwarp();
-        float* out = a.bias_part +
-                     ((((int64_t)it.h * a.B + it.b) * p.tiles + it.tile) * EW + (warp - 2)) * a.bias.buckets;
-        for (int u = lane; u < a.bias.buckets; u += 32) {
-          out[u] = bucket[u];
-          bucket[u] = 0.f;
-        }
-        __syncwarp();
-      }
       bool fin = true;
       float v0[32];
       if (it.n > 0) {
@@ -516,14 +455,20 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 // 608 threads: warp 0 TMA (K and V once, then Q_i and dO_i into a ring, each stage with
 // its queries' lse and delta), warp 1 TMEM and the S^T and dP^T MMAs (N = 64, two buffers),
 // warps 2..17 element-wise (lanes 32 (w % 4) .., one key row each, columns 16 ((w - 2) / 4) ..),
-// warp 18 the dV and dK MMAs, whose A operands P^T and dS^T lie in shared memory.
-template <int DP>
+// warp 18 the dV and dK MMAs.  A warp writes P^T and dS^T, packed, over the first 8 of
+// its own 16 columns of S^T and dP^T: one 16-query step of the accumulations' A operand,
+// read from tensor memory.  (From shared memory the operands' reads bound the kernel:
+// 224 KB a block at 128 bytes a clock against 1024 clocks of products, 160 KB so.)
+// TMEM: buffer b's S^T at 128 b .. + 63, dP^T at + 64 .., dV 256 .., dK 384 ..
+template <int DP, bool BIAS>
 struct KvSmem {
   static constexpr int TILE = tile_bytes<DP>(), T64 = TILE / 2;
-  static constexpr int QST = 4;
-  static constexpr int K = 0, V = TILE, Q = 2 * TILE, DO = Q + QST * T64, PT = DO + QST * T64, DST = PT + PB;
-  static constexpr int STAT = DST + PB;  // [stage][lse2[64] | delta[64]] fp32
-  static constexpr int BAR = STAT + QST * 2 * 64 * 4;
+  static constexpr int QST = DP == 64 ? 8 : BIAS ? 4 : 5;
+  static constexpr int K = 0, V = TILE, Q = 2 * TILE, DO = Q + QST * T64;
+  static constexpr int STAT = DO + QST * T64;                              // [stage][lse2[64] | delta[64]] fp32
+  static constexpr int BUCKET = STAT + QST * 2 * 64 * 4;                   // [16][MAX_BUCKETS] fp32
+  static constexpr int DIAG = BUCKET + (BIAS ? EW * MAX_BUCKETS * 4 : 0);  // [16][48] fp32
+  static constexpr int BAR = DIAG + (BIAS ? EW * 48 * 4 : 0);
   static constexpr int NBAR = 9 + 2 * QST;
   static constexpr int USED = BAR + 8 * NBAR + 16;
   // the tiles need 1024-byte alignment: the window starts so aligned on this GPU, and
@@ -532,20 +477,12 @@ struct KvSmem {
   static_assert(USED <= 232448, "more than 227 KB of shared memory");
 };
 
-// 8 words of packed pairs (columns 16 c .. + 15 of this row) into a 128-byte-swizzled
-// [128][64] buffer.
-__device__ __forceinline__ void store_quarter(uint8_t* buf, int row, int c, const uint32_t (&w)[8]) {
-  uint8_t* r = buf + row * 128;
-  *reinterpret_cast<uint4*>(r + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(r + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
 template <int DP, bool BIAS>
 __global__ void __launch_bounds__(NT, 1)
 xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                  const __grid_constant__ Plan p) {
-  using L = KvSmem<DP>;
+  using L = KvSmem<DP, BIAS>;
   constexpr int TILE = L::TILE, T64 = L::T64, QST = L::QST;
   constexpr uint32_t IDESC_ACC = ptx::idesc_bf16_f32(128, DP, false, true);
   extern __shared__ uint8_t smem_raw[];
@@ -557,10 +494,10 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   }
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + L::BAR;
-  const uint32_t bar_kv = bars, pd_full = bars + 8u, pd_empty = bars + 16u, bar_fin = bars + 24u;
-  const uint32_t sdp_drain = bars + 32u;
-  auto sdp_full = [&](int b) { return bars + 8u * (5 + b); };
-  auto sdp_empty = [&](int b) { return bars + 8u * (7 + b); };
+  const uint32_t bar_kv = bars, bar_fin = bars + 8u, sdp_drain = bars + 16u;
+  auto sdp_full = [&](int b) { return bars + 8u * (3 + b); };   // S^T and dP^T formed
+  auto pd_full = [&](int b) { return bars + 8u * (5 + b); };    // P^T and dS^T written over them
+  auto pd_empty = [&](int b) { return bars + 8u * (7 + b); };   // and read
   auto q_full = [&](int s) { return bars + 8u * (9 + s); };
   auto q_empty = [&](int s) { return bars + 8u * (9 + QST + s); };
   const uint32_t tslot = bars + 8u * L::NBAR;
@@ -570,13 +507,12 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 
   if (tid == 0) {
     ptx::mbar_init(bar_kv, 1);
-    ptx::mbar_init(pd_full, EW);
-    ptx::mbar_init(pd_empty, 1);
     ptx::mbar_init(bar_fin, 1);
     ptx::mbar_init(sdp_drain, 1);
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(sdp_full(b), 1);
-      ptx::mbar_init(sdp_empty(b), EW);
+      ptx::mbar_init(pd_full(b), EW);
+      ptx::mbar_init(pd_empty(b), 1);
     }
     for (int s = 0; s < 2 * QST; ++s) ptx::mbar_init(q_full(s), 1);
     ptx::fence_mbar_init();
@@ -676,7 +612,7 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       for (int ii = 0; ii < n && ok; ++ii) {  // S^T = K Q_i^T, dP^T = V dO_i^T into buffer ii % 2
         const int s = ii % QST, b = ii & 1;
         if (!wait1(q_full(s), (ii / QST) & 1) ||
-            (ii >= 2 && !wait1(sdp_empty(b), ((ii / 2) & 1) ^ 1))) {  // (block ii - 2 has been loaded)
+            (ii >= 2 && !wait1(pd_empty(b), ((ii / 2) & 1) ^ 1))) {  // (block ii - 2 is done with)
           ok = false;
           wait_failed(204);
           break;
@@ -700,8 +636,8 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   } else if (warp == ACC_WARP) {
     if (lane == 0 && n > 0) {
       for (int ii = 0; ii < n && ok; ++ii) {  // dV += P^T dO_i, dK += dS^T Q_i
-        const int s = ii % QST;
-        if (!wait1(pd_full, ii & 1)) {
+        const int s = ii % QST, b = ii & 1;
+        if (!wait1(pd_full(b), (ii / 2) & 1)) {
           ok = false;
           wait_failed(206);
           break;
@@ -711,12 +647,12 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const uint32_t accum = (ii > 0 || kk > 0) ? 1u : 0u;
-          ptx::mma_bf16(t_dv, kmajor_desc(base + L::PT, kk), mnmajor_desc(dt, kk, BOX64), IDESC_ACC, accum);
-          ptx::mma_bf16(t_dk, kmajor_desc(base + L::DST, kk), mnmajor_desc(qt, kk, BOX64), IDESC_ACC, accum);
+          ptx::mma_bf16_ts(t_dv, t_st(b) + 16u * kk, mnmajor_desc(dt, kk, BOX64), IDESC_ACC, accum);
+          ptx::mma_bf16_ts(t_dk, t_dpt(b) + 16u * kk, mnmajor_desc(qt, kk, BOX64), IDESC_ACC, accum);
         }
         // S^T, dP^T of block ii (which also read Q_i, dO_i) completed before P^T and
         // dS^T could be handed over: the stage is free once these MMAs are
-        ptx::mma_commit(pd_empty);
+        ptx::mma_commit(pd_empty(b));
         ptx::mma_commit(q_empty(s));
       }
       ptx::mma_commit(bar_fin);  // completes once every MMA this thread issued has
@@ -731,10 +667,38 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     const bool valid_k = kj < len;
     const uint32_t lane_off = (uint32_t)(qq * 32) << 16;
     int hh = 0, i = i0 - 1;
-    float left = 0.f, right = 0.f;
+    float left = 0.f, right = 0.f, far_left = 0.f, far_right = 0.f;
+    const bool grad = BIAS && a.bias_part != nullptr;
+    float* bucket = reinterpret_cast<float*>(gbase + L::BUCKET) + (warp - 2) * MAX_BUCKETS;
+    float* diag = reinterpret_cast<float*>(gbase + L::DIAG) + (warp - 2) * 48;
+    if (grad) {
+      for (int x = lane; x < a.bias.buckets; x += 32) bucket[x] = 0.f;
+      __syncwarp();
+    }
+    auto flush = [&](int head) {  // the warp's buckets of a finished head, and 0 for the next
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        far_left += __shfl_xor_sync(~0u, far_left, o);
+        far_right += __shfl_xor_sync(~0u, far_right, o);
+      }
+      if (lane == 0) {
+        bucket[a.bias.left] += far_left;
+        bucket[a.bias.right] += far_right;
+      }
+      __syncwarp();
+      far_left = far_right = 0.f;
+      float* out = a.bias_part + ((((int64_t)(g * a.share + head) * a.B + bb) * p.tiles + k0 / 128) * EW + (warp - 2)) *
+                                     a.bias.buckets;
+      for (int x = lane; x < a.bias.buckets; x += 32) {
+        out[x] = bucket[x];
+        bucket[x] = 0.f;
+      }
+      __syncwarp();
+    };
     for (int ii = 0; ii < n && ok; ++ii) {
       const int s = ii % QST, b = ii & 1;
       if (++i == i0 + per_head) {
+        if (grad) flush(hh);
         i = i0;
         ++hh;
       }
@@ -752,17 +716,15 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       ptx::tc_fence_after();
       float v[16], w[16];
       ptx::tmem_ld16x2(t_st(b) + lane_off + c * 16, t_dpt(b) + lane_off + c * 16, v, w);
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(sdp_empty(b));
       const float* st = stat + s * 128 + c * 16;  // lse of these 16 queries; delta at + 64
       const int qb = i * 64 + c * 16;
       float mul = p.scale_log2, add = 0.f;
+      const bool on_right = BIAS && kw - (p0 + qb + 15) >= a.bias.R;
+      const bool on_left = BIAS && !on_right && kw + 31 - (p0 + qb) <= -a.bias.R;
       if (BIAS) {
-        const int lo = kw - (p0 + qb + 15), hi = kw + 31 - (p0 + qb);
-        if (lo >= a.bias.R) {
+        if (on_right) {
           add = right;
-        } else if (hi <= -a.bias.R) {
+        } else if (on_left) {
           add = left;
         } else {
           const float* bv = a.bias.at(g * a.share + hh, kj - (p0 + qb));
@@ -791,6 +753,10 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             const uint64_t ds = f2_mul(pr, f2_add(f2_pack(w[x + e], w[x + e + 1]), f2_pack(-d0, -d1)));
             pp[(x + e) / 2] = pack2(f2_lo(pr), f2_hi(pr));
             pd[(x + e) / 2] = pack2(f2_lo(ds), f2_hi(ds));
+            if (BIAS) {
+              w[x + e] = f2_lo(ds);
+              w[x + e + 1] = f2_hi(ds);
+            }
           }
         }
       } else {
@@ -810,17 +776,43 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
           pd[x] = pack2(w[2 * x], w[2 * x + 1]);
         }
       }
-      // the P^T and dS^T buffers are free once block ii - 1's accumulation is done
-      if (ii >= 1 && !warp_wait(pd_empty, (ii - 1) & 1)) {
-        ok = false;
-        if (lane == 0) wait_failed(209);
-        break;
-      }
-      store_quarter(gbase + L::PT, row, c, pp);
-      store_quarter(gbase + L::DST, row, c, pd);
-      ptx::fence_async_smem();
+      ptx::tmem_st8_nowait(t_st(b) + lane_off + c * 16, pp);
+      ptx::tmem_st8_nowait(t_dpt(b) + lane_off + c * 16, pd);
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(pd_full);
+      if (lane == 0) ptx::mbar_arrive(pd_full(b));
+      if (!grad) continue;
+      if (!on_left && !on_right) {
+        // sums along the diagonals, that of element (r, x) r - x + 15
+        float run = 0.f;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          run = __shfl_up_sync(0xffffffffu, run, 1);
+          run = (lane == 0 ? 0.f : run) + w[x];
+          if (lane == 31) diag[46 - x] = run;
+        }
+        if (lane < 31) diag[lane] = run;
+        __syncwarp();
+        const int n0 = kw - (p0 + qb) - 15;  // the distance of diagonal 0
+        for (int x = lane; x < a.bias.buckets; x += 32) {
+          const int2 r = a.bias.range[x];
+          float y = 0.f;
+          for (int d = max(0, r.x - n0); d <= min(46, r.y - n0); ++d) y += diag[d];
+          bucket[x] += y;
+        }
+        __syncwarp();
+      } else {
+        float sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) sum += w[x];
+        if (on_left) far_left += sum;
+        else far_right += sum;
+      }
+    }
+    if (grad && ok) {  // (heads without blocks too: their partial sums are 0)
+      flush(hh);
+      for (int x = hh + 1; x < a.share; ++x) flush(x);
     }
     bool fin = true;
     if (n > 0) fin = warp_wait(bar_fin, 0);
@@ -869,8 +861,8 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
   OASES_TRY(map4d(&tdo64, a.d_o, a.sdo, a.D, a.Sq, a.H, a.B, 64));
   OASES_TRY(map4d(&tk, a.k, a.sk, a.D, a.Sk, a.G, a.B, 128));
   OASES_TRY(map4d(&tv, a.v, a.sv, a.D, a.Sk, a.G, a.B, 128));
-  using Dq = DqSmem<DP, BIAS>;
-  using Kv = KvSmem<DP>;
+  using Dq = DqSmem<DP>;
+  using Kv = KvSmem<DP, BIAS>;
   static DeviceOnce attr;
   OASES_TRY(attr.run([] {
     const cudaError_t e = cudaFuncSetAttribute(xattn_dq_kernel<DP, BIAS>,
@@ -890,10 +882,12 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
   const int64_t ctas = (int64_t)((a.Sk + 127) / 128) * a.B * a.G;
   if (items > INT32_MAX / 2 || ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   p.items = (int)items;
+  Plan pk = p;
+  pk.tiles = (a.Sk + 127) / 128;
   OASES_TRY(launch_pdl(xattn_dq_kernel<DP, BIAS>, dim3((unsigned)std::min<int64_t>(items, sm_count())), dim3(NT),
                        Dq::BYTES, st, tq128, tdo128, tk, tv, p));
   return launch_pdl(xattn_dkv_kernel<DP, BIAS>, dim3((unsigned)ctas), dim3(NT), Kv::BYTES, st, tk, tv, tq64,
-                    tdo64, p);
+                    tdo64, pk);
 }
 
 }  // namespace
