@@ -30,6 +30,13 @@ inline int current_device() {
   int d = 0;
   return cudaGetDevice(&d) == cudaSuccess ? d : 0;
 }
+// SMs of the current device (152 where there is none to ask).
+inline int sm_count() {
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, current_device()) != cudaSuccess) n = 0;
+  return n > 0 ? n : 152;
+}
+
 // Unique id of the calling thread's current CUDA context (the driver's
 // context id, never reused within the process), 0 if there is none yet.
 // Host caches of per-device state (events, streams, kernel attributes, device

@@ -28,7 +28,7 @@ namespace {
 
 enum class Partner { NONE, PAIRS, LANES, LOADS };
 constexpr int WARPS = 8;
-constexpr int BWD_CTAS_PER_SM = 4;
+constexpr int BWD_CTAS_PER_SM = 2;
 
 struct Tensor {
   const void* x;      // forward: input; backward: the same
@@ -47,11 +47,14 @@ struct QkArgs {
   const int64_t* positions;
   int64_t pos_batch;  // elements between sequences in positions (0: shared)
   int positions_len;
+  int tables16;       // cos and sin are 16-byte aligned
+  int batches;        // of rows in flight that a unit goes through
   int seq, D, rot, L;
   int units[2];       // units per token
   int64_t tokens, total;
   float eps;
-  float* part;        // backward: [blocks][2][D]
+  int q_blocks;       // backward: blocks that go through the queries, the others the keys
+  float* part;        // backward: [blocks][D]
 };
 
 // Eight values of a row as loaded.
@@ -98,6 +101,13 @@ struct Raw<float> {
     return r;
   }
 };
+// 8 values in fp32
+template <typename T>
+__device__ __forceinline__ void get8(const T* p, float (&f)[8]) {
+  Raw<T> r;
+  r.load(p);
+  r.get(f);
+}
 __device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&f)[8]) {
   uint32_t w[4];
 #pragma unroll
@@ -146,6 +156,23 @@ struct Place {
     const int half = a.rot / 2;
     const float* ct = a.cos + (good ? p : 0) * half;
     const float* st = a.sin + (good ? p : 0) * half;
+    if (P == Partner::LANES && i0 < a.rot) {  // rot % 16 == 0: a lane is on one side, 16 bytes aligned
+      const bool first = i0 < half;
+      const int at = first ? i0 : i0 - half;
+      if (a.tables16) {
+        get8(ct + at, c);
+        get8(st + at, s);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = ct[at + e], s[e] = st[at + e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        c[e] = good ? c[e] : NAN;
+        s[e] = !good ? NAN : first ? -s[e] : s[e];
+      }
+      return;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int i = i0 + e;
@@ -157,6 +184,17 @@ struct Place {
         const float v = good ? st[at] : NAN;
         s[e] = first ? -v : v;
       }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void partner_weights(const QkArgs& a, const T* w, const float (&own)[8],
+                                                  float (&o)[8]) const {
+    if (P == Partner::LANES) {
+      get8(w + 8 * lane, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o[e] = P == Partner::PAIRS ? own[e ^ 1] : P == Partner::LOADS ? ld_elem(w, partner(a, e)) : 0.f;
     }
   }
   // the partners' values of a row whose own values are `raw`
@@ -199,168 +237,189 @@ __device__ __forceinline__ Unit unit_of(const QkArgs& a, int64_t u, int heads_pe
   return r;
 }
 
-constexpr int FWD_ROWS = 4, BWD_ROWS = 2;  // rows of one lane in flight
+// rows of one lane in flight: what the registers hold
+constexpr int rows_in_flight(bool bwd, bool f32, Partner p) { return p == Partner::LOADS || (bwd && f32) ? 2 : 4; }
 
 template <typename T, Partner P>
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * WARPS, 3)
 qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int ROWS = rows_in_flight(false, sizeof(T) == 4, P);
   pdl_wait();
   pdl_trigger();
   const int64_t u = (int64_t)blockIdx.x * WARPS + threadIdx.x / 32;
   if (u >= a.total) return;
   const int groups = 32 / a.L, sub = threadIdx.x % 32 / a.L;
-  const Unit un = unit_of(a, u, FWD_ROWS * groups);
+  const Unit un = unit_of(a, u, ROWS * groups * a.batches);
   const Tensor& t = a.t[un.which];
   const Place<P> pl(a);
   const int64_t b = un.token / a.seq, tk = un.token - b * a.seq;
   const T* x = static_cast<const T*>(t.x) + b * t.xb + tk * t.xs;
-  Raw<T> raw[FWD_ROWS];
-  bool valid[FWD_ROWS];
-#pragma unroll
-  for (int k = 0; k < FWD_ROWS; ++k) {
-    const int h = un.h0 + k * groups + sub;
-    valid[k] = pl.active && h < t.heads;
-    raw[k].zero();
-    if (valid[k]) raw[k].load(x + h * t.xh + pl.i0);
-  }
+  T* y = static_cast<T*>(t.out) + b * t.yb + tk * t.ys;
+  const float over_d = 1.f / (float)a.D;
   float A[8], B[8];  // the factors of a value and of its partner
+  Raw<T> raw[ROWS];
+  auto load = [&](int batch) {
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int h = un.h0 + (batch * ROWS + k) * groups + sub;
+      raw[k].zero();
+      if (pl.active && h < t.heads) raw[k].load(x + h * t.xh + pl.i0);
+    }
+  };
+  load(0);
   pl.angles(a, un.token, A, B);
   if (t.w != nullptr && pl.active) {
     const T* w = static_cast<const T*>(t.w);
+    float own[8], other[8];
+    get8(w + pl.i0, own);
+    pl.template partner_weights<T>(a, w, own, other);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      A[e] *= ld_elem(w, pl.i0 + e);
-      if (P != Partner::NONE) B[e] *= ld_elem(w, pl.partner(a, e));
+      A[e] *= own[e];
+      if (P != Partner::NONE) B[e] *= other[e];
     }
   }
-  T* y = static_cast<T*>(t.out) + b * t.yb + tk * t.ys;
+  for (int batch = 0; batch < a.batches && un.h0 + batch * ROWS * groups < t.heads; ++batch) {
+    if (batch) load(batch);
 #pragma unroll
-  for (int k = 0; k < FWD_ROWS; ++k) {
-    const int h = un.h0 + k * groups + sub;
-    float v[8], o[8];
-    raw[k].get(v);
-    pl.partners(a, raw[k], v, x + h * t.xh, valid[k], o);
-    float ss = 0.f;
+    for (int k = 0; k < ROWS; ++k) {
+      const int h = un.h0 + (batch * ROWS + k) * groups + sub;
+      const bool valid = pl.active && h < t.heads;
+      float v[8], o[8];
+      raw[k].get(v);
+      pl.partners(a, raw[k], v, x + h * t.xh, valid, o);
+      float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-    const float r = 1.f / sqrtf(lanes_sum(ss, a.L) / (float)a.D + a.eps);
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+      const float r = 1.f / sqrtf(fmaf(lanes_sum(ss, a.L), over_d, a.eps));
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = r * (P == Partner::NONE ? v[e] * A[e] : fmaf(o[e], B[e], v[e] * A[e]));
-    __syncwarp();  // y may be x: a row's partners have been read
-    if (valid[k]) put8(y + h * t.yh + pl.i0, v);
+      for (int e = 0; e < 8; ++e)
+        v[e] = r * (P == Partner::NONE ? v[e] * A[e] : fmaf(o[e], B[e], v[e] * A[e]));
+      __syncwarp();  // y may be x: a row's partners have been read
+      if (valid) put8(y + h * t.yh + pl.i0, v);
+    }
   }
 }
 
 template <typename T, Partner P>
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * WARPS, 2)
 qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
-  __shared__ float red[2][WARPS][256];
+  constexpr int ROWS = rows_in_flight(true, sizeof(T) == 4, P);
+  __shared__ float red[WARPS][256];
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int groups = 32 / a.L, sub = lane / a.L;
   const Place<P> pl(a);
-  float dw[2][8] = {};
-  for (int64_t u = (int64_t)blockIdx.x * WARPS + warp; u < a.total; u += (int64_t)gridDim.x * WARPS) {
-    const Unit un = unit_of(a, u, BWD_ROWS * groups);
-    const Tensor& t = a.t[un.which];
-    const int64_t b = un.token / a.seq, tk = un.token - b * a.seq;
+  const float over_d = 1.f / (float)a.D;
+  const int which = (int)blockIdx.x >= a.q_blocks;
+  const int first = which ? a.q_blocks : 0, blocks = which ? gridDim.x - a.q_blocks : a.q_blocks;
+  const Tensor& t = a.t[which];
+  float dw[8] = {};
+  for (int64_t u = (int64_t)(blockIdx.x - first) * WARPS + warp; u < a.tokens * a.units[which];
+       u += (int64_t)blocks * WARPS) {
+    const int64_t token = u / a.units[which];
+    const int h0 = (int)(u - token * a.units[which]) * ROWS * groups * a.batches;
+    const int64_t b = token / a.seq, tk = token - b * a.seq;
     const T* x = static_cast<const T*>(t.x) + b * t.xb + tk * t.xs;
     const T* dy = static_cast<const T*>(t.dy) + b * t.yb + tk * t.ys;
-    Raw<T> rx[BWD_ROWS], rg[BWD_ROWS];
-    bool valid[BWD_ROWS];
-#pragma unroll
-    for (int k = 0; k < BWD_ROWS; ++k) {
-      const int h = un.h0 + k * groups + sub;
-      valid[k] = pl.active && h < t.heads;
-      rx[k].zero();
-      rg[k].zero();
-      if (valid[k]) {
-        rx[k].load(x + h * t.xh + pl.i0);
-        rg[k].load(dy + h * t.yh + pl.i0);
-      }
-    }
     float c[8], s[8], w[8];
-    pl.angles(a, un.token, c, s);
+    Raw<T> rx[ROWS], rg[ROWS];
+    auto load = [&](int batch) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      w[e] = t.w != nullptr && pl.active ? ld_elem(static_cast<const T*>(t.w), pl.i0 + e) : 1.f;
-    T* dx = t.out ? static_cast<T*>(t.out) + b * t.ob + tk * t.os : nullptr;
-    float add[8] = {};
-#pragma unroll
-    for (int k = 0; k < BWD_ROWS; ++k) {
-      const int h = un.h0 + k * groups + sub;
-      float xv[8], gv[8], o[8];
-      rx[k].get(xv);
-      rg[k].get(gv);
-      pl.partners(a, rg[k], gv, dy + h * t.yh, valid[k], o);
-      float ss = 0.f, sg = 0.f, gw[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (P != Partner::NONE) gv[e] = fmaf(-s[e], o[e], gv[e] * c[e]);  // R^T dy
-        gw[e] = gv[e] * w[e];
-        ss = fmaf(xv[e], xv[e], ss);
-        sg = fmaf(gw[e], xv[e], sg);
+      for (int k = 0; k < ROWS; ++k) {
+        const int h = h0 + (batch * ROWS + k) * groups + sub;
+        rx[k].zero();
+        rg[k].zero();
+        if (pl.active && h < t.heads) {
+          rx[k].load(x + h * t.xh + pl.i0);
+          rg[k].load(dy + h * t.yh + pl.i0);
+        }
       }
-      const float r = 1.f / sqrtf(lanes_sum(ss, a.L) / (float)a.D + a.eps);
-      const float m = lanes_sum(sg, a.L) / (float)a.D * r * r;
-      if (valid[k]) {
+    };
+    load(0);
+    pl.angles(a, token, c, s);
+    if (t.w != nullptr && pl.active) {
+      get8(static_cast<const T*>(t.w) + pl.i0, w);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) add[e] = fmaf(gv[e], xv[e] * r, add[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) gw[e] = r * fmaf(-xv[e], m, gw[e]);
-      __syncwarp();  // dx may be dy: a row's partners have been read
-      if (valid[k] && dx != nullptr) put8(dx + h * t.oh + pl.i0, gw);
+      for (int e = 0; e < 8; ++e) w[e] = 1.f;
     }
+    T* dx = t.out ? static_cast<T*>(t.out) + b * t.ob + tk * t.os : nullptr;
+    for (int batch = 0; batch < a.batches && h0 + batch * ROWS * groups < t.heads; ++batch) {
+      if (batch) load(batch);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {  // (uniform per warp)
-      if (un.which) dw[1][e] += add[e];
-      else dw[0][e] += add[e];
+      for (int k = 0; k < ROWS; ++k) {
+        const int h = h0 + (batch * ROWS + k) * groups + sub;
+        const bool valid = pl.active && h < t.heads;
+        float xv[8], gv[8], o[8];
+        rx[k].get(xv);
+        rg[k].get(gv);
+        pl.partners(a, rg[k], gv, dy + h * t.yh, valid, o);
+        float ss = 0.f, sg = 0.f, gw[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (P != Partner::NONE) gv[e] = fmaf(-s[e], o[e], gv[e] * c[e]);  // R^T dy
+          gw[e] = gv[e] * w[e];
+          ss = fmaf(xv[e], xv[e], ss);
+          sg = fmaf(gw[e], xv[e], sg);
+        }
+#pragma unroll 1
+        for (int o2 = a.L / 2; o2; o2 >>= 1) {
+          ss += __shfl_xor_sync(~0u, ss, o2);
+          sg += __shfl_xor_sync(~0u, sg, o2);
+        }
+        const float r = 1.f / sqrtf(fmaf(ss, over_d, a.eps));
+        const float m = sg * over_d * r * r;
+        if (valid) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dw[e] = fmaf(gv[e], xv[e] * r, dw[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gw[e] = r * fmaf(-xv[e], m, gw[e]);
+        __syncwarp();  // dx may be dy: a row's partners have been read
+        if (valid && dx != nullptr) put8(dx + h * t.oh + pl.i0, gw);
+      }
     }
   }
   if (a.part == nullptr) return;
   // over the warp's head groups, then over the warps, in a fixed order
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      for (int o = a.L; o < 32; o <<= 1) dw[q][e] += __shfl_xor_sync(~0u, dw[q][e], o);
-      if (lane < a.L && pl.active) red[q][warp][pl.i0 + e] = dw[q][e];
-    }
+  for (int e = 0; e < 8; ++e) {
+    for (int o = a.L; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(~0u, dw[e], o);
+    if (lane < a.L && pl.active) red[warp][pl.i0 + e] = dw[e];
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
-    const int q = i / a.D, d = i - q * a.D;
+  for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < WARPS; ++k) v += red[q][k][d];
-    a.part[(int64_t)blockIdx.x * 2 * a.D + i] = v;
+    for (int k = 0; k < WARPS; ++k) v += red[k][d];
+    a.part[(int64_t)blockIdx.x * a.D + d] = v;
   }
 }
 
 // Weights' gradients: the blocks' partial rows in a fixed order, 32 columns of a
 // block and 32 rows at a time.
 __global__ void __launch_bounds__(1024)
-qknorm_dw_kernel(const float* part, int blocks, int D, void* dwq, void* dwk, DType t, int accumulate) {
+qknorm_dw_kernel(const float* part, int q_blocks, int blocks, int D, void* dwq, void* dwk, DType t,
+                 int accumulate) {
   __shared__ float red[32][33];
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x * 32 + threadIdx.x % 32, r0 = threadIdx.x / 32;
+  const int last = blockIdx.y ? blocks : q_blocks;
   float v = 0.f;
-  if (c < 2 * D)
-    for (int r = r0; r < blocks; r += 32) v += part[(int64_t)r * 2 * D + c];
+  if (c < D)
+    for (int r = (blockIdx.y ? q_blocks : 0) + r0; r < last; r += 32) v += part[(int64_t)r * D + c];
   red[r0][threadIdx.x % 32] = v;
   __syncthreads();
-  if (r0 != 0 || c >= 2 * D) return;
+  void* out = blockIdx.y ? dwk : dwq;
+  if (r0 != 0 || c >= D || out == nullptr) return;
   v = 0.f;
 #pragma unroll
   for (int r = 0; r < 32; ++r) v += red[r][threadIdx.x];
-  void* out = c < D ? dwq : dwk;
-  const int64_t i = c < D ? c : c - D;
-  if (out == nullptr) return;
-  if (accumulate) v += static_cast<const float*>(out)[i];
-  store_any(out, t, i, v);
+  if (accumulate) v += static_cast<const float*>(out)[c];
+  store_any(out, t, c, v);
 }
 
 bool strides_ok(const oases_strides& s, int64_t esize, int batch, int seq, int heads) {
@@ -395,9 +454,16 @@ oases_status qk_check(const oases_qknorm_desc* d, bool backward) {
   return OASES_OK;
 }
 
+Partner partner_of(const oases_qknorm_desc* d) {
+  if (d->rot == 0) return Partner::NONE;
+  if (d->interleaved) return Partner::PAIRS;
+  return d->rot % 16 == 0 ? Partner::LANES : Partner::LOADS;
+}
+
 // The parts of the launch that follow from the descriptor.
-QkArgs qk_args(const oases_qknorm_desc* d, int rows) {
+QkArgs qk_args(const oases_qknorm_desc* d, bool bwd) {
   QkArgs a = {};
+  const int rows = rows_in_flight(bwd, d->dtype == OASES_F32, partner_of(d));
   a.seq = std::max(d->seq, 1);
   a.D = d->head_dim;
   a.rot = d->rot;
@@ -407,7 +473,14 @@ QkArgs qk_args(const oases_qknorm_desc* d, int rows) {
   a.pos_batch = d->positions_shared ? 0 : d->seq;
   a.eps = d->eps;
   a.tokens = (int64_t)d->batch * d->seq;
-  const int heads[2] = {d->heads, d->kv_heads}, per = rows * 32 / a.L;
+  // a unit goes through all of its token's heads where the tokens alone fill the GPU (64
+  // warps an SM), so that the angles and weights are loaded once; through one batch of
+  // rows in flight where they do not
+  const int heads[2] = {d->heads, d->kv_heads}, batch = rows * 32 / a.L;
+  const int most = std::max(1, (std::max(heads[0], heads[1]) + batch - 1) / batch);
+  a.batches = 1;
+  while (a.batches < most && a.tokens * 2 * (most / (a.batches + 1)) >= 64ll * sm_count()) ++a.batches;
+  const int per = batch * a.batches;
   const oases_strides* x[2] = {&d->q, &d->k};
   const oases_strides* y[2] = {&d->q_out, &d->k_out};
   const oases_strides* o[2] = {&d->dq, &d->dk};
@@ -423,16 +496,18 @@ QkArgs qk_args(const oases_qknorm_desc* d, int rows) {
   return a;
 }
 
-Partner partner_of(const oases_qknorm_desc* d) {
-  if (d->rot == 0) return Partner::NONE;
-  if (d->interleaved) return Partner::PAIRS;
-  return d->rot % 16 == 0 ? Partner::LANES : Partner::LOADS;
-}
-
-int bwd_blocks(const QkArgs& a) {
-  int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, current_device()) != cudaSuccess) sms = 0;
-  return (int)std::min<int64_t>((a.total + WARPS - 1) / WARPS, BWD_CTAS_PER_SM * (sms > 0 ? sms : 152));
+// Blocks of the backward, and how many of them go through the queries: in proportion.
+int bwd_blocks(const QkArgs& a, int* q_blocks) {
+  const int64_t u[2] = {a.tokens * a.units[0], a.tokens * a.units[1]};
+  const int64_t need[2] = {(u[0] + WARPS - 1) / WARPS, (u[1] + WARPS - 1) / WARPS};
+  const int64_t most = BWD_CTAS_PER_SM * sm_count();
+  if (need[0] + need[1] <= most) {
+    *q_blocks = (int)need[0];
+    return (int)(need[0] + need[1]);
+  }
+  const int64_t q = most * u[0] / (u[0] + u[1]);
+  *q_blocks = (int)std::max<int64_t>(need[0] > 0, std::min<int64_t>(q, most - (need[1] > 0)));
+  return (int)most;
 }
 
 template <typename T, bool BWD>
@@ -457,8 +532,9 @@ cudaError_t launch(Partner p, const QkArgs& a, int blocks, cudaStream_t st) {
 extern "C" size_t oases_qknorm_workspace_bytes(const oases_qknorm_desc* desc) {
   using namespace oases;
   if (qk_check(desc, false) != OASES_OK) return 0;
-  const QkArgs a = qk_args(desc, BWD_ROWS);
-  return a.total == 0 ? 0 : align256((size_t)bwd_blocks(a) * 2 * a.D * 4);
+  const QkArgs a = qk_args(desc, true);
+  int q_blocks;
+  return a.total == 0 ? 0 : align256((size_t)bwd_blocks(a, &q_blocks) * a.D * 4);
 }
 
 extern "C" oases_status oases_qknorm_fwd(const oases_qknorm_desc* desc, const void* q, const void* k,
@@ -473,7 +549,7 @@ extern "C" oases_status oases_qknorm_fwd(const oases_qknorm_desc* desc, const vo
   if (misaligned({q, k, q_weight, k_weight, q_out, k_out}, 16) || misaligned({cos, sin}, 4) ||
       misaligned({positions}, 8))
     return OASES_ERR_INVALID_ARG;
-  QkArgs a = qk_args(desc, FWD_ROWS);
+  QkArgs a = qk_args(desc, false);
   if (a.total == 0) return OASES_OK;
   if ((desc->heads && (!q || !q_out)) || (desc->kv_heads && (!k || !k_out)) ||
       (desc->rot && (!cos || !sin)))
@@ -481,7 +557,7 @@ extern "C" oases_status oases_qknorm_fwd(const oases_qknorm_desc* desc, const vo
   if ((a.total + WARPS - 1) / WARPS > INT32_MAX) return OASES_ERR_UNSUPPORTED;
   a.t[0].x = q, a.t[0].out = q_out, a.t[0].w = q_weight;
   a.t[1].x = k, a.t[1].out = k_out, a.t[1].w = k_weight;
-  a.cos = cos, a.sin = sin, a.positions = positions;
+  a.cos = cos, a.sin = sin, a.positions = positions, a.tables16 = !misaligned({cos, sin}, 16);
   const int blocks = (int)((a.total + WARPS - 1) / WARPS);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return api_end(desc->dtype == OASES_F32
@@ -504,7 +580,7 @@ extern "C" oases_status oases_qknorm_bwd(const oases_qknorm_desc* desc, const vo
     return OASES_ERR_INVALID_ARG;
   if ((dq_weight && !q_weight) || (dk_weight && !k_weight)) return OASES_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  QkArgs a = qk_args(desc, BWD_ROWS);
+  QkArgs a = qk_args(desc, true);
   if (a.total == 0) {  // sums over no rows
     if (desc->accumulate) return OASES_OK;
     const size_t n = (size_t)a.D * dtype_size(static_cast<DType>(desc->grad_dtype));
@@ -516,20 +592,20 @@ extern "C" oases_status oases_qknorm_bwd(const oases_qknorm_desc* desc, const vo
   if ((desc->heads && (!q || !dq_out)) || (desc->kv_heads && (!k || !dk_out)) ||
       (desc->rot && (!cos || !sin)))
     return OASES_ERR_INVALID_ARG;
-  const int blocks = bwd_blocks(a);
+  const int blocks = bwd_blocks(a, &a.q_blocks);
   const bool weights = dq_weight || dk_weight;
-  if (weights && (!workspace || ws_bytes < align256((size_t)blocks * 2 * a.D * 4)))
+  if (weights && (!workspace || ws_bytes < align256((size_t)blocks * a.D * 4)))
     return OASES_ERR_WORKSPACE;
   a.t[0].x = q, a.t[0].dy = dq_out, a.t[0].out = dq, a.t[0].w = q_weight;
   a.t[1].x = k, a.t[1].dy = dk_out, a.t[1].out = dk, a.t[1].w = k_weight;
-  a.cos = cos, a.sin = sin, a.positions = positions;
+  a.cos = cos, a.sin = sin, a.positions = positions, a.tables16 = !misaligned({cos, sin}, 16);
   a.part = weights ? static_cast<float*>(workspace) : nullptr;
   cudaError_t e = desc->dtype == OASES_F32
                       ? launch<float, true>(partner_of(desc), a, blocks, st)
                       : launch<__nv_bfloat16, true>(partner_of(desc), a, blocks, st);
   if (e == cudaSuccess && weights)
-    e = launch_pdl(qknorm_dw_kernel, dim3((2 * a.D + 31) / 32), dim3(1024), 0, st,
-                   (const float*)a.part, blocks, a.D, dq_weight, dk_weight,
+    e = launch_pdl(qknorm_dw_kernel, dim3((a.D + 31) / 32, 2), dim3(1024), 0, st,
+                   (const float*)a.part, a.q_blocks, blocks, a.D, dq_weight, dk_weight,
                    static_cast<DType>(desc->grad_dtype), desc->accumulate);
   return api_end(e);
 }

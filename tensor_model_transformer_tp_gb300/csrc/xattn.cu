@@ -42,11 +42,6 @@ struct Big {
   }
 };
 
-// Of one sign's N buckets, the smallest distance of each but the first.
-struct Borders {
-  int n;  // N - 1
-  int at[MAX_BUCKETS];
-};
 Borders borders(int N, int max_distance) {
   Borders r;
   const int E = N / 2, L = N - E;
@@ -165,13 +160,7 @@ xattn_bias_kernel(const T* table, float* value, int2* range, const __grid_consta
   if (i >= pitch) return;
   const int n = i - (R + BIAS_PAD);
   const int x = bidirectional ? abs(n) : max(-n, 0);
-  int lo = 0, hi = border.n;  // the number of borders at or below x
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (border.at[mid] <= x) lo = mid + 1;
-    else hi = mid;
-  }
-  const int bucket = lo + (bidirectional && n > 0 ? N : 0);
+  const int bucket = border.bucket(x) + (bidirectional && n > 0 ? N : 0);
   const float v = ld_elem(table, (int64_t)bucket * heads + h);
   float w = v * factor;
   if (fabsf(v) < INFINITY) w = fminf(fmaxf(w, -3.402823466e38f), 3.402823466e38f);
@@ -262,7 +251,7 @@ Layout layout(const Shape& s, bool backward) {
   };
   const Args& a = s.a;
   if (a.B == 0 || a.Sq == 0 || a.Sk == 0) return l;
-  if (a.bias.buckets) {
+  if (a.bias.buckets && (backward || !xattn_few_takes(a))) {
     take(&l.value, (size_t)a.H * a.bias.pitch * 4);
     take(&l.range, (size_t)a.bias.buckets * 8);
   }
@@ -345,12 +334,13 @@ cudaError_t forward(Shape& s, const void* bias, char* ws, cudaStream_t st) {
   }
   const Layout l = layout(s, false);
   const bool few = xattn_few_takes(a);
-  if (a.bias.buckets)
-    OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, few || a.t == DType::BF16 ? LOG2E : 1.f, st));
+  if (a.bias.buckets && !few)
+    OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, a.t == DType::BF16 ? LOG2E : 1.f, st));
   a.splits = l.splits;
   a.part_o = reinterpret_cast<float*>(ws + l.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + l.part_lse);
-  OASES_TRY(few ? xattn_few(a, st) : a.t == DType::BF16 ? xattn_fwd_tc(a, st) : xattn_fwd_f32(a, st));
+  OASES_TRY(few ? xattn_few(a, bias, s.border, s.bidirectional, st)
+                : a.t == DType::BF16 ? xattn_fwd_tc(a, st) : xattn_fwd_f32(a, st));
   return a.splits > 1 ? join_splits(a, st) : cudaSuccess;
 }
 

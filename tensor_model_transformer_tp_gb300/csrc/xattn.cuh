@@ -15,6 +15,22 @@ struct Strides {
 constexpr int MAX_BUCKETS = 128;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
 
+// Of one sign's n + 1 buckets, the smallest distance of each but the first.
+struct Borders {
+  int n;
+  int at[MAX_BUCKETS];
+  // the bucket of distance x
+  __host__ __device__ int bucket(int x) const {
+    int lo = 0, hi = n;  // the number of borders at or below x
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (at[mid] <= x) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo;
+  }
+};
+
 // The bias by distance, written to the workspace by bias_tables(): for every head the
 // values at n = -(R + PAD) .. R + PAD, where R is the distance from which the bucket no
 // longer changes; the PAD places beyond repeat the ends, so that a tile that holds some
@@ -62,19 +78,13 @@ struct Args {
   }
 };
 
-// SMs of the current device (152 where there is none to ask).
-inline int sm_count() {
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, current_device()) != cudaSuccess) n = 0;
-  return n > 0 ? n : 152;
-}
-
 }  // namespace xattn
 
 // forward of a few rows a key head, any type
 bool xattn_few_takes(const xattn::Args& a);
 int xattn_few_splits(const xattn::Args& a);
-cudaError_t xattn_few(const xattn::Args& a, cudaStream_t st);
+cudaError_t xattn_few(const xattn::Args& a, const void* table, const xattn::Borders& border,
+                      bool bidirectional, cudaStream_t st);
 // bf16, tensor cores
 cudaError_t xattn_fwd_tc(const xattn::Args& a, cudaStream_t st);
 cudaError_t xattn_bwd_tc(const xattn::Args& a, cudaStream_t st);

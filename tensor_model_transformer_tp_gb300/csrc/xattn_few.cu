@@ -9,6 +9,8 @@
 // CTAs shares the keys that the sequence has (so that ragged batches stay even) and
 // joins its groups' results through distributed shared memory; only where sequences and
 // key heads are too few for the GPU are the keys split further, through memory.
+// The position bias: R or more away one value on each side, kept in a register; nearer,
+// the bucket is searched for and the table read (no table by distance is made).
 #include <math.h>
 
 #include <algorithm>
@@ -40,10 +42,24 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&f)[EPL<T>]) {
   }
 }
 
+// The bias's table in x's type, and what finds a bucket.
+struct Table {
+  const void* p;
+  Borders border;
+  int bidirectional;
+  // bias of head h at relative position n, in units of log2(e); finite values stay so
+  template <typename T>
+  __device__ __forceinline__ float at(int heads, int h, int n) const {
+    const int u = border.bucket(bidirectional ? abs(n) : max(-n, 0)) + (bidirectional && n > 0 ? border.n + 1 : 0);
+    const float v = ld_elem(static_cast<const T*>(p), (int64_t)u * heads + h);
+    return fabsf(v) < INFINITY ? fminf(fmaxf(v * LOG2E, -3.402823466e38f), 3.402823466e38f) : v;
+  }
+};
+
 // LPK lanes a key, R rows (query i, query head hh of the group: row i share + hh).
 template <typename T, int LPK, int R>
 __global__ void __launch_bounds__(NT)
-xattn_few_kernel(const __grid_constant__ Args a, int rows) {
+xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table table, int rows) {
   constexpr int E = EPL<T>, GROUPS = 32 / LPK, KU = R == 1 ? 4 : 2, D_MAX = LPK * E;
   __shared__ float red_o[WARPS][R][D_MAX], red_m[WARPS][R], red_l[WARPS][R];
   __shared__ float out_o[R][D_MAX], out_m[R], out_l[R];
@@ -63,6 +79,7 @@ xattn_few_kernel(const __grid_constant__ Args a, int rows) {
 
   float q[R][E], acc[R][E], m[R], l[R];
   int vis[R], pos[R];
+  float left[R], right[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int i = r / a.share, h = g * a.share + r % a.share;
@@ -72,6 +89,11 @@ xattn_few_kernel(const __grid_constant__ Args a, int rows) {
       v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + b * a.sq.b + i * a.sq.s + h * a.sq.h + sub * E);
     unpack<T>(v, q[r]);
     pos[r] = p0 + i;
+    left[r] = right[r] = 0.f;
+    if (a.bias.buckets && in) {
+      left[r] = table.at<T>(a.H, h, -a.bias.R);
+      right[r] = table.at<T>(a.H, h, a.bias.R);
+    }
     vis[r] = !in ? 0 : a.causal ? min(len, p0 + i + 1) : len;
     m[r] = -INFINITY;
     l[r] = 0.f;
@@ -83,17 +105,26 @@ xattn_few_kernel(const __grid_constant__ Args a, int rows) {
   }
   const T* kp = static_cast<const T*>(a.k) + b * a.sk.b + g * a.sk.h + sub * E;
   const T* vp = static_cast<const T*>(a.v) + b * a.sv.b + g * a.sv.h + sub * E;
-  for (int k0 = k_begin + warp * GROUPS * KU + grp; k0 - grp < k_end; k0 += STEP) {
-    uint4 kv[KU], vv[KU];
+  // a step's keys and values are loaded while the step before is worked on
+  uint4 kn[KU], vn[KU];
+  auto load = [&](int k0) {
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
       const int key = k0 + u * GROUPS;
-      kv[u] = vv[u] = make_uint4(0, 0, 0, 0);
+      kn[u] = vn[u] = make_uint4(0, 0, 0, 0);
       if (key < k_end && cols) {
-        kv[u] = *reinterpret_cast<const uint4*>(kp + key * a.sk.s);
-        vv[u] = *reinterpret_cast<const uint4*>(vp + key * a.sv.s);
+        kn[u] = *reinterpret_cast<const uint4*>(kp + key * a.sk.s);
+        vn[u] = *reinterpret_cast<const uint4*>(vp + key * a.sv.s);
       }
     }
+  };
+  const int k_first = k_begin + warp * GROUPS * KU + grp;
+  load(k_first);
+  for (int k0 = k_first; k0 - grp < k_end; k0 += STEP) {
+    uint4 kv[KU], vv[KU];
+#pragma unroll
+    for (int u = 0; u < KU; ++u) kv[u] = kn[u], vv[u] = vn[u];
+    load(k0 + STEP);
     float s[R][KU];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
@@ -120,7 +151,10 @@ xattn_few_kernel(const __grid_constant__ Args a, int rows) {
 #pragma unroll
       for (int u = 0; u < KU; ++u) {
         const int key = k0 + u * GROUPS;
-        if (a.bias.buckets && r < rows) s[r][u] += a.bias.clamped(h, key - pos[r]);
+        if (a.bias.buckets && r < rows) {
+          const int n = key - pos[r];
+          s[r][u] += n <= -a.bias.R ? left[r] : n >= a.bias.R ? right[r] : table.at<T>(a.H, h, n);
+        }
         if (key >= k_end || key >= vis[r]) s[r][u] = -INFINITY;
         mx = fmaxf(mx, s[r][u]);
       }
@@ -220,7 +254,7 @@ xattn_few_kernel(const __grid_constant__ Args a, int rows) {
 }
 
 template <typename T, int LPK, int R>
-cudaError_t launch(const Args& a, int rows, int csize, cudaStream_t st) {
+cudaError_t launch(const Args& a, const Table& tb, int rows, int csize, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(csize * a.splits, a.B * a.G);
   cfg.blockDim = dim3(NT);
@@ -234,19 +268,21 @@ cudaError_t launch(const Args& a, int rows, int csize, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   ++g_launch_count;
-  return cudaLaunchKernelEx(&cfg, xattn_few_kernel<T, LPK, R>, a, rows);
+  return cudaLaunchKernelEx(&cfg, xattn_few_kernel<T, LPK, R>, a, tb, rows);
 }
 template <typename T, int LPK>
-cudaError_t launch_rows(const Args& a, int rows, int csize, cudaStream_t st) {
-  return rows == 1   ? launch<T, LPK, 1>(a, rows, csize, st)
-         : rows == 2 ? launch<T, LPK, 2>(a, rows, csize, st)
-                     : launch<T, LPK, 4>(a, rows, csize, st);
+cudaError_t launch_rows(const Args& a, const Table& tb, int rows, int csize, cudaStream_t st) {
+  return rows == 1   ? launch<T, LPK, 1>(a, tb, rows, csize, st)
+         : rows == 2 ? launch<T, LPK, 2>(a, tb, rows, csize, st)
+                     : launch<T, LPK, 4>(a, tb, rows, csize, st);
 }
 
-// CTAs of a cluster: at least 128 keys each.
-int cluster_size(int Sk) {
+// CTAs of a cluster: two an SM in all, with 256 keys each at least (at 320 sequences and
+// key heads of up to 1500 keys of 64 values, clusters of 1, 2, 4, 8: 15, 19, 21, 34 us:
+// a CTA's start and the join cost more than its keys).
+int cluster_size(const Args& a) {
   int c = 1;
-  while (c < MAX_CLUSTER && Sk >= 256 * c) c *= 2;
+  while (c < MAX_CLUSTER && (int64_t)a.B * a.G * c < 2 * sm_count() && a.Sk >= 512 * c) c *= 2;
   return c;
 }
 
@@ -258,22 +294,24 @@ int cluster_size(int Sk) {
 bool xattn_few_takes(const Args& a) {
   return (int64_t)a.Sq * a.share <= 4 && (int64_t)a.B * a.G <= 65535;
 }
-// Shares of the keys beyond the cluster's: four CTAs an SM, and 512 keys to a CTA at least.
+// Shares of the keys beyond the cluster's: two CTAs an SM, and 512 keys to a CTA at least.
 int xattn_few_splits(const Args& a) {
-  const int c = cluster_size(a.Sk);
-  const int64_t ctas = (int64_t)a.B * a.G * c, places = 4 * sm_count();
+  const int c = cluster_size(a);
+  const int64_t ctas = (int64_t)a.B * a.G * c, places = 2 * sm_count();
   if (c < MAX_CLUSTER || ctas >= places) return 1;
   return (int)std::max<int64_t>(1, std::min<int64_t>(places / ctas, a.Sk / (512 * c)));
 }
-cudaError_t xattn_few(const Args& a, cudaStream_t st) {
-  const int rows = a.Sq * a.share, c = cluster_size(a.Sk), chunks = a.D * (int)dtype_size(a.t) / 16;
+cudaError_t xattn_few(const Args& a, const void* table, const Borders& border, bool bidirectional,
+                      cudaStream_t st) {
+  const Table tb{table, border, bidirectional ? 1 : 0};
+  const int rows = a.Sq * a.share, c = cluster_size(a), chunks = a.D * (int)dtype_size(a.t) / 16;
   if (a.t == DType::BF16)
-    return chunks <= 4   ? launch_rows<__nv_bfloat16, 4>(a, rows, c, st)
-           : chunks <= 8 ? launch_rows<__nv_bfloat16, 8>(a, rows, c, st)
-                         : launch_rows<__nv_bfloat16, 16>(a, rows, c, st);
-  return chunks <= 8    ? launch_rows<float, 8>(a, rows, c, st)
-         : chunks <= 16 ? launch_rows<float, 16>(a, rows, c, st)
-                        : launch_rows<float, 32>(a, rows, c, st);
+    return chunks <= 4   ? launch_rows<__nv_bfloat16, 4>(a, tb, rows, c, st)
+           : chunks <= 8 ? launch_rows<__nv_bfloat16, 8>(a, tb, rows, c, st)
+                         : launch_rows<__nv_bfloat16, 16>(a, tb, rows, c, st);
+  return chunks <= 8    ? launch_rows<float, 8>(a, tb, rows, c, st)
+         : chunks <= 16 ? launch_rows<float, 16>(a, tb, rows, c, st)
+                        : launch_rows<float, 32>(a, tb, rows, c, st);
 }
 
 }  // namespace oases

@@ -388,6 +388,9 @@ def _attn_common(q, k, v, kv_lens, q_start, bias, causal, start, scale, max_dist
                 scale=D ** -0.5 if scale is None else scale, q=sq, k=sk, v=sv)
 
 
+_NO_OUT = (None, None, None)
+
+
 def _row_strides(shape) -> Strides:
     """Of a contiguous [batch, tokens, heads, head_dim] tensor."""
     B, S, H, D = shape
@@ -417,6 +420,11 @@ def _attn_bwd_plan(q, k, v, o, lse, do, outs, kv_lens, q_start, bias, dbias, nee
     d.accumulate = int(dbias is not None)
     d.grad_dtype = 0 if dbias is not None else d.dtype
     return ctypes.byref(d), *_sized(q[3], (oases_attn_workspace_bytes, d, True))
+
+
+def _out(x: Optional[torch.Tensor], given: Optional[torch.Tensor]):
+    return torch.empty_like(x, memory_format=torch.contiguous_format) \
+        if given is None and x is not None else given
 
 
 def _start(q_start):
@@ -453,8 +461,8 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     desc, n_ws, stat = _attn_fwd_plan(
         _view(q), _view(k), _view(v), _sig(kv_lens), _sig(start), _sig(bias),
         *_options(causal, number, scale, max_distance, bidirectional))
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(stat, dtype=torch.float32, device=q.device)
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = q.new_empty(stat, dtype=torch.float32)
     _call(lib().oases_attn_fwd, q.get_device(), n_ws, desc, _ptr(q), _ptr(k), _ptr(v),
           _ptr(kv_lens), _ptr(start), _ptr(bias), _ptr(o), _ptr(lse))
     return o, lse
@@ -465,7 +473,7 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
              causal: bool = False, q_start: Union[int, torch.Tensor, None] = None,
              scale: Optional[float] = None, bias: Optional[torch.Tensor] = None,
              max_distance: int = 128, bidirectional: Optional[bool] = None,
-             out: Tuple[Optional[torch.Tensor], ...] = (None, None, None),
+             out: Tuple[Optional[torch.Tensor], ...] = _NO_OUT,
              dbias: Optional[torch.Tensor] = None, need_dbias: bool = True
              ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
     """Gradients (dq, dk, dv, dbias) of attn_fwd for the gradient do of o, with the same
@@ -479,11 +487,10 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     """
     start, number = _start(q_start)
     desc, n_ws = _attn_bwd_plan(
-        _view(q), _view(k), _view(v), _view(o), _sig(lse), _view(do), tuple(map(_view, out)),
+        _view(q), _view(k), _view(v), _view(o), _sig(lse), _view(do), _NO_OUT if out is _NO_OUT else tuple(map(_view, out)),
         _sig(kv_lens), _sig(start), _sig(bias), _sig(dbias), bool(need_dbias),
         *_options(causal, number, scale, max_distance, bidirectional))
-    dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if t is None else t
-                  for x, t in zip((q, k, v), out))
+    dq, dk, dv = _out(q, out[0]), _out(k, out[1]), _out(v, out[2])
     if dbias is None and bias is not None and need_dbias:
         dbias = torch.empty_like(bias)
     _call(lib().oases_attn_bwd, q.get_device(), n_ws, desc, _ptr(q), _ptr(k), _ptr(v),
@@ -561,11 +568,6 @@ def _qknorm_bwd_plan(q, k, dqo, dko, outs, grads, *rest):
     d.accumulate = int(accumulate)
     d.grad_dtype = 0 if accumulate else d.dtype
     return ctypes.byref(d), *_sized(q[3], (oases_qknorm_workspace_bytes, d))
-
-
-def _out(x: Optional[torch.Tensor], given: Optional[torch.Tensor]):
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device) if given is None and x is not None \
-        else given
 
 
 def qk_norm_rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], cos: Optional[torch.Tensor],
