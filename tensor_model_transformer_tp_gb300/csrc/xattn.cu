@@ -119,6 +119,7 @@ oases_status shape(const oases_attn_desc* d, bool backward, Shape* s) {
   a.q_start0 = d->q_start;
   a.scale = d->scale;
   a.splits = 1;
+  a.q_pitch = (Sq + 127) / 128 * 128;
   s->grad_f32 = d->grad_dtype == OASES_F32;
   s->accumulate = d->accumulate != 0;
   if (N) {
@@ -137,10 +138,10 @@ oases_status shape(const oases_attn_desc* d, bool backward, Shape* s) {
 
 // ---- the bias by distance ---------------------------------------------------------
 // value[h][n + R + PAD] = factor * table[bucket(n)][h], and the run of distances of
-// each bucket.  A finite value stays finite behind the factor.
+// each bucket, and the bucket of each n.  A finite value stays finite behind the factor.
 template <typename T>
 __global__ void __launch_bounds__(256)
-xattn_bias_kernel(const T* table, float* value, int2* range, const __grid_constant__ Borders border,
+xattn_bias_kernel(const T* table, float* value, int2* range, uint8_t* index, const __grid_constant__ Borders border,
                   int heads, int pitch, int R, int buckets, int bidirectional, float factor) {
   pdl_wait();
   pdl_trigger();
@@ -161,6 +162,7 @@ xattn_bias_kernel(const T* table, float* value, int2* range, const __grid_consta
   const int n = i - (R + BIAS_PAD);
   const int x = bidirectional ? abs(n) : max(-n, 0);
   const int bucket = border.bucket(x) + (bidirectional && n > 0 ? N : 0);
+  if (h == 0 && abs(n) <= R) index[n + R] = (uint8_t)bucket;
   const float v = ld_elem(table, (int64_t)bucket * heads + h);
   float w = v * factor;
   if (fabsf(v) < INFINITY) w = fminf(fmaxf(w, -3.402823466e38f), 3.402823466e38f);
@@ -239,7 +241,8 @@ cudaError_t join_splits(const Args& a, cudaStream_t st) {
 
 // ---- workspace ---------------------------------------------------------------------
 struct Layout {
-  size_t value = 0, range = 0, delta = 0, part = 0, part_o = 0, part_lse = 0, total = 0;
+  size_t value = 0, range = 0, index = 0, delta = 0, part = 0, part_o = 0, part_lse = 0, total = 0;
+  size_t neg_lse2 = 0, piece_dq = 0, piece_dkv = 0;
   int splits = 1;
   int64_t rows = 0;  // partial rows of the bias gradient, for each head
 };
@@ -254,6 +257,7 @@ Layout layout(const Shape& s, bool backward) {
   if (a.bias.buckets && (backward || !xattn_few_takes(a))) {
     take(&l.value, (size_t)a.H * a.bias.pitch * 4);
     take(&l.range, (size_t)a.bias.buckets * 8);
+    take(&l.index, (size_t)2 * s.R + 1);
   }
   if (!backward) {
     const int sms = sm_count();
@@ -268,9 +272,17 @@ Layout layout(const Shape& s, bool backward) {
       take(&l.part_lse, (size_t)l.splits * a.B * a.Sq * a.H * 4);
     }
   } else {
-    take(&l.delta, (size_t)a.B * a.H * a.Sq * 4);
+    take(&l.delta, (size_t)a.B * a.H * a.q_pitch * 4);
+    if (a.t == DType::BF16) take(&l.neg_lse2, (size_t)a.B * a.H * a.q_pitch * 4);
+    l.rows = (int64_t)a.B * ((a.Sq + 63) / 64);
+    BwdCut cut;
+    if (a.t == DType::BF16 && xattn_bwd_cut(a, &cut)) {  // (else the call itself refuses)
+      if (cut.dq.pieces > 1) take(&l.piece_dq, (size_t)cut.dq.rest * cut.dq.pieces * 128 * a.D * 4);
+      if (cut.dkv.pieces > 1) take(&l.piece_dkv, (size_t)cut.dkv.rest * cut.dkv.pieces * 2 * 128 * a.D * 4);
+      const int64_t tiles = (int64_t)a.B * ((a.Sk + 127) / 128);  // as kv_item() counts them
+      l.rows = (tiles + (tiles - cut.dkv.whole / a.G) * (cut.dkv.pieces - 1)) * DKV_WARPS;
+    }
     if (a.bias.buckets) {
-      l.rows = (int64_t)a.B * (a.t == DType::BF16 ? (a.Sk + 127) / 128 * 16 : (a.Sq + 63) / 64);
       take(&l.part, (size_t)l.rows * a.H * a.bias.buckets * 4);
     }
   }
@@ -285,12 +297,14 @@ cudaError_t bias_tables(const Shape& s, const void* table, char* ws, const Layou
   int2* range = reinterpret_cast<int2*>(ws + l.range);
   out->value = value;
   out->range = range;
+  uint8_t* index = reinterpret_cast<uint8_t*>(ws + l.index);
+  out->index = index;
   const dim3 grid((b.pitch + 255) / 256, s.a.H);
   if (s.a.t == DType::F32)
-    return launch_pdl(xattn_bias_kernel<float>, grid, dim3(256), 0, st, (const float*)table, value, range,
+    return launch_pdl(xattn_bias_kernel<float>, grid, dim3(256), 0, st, (const float*)table, value, range, index,
                       s.border, s.a.H, b.pitch, s.R, b.buckets, (int)s.bidirectional, factor);
   return launch_pdl(xattn_bias_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
-                    (const __nv_bfloat16*)table, value, range, s.border, s.a.H, b.pitch, s.R,
+                    (const __nv_bfloat16*)table, value, range, index, s.border, s.a.H, b.pitch, s.R,
                     b.buckets, (int)s.bidirectional, factor);
 }
 
@@ -357,6 +371,10 @@ cudaError_t backward(Shape& s, const void* bias, void* dbias, char* ws, cudaStre
   const Layout l = layout(s, true);
   if (a.bias.buckets) OASES_TRY(bias_tables(s, bias, ws, l, &a.bias, a.t == DType::BF16 ? LOG2E : 1.f, st));
   a.delta = reinterpret_cast<float*>(ws + l.delta);
+  a.neg_lse2 = reinterpret_cast<float*>(ws + l.neg_lse2);
+  a.bias_rows = l.rows;
+  a.piece_dq = reinterpret_cast<float*>(ws + l.piece_dq);
+  a.piece_dkv = reinterpret_cast<float*>(ws + l.piece_dkv);
   a.bias_part = dbias ? reinterpret_cast<float*>(ws + l.part) : nullptr;
   OASES_TRY(a.t == DType::BF16 ? xattn_bwd_tc(a, st) : xattn_bwd_f32(a, st));
   if (!dbias) return cudaSuccess;

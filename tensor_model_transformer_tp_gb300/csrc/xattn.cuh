@@ -39,6 +39,7 @@ constexpr int BIAS_PAD = 320;
 struct Bias {
   const float* value = nullptr;  // [heads][pitch], in units of log2(e) for the tensor-core kernels
   const int2* range = nullptr;   // [buckets]: the distances n of each bucket (first, last)
+  const uint8_t* index = nullptr;  // the bucket of n = -R .. R
   int pitch = 0, R = 0, buckets = 0;
   int left = 0, right = 0;       // buckets of n <= -R and of n >= R
   __device__ __forceinline__ const float* at(int h, int n) const {  // |n| <= R + PAD
@@ -47,6 +48,14 @@ struct Bias {
   __device__ __forceinline__ float clamped(int h, int n) const { return *at(h, max(-R, min(R, n))); }
 };
 
+// Element-wise warps of the dk, dv kernel (bf16): each writes a partial row of the
+// bias's gradient.
+constexpr int DKV_WARPS = 16;
+
+// A query whose lse lies below this gives no gradient: none of its keys counts (lse =
+// -infinity), or all of its scores lie where fp32 no longer tells weights apart.
+constexpr float LSE_LOWEST = -1048576.f;
+
 struct Args {
   const void *q, *k, *v;
   Strides sq, sk, sv, so, sdo, sdq, sdk, sdv;
@@ -54,14 +63,18 @@ struct Args {
   float* lse;        // [batch][heads][q_len]
   const void* d_o;
   void *dq, *dk, *dv;
-  float* delta;      // [batch][heads][q_len], workspace
+  float* delta;      // workspace: fp32 [batch][heads][q_len]; bf16 -delta, and -lse in base 2,
+  float* neg_lse2;   // [batch][heads][q_pitch]
+  int q_pitch;       // q_len, rounded up to whole tiles
   const int *kv_lens, *q_start;
   int q_start0;
   int B, Sq, Sk, H, G, share, D, causal;
   DType t;
   float scale;
   Bias bias;
-  float* bias_part;  // partial gradients of the bias, null: not wanted
+  float* bias_part;  // partial gradients of the bias [heads][bias_rows][buckets], null: not wanted
+  int64_t bias_rows;
+  float *piece_dq, *piece_dkv;  // sums of pieces of items (bf16 backward), workspace
   int splits;        // forward: shares of the keys, joined by join_splits()
   float* part_o;     // [splits][batch][q_len][heads][D], normalised
   float* part_lse;   // [splits][batch][heads][q_len]
@@ -78,6 +91,14 @@ struct Args {
   }
 };
 
+// Backward, bf16: items in whole rounds of the SMs, then `rest` items of `pieces` each.
+struct Pieces {
+  int whole, rest, pieces;
+};
+struct BwdCut {
+  Pieces dq, dkv;
+};
+
 }  // namespace xattn
 
 // forward of a few rows a key head, any type
@@ -87,6 +108,7 @@ cudaError_t xattn_few(const xattn::Args& a, const void* table, const xattn::Bord
                       bool bidirectional, cudaStream_t st);
 // bf16, tensor cores
 cudaError_t xattn_fwd_tc(const xattn::Args& a, cudaStream_t st);
+bool xattn_bwd_cut(const xattn::Args& a, xattn::BwdCut* cut);  // false: too many items
 cudaError_t xattn_bwd_tc(const xattn::Args& a, cudaStream_t st);
 // fp32 (CUDA cores)
 cudaError_t xattn_fwd_f32(const xattn::Args& a, cudaStream_t st);

@@ -4,24 +4,30 @@
 //   P = e^(s - lse), delta = rowsum(dO * O), dP = dO V^T, dS = P (dP - delta),
 //   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO, and dS summed by bucket.
 // Two kernels own disjoint outputs, so there are no atomics:
-//   dq kernel   persistent: items of 128 queries, looped over blocks of 128 keys
-//   dkv kernel  a CTA per 128 keys of a key head, looped over its query heads and
-//               blocks of 64 queries
-// and dS is formed twice (9 products of the definition's 7).  Both are pipelines of one
-// TMA warp, two MMA-issuing threads (one for S and dP, one for the accumulations: a
-// thread that issued both would wait at one's barrier while the other's operands are
-// ready) and 16 element-wise warps, four per TMEM lane quarter.  P and dS are rounded
-// to bf16, the operand type; the bias's gradient sums dS before that.
+//   dq kernel   items of 128 queries, looped over blocks of 128 keys
+//   dkv kernel  items of 128 keys of a key head, looped over its query heads and blocks
+//               of 64 (DP = 128) or 128 queries (DP = 64)
+// and dS is formed twice (9 products of the definition's 7).  Both are persistent
+// pipelines of one TMA warp, two MMA-issuing threads (one for S and dP, one for the
+// accumulations: a thread that issued both would wait at one's barrier while the other's
+// operands are ready) and 16 element-wise warps, each on 32 rows x 32 columns of a block.
+// P and dS, rounded to bf16, the operand type, are written packed over S (or dP) in tensor
+// memory and read from there as the accumulations' A operand; the bias's gradient sums dS
+// before the rounding.
 //
-// The bias's gradient (dkv kernel).  A warp's 32 x 16 scores that lie R or more from the
+// Items beyond whole rounds of the GPU's SMs are cut into pieces of their blocks, one for
+// each SM; a piece writes fp32 sums of its own, which xattn_bwd_join_kernel adds in order.
+//
+// The bias's gradient (dkv kernel).  A warp's 32 x 32 scores that lie R or more from the
 // diagonal on one side belong to one bucket: every thread adds its own.  Nearer ones are
-// summed along their 47 diagonals, by passing a running sum from lane to lane as the column
-// advances (lane r adds element (r, c) at step c, so a sum that moves one lane a step
-// stays on its diagonal), and the sums of each bucket's run of diagonals are added to
-// the warp's own buckets in shared memory: a fixed order throughout.
+// summed along their 63 diagonals, by passing a running sum from lane to lane as the
+// column advances (lane r adds element (r, c) at step c, so a sum that moves one lane a
+// step stays on its diagonal), and each bucket's run of diagonals is added to the warp's
+// own buckets in shared memory: a fixed order throughout.
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "xattn_tc.cuh"
 
@@ -33,10 +39,20 @@ namespace {
 using namespace xattn;
 
 constexpr uint64_t WAIT = 1ull << 29;  // cycles before a wait gives up (~0.25 s)
-constexpr int NT = 608, ACC_WARP = 18, EW = 16;
+// Warps 0..3 load and issue, 4..19 work element by element.  Registers move from the first
+// warpgroup to the others: 128 x 64 + 512 x 104 = 640 x 96, what a block starts with.
+constexpr int NT = 640, ACC_WARP = 2, EW = 16, EW0 = 4;
+constexpr int REGS = 96, REGS_ISSUE = 64, REGS_EW = 104;
+static_assert(128 * REGS_ISSUE + 32 * EW * REGS_EW == NT * REGS, "registers of the warpgroups");
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 constexpr int BOX64 = 64 * 64 * 2;  // one TMA box of 64 rows
-constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, false, false);
-constexpr uint32_t IDESC_N64 = ptx::idesc_bf16_f32(128, 64, false, false);
 
 __device__ __forceinline__ void wait_failed(int site) { atomicCAS(&g_xattn_bwd_error, 0, site); }
 __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, WAIT); }
@@ -44,29 +60,56 @@ __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity) { return pt
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait1(bar, parity));
 }
-// A row's lse in base 2; a query without keys: every weight 0.
-__device__ __forceinline__ float lse2_of(float lse) { return lse == -INFINITY ? INFINITY : lse * LOG2E; }
+// A row's -lse in base 2, so that its weights are 2^(s - lse); a query without keys: every
+// weight 0.
+__device__ __forceinline__ float minus_lse2(float lse) { return lse < LSE_LOWEST ? -INFINITY : -lse * LOG2E; }
 
 struct Plan {
   Args a;
-  int tiles, items;  // dq: 128-query tiles; dkv: 128-key tiles
+  int tiles;          // dq: 128-query tiles; dkv: 128-key tiles
+  Pieces cut;
   float scale_log2;
+  float* part;        // the pieces' sums: dq [piece][128][D]; dkv [piece][dk, dv][128][D]
 };
 
-// delta: 16 lanes a row, 16 bytes each.
+// Work k of CTA c of G: an item, and which of its pieces (-1: all of it).
+struct Work {
+  int item, piece;
+  int part;  // the piece's place in p.part
+};
+__device__ __forceinline__ bool work_at(const Plan& p, int k, int c, int G, Work* w) {
+  const int i = persistent_item(k, c, G);  // (whole rounds: cut.whole is a multiple of G, or 0)
+  if (i < p.cut.whole) {
+    *w = {i, -1, 0};
+    return true;
+  }
+  const int r = k * G + c - p.cut.whole;
+  if (r >= p.cut.rest * p.cut.pieces) return false;
+  *w = {p.cut.whole + r / p.cut.pieces, p.cut.pieces > 1 ? r % p.cut.pieces : -1, r};
+  return true;
+}
+// Blocks [first, end) of a piece, of the item's n.
+__device__ __forceinline__ void cut_blocks(const Plan& p, int piece, int n, int* first, int* end) {
+  *first = piece < 0 ? 0 : (int)((int64_t)n * piece / p.cut.pieces);
+  *end = piece < 0 ? n : (int)((int64_t)n * (piece + 1) / p.cut.pieces);
+}
+
+// Every row's -lse (base 2) and -delta, [batch][heads][q_pitch] each, so that a block's are
+// one copy: 16 lanes a row, 16 bytes each.  Rows behind the queries have no weights.
 __global__ void __launch_bounds__(256)
-xattn_delta_kernel(const __grid_constant__ Args a, int64_t rows) {
+xattn_stats_kernel(const __grid_constant__ Args a, int64_t rows) {
   pdl_wait();
   pdl_trigger();
   const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 16;  // (batch, query, head)
   const int c = threadIdx.x % 16 * 8;
   float d = 0.f;
-  int64_t at = 0;
+  int64_t b = 0;
+  int h = 0, qi = 0;
   if (r < rows) {
-    const int64_t bq = r / a.H, b = bq / a.Sq;
-    const int h = (int)(r - bq * a.H), qi = (int)(bq - b * a.Sq);
-    at = a.stat((int)b, h, qi);
-    if (c < a.D) {
+    const int64_t bq = r / a.H;
+    b = bq / a.q_pitch;
+    h = (int)(r - bq * a.H), qi = (int)(bq - b * a.q_pitch);
+    if (c < a.D && qi < a.Sq) {
       const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + b * a.so.b +
                                                       qi * a.so.s + h * a.so.h + c);
       const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_o) + b * a.sdo.b +
@@ -81,44 +124,79 @@ xattn_delta_kernel(const __grid_constant__ Args a, int64_t rows) {
   }
 #pragma unroll
   for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
-  if (r < rows && c == 0) a.delta[at] = d;
+  if (r < rows && c == 0) {
+    const int64_t at = (b * a.H + h) * a.q_pitch + qi;
+    a.neg_lse2[at] = qi < a.Sq ? minus_lse2(a.lse[a.stat((int)b, h, qi)]) : -INFINITY;
+    a.delta[at] = -d;
+  }
+}
+
+// 128 rows x DP columns through a map of 64-row boxes (two of a column group lie one
+// behind the other, as one of 128 rows would).
+template <int DP>
+__device__ __forceinline__ void load_two(uint32_t dst, const void* tmap, uint32_t bar, int row, int head, int batch) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      tma_load_4d(dst + c * BOX + r * BOX64, tmap, bar, 64 * c, row + 64 * r, head, batch);
+}
+
+// 32 columns of a row from tensor memory, times `scale`: in bf16 to the row `out` (columns
+// from D on left out), or in fp32 to a piece's row.
+__device__ __forceinline__ void store_row(__nv_bfloat16* out, const float (&v)[32], int columns, float scale) {
+#pragma unroll
+  for (int x = 0; x < 32; x += 8)
+    if (x < columns)
+      *reinterpret_cast<uint4*>(out + x) = make_uint4(pack2(v[x] * scale, v[x + 1] * scale), pack2(v[x + 2] * scale, v[x + 3] * scale),
+                                                      pack2(v[x + 4] * scale, v[x + 5] * scale), pack2(v[x + 6] * scale, v[x + 7] * scale));
+}
+__device__ __forceinline__ void store_part(float* out, const float (&v)[32], int columns) {
+#pragma unroll
+  for (int x = 0; x < 32; x += 4)
+    if (x < columns) *reinterpret_cast<float4*>(out + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
 }
 
 // ---- dq ---------------------------------------------------------------------------------
-// 608 threads: warp 0 TMA (per item K_0 and V_0, then Q and dO, then the K_j and V_j
-// rings, which run on across items), warp 1 TMEM and the S and dP MMAs, warps 2..17
-// element-wise (lanes 32 (w % 4) .. of a block, columns 32 ((w - 2) / 4) ..), warp 18 the
-// dQ MMAs.  TMEM: S 0..127, dP 128..255, dQ 256.., dS (packed bf16) 384..447.  S and dP
-// have one buffer each: the element-wise warps load their columns and release both at
-// once, so the next block's are formed while they work.
+// Warp 0 TMA (per item K and V of its first block, then Q and dO, then the rings of K and
+// V, which run on across items), warp 1 TMEM and the S and dP MMAs, warp 2 the dQ MMAs,
+// warps 4..19 element-wise (lanes 32 (w % 4) .. of a block, columns 32 (w / 4 - 1) ..).  TMEM: S of even blocks 0..127, of odd blocks 128..255, dP 256..383, dQ 384..
+// An element-wise warp forms its weights from S while dP is made, releases dP as soon as
+// its columns are loaded, and writes dS packed over the first 16 of its own 32 columns of
+// S: the tensor cores go from S, dP of block j + 1 to dQ of block j.
 template <int DP>
 struct DqSmem {
   static constexpr int TILE = tile_bytes<DP>();
   static constexpr int KST = DP == 64 ? 4 : 3, VST = DP == 64 ? 4 : 2;
   static constexpr int Q = 0, DO = TILE, K = 2 * TILE, V = K + KST * TILE;
   static constexpr int BAR = V + VST * TILE;
-  static constexpr int NBAR = 8 + 2 * KST + 2 * VST;
+  static constexpr int NBAR = 12 + 2 * KST + 2 * VST;
   static constexpr int BYTES = BAR + 8 * NBAR + 16 + 1024;
   static_assert(BYTES <= 232448, "more than 227 KB of shared memory");
 };
 
 struct DqItem {
-  int h, b, q0, p0, len, n, tile;  // head, sequence, first query and its position, keys, key blocks
+  int h, b, q0, p0, len;   // head, sequence, first query and its position, keys
+  int j0, n;               // key blocks: the first, and how many
+  float* part;             // a piece's sums
 };
-__device__ __forceinline__ DqItem dq_item(const Plan& p, int i) {
+__device__ __forceinline__ DqItem dq_item(const Plan& p, const Work& w) {
   const Args& a = p.a;
   const int bh = a.H * a.B;
   DqItem it;
-  it.tile = p.tiles - 1 - i / bh;
-  const int r = i % bh;
+  const int tile = p.tiles - 1 - w.item / bh;
+  const int r = w.item % bh;
   it.h = r % a.H;
   it.b = r / a.H;
-  it.q0 = it.tile * 128;
+  it.q0 = tile * 128;
   it.len = a.len(it.b);
   it.p0 = a.start(it.b) + it.q0;
   const int rows = min(128, a.Sq - it.q0);
   const int vis = a.causal ? min(it.len, max(0, it.p0 + rows)) : it.len;
-  it.n = (vis + 127) / 128;
+  int end;
+  cut_blocks(p, w.piece, (vis + 127) / 128, &it.j0, &end);
+  it.n = end - it.j0;
+  it.part = w.piece < 0 ? nullptr : p.part + (int64_t)w.part * 128 * a.D;
   return it;
 }
 
@@ -129,32 +207,39 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 const __grid_constant__ Plan p) {
   using L = DqSmem<DP>;
   constexpr int TILE = L::TILE, KST = L::KST, VST = L::VST;
+  constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t IDESC_DQ = ptx::idesc_bf16_f32(128, DP, false, true);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + L::BAR;
-  const uint32_t qdo_full = bars, qdo_empty = bars + 8u, sdp_full = bars + 16u, sdp_empty = bars + 24u;
-  const uint32_t ds_full = bars + 32u, ds_empty = bars + 40u, bar_fin = bars + 48u, sdp_drain = bars + 56u;
-  auto k_full = [&](uint32_t s) { return bars + 8u * (8 + s); };
-  auto k_empty = [&](uint32_t s) { return bars + 8u * (8 + KST + s); };
-  auto v_full = [&](uint32_t s) { return bars + 8u * (8 + 2 * KST + s); };
-  auto v_empty = [&](uint32_t s) { return bars + 8u * (8 + 2 * KST + VST + s); };
+  const uint32_t qdo_full = bars, qdo_empty = bars + 8u, dp_full = bars + 16u, dp_empty = bars + 24u;
+  const uint32_t bar_fin = bars + 32u, drain = bars + 40u;
+  auto s_full = [&](uint32_t b) { return bars + 8u * (6 + b); };
+  auto ds_full = [&](uint32_t b) { return bars + 8u * (8 + b); };    // dS written over S
+  auto ds_empty = [&](uint32_t b) { return bars + 8u * (10 + b); };  // and read
+  auto k_full = [&](uint32_t s) { return bars + 8u * (12 + s); };
+  auto k_empty = [&](uint32_t s) { return bars + 8u * (12 + KST + s); };
+  auto v_full = [&](uint32_t s) { return bars + 8u * (12 + 2 * KST + s); };
+  auto v_empty = [&](uint32_t s) { return bars + 8u * (12 + 2 * KST + VST + s); };
   const uint32_t tslot = bars + 8u * L::NBAR;
   const Args& a = p.a;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
   const int cta = blockIdx.x, G = gridDim.x;
 
   if (tid == 0) {
     ptx::mbar_init(qdo_full, 1);
     ptx::mbar_init(qdo_empty, 1);
-    ptx::mbar_init(sdp_full, 1);
-    ptx::mbar_init(sdp_empty, EW);
-    ptx::mbar_init(ds_full, EW);
-    ptx::mbar_init(ds_empty, 1);
+    ptx::mbar_init(dp_full, 1);
+    ptx::mbar_init(dp_empty, EW);
     ptx::mbar_init(bar_fin, 1);
-    ptx::mbar_init(sdp_drain, 1);
+    ptx::mbar_init(drain, 1);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(s_full(b), 1);
+      ptx::mbar_init(ds_full(b), EW);
+      ptx::mbar_init(ds_empty(b), 1);
+    }
     for (int s = 0; s < 2 * KST + 2 * VST; ++s) ptx::mbar_init(k_full(s), 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tq);
@@ -170,231 +255,241 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + (tslot - base));
-  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dq = tmem + 256, t_ds = tmem + 384;
+  auto t_s = [&](uint32_t b) { return tmem + 128u * b; };
+  const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
   pdl_wait();
   pdl_trigger();
   bool ok = true;
+  Work wk;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t ke = 0, nq = 0;  // ring entries (of K and of V) and Q/dO tiles loaded
-      auto load_kv = [&](int r, int g, int b) {
-        const uint32_t sk = ke % KST, uk = ke / KST, sv = ke % VST, uv = ke / VST;
-        if (uk > 0 && !wait1(k_empty(sk), (uk - 1) & 1)) return false;
-        ptx::mbar_arrive_expect_tx(k_full(sk), TILE);
-        load_tile<DP, 128>(base + L::K + sk * TILE, &tk, k_full(sk), r, g, b);
-        bool landed = true;
-        if (uv > 0) landed = wait1(v_empty(sv), (uv - 1) & 1);
-        if (landed) {
-          ptx::mbar_arrive_expect_tx(v_full(sv), TILE);
-          load_tile<DP, 128>(base + L::V + sv * TILE, &tv, v_full(sv), r, g, b);
-          ++ke;
-        } else {  // (K's load of this entry must land too before the CTA exits)
-          (void)wait1(k_full(sk), uk & 1);
+  if (warp < EW0) {
+    fewer_registers<REGS_ISSUE>();
+    if (warp == 0) {
+      if (ptx::elect_one()) {
+        uint32_t ke = 0, nq = 0;  // ring entries (of K and of V) and Q/dO tiles loaded
+        auto load_kv = [&](int r, int g, int b) {
+          const uint32_t sk = ke % KST, uk = ke / KST, sv = ke % VST, uv = ke / VST;
+          if (uk > 0 && !wait1(k_empty(sk), (uk - 1) & 1)) return false;
+          ptx::mbar_arrive_expect_tx(k_full(sk), TILE);
+          load_tile<DP, 128>(base + L::K + sk * TILE, &tk, k_full(sk), r, g, b);
+          bool landed = true;
+          if (uv > 0) landed = wait1(v_empty(sv), (uv - 1) & 1);
+          if (landed) {
+            ptx::mbar_arrive_expect_tx(v_full(sv), TILE);
+            load_tile<DP, 128>(base + L::V + sv * TILE, &tv, v_full(sv), r, g, b);
+            ++ke;
+          } else {  // (K's load of this entry must land too before the CTA exits)
+            (void)wait1(k_full(sk), uk & 1);
+          }
+          return landed;
+        };
+        for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
+          const DqItem it = dq_item(p, wk);
+          if (it.n == 0) continue;
+          const int g = it.h / a.share;
+          ok = load_kv(it.j0 * 128, g, it.b);
+          // Q and dO are free once the previous item's last S and dP are done
+          if (ok && nq > 0 && !wait1(qdo_empty, (nq - 1) & 1)) ok = false;
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(qdo_full, 2 * TILE);
+          load_two<DP>(base + L::Q, &tq, qdo_full, it.q0, it.h, it.b);
+          load_two<DP>(base + L::DO, &tdo, qdo_full, it.q0, it.h, it.b);
+          ++nq;
+          for (int j = 1; j < it.n && ok; ++j) ok = load_kv((it.j0 + j) * 128, g, it.b);
         }
-        return landed;
-      };
-      for (int k = 0; ok; ++k) {
-        const int i = persistent_item(k, cta, G);
-        if (i >= p.items) break;
-        const DqItem it = dq_item(p, i);
-        if (it.n == 0) continue;
-        const int g = it.h / a.share;
-        ok = load_kv(0, g, it.b);
-        // Q and dO are free once the previous item's last S and dP are done
-        if (ok && nq > 0 && !wait1(qdo_empty, (nq - 1) & 1)) ok = false;
-        if (!ok) break;
-        ptx::mbar_arrive_expect_tx(qdo_full, 2 * TILE);
-        load_tile<DP, 128>(base + L::Q, &tq, qdo_full, it.q0, it.h, it.b);
-        load_tile<DP, 128>(base + L::DO, &tdo, qdo_full, it.q0, it.h, it.b);
-        ++nq;
-        for (int j = 1; j < it.n && ok; ++j) ok = load_kv(j * 128, g, it.b);
+        if (!ok) wait_failed(101);
+        // every load issued has landed before the CTA may exit
+        bool dr = true;
+        for (uint32_t s = 0; s < KST; ++s)
+          if (ke > s) dr = wait1(k_full(s), ((ke - 1 - s) / KST) & 1) && dr;
+        for (uint32_t s = 0; s < VST; ++s)
+          if (ke > s) dr = wait1(v_full(s), ((ke - 1 - s) / VST) & 1) && dr;
+        if (nq > 0) dr = wait1(qdo_full, (nq - 1) & 1) && dr;
+        if (!dr) wait_failed(102);
       }
-      if (!ok) wait_failed(101);
-      // every load issued has landed before the CTA may exit
-      bool dr = true;
-      for (uint32_t s = 0; s < KST; ++s)
-        if (ke > s) dr = wait1(k_full(s), ((ke - 1 - s) / KST) & 1) && dr;
-      for (uint32_t s = 0; s < VST; ++s)
-        if (ke > s) dr = wait1(v_full(s), ((ke - 1 - s) / VST) & 1) && dr;
-      if (nq > 0) dr = wait1(qdo_full, (nq - 1) & 1) && dr;
-      if (!dr) wait_failed(102);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t g = 0, nq = 0;  // blocks (= ring entries) and items with blocks so far
-      for (int k = 0; ok; ++k) {
-        const int i = persistent_item(k, cta, G);
-        if (i >= p.items) break;
-        const DqItem it = dq_item(p, i);
-        if (it.n == 0) continue;
-        if (!wait1(qdo_full, nq & 1)) {
+    } else if (warp == 1) {
+      if (ptx::elect_one()) {
+        uint32_t g = 0, nq = 0;  // blocks (= ring entries) and items with blocks so far
+        for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
+          const DqItem it = dq_item(p, wk);
+          if (it.n == 0) continue;
+          if (!wait1(qdo_full, nq & 1)) {
+            ok = false;
+            wait_failed(103);
+            break;
+          }
+          ++nq;
+          for (int j = 0; j < it.n; ++j, ++g) {  // S = Q K_j^T, dP = dO V_j^T
+            const uint32_t sk = g % KST, sv = g % VST, b = g & 1;
+            // (dQ of the block before the last, whose dS lay in this buffer, is done)
+            if (!wait1(k_full(sk), (g / KST) & 1) || (g >= 2 && !wait1(ds_empty(b), ((g / 2) & 1) ^ 1))) {
+              ok = false;
+              wait_failed(104);
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t kt = base + L::K + sk * TILE, vt = base + L::V + sv * TILE;
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk)
+              ptx::mma_bf16(t_s(b), kmajor_desc(base + L::Q, kk), kmajor_desc(kt, kk), IDESC_S, kk > 0);
+            ptx::mma_commit(s_full(b));
+            // (the element-wise warps have loaded the previous block's dP)
+            if (!wait1(v_full(sv), (g / VST) & 1) || (g >= 1 && !wait1(dp_empty, (g - 1) & 1))) {
+              ok = false;
+              wait_failed(105);
+              break;
+            }
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk)
+              ptx::mma_bf16(t_dp, kmajor_desc(base + L::DO, kk), kmajor_desc(vt, kk), IDESC_S, kk > 0);
+            ptx::mma_commit(dp_full);
+            ptx::mma_commit(v_empty(sv));
+            if (j + 1 == it.n) ptx::mma_commit(qdo_empty);  // the item's last read of Q and dO
+          }
+        }
+        ptx::mma_commit(drain);  // completes once every MMA this thread issued has
+        if (!wait1(drain, 0)) {
           ok = false;
-          wait_failed(103);
-          break;
+          wait_failed(107);
         }
-        ++nq;
-        for (int j = 0; j < it.n && ok; ++j, ++g) {  // S_j = Q K_j^T, dP_j = dO V_j^T
-          const uint32_t sk = g % KST, sv = g % VST;
-          // (the element-wise warps have loaded the previous block's S and dP)
-          if (!wait1(k_full(sk), (g / KST) & 1) || !wait1(v_full(sv), (g / VST) & 1) ||
-              (g >= 1 && !wait1(sdp_empty, (g - 1) & 1))) {
-            ok = false;
-            wait_failed(104);
-            break;
+      }
+    } else if (warp == ACC_WARP) {
+      if (ptx::elect_one()) {
+        uint32_t g = 0, nk = 0;  // blocks, items with blocks finished
+        for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
+          const DqItem it = dq_item(p, wk);
+          if (it.n == 0) continue;
+          for (int j = 0; j < it.n; ++j, ++g) {  // dQ += dS_j K_j
+            const uint32_t sk = g % KST, b = g & 1;
+            if (!wait1(ds_full(b), (g / 2) & 1)) {
+              ok = false;
+              wait_failed(106);
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t kt = base + L::K + sk * TILE;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              ptx::mma_bf16_ts(t_dq, t_s(b) + 32u * (kk >> 1) + 8u * (kk & 1), mnmajor_desc(kt, kk), IDESC_DQ,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+            // S_j, which also read K_j, completed before dS_j could be handed over, so K_j is
+            // free once these MMAs are
+            ptx::mma_commit(ds_empty(b));
+            ptx::mma_commit(k_empty(sk));
           }
-          ptx::tc_fence_after();
-          const uint32_t kt = base + L::K + sk * TILE, vt = base + L::V + sv * TILE;
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            ptx::mma_bf16(t_s, kmajor_desc(base + L::Q, kk), kmajor_desc(kt, kk), IDESC_S, kk > 0);
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            ptx::mma_bf16(t_dp, kmajor_desc(base + L::DO, kk), kmajor_desc(vt, kk), IDESC_S, kk > 0);
-          ptx::mma_commit(sdp_full);
-          ptx::mma_commit(v_empty(sv));
-          if (j + 1 == it.n) ptx::mma_commit(qdo_empty);  // the item's last read of Q and dO
+          if (!ok) break;
+          ptx::mma_commit(bar_fin);  // the item's dQ is complete once this does
+          ++nk;
         }
-      }
-      ptx::mma_commit(sdp_drain);  // completes once every MMA this thread issued has
-      if (!wait1(sdp_drain, 0)) {
-        ok = false;
-        wait_failed(107);
-      }
-    }
-  } else if (warp == ACC_WARP) {
-    if (lane == 0) {
-      uint32_t g = 0, nk = 0;  // blocks, items with blocks finished
-      for (int k = 0; ok; ++k) {
-        const int i = persistent_item(k, cta, G);
-        if (i >= p.items) break;
-        const DqItem it = dq_item(p, i);
-        if (it.n == 0) continue;
-        for (int j = 0; j < it.n && ok; ++j, ++g) {  // dQ += dS_j K_j
-          const uint32_t sk = g % KST;
-          if (!wait1(ds_full, g & 1)) {
-            ok = false;
-            wait_failed(106);
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t kt = base + L::K + sk * TILE;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            ptx::mma_bf16_ts(t_dq, t_ds + 8u * kk, mnmajor_desc(kt, kk), IDESC_DQ, (j > 0 || kk > 0) ? 1u : 0u);
-          // S_j, dP_j (which also read K_j) completed before dS_j could be handed over,
-          // so K_j is free once these MMAs are
-          ptx::mma_commit(ds_empty);
-          ptx::mma_commit(k_empty(sk));
+        // every MMA this thread issued is complete before the CTA may exit
+        if (nk > 0 && !wait1(bar_fin, (nk - 1) & 1)) {
+          ok = false;
+          wait_failed(111);
         }
-        if (!ok) break;
-        ptx::mma_commit(bar_fin);  // the item's dQ is complete once this does
-        ++nk;
-      }
-      // every MMA this thread issued is complete before the CTA may exit
-      if (nk > 0 && !wait1(bar_fin, (nk - 1) & 1)) {
-        ok = false;
-        wait_failed(111);
-      }
-      if (!ok) {  // one more commit drains whatever was issued after the last finished item
-        ptx::mma_commit(bar_fin);
-        (void)wait1(bar_fin, nk & 1);
+        if (!ok) {  // one more commit drains whatever was issued after the last finished item
+          ptx::mma_commit(bar_fin);
+          (void)wait1(bar_fin, nk & 1);
+        }
       }
     }
   } else {
-    const int qq = warp & 3, sub = (warp - 2) >> 2;  // lane quarter; columns 32 sub .. + 31
+    more_registers<REGS_EW>();
+    const int qq = warp & 3, sub = (warp - EW0) >> 2;  // lane quarter; columns 32 sub .. + 31
     const int row = qq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(qq * 32) << 16;
     uint32_t g = 0, nf = 0;
-    // this row's LSE (base 2) and delta of an item, read one item ahead
-    auto stats = [&](int i, float& lse2, float& dlt) {
-      lse2 = INFINITY;
-      dlt = 0.f;
-      if (i >= p.items) return;
-      const DqItem it = dq_item(p, i);
-      if (it.q0 + row < a.Sq) {
-        const int64_t at = a.stat(it.b, it.h, it.q0 + row);
-        lse2 = lse2_of(a.lse[at]);
-        dlt = a.delta[at];
-      }
+    // this row's -lse (base 2) and -delta of an item, read one item ahead
+    auto stats = [&](int k, float& nl, float& nd) {
+      nl = -INFINITY;
+      nd = 0.f;
+      Work w;
+      if (!work_at(p, k, cta, G, &w)) return;
+      const DqItem it = dq_item(p, w);
+      const int64_t at = ((int64_t)it.b * a.H + it.h) * a.q_pitch + it.q0 + row;
+      nl = a.neg_lse2[at];
+      nd = a.delta[at];
     };
-    float lse2_next, dlt_next;
-    stats(persistent_item(0, cta, G), lse2_next, dlt_next);
-    for (int k = 0; ok; ++k) {
-      const int i = persistent_item(k, cta, G);
-      if (i >= p.items) break;
-      const DqItem it = dq_item(p, i);
+    float nl_next, nd_next;
+    stats(0, nl_next, nd_next);
+    for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
+      const DqItem it = dq_item(p, wk);
       const int qi = it.q0 + row;
       const bool valid_q = qi < a.Sq;
-      const float lse2 = lse2_next, dlt = dlt_next;
-      stats(persistent_item(k + 1, cta, G), lse2_next, dlt_next);
+      const float nl = nl_next, nd = nd_next;
+      stats(k + 1, nl_next, nd_next);
       const int w0 = it.p0 + qq * 32;  // position of the warp's first query
       float left = 0.f, right = 0.f;
       if (BIAS) {
         left = *a.bias.at(it.h, -a.bias.R);
         right = *a.bias.at(it.h, a.bias.R);
       }
-      for (int j = 0; j < it.n && ok; ++j, ++g) {
-        if (!warp_wait(sdp_full, g & 1)) {
+      for (int j = 0; j < it.n; ++j, ++g) {
+        const uint32_t b = g & 1, own = t_s(b) + lane_off + sub * 32;
+        if (!warp_wait(s_full(b), (g / 2) & 1)) {
           ok = false;
           if (lane == 0) wait_failed(108);
           break;
         }
         ptx::tc_fence_after();
-        float v[32], w[32];
-        ptx::tmem_ld32x2(t_s + lane_off + sub * 32, t_dp + lane_off + sub * 32, v, w);
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(sdp_empty);  // the TMEM buffers may be overwritten
-        const int kb = j * 128 + sub * 32;
+        float v[32];
+        ptx::tmem_ld32(own, v);
+        const int kb = (it.j0 + j) * 128 + sub * 32;
         // 32 x 32 scores wholly visible need no mask (warp-uniform)
         const bool full = it.q0 + qq * 32 + 32 <= a.Sq && kb + 32 <= it.len && (!a.causal || kb + 31 <= w0);
         const bool on_right = BIAS && kb - (w0 + 31) >= a.bias.R;
         const bool on_left = BIAS && !on_right && kb + 31 - w0 <= -a.bias.R;
-        const bool near = BIAS && !on_left && !on_right;
-        const float shift = (on_right ? right : on_left ? left : 0.f) - lse2;
+        const float shift = (on_right ? right : on_left ? left : 0.f) + nl;
         float mul = p.scale_log2;
-        if (near) {
+        if (BIAS && !on_left && !on_right) {
           const float* bv = a.bias.at(it.h, kb - w0) - lane;
 #pragma unroll
           for (int c = 0; c < 32; ++c) v[c] = fmaf(v[c], p.scale_log2, __ldg(bv + c));
           mul = 1.f;
         }
-        uint32_t pk[16];  // dS as packed bf16 pairs (keys 2i, 2i+1 of these 32)
-        if (full) {
-          const uint64_t sc = f2_splat(mul), sh = f2_splat(shift), nd = f2_splat(-dlt);
+        const uint64_t sc = f2_splat(mul), sh = f2_splat(shift);
 #pragma unroll
-          for (int i2 = 0; i2 < 16; ++i2) {
-            const uint64_t x = f2_fma(f2_pack(v[2 * i2], v[2 * i2 + 1]), sc, sh);
-            const uint64_t pr = f2_pack(fast_exp2(f2_lo(x)), fast_exp2(f2_hi(x)));
-            const uint64_t ds = f2_mul(pr, f2_add(f2_pack(w[2 * i2], w[2 * i2 + 1]), nd));
-            pk[i2] = pack2(f2_lo(ds), f2_hi(ds));
-          }
-        } else {
-          // keys kb + c with c >= nvis are past the diagonal or the sequence's keys (all
-          // of them for a row past the queries)
-          const int nvis = valid_q ? (a.causal ? min(w0 + lane + 1, it.len) : it.len) - kb : 0;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float e = fast_exp2(fmaf(v[c], mul, shift));
-            v[c] = c < nvis ? e * (w[c] - dlt) : 0.f;
-          }
-#pragma unroll
-          for (int i2 = 0; i2 < 16; ++i2) pk[i2] = pack2(v[2 * i2], v[2 * i2 + 1]);
+        for (int c = 0; c < 32; c += 2) {
+          const uint64_t x = f2_fma(f2_pack(v[c], v[c + 1]), sc, sh);
+          v[c] = fast_exp2(f2_lo(x));
+          v[c + 1] = fast_exp2(f2_hi(x));
         }
-        // the dS columns are free once the previous block's dQ MMAs are done
-        if (g >= 1 && !warp_wait(ds_empty, (g - 1) & 1)) {
+        if (!warp_wait(dp_full, g & 1)) {
           ok = false;
           if (lane == 0) wait_failed(109);
           break;
         }
         ptx::tc_fence_after();
-        ptx::tmem_st16_nowait(t_ds + lane_off + sub * 16, pk);
+        float w[32];
+        ptx::tmem_ld32(t_dp + lane_off + sub * 32, w);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(dp_empty);  // dP's buffer may be overwritten
+        uint32_t pk[16];  // dS as packed bf16 pairs (keys 2i, 2i+1 of these 32)
+        if (full) {
+          const uint64_t nd2 = f2_splat(nd);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t ds = f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), f2_add(f2_pack(w[2 * i], w[2 * i + 1]), nd2));
+            pk[i] = pack2(f2_lo(ds), f2_hi(ds));
+          }
+        } else {
+          // keys kb + c with c >= nvis are past the diagonal or the sequence's keys (all
+          // of them for a row past the queries); what dP holds there may be anything
+          const int nvis = valid_q ? (a.causal ? min(w0 + lane + 1, it.len) : it.len) - kb : 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = 2 * i < nvis ? v[2 * i] * (w[2 * i] + nd) : 0.f;
+            const float y = 2 * i + 1 < nvis ? v[2 * i + 1] * (w[2 * i + 1] + nd) : 0.f;
+            pk[i] = pack2(x, y);
+          }
+        }
+        ptx::tmem_st16_nowait(own, pk);
         // the keys behind the sequence's, where the tensor goes on: their rows of K
-        // cleared (S and dP of this block, which also read the tile, are complete)
-        if (j * 128 + 128 > it.len && it.len < a.Sk) {
-          const int r = (warp - 2) * 8 + lane / 4;
-          if (j * 128 + r >= it.len) {
+        // cleared (S of this block, which also read the tile, is complete)
+        if ((it.j0 + j) * 128 + 128 > it.len && it.len < a.Sk) {
+          const int r = (warp - EW0) * 8 + lane / 4;
+          if ((it.j0 + j) * 128 + r >= it.len) {
             uint8_t* kr = gbase + L::K + g % KST * TILE + r * 128 + (lane & 3) * 32;
 #pragma unroll
             for (int c = 0; c < DP / 64; ++c) {
@@ -408,38 +503,34 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ds_full);
+        if (lane == 0) ptx::mbar_arrive(ds_full(b));
       }
       if (!ok) break;
-      bool fin = true;
-      float v0[32];
+      float v[32];
       if (it.n > 0) {
         // the item's last accumulation is complete (or the MMA thread gave up)
-        fin = warp_wait(bar_fin, nf & 1);
+        if (!warp_wait(bar_fin, nf & 1)) {
+          ok = false;
+          if (lane == 0) wait_failed(112);
+          break;
+        }
         ++nf;
         ptx::tc_fence_after();
         // tcgen05.ld is warp-collective: every lane loads (DP = 64: what the last two
         // column groups load is not used)
-        ptx::tmem_ld32(t_dq + lane_off + sub * 32, v0);
+        ptx::tmem_ld32(t_dq + lane_off + (sub * 32 < DP ? sub * 32 : 0), v);
       } else {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v0[c] = 0.f;
+        for (int c = 0; c < 32; ++c) v[c] = 0.f;
       }
-      if (fin && valid_q && sub * 32 < DP) {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + it.b * a.sdq.b + qi * a.sdq.s + it.h * a.sdq.h + sub * 32;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (sub * 32 + 8 * u < a.D)
-            *reinterpret_cast<uint4*>(out + 8 * u) =
-                make_uint4(pack2(v0[8 * u] * a.scale, v0[8 * u + 1] * a.scale),
-                           pack2(v0[8 * u + 2] * a.scale, v0[8 * u + 3] * a.scale),
-                           pack2(v0[8 * u + 4] * a.scale, v0[8 * u + 5] * a.scale),
-                           pack2(v0[8 * u + 6] * a.scale, v0[8 * u + 7] * a.scale));
+      if (valid_q && sub * 32 < a.D) {
+        if (it.part)
+          store_part(it.part + row * a.D + sub * 32, v, a.D - sub * 32);
+        else
+          store_row(static_cast<__nv_bfloat16*>(a.dq) + it.b * a.sdq.b + qi * a.sdq.s + it.h * a.sdq.h + sub * 32, v,
+                    a.D - sub * 32, a.scale);
       }
-      if (!fin) {
-        ok = false;
-        if (lane == 0) wait_failed(112);
-      }
+      __syncwarp();
     }
   }
   if (!ok) atomicCAS(&g_xattn_bwd_error, 0, 3);
@@ -452,24 +543,211 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 }
 
 // ---- dk, dv -------------------------------------------------------------------------------
-// 608 threads: warp 0 TMA (K and V once, then Q_i and dO_i into a ring, each stage with
-// its queries' lse and delta), warp 1 TMEM and the S^T and dP^T MMAs (N = 64, two buffers),
-// warps 2..17 element-wise (lanes 32 (w % 4) .., one key row each, columns 16 ((w - 2) / 4) ..),
-// warp 18 the dV and dK MMAs.  A warp writes P^T and dS^T, packed, over the first 8 of
-// its own 16 columns of S^T and dP^T: one 16-query step of the accumulations' A operand,
-// read from tensor memory.  (From shared memory the operands' reads bound the kernel:
-// 224 KB a block at 128 bytes a clock against 1024 clocks of products, 160 KB so.)
-// TMEM: buffer b's S^T at 128 b .. + 63, dP^T at + 64 .., dV 256 .., dK 384 ..
-template <int DP, bool BIAS>
-struct KvSmem {
-  static constexpr int TILE = tile_bytes<DP>(), T64 = TILE / 2;
-  static constexpr int QST = DP == 64 ? 8 : BIAS ? 4 : 5;
-  static constexpr int K = 0, V = TILE, Q = 2 * TILE, DO = Q + QST * T64;
-  static constexpr int STAT = DO + QST * T64;                              // [stage][lse2[64] | delta[64]] fp32
-  static constexpr int BUCKET = STAT + QST * 2 * 64 * 4;                   // [16][MAX_BUCKETS] fp32
-  static constexpr int DIAG = BUCKET + (BIAS ? EW * MAX_BUCKETS * 4 : 0);  // [16][48] fp32
-  static constexpr int BAR = DIAG + (BIAS ? EW * 48 * 4 : 0);
-  static constexpr int NBAR = 9 + 2 * QST;
+// 128 keys of one key head.  Block x of the item's, from `first` on n of them: BQ queries
+// from i0 + x % per_head on, of query head g share + x / per_head.
+struct KvItem {
+  int g, b, k0, len, p0, i0, per_head, first, n;
+};
+template <int BQ>
+__device__ __forceinline__ KvItem kv_item(const Plan& p, const Work& w) {
+  const Args& a = p.a;
+  KvItem it;
+  int u = w.item;
+  it.g = u % a.G;
+  const int bt = u / a.G;
+  it.b = bt % a.B;
+  it.k0 = bt / a.B * 128;  // key tile 0 (causal: the most query blocks) first
+  it.len = a.len(it.b);
+  it.p0 = a.start(it.b);
+  it.i0 = a.causal ? max(0, it.k0 - it.p0) / BQ : 0;  // blocks before see none of these keys
+  it.per_head = it.k0 < it.len ? max(0, (a.Sq + BQ - 1) / BQ - it.i0) : 0;
+  int end;
+  cut_blocks(p, w.piece, it.per_head * a.share, &it.first, &end);
+  it.n = end - it.first;
+  return it;
+}
+
+// Two pairs of floats from shared memory.  (In the order of the program: the compiler would
+// fetch a block's all at once, and spill.)
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& x, uint64_t& y) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(addr));
+}
+
+// A warp's part of a block, 32 keys (rows) x 32 queries: where it lies, and the bias that
+// all of its scores have.
+template <bool BIAS>
+struct KvTile {
+  bool on_left, on_right;  // R or more from the diagonal
+  float mul, add;
+
+  // scores v of keys kw + lane, queries from position pq on
+  __device__ __forceinline__ void start(const Plan& p, int h, int kw, int pq, int lane, float (&v)[32]) {
+    mul = p.scale_log2;
+    if (!BIAS) return;
+    add = 0.f;
+    on_right = kw - (pq + 31) >= p.a.bias.R;
+    on_left = !on_right && kw + 31 - pq <= -p.a.bias.R;
+    if (on_right) {
+      add = __ldg(p.a.bias.at(h, p.a.bias.R));
+    } else if (on_left) {
+      add = __ldg(p.a.bias.at(h, -p.a.bias.R));
+    } else {
+      const float* bv = p.a.bias.at(h, kw - pq) + lane;
+#pragma unroll
+      for (int x = 0; x < 32; ++x) v[x] = fmaf(v[x], p.scale_log2, __ldg(bv - x));
+      mul = 1.f;
+    }
+  }
+  // Scores to weights, nl the shared address of the queries' -lse (base 2).
+  __device__ __forceinline__ void weights(uint32_t nl, float (&v)[32]) const {
+    const uint64_t sc = f2_splat(mul), ad = BIAS ? f2_splat(add) : 0ull;
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) {
+      uint64_t n[2];
+      lds_pairs(nl + 4 * x, n[0], n[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (BIAS) n[e] = f2_add(n[e], ad);
+        const uint64_t y = f2_fma(f2_pack(v[x + 2 * e], v[x + 2 * e + 1]), sc, n[e]);
+        v[x + 2 * e] = fast_exp2(f2_lo(y));
+        v[x + 2 * e + 1] = fast_exp2(f2_hi(y));
+      }
+    }
+  }
+};
+// Weights v[FIRST ..] to dS, from 16 of dP and the shared address of the queries' -delta.
+template <int FIRST>
+__device__ __forceinline__ void gradients(uint32_t nd, const float (&w)[16], float (&v)[32]) {
+#pragma unroll
+  for (int x = 0; x < 16; x += 4) {
+    uint64_t n[2];
+    lds_pairs(nd + 4 * (FIRST + x), n[0], n[1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int at = FIRST + x + 2 * e;
+      const uint64_t ds = f2_mul(f2_pack(v[at], v[at + 1]), f2_add(f2_pack(w[x + 2 * e], w[x + 2 * e + 1]), n[e]));
+      v[at] = f2_lo(ds);
+      v[at + 1] = f2_hi(ds);
+    }
+  }
+}
+
+// A warp's share of the bias's gradient: sums by bucket in shared memory, those of scores
+// far from the diagonal in registers.
+struct KvBias {
+  float far_left = 0.f, far_right = 0.f;
+  uint32_t bucket, diag;  // shared addresses, the warp's own: [MAX_BUCKETS], [64] fp32
+
+  __device__ __forceinline__ void init(const Args& a, uint32_t buckets, uint32_t diagonals, int lane) {
+    bucket = buckets;
+    diag = diagonals;
+    for (int x = lane; x < a.bias.buckets; x += 32) ptx::sts(bucket + 4 * x, 0.f);
+    __syncwarp();
+  }
+  // dS w of 32 keys, the first at distance n0 + 31 from query 0, summed by bucket.
+  __device__ __forceinline__ void sum(const Args& a, bool on_left, bool on_right, int n0, int lane, const float (&w)[32]) {
+    if (on_left || on_right) {
+      float s[4] = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+      for (int x = 4; x < 32; ++x) s[x & 3] += w[x];
+      const float t = (s[0] + s[1]) + (s[2] + s[3]);
+      if (on_left) far_left += t;
+      else far_right += t;
+      return;
+    }
+    // along the diagonals, that of element (r, x) r - x + 31, of distance n0 + the same
+    float run = 0.f;
+#pragma unroll
+    for (int x = 0; x < 32; ++x) {
+      run = __shfl_up_sync(0xffffffffu, run, 1);
+      run = (lane == 0 ? 0.f : run) + w[x];
+      if (lane == 31) ptx::sts(diag + 4 * (62 - x), run);
+    }
+    if (lane < 31) ptx::sts(diag + 4 * lane, run);
+    else ptx::sts(diag + 4 * 63, 0.f);
+    __syncwarp();
+    // a bucket's diagonals stand side by side: sums within runs of equal buckets, added by
+    // each run's last lane
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int n = n0 + 32 * half + lane;
+      const int u = a.bias.index[max(-a.bias.R, min(a.bias.R, n)) + a.bias.R];
+      const int before = __shfl_up_sync(0xffffffffu, u, 1);
+      const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 || u != before);
+      const int first = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));  // of this lane's run
+      float t = ptx::lds(diag + 128 * half + 4 * lane);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float below = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane - o >= first) t += below;
+      }
+      if (lane == 31 || (heads >> (lane + 1) & 1)) ptx::sts(bucket + 4 * u, ptx::lds(bucket + 4 * u) + t);
+      __syncwarp();
+    }
+  }
+  // The buckets of a finished head as one of its item's DKV_WARPS partial rows, and 0 for
+  // the next.
+  __device__ __forceinline__ void flush(const Plan& p, Work w, int h, int warp_row, int lane) {
+    const Args& a = p.a;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      far_left += __shfl_xor_sync(~0u, far_left, o);
+      far_right += __shfl_xor_sync(~0u, far_right, o);
+    }
+    if (lane == 0) {
+      ptx::sts(bucket + 4 * a.bias.left, ptx::lds(bucket + 4 * a.bias.left) + far_left);
+      ptx::sts(bucket + 4 * a.bias.right, ptx::lds(bucket + 4 * a.bias.right) + far_right);
+    }
+    __syncwarp();
+    far_left = far_right = 0.f;
+    // rows [0, batch tiles) are those of whole items and of first pieces, then the other
+    // pieces' of the items from the first (sequence, tile) with a cut one on
+    const int bt = w.item / a.G, cut0 = p.cut.whole / a.G, others = p.cut.pieces - 1;
+    const int64_t beyond = (int64_t)a.B * p.tiles + (int64_t)(bt - cut0) * others;
+    auto at = [&](int64_t row) {
+      return a.bias_part + (h * a.bias_rows + row * DKV_WARPS + warp_row) * a.bias.buckets;
+    };
+    float* out = at(w.piece <= 0 ? bt : beyond + w.piece - 1);
+    for (int x = lane; x < a.bias.buckets; x += 32) {
+      out[x] = ptx::lds(bucket + 4 * x);
+      ptx::sts(bucket + 4 * x, 0.f);
+    }
+    if (w.piece < 0 && bt >= cut0)  // (a whole item beside cut ones: it has no other pieces)
+      for (int q = 0; q < others; ++q)
+        for (int x = lane; x < a.bias.buckets; x += 32) at(beyond + q)[x] = 0.f;
+    __syncwarp();
+  }
+};
+
+// Warp 0 TMA (an item's K and V, then Q_i and dO_i into a ring, each stage with its queries'
+// lse and delta), warp 1 TMEM and the S^T and dP^T MMAs, warp 2 the dV and dK MMAs, warps
+// 4..19 element-wise (lanes 32 (w % 4) .., one key row each, 32 columns).  An
+// element-wise warp starts on S^T while dP^T is formed.
+//
+// DP = 64: blocks of 128 queries, all 16 warps on each.  TMEM: S^T of even blocks 0..127, of
+// odd ones 128..255, dP^T 256..383 (released as soon as it is loaded), dV 384.., dK 448..;
+// P^T and dS^T, packed, stand over a warp's own 32 columns of S^T.
+//
+// DP = 128: the accumulators leave room for 64 queries a block: S^T of buffer b at 128 b ..,
+// dP^T at + 64 .., dV 256.., dK 384..; P^T over S^T, dS^T over dP^T.  Two groups of 8 warps
+// take a buffer each, so that one works while the other waits for its block (all 16 on every
+// block, 16 columns each, waited on every barrier twice as often: 629 us against TODO at 8
+// sequences of 2048, 19 heads).  The products read 64 queries' operands with the whole of K
+// and V: bound by shared memory's 128 bytes a clock, 1280 clocks a block against 1024 of the
+// tensor cores'.
+template <int DP_, bool BIAS>
+struct Kv {
+  static constexpr int DP = DP_, BQ = DP == 64 ? 128 : 64;
+  static constexpr int GROUPS = DP == 64 ? 1 : 2;               // of element-wise warps, a block each
+  static constexpr int NDP = DP == 64 ? 1 : 2, NSET = DP == 64 ? 2 : 1;  // buffers of dP^T; of K and V
+  static constexpr int QST = DP == 64 ? 4 : BIAS ? 4 : 5;
+  static constexpr int TILE = tile_bytes<DP>(), QTILE = TILE / 128 * BQ;
+  static constexpr int KV = 0, Q = NSET * 2 * TILE, DO = Q + QST * QTILE;  // [set][K | V]
+  static constexpr int STAT = DO + QST * QTILE;                            // [stage][-lse2[BQ] | -delta[BQ]] fp32
+  static constexpr int BUCKET = STAT + QST * 2 * BQ * 4;                   // [16][MAX_BUCKETS] fp32
+  static constexpr int DIAG = BUCKET + (BIAS ? EW * MAX_BUCKETS * 4 : 0);  // [16][64] fp32
+  static constexpr int BAR = DIAG + (BIAS ? EW * 64 * 4 : 0);
+  static constexpr int NBAR = 4 + 8 + NDP + 2 * NSET + 2 * QST;
   static constexpr int USED = BAR + 8 * NBAR + 16;
   // the tiles need 1024-byte alignment: the window starts so aligned on this GPU, and
   // the kernel checks that what rounding takes is there
@@ -482,8 +760,10 @@ __global__ void __launch_bounds__(NT, 1)
 xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                  const __grid_constant__ Plan p) {
-  using L = KvSmem<DP, BIAS>;
-  constexpr int TILE = L::TILE, T64 = L::T64, QST = L::QST;
+  using L = Kv<DP, BIAS>;
+  constexpr int TILE = L::TILE, QTILE = L::QTILE, QST = L::QST, NSET = L::NSET, NDP = L::NDP, BQ = L::BQ;
+  constexpr int GROUPS = L::GROUPS, QBOX = BQ * 128;
+  constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, BQ, false, false);
   constexpr uint32_t IDESC_ACC = ptx::idesc_bf16_f32(128, DP, false, true);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -494,27 +774,33 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   }
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + L::BAR;
-  const uint32_t bar_kv = bars, bar_fin = bars + 8u, sdp_drain = bars + 16u;
-  auto sdp_full = [&](int b) { return bars + 8u * (3 + b); };   // S^T and dP^T formed
-  auto pd_full = [&](int b) { return bars + 8u * (5 + b); };    // P^T and dS^T written over them
-  auto pd_empty = [&](int b) { return bars + 8u * (7 + b); };   // and read
-  auto q_full = [&](int s) { return bars + 8u * (9 + s); };
-  auto q_empty = [&](int s) { return bars + 8u * (9 + QST + s); };
+  const uint32_t bar_fin = bars, drain = bars + 8u, acc_empty = bars + 16u, dp_empty = bars + 24u;
+  auto s_full = [&](uint32_t b) { return bars + 8u * (4 + b); };    // S^T formed
+  auto p_full = [&](uint32_t b) { return bars + 8u * (6 + b); };    // P^T written
+  auto ds_full = [&](uint32_t b) { return bars + 8u * (8 + b); };   // dS^T written
+  auto pd_empty = [&](uint32_t b) { return bars + 8u * (10 + b); };  // and both read
+  auto dp_full = [&](uint32_t b) { return bars + 8u * (12 + b); };  // dP^T formed
+  auto kv_full = [&](uint32_t e) { return bars + 8u * (12 + NDP + e); };
+  auto kv_empty = [&](uint32_t e) { return bars + 8u * (12 + NDP + NSET + e); };
+  auto q_full = [&](uint32_t s) { return bars + 8u * (12 + NDP + 2 * NSET + s); };
+  auto q_empty = [&](uint32_t s) { return bars + 8u * (12 + NDP + 2 * NSET + QST + s); };
   const uint32_t tslot = bars + 8u * L::NBAR;
-  float* stat = reinterpret_cast<float*>(gbase + L::STAT);
   const Args& a = p.a;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
+  const int cta = blockIdx.x, G = gridDim.x;
 
   if (tid == 0) {
-    ptx::mbar_init(bar_kv, 1);
     ptx::mbar_init(bar_fin, 1);
-    ptx::mbar_init(sdp_drain, 1);
+    ptx::mbar_init(drain, 1);
+    ptx::mbar_init(acc_empty, EW);
+    ptx::mbar_init(dp_empty, EW);
     for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(sdp_full(b), 1);
-      ptx::mbar_init(pd_full(b), EW);
+      ptx::mbar_init(s_full(b), 1);
+      ptx::mbar_init(p_full(b), EW / GROUPS);
+      ptx::mbar_init(ds_full(b), EW / GROUPS);
       ptx::mbar_init(pd_empty(b), 1);
     }
-    for (int s = 0; s < 2 * QST; ++s) ptx::mbar_init(q_full(s), 1);
+    for (int x = 0; x < NDP + 2 * NSET + 2 * QST; ++x) ptx::mbar_init(dp_full(x), 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tk);
     ptx::prefetch_tmap(&tv);
@@ -529,318 +815,325 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + (tslot - base));
-  auto t_st = [&](int b) { return tmem + (uint32_t)(b * 128); };
-  auto t_dpt = [&](int b) { return tmem + (uint32_t)(b * 128 + 64); };
-  const uint32_t t_dv = tmem + 256, t_dk = tmem + 384;
+  auto t_s = [&](uint32_t b) { return tmem + 128u * b; };
+  auto t_dp = [&](uint32_t b) { return NDP == 1 ? tmem + 256u : tmem + 128u * b + 64u; };
+  // where a warp's packed words of its columns 32 c .. stand: P^T at t_s + 32 c
+  auto t_ds = [&](uint32_t b) { return NDP == 1 ? t_s(b) + 16u : t_dp(b); };
+  const uint32_t t_dv = tmem + (DP == 64 ? 384 : 256), t_dk = t_dv + DP;
   pdl_wait();
   pdl_trigger();
   bool ok = true;
+  Work wk;
 
-  // key tile 0 (causal: the most query blocks) first
-  int u = blockIdx.x;
-  const int g = u % a.G;
-  u /= a.G;
-  const int bb = u % a.B, k0 = u / a.B * 128;
-  const int len = a.len(bb), p0 = a.start(bb);
-  const int i0 = a.causal ? max(0, k0 - p0) / 64 : 0;  // blocks before see none of these keys
-  const int per_head = k0 < len ? max(0, (a.Sq + 63) / 64 - i0) : 0;
-  const int n = per_head * a.share;
-  // block ii: of query head g share + ii / per_head, its query block i0 + ii % per_head
-
-  if (warp == 0) {
-    if (lane == 0 && n > 0) {
-      ptx::mbar_arrive_expect_tx(bar_kv, 2 * TILE);
-      load_tile<DP, 128>(base + L::K, &tk, bar_kv, k0, g, bb);
-      load_tile<DP, 128>(base + L::V, &tv, bar_kv, k0, g, bb);
-    }
-    // lse (log2 units) and delta of block ii's 64 queries, two of each per lane; the
-    // next block's are loaded before the wait for its stage
-    int hh = 0, i = i0 - 1;  // of the block loaded last
-    auto ld_stat = [&](int ii, float (&v)[4]) {
-      if (++i == i0 + per_head) {
-        i = i0;
-        ++hh;
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int qi = i * 64 + lane + 32 * x;
-        const bool in = ii < n && qi < a.Sq;
-        const int64_t at = in ? a.stat(bb, g * a.share + hh, qi) : 0;
-        v[x] = in ? lse2_of(a.lse[at]) : INFINITY;
-        v[2 + x] = in ? a.delta[at] : 0.f;
-      }
-    };
-    float cur[4];
-    if (n > 0) ld_stat(0, cur);
-    int nl = 0;  // query blocks whose loads were issued
-    for (int ii = 0; ii < n; ++ii) {
-      const int s = ii % QST, ci = i, ch = hh;
-      float nxt[4];
-      ld_stat(ii + 1, nxt);
-      bool w = true;
-      if (lane == 0 && ii >= QST) w = wait1(q_empty(s), ((ii / QST) & 1) ^ 1);
-      if (!__shfl_sync(0xffffffffu, w, 0)) {
-        ok = false;
-        if (lane == 0) wait_failed(201);
-        break;
-      }
-      float* st = stat + s * 128;
-      st[lane] = cur[0];
-      st[lane + 32] = cur[1];
-      st[64 + lane] = cur[2];
-      st[64 + lane + 32] = cur[3];
-      __syncwarp();  // the warp's stores precede lane 0's arrive on the stage barrier
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(q_full(s), 2 * T64);
-        load_tile<DP, 64>(base + L::Q + s * T64, &tq, q_full(s), ci * 64, g * a.share + ch, bb);
-        load_tile<DP, 64>(base + L::DO + s * T64, &tdo, q_full(s), ci * 64, g * a.share + ch, bb);
-      }
-      nl = ii + 1;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) cur[x] = nxt[x];
-    }
-    if (lane == 0 && n > 0) {
-      // every load issued has landed before the CTA may exit
-      bool dr = wait1(bar_kv, 0);
-      for (int s = 0; s < QST && s < nl; ++s) dr = wait1(q_full(s), ((nl - 1 - s) / QST) & 1) && dr;
-      if (!dr) wait_failed(202);
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
-      ok = wait1(bar_kv, 0);
-      if (!ok) wait_failed(203);
-      for (int ii = 0; ii < n && ok; ++ii) {  // S^T = K Q_i^T, dP^T = V dO_i^T into buffer ii % 2
-        const int s = ii % QST, b = ii & 1;
-        if (!wait1(q_full(s), (ii / QST) & 1) ||
-            (ii >= 2 && !wait1(pd_empty(b), ((ii / 2) & 1) ^ 1))) {  // (block ii - 2 is done with)
-          ok = false;
-          wait_failed(204);
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t qt = base + L::Q + s * T64, dt = base + L::DO + s * T64;
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          ptx::mma_bf16(t_st(b), kmajor_desc(base + L::K, kk), kmajor_desc(qt, kk, BOX64), IDESC_N64, kk > 0);
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          ptx::mma_bf16(t_dpt(b), kmajor_desc(base + L::V, kk), kmajor_desc(dt, kk, BOX64), IDESC_N64, kk > 0);
-        ptx::mma_commit(sdp_full(b));
-      }
-      ptx::mma_commit(sdp_drain);  // completes once every MMA this thread issued has
-      if (!wait1(sdp_drain, 0)) {
-        ok = false;
-        wait_failed(207);
-      }
-    }
-  } else if (warp == ACC_WARP) {
-    if (lane == 0 && n > 0) {
-      for (int ii = 0; ii < n && ok; ++ii) {  // dV += P^T dO_i, dK += dS^T Q_i
-        const int s = ii % QST, b = ii & 1;
-        if (!wait1(pd_full(b), (ii / 2) & 1)) {
-          ok = false;
-          wait_failed(206);
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t qt = base + L::Q + s * T64, dt = base + L::DO + s * T64;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint32_t accum = (ii > 0 || kk > 0) ? 1u : 0u;
-          ptx::mma_bf16_ts(t_dv, t_st(b) + 16u * kk, mnmajor_desc(dt, kk, BOX64), IDESC_ACC, accum);
-          ptx::mma_bf16_ts(t_dk, t_dpt(b) + 16u * kk, mnmajor_desc(qt, kk, BOX64), IDESC_ACC, accum);
-        }
-        // S^T, dP^T of block ii (which also read Q_i, dO_i) completed before P^T and
-        // dS^T could be handed over: the stage is free once these MMAs are
-        ptx::mma_commit(pd_empty(b));
-        ptx::mma_commit(q_empty(s));
-      }
-      ptx::mma_commit(bar_fin);  // completes once every MMA this thread issued has
-      if (!wait1(bar_fin, 0)) {
-        ok = false;
-        wait_failed(211);
-      }
-    }
-  } else {
-    const int qq = warp & 3, c = (warp - 2) >> 2;  // lane quarter; columns 16 c .. + 15
-    const int row = qq * 32 + lane, kj = k0 + row, kw = k0 + qq * 32;
-    const bool valid_k = kj < len;
-    const uint32_t lane_off = (uint32_t)(qq * 32) << 16;
-    int hh = 0, i = i0 - 1;
-    float left = 0.f, right = 0.f, far_left = 0.f, far_right = 0.f;
-    const bool grad = BIAS && a.bias_part != nullptr;
-    float* bucket = reinterpret_cast<float*>(gbase + L::BUCKET) + (warp - 2) * MAX_BUCKETS;
-    float* diag = reinterpret_cast<float*>(gbase + L::DIAG) + (warp - 2) * 48;
-    if (grad) {
-      for (int x = lane; x < a.bias.buckets; x += 32) bucket[x] = 0.f;
-      __syncwarp();
-    }
-    auto flush = [&](int head) {  // the warp's buckets of a finished head, and 0 for the next
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        far_left += __shfl_xor_sync(~0u, far_left, o);
-        far_right += __shfl_xor_sync(~0u, far_right, o);
-      }
-      if (lane == 0) {
-        bucket[a.bias.left] += far_left;
-        bucket[a.bias.right] += far_right;
-      }
-      __syncwarp();
-      far_left = far_right = 0.f;
-      float* out = a.bias_part + ((((int64_t)(g * a.share + head) * a.B + bb) * p.tiles + k0 / 128) * EW + (warp - 2)) *
-                                     a.bias.buckets;
-      for (int x = lane; x < a.bias.buckets; x += 32) {
-        out[x] = bucket[x];
-        bucket[x] = 0.f;
-      }
-      __syncwarp();
-    };
-    for (int ii = 0; ii < n && ok; ++ii) {
-      const int s = ii % QST, b = ii & 1;
-      if (++i == i0 + per_head) {
-        if (grad) flush(hh);
-        i = i0;
-        ++hh;
-      }
-      if (BIAS && i == i0) {
-        left = *a.bias.at(g * a.share + hh, -a.bias.R);
-        right = *a.bias.at(g * a.share + hh, a.bias.R);
-      }
-      // this block's S^T, dP^T are in TMEM (which also means its stage, and the lse and
-      // delta stored with it, have landed)
-      if (!warp_wait(sdp_full(b), (ii / 2) & 1) || !warp_wait(q_full(s), (ii / QST) & 1)) {
-        ok = false;
-        if (lane == 0) wait_failed(208);
-        break;
-      }
-      ptx::tc_fence_after();
-      float v[16], w[16];
-      ptx::tmem_ld16x2(t_st(b) + lane_off + c * 16, t_dpt(b) + lane_off + c * 16, v, w);
-      const float* st = stat + s * 128 + c * 16;  // lse of these 16 queries; delta at + 64
-      const int qb = i * 64 + c * 16;
-      float mul = p.scale_log2, add = 0.f;
-      const bool on_right = BIAS && kw - (p0 + qb + 15) >= a.bias.R;
-      const bool on_left = BIAS && !on_right && kw + 31 - (p0 + qb) <= -a.bias.R;
-      if (BIAS) {
-        if (on_right) {
-          add = right;
-        } else if (on_left) {
-          add = left;
-        } else {
-          const float* bv = a.bias.at(g * a.share + hh, kj - (p0 + qb));
-#pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] = fmaf(v[x], p.scale_log2, __ldg(bv - x));
-          mul = 1.f;
-        }
-      }
-      uint32_t pp[8], pd[8];
-      // scores wholly visible need no mask (warp-uniform)
-      const bool full = kw + 32 <= len && qb + 16 <= a.Sq && (!a.causal || p0 + qb >= kw + 31);
-      if (full) {
-        const uint64_t sc = f2_splat(mul), ad = f2_splat(add);
-#pragma unroll
-        for (int x = 0; x < 16; x += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(st + x);
-          const float4 d4 = *reinterpret_cast<const float4*>(st + 64 + x);
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float l0 = e == 0 ? l4.x : l4.z, l1 = e == 0 ? l4.y : l4.w;
-            const float d0 = e == 0 ? d4.x : d4.z, d1 = e == 0 ? d4.y : d4.w;
-            uint64_t sh = f2_pack(-l0, -l1);
-            if (BIAS) sh = f2_add(sh, ad);
-            const uint64_t y = f2_fma(f2_pack(v[x + e], v[x + e + 1]), sc, sh);
-            const uint64_t pr = f2_pack(fast_exp2(f2_lo(y)), fast_exp2(f2_hi(y)));
-            const uint64_t ds = f2_mul(pr, f2_add(f2_pack(w[x + e], w[x + e + 1]), f2_pack(-d0, -d1)));
-            pp[(x + e) / 2] = pack2(f2_lo(pr), f2_hi(pr));
-            pd[(x + e) / 2] = pack2(f2_lo(ds), f2_hi(ds));
-            if (BIAS) {
-              w[x + e] = f2_lo(ds);
-              w[x + e + 1] = f2_hi(ds);
+  if (warp < EW0) {
+    fewer_registers<REGS_ISSUE>();
+    if (warp == 0) {
+      if (ptx::elect_one()) {
+        uint32_t ii = 0, nk = 0;  // blocks and items with blocks so far
+        for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
+          const KvItem it = kv_item<BQ>(p, wk);
+          if (it.n == 0) continue;
+          const uint32_t e = nk % NSET;
+          if (nk >= NSET && !wait1(kv_empty(e), ((nk / NSET) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          ptx::mbar_arrive_expect_tx(kv_full(e), 2 * TILE);
+          load_tile<DP, 128>(base + L::KV + 2 * e * TILE, &tk, kv_full(e), it.k0, it.g, it.b);
+          load_tile<DP, 128>(base + L::KV + (2 * e + 1) * TILE, &tv, kv_full(e), it.k0, it.g, it.b);
+          ++nk;
+          int head = it.g * a.share + it.first / it.per_head, i = it.i0 + it.first % it.per_head;
+          for (int j = 0; j < it.n; ++j, ++ii) {
+            const uint32_t s = ii % QST;
+            if (ii >= QST && !wait1(q_empty(s), ((ii / QST) & 1) ^ 1)) {
+              ok = false;
+              break;
+            }
+            ptx::mbar_arrive_expect_tx(q_full(s), 2 * QTILE + 2 * BQ * 4);
+            if (BQ == 64) {
+              load_tile<DP, 64>(base + L::Q + s * QTILE, &tq, q_full(s), i * 64, head, it.b);
+              load_tile<DP, 64>(base + L::DO + s * QTILE, &tdo, q_full(s), i * 64, head, it.b);
+            } else {
+              load_two<DP>(base + L::Q + s * QTILE, &tq, q_full(s), i * 128, head, it.b);
+              load_two<DP>(base + L::DO + s * QTILE, &tdo, q_full(s), i * 128, head, it.b);
+            }
+            const int64_t at = ((int64_t)it.b * a.H + head) * a.q_pitch + i * BQ;
+            const uint32_t st = base + L::STAT + s * (2 * BQ * 4);
+            ptx::bulk_load(st, a.neg_lse2 + at, BQ * 4, q_full(s));
+            ptx::bulk_load(st + BQ * 4, a.delta + at, BQ * 4, q_full(s));
+            if (++i == it.i0 + it.per_head) {
+              i = it.i0;
+              ++head;
             }
           }
         }
-      } else {
-        // queries qb + x with x < lo are before this key (causal), those with x >= hi past
-        // the last; a key past the sequence's sees none
-        const int lo = a.causal ? kj - p0 - qb : -(1 << 30), hi = valid_k ? a.Sq - qb : 0;
+        if (!ok) wait_failed(201);
+        // every load issued has landed before the CTA may exit
+        bool dr = true;
+        for (uint32_t e = 0; e < NSET; ++e)
+          if (nk > e) dr = wait1(kv_full(e), ((nk - 1 - e) / NSET) & 1) && dr;
+        for (uint32_t s = 0; s < QST; ++s)
+          if (ii > s) dr = wait1(q_full(s), ((ii - 1 - s) / QST) & 1) && dr;
+        if (!dr) wait_failed(202);
+      }
+    } else if (warp == 1) {
+      if (ptx::elect_one()) {
+        uint32_t ii = 0, nk = 0;
+        for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
+          const KvItem it = kv_item<BQ>(p, wk);
+          if (it.n == 0) continue;
+          const uint32_t e = nk % NSET;
+          if (!wait1(kv_full(e), (nk / NSET) & 1)) {
+            ok = false;
+            wait_failed(203);
+            break;
+          }
+          ++nk;
+          const uint32_t kt = base + L::KV + 2 * e * TILE, vt = kt + TILE;
+          for (int j = 0; j < it.n; ++j, ++ii) {  // S^T = K Q_i^T, dP^T = V dO_i^T
+            const uint32_t s = ii % QST, b = ii & 1;
+            // (the accumulations of the block before the last, whose operands lay in this
+            // buffer, are done)
+            if (!wait1(q_full(s), (ii / QST) & 1) || (ii >= 2 && !wait1(pd_empty(b), ((ii / 2) & 1) ^ 1))) {
+              ok = false;
+              wait_failed(204);
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t qt = base + L::Q + s * QTILE, dt = base + L::DO + s * QTILE;
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const bool in = x >= lo && x < hi;
-          const float e = fast_exp2(fmaf(v[x], mul, add - st[x]));
-          v[x] = in ? e : 0.f;
-          w[x] = in ? e * (w[x] - st[64 + x]) : 0.f;
+            for (int kk = 0; kk < DP / 16; ++kk)
+              ptx::mma_bf16(t_s(b), kmajor_desc(kt, kk), kmajor_desc(qt, kk, QBOX), IDESC_S, kk > 0);
+            ptx::mma_commit(s_full(b));
+            if (NDP == 1) {  // (the element-wise warps have loaded the previous block's dP^T)
+              if (ii >= 1 && !wait1(dp_empty, (ii - 1) & 1)) {
+                ok = false;
+                wait_failed(205);
+                break;
+              }
+              ptx::tc_fence_after();
+            }
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk)
+              ptx::mma_bf16(t_dp(b), kmajor_desc(vt, kk), kmajor_desc(dt, kk, QBOX), IDESC_S, kk > 0);
+            ptx::mma_commit(dp_full(NDP == 1 ? 0 : b));
+          }
+          if (ok) ptx::mma_commit(kv_empty(e));  // the item's last read of K and V
         }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          pp[x] = pack2(v[2 * x], v[2 * x + 1]);
-          pd[x] = pack2(w[2 * x], w[2 * x + 1]);
+        ptx::mma_commit(drain);  // completes once every MMA this thread issued has
+        if (!wait1(drain, 0)) {
+          ok = false;
+          wait_failed(207);
         }
       }
-      ptx::tmem_st8_nowait(t_st(b) + lane_off + c * 16, pp);
-      ptx::tmem_st8_nowait(t_dpt(b) + lane_off + c * 16, pd);
+    } else if (warp == ACC_WARP) {
+      if (ptx::elect_one()) {
+        uint32_t ii = 0, nk = 0;
+        for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
+          const KvItem it = kv_item<BQ>(p, wk);
+          if (it.n == 0) continue;
+          // (the element-wise warps have read the item before's dV and dK)
+          if (nk > 0 && !wait1(acc_empty, (nk - 1) & 1)) {
+            ok = false;
+            wait_failed(210);
+            break;
+          }
+          for (int j = 0; j < it.n; ++j, ++ii) {  // dV += P^T dO_i, dK += dS^T Q_i
+            const uint32_t s = ii % QST, b = ii & 1;
+            const uint32_t qt = base + L::Q + s * QTILE, dt = base + L::DO + s * QTILE;
+            if (!wait1(p_full(b), (ii / 2) & 1)) {
+              ok = false;
+              wait_failed(206);
+              break;
+            }
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < BQ / 16; ++kk)
+              ptx::mma_bf16_ts(t_dv, t_s(b) + 32u * (kk >> 1) + 8u * (kk & 1), mnmajor_desc(dt, kk, QBOX), IDESC_ACC,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+            if (!wait1(ds_full(b), (ii / 2) & 1)) {
+              ok = false;
+              wait_failed(213);
+              break;
+            }
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < BQ / 16; ++kk)
+              ptx::mma_bf16_ts(t_dk, t_ds(b) + 32u * (kk >> 1) + 8u * (kk & 1), mnmajor_desc(qt, kk, QBOX), IDESC_ACC,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+            // S^T, dP^T of block ii (which also read Q_i, dO_i) completed before P^T and
+            // dS^T could be handed over: the stage is free once these MMAs are
+            ptx::mma_commit(pd_empty(b));
+            ptx::mma_commit(q_empty(s));
+          }
+          if (!ok) break;
+          ptx::mma_commit(bar_fin);  // the item's dV and dK are complete once this is
+          ++nk;
+        }
+        // every MMA this thread issued is complete before the CTA may exit
+        if (nk > 0 && !wait1(bar_fin, (nk - 1) & 1)) {
+          ok = false;
+          wait_failed(211);
+        }
+        if (!ok) {  // one more commit drains whatever was issued after the last finished item
+          ptx::mma_commit(bar_fin);
+          (void)wait1(bar_fin, nk & 1);
+        }
+      }
+    }
+  } else {
+    more_registers<REGS_EW>();
+    const int qq = warp & 3, part = (warp - EW0) >> 2;  // lane quarter
+    const int group = GROUPS == 2 ? part >> 1 : 0, c = GROUPS == 2 ? part & 1 : part;  // columns 32 c ..
+    const uint32_t lane_off = (uint32_t)(qq * 32) << 16;
+    const bool grad = BIAS && a.bias_part != nullptr;
+    KvBias kb;
+    if (grad)
+      kb.init(a, base + L::BUCKET + (warp - EW0) * MAX_BUCKETS * 4, base + L::DIAG + (warp - EW0) * 256, lane);
+    // Block ii of the warp, queries from qi on: weights and dS (masked where !FULL).
+    auto block = [&](auto FULL, uint32_t ii, int h, int kw, int len, int p0, int qi) {
+      const uint32_t b = ii & 1, own = lane_off + c * 32;
+      const uint32_t st = base + L::STAT + ii % QST * (2 * BQ * 4) + c * 128;
+      const int pq = p0 + qi;
+      // queries qi + x with x < lo are before this key (causal), those with x >= hi past the
+      // last; a key past the sequence's sees none
+      int lo = 0, hi = 0;
+      if (!FULL) {
+        lo = a.causal ? kw + lane - pq : -(1 << 30);
+        hi = kw + lane < len ? a.Sq - qi : 0;
+      }
+      float v[32];
+      ptx::tmem_ld32(t_s(b) + own, v);
+      KvTile<BIAS> tile;
+      tile.start(p, h, kw, pq, lane, v);
+      tile.weights(st, v);
+      if (!FULL) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+          if (x < lo || x >= hi) v[x] = 0.f;
+      }
+      {
+        uint32_t pk[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) pk[x] = pack2(v[2 * x], v[2 * x + 1]);
+        ptx::tmem_st16_nowait(t_s(b) + own, pk);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_full(b));
+      }
+      if (!warp_wait(dp_full(NDP == 1 ? 0 : b), (NDP == 1 ? ii : ii / 2) & 1)) {
+        if (lane == 0) wait_failed(209);
+        return false;
+      }
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float w[16];
+        ptx::tmem_ld16(t_dp(b) + own + 16 * half, w);
+        if (NDP == 1 && half == 1) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(dp_empty);  // dP^T's buffer may be overwritten
+        }
+        if (half == 0) gradients<0>(st + 4 * BQ, w, v);
+        else gradients<16>(st + 4 * BQ, w, v);
+        if (!FULL) {  // (0 times what a hidden key holds)
+#pragma unroll
+          for (int x = 16 * half; x < 16 * half + 16; ++x)
+            if (x < lo || x >= hi) v[x] = 0.f;
+        }
+        uint32_t pk[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) pk[x] = pack2(v[16 * half + 2 * x], v[16 * half + 2 * x + 1]);
+        ptx::tmem_st8_nowait(t_ds(b) + own + 8 * half, pk);
+      }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(pd_full(b));
-      if (!grad) continue;
-      if (!on_left && !on_right) {
-        // sums along the diagonals, that of element (r, x) r - x + 15
-        float run = 0.f;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          run = __shfl_up_sync(0xffffffffu, run, 1);
-          run = (lane == 0 ? 0.f : run) + w[x];
-          if (lane == 31) diag[46 - x] = run;
+      if (lane == 0) ptx::mbar_arrive(ds_full(b));
+      if (BIAS && grad) kb.sum(a, tile.on_left, tile.on_right, kw - pq - 31, lane, v);
+      return true;
+    };
+    uint32_t ii0 = 0, nk = 0;
+    for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
+      int n;
+      {
+        const KvItem it = kv_item<BQ>(p, wk);
+        n = it.n;
+        const int kw = it.k0 + qq * 32, end = (it.g + 1) * a.share;
+        int h = it.g * a.share;  // the head whose buckets are being summed
+        int j = 0;
+        if (GROUPS == 2) j = (int)((ii0 + (uint32_t)group) & 1);  // the group's first block
+        int i = it.first + j;
+        for (; j < n; j += GROUPS, i += GROUPS) {
+          const uint32_t ii = ii0 + (uint32_t)j;
+          while (i >= it.per_head) {  // (i: the block's place among its head's)
+            if (grad) kb.flush(p, wk, h, warp - EW0, lane);
+            i -= it.per_head;
+            ++h;
+          }
+          // this block's lse and delta have landed, and its S^T is in TMEM
+          if (!warp_wait(q_full(ii % QST), (ii / QST) & 1) || !warp_wait(s_full(ii & 1), (ii / 2) & 1)) {
+            ok = false;
+            if (lane == 0) wait_failed(208);
+            break;
+          }
+          ptx::tc_fence_after();
+          // scores wholly visible need no mask (warp-uniform)
+          const int qi = (it.i0 + i) * BQ + c * 32;
+          const bool full = kw + 32 <= it.len && qi + 32 <= a.Sq && (!a.causal || it.p0 + qi >= kw + 31);
+          ok = full ? block(std::true_type{}, ii, h, kw, it.len, it.p0, qi)
+                    : block(std::false_type{}, ii, h, kw, it.len, it.p0, qi);
+          if (!ok) break;
         }
-        if (lane < 31) diag[lane] = run;
-        __syncwarp();
-        const int n0 = kw - (p0 + qb) - 15;  // the distance of diagonal 0
-        for (int x = lane; x < a.bias.buckets; x += 32) {
-          const int2 r = a.bias.range[x];
-          float y = 0.f;
-          for (int d = max(0, r.x - n0); d <= min(46, r.y - n0); ++d) y += diag[d];
-          bucket[x] += y;
-        }
-        __syncwarp();
-      } else {
-        float sum = 0.f;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) sum += w[x];
-        if (on_left) far_left += sum;
-        else far_right += sum;
+        if (!ok) break;
+        ii0 += (uint32_t)n;
+        if (grad)  // (heads without blocks too: their partial sums are 0)
+          for (; h < end; ++h) kb.flush(p, wk, h, warp - EW0, lane);
       }
-    }
-    if (grad && ok) {  // (heads without blocks too: their partial sums are 0)
-      flush(hh);
-      for (int x = hh + 1; x < a.share; ++x) flush(x);
-    }
-    bool fin = true;
-    if (n > 0) fin = warp_wait(bar_fin, 0);
-    ptx::tc_fence_after();
+      if (n > 0) {
+        if (!warp_wait(bar_fin, nk & 1)) {
+          ok = false;
+          if (lane == 0) wait_failed(212);
+          break;
+        }
+        ++nk;
+        ptx::tc_fence_after();
+      }
+      // (the item once more: what is not needed among its blocks holds no registers there)
+      asm volatile("" : "+r"(wk.item));
+      const KvItem it = kv_item<BQ>(p, wk);
+      float* const sums = wk.piece < 0 ? nullptr : p.part + (int64_t)wk.part * 2 * 128 * a.D;
+      const int kw = it.k0 + qq * 32;
+      // 2 DP columns of dK and dV: DP / 2 of them to each of the four column groups
+      const int key = kw + lane;
+      const bool in = key < it.len && it.n > 0;
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {  // dK (scaled), then dV
-      float v0[32];
-      // tcgen05.ld is warp-collective: every lane loads (DP = 64: the last two column
-      // groups' are not used)
-      if (n > 0) ptx::tmem_ld32((part == 0 ? t_dk : t_dv) + lane_off + (c * 32 < DP ? c * 32 : 0), v0);
-      const Strides& sd = part == 0 ? a.sdk : a.sdv;
-      const float sc = part == 0 ? a.scale : 1.f;
-      const bool store = ok && fin && kj < a.Sk && c * 32 < DP;
+      for (int x = 0; x < DP / 64; ++x) {
+        const bool dk = DP == 64 ? part < 2 : x == 0;
+        const int col = DP == 64 ? (part & 1) * 32 : part * 32;
+        float v[32];
+        if (it.n > 0) {
+          ptx::tmem_ld32((dk ? t_dk : t_dv) + lane_off + col, v);  // every lane loads
+          if (x == DP / 64 - 1) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(acc_empty);
+          }
+        }
 #pragma unroll
-      for (int x = 0; x < 32; ++x)  // nothing of what stands behind the sequence's keys
-        if (!valid_k || n == 0) v0[x] = 0.f;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(part == 0 ? a.dk : a.dv) + bb * sd.b + kj * sd.s + g * sd.h + c * 32;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (store && c * 32 + 8 * x < a.D)
-          *reinterpret_cast<uint4*>(out + 8 * x) =
-              make_uint4(pack2(v0[8 * x] * sc, v0[8 * x + 1] * sc), pack2(v0[8 * x + 2] * sc, v0[8 * x + 3] * sc),
-                         pack2(v0[8 * x + 4] * sc, v0[8 * x + 5] * sc), pack2(v0[8 * x + 6] * sc, v0[8 * x + 7] * sc));
-      __syncwarp();  // the next tcgen05.ld is warp-collective
-    }
-    if (!fin) {
-      ok = false;
-      if (lane == 0) wait_failed(212);
+        for (int y = 0; y < 32; ++y) v[y] = in ? v[y] : 0.f;  // (0 behind the sequence's keys)
+        if (key < a.Sk && col < a.D) {
+          const Strides& sd = dk ? a.sdk : a.sdv;
+          if (sums)
+            store_part(sums + ((dk ? 0 : 128) + key - it.k0) * a.D + col, v, a.D - col);
+          else
+            store_row(static_cast<__nv_bfloat16*>(dk ? a.dk : a.dv) + it.b * sd.b + key * sd.s + it.g * sd.h + col, v,
+                      a.D - col, dk ? a.scale : 1.f);
+        }
+        __syncwarp();  // the next tcgen05.ld is warp-collective
+      }
     }
   }
   if (!ok) atomicCAS(&g_xattn_bwd_error, 0, 5);
@@ -852,49 +1145,115 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   }
 }
 
+// ---- pieces joined ------------------------------------------------------------------------
+// blockIdx.y: a cut item of dq, then of dk, then of dv; 32 rows a CTA, 8 lanes a row.
+__global__ void __launch_bounds__(256)
+xattn_bwd_join_kernel(const __grid_constant__ Plan pq, const __grid_constant__ Plan pk) {
+  pdl_wait();
+  pdl_trigger();
+  const Args& a = pq.a;
+  const int nq = pq.cut.pieces > 1 ? pq.cut.rest : 0, nk = pk.cut.pieces > 1 ? pk.cut.rest : 0;
+  int y = blockIdx.y;
+  const bool is_q = y < nq, is_k = !is_q && y < nq + nk;
+  y -= is_q ? 0 : is_k ? nq : nq + nk;
+  const Plan& p = is_q ? pq : pk;
+  const int row = blockIdx.x * 32 + threadIdx.x / 8, lane = threadIdx.x % 8;
+  const int item = p.cut.whole + y;
+  __nv_bfloat16* out;
+  if (is_q) {
+    const int bh = a.H * a.B, r = item % bh, qi = (p.tiles - 1 - item / bh) * 128 + row;
+    if (qi >= a.Sq) return;
+    out = static_cast<__nv_bfloat16*>(a.dq) + r / a.H * a.sdq.b + qi * a.sdq.s + r % a.H * a.sdq.h;
+  } else {
+    const int bt = item / a.G, key = bt / a.B * 128 + row;
+    if (key >= a.Sk) return;
+    const Strides& sd = is_k ? a.sdk : a.sdv;
+    out = static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dv) + bt % a.B * sd.b + key * sd.s + item % a.G * sd.h;
+  }
+  const int64_t step = (int64_t)(is_q ? 1 : 2) * 128 * a.D;
+  const float* part = p.part + y * p.cut.pieces * step + ((is_q || is_k ? 0 : 128) + row) * a.D;
+  const float scale = is_q || is_k ? a.scale : 1.f;
+  for (int c = 4 * lane; c < a.D; c += 32) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int q = 0; q < p.cut.pieces; ++q) {
+      const float4 x = *reinterpret_cast<const float4*>(part + q * step + c);
+      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(out + c) = make_uint2(pack2(s.x * scale, s.y * scale), pack2(s.z * scale, s.w * scale));
+  }
+}
+
 template <int DP, bool BIAS>
-cudaError_t launch(const Args& a, cudaStream_t st) {
-  CUtensorMap tq128, tdo128, tq64, tdo64, tk, tv;
-  OASES_TRY(map4d(&tq128, a.q, a.sq, a.D, a.Sq, a.H, a.B, 128));
-  OASES_TRY(map4d(&tdo128, a.d_o, a.sdo, a.D, a.Sq, a.H, a.B, 128));
-  OASES_TRY(map4d(&tq64, a.q, a.sq, a.D, a.Sq, a.H, a.B, 64));
-  OASES_TRY(map4d(&tdo64, a.d_o, a.sdo, a.D, a.Sq, a.H, a.B, 64));
+cudaError_t launch(const Args& a, const BwdCut& cut, cudaStream_t st) {
+  CUtensorMap tq, tdo, tk, tv;
+  OASES_TRY(map4d(&tq, a.q, a.sq, a.D, a.Sq, a.H, a.B, 64));
+  OASES_TRY(map4d(&tdo, a.d_o, a.sdo, a.D, a.Sq, a.H, a.B, 64));
   OASES_TRY(map4d(&tk, a.k, a.sk, a.D, a.Sk, a.G, a.B, 128));
   OASES_TRY(map4d(&tv, a.v, a.sv, a.D, a.Sk, a.G, a.B, 128));
-  using Dq = DqSmem<DP>;
-  using Kv = KvSmem<DP, BIAS>;
+  constexpr int DQ_BYTES = DqSmem<DP>::BYTES, DKV_BYTES = Kv<DP, BIAS>::BYTES;
   static DeviceOnce attr;
-  OASES_TRY(attr.run([] {
-    const cudaError_t e = cudaFuncSetAttribute(xattn_dq_kernel<DP, BIAS>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, Dq::BYTES);
+  OASES_TRY(attr.run([&] {
+    for (const void* f : {(const void*)xattn_dq_kernel<DP, BIAS>, (const void*)xattn_dkv_kernel<DP, BIAS>}) {
+      cudaFuncAttributes at;
+      const cudaError_t e = cudaFuncGetAttributes(&at, f);
+      if (e != cudaSuccess) return e;
+      if (at.numRegs != REGS) return cudaErrorInvalidKernelImage;  // (the warpgroups' shares would not add up)
+    }
+    const cudaError_t e =
+        cudaFuncSetAttribute(xattn_dq_kernel<DP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, DQ_BYTES);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(xattn_dkv_kernel<DP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Kv::BYTES);
+    return cudaFuncSetAttribute(xattn_dkv_kernel<DP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, DKV_BYTES);
   }));
-  const int64_t rows = (int64_t)a.B * a.Sq * a.H;
+  const int64_t rows = (int64_t)a.B * a.q_pitch * a.H;
   if ((rows + 15) / 16 > INT32_MAX) return cudaErrorInvalidConfiguration;
-  OASES_TRY(launch_pdl(xattn_delta_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, st, a, rows));
-  Plan p;
-  p.a = a;
-  p.scale_log2 = LOG2E * a.scale;
-  p.tiles = (a.Sq + 127) / 128;
-  const int64_t items = (int64_t)p.tiles * a.B * a.H;
-  const int64_t ctas = (int64_t)((a.Sk + 127) / 128) * a.B * a.G;
-  if (items > INT32_MAX / 2 || ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  p.items = (int)items;
-  Plan pk = p;
+  OASES_TRY(launch_pdl(xattn_stats_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, st, a, rows));
+  Plan pq;
+  pq.a = a;
+  pq.scale_log2 = LOG2E * a.scale;
+  Plan pk = pq;
+  pq.tiles = (a.Sq + 127) / 128;
+  pq.cut = cut.dq;
+  pq.part = a.piece_dq;
   pk.tiles = (a.Sk + 127) / 128;
-  OASES_TRY(launch_pdl(xattn_dq_kernel<DP, BIAS>, dim3((unsigned)std::min<int64_t>(items, sm_count())), dim3(NT),
-                       Dq::BYTES, st, tq128, tdo128, tk, tv, p));
-  return launch_pdl(xattn_dkv_kernel<DP, BIAS>, dim3((unsigned)ctas), dim3(NT), Kv::BYTES, st, tk, tv, tq64,
-                    tdo64, pk);
+  pk.cut = cut.dkv;
+  pk.part = a.piece_dkv;
+  auto grid = [](const Pieces& c) { return dim3((unsigned)(c.whole ? sm_count() : c.rest * c.pieces)); };
+  OASES_TRY(launch_pdl(xattn_dq_kernel<DP, BIAS>, grid(pq.cut), dim3(NT), DQ_BYTES, st, tq, tdo, tk, tv, pq));
+  OASES_TRY(launch_pdl(xattn_dkv_kernel<DP, BIAS>, grid(pk.cut), dim3(NT), DKV_BYTES, st, tk, tv, tq, tdo, pk));
+  const int joins = (pq.cut.pieces > 1 ? pq.cut.rest : 0) + (pk.cut.pieces > 1 ? 2 * pk.cut.rest : 0);
+  if (joins == 0) return cudaSuccess;
+  return launch_pdl(xattn_bwd_join_kernel, dim3(4, (unsigned)joins), dim3(256), 0, st, pq, pk);
+}
+
+// Items in whole rounds of the SMs, and the rest in as many pieces as fill one more round,
+// `least` of an item's `blocks` to a piece at least.
+Pieces pieces(int64_t items, int blocks, int least) {
+  const int sms = sm_count();
+  Pieces c;
+  c.rest = (int)(items % sms);
+  c.whole = (int)(items - c.rest);
+  c.pieces = c.rest ? std::max(1, std::min(sms / c.rest, blocks / least)) : 1;
+  return c;
 }
 
 }  // namespace
 
+bool xattn_bwd_cut(const Args& a, BwdCut* cut) {
+  const int64_t nq = (int64_t)((a.Sq + 127) / 128) * a.B * a.H, nk = (int64_t)((a.Sk + 127) / 128) * a.B * a.G;
+  if (std::max(nq, nk) > INT32_MAX / 2) return false;
+  const int bq = a.D <= 64 ? 128 : 64;
+  // (a piece's sums cost 64 or 128 KB written and read again, the time of about two blocks)
+  cut->dq = pieces(nq, (a.Sk + 127) / 128, 4);
+  cut->dkv = pieces(nk, (int)std::min<int64_t>((int64_t)((a.Sq + bq - 1) / bq) * a.share, INT32_MAX / 2), a.D <= 64 ? 4 : 8);
+  return true;
+}
+
 cudaError_t xattn_bwd_tc(const Args& a, cudaStream_t st) {
-  if (a.D <= 64) return a.bias.buckets ? launch<64, true>(a, st) : launch<64, false>(a, st);
-  return a.bias.buckets ? launch<128, true>(a, st) : launch<128, false>(a, st);
+  BwdCut cut;
+  if (!xattn_bwd_cut(a, &cut)) return cudaErrorInvalidConfiguration;
+  if (a.D <= 64) return a.bias.buckets ? launch<64, true>(a, cut, st) : launch<64, false>(a, cut, st);
+  return a.bias.buckets ? launch<128, true>(a, cut, st) : launch<128, false>(a, cut, st);
 }
 
 int xattn_bwd_read_and_clear_error() {

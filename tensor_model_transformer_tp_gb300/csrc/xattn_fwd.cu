@@ -204,7 +204,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       if (!dr) wait_failed(13);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       uint32_t qc0 = 0u, qc1 = 0u, pc0 = 0u, pc1 = 0u;  // Q loads and hand-overs of P consumed
       // A ring entry is read by tile 0 first (it starts every item before tile 1 does
       // and its blocks are no more), so tile 1's MMA releases it, or tile 0's where tile
@@ -385,14 +385,13 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         }
         // P = 2^(s - m_ref): scale and shift in one fp32x2 FMA per pair, the row sum in
         // four fp32x2 accumulators; the packed word of keys (2c, 2c + 1) goes to sv[c]
-        const bool live = m_ref != -INFINITY;
-        const uint64_t sc2 = f2_splat(mul), nm2 = f2_splat(add - m_ref);
+        // (no visible key so far: every weight 0, but a NaN stays one)
+        const uint64_t sc2 = f2_splat(mul), nm2 = f2_splat(m_ref == -INFINITY ? -INFINITY : add - m_ref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
           const uint64_t x = f2_fma(f2_pack(sv[2 * c], sv[2 * c + 1]), sc2, nm2);
-          float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
-          if (!live) p0 = p1 = 0.f;  // (a row with no visible key; x is NaN there)
+          const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
           acc[c % 4] = f2_add(acc[c % 4], f2_pack(p0, p1));
           sv[c] = __uint_as_float(pack2(p0, p1));
         }

@@ -249,7 +249,7 @@ xattn_dq_simt_kernel(const __grid_constant__ Args a, int tiles) {
       const bool valid = q0 + r < a.Sq;
       if (valid) a.delta[a.stat(b, h, q0 + r)] = d;
       const float l = valid ? a.lse[a.stat(b, h, q0 + r)] : INFINITY;
-      lse[r] = l == -INFINITY ? INFINITY : l;  // a row without keys: every weight 0
+      lse[r] = l < LSE_LOWEST ? INFINITY : l;  // a row without keys: every weight 0
     }
   }
   float acc[4][DP / 16] = {};
@@ -339,7 +339,7 @@ xattn_dkv_simt_kernel(const __grid_constant__ Args a, int tiles) {
       if (threadIdx.x < TQ) {
         const int qi = i * TQ + threadIdx.x;
         const float l = qi < a.Sq ? a.lse[a.stat(b, h, qi)] : INFINITY;
-        lse[threadIdx.x] = l == -INFINITY ? INFINITY : l;
+        lse[threadIdx.x] = l < LSE_LOWEST ? INFINITY : l;
         delta[threadIdx.x] = qi < a.Sq ? a.delta[a.stat(b, h, qi)] : 0.f;
       }
       __syncthreads();

@@ -334,6 +334,25 @@ def test_captured_replayed_and_on_another_stream():
                 assert x is y is None or torch.equal(x, y)
 
 
+# few items over long keys or many queries, whose backward cuts them into pieces
+CUT = [(1, 70, 2100, 2, 1, 64), (2, 1300, 70, 4, 2, 64), (1, 70, 1500, 1, 1, 128),
+       (1, 1300, 150, 2, 1, 128), (3, 900, 1200, 4, 4, 40)]
+
+
+@pytest.mark.parametrize("shape", CUT)
+@pytest.mark.parametrize("biased", [False, True])
+def test_items_in_pieces(shape, biased):
+    lens = [shape[2] - shape[2] // 3 * b for b in range(shape[0])]
+    run("bf16", *shape, lens=lens, buckets=32 if biased else 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_whole_rounds_and_pieces(D):
+    """More items than SMs, the last of them cut: 200 of dq, 160 of dk and dv."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    run("bf16", 1, 1100, 1100, sms // 9 + 4, sms // 9 + 4, D, buckets=16, causal=True)
+
+
 def test_many_sequences_and_heads():
     """More (sequence, head) pairs than SMs, ragged, with splits of long keys."""
     c = Case("bf16", 40, 3, 500, 8, 2, 64, lens=[(37 * i) % 501 for i in range(40)], causal=True,
