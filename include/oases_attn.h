@@ -17,7 +17,9 @@
  * here too, so a shard is a slice of the heads.  The scores are never stored.
  *
  * A query that sees no key (kv_lens[b] = 0, or a bias of -infinity on all of
- * them) has o = 0 and lse = -infinity, and gives no gradient.  What stands in k
+ * them) has o = 0 and lse = -infinity, and gives no gradient.  Nor does one whose
+ * lse lies below -2^20 (a finite bias that hides all of its keys): from there on an
+ * fp32 lse no longer tells their weights.  One that sees a single key has dS = 0.  What stands in k
  * and v at and behind kv_lens[b] is not used, whatever it holds; dk and dv are 0
  * there.  kv_lens values outside [0, k_len] are taken as the nearest in it.
  *
@@ -41,7 +43,8 @@
  *
  * Precision.  Scores, softmax statistics and all sums are fp32.  In bf16 the
  * weights e^(s - m) and dS are rounded to bf16 as operands of the products with
- * v, d_o, k and q; delta is formed from the rounded o.  fp32 rounds nothing but
+ * v, d_o, k and q; delta is formed from the rounded o, but as sum P dP where a query
+ * sees 128 keys or less, and for dk, dv and dbias wherever there is a bias.  fp32 rounds nothing but
  * fp32 sums.
  */
 #ifndef OASES_ATTN_H

@@ -277,7 +277,7 @@ Layout layout(const Shape& s, bool backward) {
     l.rows = (int64_t)a.B * ((a.Sq + 63) / 64);
     BwdCut cut;
     if (a.t == DType::BF16 && xattn_bwd_cut(a, &cut)) {  // (else the call itself refuses)
-      if (cut.dq.pieces > 1) take(&l.piece_dq, (size_t)cut.dq.rest * cut.dq.pieces * 128 * a.D * 4);
+      if (cut.dq.pieces > 1) take(&l.piece_dq, (size_t)cut.dq.rest * cut.dq.pieces * xattn_dq_piece_bytes(a.D));
       if (cut.dkv.pieces > 1) take(&l.piece_dkv, (size_t)cut.dkv.rest * cut.dkv.pieces * 2 * 128 * a.D * 4);
       const int64_t tiles = (int64_t)a.B * ((a.Sk + 127) / 128);  // as kv_item() counts them
       l.rows = (tiles + (tiles - cut.dkv.whole / a.G) * (cut.dkv.pieces - 1)) * DKV_WARPS;

@@ -108,6 +108,7 @@ cudaError_t xattn_few(const xattn::Args& a, const void* table, const xattn::Bord
                       bool bidirectional, cudaStream_t st);
 // bf16, tensor cores
 cudaError_t xattn_fwd_tc(const xattn::Args& a, cudaStream_t st);
+size_t xattn_dq_piece_bytes(int D);
 bool xattn_bwd_cut(const xattn::Args& a, xattn::BwdCut* cut);  // false: too many items
 cudaError_t xattn_bwd_tc(const xattn::Args& a, cudaStream_t st);
 // fp32 (CUDA cores)

@@ -16,7 +16,13 @@
 // before the rounding.
 //
 // Items beyond whole rounds of the GPU's SMs are cut into pieces of their blocks, one for
-// each SM; a piece writes fp32 sums of its own, which xattn_bwd_join_kernel adds in order.
+// each SM; a piece writes fp32 sums of its own, which the join kernels add in order.
+//
+// delta.  From the rounded o it is off by up to 2^-8 of |dO||o|, which shows in rows of few
+// keys (o as large as v) and in the bias's gradient (a row's error, summed over its keys).
+// Its definition is sum P dP, and what dS sums to over a row is the difference: the dq
+// kernel takes it from its first block where a row has no other, and corrects delta for
+// the dkv kernel there and wherever there is a bias.
 //
 // The bias's gradient (dkv kernel).  A warp's 32 x 32 scores that lie R or more from the
 // diagonal on one side belong to one bucket: every thread adds its own.  Nearer ones are
@@ -169,17 +175,23 @@ struct DqSmem {
   static constexpr int TILE = tile_bytes<DP>();
   static constexpr int KST = DP == 64 ? 4 : 3, VST = DP == 64 ? 4 : 2;
   static constexpr int Q = 0, DO = TILE, K = 2 * TILE, V = K + KST * TILE;
-  static constexpr int BAR = V + VST * TILE;
-  static constexpr int NBAR = 12 + 2 * KST + 2 * VST;
-  static constexpr int BYTES = BAR + 8 * NBAR + 16 + 1024;
-  static_assert(BYTES <= 232448, "more than 227 KB of shared memory");
+  static constexpr int RED = V + VST * TILE;  // [column group][128] fp32: partial sums of the rows
+  static constexpr int BAR = RED + 4 * 128 * 4;
+  static constexpr int NBAR = 14 + 2 * KST + 2 * VST;
+  static constexpr int USED = BAR + 8 * NBAR + 16;
+  // the tiles need 1024-byte alignment: the window starts so aligned on this GPU, and
+  // the kernel checks that what rounding takes is there
+  static constexpr int BYTES = USED + 1024 <= 232448 ? USED + 1024 : 232448;
+  static_assert(USED <= 232448, "more than 227 KB of shared memory");
 };
 
 struct DqItem {
   int h, b, q0, p0, len;   // head, sequence, first query and its position, keys
-  int j0, n;               // key blocks: the first, and how many
-  float* part;             // a piece's sums
+  int j0, n, whole;        // key blocks: the first, how many, and how many without the cut
+  float* part;             // a piece's sums: dQ [128][D], then the rows' sums of dS
 };
+// The bytes of a piece of dq are 4 dq_piece(D).
+__host__ __device__ __forceinline__ int64_t dq_piece(int D) { return 128 * (D + 1); }
 __device__ __forceinline__ DqItem dq_item(const Plan& p, const Work& w) {
   const Args& a = p.a;
   const int bh = a.H * a.B;
@@ -194,9 +206,10 @@ __device__ __forceinline__ DqItem dq_item(const Plan& p, const Work& w) {
   const int rows = min(128, a.Sq - it.q0);
   const int vis = a.causal ? min(it.len, max(0, it.p0 + rows)) : it.len;
   int end;
-  cut_blocks(p, w.piece, (vis + 127) / 128, &it.j0, &end);
+  it.whole = (vis + 127) / 128;
+  cut_blocks(p, w.piece, it.whole, &it.j0, &end);
   it.n = end - it.j0;
-  it.part = w.piece < 0 ? nullptr : p.part + (int64_t)w.part * 128 * a.D;
+  it.part = w.piece < 0 ? nullptr : p.part + w.part * dq_piece(a.D);
   return it;
 }
 
@@ -212,6 +225,10 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
+  if (base - raw + L::USED > (uint32_t)L::BYTES) {  // (uniform: every thread leaves)
+    if (threadIdx.x == 0) wait_failed(4);
+    return;
+  }
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + L::BAR;
   const uint32_t qdo_full = bars, qdo_empty = bars + 8u, dp_full = bars + 16u, dp_empty = bars + 24u;
@@ -219,10 +236,11 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
   auto s_full = [&](uint32_t b) { return bars + 8u * (6 + b); };
   auto ds_full = [&](uint32_t b) { return bars + 8u * (8 + b); };    // dS written over S
   auto ds_empty = [&](uint32_t b) { return bars + 8u * (10 + b); };  // and read
-  auto k_full = [&](uint32_t s) { return bars + 8u * (12 + s); };
-  auto k_empty = [&](uint32_t s) { return bars + 8u * (12 + KST + s); };
-  auto v_full = [&](uint32_t s) { return bars + 8u * (12 + 2 * KST + s); };
-  auto v_empty = [&](uint32_t s) { return bars + 8u * (12 + 2 * KST + VST + s); };
+  const uint32_t red_full = bars + 96u, red_empty = bars + 104u;
+  auto k_full = [&](uint32_t s) { return bars + 8u * (14 + s); };
+  auto k_empty = [&](uint32_t s) { return bars + 8u * (14 + KST + s); };
+  auto v_full = [&](uint32_t s) { return bars + 8u * (14 + 2 * KST + s); };
+  auto v_empty = [&](uint32_t s) { return bars + 8u * (14 + 2 * KST + VST + s); };
   const uint32_t tslot = bars + 8u * L::NBAR;
   const Args& a = p.a;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
@@ -235,6 +253,8 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     ptx::mbar_init(dp_empty, EW);
     ptx::mbar_init(bar_fin, 1);
     ptx::mbar_init(drain, 1);
+    ptx::mbar_init(red_full, EW);
+    ptx::mbar_init(red_empty, EW);
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(s_full(b), 1);
       ptx::mbar_init(ds_full(b), EW);
@@ -410,13 +430,30 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
       nl = a.neg_lse2[at];
       nd = a.delta[at];
     };
+    // a row's sum of the four column groups' x, by all 16 warps
+    uint32_t nred = 0;
+    const uint32_t red = base + L::RED + row * 4;
+    auto row_sum = [&](float x, float& sum) {
+      if (nred > 0 && !warp_wait(red_empty, (nred - 1) & 1)) return false;
+      ptx::sts(red + sub * 512, x);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(red_full);
+      if (!warp_wait(red_full, nred & 1)) return false;
+      sum = (ptx::lds(red) + ptx::lds(red + 512)) + (ptx::lds(red + 1024) + ptx::lds(red + 1536));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(red_empty);
+      ++nred;
+      return true;
+    };
     float nl_next, nd_next;
     stats(0, nl_next, nd_next);
     for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
       const DqItem it = dq_item(p, wk);
       const int qi = it.q0 + row;
       const bool valid_q = qi < a.Sq;
-      const float nl = nl_next, nd = nd_next;
+      const float nl = nl_next;
+      float nd = nd_next;
+      float off = 0.f;  // the row's sum of dS: how far delta is from sum P dP
       stats(k + 1, nl_next, nd_next);
       const int w0 = it.p0 + qq * 32;  // position of the warp's first query
       float left = 0.f, right = 0.f;
@@ -466,22 +503,43 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(dp_empty);  // dP's buffer may be overwritten
         uint32_t pk[16];  // dS as packed bf16 pairs (keys 2i, 2i+1 of these 32)
-        if (full) {
+        // keys kb + c with c >= nvis are past the diagonal or the sequence's keys (all of
+        // them for a row past the queries); what dP holds there may be anything
+        const int seen = valid_q ? (a.causal ? min(w0 + lane + 1, it.len) : it.len) : 0;
+        int nvis = seen - kb;
+        if (it.whole == 1) {
+          float x = 0.f, sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x += c < nvis ? v[c] * w[c] : 0.f;
+          if (!row_sum(x, sum)) {
+            ok = false;
+            if (lane == 0) wait_failed(113);
+            break;
+          }
+          off = sum + nd;
+          nd = -sum;
+          if (seen == 1) nvis = 0;  // one key, of weight 1: no gradient, not a rounding's
+        }
+        if (full && it.whole > 1) {
           const uint64_t nd2 = f2_splat(nd);
+          uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const uint64_t ds = f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), f2_add(f2_pack(w[2 * i], w[2 * i + 1]), nd2));
             pk[i] = pack2(f2_lo(ds), f2_hi(ds));
+            if (BIAS) acc[i & 1] = f2_add(acc[i & 1], ds);
+          }
+          if (BIAS) {
+            const uint64_t sum = f2_add(acc[0], acc[1]);
+            off += f2_lo(sum) + f2_hi(sum);
           }
         } else {
-          // keys kb + c with c >= nvis are past the diagonal or the sequence's keys (all
-          // of them for a row past the queries); what dP holds there may be anything
-          const int nvis = valid_q ? (a.causal ? min(w0 + lane + 1, it.len) : it.len) - kb : 0;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float x = 2 * i < nvis ? v[2 * i] * (w[2 * i] + nd) : 0.f;
             const float y = 2 * i + 1 < nvis ? v[2 * i + 1] * (w[2 * i + 1] + nd) : 0.f;
             pk[i] = pack2(x, y);
+            if (BIAS && it.whole > 1) off += x + y;
           }
         }
         ptx::tmem_st16_nowait(own, pk);
@@ -506,6 +564,22 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         if (lane == 0) ptx::mbar_arrive(ds_full(b));
       }
       if (!ok) break;
+      // what follows takes delta as sum P dP
+      if (it.whole == 1 || BIAS) {
+        if (it.whole > 1) {
+          const float x = off;
+          if (!row_sum(x, off)) {
+            ok = false;
+            if (lane == 0) wait_failed(114);
+            break;
+          }
+        }
+        if (it.part) {
+          if (sub == 0) it.part[128 * a.D + row] = it.n > 0 ? off : 0.f;
+        } else if (sub == 0 && it.n > 0) {
+          a.delta[((int64_t)it.b * a.H + it.h) * a.q_pitch + it.q0 + row] = it.whole == 1 ? nd : nd - off;
+        }
+      }
       float v[32];
       if (it.n > 0) {
         // the item's last accumulation is complete (or the MMA thread gave up)
@@ -1038,10 +1112,13 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         }
         if (half == 0) gradients<0>(st + 4 * BQ, w, v);
         else gradients<16>(st + 4 * BQ, w, v);
-        if (!FULL) {  // (0 times what a hidden key holds)
+        if (!FULL) {
+          // 0 times what a hidden key holds; and a query that sees one key, of weight 1, gives
+          // no gradient, not a rounding's: any of a sequence of one key, causal the one at key 0
+          const int first = a.causal && kw + lane == 0 ? lo + 1 : lo, end = len == 1 ? 0 : hi;
 #pragma unroll
           for (int x = 16 * half; x < 16 * half + 16; ++x)
-            if (x < lo || x >= hi) v[x] = 0.f;
+            if (x < first || x >= end) v[x] = 0.f;
         }
         uint32_t pk[8];
 #pragma unroll
@@ -1146,33 +1223,50 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 }
 
 // ---- pieces joined ------------------------------------------------------------------------
-// blockIdx.y: a cut item of dq, then of dk, then of dv; 32 rows a CTA, 8 lanes a row.
+// A cut item's 32 rows a CTA, 8 lanes a row: dq, and -delta of rows whose sums of dS were
+// taken (a block of keys in all, or `sums`).
 __global__ void __launch_bounds__(256)
-xattn_bwd_join_kernel(const __grid_constant__ Plan pq, const __grid_constant__ Plan pk) {
+xattn_dq_join_kernel(const __grid_constant__ Plan p, int sums) {
   pdl_wait();
   pdl_trigger();
-  const Args& a = pq.a;
-  const int nq = pq.cut.pieces > 1 ? pq.cut.rest : 0, nk = pk.cut.pieces > 1 ? pk.cut.rest : 0;
-  int y = blockIdx.y;
-  const bool is_q = y < nq, is_k = !is_q && y < nq + nk;
-  y -= is_q ? 0 : is_k ? nq : nq + nk;
-  const Plan& p = is_q ? pq : pk;
+  const Args& a = p.a;
   const int row = blockIdx.x * 32 + threadIdx.x / 8, lane = threadIdx.x % 8;
-  const int item = p.cut.whole + y;
-  __nv_bfloat16* out;
-  if (is_q) {
-    const int bh = a.H * a.B, r = item % bh, qi = (p.tiles - 1 - item / bh) * 128 + row;
-    if (qi >= a.Sq) return;
-    out = static_cast<__nv_bfloat16*>(a.dq) + r / a.H * a.sdq.b + qi * a.sdq.s + r % a.H * a.sdq.h;
-  } else {
-    const int bt = item / a.G, key = bt / a.B * 128 + row;
-    if (key >= a.Sk) return;
-    const Strides& sd = is_k ? a.sdk : a.sdv;
-    out = static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dv) + bt % a.B * sd.b + key * sd.s + item % a.G * sd.h;
+  const Work w = {p.cut.whole + (int)blockIdx.y, 0, (int)blockIdx.y * p.cut.pieces};
+  const DqItem it = dq_item(p, w);
+  const int qi = it.q0 + row;
+  if (qi >= a.Sq) return;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + it.b * a.sdq.b + qi * a.sdq.s + it.h * a.sdq.h;
+  const int64_t step = dq_piece(a.D);
+  for (int c = 4 * lane; c < a.D; c += 32) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int q = 0; q < p.cut.pieces; ++q) {
+      const float4 x = *reinterpret_cast<const float4*>(it.part + q * step + row * a.D + c);
+      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(out + c) = make_uint2(pack2(s.x * a.scale, s.y * a.scale), pack2(s.z * a.scale, s.w * a.scale));
   }
-  const int64_t step = (int64_t)(is_q ? 1 : 2) * 128 * a.D;
-  const float* part = p.part + y * p.cut.pieces * step + ((is_q || is_k ? 0 : 128) + row) * a.D;
-  const float scale = is_q || is_k ? a.scale : 1.f;
+  if (lane == 0 && (sums || it.whole == 1)) {
+    float off = 0.f;
+    for (int q = 0; q < p.cut.pieces; ++q) off += it.part[q * step + 128 * a.D + row];
+    a.delta[((int64_t)it.b * a.H + it.h) * a.q_pitch + qi] -= off;
+  }
+}
+// dk (even blockIdx.y) and dv of a cut item.
+__global__ void __launch_bounds__(256)
+xattn_dkv_join_kernel(const __grid_constant__ Plan p) {
+  pdl_wait();
+  pdl_trigger();
+  const Args& a = p.a;
+  const int row = blockIdx.x * 32 + threadIdx.x / 8, lane = threadIdx.x % 8;
+  const int y = blockIdx.y / 2, item = p.cut.whole + y, bt = item / a.G, key = bt / a.B * 128 + row;
+  const bool dk = blockIdx.y % 2 == 0;
+  if (key >= a.Sk) return;
+  const Strides& sd = dk ? a.sdk : a.sdv;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dk ? a.dk : a.dv) + bt % a.B * sd.b + key * sd.s + item % a.G * sd.h;
+  const int64_t step = (int64_t)2 * 128 * a.D;
+  const float* part = p.part + y * p.cut.pieces * step + ((dk ? 0 : 128) + row) * a.D;
+  const float scale = dk ? a.scale : 1.f;
   for (int c = 4 * lane; c < a.D; c += 32) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -1220,10 +1314,11 @@ cudaError_t launch(const Args& a, const BwdCut& cut, cudaStream_t st) {
   pk.part = a.piece_dkv;
   auto grid = [](const Pieces& c) { return dim3((unsigned)(c.whole ? sm_count() : c.rest * c.pieces)); };
   OASES_TRY(launch_pdl(xattn_dq_kernel<DP, BIAS>, grid(pq.cut), dim3(NT), DQ_BYTES, st, tq, tdo, tk, tv, pq));
+  if (pq.cut.pieces > 1)
+    OASES_TRY(launch_pdl(xattn_dq_join_kernel, dim3(4, (unsigned)pq.cut.rest), dim3(256), 0, st, pq, (int)BIAS));
   OASES_TRY(launch_pdl(xattn_dkv_kernel<DP, BIAS>, grid(pk.cut), dim3(NT), DKV_BYTES, st, tk, tv, tq, tdo, pk));
-  const int joins = (pq.cut.pieces > 1 ? pq.cut.rest : 0) + (pk.cut.pieces > 1 ? 2 * pk.cut.rest : 0);
-  if (joins == 0) return cudaSuccess;
-  return launch_pdl(xattn_bwd_join_kernel, dim3(4, (unsigned)joins), dim3(256), 0, st, pq, pk);
+  if (pk.cut.pieces == 1) return cudaSuccess;
+  return launch_pdl(xattn_dkv_join_kernel, dim3(4, 2 * (unsigned)pk.cut.rest), dim3(256), 0, st, pk);
 }
 
 // Items in whole rounds of the SMs, and the rest in as many pieces as fill one more round,
@@ -1239,6 +1334,7 @@ Pieces pieces(int64_t items, int blocks, int least) {
 
 }  // namespace
 
+size_t xattn_dq_piece_bytes(int D) { return 4 * (size_t)dq_piece(D); }
 bool xattn_bwd_cut(const Args& a, BwdCut* cut) {
   const int64_t nq = (int64_t)((a.Sq + 127) / 128) * a.B * a.H, nk = (int64_t)((a.Sk + 127) / 128) * a.B * a.G;
   if (std::max(nq, nk) > INT32_MAX / 2) return false;

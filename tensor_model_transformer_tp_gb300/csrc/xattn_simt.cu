@@ -202,10 +202,11 @@ xattn_fwd_simt_kernel(const __grid_constant__ Args a, int tiles) {
 
 // Rows' weights and score gradients from s and dP of a tile (both overwritten):
 // element (i, c) belongs to key `key` and a query at position p whose statistics are
-// lse and delta; visible says whether the key counts.
-__device__ __forceinline__ void weight_and_grad(float& s, float& dp, bool visible, float lse, float delta) {
+// lse and delta; visible says whether the key counts, and alone whether it is the query's
+// only one, of weight 1: no gradient, not a rounding's.
+__device__ __forceinline__ void weight_and_grad(float& s, float& dp, bool visible, bool alone, float lse, float delta) {
   const float w = visible ? expf(s - lse) : 0.f;
-  dp = visible ? w * (dp - delta) : 0.f;
+  dp = visible && !alone ? w * (dp - delta) : 0.f;
   s = w;
 }
 
@@ -271,7 +272,7 @@ xattn_dq_simt_kernel(const __grid_constant__ Args a, int tiles) {
         const int key = j * TQ + tx + 16 * c;
         s[i][c] *= a.scale;
         if (a.bias.buckets) s[i][c] += a.bias.clamped(h, key - p);
-        weight_and_grad(s[i][c], dp[i][c], key < vis, lse[r], delta[r]);
+        weight_and_grad(s[i][c], dp[i][c], key < vis, vis == 1, lse[r], delta[r]);
         Ds[r * PITCH_P + tx + 16 * c] = dp[i][c];
       }
     }
@@ -355,7 +356,7 @@ xattn_dkv_simt_kernel(const __grid_constant__ Args a, int tiles) {
           s[r][c] *= a.scale;
           if (a.bias.buckets) s[r][c] += a.bias.clamped(h, key - p);
           const bool visible = key < len && qi < a.Sq && (!a.causal || key <= p);
-          weight_and_grad(s[r][c], dp[r][c], visible, lse[x], delta[x]);
+          weight_and_grad(s[r][c], dp[r][c], visible, len == 1 || (a.causal && p == 0), lse[x], delta[x]);
           Ps[(4 * ty + r) * PITCH_P + x] = s[r][c];
           Ds[(4 * ty + r) * PITCH_P + x] = dp[r][c];
         }

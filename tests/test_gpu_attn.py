@@ -334,6 +334,68 @@ def test_captured_replayed_and_on_another_stream():
                 assert x is y is None or torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Sq,Sk,causal", [(1, 1, False), (150, 1, False), (200, 200, True), (3, 400, False)])
+def test_a_single_key_gives_no_gradient(dtype, Sq, Sk, causal):
+    """Of weight 1 whatever its score: dq, dk and dbias are 0, not what roundings leave."""
+    lens = [Sk, 1]
+    c, o, lse, (dq, dk, dv, db) = run(dtype, 2, Sq, Sk, 4, 2, 64, lens=lens, causal=causal, buckets=16)
+    assert not dq[1].any() and not dk[1].any()
+    assert torch.equal(o[1, :, 2], c.v[1, :1, 1].expand(Sq, -1))
+    if causal:
+        assert not dq[0, 0].any()
+    if Sk == 1:
+        assert not dq.any() and not dk.any() and not db.any()
+
+
+@pytest.mark.parametrize("Sq,Sk", [(300, 3), (130, 40), (257, 128), (400, 400)])
+def test_delta_is_that_of_the_weights(Sq, Sk):
+    """Rows of few keys, where delta of the rounded o would show: what remains is the
+    rounding of dS and of dq, at most half a step of bf16 each, so that the norm of the
+    error is at most 2 u |dq| and, the roundings' signs being random, near 1.4 u / sqrt(3);
+    dbias has its own rounding alone."""
+    c = Case("bf16", 2, Sq, Sk, 2, 2, 64, buckets=32, causal=Sq == Sk)
+    o, lse = c.forward()
+    dq, dk, dv, db = c.backward(o, lse)
+    wide = {n: getattr(c, n).double().requires_grad_(True) for n in ("q", "k", "v", "bias")}
+    s = torch.einsum("bihd,bjhd->bhij", wide["q"], wide["k"]) * c.scale
+    at = torch.tensor(bucket_map(Sq, Sk, 0, 32, 128, c.both), device="cuda")
+    s = s + wide["bias"][at].permute(2, 0, 1)
+    if c.causal:
+        see = torch.tensor(visible_keys(Sq, Sk, Sk, 0, True), device="cuda")
+        s = s.masked_fill(~see, float("-inf"))
+    want = torch.autograd.grad(torch.einsum("bhij,bjhd->bihd", torch.softmax(s, -1), wide["v"]),
+                               [wide["q"], wide["k"], wide["bias"]], c.do.double())
+    u = 2.0 ** -8
+    for got, w, most in ((dq, want[0], 2 * u), (dk, want[1], 2 * u), (db, want[2], u)):
+        assert (got.double() - w).norm() <= most * w.norm() * 1.05
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Sq", [1, 140])
+def test_a_nan_shows(dtype, Sq):
+    """A query of NaN has a NaN for an output, beside others that have none."""
+    c = Case(dtype, 1, Sq, 200, 2, 1, 64)
+    c.q[0, Sq // 2, 1] = float("nan")
+    o, lse = c.forward()
+    bad = torch.zeros(1, Sq, 2, dtype=torch.bool, device="cuda")
+    bad[0, Sq // 2, 1] = True
+    assert torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
+    assert torch.equal(lse.isnan(), bad.transpose(1, 2))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [-1e30, -1e9, -3e7])
+def test_scores_beyond_what_weights_resolve_give_no_gradient(dtype, value):
+    """A bias that hides every key by a finite value: no gradient, and none of it infinite."""
+    c = Case(dtype, 1, 150, 150, 2, 2, 64, buckets=32)
+    c.bias[:, 1] = value
+    o, lse = c.forward()
+    dq, dk, dv, db = c.backward(o, lse)
+    assert all(torch.isfinite(x).all() for x in (o, lse, dq, dk, dv, db))
+    assert not dq[:, :, 1].any() and not dk[:, :, 1].any() and not db[:, 1].any()
+
+
 # few items over long keys or many queries, whose backward cuts them into pieces
 CUT = [(1, 70, 2100, 2, 1, 64), (2, 1300, 70, 4, 2, 64), (1, 70, 1500, 1, 1, 128),
        (1, 1300, 150, 2, 1, 128), (3, 900, 1200, 4, 4, 40)]
