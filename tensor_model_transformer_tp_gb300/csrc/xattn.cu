@@ -266,7 +266,7 @@ Layout layout(const Shape& s, bool backward) {
     else if (a.t == DType::BF16)
       l.splits = shares((int64_t)a.B * a.H * ((a.Sq + 255) / 256), sms, (a.Sk + 127) / 128, 4);
     else
-      l.splits = shares((int64_t)a.B * a.H * ((a.Sq + 63) / 64), 2 * sms, (a.Sk + 63) / 64, 4);
+      l.splits = xattn_f32_cut(a).q_shares;
     if (l.splits > 1) {
       take(&l.part_o, (size_t)l.splits * a.B * a.Sq * a.H * a.D * 4);
       take(&l.part_lse, (size_t)l.splits * a.B * a.Sq * a.H * 4);
@@ -274,9 +274,13 @@ Layout layout(const Shape& s, bool backward) {
   } else {
     take(&l.delta, (size_t)a.B * a.H * a.q_pitch * 4);
     if (a.t == DType::BF16) take(&l.neg_lse2, (size_t)a.B * a.H * a.q_pitch * 4);
-    l.rows = (int64_t)a.B * ((a.Sq + 63) / 64);
     BwdCut cut;
-    if (a.t == DType::BF16 && xattn_bwd_cut(a, &cut)) {  // (else the call itself refuses)
+    if (a.t == DType::F32) {
+      const F32Cut c = xattn_f32_cut(a);
+      if (c.q_shares > 1) take(&l.piece_dq, (size_t)c.q_shares * a.B * a.Sq * a.H * a.D * 4);
+      if (c.kv_shares > 1) take(&l.piece_dkv, (size_t)c.kv_shares * 2 * a.B * a.Sk * a.G * a.D * 4);
+      l.rows = (int64_t)a.B * ((a.Sq + c.q_rows - 1) / c.q_rows) * c.q_shares;
+    } else if ( xattn_bwd_cut(a, &cut)) {  // (else the call itself refuses)
       if (cut.dq.pieces > 1) take(&l.piece_dq, (size_t)cut.dq.rest * cut.dq.pieces * xattn_dq_piece_bytes(a.D));
       if (cut.dkv.pieces > 1) take(&l.piece_dkv, (size_t)cut.dkv.rest * cut.dkv.pieces * 2 * 128 * a.D * 4);
       const int64_t tiles = (int64_t)a.B * ((a.Sk + 127) / 128);  // as kv_item() counts them

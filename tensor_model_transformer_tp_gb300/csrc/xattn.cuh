@@ -74,7 +74,7 @@ struct Args {
   Bias bias;
   float* bias_part;  // partial gradients of the bias [heads][bias_rows][buckets], null: not wanted
   int64_t bias_rows;
-  float *piece_dq, *piece_dkv;  // sums of pieces of items (bf16 backward), workspace
+  float *piece_dq, *piece_dkv;  // sums of pieces of items or shares (backward), workspace
   int splits;        // forward: shares of the keys, joined by join_splits()
   float* part_o;     // [splits][batch][q_len][heads][D], normalised
   float* part_lse;   // [splits][batch][heads][q_len]
@@ -98,6 +98,10 @@ struct Pieces {
 struct BwdCut {
   Pieces dq, dkv;
 };
+// fp32: rows of a tile, and the shares of the other side's blocks of the backward.
+struct F32Cut {
+  int q_rows, kv_rows, q_shares, kv_shares;
+};
 
 }  // namespace xattn
 
@@ -112,6 +116,7 @@ size_t xattn_dq_piece_bytes(int D);
 bool xattn_bwd_cut(const xattn::Args& a, xattn::BwdCut* cut);  // false: too many items
 cudaError_t xattn_bwd_tc(const xattn::Args& a, cudaStream_t st);
 // fp32 (CUDA cores)
+xattn::F32Cut xattn_f32_cut(const xattn::Args& a);
 cudaError_t xattn_fwd_f32(const xattn::Args& a, cudaStream_t st);
 cudaError_t xattn_bwd_f32(const xattn::Args& a, cudaStream_t st);
 

@@ -432,3 +432,12 @@ def test_few_queries_over_long_keys():
             c = Case(dtype, 2, Sq, 4100, H, G, 128, lens=[4099, 1290])
             o, lse = c.forward()
             c.check(o, lse, c.backward(o, lse))
+
+
+@pytest.mark.parametrize("shape", [(1, 700, 60, 2, 1, 64), (1, 40, 900, 1, 1, 40), (2, 600, 300, 2, 1, 128),
+                                   (1, 1500, 1500, 16, 16, 32)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_shares_of_fp32(shape, biased):
+    """Few tiles over many blocks, and tiles of 64 rows (the last)."""
+    run("f32", *shape, lens=[shape[2] - 5 * b for b in range(shape[0])], buckets=48 if biased else 0,
+        causal=shape[1] == shape[2])
