@@ -10,8 +10,12 @@
 // per value, y_i = r (x_i A_i + x_partner B_i), and the unit's rows are in flight
 // together.  The partner of value i in the rotation sits
 //   PAIRS   beside it in the lane (interleaved),
-//   LANES   rot / 2 values on, in another lane: the raw words are shuffled,
-//   LOADS   at an offset that is no multiple of 8: loaded again, one by one.
+//   HALVES  rot / 2 values on (rot a multiple of 8): a lane of the rotated part holds four
+//           values of its first half and their four partners,
+//   LOADS   rot / 2 values on, otherwise: loaded again, one by one.
+// Arithmetic goes two values at a time.  (Before, with the partners' words shuffled from
+// other lanes, values one by one and IEEE roots and quotients, issuing bound the kernels:
+// TODO)
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -26,7 +30,7 @@ oases_status api_end(cudaError_t e);
 
 namespace {
 
-enum class Partner { NONE, PAIRS, LANES, LOADS };
+enum class Partner { NONE, PAIRS, HALVES, LOADS };
 constexpr int WARPS = 8;
 constexpr int BWD_CTAS_PER_SM = 2;
 
@@ -64,6 +68,11 @@ template <>
 struct Raw<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  // four values each
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(q);
+    v = make_uint4(x.x, x.y, y.x, y.y);
+  }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -73,12 +82,6 @@ struct Raw<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  __device__ __forceinline__ Raw shuffled(int src, int width) const {
-    Raw r;
-    r.v = make_uint4(__shfl_sync(~0u, v.x, src, width), __shfl_sync(~0u, v.y, src, width),
-                     __shfl_sync(~0u, v.z, src, width), __shfl_sync(~0u, v.w, src, width));
-    return r;
-  }
 };
 template <>
 struct Raw<float> {
@@ -87,59 +90,82 @@ struct Raw<float> {
     a = *reinterpret_cast<const float4*>(p);
     b = *reinterpret_cast<const float4*>(p + 4);
   }
+  __device__ __forceinline__ void load(const float* p, const float* q) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(q);
+  }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
-  __device__ __forceinline__ Raw shuffled(int src, int width) const {
-    Raw r;
-    r.a = make_float4(__shfl_sync(~0u, a.x, src, width), __shfl_sync(~0u, a.y, src, width),
-                      __shfl_sync(~0u, a.z, src, width), __shfl_sync(~0u, a.w, src, width));
-    r.b = make_float4(__shfl_sync(~0u, b.x, src, width), __shfl_sync(~0u, b.y, src, width),
-                      __shfl_sync(~0u, b.z, src, width), __shfl_sync(~0u, b.w, src, width));
-    return r;
-  }
 };
-// 8 values in fp32
-template <typename T>
-__device__ __forceinline__ void get8(const T* p, float (&f)[8]) {
-  Raw<T> r;
-  r.load(p);
-  r.get(f);
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
 }
-__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
+__device__ __forceinline__ void put8(__nv_bfloat16* p, __nv_bfloat16* q, const float (&f)[8]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
+  *reinterpret_cast<uint2*>(q) = make_uint2(bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+}
+__device__ __forceinline__ void put8(float* p, float* q, const float (&f)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+  *reinterpret_cast<float4*>(q) = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void put8(float* p, const float (&f)[8]) { put8(p, p + 4, f); }
+
+// 1 / sqrt(x) of x > 0: the hardware's, and one step of Newton's on it (e = (1 - x r^2) / 2).
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x), e = fmaf(-0.5f * x * r, r, 0.5f);
+  return r == 0.f ? r : fmaf(r, e, r);  // (x infinite: 0)
+}
+__device__ __forceinline__ uint64_t pair(const float (&f)[8], int e) { return f2_pack(f[e], f[e + 1]); }
+__device__ __forceinline__ void set_pair(float (&f)[8], int e, uint64_t v) { f[e] = f2_lo(v), f[e + 1] = f2_hi(v); }
+__device__ __forceinline__ float dot8(const float (&f)[8], const float (&g)[8]) {
+  uint64_t s = f2_mul(pair(f, 0), pair(g, 0));
+#pragma unroll
+  for (int e = 2; e < 8; e += 2) s = f2_fma(pair(f, e), pair(g, e), s);
+  return f2_lo(s) + f2_hi(s);
 }
 
-// A lane's place: its 8 values of a head, and where their partners are.
+// A lane's place: its 8 values of a head, from i0 and from i1 on.
 template <Partner P>
 struct Place {
-  int i0;        // first value
-  bool active;
-  int lane;      // LANES: the partner's lane within the head's
+  int i0, i1;
+  bool active, turned;  // turned: in two halves (HALVES: of the rotated part; NONE: of the head)
   __device__ __forceinline__ Place(const QkArgs& a) {
     const int c = threadIdx.x % a.L;
-    i0 = 8 * c;
-    active = i0 < a.D;
-    const int half = a.rot / 2;
-    lane = P != Partner::LANES || i0 >= a.rot ? c : i0 < half ? c + half / 8 : c - half / 8;
+    active = 8 * c < a.D;
+    const int part = P == Partner::HALVES ? a.rot : P == Partner::NONE ? a.D : 0;
+    turned = 8 * c < part;
+    i0 = turned ? 4 * c : 8 * c;
+    i1 = i0 + (turned ? part / 2 : 4);
   }
-  // partner of value i0 + e
+  __device__ __forceinline__ int index(int e) const { return e < 4 ? i0 + e : i1 + e - 4; }
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, Raw<T>& r) const {
+    if (P == Partner::HALVES || P == Partner::NONE) r.load(row + i0, row + i1);
+    else r.load(row + i0);
+  }
+  template <typename T>
+  __device__ __forceinline__ void get(const T* row, float (&f)[8]) const {
+    Raw<T> r;
+    load(row, r);
+    r.get(f);
+  }
+  template <typename T>
+  __device__ __forceinline__ void put(T* row, const float (&f)[8]) const {
+    if (P == Partner::HALVES || P == Partner::NONE) put8(row + i0, row + i1, f);
+    else put8(row + i0, f);
+  }
+  // LOADS: the partner of value e
   __device__ __forceinline__ int partner(const QkArgs& a, int e) const {
     const int i = i0 + e;
     if (i >= a.rot) return i;
-    if (P == Partner::PAIRS) return i ^ 1;
     return i < a.rot / 2 ? i + a.rot / 2 : i - a.rot / 2;
   }
   // cos and signed sin of the lane's values: y_i = x_i c_i + x_partner s_i
@@ -156,20 +182,22 @@ struct Place {
     const int half = a.rot / 2;
     const float* ct = a.cos + (good ? p : 0) * half;
     const float* st = a.sin + (good ? p : 0) * half;
-    if (P == Partner::LANES && i0 < a.rot) {  // rot % 16 == 0: a lane is on one side, 16 bytes aligned
-      const bool first = i0 < half;
-      const int at = first ? i0 : i0 - half;
-      if (a.tables16) {
-        get8(ct + at, c);
-        get8(st + at, s);
-      } else {
+    if (P == Partner::HALVES) {
+      float u[4] = {1.f, 1.f, 1.f, 1.f}, v[4] = {};
+      if (turned) {
+        if (a.tables16) {
+          *reinterpret_cast<float4*>(u) = *reinterpret_cast<const float4*>(ct + i0);
+          *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(st + i0);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = ct[at + e], s[e] = st[at + e];
+          for (int e = 0; e < 4; ++e) u[e] = ct[i0 + e], v[e] = st[i0 + e];
+        }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e] = good ? c[e] : NAN;
-        s[e] = !good ? NAN : first ? -s[e] : s[e];
+      for (int e = 0; e < 4; ++e) {
+        if (turned && !good) u[e] = v[e] = NAN;
+        c[e] = c[e + 4] = u[e];
+        s[e] = -v[e], s[e + 4] = v[e];
       }
       return;
     }
@@ -189,30 +217,23 @@ struct Place {
   template <typename T>
   __device__ __forceinline__ void partner_weights(const QkArgs& a, const T* w, const float (&own)[8],
                                                   float (&o)[8]) const {
-    if (P == Partner::LANES) {
-      get8(w + 8 * lane, o);
-    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[e] = P == Partner::PAIRS ? own[e ^ 1] : P == Partner::LOADS ? ld_elem(w, partner(a, e)) : 0.f;
-    }
+    for (int e = 0; e < 8; ++e)
+      o[e] = P == Partner::PAIRS    ? own[e ^ 1]
+             : P == Partner::HALVES ? own[e ^ 4]
+             : P == Partner::LOADS  ? ld_elem(w, partner(a, e))
+                                    : 0.f;
   }
-  // the partners' values of a row whose own values are `raw`
+  // the partners' values of a row whose own values are x
   template <typename T>
-  __device__ __forceinline__ void partners(const QkArgs& a, const Raw<T>& raw, const float (&x)[8],
-                                           const T* row, bool valid, float (&o)[8]) const {
-    if (P == Partner::PAIRS) {
+  __device__ __forceinline__ void partners(const QkArgs& a, const float (&x)[8], const T* row, bool valid,
+                                           float (&o)[8]) const {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
-    } else if (P == Partner::LANES) {
-      raw.shuffled(lane, a.L).get(o);
-    } else if (P == Partner::LOADS) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = valid && i0 + e < a.rot ? ld_elem(row, partner(a, e)) : 0.f;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = 0.f;
-    }
+    for (int e = 0; e < 8; ++e)
+      o[e] = P == Partner::PAIRS    ? x[e ^ 1]
+             : P == Partner::HALVES ? x[e ^ 4]
+             : P == Partner::LOADS  ? (valid && i0 + e < a.rot ? ld_elem(row, partner(a, e)) : 0.f)
+                                    : 0.f;
   }
 };
 
@@ -263,7 +284,7 @@ qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
     for (int k = 0; k < ROWS; ++k) {
       const int h = un.h0 + (batch * ROWS + k) * groups + sub;
       raw[k].zero();
-      if (pl.active && h < t.heads) raw[k].load(x + h * t.xh + pl.i0);
+      if (pl.active && h < t.heads) pl.load(x + h * t.xh, raw[k]);
     }
   };
   load(0);
@@ -271,7 +292,7 @@ qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
   if (t.w != nullptr && pl.active) {
     const T* w = static_cast<const T*>(t.w);
     float own[8], other[8];
-    get8(w + pl.i0, own);
+    pl.get(w, own);
     pl.template partner_weights<T>(a, w, own, other);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -284,19 +305,22 @@ qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       const int h = un.h0 + (batch * ROWS + k) * groups + sub;
+      if (h - sub >= t.heads) break;  // (uniform: none of the warp's)
       const bool valid = pl.active && h < t.heads;
       float v[8], o[8];
       raw[k].get(v);
-      pl.partners(a, raw[k], v, x + h * t.xh, valid, o);
-      float ss = 0.f;
+      pl.partners(a, v, x + h * t.xh, valid, o);
+      const float r = inverse_root(fmaf(lanes_sum(dot8(v, v), a.L), over_d, a.eps));
+      const uint64_t r2 = f2_splat(r);
+      float y8[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-      const float r = 1.f / sqrtf(fmaf(lanes_sum(ss, a.L), over_d, a.eps));
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = r * (P == Partner::NONE ? v[e] * A[e] : fmaf(o[e], B[e], v[e] * A[e]));
+      for (int e = 0; e < 8; e += 2) {
+        uint64_t z = f2_mul(pair(v, e), pair(A, e));
+        if (P != Partner::NONE) z = f2_fma(pair(o, e), pair(B, e), z);
+        set_pair(y8, e, f2_mul(z, r2));
+      }
       __syncwarp();  // y may be x: a row's partners have been read
-      if (valid) put8(y + h * t.yh + pl.i0, v);
+      if (valid) pl.put(y + h * t.yh, y8);
     }
   }
 }
@@ -332,15 +356,15 @@ qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
         rx[k].zero();
         rg[k].zero();
         if (pl.active && h < t.heads) {
-          rx[k].load(x + h * t.xh + pl.i0);
-          rg[k].load(dy + h * t.yh + pl.i0);
+          pl.load(x + h * t.xh, rx[k]);
+          pl.load(dy + h * t.yh, rg[k]);
         }
       }
     };
     load(0);
     pl.angles(a, token, c, s);
     if (t.w != nullptr && pl.active) {
-      get8(static_cast<const T*>(t.w) + pl.i0, w);
+      pl.get(static_cast<const T*>(t.w), w);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = 1.f;
@@ -351,34 +375,34 @@ qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
 #pragma unroll
       for (int k = 0; k < ROWS; ++k) {
         const int h = h0 + (batch * ROWS + k) * groups + sub;
+        if (h - sub >= t.heads) break;  // (uniform: none of the warp's)
         const bool valid = pl.active && h < t.heads;
-        float xv[8], gv[8], o[8];
+        float xv[8], gv[8], o[8], gw[8];
         rx[k].get(xv);
         rg[k].get(gv);
-        pl.partners(a, rg[k], gv, dy + h * t.yh, valid, o);
-        float ss = 0.f, sg = 0.f, gw[8];
+        pl.partners(a, gv, dy + h * t.yh, valid, o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (P != Partner::NONE) gv[e] = fmaf(-s[e], o[e], gv[e] * c[e]);  // R^T dy
-          gw[e] = gv[e] * w[e];
-          ss = fmaf(xv[e], xv[e], ss);
-          sg = fmaf(gw[e], xv[e], sg);
+        for (int e = 0; e < 8; e += 2) {
+          if (P != Partner::NONE)  // R^T dy
+            set_pair(gv, e, f2_fma(pair(o, e), f2_pack(-s[e], -s[e + 1]), f2_mul(pair(gv, e), pair(c, e))));
+          set_pair(gw, e, f2_mul(pair(gv, e), pair(w, e)));
         }
+        float ss = dot8(xv, xv), sg = dot8(gw, xv);
 #pragma unroll 1
         for (int o2 = a.L / 2; o2; o2 >>= 1) {
           ss += __shfl_xor_sync(~0u, ss, o2);
           sg += __shfl_xor_sync(~0u, sg, o2);
         }
-        const float r = 1.f / sqrtf(fmaf(ss, over_d, a.eps));
-        const float m = sg * over_d * r * r;
-        if (valid) {
+        const float r = inverse_root(fmaf(ss, over_d, a.eps));
+        const uint64_t r2 = f2_splat(r), m2 = f2_splat(-(sg * over_d * r * r));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dw[e] = fmaf(gv[e], xv[e] * r, dw[e]);
+        for (int e = 0; e < 8; e += 2) {
+          const uint64_t d = f2_fma(pair(gv, e), f2_mul(pair(xv, e), r2), pair(dw, e));
+          if (valid) set_pair(dw, e, d);
+          set_pair(gw, e, f2_mul(f2_fma(pair(xv, e), m2, pair(gw, e)), r2));
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) gw[e] = r * fmaf(-xv[e], m, gw[e]);
         __syncwarp();  // dx may be dy: a row's partners have been read
-        if (valid && dx != nullptr) put8(dx + h * t.oh + pl.i0, gw);
+        if (valid && dx != nullptr) pl.put(dx + h * t.oh, gw);
       }
     }
   }
@@ -387,7 +411,7 @@ qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     for (int o = a.L; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(~0u, dw[e], o);
-    if (lane < a.L && pl.active) red[warp][pl.i0 + e] = dw[e];
+    if (lane < a.L && pl.active) red[warp][pl.index(e)] = dw[e];
   }
   __syncthreads();
   for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
@@ -457,7 +481,7 @@ oases_status qk_check(const oases_qknorm_desc* d, bool backward) {
 Partner partner_of(const oases_qknorm_desc* d) {
   if (d->rot == 0) return Partner::NONE;
   if (d->interleaved) return Partner::PAIRS;
-  return d->rot % 16 == 0 ? Partner::LANES : Partner::LOADS;
+  return d->rot % 8 == 0 ? Partner::HALVES : Partner::LOADS;
 }
 
 // The parts of the launch that follow from the descriptor.
@@ -516,12 +540,12 @@ cudaError_t launch(Partner p, const QkArgs& a, int blocks, cudaStream_t st) {
   if (BWD)
     kern = p == Partner::NONE    ? qknorm_bwd_kernel<T, Partner::NONE>
            : p == Partner::PAIRS ? qknorm_bwd_kernel<T, Partner::PAIRS>
-           : p == Partner::LANES ? qknorm_bwd_kernel<T, Partner::LANES>
+           : p == Partner::HALVES ? qknorm_bwd_kernel<T, Partner::HALVES>
                                  : qknorm_bwd_kernel<T, Partner::LOADS>;
   else
     kern = p == Partner::NONE    ? qknorm_fwd_kernel<T, Partner::NONE>
            : p == Partner::PAIRS ? qknorm_fwd_kernel<T, Partner::PAIRS>
-           : p == Partner::LANES ? qknorm_fwd_kernel<T, Partner::LANES>
+           : p == Partner::HALVES ? qknorm_fwd_kernel<T, Partner::HALVES>
                                  : qknorm_fwd_kernel<T, Partner::LOADS>;
   return launch_pdl(kern, dim3(blocks), dim3(32 * WARPS), 0, st, a);
 }

@@ -9,8 +9,11 @@
 // CTAs shares the keys that the sequence has (so that ragged batches stay even) and
 // joins its groups' results through distributed shared memory; only where sequences and
 // key heads are too few for the GPU are the keys split further, through memory.
-// The position bias: R or more away one value on each side, kept in a register; nearer,
-// the bucket is searched for and the table read (no table by distance is made).
+// Ragged sequences are taken longest first, rounds of the SMs in snake order, so that the
+// CTAs that share an SM have about the same keys together (16 sequences of up to 1500 keys,
+// 20 heads of 64: 15 -> TODO us with the keys in L2, 24 -> TODO from memory).
+// The position bias: R or more away one value on each side, kept in a register; nearer, by
+// distance from shared memory where R is at most NEAR, else searched for.
 #include <math.h>
 
 #include <algorithm>
@@ -24,6 +27,7 @@ using namespace xattn;
 
 constexpr int WARPS = 8, NT = 32 * WARPS;
 constexpr int MAX_CLUSTER = 8;
+constexpr int NEAR = 256;  // distances on each side in shared memory
 
 template <typename T>
 constexpr int EPL = 16 / (int)sizeof(T);  // values of a lane
@@ -58,16 +62,34 @@ struct Table {
 
 // LPK lanes a key, R rows (query i, query head hh of the group: row i share + hh).
 template <typename T, int LPK, int R>
-__global__ void __launch_bounds__(NT)
-xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table table, int rows) {
+__global__ void __launch_bounds__(NT, R == 1 ? 3 : 2)
+xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table table, int rows, int sms) {
   constexpr int E = EPL<T>, GROUPS = 32 / LPK, KU = R == 1 ? 4 : 2, D_MAX = LPK * E;
   __shared__ float red_o[WARPS][R][D_MAX], red_m[WARPS][R], red_l[WARPS][R];
   __shared__ float out_o[R][D_MAX], out_m[R], out_l[R];
+  __shared__ float near[R][2 * NEAR + 1];
+  __shared__ int lens[NT], order[NT];
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % LPK, grp = lane / LPK;
   const int csize = gridDim.x / a.splits, rank = blockIdx.x % csize, sp = blockIdx.x / csize;
-  const int g = blockIdx.y % a.G, b = blockIdx.y / a.G;
+  int y = blockIdx.y;
+  if (a.kv_lens && a.B > 1 && a.B <= NT) {
+    // place y of the rounds' snake order, in the sequences by falling length
+    const int round = y / sms, at = y % sms, n = min(sms, (int)gridDim.y - round * sms);
+    if (round & 1) y = round * sms + n - 1 - at;
+    const int t = threadIdx.x;
+    if (t < a.B) lens[t] = a.len(t);
+    __syncthreads();
+    if (t < a.B) {
+      int rank = 0;
+      for (int x = 0; x < a.B; ++x) rank += lens[x] > lens[t] || (lens[x] == lens[t] && x < t);
+      order[rank] = t;
+    }
+    __syncthreads();
+    y = order[y / a.G] * a.G + y % a.G;
+  }
+  const int g = y % a.G, b = y / a.G;
   const int len = a.len(b), p0 = a.start(b);
   const int seen = a.causal ? min(len, max(0, p0 + a.Sq)) : len;
   // this CTA's keys: an even share, in whole steps of a CTA's groups
@@ -120,6 +142,13 @@ xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table t
   };
   const int k_first = k_begin + warp * GROUPS * KU + grp;
   load(k_first);
+  const bool by_distance = a.bias.buckets && a.bias.R <= NEAR;
+  if (by_distance) {
+    const int n = 2 * a.bias.R + 1;
+    for (int x = threadIdx.x; x < rows * n; x += NT)
+      near[x / n][x % n] = table.at<T>(a.H, g * a.share + x / n % a.share, x % n - a.bias.R);
+    __syncthreads();
+  }
   for (int k0 = k_first; k0 - grp < k_end; k0 += STEP) {
     uint4 kv[KU], vv[KU];
 #pragma unroll
@@ -153,7 +182,10 @@ xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table t
         const int key = k0 + u * GROUPS;
         if (a.bias.buckets && r < rows) {
           const int n = key - pos[r];
-          s[r][u] += n <= -a.bias.R ? left[r] : n >= a.bias.R ? right[r] : table.at<T>(a.H, h, n);
+          s[r][u] += n <= -a.bias.R   ? left[r]
+                     : n >= a.bias.R ? right[r]
+                     : by_distance   ? near[r][n + a.bias.R]
+                                     : table.at<T>(a.H, h, n);
         }
         if (key >= k_end || key >= vis[r]) s[r][u] = -INFINITY;
         mx = fmaxf(mx, s[r][u]);
@@ -268,7 +300,7 @@ cudaError_t launch(const Args& a, const Table& tb, int rows, int csize, cudaStre
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   ++g_launch_count;
-  return cudaLaunchKernelEx(&cfg, xattn_few_kernel<T, LPK, R>, a, tb, rows);
+  return cudaLaunchKernelEx(&cfg, xattn_few_kernel<T, LPK, R>, a, tb, rows, sm_count());
 }
 template <typename T, int LPK>
 cudaError_t launch_rows(const Args& a, const Table& tb, int rows, int csize, cudaStream_t st) {
