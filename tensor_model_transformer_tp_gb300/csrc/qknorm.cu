@@ -13,9 +13,10 @@
 //   HALVES  rot / 2 values on (rot a multiple of 8): a lane of the rotated part holds four
 //           values of its first half and their four partners,
 //   LOADS   rot / 2 values on, otherwise: loaded again, one by one.
-// Arithmetic goes two values at a time.  (Before, with the partners' words shuffled from
-// other lanes, values one by one and IEEE roots and quotients, issuing bound the kernels:
-// TODO)
+// Arithmetic goes two values at a time.  8192 tokens of 20 + 20 heads of 128, forward and
+// backward (420 MB): 98 us; with the partners' words shuffled from other lanes, values one
+// by one and IEEE roots and quotients, which issuing bound, 121.  (Persistent warps with
+// the loads ahead in shared memory read as much at once with fewer warps, and took 98.)
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -182,7 +183,7 @@ struct Place {
     const int half = a.rot / 2;
     const float* ct = a.cos + (good ? p : 0) * half;
     const float* st = a.sin + (good ? p : 0) * half;
-    if (P == Partner::HALVES) {
+    if constexpr (P == Partner::HALVES) {
       float u[4] = {1.f, 1.f, 1.f, 1.f}, v[4] = {};
       if (turned) {
         if (a.tables16) {
@@ -199,18 +200,18 @@ struct Place {
         c[e] = c[e + 4] = u[e];
         s[e] = -v[e], s[e + 4] = v[e];
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = i0 + e;
-      c[e] = 1.f, s[e] = 0.f;
-      if (i < a.rot) {
-        const int at = P == Partner::PAIRS ? i / 2 : i < half ? i : i - half;
-        const bool first = P == Partner::PAIRS ? (i & 1) == 0 : i < half;
-        c[e] = good ? ct[at] : NAN;
-        const float v = good ? st[at] : NAN;
-        s[e] = first ? -v : v;
+      for (int e = 0; e < 8; ++e) {
+        const int i = i0 + e;
+        c[e] = 1.f, s[e] = 0.f;
+        if (i < a.rot) {
+          const int at = P == Partner::PAIRS ? i / 2 : i < half ? i : i - half;
+          const bool first = P == Partner::PAIRS ? (i & 1) == 0 : i < half;
+          c[e] = good ? ct[at] : NAN;
+          const float v = good ? st[at] : NAN;
+          s[e] = first ? -v : v;
+        }
       }
     }
   }
@@ -237,9 +238,15 @@ struct Place {
   }
 };
 
-__device__ __forceinline__ float lanes_sum(float v, int L) {
-  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
+// Sums over the L lanes of a head (a power of two): every step a predicate, no loop.
+template <int N>
+__device__ __forceinline__ void lanes_sum(int L, float (&v)[N]) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    if (L > o) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(~0u, v[i], o);
+    }
 }
 
 // Unit u: which token, tensor and first head.
@@ -259,7 +266,10 @@ __device__ __forceinline__ Unit unit_of(const QkArgs& a, int64_t u, int heads_pe
 }
 
 // rows of one lane in flight: what the registers hold
-constexpr int rows_in_flight(bool bwd, bool f32, Partner p) { return p == Partner::LOADS || (bwd && f32) ? 2 : 4; }
+// (20 heads of 128 are two batches of 5 rows; three of 4 took 104 us, forward and backward)
+constexpr int rows_in_flight(bool bwd, bool f32, Partner p) {
+  return p == Partner::LOADS || (bwd && f32) ? 2 : f32 ? 4 : 5;
+}
 
 template <typename T, Partner P>
 __global__ void __launch_bounds__(32 * WARPS, 3)
@@ -274,17 +284,21 @@ qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
   const Tensor& t = a.t[un.which];
   const Place<P> pl(a);
   const int64_t b = un.token / a.seq, tk = un.token - b * a.seq;
-  const T* x = static_cast<const T*>(t.x) + b * t.xb + tk * t.xs;
-  T* y = static_cast<T*>(t.out) + b * t.yb + tk * t.ys;
+  // the lane's first row, and from one to the next
+  const T* x = static_cast<const T*>(t.x) + b * t.xb + tk * t.xs + (un.h0 + sub) * t.xh;
+  T* y = static_cast<T*>(t.out) + b * t.yb + tk * t.ys + (un.h0 + sub) * t.yh;
+  const int64_t x_step = groups * t.xh, y_step = groups * t.yh;
   const float over_d = 1.f / (float)a.D;
   float A[8], B[8];  // the factors of a value and of its partner
   Raw<T> raw[ROWS];
+  const T* next = x;  // the next row to load
   auto load = [&](int batch) {
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       const int h = un.h0 + (batch * ROWS + k) * groups + sub;
       raw[k].zero();
-      if (pl.active && h < t.heads) pl.load(x + h * t.xh, raw[k]);
+      if (pl.active && h < t.heads) pl.load(next, raw[k]);
+      next += x_step;
     }
   };
   load(0);
@@ -309,9 +323,10 @@ qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
       const bool valid = pl.active && h < t.heads;
       float v[8], o[8];
       raw[k].get(v);
-      pl.partners(a, v, x + h * t.xh, valid, o);
-      const float r = inverse_root(fmaf(lanes_sum(dot8(v, v), a.L), over_d, a.eps));
-      const uint64_t r2 = f2_splat(r);
+      pl.partners(a, v, x, valid, o);
+      float ss[1] = {dot8(v, v)};
+      lanes_sum(a.L, ss);
+      const uint64_t r2 = f2_splat(inverse_root(fmaf(ss[0], over_d, a.eps)));
       float y8[8];
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
@@ -320,7 +335,9 @@ qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
         set_pair(y8, e, f2_mul(z, r2));
       }
       __syncwarp();  // y may be x: a row's partners have been read
-      if (valid) pl.put(y + h * t.yh, y8);
+      if (valid) pl.put(y, y8);
+      x += x_step;
+      y += y_step;
     }
   }
 }
@@ -345,8 +362,9 @@ qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
     const int64_t token = u / a.units[which];
     const int h0 = (int)(u - token * a.units[which]) * ROWS * groups * a.batches;
     const int64_t b = token / a.seq, tk = token - b * a.seq;
-    const T* x = static_cast<const T*>(t.x) + b * t.xb + tk * t.xs;
-    const T* dy = static_cast<const T*>(t.dy) + b * t.yb + tk * t.ys;
+    const T* x = static_cast<const T*>(t.x) + b * t.xb + tk * t.xs + (h0 + sub) * t.xh;  // next to load
+    const T* dy = static_cast<const T*>(t.dy) + b * t.yb + tk * t.ys + (h0 + sub) * t.yh;
+    const T* dy_row = dy;  // in work
     float c[8], s[8], w[8];
     Raw<T> rx[ROWS], rg[ROWS];
     auto load = [&](int batch) {
@@ -356,9 +374,11 @@ qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
         rx[k].zero();
         rg[k].zero();
         if (pl.active && h < t.heads) {
-          pl.load(x + h * t.xh, rx[k]);
-          pl.load(dy + h * t.yh, rg[k]);
+          pl.load(x, rx[k]);
+          pl.load(dy, rg[k]);
         }
+        x += groups * t.xh;
+        dy += groups * t.yh;
       }
     };
     load(0);
@@ -369,7 +389,10 @@ qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = 1.f;
     }
-    T* dx = t.out ? static_cast<T*>(t.out) + b * t.ob + tk * t.os : nullptr;
+    T* dx = static_cast<T*>(t.out);
+    if (dx != nullptr) dx += b * t.ob + tk * t.os + (h0 + sub) * t.oh;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = -s[e];  // of R^T
     for (int batch = 0; batch < a.batches && h0 + batch * ROWS * groups < t.heads; ++batch) {
       if (batch) load(batch);
 #pragma unroll
@@ -380,29 +403,29 @@ qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
         float xv[8], gv[8], o[8], gw[8];
         rx[k].get(xv);
         rg[k].get(gv);
-        pl.partners(a, gv, dy + h * t.yh, valid, o);
+        pl.partners(a, gv, dy_row, valid, o);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           if (P != Partner::NONE)  // R^T dy
-            set_pair(gv, e, f2_fma(pair(o, e), f2_pack(-s[e], -s[e + 1]), f2_mul(pair(gv, e), pair(c, e))));
+            set_pair(gv, e, f2_fma(pair(o, e), pair(s, e), f2_mul(pair(gv, e), pair(c, e))));
           set_pair(gw, e, f2_mul(pair(gv, e), pair(w, e)));
         }
-        float ss = dot8(xv, xv), sg = dot8(gw, xv);
-#pragma unroll 1
-        for (int o2 = a.L / 2; o2; o2 >>= 1) {
-          ss += __shfl_xor_sync(~0u, ss, o2);
-          sg += __shfl_xor_sync(~0u, sg, o2);
-        }
-        const float r = inverse_root(fmaf(ss, over_d, a.eps));
-        const uint64_t r2 = f2_splat(r), m2 = f2_splat(-(sg * over_d * r * r));
+        float sums[2] = {dot8(xv, xv), dot8(gw, xv)};
+        lanes_sum(a.L, sums);
+        const float r = inverse_root(fmaf(sums[0], over_d, a.eps));
+        const uint64_t r2 = f2_splat(r), m2 = f2_splat(-(sums[1] * over_d * r * r));
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           const uint64_t d = f2_fma(pair(gv, e), f2_mul(pair(xv, e), r2), pair(dw, e));
-          if (valid) set_pair(dw, e, d);
+          set_pair(dw, e, d);  // (0 of a lane without a row, but in a token that is NaN anyway)
           set_pair(gw, e, f2_mul(f2_fma(pair(xv, e), m2, pair(gw, e)), r2));
         }
         __syncwarp();  // dx may be dy: a row's partners have been read
-        if (valid && dx != nullptr) pl.put(dx + h * t.oh, gw);
+        if (t.out != nullptr) {
+          if (valid) pl.put(dx, gw);
+          dx += groups * t.oh;
+        }
+        if (P == Partner::LOADS) dy_row += groups * t.yh;
       }
     }
   }
