@@ -176,7 +176,8 @@ struct DqSmem {
   static constexpr int KST = DP == 64 ? 4 : 3, VST = DP == 64 ? 4 : 2;
   static constexpr int Q = 0, DO = TILE, K = 2 * TILE, V = K + KST * TILE;
   static constexpr int RED = V + VST * TILE;  // [column group][128] fp32: partial sums of the rows
-  static constexpr int BAR = RED + 4 * 128 * 4;
+  static constexpr int ORDER = RED + 4 * 128 * 4;  // the sequences in order
+  static constexpr int BAR = ORDER + MAX_ORDER;
   static constexpr int NBAR = 14 + 2 * KST + 2 * VST;
   static constexpr int USED = BAR + 8 * NBAR + 16;
   // the tiles need 1024-byte alignment: the window starts so aligned on this GPU, and
@@ -192,14 +193,12 @@ struct DqItem {
 };
 // The bytes of a piece of dq are 4 dq_piece(D).
 __host__ __device__ __forceinline__ int64_t dq_piece(int D) { return 128 * (D + 1); }
-__device__ __forceinline__ DqItem dq_item(const Plan& p, const Work& w) {
+__device__ __forceinline__ DqItem dq_item(const Plan& p, const Order* o, const Work& w) {
   const Args& a = p.a;
-  const int bh = a.H * a.B;
   DqItem it;
-  const int tile = p.tiles - 1 - w.item / bh;
-  const int r = w.item % bh;
-  it.h = r % a.H;
-  it.b = r / a.H;
+  it.h = w.item % a.H;
+  int tile;
+  query_item(a, o, w.item / a.H, p.tiles, &tile, &it.b);
   it.q0 = tile * 128;
   it.len = a.len(it.b);
   it.p0 = a.start(it.b) + it.q0;
@@ -279,6 +278,9 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
   const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
   pdl_wait();
   pdl_trigger();
+  // (the items here need no counts of tiles: those stay in the scratch)
+  Order* const order = reinterpret_cast<Order*>(gbase + L::ORDER);
+  if (ragged(a)) order_sequences(a, reinterpret_cast<int*>(gbase), order, reinterpret_cast<int*>(gbase) + MAX_ORDER);
   bool ok = true;
   Work wk;
 
@@ -304,7 +306,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
           return landed;
         };
         for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
-          const DqItem it = dq_item(p, wk);
+          const DqItem it = dq_item(p, order, wk);
           if (it.n == 0) continue;
           const int g = it.h / a.share;
           ok = load_kv(it.j0 * 128, g, it.b);
@@ -331,7 +333,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
       if (ptx::elect_one()) {
         uint32_t g = 0, nq = 0;  // blocks (= ring entries) and items with blocks so far
         for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
-          const DqItem it = dq_item(p, wk);
+          const DqItem it = dq_item(p, order, wk);
           if (it.n == 0) continue;
           if (!wait1(qdo_full, nq & 1)) {
             ok = false;
@@ -378,7 +380,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
       if (ptx::elect_one()) {
         uint32_t g = 0, nk = 0;  // blocks, items with blocks finished
         for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
-          const DqItem it = dq_item(p, wk);
+          const DqItem it = dq_item(p, order, wk);
           if (it.n == 0) continue;
           for (int j = 0; j < it.n; ++j, ++g) {  // dQ += dS_j K_j
             const uint32_t sk = g % KST, b = g & 1;
@@ -425,7 +427,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
       nd = 0.f;
       Work w;
       if (!work_at(p, k, cta, G, &w)) return;
-      const DqItem it = dq_item(p, w);
+      const DqItem it = dq_item(p, order, w);
       const int64_t at = ((int64_t)it.b * a.H + it.h) * a.q_pitch + it.q0 + row;
       nl = a.neg_lse2[at];
       nd = a.delta[at];
@@ -448,7 +450,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     float nl_next, nd_next;
     stats(0, nl_next, nd_next);
     for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
-      const DqItem it = dq_item(p, wk);
+      const DqItem it = dq_item(p, order, wk);
       const int qi = it.q0 + row;
       const bool valid_q = qi < a.Sq;
       const float nl = nl_next;
@@ -623,14 +625,13 @@ struct KvItem {
   int g, b, k0, len, p0, i0, per_head, first, n;
 };
 template <int BQ>
-__device__ __forceinline__ KvItem kv_item(const Plan& p, const Work& w) {
+__device__ __forceinline__ KvItem kv_item(const Plan& p, const Order* o, const Work& w) {
   const Args& a = p.a;
   KvItem it;
-  int u = w.item;
-  it.g = u % a.G;
-  const int bt = u / a.G;
-  it.b = bt % a.B;
-  it.k0 = bt / a.B * 128;  // key tile 0 (causal: the most query blocks) first
+  it.g = w.item % a.G;
+  int tile;
+  key_item(a, o, w.item / a.G, p.tiles, &tile, &it.b);
+  it.k0 = tile * 128;
   it.len = a.len(it.b);
   it.p0 = a.start(it.b);
   it.i0 = a.causal ? max(0, it.k0 - it.p0) / BQ : 0;  // blocks before see none of these keys
@@ -814,13 +815,14 @@ struct Kv {
   static constexpr int DP = DP_, BQ = DP == 64 ? 128 : 64;
   static constexpr int GROUPS = DP == 64 ? 1 : 2;               // of element-wise warps, a block each
   static constexpr int NDP = DP == 64 ? 1 : 2, NSET = DP == 64 ? 2 : 1;  // buffers of dP^T; of K and V
-  static constexpr int QST = DP == 64 ? 4 : BIAS ? 4 : 5;
+  static constexpr int QST = 4;
   static constexpr int TILE = tile_bytes<DP>(), QTILE = TILE / 128 * BQ;
   static constexpr int KV = 0, Q = NSET * 2 * TILE, DO = Q + QST * QTILE;  // [set][K | V]
   static constexpr int STAT = DO + QST * QTILE;                            // [stage][-lse2[BQ] | -delta[BQ]] fp32
   static constexpr int BUCKET = STAT + QST * 2 * BQ * 4;                   // [16][MAX_BUCKETS] fp32
   static constexpr int DIAG = BUCKET + (BIAS ? EW * MAX_BUCKETS * 4 : 0);  // [16][64] fp32
-  static constexpr int BAR = DIAG + (BIAS ? EW * 64 * 4 : 0);
+  static constexpr int ORDER = DIAG + (BIAS ? EW * 64 * 4 : 0);  // Order
+  static constexpr int BAR = ORDER + ((int)sizeof(Order) + 15) / 16 * 16;
   static constexpr int NBAR = 4 + 8 + NDP + 2 * NSET + 2 * QST;
   static constexpr int USED = BAR + 8 * NBAR + 16;
   // the tiles need 1024-byte alignment: the window starts so aligned on this GPU, and
@@ -896,6 +898,8 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   const uint32_t t_dv = tmem + (DP == 64 ? 384 : 256), t_dk = t_dv + DP;
   pdl_wait();
   pdl_trigger();
+  Order* const order = reinterpret_cast<Order*>(gbase + L::ORDER);
+  if (ragged(a)) order_sequences(a, reinterpret_cast<int*>(gbase), order, order->tiles);
   bool ok = true;
   Work wk;
 
@@ -905,7 +909,7 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       if (ptx::elect_one()) {
         uint32_t ii = 0, nk = 0;  // blocks and items with blocks so far
         for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
-          const KvItem it = kv_item<BQ>(p, wk);
+          const KvItem it = kv_item<BQ>(p, order, wk);
           if (it.n == 0) continue;
           const uint32_t e = nk % NSET;
           if (nk >= NSET && !wait1(kv_empty(e), ((nk / NSET) & 1) ^ 1)) {
@@ -954,7 +958,7 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       if (ptx::elect_one()) {
         uint32_t ii = 0, nk = 0;
         for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
-          const KvItem it = kv_item<BQ>(p, wk);
+          const KvItem it = kv_item<BQ>(p, order, wk);
           if (it.n == 0) continue;
           const uint32_t e = nk % NSET;
           if (!wait1(kv_full(e), (nk / NSET) & 1)) {
@@ -1004,7 +1008,7 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       if (ptx::elect_one()) {
         uint32_t ii = 0, nk = 0;
         for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
-          const KvItem it = kv_item<BQ>(p, wk);
+          const KvItem it = kv_item<BQ>(p, order, wk);
           if (it.n == 0) continue;
           // (the element-wise warps have read the item before's dV and dK)
           if (nk > 0 && !wait1(acc_empty, (nk - 1) & 1)) {
@@ -1136,7 +1140,7 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     for (int k = 0; ok && work_at(p, k, cta, G, &wk); ++k) {
       int n;
       {
-        const KvItem it = kv_item<BQ>(p, wk);
+        const KvItem it = kv_item<BQ>(p, order, wk);
         n = it.n;
         const int kw = it.k0 + qq * 32, end = (it.g + 1) * a.share;
         int h = it.g * a.share;  // the head whose buckets are being summed
@@ -1180,7 +1184,7 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       }
       // (the item once more: what is not needed among its blocks holds no registers there)
       asm volatile("" : "+r"(wk.item));
-      const KvItem it = kv_item<BQ>(p, wk);
+      const KvItem it = kv_item<BQ>(p, order, wk);
       float* const sums = wk.piece < 0 ? nullptr : p.part + (int64_t)wk.part * 2 * 128 * a.D;
       const int kw = it.k0 + qq * 32;
       // 2 DP columns of dK and dV: DP / 2 of them to each of the four column groups
@@ -1230,9 +1234,12 @@ xattn_dq_join_kernel(const __grid_constant__ Plan p, int sums) {
   pdl_wait();
   pdl_trigger();
   const Args& a = p.a;
+  __shared__ Order order;
+  __shared__ int lens[MAX_ORDER];
+  if (ragged(a)) order_sequences(a, lens, &order, order.tiles);
   const int row = blockIdx.x * 32 + threadIdx.x / 8, lane = threadIdx.x % 8;
   const Work w = {p.cut.whole + (int)blockIdx.y, 0, (int)blockIdx.y * p.cut.pieces};
-  const DqItem it = dq_item(p, w);
+  const DqItem it = dq_item(p, &order, w);
   const int qi = it.q0 + row;
   if (qi >= a.Sq) return;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + it.b * a.sdq.b + qi * a.sdq.s + it.h * a.sdq.h;
@@ -1258,12 +1265,18 @@ xattn_dkv_join_kernel(const __grid_constant__ Plan p) {
   pdl_wait();
   pdl_trigger();
   const Args& a = p.a;
+  __shared__ Order order;
+  __shared__ int lens[MAX_ORDER];
+  if (ragged(a)) order_sequences(a, lens, &order, order.tiles);
   const int row = blockIdx.x * 32 + threadIdx.x / 8, lane = threadIdx.x % 8;
-  const int y = blockIdx.y / 2, item = p.cut.whole + y, bt = item / a.G, key = bt / a.B * 128 + row;
+  const int y = blockIdx.y / 2, item = p.cut.whole + y;
+  int tile, b;
+  key_item(a, &order, item / a.G, p.tiles, &tile, &b);
+  const int key = tile * 128 + row;
   const bool dk = blockIdx.y % 2 == 0;
   if (key >= a.Sk) return;
   const Strides& sd = dk ? a.sdk : a.sdv;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dk ? a.dk : a.dv) + bt % a.B * sd.b + key * sd.s + item % a.G * sd.h;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dk ? a.dk : a.dv) + b * sd.b + key * sd.s + item % a.G * sd.h;
   const int64_t step = (int64_t)2 * 128 * a.D;
   const float* part = p.part + y * p.cut.pieces * step + ((dk ? 0 : 128) + row) * a.D;
   const float scale = dk ? a.scale : 1.f;

@@ -4,8 +4,7 @@
 // A persistent kernel, one CTA per SM, 320 threads.  A work item is 256 queries of one
 // (sequence, head), two tiles of 128 that share every block of 128 keys, over one share
 // of the keys (all of them unless there are few items: then the shares' results are
-// joined by join_splits()).  Items are numbered heaviest first where causal and dealt in
-// snake order.
+// joined by join_splits()).  Items are numbered heaviest first and dealt in snake order.
 //   warp 0      TMA loads in the order the MMAs consume them: Q_0, then K_j and V_j into
 //               rings that run on across items, Q_1 after the first block;
 //   warp 1      TMEM allocation (512 columns); one thread issues the MMAs;
@@ -51,11 +50,15 @@ struct Smem {
   static constexpr int TILE = tile_bytes<DP>();
   static constexpr int ST = DP == 128 ? 2 : 4;  // stages of K and of V
   static constexpr int Q = 0, K = 2 * TILE, V = K + ST * TILE, EPI = V + ST * TILE;
-  static constexpr int BAR = EPI + 8 * 4096;
+  static constexpr int ORDER = EPI + 8 * 4096;  // Order
+  static constexpr int BAR = ORDER + ((int)sizeof(Order) + 15) / 16 * 16;
   // q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain, then the rings'
   static constexpr int NBAR = 11 + 4 * ST;
-  static constexpr int BYTES = BAR + 8 * NBAR + 16 + 1024;
-  static_assert(BYTES <= 232448, "more than 227 KB of shared memory");
+  static constexpr int USED = BAR + 8 * NBAR + 16;
+  // the tiles need 1024-byte alignment: the window starts so aligned on this GPU, and
+  // the kernel checks that what rounding takes is there
+  static constexpr int BYTES = USED + 1024 <= 232448 ? USED + 1024 : 232448;
+  static_assert(USED <= 232448, "more than 227 KB of shared memory");
 };
 
 struct Item {
@@ -70,16 +73,14 @@ struct Plan {
   float scale_log2;
 };
 
-__device__ __forceinline__ Item item_at(const Plan& p, int i) {
+__device__ __forceinline__ Item item_at(const Plan& p, const Order* o, int i) {
   const Args& a = p.a;
   Item it;
-  const int per = a.splits * a.H * a.B;
-  const int pair = p.pairs - 1 - i / per;
-  int r = i % per;
-  it.split = r % a.splits;
-  r /= a.splits;
-  it.h = r % a.H;
-  it.b = r / a.H;
+  it.split = i % a.splits;
+  i /= a.splits;
+  it.h = i % a.H;
+  int pair;
+  query_item(a, o, i / a.H, p.pairs, &pair, &it.b);
   it.q0 = pair * 256;
   it.len = a.len(it.b);
   it.p0 = a.start(it.b) + it.q0;
@@ -110,6 +111,10 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
+  if (base - raw + L::USED > (uint32_t)L::BYTES) {  // (uniform: every thread leaves)
+    if (threadIdx.x == 0) wait_failed(6);
+    return;
+  }
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + L::BAR;
   auto q_full = [&](int t) { return bars + 8u * t; };
@@ -152,6 +157,8 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + (tslot - base));
   pdl_wait();
   pdl_trigger();
+  Order* const order = reinterpret_cast<Order*>(gbase + L::ORDER);
+  if (ragged(a)) order_sequences(a, reinterpret_cast<int*>(gbase), order, order->tiles);
   bool ok = true;
 
   if (warp == 0) {
@@ -168,7 +175,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       for (int k = 0; ok; ++k) {
         const int i = persistent_item(k, cta, G);
         if (i >= p.items) break;
-        const Item it = item_at(p, i);
+        const Item it = item_at(p, order, i);
         const int nmax = max(it.n0, it.n1), g = it.h / a.share;
         if (it.n0 > 0) ok = load_q(it, 0);
         for (int j = 0; j < nmax && ok; ++j) {
@@ -251,7 +258,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       uint32_t kb = 0;  // ring entry of the item's block 0
       Item it{};
       if (i < p.items) {
-        it = item_at(p, i);
+        it = item_at(p, order, i);
         ok = start_tile(it, 0, 0u) && start_tile(it, 1, 0u);
       }
       while (ok && i < p.items) {
@@ -259,7 +266,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         const int inext = persistent_item(k + 1, cta, G);
         const bool has_next = inext < p.items;
         Item nx{};
-        if (has_next) nx = item_at(p, inext);
+        if (has_next) nx = item_at(p, order, inext);
         const uint32_t kb_next = kb + (uint32_t)nmax;
         bool started0 = !has_next, started1 = !has_next;  // the next item's tiles
         for (int j = 0; j < nmax && ok; ++j) {
@@ -312,7 +319,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     for (int k = 0; ok; ++k) {
       const int i = persistent_item(k, cta, G);
       if (i >= p.items) break;
-      const Item it = item_at(p, i);
+      const Item it = item_at(p, order, i);
       const int nt = t ? it.n1 : it.n0;
       const int qi = it.q0 + 128 * t + row;         // the thread's query
       const int pi = it.p0 + 128 * t + row;         // and its position

@@ -66,6 +66,69 @@ __device__ __forceinline__ int persistent_item(int k, int c, int G) {
   return k * G + ((k & 1) ? G - 1 - c : c);
 }
 
+// Ragged sequences (up to MAX_ORDER of them) by falling number of keys, so that items of
+// falling size are dealt out and those without keys come last: order[place] is the
+// sequence, tiles[place] how many tiles of 128 keys the sequences before it have
+// (tiles[batch]: all).  By all of a CTA's threads, MAX_ORDER at least, before it loads
+// anything to shared memory; `lens` is scratch, `tiles` o->tiles or scratch too.  8 sequences of up to 1531 keys, 16 heads of
+// 64, forward and backward: 149 -> TODO us.
+constexpr int MAX_ORDER = 256;
+struct Order {
+  uint8_t order[MAX_ORDER];
+  int tiles[MAX_ORDER + 4];
+};
+__device__ __forceinline__ bool ragged(const Args& a) { return a.kv_lens != nullptr && a.B > 1 && a.B <= MAX_ORDER; }
+__device__ __forceinline__ void order_sequences(const Args& a, int* lens, Order* o, int* tiles) {
+  const int t = threadIdx.x;
+  if (t < a.B) lens[t] = a.len(t);
+  __syncthreads();
+  if (t < a.B) {
+    const int mine = lens[t];
+    int place = 0, before = 0, all = 0;
+    for (int x = 0; x < a.B; ++x) {
+      const int n = (lens[x] + 127) / 128;
+      const bool first = lens[x] > mine || (lens[x] == mine && x < t);
+      place += first;
+      before += first ? n : 0;
+      all += n;
+    }
+    o->order[place] = (uint8_t)t;
+    tiles[place] = before;
+    if (place == 0) tiles[a.B] = all;
+  }
+  ptx::fence_async_smem();  // (TMA writes over `lens` next)
+  __syncthreads();
+}
+// Item r of batch x tiles in the order of their work: causal by falling tile (the last
+// queries see the most keys), otherwise sequence by sequence.
+__device__ __forceinline__ void query_item(const Args& a, const Order* o, int r, int tiles, int* tile, int* b) {
+  const int place = a.causal ? r % a.B : r / tiles;
+  *tile = a.causal ? tiles - 1 - r / a.B : r % tiles;
+  *b = ragged(a) ? o->order[place] : place;
+}
+// ... of key tiles: causal by rising tile (the first keys are seen by the most queries),
+// otherwise the tiles that hold keys, sequence by sequence, then the others.
+__device__ __forceinline__ void key_item(const Args& a, const Order* o, int r, int tiles, int* tile, int* b) {
+  if (a.causal || !ragged(a)) {
+    const int place = r % a.B;
+    *tile = r / a.B;
+    *b = ragged(a) ? o->order[place] : place;
+    return;
+  }
+  const int full = o->tiles[a.B];
+  const bool held = r < full;
+  const int x = held ? r : r - full;
+  int lo = 0, hi = a.B;  // the last place whose tiles begin at or before x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2, first = held ? o->tiles[mid] : mid * tiles - o->tiles[mid];
+    if (first <= x) lo = mid;
+    else hi = mid;
+  }
+  const int first = held ? o->tiles[lo] : lo * tiles - o->tiles[lo];
+  *tile = (held ? 0 : o->tiles[lo + 1] - o->tiles[lo]) + x - first;
+  *b = o->order[lo];
+}
+
 // ---- host ---------------------------------------------------------------------------
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
