@@ -181,6 +181,7 @@ xattn_bias_grad_kernel(const float* part, int64_t rows, int heads, int buckets, 
   const int u = threadIdx.x % buckets, r0 = threadIdx.x / buckets;
   float v = 0.f;
   if (r0 < lanes)
+#pragma unroll 8
     for (int64_t r = r0; r < rows; r += lanes) v += part[(h * rows + r) * buckets + u];
   red[threadIdx.x] = v;
   __syncthreads();

@@ -101,40 +101,50 @@ __device__ __forceinline__ void cut_blocks(const Plan& p, int piece, int n, int*
 }
 
 // Every row's -lse (base 2) and -delta, [batch][heads][q_pitch] each, so that a block's are
-// one copy: 16 lanes a row, 16 bytes each.  Rows behind the queries have no weights.
+// one copy: 16 lanes a row, 16 bytes each, four queries of a head at a time.  Rows behind
+// the queries have no weights.
 __global__ void __launch_bounds__(256)
-xattn_stats_kernel(const __grid_constant__ Args a, int64_t rows) {
+xattn_stats_kernel(const __grid_constant__ Args a, int64_t fours) {
   pdl_wait();
   pdl_trigger();
-  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 16;  // (batch, query, head)
-  const int c = threadIdx.x % 16 * 8;
-  float d = 0.f;
-  int64_t b = 0;
-  int h = 0, qi = 0;
-  if (r < rows) {
-    const int64_t bq = r / a.H;
-    b = bq / a.q_pitch;
-    h = (int)(r - bq * a.H), qi = (int)(bq - b * a.q_pitch);
-    if (c < a.D && qi < a.Sq) {
-      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + b * a.so.b +
-                                                      qi * a.so.s + h * a.so.h + c);
-      const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_o) + b * a.sdo.b +
-                                                      qi * a.sdo.s + h * a.sdo.h + c);
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
+  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 16;  // (batch, four queries, head)
+  const int lane = threadIdx.x % 16, c = lane * 8;
+  const int64_t bq = r / a.H;
+  const int h = (int)(r - bq * a.H), per = a.q_pitch / 4;
+  const int64_t b = bq / per;
+  const int q0 = (int)(bq - b * per) * 4;
+  uint4 x[4], y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(w[i] << 16), d);
-        d = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(w[i] & 0xffff0000u), d);
-      }
+  for (int i = 0; i < 4; ++i) {
+    x[i] = y[i] = make_uint4(0, 0, 0, 0);
+    if (r < fours && c < a.D && q0 + i < a.Sq) {
+      x[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + b * a.so.b + (q0 + i) * a.so.s +
+                                             h * a.so.h + c);
+      y[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_o) + b * a.sdo.b + (q0 + i) * a.sdo.s +
+                                             h * a.sdo.h + c);
+    }
+  }
+  float d[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      d[i] = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(w[e] << 16), d[i]);
+      d[i] = fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(w[e] & 0xffff0000u), d[i]);
     }
   }
 #pragma unroll
-  for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
-  if (r < rows && c == 0) {
-    const int64_t at = (b * a.H + h) * a.q_pitch + qi;
-    a.neg_lse2[at] = qi < a.Sq ? minus_lse2(a.lse[a.stat((int)b, h, qi)]) : -INFINITY;
-    a.delta[at] = -d;
-  }
+  for (int o = 8; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] += __shfl_xor_sync(~0u, d[i], o);
+  if (r >= fours || lane > 0) return;
+  const int64_t at = (b * a.H + h) * a.q_pitch + q0;
+  float l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) l[i] = q0 + i < a.Sq ? minus_lse2(a.lse[a.stat((int)b, h, q0 + i)]) : -INFINITY;
+  *reinterpret_cast<float4*>(a.neg_lse2 + at) = make_float4(l[0], l[1], l[2], l[3]);
+  *reinterpret_cast<float4*>(a.delta + at) = make_float4(-d[0], -d[1], -d[2], -d[3]);
 }
 
 // 128 rows x DP columns through a map of 64-row boxes (two of a column group lie one
@@ -1312,7 +1322,7 @@ cudaError_t launch(const Args& a, const BwdCut& cut, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(xattn_dkv_kernel<DP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, DKV_BYTES);
   }));
-  const int64_t rows = (int64_t)a.B * a.q_pitch * a.H;
+  const int64_t rows = (int64_t)a.B * (a.q_pitch / 4) * a.H;
   if ((rows + 15) / 16 > INT32_MAX) return cudaErrorInvalidConfiguration;
   OASES_TRY(launch_pdl(xattn_stats_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, st, a, rows));
   Plan pq;

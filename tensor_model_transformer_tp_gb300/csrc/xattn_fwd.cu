@@ -99,6 +99,11 @@ __device__ __forceinline__ Item item_at(const Plan& p, const Order* o, int i) {
   return it;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ void wait_failed(int site) { atomicCAS(&g_xattn_fwd_error, 0, site); }
 
 template <int DP, bool BIAS>
@@ -366,15 +371,14 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
           for (int c = 0; c < 128; ++c)
             if (c >= nvis) sv[c] = -INFINITY;
         }
-        // row maximum in eight independent chains (mul is positive)
+        // row maximum in eight independent chains, two scores a step (mul is positive)
         float pm[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) pm[c] = sv[c];
+        for (int c = 0; c < 8; ++c) pm[c] = fmaxf(sv[2 * c], sv[2 * c + 1]);
 #pragma unroll
-        for (int c = 8; c < 128; ++c) pm[c % 8] = fmaxf(pm[c % 8], sv[c]);
-        const float mx = fmaf(fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
-                                    fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7]))),
-                              mul, add);
+        for (int c = 16; c < 128; c += 2) pm[c / 2 % 8] = max3(pm[c / 2 % 8], sv[c], sv[c + 1]);
+        const float mx =
+            fmaf(max3(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])), mul, add);
         const float m_new = fmaxf(m_ref, mx);
         // O_t is rescaled by f (below) where the reference maximum is raised
         float f = 1.f;
