@@ -5,13 +5,15 @@
 // by HBM.  A tile of a matrix product would be nearly empty; here a key's values lie in
 // the lanes of a part of a warp, 16 bytes each, and every row's product with it is
 // summed by shuffles.  Each such group of lanes goes through its own keys with its own
-// running maximum and sum, KU keys' loads of K and V in flight together.  A cluster of
-// CTAs shares the keys that the sequence has (so that ragged batches stay even) and
-// joins its groups' results through distributed shared memory; only where sequences and
-// key heads are too few for the GPU are the keys split further, through memory.
-// Ragged sequences are taken longest first, rounds of the SMs in snake order, so that the
-// CTAs that share an SM have about the same keys together (16 sequences of up to 1500 keys,
-// 20 heads of 64: 15 -> TODO us with the keys in L2, 24 -> TODO from memory).
+// running maximum and sum, KU keys at a time, the next ones' loads in flight in the
+// registers that these have left (a whole step ahead, in registers of its own, leaves two
+// CTAs an SM instead of three: 64 sequences of up to 2000 keys, 16 heads of 64, 50 us
+// against 46; through shared memory, 49).  A cluster of CTAs shares the keys that the
+// sequence has and joins its groups' results through distributed shared memory; only
+// where sequences and key heads are too few for the GPU are the keys split further,
+// through memory.  Ragged sequences are taken longest first, rounds of the SMs in snake
+// order, so that the CTAs that share an SM have about the same keys together (16 sequences
+// of up to 1500 keys, 20 heads of 64: 14 us with the keys in L2, 21 from memory; 59 MB).
 // The position bias: R or more away one value on each side, kept in a register; nearer, by
 // distance from shared memory where R is at most NEAR, else searched for.
 #include <math.h>
@@ -61,13 +63,13 @@ struct Table {
 };
 
 // LPK lanes a key, R rows (query i, query head hh of the group: row i share + hh).
-template <typename T, int LPK, int R>
+template <typename T, int LPK, int R, bool BIAS>
 __global__ void __launch_bounds__(NT, R == 1 ? 3 : 2)
 xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table table, int rows, int sms) {
-  constexpr int E = EPL<T>, GROUPS = 32 / LPK, KU = R == 1 ? 4 : 2, D_MAX = LPK * E;
+  constexpr int E = EPL<T>, GROUPS = 32 / LPK, KU = R == 4 ? 2 : 4, D_MAX = LPK * E;
   __shared__ float red_o[WARPS][R][D_MAX], red_m[WARPS][R], red_l[WARPS][R];
   __shared__ float out_o[R][D_MAX], out_m[R], out_l[R];
-  __shared__ float near[R][2 * NEAR + 1];
+  __shared__ float near[BIAS ? R : 1][BIAS ? 2 * NEAR + 1 : 1];
   __shared__ int lens[NT], order[NT];
   pdl_wait();
   pdl_trigger();
@@ -112,7 +114,7 @@ xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table t
     unpack<T>(v, q[r]);
     pos[r] = p0 + i;
     left[r] = right[r] = 0.f;
-    if (a.bias.buckets && in) {
+    if (BIAS && in) {
       left[r] = table.at<T>(a.H, h, -a.bias.R);
       right[r] = table.at<T>(a.H, h, a.bias.R);
     }
@@ -127,22 +129,20 @@ xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table t
   }
   const T* kp = static_cast<const T*>(a.k) + b * a.sk.b + g * a.sk.h + sub * E;
   const T* vp = static_cast<const T*>(a.v) + b * a.sv.b + g * a.sv.h + sub * E;
-  // a step's keys and values are loaded while the step before is worked on
-  uint4 kn[KU], vn[KU];
-  auto load = [&](int k0) {
+  // a step's keys are loaded once the step before has used its own, and its values likewise
+  uint4 kv[KU], vv[KU];
+  auto load = [&](uint4 (&to)[KU], const T* from, int64_t stride, int k0) {
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
       const int key = k0 + u * GROUPS;
-      kn[u] = vn[u] = make_uint4(0, 0, 0, 0);
-      if (key < k_end && cols) {
-        kn[u] = *reinterpret_cast<const uint4*>(kp + key * a.sk.s);
-        vn[u] = *reinterpret_cast<const uint4*>(vp + key * a.sv.s);
-      }
+      to[u] = make_uint4(0, 0, 0, 0);
+      if (key < k_end && cols) to[u] = *reinterpret_cast<const uint4*>(from + key * stride);
     }
   };
   const int k_first = k_begin + warp * GROUPS * KU + grp;
-  load(k_first);
-  const bool by_distance = a.bias.buckets && a.bias.R <= NEAR;
+  load(kv, kp, a.sk.s, k_first);
+  load(vv, vp, a.sv.s, k_first);
+  const bool by_distance = BIAS && a.bias.R <= NEAR;
   if (by_distance) {
     const int n = 2 * a.bias.R + 1;
     for (int x = threadIdx.x; x < rows * n; x += NT)
@@ -150,10 +150,6 @@ xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table t
     __syncthreads();
   }
   for (int k0 = k_first; k0 - grp < k_end; k0 += STEP) {
-    uint4 kv[KU], vv[KU];
-#pragma unroll
-    for (int u = 0; u < KU; ++u) kv[u] = kn[u], vv[u] = vn[u];
-    load(k0 + STEP);
     float s[R][KU];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
@@ -167,6 +163,7 @@ xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table t
         s[r][u] = d;
       }
     }
+    load(kv, kp, a.sk.s, k0 + STEP);
 #pragma unroll
     for (int o = LPK / 2; o; o >>= 1)
 #pragma unroll
@@ -180,7 +177,7 @@ xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table t
 #pragma unroll
       for (int u = 0; u < KU; ++u) {
         const int key = k0 + u * GROUPS;
-        if (a.bias.buckets && r < rows) {
+        if (BIAS && r < rows) {
           const int n = key - pos[r];
           s[r][u] += n <= -a.bias.R   ? left[r]
                      : n >= a.bias.R ? right[r]
@@ -211,6 +208,7 @@ xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table t
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[r][e] = fmaf(s[r][u], f[e], acc[r][e]);
     }
+    load(vv, vp, a.sv.s, k0 + STEP);
   }
   // the warp's groups, then the CTA's warps, then the cluster's CTAs
 #pragma unroll
@@ -285,7 +283,7 @@ xattn_few_kernel(const __grid_constant__ Args a, const __grid_constant__ Table t
   if (csize > 1) ptx::cluster_sync();  // no CTA leaves while another reads its results
 }
 
-template <typename T, int LPK, int R>
+template <typename T, int LPK, int R, bool BIAS>
 cudaError_t launch(const Args& a, const Table& tb, int rows, int csize, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(csize * a.splits, a.B * a.G);
@@ -298,15 +296,20 @@ cudaError_t launch(const Args& a, const Table& tb, int rows, int csize, cudaStre
   attr[1].val.clusterDim.x = csize;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = csize > 1 ? 2 : 1;
   ++g_launch_count;
-  return cudaLaunchKernelEx(&cfg, xattn_few_kernel<T, LPK, R>, a, tb, rows, sm_count());
+  return cudaLaunchKernelEx(&cfg, xattn_few_kernel<T, LPK, R, BIAS>, a, tb, rows, sm_count());
+}
+template <typename T, int LPK, bool BIAS>
+cudaError_t launch_bias(const Args& a, const Table& tb, int rows, int csize, cudaStream_t st) {
+  return rows == 1   ? launch<T, LPK, 1, BIAS>(a, tb, rows, csize, st)
+         : rows == 2 ? launch<T, LPK, 2, BIAS>(a, tb, rows, csize, st)
+                     : launch<T, LPK, 4, BIAS>(a, tb, rows, csize, st);
 }
 template <typename T, int LPK>
 cudaError_t launch_rows(const Args& a, const Table& tb, int rows, int csize, cudaStream_t st) {
-  return rows == 1   ? launch<T, LPK, 1>(a, tb, rows, csize, st)
-         : rows == 2 ? launch<T, LPK, 2>(a, tb, rows, csize, st)
-                     : launch<T, LPK, 4>(a, tb, rows, csize, st);
+  return a.bias.buckets ? launch_bias<T, LPK, true>(a, tb, rows, csize, st)
+                        : launch_bias<T, LPK, false>(a, tb, rows, csize, st);
 }
 
 // CTAs of a cluster: two an SM in all, with 256 keys each at least (at 320 sequences and

@@ -9,7 +9,7 @@
 // padding, so that eight rows read at once (16 bytes each) fall into different banks.  At
 // RI = 4 both kinds of product are bound by the FMAs (16 clocks of them a warp against 12 of
 // reads), at RI = 2 by the reads (10 against 8): 32 rows are for grids that would leave SMs
-// idle (2 sequences of 130, 6 heads of 64, forward and backward: 86 -> TODO us).
+// idle (2 sequences of 130, 6 heads of 64, forward and backward: 86 -> 68 us).
 #include <math.h>
 
 #include <algorithm>

@@ -396,6 +396,20 @@ def test_scores_beyond_what_weights_resolve_give_no_gradient(dtype, value):
     assert not dq[:, :, 1].any() and not dk[:, :, 1].any() and not db[:, 1].any()
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_ragged_sequences(causal, D):
+    """Sequences in another order of length than of place, some empty, some alike."""
+    lens = [0, 300, 17, 300, 129, 256, 1, 0, 270]
+    run("bf16", 9, 200, 300, 4, 2, D, lens=lens, causal=causal, start=[0, 100, 3, 99, 0, 57, 0, 0, 71] if causal else 0,
+        buckets=16)
+
+
+@pytest.mark.parametrize("Sq", [1, 5])
+def test_more_ragged_sequences_than_are_ordered(Sq):
+    run("bf16", 270, Sq, 140, 2, 2, 40, lens=[(37 * b) % 141 for b in range(270)])
+
+
 # few items over long keys or many queries, whose backward cuts them into pieces
 CUT = [(1, 70, 2100, 2, 1, 64), (2, 1300, 70, 4, 2, 64), (1, 70, 1500, 1, 1, 128),
        (1, 1300, 150, 2, 1, 128), (3, 900, 1200, 4, 4, 40)]
