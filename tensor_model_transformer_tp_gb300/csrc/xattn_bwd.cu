@@ -26,7 +26,7 @@
 //
 // The bias's gradient (dkv kernel).  A warp's 32 x 32 scores that lie R or more from the
 // diagonal on one side belong to one bucket: every thread adds its own.  Nearer ones are
-// summed along their 63 diagonals, by passing a running sum from lane to lane as the
+// summed along their 63 diagonals, by passing running sums from lane to lane as the
 // column advances (lane r adds element (r, c) at step c, so a sum that moves one lane a
 // step stays on its diagonal), and each bucket's run of diagonals is added to the warp's
 // own buckets in shared memory: a fixed order throughout.
@@ -721,7 +721,7 @@ __device__ __forceinline__ void gradients(uint32_t nd, const float (&w)[16], flo
 // far from the diagonal in registers.
 struct KvBias {
   float far_left = 0.f, far_right = 0.f;
-  uint32_t bucket, diag;  // shared addresses, the warp's own: [MAX_BUCKETS], [64] fp32
+  uint32_t bucket, diag;  // shared addresses, the warp's own: [MAX_BUCKETS], [2][64] fp32
 
   __device__ __forceinline__ void init(const Args& a, uint32_t buckets, uint32_t diagonals, int lane) {
     bucket = buckets;
@@ -740,16 +740,24 @@ struct KvBias {
       else far_right += t;
       return;
     }
-    // along the diagonals, that of element (r, x) r - x + 31, of distance n0 + the same
-    float run = 0.f;
+    // along the diagonals, that of element (r, x) r - x + 31, of distance n0 + the same; two
+    // chains, of columns 0 .. 15 (diagonals 16 .. 62) and 16 .. 31 (0 .. 46)
+    float run0 = 0.f, run1 = 0.f;
 #pragma unroll
-    for (int x = 0; x < 32; ++x) {
-      run = __shfl_up_sync(0xffffffffu, run, 1);
-      run = (lane == 0 ? 0.f : run) + w[x];
-      if (lane == 31) ptx::sts(diag + 4 * (62 - x), run);
+    for (int x = 0; x < 16; ++x) {
+      run0 = __shfl_up_sync(0xffffffffu, run0, 1);
+      run1 = __shfl_up_sync(0xffffffffu, run1, 1);
+      run0 = (lane == 0 ? 0.f : run0) + w[x];
+      run1 = (lane == 0 ? 0.f : run1) + w[16 + x];
+      if (lane == 31) {
+        ptx::sts(diag + 4 * (62 - x), run0);
+        ptx::sts(diag + 256 + 4 * (46 - x), run1);
+      }
     }
-    if (lane < 31) ptx::sts(diag + 4 * lane, run);
-    else ptx::sts(diag + 4 * 63, 0.f);
+    if (lane < 31) {
+      ptx::sts(diag + 4 * (16 + lane), run0);
+      ptx::sts(diag + 256 + 4 * lane, run1);
+    }
     __syncwarp();
     // a bucket's diagonals stand side by side: sums within runs of equal buckets, added by
     // each run's last lane
@@ -760,7 +768,10 @@ struct KvBias {
       const int before = __shfl_up_sync(0xffffffffu, u, 1);
       const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 || u != before);
       const int first = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));  // of this lane's run
-      float t = ptx::lds(diag + 128 * half + 4 * lane);
+      const int d = 32 * half + lane;  // (63: none)
+      float t = 0.f;
+      if (d >= 16 && d < 63) t = ptx::lds(diag + 4 * d);
+      if (d < 47) t += ptx::lds(diag + 256 + 4 * d);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float below = __shfl_up_sync(0xffffffffu, t, o);
@@ -830,8 +841,8 @@ struct Kv {
   static constexpr int KV = 0, Q = NSET * 2 * TILE, DO = Q + QST * QTILE;  // [set][K | V]
   static constexpr int STAT = DO + QST * QTILE;                            // [stage][-lse2[BQ] | -delta[BQ]] fp32
   static constexpr int BUCKET = STAT + QST * 2 * BQ * 4;                   // [16][MAX_BUCKETS] fp32
-  static constexpr int DIAG = BUCKET + (BIAS ? EW * MAX_BUCKETS * 4 : 0);  // [16][64] fp32
-  static constexpr int ORDER = DIAG + (BIAS ? EW * 64 * 4 : 0);  // Order
+  static constexpr int DIAG = BUCKET + (BIAS ? EW * MAX_BUCKETS * 4 : 0);  // [16][2][64] fp32
+  static constexpr int ORDER = DIAG + (BIAS ? EW * 128 * 4 : 0);  // Order
   static constexpr int BAR = ORDER + ((int)sizeof(Order) + 15) / 16 * 16;
   static constexpr int NBAR = 4 + 8 + NDP + 2 * NSET + 2 * QST;
   static constexpr int USED = BAR + 8 * NBAR + 16;
@@ -1077,7 +1088,7 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     const bool grad = BIAS && a.bias_part != nullptr;
     KvBias kb;
     if (grad)
-      kb.init(a, base + L::BUCKET + (warp - EW0) * MAX_BUCKETS * 4, base + L::DIAG + (warp - EW0) * 256, lane);
+      kb.init(a, base + L::BUCKET + (warp - EW0) * MAX_BUCKETS * 4, base + L::DIAG + (warp - EW0) * 512, lane);
     // Block ii of the warp, queries from qi on: weights and dS (masked where !FULL).
     auto block = [&](auto FULL, uint32_t ii, int h, int kw, int len, int p0, int qi) {
       const uint32_t b = ii & 1, own = lane_off + c * 32;

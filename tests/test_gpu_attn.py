@@ -455,3 +455,48 @@ def test_shares_of_fp32(shape, biased):
     """Few tiles over many blocks, and tiles of 64 rows (the last)."""
     run("f32", *shape, lens=[shape[2] - 5 * b for b in range(shape[0])], buckets=48 if biased else 0,
         causal=shape[1] == shape[2])
+
+
+@pytest.mark.parametrize("dtype,most", [("f32", 2e-3), ("bf16", 0.15)])
+def test_a_layer_of_one_projection(dtype, most):
+    """Norms and rotation, attention, and both backward into slices of one packed gradient,
+    against autograd in 64 bits.  In fp32 each of six stages is off by g(K) = K 2^-23 at most,
+    K <= 100 terms, which the softmax (scores up to 8) multiplies by 16 at most: 1.2e-3.  In
+    bf16 the rounded q' and k' move a score by 2 u sqrt(D) at most, a weight by twice that, and
+    five more roundings add u each: 0.14 of the gradients' norm."""
+    B, S, H, G, D, R = 3, 100, 4, 2, 64, 32
+    gen = torch.Generator().manual_seed(5)
+    make = lambda *shape: torch.randn(*shape, generator=gen).to(T[dtype]).cuda()  # noqa: E731
+    qkv, wq, wk, do = make(B, S, H + 2 * G, D), make(D), make(D), make(B, S, H, D)
+    bias = make(16, H)
+    lens = torch.tensor([100, 37, 64], dtype=torch.int32, device="cuda")
+    angle = torch.arange(S, device="cuda")[:, None] * 100.0 ** (-torch.arange(R // 2, device="cuda") / (R // 2))
+    cos, sin = angle.cos().float(), angle.sin().float()
+    q, k, v = qkv[:, :, :H], qkv[:, :, H:H + G], qkv[:, :, H + G:]
+    opt = dict(kv_lens=lens, causal=True, bias=bias)
+    q2, k2 = F.qk_norm_rope_fwd(q, k, cos, sin, q_weight=wq, k_weight=wk)
+    o, lse = F.attn_fwd(q2, k2, v, **opt)
+    grad = torch.empty_like(qkv)
+    dq, dk, dv = grad[:, :, :H], grad[:, :, H:H + G], grad[:, :, H + G:]
+    _, _, _, db = F.attn_bwd(q2, k2, v, o, lse, do, out=(dq, dk, dv), **opt)
+    _, _, dwq, dwk = F.qk_norm_rope_bwd(q, k, dq, dk, cos, sin, q_weight=wq, k_weight=wk, out=(dq, dk))
+    oz.oases_check_device(torch.cuda.current_stream())
+
+    wide = [x.double().requires_grad_(True) for x in (qkv, wq, wk, bias)]
+
+    def turned(x, w):
+        x = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6) * w
+        a, b, rest = x[..., :R // 2], x[..., R // 2:R], x[..., R:]
+        c, s = cos.double()[None, :, None], sin.double()[None, :, None]
+        return torch.cat([a * c - b * s, a * s + b * c, rest], -1)
+
+    Q = turned(wide[0][:, :, :H], wide[1])
+    K, V = turned(wide[0][:, :, H:H + G], wide[2]), wide[0][:, :, H + G:]
+    at = torch.tensor(bucket_map(S, S, 0, 16, 128, False), device="cuda")
+    s = torch.einsum("bihd,bjhd->bhij", Q, K.repeat_interleave(H // G, 2)) * D ** -0.5 + wide[3][at].permute(2, 0, 1)
+    n = torch.arange(S, device="cuda")
+    s = s.masked_fill((n[None] > n[:, None]) | (n >= lens[:, None, None, None]), float("-inf"))
+    want_o = torch.einsum("bhij,bjhd->bihd", torch.softmax(s, -1), V.repeat_interleave(H // G, 2))
+    want = torch.autograd.grad(want_o, wide, do.double())
+    for got, w in ((o, want_o.detach()), (grad, want[0]), (dwq, want[1]), (dwk, want[2]), (db, want[3])):
+        assert (got.double() - w).norm() <= most * w.norm()
