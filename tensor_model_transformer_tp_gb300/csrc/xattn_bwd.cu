@@ -50,14 +50,6 @@ constexpr uint64_t WAIT = 1ull << 29;  // cycles before a wait gives up (~0.25 s
 constexpr int NT = 640, ACC_WARP = 2, EW = 16, EW0 = 4;
 constexpr int REGS = 96, REGS_ISSUE = 64, REGS_EW = 104;
 static_assert(128 * REGS_ISSUE + 32 * EW * REGS_EW == NT * REGS, "registers of the warpgroups");
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
 constexpr int BOX64 = 64 * 64 * 2;  // one TMA box of 64 rows
 
 __device__ __forceinline__ void wait_failed(int site) { atomicCAS(&g_xattn_bwd_error, 0, site); }
@@ -732,10 +724,11 @@ struct KvBias {
   // dS w of 32 keys, the first at distance n0 + 31 from query 0, summed by bucket.
   __device__ __forceinline__ void sum(const Args& a, bool on_left, bool on_right, int n0, int lane, const float (&w)[32]) {
     if (on_left || on_right) {
-      float s[4] = {w[0], w[1], w[2], w[3]};
+      uint64_t s[2] = {f2_pack(w[0], w[1]), f2_pack(w[2], w[3])};
 #pragma unroll
-      for (int x = 4; x < 32; ++x) s[x & 3] += w[x];
-      const float t = (s[0] + s[1]) + (s[2] + s[3]);
+      for (int x = 4; x < 32; x += 2) s[x / 2 & 1] = f2_add(s[x / 2 & 1], f2_pack(w[x], w[x + 1]));
+      s[0] = f2_add(s[0], s[1]);
+      const float t = f2_lo(s[0]) + f2_hi(s[0]);
       if (on_left) far_left += t;
       else far_right += t;
       return;

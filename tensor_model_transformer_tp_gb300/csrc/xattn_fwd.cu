@@ -1,14 +1,14 @@
 // Attention over keys of another length, forward, on the 5th-generation tensor cores
 // (bf16 in, fp32 softmax).
 //
-// A persistent kernel, one CTA per SM, 320 threads.  A work item is 256 queries of one
+// A persistent kernel, one CTA per SM, 384 threads.  A work item is 256 queries of one
 // (sequence, head), two tiles of 128 that share every block of 128 keys, over one share
 // of the keys (all of them unless there are few items: then the shares' results are
 // joined by join_splits()).  Items are numbered heaviest first and dealt in snake order.
 //   warp 0      TMA loads in the order the MMAs consume them: Q_0, then K_j and V_j into
 //               rings that run on across items, Q_1 after the first block;
 //   warp 1      TMEM allocation (512 columns); one thread issues the MMAs;
-//   warps 2..5  softmax of tile 0, warps 6..9 of tile 1: a thread owns one query's row.
+//   warps 4..7  softmax of tile 0, warps 8..11 of tile 1: a thread owns one query's row.
 // TMEM: S_t (then P_t) in columns 128 t .. + 127, O_t in 256 + 128 t ..
 // Per tile t and block j:
 //   S_t = Q_t K_j^T        A and B from shared memory
@@ -41,7 +41,10 @@ __device__ int g_xattn_fwd_error;
 namespace {
 using namespace xattn;
 
-constexpr int NT = 320;
+// Registers move from the first warpgroup to the softmax warps: 128 x 72 + 256 x 216 =
+// 384 x 168, what a block starts with.
+constexpr int NT = 384, REGS = 168, REGS_ISSUE = 72, REGS_SOFTMAX = 216;
+static_assert(128 * REGS_ISSUE + 256 * REGS_SOFTMAX == NT * REGS, "registers of the warpgroups");
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, false, false);
 
@@ -52,8 +55,8 @@ struct Smem {
   static constexpr int Q = 0, K = 2 * TILE, V = K + ST * TILE, EPI = V + ST * TILE;
   static constexpr int ORDER = EPI + 8 * 4096;  // Order
   static constexpr int BAR = ORDER + ((int)sizeof(Order) + 15) / 16 * 16;
-  // q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain, then the rings'
-  static constexpr int NBAR = 11 + 4 * ST;
+  // q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], drain, then the rings'
+  static constexpr int NBAR = 13 + 4 * ST;
   static constexpr int USED = BAR + 8 * NBAR + 16;
   // the tiles need 1024-byte alignment: the window starts so aligned on this GPU, and
   // the kernel checks that what rounding takes is there
@@ -125,13 +128,13 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   auto q_full = [&](int t) { return bars + 8u * t; };
   auto q_empty = [&](int t) { return bars + 8u * (2 + t); };
   auto s_full = [&](int t) { return bars + 8u * (4 + t); };
-  auto p_full = [&](int t) { return bars + 8u * (6 + t); };
-  auto o_full = [&](int t) { return bars + 8u * (8 + t); };
-  const uint32_t bar_drain = bars + 8u * 10;
-  auto k_full = [&](uint32_t s) { return bars + 8u * (11 + s); };
-  auto k_empty = [&](uint32_t s) { return bars + 8u * (11 + ST + s); };
-  auto v_full = [&](uint32_t s) { return bars + 8u * (11 + 2 * ST + s); };
-  auto v_empty = [&](uint32_t s) { return bars + 8u * (11 + 3 * ST + s); };
+  auto p_full = [&](int t, int half) { return bars + 8u * (6 + 2 * half + t); };  // P of 64 keys
+  auto o_full = [&](int t) { return bars + 8u * (10 + t); };
+  const uint32_t bar_drain = bars + 8u * 12;
+  auto k_full = [&](uint32_t s) { return bars + 8u * (13 + s); };
+  auto k_empty = [&](uint32_t s) { return bars + 8u * (13 + ST + s); };
+  auto v_full = [&](uint32_t s) { return bars + 8u * (13 + 2 * ST + s); };
+  auto v_empty = [&](uint32_t s) { return bars + 8u * (13 + 3 * ST + s); };
   const uint32_t tslot = bars + 8u * L::NBAR;
   const Args& a = p.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -142,7 +145,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       ptx::mbar_init(q_full(t), 1);
       ptx::mbar_init(q_empty(t), 1);
       ptx::mbar_init(s_full(t), 1);
-      ptx::mbar_init(p_full(t), 4);  // one arrival per softmax warp of the tile
+      for (int half = 0; half < 2; ++half) ptx::mbar_init(p_full(t, half), 4);  // one arrival per softmax warp of the tile
       ptx::mbar_init(o_full(t), 1);
     }
     ptx::mbar_init(bar_drain, 1);
@@ -166,157 +169,164 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   if (ragged(a)) order_sequences(a, reinterpret_cast<int*>(gbase), order, order->tiles);
   bool ok = true;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t ke = 0, qn[2] = {0u, 0u};  // ring entries loaded (entry e in stage e % ST), Q loads
-      auto load_q = [&](const Item& it, int t) {
-        if (qn[t] > 0 && !ptx::mbar_wait(q_empty(t), (qn[t] - 1) & 1)) return false;
-        ptx::mbar_arrive_expect_tx(q_full(t), TILE);
-        load_tile<DP, 128>(base + L::Q + t * TILE, &tq, q_full(t), it.q0 + 128 * t, it.h, it.b);
-        ++qn[t];
-        return true;
-      };
-      uint32_t ve = 0;
-      for (int k = 0; ok; ++k) {
-        const int i = persistent_item(k, cta, G);
-        if (i >= p.items) break;
-        const Item it = item_at(p, order, i);
-        const int nmax = max(it.n0, it.n1), g = it.h / a.share;
-        if (it.n0 > 0) ok = load_q(it, 0);
-        for (int j = 0; j < nmax && ok; ++j) {
-          const int r = (it.j0 + j) * 128;
-          const uint32_t s = ke % ST, u = ke / ST;
-          if (u > 0 && !ptx::mbar_wait(k_empty(s), (u - 1) & 1)) {
-            ok = false;
-            break;
+  if (warp < 4) {
+    fewer_registers<REGS_ISSUE>();
+    if (warp == 0) {
+      if (ptx::elect_one()) {
+        uint32_t ke = 0, qn[2] = {0u, 0u};  // ring entries loaded (entry e in stage e % ST), Q loads
+        auto load_q = [&](const Item& it, int t) {
+          if (qn[t] > 0 && !ptx::mbar_wait(q_empty(t), (qn[t] - 1) & 1)) return false;
+          ptx::mbar_arrive_expect_tx(q_full(t), TILE);
+          load_tile<DP, 128>(base + L::Q + t * TILE, &tq, q_full(t), it.q0 + 128 * t, it.h, it.b);
+          ++qn[t];
+          return true;
+        };
+        uint32_t ve = 0;
+        for (int k = 0; ok; ++k) {
+          const int i = persistent_item(k, cta, G);
+          if (i >= p.items) break;
+          const Item it = item_at(p, order, i);
+          const int nmax = max(it.n0, it.n1), g = it.h / a.share;
+          if (it.n0 > 0) ok = load_q(it, 0);
+          for (int j = 0; j < nmax && ok; ++j) {
+            const int r = (it.j0 + j) * 128;
+            const uint32_t s = ke % ST, u = ke / ST;
+            if (u > 0 && !ptx::mbar_wait(k_empty(s), (u - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            ptx::mbar_arrive_expect_tx(k_full(s), TILE);
+            load_tile<DP, 128>(base + L::K + s * TILE, &tk, k_full(s), r, g, it.b);
+            ++ke;
+            if (u > 0 && !ptx::mbar_wait(v_empty(s), (u - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            ptx::mbar_arrive_expect_tx(v_full(s), TILE);
+            load_tile<DP, 128>(base + L::V + s * TILE, &tv, v_full(s), r, g, it.b);
+            ++ve;
+            if (j == 0 && it.n1 > 0) ok = load_q(it, 1);
           }
-          ptx::mbar_arrive_expect_tx(k_full(s), TILE);
-          load_tile<DP, 128>(base + L::K + s * TILE, &tk, k_full(s), r, g, it.b);
-          ++ke;
-          if (u > 0 && !ptx::mbar_wait(v_empty(s), (u - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          ptx::mbar_arrive_expect_tx(v_full(s), TILE);
-          load_tile<DP, 128>(base + L::V + s * TILE, &tv, v_full(s), r, g, it.b);
-          ++ve;
-          if (j == 0 && it.n1 > 0) ok = load_q(it, 1);
         }
+        if (!ok) wait_failed(11);
+        // every load issued has landed before the CTA may exit: the last entry of each
+        // stage, the last Q of each tile
+        bool dr = true;
+        for (uint32_t s = 0; s < ST; ++s) {
+          if (ke > s) dr = ptx::mbar_wait(k_full(s), ((ke - 1 - s) / ST) & 1) && dr;
+          if (ve > s) dr = ptx::mbar_wait(v_full(s), ((ve - 1 - s) / ST) & 1) && dr;
+        }
+        for (int t = 0; t < 2; ++t)
+          if (qn[t] > 0) dr = ptx::mbar_wait(q_full(t), (qn[t] - 1) & 1) && dr;
+        if (!dr) wait_failed(13);
       }
-      if (!ok) wait_failed(11);
-      // every load issued has landed before the CTA may exit: the last entry of each
-      // stage, the last Q of each tile
-      bool dr = true;
-      for (uint32_t s = 0; s < ST; ++s) {
-        if (ke > s) dr = ptx::mbar_wait(k_full(s), ((ke - 1 - s) / ST) & 1) && dr;
-        if (ve > s) dr = ptx::mbar_wait(v_full(s), ((ve - 1 - s) / ST) & 1) && dr;
-      }
-      for (int t = 0; t < 2; ++t)
-        if (qn[t] > 0) dr = ptx::mbar_wait(q_full(t), (qn[t] - 1) & 1) && dr;
-      if (!dr) wait_failed(13);
-    }
-  } else if (warp == 1) {
-    if (ptx::elect_one()) {
-      uint32_t qc0 = 0u, qc1 = 0u, pc0 = 0u, pc1 = 0u;  // Q loads and hand-overs of P consumed
-      // A ring entry is read by tile 0 first (it starts every item before tile 1 does
-      // and its blocks are no more), so tile 1's MMA releases it, or tile 0's where tile
-      // 1 does not read it (last).
-      auto issue_s = [&](int t, uint32_t e, bool last) {  // S_t = Q_t K_e^T
-        const uint32_t s = e % ST;
-        if (!ptx::mbar_wait(k_full(s), (e / ST) & 1)) return false;
-        ptx::tc_fence_after();
-        const uint32_t qt = base + L::Q + t * TILE, kt = base + L::K + s * TILE;
+    } else if (warp == 1) {
+      if (ptx::elect_one()) {
+        uint32_t qc0 = 0u, qc1 = 0u, pc0 = 0u, pc1 = 0u;  // Q loads and hand-overs of P consumed
+        // A ring entry is read by tile 0 first (it starts every item before tile 1 does
+        // and its blocks are no more), so tile 1's MMA releases it, or tile 0's where tile
+        // 1 does not read it (last).
+        auto issue_s = [&](int t, uint32_t e, bool last) {  // S_t = Q_t K_e^T
+          const uint32_t s = e % ST;
+          if (!ptx::mbar_wait(k_full(s), (e / ST) & 1)) return false;
+          ptx::tc_fence_after();
+          const uint32_t qt = base + L::Q + t * TILE, kt = base + L::K + s * TILE;
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          ptx::mma_bf16(tmem + 128u * t, kmajor_desc(qt, kk), kmajor_desc(kt, kk), IDESC_S, kk > 0);
-        ptx::mma_commit(s_full(t));
-        if (last) ptx::mma_commit(k_empty(s));
-        return true;
-      };
-      auto issue_pv = [&](int t, uint32_t e, int j, bool last) {  // O_t += P_t V_e
-        uint32_t& pc = t ? pc1 : pc0;
-        if (!ptx::mbar_wait(p_full(t), pc & 1)) return false;
-        ++pc;
-        const uint32_t s = e % ST;
-        if (!ptx::mbar_wait(v_full(s), (e / ST) & 1)) return false;
-        ptx::tc_fence_after();
-        const uint32_t vt = base + L::V + s * TILE;
+          for (int kk = 0; kk < DP / 16; ++kk)
+            ptx::mma_bf16(tmem + 128u * t, kmajor_desc(qt, kk), kmajor_desc(kt, kk), IDESC_S, kk > 0);
+          ptx::mma_commit(s_full(t));
+          if (last) ptx::mma_commit(k_empty(s));
+          return true;
+        };
+        auto issue_pv = [&](int t, uint32_t e, int j, bool last) {  // O_t += P_t V_e
+          uint32_t& pc = t ? pc1 : pc0;
+          const uint32_t s = e % ST;
+          if (!ptx::mbar_wait(v_full(s), (e / ST) & 1)) return false;
+          const uint32_t vt = base + L::V + s * TILE;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_bf16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * kk, mnmajor_desc(vt, kk), IDESC_PV,
-                           (j > 0 || kk > 0) ? 1u : 0u);
-        if (last) ptx::mma_commit(v_empty(s));
-        return true;
-      };
-      // S_t(0) of an item whose block 0 is at ring entry e0 (nothing for an empty tile)
-      auto start_tile = [&](const Item& it, int t, uint32_t e0) {
-        const int n = t ? it.n1 : it.n0;
-        if (n == 0) return true;
-        uint32_t& qc = t ? qc1 : qc0;
-        if (!ptx::mbar_wait(q_full(t), qc & 1)) return false;
-        ++qc;
-        if (!issue_s(t, e0, t == 1 || it.n1 == 0)) return false;
-        if (n == 1) ptx::mma_commit(q_empty(t));  // the tile's last S of the item
-        return true;
-      };
-      int k = 0, i = persistent_item(0, cta, G);
-      uint32_t kb = 0;  // ring entry of the item's block 0
-      Item it{};
-      if (i < p.items) {
-        it = item_at(p, order, i);
-        ok = start_tile(it, 0, 0u) && start_tile(it, 1, 0u);
-      }
-      while (ok && i < p.items) {
-        const int nmax = max(it.n0, it.n1);
-        const int inext = persistent_item(k + 1, cta, G);
-        const bool has_next = inext < p.items;
-        Item nx{};
-        if (has_next) nx = item_at(p, order, inext);
-        const uint32_t kb_next = kb + (uint32_t)nmax;
-        bool started0 = !has_next, started1 = !has_next;  // the next item's tiles
-        for (int j = 0; j < nmax && ok; ++j) {
-          bool done0 = false, done1 = false;  // the tile's last PV of the item issued in this round
+          for (int half = 0; half < 2; ++half) {
+            if (!ptx::mbar_wait(p_full(t, half), pc & 1)) return false;
+            ptx::tc_fence_after();
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int n = t ? it.n1 : it.n0;
-            if (!ok || j >= n) continue;
-            ok = issue_pv(t, kb + j, j, t == 1 || it.n1 <= j);
-            if (!ok) break;
-            if (j + 1 < n) {
-              ok = issue_s(t, kb + j + 1, t == 1 || it.n1 <= j + 1);
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              ptx::mma_bf16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * kk, mnmajor_desc(vt, kk), IDESC_PV,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          ++pc;
+          if (last) ptx::mma_commit(v_empty(s));
+          return true;
+        };
+        // S_t(0) of an item whose block 0 is at ring entry e0 (nothing for an empty tile)
+        auto start_tile = [&](const Item& it, int t, uint32_t e0) {
+          const int n = t ? it.n1 : it.n0;
+          if (n == 0) return true;
+          uint32_t& qc = t ? qc1 : qc0;
+          if (!ptx::mbar_wait(q_full(t), qc & 1)) return false;
+          ++qc;
+          if (!issue_s(t, e0, t == 1 || it.n1 == 0)) return false;
+          if (n == 1) ptx::mma_commit(q_empty(t));  // the tile's last S of the item
+          return true;
+        };
+        int k = 0, i = persistent_item(0, cta, G);
+        uint32_t kb = 0;  // ring entry of the item's block 0
+        Item it{};
+        if (i < p.items) {
+          it = item_at(p, order, i);
+          ok = start_tile(it, 0, 0u) && start_tile(it, 1, 0u);
+        }
+        while (ok && i < p.items) {
+          const int nmax = max(it.n0, it.n1);
+          const int inext = persistent_item(k + 1, cta, G);
+          const bool has_next = inext < p.items;
+          Item nx{};
+          if (has_next) nx = item_at(p, order, inext);
+          const uint32_t kb_next = kb + (uint32_t)nmax;
+          bool started0 = !has_next, started1 = !has_next;  // the next item's tiles
+          for (int j = 0; j < nmax && ok; ++j) {
+            bool done0 = false, done1 = false;  // the tile's last PV of the item issued in this round
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int n = t ? it.n1 : it.n0;
+              if (!ok || j >= n) continue;
+              ok = issue_pv(t, kb + j, j, t == 1 || it.n1 <= j);
               if (!ok) break;
-              if (j + 2 == n) ptx::mma_commit(q_empty(t));  // the tile's last S of the item
-            } else {
-              ptx::mma_commit(o_full(t));  // the tile's last PV of the item
-              if (t) done1 = true; else done0 = true;
+              if (j + 1 < n) {
+                ok = issue_s(t, kb + j + 1, t == 1 || it.n1 <= j + 1);
+                if (!ok) break;
+                if (j + 2 == n) ptx::mma_commit(q_empty(t));  // the tile's last S of the item
+              } else {
+                ptx::mma_commit(o_full(t));  // the tile's last PV of the item
+                if (t) done1 = true; else done0 = true;
+              }
+            }
+            // a tile whose item ended in this round starts the next one, tile 0 first
+            if (ok && !started0 && (done0 || done1)) {
+              ok = start_tile(nx, 0, kb_next);
+              started0 = true;
+            }
+            if (ok && !started1 && done1) {
+              ok = start_tile(nx, 1, kb_next);
+              started1 = true;
             }
           }
-          // a tile whose item ended in this round starts the next one, tile 0 first
-          if (ok && !started0 && (done0 || done1)) {
-            ok = start_tile(nx, 0, kb_next);
-            started0 = true;
-          }
-          if (ok && !started1 && done1) {
-            ok = start_tile(nx, 1, kb_next);
-            started1 = true;
-          }
+          if (ok && !started0) ok = start_tile(nx, 0, kb_next);
+          if (ok && !started1) ok = start_tile(nx, 1, kb_next);
+          kb = kb_next;
+          it = nx;
+          i = inext;
+          ++k;
         }
-        if (ok && !started0) ok = start_tile(nx, 0, kb_next);
-        if (ok && !started1) ok = start_tile(nx, 1, kb_next);
-        kb = kb_next;
-        it = nx;
-        i = inext;
-        ++k;
-      }
-      if (!ok) wait_failed(14);
-      ptx::mma_commit(bar_drain);  // completes once every MMA issued above has
-      if (!ptx::mbar_wait(bar_drain, 0)) {
-        ok = false;
-        wait_failed(18);
+        if (!ok) wait_failed(14);
+        ptx::mma_commit(bar_drain);  // completes once every MMA issued above has
+        if (!ptx::mbar_wait(bar_drain, 0)) {
+          ok = false;
+          wait_failed(18);
+        }
       }
     }
   } else {
-    const int t = (warp - 2) >> 2, qq = warp & 3;
+    more_registers<REGS_SOFTMAX>();
+    const int t = (warp - 4) >> 2, qq = warp & 3;
     const int row = qq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(qq * 32) << 16;
     const uint32_t t_s = tmem + 128u * t + lane_off, t_o = tmem + 256u + 128u * t + lane_off;
@@ -394,27 +404,6 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             m_ref = m_new;
           }
         }
-        // P = 2^(s - m_ref): scale and shift in one fp32x2 FMA per pair, the row sum in
-        // four fp32x2 accumulators; the packed word of keys (2c, 2c + 1) goes to sv[c]
-        // (no visible key so far: every weight 0, but a NaN stays one)
-        const uint64_t sc2 = f2_splat(mul), nm2 = f2_splat(m_ref == -INFINITY ? -INFINITY : add - m_ref);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const uint64_t x = f2_fma(f2_pack(sv[2 * c], sv[2 * c + 1]), sc2, nm2);
-          const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
-          acc[c % 4] = f2_add(acc[c % 4], f2_pack(p0, p1));
-          sv[c] = __uint_as_float(pack2(p0, p1));
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t w[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(sv[32 * half + c]);
-          ptx::tmem_st32_nowait(t_s + 32u * half, w);
-        }
-        const uint64_t acc2 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
-        const float rs = f2_lo(acc2) + f2_hi(acc2);
         if (rescale) {
 #pragma unroll 1
           for (int c0 = 0; c0 < DP; c0 += 32) {
@@ -446,11 +435,31 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
           ptx::fence_async_smem();
           __syncwarp();
         }
-        ptx::tmem_wait_st();
+        // P = 2^(s - m_ref): scale and shift in one fp32x2 FMA per pair, the row sum in
+        // four fp32x2 accumulators; handed over 64 keys at a time
+        // (no visible key so far: every weight 0, but a NaN stays one)
+        const uint64_t sc2 = f2_splat(mul), nm2 = f2_splat(m_ref == -INFINITY ? -INFINITY : add - m_ref);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int at = 64 * half + 2 * c;
+            const uint64_t x = f2_fma(f2_pack(sv[at], sv[at + 1]), sc2, nm2);
+            const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
+            acc[c % 4] = f2_add(acc[c % 4], f2_pack(p0, p1));
+            w[c] = pack2(p0, p1);
+          }
+          ptx::tmem_st32_nowait(t_s + 32u * half, w);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(p_full(t, half));
+        }
+        const uint64_t acc2 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
+        const float rs = f2_lo(acc2) + f2_hi(acc2);
         l += rs;
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(p_full(t));
       }
       kb += (uint32_t)max(it.n0, it.n1);
       if (!ok) break;
@@ -490,7 +499,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       // O rows through this warp's 4 KB of shared memory, 64 columns at a time: lane r
       // writes its row's 128 bytes as eight 16-byte chunks (chunk c at c ^ (r & 7), so
       // that eight lanes cover all banks), then a store writes 4 rows x 128 bytes
-      uint8_t* stg = gbase + L::EPI + (warp - 2) * 4096;
+      uint8_t* stg = gbase + L::EPI + (warp - 4) * 4096;
       const int rw0 = it.q0 + 128 * t + qq * 32;  // the warp's first query
       __nv_bfloat16* ow = static_cast<__nv_bfloat16*>(a.o) + it.b * a.so.b + it.h * a.so.h + rw0 * a.so.s;
 #pragma unroll
@@ -532,6 +541,9 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
   OASES_TRY(map4d(&tv, a.v, a.sv, a.D, a.Sk, a.G, a.B, 128));
   static DeviceOnce attr;
   OASES_TRY(attr.run([] {
+    cudaFuncAttributes at;
+    OASES_TRY(cudaFuncGetAttributes(&at, xattn_fwd_kernel<DP, BIAS>));
+    if (at.numRegs != REGS) return cudaErrorInvalidKernelImage;  // (the warpgroups' shares would not add up)
     return cudaFuncSetAttribute(xattn_fwd_kernel<DP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 Smem<DP>::BYTES);
   }));

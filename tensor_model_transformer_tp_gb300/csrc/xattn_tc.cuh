@@ -60,6 +60,16 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const void* tmap, uint32
   for (int c = 0; c < DP / 64; ++c) tma_load_4d(dst + c * ROWS * 128, tmap, bar, 64 * c, row, head, batch);
 }
 
+// Registers of a warpgroup's threads, given up or taken over from those that gave up theirs.
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Item k of CTA c (of G) in a persistent kernel whose items are numbered heaviest
 // first: rounds of G items, in snake order.
 __device__ __forceinline__ int persistent_item(int k, int c, int G) {
