@@ -41,9 +41,10 @@ __device__ int g_xattn_fwd_error;
 namespace {
 using namespace xattn;
 
-// Registers move from the first warpgroup to the softmax warps: 128 x 72 + 256 x 216 =
-// 384 x 168, what a block starts with.
-constexpr int NT = 384, REGS = 168, REGS_ISSUE = 72, REGS_SOFTMAX = 216;
+// Registers move from the first warpgroup to the softmax warps: 128 x 120 + 256 x 192 =
+// 384 x 168, what a block starts with.  (The thread that issues the MMAs is on every block's
+// path: 72 registers make it spill, 226 against 206 us at 8 x 2048, 19 heads of 128.)
+constexpr int NT = 384, REGS = 168, REGS_ISSUE = 120, REGS_SOFTMAX = 192;
 static_assert(128 * REGS_ISSUE + 256 * REGS_SOFTMAX == NT * REGS, "registers of the warpgroups");
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, false, false);
