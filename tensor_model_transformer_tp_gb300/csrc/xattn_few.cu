@@ -329,12 +329,13 @@ int cluster_size(const Args& a) {
 bool xattn_few_takes(const Args& a) {
   return (int64_t)a.Sq * a.share <= 4 && (int64_t)a.B * a.G <= 65535;
 }
-// Shares of the keys beyond the cluster's: two CTAs an SM, and 512 keys to a CTA at least.
+// Shares of the keys beyond the cluster's: two CTAs an SM, and 256 keys to a CTA at least
+// (4 sequences of up to 8192 keys, 8 heads on 2 of 128: 24 us, 30 with 512).
 int xattn_few_splits(const Args& a) {
   const int c = cluster_size(a);
   const int64_t ctas = (int64_t)a.B * a.G * c, places = 2 * sm_count();
   if (c < MAX_CLUSTER || ctas >= places) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(places / ctas, a.Sk / (512 * c)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(places / ctas, a.Sk / (256 * c)));
 }
 cudaError_t xattn_few(const Args& a, const void* table, const Borders& border, bool bidirectional,
                       cudaStream_t st) {
