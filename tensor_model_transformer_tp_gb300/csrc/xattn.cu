@@ -139,6 +139,7 @@ oases_status shape(const oases_attn_desc* d, bool backward, Shape* s) {
 // ---- the bias by distance ---------------------------------------------------------
 // value[h][n + R + PAD] = factor * table[bucket(n)][h], and the run of distances of
 // each bucket, and the bucket of each n.  A finite value stays finite behind the factor.
+// (The heads along the grid's first dimension: the second ends at 65535.)
 template <typename T>
 __global__ void __launch_bounds__(256)
 xattn_bias_kernel(const T* table, float* value, int2* range, uint8_t* index, const __grid_constant__ Borders border,
@@ -157,7 +158,7 @@ xattn_bias_kernel(const T* table, float* value, int2* range, uint8_t* index, con
       r = make_int2(-last, !bidirectional && u == 0 ? FAR : -first);
     range[threadIdx.x] = r;
   }
-  const int h = blockIdx.y, i = blockIdx.x * blockDim.x + threadIdx.x;
+  const int h = blockIdx.x, i = blockIdx.y * blockDim.x + threadIdx.x;
   if (i >= pitch) return;
   const int n = i - (R + BIAS_PAD);
   const int x = bidirectional ? abs(n) : max(-n, 0);
@@ -304,7 +305,7 @@ cudaError_t bias_tables(const Shape& s, const void* table, char* ws, const Layou
   out->range = range;
   uint8_t* index = reinterpret_cast<uint8_t*>(ws + l.index);
   out->index = index;
-  const dim3 grid((b.pitch + 255) / 256, s.a.H);
+  const dim3 grid(s.a.H, (b.pitch + 255) / 256);
   if (s.a.t == DType::F32)
     return launch_pdl(xattn_bias_kernel<float>, grid, dim3(256), 0, st, (const float*)table, value, range, index,
                       s.border, s.a.H, b.pitch, s.R, b.buckets, (int)s.bidirectional, factor);
