@@ -21,8 +21,9 @@
 // delta.  From the rounded o it is off by up to 2^-8 of |dO||o|, which shows in rows of few
 // keys (o as large as v) and in the bias's gradient (a row's error, summed over its keys).
 // Its definition is sum P dP, and what dS sums to over a row is the difference: the dq
-// kernel takes it from its first block where a row has no other, and corrects delta for
-// the dkv kernel there and wherever there is a bias.
+// kernel takes it from the first block of keys for the rows that see no other (an item of
+// queries that begins behind a cache may hold such rows beside others), and corrects delta
+// for the dkv kernel there and wherever there is a bias.
 //
 // The bias's gradient (dkv kernel).  A warp's 32 x 32 scores that lie R or more from the
 // diagonal on one side belong to one bucket: every thread adds its own.  Nearer ones are
@@ -191,6 +192,7 @@ struct DqSmem {
 struct DqItem {
   int h, b, q0, p0, len;   // head, sequence, first query and its position, keys
   int j0, n, whole;        // key blocks: the first, how many, and how many without the cut
+  bool few;                // some query sees the first block's keys and no others
   float* part;             // a piece's sums: dQ [128][D], then the rows' sums of dS
 };
 // The bytes of a piece of dq are 4 dq_piece(D).
@@ -208,6 +210,7 @@ __device__ __forceinline__ DqItem dq_item(const Plan& p, const Order* o, const W
   const int vis = a.causal ? min(it.len, max(0, it.p0 + rows)) : it.len;
   int end;
   it.whole = (vis + 127) / 128;
+  it.few = it.whole == 1 || (it.whole > 1 && a.causal && it.p0 < 128);
   cut_blocks(p, w.piece, it.whole, &it.j0, &end);
   it.n = end - it.j0;
   it.part = w.piece < 0 ? nullptr : p.part + w.part * dq_piece(a.D);
@@ -460,6 +463,9 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
       float off = 0.f;  // the row's sum of dS: how far delta is from sum P dP
       stats(k + 1, nl_next, nd_next);
       const int w0 = it.p0 + qq * 32;  // position of the warp's first query
+      // the row's keys (none past the queries), and whether they all stand in the first block
+      const int seen = valid_q ? (a.causal ? min(w0 + lane + 1, it.len) : it.len) : 0;
+      const bool few_row = it.few && seen <= 128;
       float left = 0.f, right = 0.f;
       if (BIAS) {
         left = *a.bias.at(it.h, -a.bias.R);
@@ -509,9 +515,8 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         uint32_t pk[16];  // dS as packed bf16 pairs (keys 2i, 2i+1 of these 32)
         // keys kb + c with c >= nvis are past the diagonal or the sequence's keys (all of
         // them for a row past the queries); what dP holds there may be anything
-        const int seen = valid_q ? (a.causal ? min(w0 + lane + 1, it.len) : it.len) : 0;
         int nvis = seen - kb;
-        if (it.whole == 1) {
+        if (it.few && it.j0 + j == 0) {
           float x = 0.f, sum = 0.f;
 #pragma unroll
           for (int c = 0; c < 32; ++c) x += c < nvis ? v[c] * w[c] : 0.f;
@@ -520,11 +525,13 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             if (lane == 0) wait_failed(113);
             break;
           }
-          off = sum + nd;
-          nd = -sum;
+          if (few_row) {
+            off = sum + nd;
+            nd = -sum;
+          }
           if (seen == 1) nvis = 0;  // one key, of weight 1: no gradient, not a rounding's
         }
-        if (full && it.whole > 1) {
+        if (full && !it.few) {
           const uint64_t nd2 = f2_splat(nd);
           uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
@@ -543,7 +550,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const float x = 2 * i < nvis ? v[2 * i] * (w[2 * i] + nd) : 0.f;
             const float y = 2 * i + 1 < nvis ? v[2 * i + 1] * (w[2 * i + 1] + nd) : 0.f;
             pk[i] = pack2(x, y);
-            if (BIAS && it.whole > 1) off += x + y;
+            if (BIAS && !few_row) off += x + y;
           }
         }
         ptx::tmem_st16_nowait(own, pk);
@@ -569,9 +576,10 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
       }
       if (!ok) break;
       // what follows takes delta as sum P dP
-      if (it.whole == 1 || BIAS) {
-        if (it.whole > 1) {
-          const float x = off;
+      if (it.few || BIAS) {
+        if (BIAS && it.whole > 1) {
+          // (a row of few keys has its whole sum in every column group)
+          const float x = few_row && sub > 0 ? 0.f : off;
           if (!row_sum(x, off)) {
             ok = false;
             if (lane == 0) wait_failed(114);
@@ -581,7 +589,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         if (it.part) {
           if (sub == 0) it.part[128 * a.D + row] = it.n > 0 ? off : 0.f;
         } else if (sub == 0 && it.n > 0) {
-          a.delta[((int64_t)it.b * a.H + it.h) * a.q_pitch + it.q0 + row] = it.whole == 1 ? nd : nd - off;
+          a.delta[((int64_t)it.b * a.H + it.h) * a.q_pitch + it.q0 + row] = few_row ? nd : nd - off;
         }
       }
       float v[32];
@@ -1242,7 +1250,7 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 
 // ---- pieces joined ------------------------------------------------------------------------
 // A cut item's 32 rows a CTA, 8 lanes a row: dq, and -delta of rows whose sums of dS were
-// taken (a block of keys in all, or `sums`).
+// taken (of the first block's keys alone, or `sums`).
 __global__ void __launch_bounds__(256)
 xattn_dq_join_kernel(const __grid_constant__ Plan p, int sums) {
   pdl_wait();
@@ -1267,7 +1275,7 @@ xattn_dq_join_kernel(const __grid_constant__ Plan p, int sums) {
     }
     *reinterpret_cast<uint2*>(out + c) = make_uint2(pack2(s.x * a.scale, s.y * a.scale), pack2(s.z * a.scale, s.w * a.scale));
   }
-  if (lane == 0 && (sums || it.whole == 1)) {
+  if (lane == 0 && (sums || it.few)) {
     float off = 0.f;
     for (int q = 0; q < p.cut.pieces; ++q) off += it.part[q * step + 128 * a.D + row];
     a.delta[((int64_t)it.b * a.H + it.h) * a.q_pitch + qi] -= off;

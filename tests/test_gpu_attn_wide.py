@@ -2,10 +2,12 @@
 beside those of test_gpu_attn.py, whose definition and bounds these tests use."""
 import copy
 
+import numpy as np
 import pytest
 import torch
 
 import tensor_model_transformer_tp_gb300 as oz
+from oracle.xattn import bucket_map
 from test_gpu_attn import Case
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +42,38 @@ def test_more_heads_with_a_bias_than_a_grid_is_wide(dtype, Sq):
     for first, end in ((0, 8), (32760, 32776), (65528, 65544), (H - 8, H)):
         heads_of(c, first, end).check(o[:, :, first:end], lse[:, first:end],
                                       [x[:, :, first:end] for x in (dq, dk, dv)] + [db[:, first:end]])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("Sq,Sk,start", [(200, 201, 1), (150, 250, [100, 1, 50]), (128, 1100, [100, 127, 64]),
+                                         (300, 200, [-100, -1, -257])])
+def test_delta_of_few_keys_behind_a_start(Sq, Sk, start, biased, D):
+    """Queries that see 128 keys or less beside others, of the same tile, that see more.  Their
+    values of v are 1 + noise / 16, so that delta from the rounded o would be off by up to
+    u |dO| sqrt(D) where dP - delta is |dO| sqrt(D) / 16 in size: 0.0625 / sqrt(3) of dS, nine
+    times what may remain.  That is the rounding of dS and of dq (of dk), half a step each: the norm
+    of the error is at most 2 u of the gradient's.  The other queries have no dO."""
+    B = 3
+    c = Case("bf16", B, Sq, Sk, 4, 2, D, causal=True, start=start if isinstance(start, list) else [start] * B,
+             buckets=16 if biased else 0, far=100)
+    c.v.mul_(1 / 16).add_(1.0)
+    seen = torch.tensor(c.start, device="cuda")[:, None] + torch.arange(1, Sq + 1, device="cuda")    # [B, Sq]
+    c.do[seen > 128] = 0.0
+    o, lse = c.forward()
+    dq, dk, dv, db = c.backward(o, lse)
+    oz.oases_check_device(torch.cuda.current_stream())
+    wide = {n: getattr(c, n).double().requires_grad_(True) for n in ["q", "k", "v"] + ["bias"] * biased}
+    k, v = (wide[n].repeat_interleave(2, dim=2) for n in "kv")
+    s = torch.einsum("bihd,bjhd->bhij", wide["q"], k) * c.scale
+    if biased:
+        at = torch.tensor(np.stack([bucket_map(Sq, Sk, p, 16, 100, False) for p in c.start]), device="cuda")
+        s = s + wide["bias"][at].permute(0, 3, 1, 2)
+    hide = (torch.arange(Sk, device="cuda")[None, None] >= seen[:, :, None])[:, None]
+    none = hide.all(-1, keepdim=True)
+    P = torch.softmax(s.masked_fill(hide, float("-inf")).masked_fill(none, 0.0), -1).masked_fill(none, 0.0)
+    want = torch.autograd.grad(torch.einsum("bhij,bjhd->bihd", P, v), list(wide.values()), c.do.double())
+    u = 2.0 ** -8
+    got = [dq, dk, dv] + [db] * biased
+    for name, x, w, most in zip(("dq", "dk", "dv", "dbias"), got, want, (2 * u, 2 * u, 2 * u, u)):
+        assert (x.double() - w).norm() <= most * w.norm() * 1.05, name
