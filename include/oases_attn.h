@@ -18,10 +18,10 @@
  *
  * A query that sees no key (kv_lens[b] = 0, or a bias of -infinity on all of
  * them) has o = 0 and lse = -infinity, and gives no gradient.  Nor does one whose
- * lse lies below -2^20 (a finite bias that hides all of its keys): from there on an
- * fp32 lse no longer tells their weights.  One that sees a single key has dS = 0.  What stands in k
- * and v at and behind kv_lens[b] is not used, whatever it holds; dk and dv are 0
- * there.  kv_lens values outside [0, k_len] are taken as the nearest in it.
+ * lse lies below -2^20 (a finite bias that hides all of its keys) or above 2^24: there
+ * an fp32 lse no longer tells their weights.  One that sees a single key has dS = 0.
+ * What stands in k and v at and behind kv_lens[b] is not used, whatever it holds; dk and
+ * dv are 0 there.  kv_lens values outside [0, k_len] are taken as the nearest in it.
  *
  * Buckets.  n = j - p_i, the key's position relative to the query's.  With
  * bidirectional set, N = buckets / 2 buckets serve each sign (those of n > 0 are

@@ -52,9 +52,11 @@ struct Bias {
 // bias's gradient.
 constexpr int DKV_WARPS = 16;
 
-// A query whose lse lies below this gives no gradient: none of its keys counts (lse =
-// -infinity), or all of its scores lie where fp32 no longer tells weights apart.
-constexpr float LSE_LOWEST = -1048576.f;
+// A query whose lse lies below -2^20 gives no gradient: none of its keys counts (lse =
+// -infinity), or all of its scores lie where fp32 no longer tells weights apart.  Nor does
+// one whose lse lies above 2^24, where the roundings of s and of lse, in base 2 some 2.7
+// together, make anything of e^(s - lse), infinity too.  (A NaN stays one.)
+__device__ __forceinline__ bool beyond_weights(float lse) { return lse < -1048576.f || lse > 16777216.f; }
 
 struct Args {
   const void *q, *k, *v;

@@ -61,7 +61,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
 }
 // A row's -lse in base 2, so that its weights are 2^(s - lse); a query without keys: every
 // weight 0.
-__device__ __forceinline__ float minus_lse2(float lse) { return lse < LSE_LOWEST ? -INFINITY : -lse * LOG2E; }
+__device__ __forceinline__ float minus_lse2(float lse) { return beyond_weights(lse) ? -INFINITY : -lse * LOG2E; }
 
 struct Plan {
   Args a;

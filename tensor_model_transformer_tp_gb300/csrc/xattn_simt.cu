@@ -287,7 +287,7 @@ xattn_dq_simt_kernel(const __grid_constant__ Args a, int tiles, int splits) {
       const bool valid = q0 + r < a.Sq;
       if (valid && sp == 0) a.delta[a.stat(b, h, q0 + r)] = d;
       const float l = valid ? a.lse[a.stat(b, h, q0 + r)] : INFINITY;
-      lse[r] = l < LSE_LOWEST ? INFINITY : l;  // a row without keys: every weight 0
+      lse[r] = beyond_weights(l) ? INFINITY : l;  // a row without keys: every weight 0
     }
   }
   __syncthreads();
@@ -399,7 +399,7 @@ xattn_dkv_simt_kernel(const __grid_constant__ Args a, int tiles, int splits) {
       if (threadIdx.x < TB) {
         const int qi = i * TB + threadIdx.x;
         const float l = qi < a.Sq ? a.lse[a.stat(b, h, qi)] : INFINITY;
-        lse[at][threadIdx.x] = l < LSE_LOWEST ? INFINITY : l;
+        lse[at][threadIdx.x] = beyond_weights(l) ? INFINITY : l;
         delta[at][threadIdx.x] = qi < a.Sq ? a.delta[a.stat(b, h, qi)] : 0.f;
       }
     }

@@ -77,3 +77,21 @@ def test_delta_of_few_keys_behind_a_start(Sq, Sk, start, biased, D):
     got = [dq, dk, dv] + [db] * biased
     for name, x, w, most in zip(("dq", "dk", "dv", "dbias"), got, want, (2 * u, 2 * u, 2 * u, u)):
         assert (x.double() - w).norm() <= most * w.norm() * 1.05, name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [3e7, 1e9, 1e30, "max"])
+def test_scores_above_what_weights_resolve_give_no_gradient(dtype, value):
+    """As those far below: from a bias that lifts every key of head 1 comes no gradient, and
+    none of it infinite; the output is that without a bias, and head 0's has its own."""
+    c = Case(dtype, 1, 150, 150, 2, 2, 64, buckets=32)
+    c.bias[:, 1] = 0.0
+    plain, _ = c.forward()
+    c.bias[:, 1] = torch.finfo(c.bias.dtype).max if value == "max" else value
+    o, lse = c.forward()
+    dq, dk, dv, db = c.backward(o, lse)
+    assert all(torch.isfinite(x).all() for x in (o, lse, dq, dk, dv, db))
+    assert torch.equal(o[:, :, 0], plain[:, :, 0])
+    for x in (dq[:, :, 1], dk[:, :, 1], dv[:, :, 1], db[:, 1]):
+        assert not x.any()
+    assert dq[:, :, 0].any() and dv[:, :, 0].any() and db[:, 0].any()
