@@ -427,13 +427,27 @@ def _out(x: Optional[torch.Tensor], given: Optional[torch.Tensor]):
         if given is None and x is not None else given
 
 
+def _whole(name: str, v) -> int:
+    if isinstance(v, int):
+        return int(v)
+    try:
+        n = int(v)
+    except (TypeError, OverflowError, ValueError):
+        n = None
+    _need(n is not None and n == v, "%s must be a whole number, got %r" % (name, v))
+    return n
+
+
 def _start(q_start):
     """(the tensor or None, the number)"""
-    return (q_start, 0) if isinstance(q_start, torch.Tensor) else (None, int(q_start or 0))
+    if q_start is None:
+        return None, 0
+    return (q_start, 0) if isinstance(q_start, torch.Tensor) else (None, _whole("q_start", q_start))
 
 
 def _options(causal, start, scale, max_distance, bidirectional):
-    return (bool(causal), start, None if scale is None else float(scale), int(max_distance),
+    return (bool(causal), start, None if scale is None else float(scale),
+            _whole("max_distance", max_distance),
             not causal if bidirectional is None else bool(bidirectional))
 
 
