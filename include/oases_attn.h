@@ -20,8 +20,11 @@
  * them) has o = 0 and lse = -infinity, and gives no gradient.  Nor does one whose
  * lse lies below -2^20 (a finite bias that hides all of its keys) or above 2^24: there
  * an fp32 lse no longer tells their weights.  One that sees a single key has dS = 0.
- * What stands in k and v at and behind kv_lens[b] is not used, whatever it holds; dk and
- * dv are 0 there.  kv_lens values outside [0, k_len] are taken as the nearest in it.
+ * What stands in k and v at and behind kv_lens[b], and causal at and behind p_q_len (keys
+ * that no query of the sequence sees), is not used, whatever it holds; dk and dv are 0
+ * there.  Nearer ones are to be finite, also where a query does not see them: its weight 0
+ * times an infinity is a NaN; and so is d_o of the queries without keys.  kv_lens values
+ * outside [0, k_len] are taken as the nearest in it, q_start values within 2^28 of 0.
  *
  * Buckets.  n = j - p_i, the key's position relative to the query's.  With
  * bidirectional set, N = buckets / 2 buckets serve each sign (those of n > 0 are

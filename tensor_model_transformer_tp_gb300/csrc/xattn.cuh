@@ -81,12 +81,15 @@ struct Args {
   float* part_o;     // [splits][batch][q_len][heads][D], normalised
   float* part_lse;   // [splits][batch][heads][q_len]
 
-  // visible keys before causality, and the first query's position, of sequence b
-  __device__ __forceinline__ int len(int b) const {
-    return kv_lens ? max(0, min(Sk, kv_lens[b])) : Sk;
-  }
+  // the first query's position of sequence b, and how many keys any of its queries sees: a
+  // causal call over a cache leaves what stands behind its last query alone (0 times a NaN
+  // there would be one)
   __device__ __forceinline__ int start(int b) const {
     return q_start ? max(-(1 << 28), min(1 << 28, q_start[b])) : q_start0;
+  }
+  __device__ __forceinline__ int len(int b) const {
+    const int n = kv_lens ? max(0, min(Sk, kv_lens[b])) : Sk;
+    return causal ? max(0, min(n, start(b) + Sq)) : n;
   }
   __device__ __forceinline__ int64_t stat(int b, int h, int i) const {
     return ((int64_t)b * H + h) * Sq + i;

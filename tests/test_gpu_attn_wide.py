@@ -95,3 +95,26 @@ def test_scores_above_what_weights_resolve_give_no_gradient(dtype, value):
     for x in (dq[:, :, 1], dk[:, :, 1], dv[:, :, 1], db[:, 1]):
         assert not x.any()
     assert dq[:, :, 0].any() and dv[:, :, 0].any() and db[:, 0].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Sq,H,D", [(1, 2, 64), (1, 8, 64), (5, 1, 128), (40, 2, 64), (150, 2, 128), (300, 1, 40)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_whatever_stands_behind_the_last_query(dtype, Sq, H, D, biased):
+    """Causal over a cache that is not full, no kv_lens: NaN and infinities behind a sequence's
+    last query, where none sees them, change nothing."""
+    start = [0, 37, 120, -Sq, 500 - Sq]
+    c = Case(dtype, 5, Sq, 500, H, 1, D, causal=True, start=start, buckets=32 if biased else 0, packed=False)
+    for b, p in enumerate(start):
+        c.k[b, p + Sq:] = 0.0
+        c.v[b, p + Sq:] = 0.0
+    o, lse = c.forward()
+    first = (o, lse, *c.backward(o, lse))
+    c.check(o, lse, first[2:])
+    for b, p in enumerate(start):
+        c.k[b, p + Sq:] = float("nan")
+        c.v[b, p + Sq:] = float("inf")
+        c.v[b, p + Sq + 3:] = float("nan")
+    o, lse = c.forward()
+    for x, y in zip(first, (o, lse, *c.backward(o, lse))):
+        assert x is y is None or torch.equal(x, y)
