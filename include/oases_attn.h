@@ -32,7 +32,7 @@
  * For a = |n| and E = N / 2 (rounded down):
  *   bucket = a                                                            a < E
  *   bucket = min(N - 1, E + floor((N - E) log(a / E) / log(max_distance / E)))  else
- * The floor is that of the real number: borders are found in whole arithmetic.
+ * The floor is that of the real number, also where it is whole (not of a rounded logarithm).
  *
  * Layout.  q, o, d_o, dq [batch, q_len, heads, head_dim] and k, v, dk, dv
  * [batch, k_len, kv_heads, head_dim], a head's values side by side and the other

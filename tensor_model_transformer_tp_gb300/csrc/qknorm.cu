@@ -14,7 +14,7 @@
 //           values of its first half and their four partners,
 //   LOADS   rot / 2 values on, otherwise: loaded again, one by one.
 // Arithmetic goes two values at a time.  8192 tokens of 20 + 20 heads of 128, forward and
-// backward (420 MB): 98 us; with the partners' words shuffled from other lanes, values one
+// backward (420 MB): 88 us; with the partners' words shuffled from other lanes, values one
 // by one and IEEE roots and quotients, which issuing bound, 121.  (Persistent warps with
 // the loads ahead in shared memory read as much at once with fewer warps, and took 98.)
 #include <cuda_runtime.h>
@@ -266,7 +266,10 @@ __device__ __forceinline__ Unit unit_of(const QkArgs& a, int64_t u, int heads_pe
 }
 
 // rows of one lane in flight: what the registers hold
-// (20 heads of 128 are two batches of 5 rows; three of 4 took 104 us, forward and backward)
+// (20 heads of 128 are two batches of 5 rows; three of 4 took 104 us, forward and backward,
+// against 90.  Of other counts some rows are empty: from a cold L2, 8192 tokens, the forward and
+// the backward of 20 + 20 heads read and write at 4.2 and 4.0 TB/s, of 16 + 16 at 3.7 and 3.6,
+// of 32 + 32 at 4.6 and 4.4, of 32 + 8 at 3.3 and 3.0)
 constexpr int rows_in_flight(bool bwd, bool f32, Partner p) {
   return p == Partner::LOADS || (bwd && f32) ? 2 : f32 ? 4 : 5;
 }

@@ -294,7 +294,7 @@ Layout layout(const Shape& s, bool backward) {
       if (c.q_shares > 1) take(&l.piece_dq, (size_t)c.q_shares * a.B * a.Sq * a.H * a.D * 4);
       if (c.kv_shares > 1) take(&l.piece_dkv, (size_t)c.kv_shares * 2 * a.B * a.Sk * a.G * a.D * 4);
       l.rows = (int64_t)a.B * ((a.Sq + c.q_rows - 1) / c.q_rows) * c.q_shares;
-    } else if ( xattn_bwd_cut(a, &cut)) {  // (else the call itself refuses)
+    } else if (xattn_bwd_cut(a, &cut)) {  // (else the call itself refuses)
       if (cut.dq.pieces > 1) take(&l.piece_dq, (size_t)cut.dq.rest * cut.dq.pieces * xattn_dq_piece_bytes(a.D));
       if (cut.dkv.pieces > 1) take(&l.piece_dkv, (size_t)cut.dkv.rest * cut.dkv.pieces * 2 * 128 * a.D * 4);
       const int64_t tiles = (int64_t)a.B * ((a.Sk + 127) / 128);  // as kv_item() counts them

@@ -828,8 +828,8 @@ struct KvBias {
 // DP = 128: the accumulators leave room for 64 queries a block: S^T of buffer b at 128 b ..,
 // dP^T at + 64 .., dV 256.., dK 384..; P^T over S^T, dS^T over dP^T.  Two groups of 8 warps
 // take a buffer each, so that one works while the other waits for its block (all 16 on every
-// block, 16 columns each, waited on every barrier twice as often: 629 us against 497 at 8
-// sequences of 2048, 19 heads).  The products read 64 queries' operands with the whole of K
+// block, 16 columns each, waited on every barrier twice as often: 629 us against 497 when
+// both were built, 505 now, at 8 sequences of 2048, 19 heads).  The products read 64 queries' operands with the whole of K
 // and V: bound by shared memory's 128 bytes a clock, 1280 clocks a block against 1024 of the
 // tensor cores'.
 template <int DP_, bool BIAS>

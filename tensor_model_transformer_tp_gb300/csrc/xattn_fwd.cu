@@ -25,9 +25,10 @@
 // the blocks around the diagonal add a value per score, from the head's table by
 // distance (a lane's 128 values are consecutive, neighbouring lanes' shifted by one).
 //
-// Keys at and behind kv_lens count for nothing whatever they hold: their scores are
-// replaced, not added to, and their rows of V are cleared in shared memory before the
-// product (0 times an infinity would be NaN).
+// Keys that no query of the sequence sees (at and behind kv_lens; causal, behind the last
+// query) count for nothing whatever they hold: their scores are replaced, not added to, and
+// their rows of V are cleared in shared memory before the product (0 times an infinity would
+// be NaN).
 #include <math.h>
 
 #include <algorithm>

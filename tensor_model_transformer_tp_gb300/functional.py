@@ -461,10 +461,14 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     q [batch, q_len, heads, head_dim], k and v [batch, k_len, kv_heads, head_dim],
     each with strides of its own; heads a multiple of kv_heads (query head h reads key
     head h // (heads // kv_heads)).  kv_lens int32 [batch]: how many keys each sequence
-    has (default k_len); what stands behind them is not used.  causal: key j is visible
+    has (default k_len); what stands behind them (causal: and behind the last query's
+    position) is not used.  causal: key j is visible
     where j <= q_start + i; q_start: the first query's position, a number for all
-    sequences or int32 [batch] (a single token behind a cache: its length - 1).  scale:
-    default head_dim ** -0.5.  bias [buckets, heads]: learned by the bucket of the
+    sequences or int32 [batch] (a single token behind a cache: its length - 1).  A cache that
+    grows is best given whole, with kv_lens and q_start as tensors: a slice of another length
+    or another number is another combination, checked anew (61 us of the host against 17).
+    Up to four rows (q_len times heads // kv_heads) run on a kernel that reads each key once;
+    beyond, a key is read by every query head that shares it.  scale: default head_dim ** -0.5.  bias [buckets, heads]: learned by the bucket of the
     key's position relative to the query's, as oases_attn.h defines it;
     bidirectional: default not causal.
     Returns o (contiguous, q's type) and lse, float32 [batch, heads, q_len]; a query
